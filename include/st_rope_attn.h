@@ -81,7 +81,7 @@ typedef enum {
   ST_ERR_UNSUPPORTED = 8  /* valid request outside what this build implements */
 } st_status;
 
-typedef enum { ST_BF16 = 0, ST_F16 = 1, ST_F32 = 2, ST_BOOL = 3, ST_I32 = 4 } st_dtype;
+typedef enum { ST_BF16 = 0, ST_F16 = 1, ST_F32 = 2, ST_BOOL = 3, ST_I32 = 4, ST_I64 = 5 } st_dtype;
 
 /* A strided view. Strides are in elements. Unused trailing dims are ignored. */
 typedef struct {
@@ -156,7 +156,12 @@ enum {
   ST_K_DW = 6,        /* norm-weight gradient reduction */
   ST_K_QPRIME = 7,    /* Q' rows for a backward without a forward's workspace */
   ST_K_PROBE = 8,     /* bounded-wait self-test */
-  ST_K_COUNT = 9
+  ST_K_CACHE_APPEND = 9,  /* st_cache_append */
+  ST_K_CACHE_ATTN = 10,   /* st_cache_attn: attention over the cache */
+  ST_K_CACHE_JOIN = 11,   /* st_cache_attn: joining the parts of split rows */
+  ST_K_VERIFY = 12,       /* st_tree_verify */
+  ST_K_CACHE_KEEP = 13,   /* st_cache_keep */
+  ST_K_COUNT = 14
 };
 
 /* Per-kernel device time between two st_timing_read calls. */
@@ -258,6 +263,121 @@ ST_API st_status st_rope_attn_fwd_noalloc(const st_tensor* q, const st_tensor* k
                                           const st_rope* rope, const st_tensor* mask, int causal, float scale,
                                           st_tensor* o, st_tensor* lse, void* stream);
 
+/* ---------------------------------------------------------------- serving
+ * A decoding step over a paged K/V cache: st_cache_append normalises and
+ * rotates the new rows and writes them into their pages, st_cache_attn attends
+ * with them over the cache (single tokens, a prompt's chunk, or a tree of
+ * drafted tokens), st_tree_verify accepts a path of the tree and draws the
+ * next token, st_cache_keep moves the path's rows to the end of the sequence.
+ *
+ * Lengths, counts, page numbers, parents, rows and tokens live on the device
+ * and are read there, so that no call waits for the GPU and every call can be
+ * captured into a CUDA graph and replayed with other lengths. What is out of
+ * range there cannot be refused by the call: it is left out as each call says,
+ * and the next st_check_status returns ST_ERR_INVALID_ARG.
+ *
+ * st_kv_cache: token `pos` of sequence b lies in row pos % page of page
+ *   pages[b, pos / page]. k, v: [N_pages, page, H_kv, D] of one dtype (bf16,
+ *   fp16 or fp32), any 16-byte strides, unit stride on D; a cache of one
+ *   piece per sequence is the case of one page per sequence. pages:
+ *   [B, max_pages] int32, unit stride on max_pages; entries behind a
+ *   sequence's last page are not read. max_pages * page <= 2^30. Sequences
+ *   may share pages that are only read.
+ * lens:   [B] int32, contiguous: tokens of each sequence in the cache before
+ *   the new rows, which take the positions lens[b], lens[b] + 1, ...
+ * counts: [B] int32, contiguous, or NULL (all T): how many of the T new rows
+ *   sequence b has (0..T); the rows behind them are padding. */
+typedef struct {
+  const st_tensor* k;
+  const st_tensor* v;
+  const st_tensor* pages;
+} st_kv_cache;
+
+/* New rows enter the cache.
+ *  q, k, v: [B, T, H, D], [B, T, H_kv, D] (twice); v of the cache's dtype, q
+ *           and k of that dtype or both fp32 (then rounded to it after norm
+ *           and rotation). H_kv divides H.
+ *  rope:    ids [B|1, T, n_axes], or cos/sin tables ([T, D], [1|B, T, D]);
+ *           the same rotation for q and k (ids_k, cos_k and sin_k must be
+ *           NULL).
+ *  q_rot:   [B, T, H, D] output in the cache's dtype: normalised, rotated q
+ *           (zero in padding rows). It may be q itself when the dtypes match.
+ * Rows whose position lies beyond the page table, or whose page number is not
+ * in [0, N_pages), are not written. Padding rows write nothing. */
+ST_API st_status st_cache_append(const st_tensor* q, const st_tensor* k, const st_tensor* v, const st_tensor* q_norm_w,
+                                 const st_tensor* k_norm_w, float eps, const st_rope* rope, const st_kv_cache* cache,
+                                 const st_tensor* lens, const st_tensor* counts, st_tensor* q_rot, void* stream);
+
+/* Bytes of device workspace that st_cache_attn needs (0 on invalid arguments,
+ * the error then in st_last_error; a call without rows needs 256). */
+ST_API size_t st_cache_attn_workspace_size(const st_tensor* q_rot, const st_kv_cache* cache, const st_tensor* parents);
+
+/* Attention over the cache, after the new rows were appended.
+ *  q_rot:   [B, T, H, D], the cache's dtype; H_kv divides H, H / H_kv <= 128.
+ *  parents: NULL: the T rows are a chain: row t sees the prefix [0, lens[b])
+ *           and the new rows 0..t. Else [B|1, T] int32, unit stride on T,
+ *           T <= 256: a tree of drafted tokens; row t sees the prefix, itself
+ *           and its ancestors. parents[t] < t, -1 for a node that follows the
+ *           prefix; anything else ends the walk up at that node.
+ *  scale:   score scale; <= 0 selects 1/sqrt(D).
+ *  o:       [B, T, H, D], the cache's dtype; lse: [B, H, T] fp32, contiguous.
+ *           Padding rows get O = 0, LSE = -inf.
+ *  workspace: 256-byte aligned; its contents need no initialisation. Calls
+ *           that may overlap on the GPU need workspaces of their own.
+ * lens[b] < 0 counts as 0; keys beyond the page table are left out; a page
+ * number not in [0, N_pages) reads as rows of zeros. Values in the cache that a
+ * row does not see must be finite where their position is below lens[b] +
+ * counts[b]; what lies behind is never used. bf16 and fp16 caches: products of
+ * 16-bit operands, the softmax weights rounded to that type, all sums in fp32.
+ * fp32 caches: fp32 throughout. Results do not depend on the run. */
+ST_API st_status st_cache_attn(const st_tensor* q_rot, const st_kv_cache* cache, const st_tensor* lens,
+                               const st_tensor* counts, const st_tensor* parents, float scale, st_tensor* o,
+                               st_tensor* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Verification of drafted tokens by speculative rejection sampling from given
+ * random numbers.
+ *  target_probs: [B, T, V] fp32, bf16 or fp16, unit stride on V: row n is the
+ *           target's distribution for the token after node n (in [0, 1],
+ *           summing to about 1; values outside are clamped, NaN counts as 0).
+ *  draft_probs: the same for the draft, row n being what node n's children
+ *           were drawn from, or NULL: children are fixed guesses.
+ *  tokens:  [B, T] int32 or int64; parents: [B|1, T] int32, unit stride on T;
+ *           T <= 1024. Node 0 is the root, already part of the sequence
+ *           (parents[0] = -1, its token is not read); 0 <= parents[n] < n for
+ *           the others, -1 for a node that is not to be reached.
+ *  counts:  [B] int32 or NULL: the nodes that sequence b has.
+ *  u_accept: [B, T] fp32, u_sample: [B] fp32, contiguous, in [0, 1).
+ * From the root on, the present node's children are tried in index order: with
+ * w_0 = p, C_0 = 1, a_0 = 0, a child with token x is accepted when
+ * u_accept * q(x) * C_k < w_k(x) and becomes the present node; else
+ * a_{k+1} = a_k + C_k, w_{k+1} = max(p - a_{k+1} q, 0), C_{k+1} = sum w_{k+1}.
+ * Without draft_probs q(x) = 1 and a rejection removes x: w(x) = 0, C_{k+1} =
+ * C_k - p(x). At the end the next token is the first v whose running sum of w
+ * exceeds u_sample * sum w (of p when w is zero everywhere, -1 when p is too).
+ * Sums are exact in units of 2^-52.
+ *  path:    [B, T] int32, contiguous: the accepted nodes from the root on, then
+ *           -1. n_accepted: [B] int32 (the root included; 0 where counts is 0).
+ *  next_token: [B], the dtype of tokens.
+ * A node whose parent or token is out of range is never reached. No workspace. */
+ST_API st_status st_tree_verify(const st_tensor* target_probs, const st_tensor* draft_probs, const st_tensor* tokens,
+                                const st_tensor* parents, const st_tensor* counts, const st_tensor* u_accept,
+                                const st_tensor* u_sample, st_tensor* path, st_tensor* n_accepted,
+                                st_tensor* next_token, void* stream);
+
+/* Rows of a cache move up, in place: position start[b] + rows[b, i] moves to
+ * start[b] + i, for i < n_rows[b]; k and v, all heads. With start = lens, rows
+ * = the accepted path and n_rows = n_accepted this turns an accepted path into
+ * the end of the sequence; with rows = the survivors of an eviction it thins a
+ * cache out.
+ *  start, n_rows: [B] int32, contiguous; rows: [B, N] int32, unit stride on N,
+ *           ascending without repetition, >= 0. lens: [B] int32 output, start +
+ *           n_rows; it may not overlap the inputs.
+ * n_rows is cut to [0, N] and to the page table's room. A row that does not
+ * ascend, or whose page is out of range, does not move. Pages that move must
+ * not be shared. */
+ST_API st_status st_cache_keep(const st_kv_cache* cache, const st_tensor* start, const st_tensor* rows,
+                               const st_tensor* n_rows, st_tensor* lens, void* stream);
+
 /* Message of the last failing call on this thread ("" if none). */
 ST_API const char* st_last_error(void);
 
@@ -282,7 +402,9 @@ ST_API st_status st_selftest_wait_timeout(long long budget_cycles, void* stream)
 
 /* Synchronises `stream` and reports ST_ERR_TIMEOUT if any kernel recorded a
  * bounded-wait timeout since the previous check (the record is then cleared),
- * or ST_ERR_CUDA if the stream holds an error. For tests and debugging. */
+ * ST_ERR_INVALID_ARG if a serving kernel met a value out of its range in device
+ * memory (likewise), or ST_ERR_CUDA if the stream holds an error. For tests and
+ * debugging. */
 ST_API st_status st_check_status(void* stream);
 
 #ifdef __cplusplus

@@ -8,7 +8,8 @@ tensor is not on a CUDA device, the call raises.
 Names follow the C-ABI: ``st_rope_attn_fwd``, ``st_rope_attn_bwd``,
 ``st_rope_attn_workspace_size``, ``st_get_stats``, ``st_reset_stats``,
 ``st_check_status``, ``st_last_error``. ``rope_attention`` wraps the pair in a
-``torch.autograd.Function``.
+``torch.autograd.Function``. The serving calls, over a paged ``KVCache``:
+``st_cache_append``, ``st_cache_attn``, ``st_tree_verify``, ``st_cache_keep``.
 
 The rotation is given either by position ids (``ids``, ``axes_dim``,
 ``theta``) or, in the form of the "Fused RoPE + SDPA" entry point, by
@@ -28,9 +29,9 @@ from . import build as _build
 
 ST_OK, ST_ERR_INVALID_ARG, ST_ERR_DTYPE, ST_ERR_SHAPE, ST_ERR_ALIGN, ST_ERR_WORKSPACE, ST_ERR_CUDA, \
     ST_ERR_TIMEOUT, ST_ERR_UNSUPPORTED = range(9)
-ST_BF16, ST_F16, ST_F32, ST_BOOL, ST_I32 = range(5)
+ST_BF16, ST_F16, ST_F32, ST_BOOL, ST_I32, ST_I64 = range(6)
 _DTYPES = {torch.bfloat16: ST_BF16, torch.float16: ST_F16, torch.float32: ST_F32, torch.bool: ST_BOOL,
-           torch.int32: ST_I32}
+           torch.int32: ST_I32, torch.int64: ST_I64}
 STATUS_NAMES = ["ST_OK", "ST_ERR_INVALID_ARG", "ST_ERR_DTYPE", "ST_ERR_SHAPE", "ST_ERR_ALIGN", "ST_ERR_WORKSPACE",
                 "ST_ERR_CUDA", "ST_ERR_TIMEOUT", "ST_ERR_UNSUPPORTED"]
 
@@ -62,13 +63,30 @@ class RopeTables:
         return [t for t in (self.cos, self.sin, self.cos_k, self.sin_k) if t is not None]
 
 
+class st_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.POINTER(st_tensor)), ("v", ctypes.POINTER(st_tensor)),
+                ("pages", ctypes.POINTER(st_tensor))]
+
+
+class KVCache:
+    """A paged K/V cache: ``k``, ``v`` [N_pages, page, H_kv, D] (bf16, fp16 or
+    fp32) and the page table ``pages`` [B, max_pages] int32; token ``pos`` of
+    sequence ``b`` lies in row ``pos % page`` of page ``pages[b, pos // page]``.
+    Holds references only: allocating pages and filling the table is the
+    caller's."""
+
+    def __init__(self, k, v, pages):
+        self.k, self.v, self.pages = k, v, pages
+
+
 class st_stats(ctypes.Structure):
     _fields_ = [(n, ctypes.c_uint64) for n in ("fwd_calls", "bwd_calls", "mask_all_true_skipped",
                                                 "mixed_dtype_calls", "tiles_skipped", "tiles_total", "timeouts",
                                                 "kernel_launches")]
 
 
-KERNEL_KINDS = ["table", "classify", "fwd", "bwd_pre", "bwd", "dq_post", "dw_reduce", "qprime", "probe"]
+KERNEL_KINDS = ["table", "classify", "fwd", "bwd_pre", "bwd", "dq_post", "dw_reduce", "qprime", "probe",
+                "cache_append", "cache_attn", "cache_join", "verify", "cache_keep"]
 
 
 class st_kernel_times(ctypes.Structure):
@@ -117,6 +135,17 @@ def lib():
             L.st_timing_enable.restype = i
             L.st_timing_read.argtypes = [ctypes.POINTER(st_kernel_times)]
             L.st_timing_read.restype = i
+            K = ctypes.POINTER(st_kv_cache)
+            L.st_cache_append.argtypes = [T, T, T, T, T, fl, R, K, T, T, T, vp]
+            L.st_cache_append.restype = i
+            L.st_cache_attn_workspace_size.argtypes = [T, K, T]
+            L.st_cache_attn_workspace_size.restype = sz
+            L.st_cache_attn.argtypes = [T, K, T, T, T, fl, T, T, vp, sz, vp]
+            L.st_cache_attn.restype = i
+            L.st_tree_verify.argtypes = [T] * 10 + [vp]
+            L.st_tree_verify.restype = i
+            L.st_cache_keep.argtypes = [K, T, T, T, T, vp]
+            L.st_cache_keep.restype = i
             _lib = L
     return _lib
 
@@ -292,6 +321,111 @@ def st_timing_read() -> dict:
     t = st_kernel_times()
     _check(lib().st_timing_read(ctypes.byref(t)))
     return {n: (int(t.launches[i]), float(t.ms[i])) for i, n in enumerate(KERNEL_KINDS)}
+
+
+# ------------------------------------------------------------------ serving
+def _cache_struct(cache):
+    c = st_kv_cache()
+    c._keep = [_t(cache.k), _t(cache.v), _t(cache.pages)]
+    c.k, c.v, c.pages = (_p(x) for x in c._keep)
+    return c
+
+
+def _device_of(*ts):
+    """The one CUDA device that all given tensors live on."""
+    dev = None
+    for t in ts:
+        for x in (t.tensors() if isinstance(t, RopeTables) else [t.k, t.v, t.pages] if isinstance(t, KVCache) else [t]):
+            if x is None:
+                continue
+            if not x.is_cuda:
+                raise StError(ST_ERR_INVALID_ARG, "all tensors must live on a CUDA device")
+            if dev is None:
+                dev = x.device
+            elif x.device != dev:
+                raise StError(ST_ERR_INVALID_ARG, f"tensors live on {dev} and on {x.device}")
+    return dev
+
+
+def _launch(dev, call):
+    """Runs a C call with ``dev`` as the current device, on that device's
+    current torch stream."""
+    if dev.index == torch.cuda.current_device():
+        _check(call(ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)))
+    else:
+        with torch.cuda.device(dev):
+            _check(call(ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)))
+
+
+def st_cache_append(q, k, v, q_norm_w, k_norm_w, eps, ids, axes_dim, theta, cache, lens, counts=None, q_rot=None):
+    """New rows enter the cache: q [B,T,H,D], k, v [B,T,H_kv,D]; k normalised
+    and rotated, and v, go to positions lens[b].. of each sequence. Returns the
+    normalised, rotated q in the cache's dtype (zero in rows behind counts[b])."""
+    dev = _device_of(q, k, v, q_norm_w, k_norm_w, ids, cache, lens, counts, q_rot)
+    if q_rot is None:
+        q_rot = torch.empty(q.shape, dtype=cache.k.dtype, device=dev)
+    r, c = _rope(ids, axes_dim, theta, None), _cache_struct(cache)
+    _launch(dev, lambda s: lib().st_cache_append(
+        _p(_t(q)), _p(_t(k)), _p(_t(v)), _p(_t(q_norm_w)), _p(_t(k_norm_w)), float(eps), ctypes.byref(r),
+        ctypes.byref(c), _p(_t(lens)), _p(_t(counts)), _p(_t(q_rot)), s))
+    return q_rot
+
+
+def st_cache_attn_workspace_size(q_rot, cache, parents=None) -> int:
+    n = lib().st_cache_attn_workspace_size(_p(_t(q_rot)), ctypes.byref(_cache_struct(cache)), _p(_t(parents)))
+    if n == 0:
+        raise StError(ST_ERR_INVALID_ARG, lib().st_last_error().decode())
+    return int(n)
+
+
+def st_cache_attn(q_rot, cache, lens, counts=None, parents=None, scale=None, o=None, lse=None, workspace=None):
+    """Attention of the new rows over the cache (after st_cache_append):
+    parents=None for a chain (single tokens, a prompt's chunk), [B|1, T] int32
+    for trees of drafted tokens. Returns (o [B,T,H,D], lse [B,H,T] fp32)."""
+    dev = _device_of(q_rot, cache, lens, counts, parents, o, lse, workspace)
+    B, T, H, _ = q_rot.shape
+    if o is None:
+        o = torch.empty(q_rot.shape, dtype=q_rot.dtype, device=dev)
+    if lse is None:
+        lse = torch.empty((B, H, T), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(st_cache_attn_workspace_size(q_rot, cache, parents), dtype=torch.uint8, device=dev)
+    c = _cache_struct(cache)
+    _launch(dev, lambda s: lib().st_cache_attn(
+        _p(_t(q_rot)), ctypes.byref(c), _p(_t(lens)), _p(_t(counts)), _p(_t(parents)), float(scale) if scale else 0.0,
+        _p(_t(o)), _p(_t(lse)), ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size(), s))
+    return o, lse
+
+
+def st_tree_verify(target_probs, draft_probs, tokens, parents, u_accept, u_sample, counts=None, path=None,
+                   n_accepted=None, next_token=None):
+    """Verification of drafted trees (see the C header): returns (path [B,T]
+    int32, the accepted nodes then -1; n_accepted [B] int32; next_token [B])."""
+    dev = _device_of(target_probs, draft_probs, tokens, parents, u_accept, u_sample, counts, path, n_accepted,
+                     next_token)
+    B, T = tokens.shape
+    if path is None:
+        path = torch.empty((B, T), dtype=torch.int32, device=dev)
+    if n_accepted is None:
+        n_accepted = torch.empty((B,), dtype=torch.int32, device=dev)
+    if next_token is None:
+        next_token = torch.empty((B,), dtype=tokens.dtype, device=dev)
+    _launch(dev, lambda s: lib().st_tree_verify(
+        _p(_t(target_probs)), _p(_t(draft_probs)), _p(_t(tokens)), _p(_t(parents)), _p(_t(counts)), _p(_t(u_accept)),
+        _p(_t(u_sample)), _p(_t(path)), _p(_t(n_accepted)), _p(_t(next_token)), s))
+    return path, n_accepted, next_token
+
+
+def st_cache_keep(cache, start, rows, n_rows, lens=None):
+    """Row start[b] + rows[b, i] of each sequence moves to start[b] + i, for
+    i < n_rows[b], in place. Returns the new lengths start + n_rows."""
+    dev = _device_of(cache, start, rows, n_rows, lens)
+    if lens is None:
+        lens = torch.empty(start.shape, dtype=torch.int32, device=dev)
+    c = _cache_struct(cache)
+    _launch(dev, lambda s: lib().st_cache_keep(ctypes.byref(c), _p(_t(start)), _p(_t(rows)), _p(_t(n_rows)),
+                                               _p(_t(lens)), s))
+    return lens
 
 
 class RopeAttention(torch.autograd.Function):

@@ -16,6 +16,7 @@
 #include "st_rope_attn.h"
 #include "st_aux.h"
 #include "st_f32.h"
+#include "st_host.h"
 #include "st_kernels.h"
 
 namespace st {
@@ -51,26 +52,31 @@ cudaEvent_t take_event() {
   return e;
 }
 
-// Launches one kernel through `fn`, counting it and, when timing is on,
-// bracketing it with events on its stream.
-template <class F>
-cudaError_t launch_counted(int kind, cudaStream_t stream, F&& fn) {
-  cudaEvent_t a = nullptr, b = nullptr;
+}  // namespace
+
+namespace st {
+
+LaunchMark launch_begin(cudaStream_t stream) {
+  LaunchMark m;
   if (g_timing.load(std::memory_order_relaxed)) {
     std::lock_guard<std::mutex> lk(g_tmu);
-    a = take_event();
-    b = take_event();
-    if (a) cudaEventRecord(a, stream);
+    m.a = take_event();
+    m.b = take_event();
+    if (m.a) cudaEventRecord(m.a, stream);
   }
-  cudaError_t e = fn();
-  if (e == cudaSuccess) ++h_launches;
-  if (a && b) {
-    cudaEventRecord(b, stream);
-    std::lock_guard<std::mutex> lk(g_tmu);
-    g_pending.push_back({kind, a, b});
-  }
-  return e;
+  return m;
 }
+
+void launch_end(const LaunchMark& m, int kind, cudaStream_t stream, cudaError_t e) {
+  if (e == cudaSuccess) ++h_launches;
+  if (m.a && m.b) {
+    cudaEventRecord(m.b, stream);
+    std::lock_guard<std::mutex> lk(g_tmu);
+    g_pending.push_back({kind, m.a, m.b});
+  }
+}
+
+void clear_error() { t_err.clear(); }
 
 st_status fail(st_status s, const char* fmt, ...) {
   char buf[512];
@@ -86,6 +92,7 @@ int elem_bytes(int dt) {
   switch (dt) {
     case ST_BF16: case ST_F16: return 2;
     case ST_F32: case ST_I32: return 4;
+    case ST_I64: return 8;
     case ST_BOOL: return 1;
     default: return 0;
   }
@@ -101,11 +108,6 @@ long long wait_budget() {
   }();
   return v;
 }
-
-struct Dev {
-  unsigned* status = nullptr;
-  unsigned long long* counters = nullptr;
-};
 
 st_status device_globals(Dev* d) {
   static Dev cache[64];
@@ -125,16 +127,8 @@ st_status device_globals(Dev* d) {
 }
 
 // ------------------------------------------------------------- validation
-struct Shape {
-  int B = 0, Sq = 0, Skv = 0, H = 0, D = 0;
-  int Hkv = 0;  // K/V heads: H is a multiple of it (grouped K/V heads)
-};
-
 static_assert(kDtBF16 == ST_BF16 && kDtF16 == ST_F16 && kDtF32 == ST_F32, "row dtype codes");
 
-constexpr unsigned bit(int dt) { return 1u << dt; }
-
-// A [B, S, H, D] tensor whose dtype is one of `dts` (a set of bit(st_dtype)).
 st_status check_bshd(const st_tensor* t, const char* name, int B, int S, int H, int D, unsigned dts,
                      RowTensor* out) {
   if (!t) return fail(ST_ERR_INVALID_ARG, "%s is NULL", name);
@@ -175,15 +169,6 @@ st_status check_vec(const st_tensor* t, const char* name, int D) {
   return ST_OK;
 }
 
-// The rotation source of q or of k: position ids (t), or in the table form
-// the caller's cos (t) and sin tables.
-struct Ids {
-  const st_tensor* t;
-  int Bt, S;
-  const st_tensor* sin = nullptr;
-  bool table = false;
-};
-
 st_status check_ids(const st_tensor* t, const char* name, int B, int S, int n_axes, Ids* out) {
   if (!t || (!t->data && S > 0)) return fail(ST_ERR_INVALID_ARG, "%s is NULL", name);
   if (t->ndim != 3) return fail(ST_ERR_SHAPE, "%s must be 3-D [B|1, S, n_axes]", name);
@@ -223,6 +208,28 @@ st_status check_tables(const st_tensor* c, const st_tensor* sn, const char* name
   out->S = S;
   return ST_OK;
 }
+
+st_status check_axes(const st_rope* rope, int D) {
+  if (rope->n_axes < 1 || rope->n_axes > 8) return fail(ST_ERR_INVALID_ARG, "rope.n_axes must be 1..8");
+  int dsum = 0;
+  for (int a = 0; a < rope->n_axes; ++a) {
+    if (rope->axes_dim[a] <= 0 || (rope->axes_dim[a] & 1))
+      return fail(ST_ERR_INVALID_ARG, "rope.axes_dim[%d]=%d must be positive and even", a, rope->axes_dim[a]);
+    dsum += rope->axes_dim[a];
+  }
+  if (dsum != D) return fail(ST_ERR_INVALID_ARG, "rope axes sum to %d, expected D=%d", dsum, D);
+  if (!(rope->theta > 0.0) || !std::isfinite(rope->theta)) return fail(ST_ERR_INVALID_ARG, "rope.theta must be > 0");
+  return ST_OK;
+}
+
+}  // namespace st
+
+namespace {
+
+struct Shape {
+  int B = 0, Sq = 0, Skv = 0, H = 0, D = 0;
+  int Hkv = 0;  // K/V heads: H is a multiple of it (grouped K/V heads)
+};
 
 struct Plan {
   Shape sh;
@@ -290,15 +297,7 @@ st_status plan_call(const st_tensor* q, const st_tensor* k, const st_tensor* v, 
     }
   } else {
     if (rope->cos_k || rope->sin_k) return fail(ST_ERR_INVALID_ARG, "rope.cos_k/sin_k need rope.cos/sin");
-    if (rope->n_axes < 1 || rope->n_axes > 8) return fail(ST_ERR_INVALID_ARG, "rope.n_axes must be 1..8");
-    int dsum = 0;
-    for (int a = 0; a < rope->n_axes; ++a) {
-      if (rope->axes_dim[a] <= 0 || (rope->axes_dim[a] & 1))
-        return fail(ST_ERR_INVALID_ARG, "rope.axes_dim[%d]=%d must be positive and even", a, rope->axes_dim[a]);
-      dsum += rope->axes_dim[a];
-    }
-    if (dsum != s.D) return fail(ST_ERR_INVALID_ARG, "rope axes sum to %d, expected D=%d", dsum, s.D);
-    if (!(rope->theta > 0.0) || !std::isfinite(rope->theta)) return fail(ST_ERR_INVALID_ARG, "rope.theta must be > 0");
+    if ((st = check_axes(rope, s.D)) != ST_OK) return st;
     if ((st = check_ids(rope->ids, "rope.ids", s.B, s.Sq, rope->n_axes, &P->ids_q)) != ST_OK) return st;
     if (rope->ids_k) {
       if ((st = check_ids(rope->ids_k, "rope.ids_k", s.B, s.Skv, rope->n_axes, &P->ids_k)) != ST_OK) return st;
@@ -432,6 +431,10 @@ void fill_common(const Plan& P, const st_tensor* qw, const st_tensor* kw, float 
   c->wait_budget = wait_budget();
 }
 
+}  // namespace
+
+namespace st {
+
 void fill_table(const Ids& ids, const st_rope* rope, float2* out, __half2* out16, unsigned* ctrl, TableParams* t) {
   memset(t, 0, sizeof(*t));
   t->Bt = ids.Bt;
@@ -472,6 +475,10 @@ st_status cuda_check(cudaError_t e, const char* what) {
   if (e != cudaSuccess) return fail(ST_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
   return ST_OK;
 }
+
+}  // namespace st
+
+namespace {
 
 // Rotary tables and mask tile classes: the first launches of a call.
 st_status launch_prelude(const Plan& P, const st_rope* rope, const st_tensor* mask, uint8_t* ws, const Dev& dev,
@@ -523,6 +530,10 @@ st_status check_out(const st_tensor* t, const char* name, int B, int S, int H, i
   return check_bshd(t, name, B, S, H, kD, bit(dtype), rt);
 }
 
+}  // namespace
+
+namespace st {
+
 // The encoder is a driver call and needs a context current on the calling
 // thread. A thread that has made no runtime call yet (an autograd worker
 // thread running the backward) has none: cudaSetDevice binds the current
@@ -541,6 +552,10 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   }();
   return fn;
 }
+
+}  // namespace st
+
+namespace {
 
 // 4-D tiled map over a bf16, fp16 or fp32 [B, S, H, D] tensor for boxes of
 // 128 bytes (64 16-bit or 32 fp32 columns) x box_rows rows with 128-byte
@@ -1087,10 +1102,12 @@ st_status st_check_status(void* stream_) {
   unsigned s = 0, z = 0;
   if ((st = cuda_check(cudaMemcpy(&s, dev.status, sizeof(s), cudaMemcpyDeviceToHost), "read status")) != ST_OK)
     return st;
-  if (s & (kStatusTimeout | kStatusLayout)) {
+  if (s & (kStatusTimeout | kStatusLayout | kStatusIndex)) {
     cudaMemcpy(dev.status, &z, sizeof(z), cudaMemcpyHostToDevice);
     if (s & kStatusLayout) return fail(ST_ERR_CUDA, "a kernel found its shared memory misaligned and did nothing");
-    return fail(ST_ERR_TIMEOUT, "a kernel's bounded wait ran out");
+    if (s & kStatusTimeout) return fail(ST_ERR_TIMEOUT, "a kernel's bounded wait ran out");
+    return fail(ST_ERR_INVALID_ARG,
+                "a serving kernel met a length, count, page, row, parent or token out of its range");
   }
   return ST_OK;
 }

@@ -36,13 +36,6 @@ __device__ __forceinline__ RowIdx row_idx(int64_t row, int S, int H, bool small)
 
 static_assert(kPairs == 64, "the table kernel indexes pairs with shifts");
 
-// Element e of a caller table as fp32.
-__device__ __forceinline__ float table_elem(const void* t, int dtype, int64_t e) {
-  if (dtype == kTabF32) return static_cast<const float*>(t)[e];
-  if (dtype == kTabBF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(t)[e]);
-  return __half2float(static_cast<const __half*>(t)[e]);
-}
-
 // (cos, sin) of id * omega_p, the angle reduced to [-pi, pi] in fp64 before
 // the fp32 sincosf so that large ids keep full fp32 accuracy; or, in the table
 // form, entry 2p of the caller's pair-duplicated cos/sin rows.
@@ -68,13 +61,9 @@ __global__ void table_kernel(const __grid_constant__ TableParams p) {
     const int64_t off = bt * p.i_sb + (int64_t)s * p.i_ss + (int64_t)a * p.i_sa;
     const double id = p.ids_f32 ? static_cast<double>(static_cast<const float*>(p.ids)[off])
                                 : static_cast<double>(static_cast<const int32_t*>(p.ids)[off]);
-    const double phi = id * p.omega[pr];
-    const double k = rint(phi * 0.15915494309189535);  // 1 / (2 pi)
-    const double red = fma(-k, 6.283185307179586, phi);
-    float sn, cs;
-    sincosf(static_cast<float>(red), &sn, &cs);
-    p.out[e] = make_float2(cs, sn);
-    p.out16[e] = __floats2half2_rn(cs, sn);
+    const float2 cs = pair_cos_sin(id, p.omega[pr]);
+    p.out[e] = cs;
+    p.out16[e] = __floats2half2_rn(cs.x, cs.y);
   }
 }
 

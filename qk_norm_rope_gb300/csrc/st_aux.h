@@ -21,6 +21,24 @@ inline int dw_reduce_blocks(int n_q, int n_k) {
 // st_dtype codes of a caller table (the C header's ST_BF16, ST_F16, ST_F32).
 constexpr int kTabBF16 = 0, kTabF16 = 1, kTabF32 = 2;
 
+// Element e of a caller table as fp32.
+__device__ __forceinline__ float table_elem(const void* t, int dtype, int64_t e) {
+  if (dtype == kTabF32) return static_cast<const float*>(t)[e];
+  if (dtype == kTabBF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(t)[e]);
+  return __half2float(static_cast<const __half*>(t)[e]);
+}
+
+// (cos, sin) of id * omega, the angle reduced to [-pi, pi] in fp64 before the
+// fp32 sincosf.
+__device__ __forceinline__ float2 pair_cos_sin(double id, double omega) {
+  const double phi = id * omega;
+  const double k = rint(phi * 0.15915494309189535);  // 1 / (2 pi)
+  const double red = fma(-k, 6.283185307179586, phi);
+  float2 r;
+  sincosf(static_cast<float>(red), &r.y, &r.x);
+  return r;
+}
+
 struct TableParams {
   const void* ids;
   int ids_f32;

@@ -1,0 +1,274 @@
+// Cached attention on the CUDA cores: fp32 caches (every product and sum in
+// fp32), and 16-bit caches whose pages the tensor-core kernel's boxes do not
+// fit (page sizes that are no multiple of 8).
+//
+// An item is kSimtRows query rows (token x head of the group) of one K/V head
+// of one sequence; its keys are walked in tiles of kSimtKeys and split over
+// p.splits CTAs, since a decoding step has few rows and many keys. Each CTA
+// leaves (O unnormalised, running maximum, sum) in the workspace and a second
+// kernel joins them; with one split it writes O and LSE itself. Bound by the
+// fp32 FMA rate and shared-memory reads: a thread holds 2 x 4 scores and 4 x 4
+// outputs, so that one 16-byte read feeds 5 to 8 FMAs.
+#include <atomic>
+#include "st_kernels.h"
+#include "st_serve.h"
+
+namespace st {
+
+namespace {
+
+constexpr int kR = kSimtRows, kN = kSimtKeys, kThreads = 256;
+constexpr int kPad = kD + 4, kPadP = kN + 4;
+
+struct Smem {
+  float q[kR][kPad];
+  float k[kN][kPad];
+  float v[kN][kD];
+  float p[kR][kPadP];
+  float corr[kR], m[kR], l[kR];
+  uint32_t anc[kR][kTreeWords];
+};
+
+// Bit j of the result: node `first + j` is seen from a row whose ancestors
+// (itself included) are `anc`.
+__device__ __forceinline__ bool tree_sees(const uint32_t* anc, int node) {
+  return node < kMaxTree && ((anc[node >> 5] >> (node & 31)) & 1u);
+}
+
+__global__ void __launch_bounds__(kThreads) simt_kernel(const __grid_constant__ CacheAttnParams p, int n_rt) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  Smem& s = *reinterpret_cast<Smem*>(raw);
+  grid_dependency_wait();
+  const int tid = threadIdx.x;
+  const int64_t item = blockIdx.x;
+  const int split = blockIdx.y;
+  const int rt = static_cast<int>(item % n_rt), hk = static_cast<int>(item / n_rt % p.kv.Hkv);
+  const int b = static_cast<int>(item / n_rt / p.kv.Hkv);
+  const int G = p.group;
+  const int64_t rows = static_cast<int64_t>(p.T) * G;
+  const int64_t row0 = static_cast<int64_t>(rt) * kR;
+  const int cnt = row_count(p.counts, b, p.T);
+  int prefix;
+  const int keys = key_count(p, b, cnt, &prefix);
+  if (tid == 0 && split == 0 && (__ldg(p.lens + b) < 0 || static_cast<int64_t>(__ldg(p.lens + b)) + cnt > keys)) atomicOr(p.status, kStatusIndex);
+
+  // the last key that any row of the item sees
+  const int t_last = static_cast<int>(min((row0 + kR - 1) / G, static_cast<int64_t>(p.T) - 1));
+  const int end = p.parents ? keys : min(keys, prefix + min(t_last + 1, cnt));
+  const int n_tiles = row0 / G < cnt ? (end + kN - 1) / kN : 0;
+  const int j_lo = static_cast<int>(static_cast<int64_t>(n_tiles) * split / p.splits);
+  const int j_hi = static_cast<int>(static_cast<int64_t>(n_tiles) * (split + 1) / p.splits);
+
+  for (int e = tid; e < kR * kD / 8; e += kThreads) {
+    const int r = e / (kD / 8), c = e % (kD / 8);
+    const int64_t row = row0 + r;
+    float x[8] = {};
+    if (row < rows) {
+      const int t = static_cast<int>(row / G), h = hk * G + static_cast<int>(row % G);
+      if (t < cnt) load_chunk8(p.q.p, b * p.q.sb + t * p.q.ss + h * p.q.sh, p.q.dt, c, x);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) s.q[r][8 * c + u] = x[u] * p.scale_log2;
+  }
+  if (tid < kR) {
+    s.m[tid] = -INFINITY;
+    s.l[tid] = 0.f;
+    if (p.parents) {  // a walk up from the row's node; parents come before children
+      const int64_t row = row0 + tid;
+      for (int w = 0; w < kTreeWords; ++w) s.anc[tid][w] = 0;
+      int node = row < rows ? static_cast<int>(row / G) : -1;
+      if (node >= cnt) node = -1;
+      while (node >= 0) {
+        s.anc[tid][node >> 5] |= 1u << (node & 31);
+        const int up = __ldg(p.parents + b * p.par_sb + node);
+        if (up >= node || up < -1) {
+          atomicOr(p.status, kStatusIndex);
+          break;
+        }
+        node = up;
+      }
+    }
+  }
+  float o[4][4] = {};
+  const int tr = tid >> 4, tc = tid & 15;   // scores: rows tr, tr + 16; keys tc + 16 i
+  const int rg = tid >> 5, dg = tid & 31;   // outputs: rows 4 rg + i; dims 4 dg..
+  for (int jt = j_lo; jt < j_hi; ++jt) {
+    const int j0 = jt * kN;
+    __syncthreads();
+    for (int e = tid; e < kN * kD / 8; e += kThreads) {
+      const int r = e / (kD / 8), c = e % (kD / 8), j = j0 + r;
+      float x[8] = {}, y[8] = {};
+      int pg, prow;
+      if (j < keys) {
+        if (kv_locate(p.kv, b, j, &pg, &prow)) {
+          load_chunk8(p.kv.k, pg * p.kv.k_sp + prow * p.kv.k_sr + hk * p.kv.k_sh, p.kv.dt, c, x);
+          load_chunk8(p.kv.v, pg * p.kv.v_sp + prow * p.kv.v_sr + hk * p.kv.v_sh, p.kv.dt, c, y);
+        } else {
+          atomicOr(p.status, kStatusIndex);
+        }
+      }
+      *reinterpret_cast<float4*>(&s.k[r][8 * c]) = make_float4(x[0], x[1], x[2], x[3]);
+      *reinterpret_cast<float4*>(&s.k[r][8 * c + 4]) = make_float4(x[4], x[5], x[6], x[7]);
+      *reinterpret_cast<float4*>(&s.v[r][8 * c]) = make_float4(y[0], y[1], y[2], y[3]);
+      *reinterpret_cast<float4*>(&s.v[r][8 * c + 4]) = make_float4(y[4], y[5], y[6], y[7]);
+    }
+    __syncthreads();
+    float sc[2][4] = {};
+#pragma unroll 8
+    for (int d = 0; d < kD; d += 4) {
+      const float4 q0 = *reinterpret_cast<const float4*>(&s.q[tr][d]), q1 = *reinterpret_cast<const float4*>(&s.q[tr + 16][d]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 kk = *reinterpret_cast<const float4*>(&s.k[tc + 16 * i][d]);
+        sc[0][i] = fmaf(q0.x, kk.x, fmaf(q0.y, kk.y, fmaf(q0.z, kk.z, fmaf(q0.w, kk.w, sc[0][i]))));
+        sc[1][i] = fmaf(q1.x, kk.x, fmaf(q1.y, kk.y, fmaf(q1.z, kk.z, fmaf(q1.w, kk.w, sc[1][i]))));
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const int r = tr + 16 * w;
+      const int64_t row = row0 + r;
+      const int t = row < rows ? static_cast<int>(row / G) : p.T;
+      float mt = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = j0 + tc + 16 * i, node = j - prefix;
+        const bool sees = t < cnt && j < keys && (node < 0 || (p.parents ? tree_sees(s.anc[r], node) : node <= t));
+        if (!sees) sc[w][i] = -INFINITY;
+        mt = fmaxf(mt, sc[w][i]);
+      }
+#pragma unroll
+      for (int x = 8; x > 0; x >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
+      const float m_old = s.m[r], m_new = fmaxf(m_old, mt), m_use = m_new == -INFINITY ? 0.f : m_new;
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float e = exp2f(sc[w][i] - m_use);
+        s.p[r][tc + 16 * i] = e;
+        sum += e;
+      }
+#pragma unroll
+      for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+      __syncwarp();  // every lane has read the row's old maximum
+      if (tc == 0) {
+        const float corr = exp2f(m_old - m_use);  // 0 while the row has seen nothing
+        s.corr[r] = corr;
+        s.m[r] = m_new;
+        s.l[r] = s.l[r] * corr + sum;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float corr = s.corr[4 * rg + i];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) o[i][u] *= corr;
+    }
+#pragma unroll 4
+    for (int k = 0; k < kN; k += 4) {
+      float4 vv[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) vv[u] = *reinterpret_cast<const float4*>(&s.v[k + u][4 * dg]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 pp = *reinterpret_cast<const float4*>(&s.p[4 * rg + i][k]);
+        const float pw[4] = {pp.x, pp.y, pp.z, pp.w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          o[i][0] = fmaf(pw[u], vv[u].x, o[i][0]);
+          o[i][1] = fmaf(pw[u], vv[u].y, o[i][1]);
+          o[i][2] = fmaf(pw[u], vv[u].z, o[i][2]);
+          o[i][3] = fmaf(pw[u], vv[u].w, o[i][3]);
+        }
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 4 * rg + i;
+    const int64_t row = row0 + r;
+    if (row >= rows) continue;
+    if (p.splits > 1) {
+      const int64_t slot = (item * p.splits + split) * kR + r;
+      *reinterpret_cast<float4*>(p.part + slot * kD + 4 * dg) = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+      if (dg == 0) {
+        float2* ml = reinterpret_cast<float2*>(p.part + static_cast<int64_t>(gridDim.x) * p.splits * kR * kD);
+        ml[slot] = make_float2(s.m[r], s.l[r]);
+      }
+      continue;
+    }
+    const float l = s.l[r], inv = l == 0.f ? 0.f : 1.f / l;
+    const int t = static_cast<int>(row / G), h = hk * G + static_cast<int>(row % G);
+    const int64_t off = b * p.o_sb + t * p.o_ss + h * p.o_sh + 4 * dg;
+    if (p.kv.dt == kDtF32)
+      *reinterpret_cast<float4*>(static_cast<float*>(p.o) + off) = make_float4(o[i][0] * inv, o[i][1] * inv, o[i][2] * inv, o[i][3] * inv);
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + off) =
+          make_uint2(pack_dt(p.kv.dt, o[i][0] * inv, o[i][1] * inv), pack_dt(p.kv.dt, o[i][2] * inv, o[i][3] * inv));
+    if (dg == 0) p.lse[(static_cast<int64_t>(b) * p.H + h) * p.T + t] = l == 0.f ? -INFINITY : (s.m[r] + log2f(l)) * kLn2;
+  }
+}
+
+// One warp per query row: the splits' parts, brought to their common maximum.
+__global__ void __launch_bounds__(256) simt_join_kernel(const __grid_constant__ CacheAttnParams p, int n_rt, int64_t items) {
+  grid_dependency_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5);
+  const int64_t item = w / kR;
+  const int r = static_cast<int>(w % kR);
+  if (item >= items) return;
+  const int rt = static_cast<int>(item % n_rt), hk = static_cast<int>(item / n_rt % p.kv.Hkv);
+  const int b = static_cast<int>(item / n_rt / p.kv.Hkv);
+  const int64_t row = static_cast<int64_t>(rt) * kR + r;
+  if (row >= static_cast<int64_t>(p.T) * p.group) return;
+  const float2* ml = reinterpret_cast<const float2*>(p.part + items * p.splits * kR * kD);
+  const int64_t slot0 = item * p.splits * kR + r;
+  float m = -INFINITY;
+  for (int s = lane; s < p.splits; s += 32) m = fmaxf(m, ml[slot0 + static_cast<int64_t>(s) * kR].x);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+  const float m_use = m == -INFINITY ? 0.f : m;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < p.splits; ++s) {
+    const int64_t slot = slot0 + static_cast<int64_t>(s) * kR;
+    const float2 x = ml[slot];
+    const float4 y = reinterpret_cast<const float4*>(p.part + slot * kD)[lane];
+    const float f = exp2f(x.x - m_use);
+    l = fmaf(f, x.y, l);
+    o.x = fmaf(f, y.x, o.x);
+    o.y = fmaf(f, y.y, o.y);
+    o.z = fmaf(f, y.z, o.z);
+    o.w = fmaf(f, y.w, o.w);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int t = static_cast<int>(row / p.group), h = hk * p.group + static_cast<int>(row % p.group);
+  const int64_t off = b * p.o_sb + t * p.o_ss + h * p.o_sh + 4 * lane;
+  if (p.kv.dt == kDtF32)
+    *reinterpret_cast<float4*>(static_cast<float*>(p.o) + off) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  else
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + off) =
+        make_uint2(pack_dt(p.kv.dt, o.x * inv, o.y * inv), pack_dt(p.kv.dt, o.z * inv, o.w * inv));
+  if (lane == 0) p.lse[(static_cast<int64_t>(b) * p.H + h) * p.T + t] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+}  // namespace
+
+cudaError_t launch_cache_attn_simt(const CacheAttnParams& p, cudaStream_t stream) {
+  static std::atomic<uint64_t> configured{0};
+  cudaError_t e = opt_in_smem(simt_kernel, sizeof(Smem), configured);
+  if (e != cudaSuccess) return e;
+  const int n_rt = static_cast<int>((static_cast<int64_t>(p.T) * p.group + kR - 1) / kR);
+  return launch_chained(simt_kernel, dim3(static_cast<unsigned>(simt_items(p.B, p.T, p.H, p.kv.Hkv)), p.splits), dim3(kThreads),
+                        sizeof(Smem), stream, p, n_rt);
+}
+
+cudaError_t launch_cache_attn_simt_join(const CacheAttnParams& p, cudaStream_t stream) {
+  const int n_rt = static_cast<int>((static_cast<int64_t>(p.T) * p.group + kR - 1) / kR);
+  const int64_t items = simt_items(p.B, p.T, p.H, p.kv.Hkv);
+  return launch_chained(simt_join_kernel, dim3(static_cast<unsigned>((items * kR + 7) / 8)), dim3(256), 0, stream, p, n_rt, items);
+}
+
+}  // namespace st

@@ -20,7 +20,7 @@ enum : uint8_t { kTileMixed = 0, kTileAllTrue = 1, kTileAllFalse = 2 };
 enum MaskKind : int { kMaskNone = 0, kMaskBool = 1, kMaskF32 = 2, kMaskBF16 = 3 };
 
 // Device status word bits.
-enum : unsigned { kStatusTimeout = 1u, kStatusLayout = 2u };
+enum : unsigned { kStatusTimeout = 1u, kStatusLayout = 2u, kStatusIndex = 4u };
 
 // Device-side counters (indices into a uint64 array).
 enum { kCtrMaskAllTrue = 0, kCtrTilesSkipped = 1, kCtrTilesTotal = 2, kCtrTimeouts = 3, kNumCounters = 8 };
