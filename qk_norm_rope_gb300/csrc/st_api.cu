@@ -553,16 +553,12 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return fn;
 }
 
-}  // namespace st
-
-namespace {
-
 // 4-D tiled map over a bf16, fp16 or fp32 [B, S, H, D] tensor for boxes of
 // 128 bytes (64 16-bit or 32 fp32 columns) x box_rows rows with 128-byte
 // swizzle. The two
 // middle dims are ordered by stride (s before h when the sequence stride is the
 // smaller one, as in a BHSD view).
-st_status encode_rows_map(const st_tensor* t, CUtensorMap* map, int* s_first, int box_rows = kTile) {
+st_status encode_rows_map(const st_tensor* t, CUtensorMap* map, int* s_first, int box_rows) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc) return fail(ST_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   const int64_t B = t->shape[0], S = t->shape[1], H = t->shape[2];
@@ -594,6 +590,10 @@ st_status encode_rows_map(const st_tensor* t, CUtensorMap* map, int* s_first, in
   if (r != CUDA_SUCCESS) return fail(ST_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled rejected the layout (error %d)", (int)r);
   return ST_OK;
 }
+
+}  // namespace st
+
+namespace {
 
 // 2-D tiled map over an fp32 rotary table [rows, 64] float2 (cos, sin) seen as
 // [rows, 128] floats, for 32-float x 128-row boxes with 128-byte swizzle: the

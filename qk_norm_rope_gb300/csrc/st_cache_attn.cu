@@ -1,0 +1,710 @@
+// Cached attention on the tensor cores (bf16 and fp16 caches): tcgen05 QK^T
+// and PV with TMEM accumulators over pages gathered by TMA, online base-2
+// softmax, split over the keys and joined.
+//
+// Work: an item is a (K/V head, sequence, group of NT 128-row query tiles); a
+// tile's rows are tokens x the query heads of the K/V head, so that one read of
+// K and V serves the whole group of heads. The items' key tiles (128 keys),
+// laid end to end, are dealt out as one continuous range per CTA: the lengths
+// live on the device, and this way any mix of lengths loads every SM alike. A
+// CTA that holds all of an item's tiles writes O and LSE; else it leaves
+// (O unnormalised, reference, sum) in the workspace, at most one such part at
+// each end of its range, and the join kernel puts them together.
+//
+// Roles (480 threads, one CTA per SM):
+//   warps 0-7   softmax, two groups of four warps; thread = query row = TMEM lane
+//   warps 8-11  Q rows of the next item into shared memory
+//   warp 12     TMEM allocation, tcgen05.mma issue (one thread)
+//   warp 13/14  TMA of K / V boxes, one lane per box
+// TMEM: S0 | S1 | O0 | O1, 128 fp32 columns each; P (16-bit) overwrites the
+// first half of its S and feeds PV from TMEM. The stream of score tiles
+// alternates between the two halves ("slots"): with NT = 2 a slot is a query
+// tile, with NT = 1 (decoding: few rows, bound by the reading of K and V) the
+// slots take alternate key tiles with accumulators of their own, which are
+// merged at the end; either way one slot's softmax runs under the other's
+// MMAs. The scores run two tiles ahead of PV, across the borders of items.
+#include <atomic>
+#include "st_kernels.h"
+#include "st_serve.h"
+
+namespace st {
+
+namespace {
+
+constexpr int kSoftWarps = 8, kWarpQ0 = 8, kQWarps = 4, kWarpMma = 12, kWarpK = 13, kWarpV = 14;
+constexpr int kTcWarps = 15, kTcThreads = kTcWarps * 32;
+constexpr float kRescale = 8.0f;  // O is rescaled when the running maximum grows by more than this (base 2)
+
+template <int NT>
+struct Lay {  // shared memory, offsets from a 1024-byte aligned base
+  static constexpr int KS = 3, VS = NT == 1 ? 3 : 2;
+  static constexpr uint32_t q = 0, k = NT * kTileBytes, v = k + KS * kTileBytes, bar = v + VS * kTileBytes;
+  static constexpr uint32_t ml = bar + 512;          // [2][128] (reference, sum), NT = 1
+  static constexpr uint32_t bytes = ml + (NT == 1 ? 2 * 128 * 8 : 0);
+  enum { QFull = 0, QEmpty, KFull, KEmpty = KFull + KS, VFull = KEmpty + KS, VEmpty = VFull + VS, SFull = VEmpty + VS,
+         PFull = SFull + 2, OFull = PFull + 2, MlFull, ORead = MlFull + 2, Num = ORead + 2 };
+};
+static_assert(Lay<1>::bytes <= 232448 && Lay<2>::bytes <= 232448, "shared memory");
+static_assert(Lay<1>::Num * 8 + 128 <= 512 && Lay<2>::Num * 8 + 128 <= 512, "barrier area");
+
+__device__ __forceinline__ constexpr uint32_t kofs(int kk) { return (kk >> 2) * kHalfBytes + (kk & 3) * 32; }
+__device__ __forceinline__ constexpr uint32_t mofs(int kk) { return kk * 2048; }
+
+struct Item {
+  int prefix, keys, cnt, n;  // n: key tiles
+};
+__device__ __forceinline__ Item item_of(const TcAttnParams& p, int nt, int b, int m) {
+  Item it;
+  it.cnt = row_count(p.c.counts, b, p.c.T);
+  it.keys = key_count(p.c, b, it.cnt, &it.prefix);
+  const int64_t t0 = static_cast<int64_t>(m) * nt * p.tpt;
+  if (t0 >= it.cnt) {
+    it.n = 0;
+  } else {
+    // a chain's last row of the group sees no further than itself
+    const int64_t end = p.c.parents ? it.keys : min(static_cast<int64_t>(it.keys), it.prefix + t0 + nt * p.tpt);
+    it.n = static_cast<int>((end + kTile - 1) / kTile);
+  }
+  return it;
+}
+
+// A CTA's walk over its range: pieces of items.
+struct Walk {
+  int h, b, m, off;
+  long long left;
+  // the present piece
+  int ph, pb, pm, kt0, kt1;
+  Item it;
+  __device__ __forceinline__ void advance(const TcAttnParams& p) {
+    off = 0;
+    if (++m == p.n_groups) {
+      m = 0;
+      if (++b == p.c.B) {
+        b = 0;
+        ++h;
+      }
+    }
+  }
+  __device__ __forceinline__ bool next(const TcAttnParams& p, int nt) {
+    if (left <= 0) return false;
+    while (true) {
+      it = item_of(p, nt, b, m);
+      if (off < it.n) break;
+      advance(p);
+    }
+    ph = h;
+    pb = b;
+    pm = m;
+    kt0 = off;
+    kt1 = static_cast<int>(min(static_cast<long long>(it.n), off + left));
+    left -= kt1 - kt0;
+    off = kt1;
+    if (off == it.n) advance(p);
+    return true;
+  }
+  __device__ __forceinline__ bool whole() const { return kt0 == 0 && kt1 == it.n; }
+};
+
+struct Start {  // found by the block, read by every role
+  int h, b, m, off;
+  long long left, total;
+};
+
+// Where the CTA's range begins: every thread sums the key tiles of a run of
+// (sequence, group) pairs, a block scan places the runs.
+__device__ __forceinline__ void find_start(const TcAttnParams& p, int nt, long long* scan, Start* st) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t pairs = static_cast<int64_t>(p.c.B) * p.n_groups;
+  const int64_t per = (pairs + kTcThreads - 1) / kTcThreads, lo = min(pairs, tid * per), hi = min(pairs, lo + per);
+  long long sum = 0;
+  for (int64_t e = lo; e < hi; ++e) {
+    const int b = static_cast<int>(e / p.n_groups), m = static_cast<int>(e - static_cast<int64_t>(b) * p.n_groups);
+    const Item it = item_of(p, nt, b, m);
+    sum += it.n;
+    if (m == 0 && blockIdx.x == 0 && (__ldg(p.c.lens + b) < 0 || static_cast<int64_t>(__ldg(p.c.lens + b)) + it.cnt > it.keys))
+      atomicOr(p.c.status, kStatusIndex);
+  }
+  long long inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += t;
+  }
+  if (lane == 31) scan[warp] = inc;
+  if (tid == 0) st->left = 0;
+  __syncthreads();
+  long long before = 0, one = 0;
+  for (int w = 0; w < kTcWarps; ++w) {
+    if (w < warp) before += scan[w];
+    one += scan[w];
+  }
+  const long long total = one * p.c.kv.Hkv;
+  const long long ctas = min(static_cast<long long>(p.ctas), total);
+  if (tid == 0) st->total = total;
+  if (blockIdx.x < ctas) {
+    const long long s0 = blockIdx.x * total / ctas, s1 = (blockIdx.x + 1) * total / ctas;
+    const int h = static_cast<int>(s0 / one);
+    long long rem = s0 - h * one - (before + inc - sum);
+    if (rem >= 0 && rem < sum) {  // one thread
+      for (int64_t e = lo; e < hi; ++e) {
+        const int b = static_cast<int>(e / p.n_groups), m = static_cast<int>(e - static_cast<int64_t>(b) * p.n_groups);
+        const Item it = item_of(p, nt, b, m);
+        if (rem < it.n) {
+          st->h = h;
+          st->b = b;
+          st->m = m;
+          st->off = static_cast<int>(rem);
+          st->left = s1 - s0;
+          JoinMeta& meta = p.meta[blockIdx.x];
+          meta.total = total;
+          meta.item_start = s0 - rem;
+          meta.n = rem > 0 ? it.n : 0;
+          meta.h = h;
+          meta.b = b;
+          meta.m = m;
+          break;
+        }
+        rem -= it.n;
+      }
+    }
+  } else if (tid == 0) {
+    p.meta[blockIdx.x].n = 0;
+  }
+  __syncthreads();
+}
+
+template <bool F16>
+__device__ __forceinline__ void issue_s(uint32_t tS, uint64_t dQ, uint64_t dK) {
+  constexpr uint32_t idesc = idesc16(F16, 128, 128, 0, 0);
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk) mma_ss(tS, sdesc_add(dQ, kofs(kk)), sdesc_add(dK, kofs(kk)), idesc, kk > 0);
+}
+template <bool F16>
+__device__ __forceinline__ void issue_pv(uint32_t tO, uint32_t tP, uint64_t dV, bool acc) {
+  constexpr uint32_t idesc = idesc16(F16, 128, 128, 0, 1);
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk) mma_ts(tO, tP + kk * 8, sdesc_add(dV, mofs(kk)), idesc, acc || kk > 0);
+}
+
+// Bits of the keys [j0, j0 + 32) that row (token t, ancestors anc) sees.
+template <bool TREE>
+__device__ __forceinline__ uint32_t key_bits(int j0, const Item& it, int t, const uint32_t (&anc)[kTreeWords]) {
+  const int n0 = j0 - it.prefix;  // node of bit 0
+  uint32_t w;
+  if constexpr (TREE) {
+    if (n0 <= -32) w = ~0u;
+    else if (n0 < 0) w = (~0u >> (32 + n0)) | (anc[0] << (-n0));
+    else {
+      uint32_t a = 0, c = 0;
+#pragma unroll
+      for (int i = 0; i < kTreeWords; ++i) {
+        if (i == (n0 >> 5)) a = anc[i];
+        if (i == (n0 >> 5) + 1) c = anc[i];
+      }
+      w = __funnelshift_r(a, c, n0 & 31);
+    }
+  } else {
+    const int k = t + 1 - n0;  // that many of the 32 are seen
+    w = k >= 32 ? ~0u : (k <= 0 ? 0u : (1u << k) - 1u);
+  }
+  const int in = it.keys - j0;
+  return in >= 32 ? w : (in <= 0 ? 0u : w & ((1u << in) - 1u));
+}
+
+// Softmax of one 128 x 128 score tile, a thread's row: running reference and
+// sum, P into the first 64 columns; O is rescaled where the reference moved.
+template <bool F16, bool MASK>
+__device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float sc, const uint32_t (&mb)[4], bool first,
+                                             float& m_run, float& l_run) {
+  uint32_t ra[16], rb[16];
+  float m0 = -INFINITY, m1 = -INFINITY;
+  tmem_ld16_issue(tS, ra);
+#pragma unroll
+  for (int q8 = 0; q8 < 8; ++q8) {
+    uint32_t(&cur)[16] = (q8 & 1) ? rb : ra;
+    uint32_t(&nxt)[16] = (q8 & 1) ? ra : rb;
+    tmem_ld_wait16(cur);
+    if (q8 < 7) tmem_ld16_issue(tS + 16 * (q8 + 1), nxt);
+    if constexpr (MASK) {
+      const uint32_t bits = mb[q8 >> 1] >> ((q8 & 1) * 16);
+#pragma unroll
+      for (int t = 0; t < 16; ++t)
+        if (!((bits >> t) & 1u)) cur[t] = 0xff800000u;
+    }
+#pragma unroll
+    for (int t = 0; t < 16; t += 4) {
+      m0 = fmax3(m0, __uint_as_float(cur[t]), __uint_as_float(cur[t + 1]));
+      m1 = fmax3(m1, __uint_as_float(cur[t + 2]), __uint_as_float(cur[t + 3]));
+    }
+  }
+  const float mt = fmaxf(m0, m1) * sc;
+  float corr = 1.f;
+  if (mt > m_run + kRescale || (m_run == -INFINITY && mt > -INFINITY)) {
+    corr = ex2(m_run - mt);  // 0 when m_run is -inf
+    m_run = mt;
+  }
+  const float m_use = m_run == -INFINITY ? 0.f : m_run;
+  const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-m_use, -m_use);
+  float2 ls = make_float2(0.f, 0.f);
+  tmem_ld16_issue(tS, ra);
+#pragma unroll
+  for (int q8 = 0; q8 < 8; ++q8) {
+    uint32_t(&cur)[16] = (q8 & 1) ? rb : ra;
+    uint32_t(&nxt)[16] = (q8 & 1) ? ra : rb;
+    tmem_ld_wait16(cur);
+    if (q8 < 7) tmem_ld16_issue(tS + 16 * (q8 + 1), nxt);
+    if constexpr (MASK) {
+      const uint32_t bits = mb[q8 >> 1] >> ((q8 & 1) * 16);
+#pragma unroll
+      for (int t = 0; t < 16; ++t)
+        if (!((bits >> t) & 1u)) cur[t] = 0xff800000u;
+    }
+    uint32_t pw[8];
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      const float2 x = __ffma2_rn(make_float2(__uint_as_float(cur[2 * t]), __uint_as_float(cur[2 * t + 1])), sc2, nm2);
+      const float p0 = ex2(x.x), p1 = ex2(x.y);
+      ls = __fadd2_rn(ls, make_float2(p0, p1));
+      pw[t] = pack16<F16>(p0, p1);
+    }
+    tmem_st8(tS + 8 * q8, pw);
+  }
+  l_run = l_run * corr + (ls.x + ls.y);
+  if (!first && __any_sync(0xffffffffu, corr != 1.f)) {  // warp-uniform: tcgen05.ld/st are collective
+#pragma unroll 1
+    for (int q4 = 0; q4 < 4; ++q4) {
+      uint32_t r32[32];
+      tmem_ld32(tO + 32 * q4, r32);
+#pragma unroll
+      for (int t = 0; t < 32; ++t) r32[t] = __float_as_uint(__uint_as_float(r32[t]) * corr);
+      tmem_st32(tO + 32 * q4, r32);
+    }
+  }
+  tmem_st_wait();
+}
+
+template <int NT, bool F16, bool TREE>
+__global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant__ TcAttnParams P) {
+  using L = Lay<NT>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* sm = smem_raw;
+  const CacheAttnParams& c = P.c;
+  grid_dependency_wait();
+  if (smem_u32(sm) & 1023u) {
+    if (threadIdx.x == 0) atomicOr(c.status, kStatusLayout);
+    return;
+  }
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::bar);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + L::Num);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+  Start* start = reinterpret_cast<Start*>(tslot + 2);
+  const int tid = threadIdx.x, warp = tid >> 5, lane_id = tid & 31;
+  const long long budget = c.wait_budget;
+
+  if (warp == kWarpMma) {
+    tmem_alloc(tslot, 512);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    mbar_init(&bars[L::QFull], kQWarps * 32);
+    mbar_init(&bars[L::QEmpty], 1);
+    for (int s = 0; s < L::KS; ++s) {
+      mbar_init(&bars[L::KFull + s], 1);
+      mbar_init(&bars[L::KEmpty + s], 1);
+    }
+    for (int s = 0; s < L::VS; ++s) {
+      mbar_init(&bars[L::VFull + s], 1);
+      mbar_init(&bars[L::VEmpty + s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars[L::SFull + s], 1);
+      mbar_init(&bars[L::PFull + s], 128);
+      mbar_init(&bars[L::MlFull + s], 128);
+      mbar_init(&bars[L::ORead + s], 128);
+    }
+    mbar_init(&bars[L::OFull], 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (tid == kWarpK * 32) tma_prefetch_desc(&P.tmap_k);
+  if (tid == kWarpV * 32) tma_prefetch_desc(&P.tmap_v);
+  // the scan's scratch lies in the Q tile, which is written later
+  find_start(P, NT, reinterpret_cast<long long*>(sm + L::q), start);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
+  Walk wk;
+  wk.h = start->h;
+  wk.b = start->b;
+  wk.m = start->m;
+  wk.off = start->off;
+  wk.left = start->left;
+  const int G = c.group, tile_rows = P.tpt * G;
+
+  if (warp < kSoftWarps) {
+    // -------------------------------------------------------------- softmax
+    // padding rows, and every row of a sequence without room for keys
+    if (c.counts || static_cast<int64_t>(c.kv.max_pages) * c.kv.page == 0) {
+      for (int b = blockIdx.x; b < c.B; b += gridDim.x) {
+        const Item it = item_of(P, NT, b, 0);
+        const int t0 = it.keys == 0 ? 0 : it.cnt;
+        for (int64_t e = tid; e < static_cast<int64_t>(c.T - t0) * c.H * 16; e += kSoftWarps * 32) {
+          const int64_t row = e >> 4;
+          const int t = t0 + static_cast<int>(row / c.H), h = static_cast<int>(row % c.H);
+          reinterpret_cast<uint4*>(static_cast<uint16_t*>(c.o) + b * c.o_sb + t * c.o_ss + h * c.o_sh)[e & 15] = make_uint4(0, 0, 0, 0);
+          if ((e & 15) == 0) c.lse[(static_cast<int64_t>(b) * c.H + h) * c.T + t] = -INFINITY;
+        }
+      }
+    }
+    const int slot = warp >> 2;
+    const int r = (warp & 3) * 32 + lane_id;
+    const uint32_t lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + slot * 128 + lane, tO = tmem + 256 + slot * 128 + lane;
+    const int rt = r / G, rg = r - rt * G;
+    const float sc = c.scale_log2;
+    long long g = 0;    // score tiles before the present piece
+    int vc = 0;         // key tiles before the present piece
+    int n_piece = 0;
+    bool ok = true, at_start = true;
+    while (ok && wk.next(P, NT)) {
+      const int steps = (wk.kt1 - wk.kt0) * NT;
+      const int t = (wk.pm * NT + (NT == 2 ? slot : 0)) * P.tpt + rt;
+      const bool valid = r < tile_rows && t < wk.it.cnt;
+      const bool act = __any_sync(0xffffffffu, valid);  // this warp has rows
+      uint32_t anc[kTreeWords] = {};
+      if (TREE && valid && wk.kt1 * kTile > wk.it.prefix) {
+        int node = t;
+        while (node >= 0) {
+#pragma unroll
+          for (int i = 0; i < kTreeWords; ++i)
+            if (i == (node >> 5)) anc[i] |= 1u << (node & 31);
+          const int up = __ldg(c.parents + wk.pb * c.par_sb + node);
+          if (up >= node || up < -1) {
+            atomicOr(c.status, kStatusIndex);
+            break;
+          }
+          node = up;
+        }
+      }
+      float m_run = -INFINITY, l_run = 0.f;
+      bool first = true;
+      for (int j = static_cast<int>((slot ^ g) & 1); j < steps; j += 2) {
+        const int kt = wk.kt0 + (NT == 2 ? j >> 1 : j), j0 = kt * kTile;
+        const long long gg = g + j;
+        if (!(ok = wait_bar_warp(&bars[L::SFull + slot], (gg >> 1) & 1, abort_flag, budget))) break;
+        tc_fence_after();
+        if (act) {
+          // the first node that the warp's first token does not see
+          const int open = TREE ? wk.it.prefix : wk.it.prefix + __shfl_sync(0xffffffffu, t, 0) + 1;
+          if (j0 + kTile <= min(open, wk.it.keys)) {
+            const uint32_t mb[4] = {~0u, ~0u, ~0u, ~0u};
+            softmax_tile<F16, false>(tS, tO, sc, mb, first, m_run, l_run);
+          } else {
+            uint32_t mb[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) mb[w] = valid ? key_bits<TREE>(j0 + 32 * w, wk.it, t, anc) : 0u;
+            softmax_tile<F16, true>(tS, tO, sc, mb, first, m_run, l_run);
+          }
+        }
+        first = false;
+        if (j0 + kTile > wk.it.keys && (NT == 1 || slot == 0)) {
+          // rows of V behind the last key hold anything: zero weights do not
+          // silence infinities and NaN, zeros do
+          const int st = (vc + kt - wk.kt0) % L::VS;
+          if (!(ok = wait_bar_warp(&bars[L::VFull + st], ((vc + kt - wk.kt0) / L::VS) & 1, abort_flag, budget))) break;
+          if (j0 + r >= wk.it.keys) zero_row(sm + L::v + st * kTileBytes, r);
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        mbar_arrive(&bars[L::PFull + slot]);
+      }
+      if (!ok) break;
+      // ---- the piece's result
+      const int h = wk.ph * G + rg;
+      const bool whole = wk.whole();
+      const int64_t pslot = 2 * static_cast<int64_t>(blockIdx.x) + (at_start ? 0 : 1);
+      at_start = false;
+      if (!(ok = wait_bar_warp(&bars[L::OFull], n_piece & 1, abort_flag, budget))) break;
+      tc_fence_after();
+      if constexpr (NT == 2) {
+        if (act) {
+          const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+          const int64_t ooff = wk.pb * c.o_sb + static_cast<int64_t>(t) * c.o_ss + static_cast<int64_t>(h) * c.o_sh;
+          const int64_t prow = pslot * P.part_rows + slot * tile_rows + r;
+#pragma unroll 1
+          for (int q4 = 0; q4 < 4; ++q4) {
+            uint32_t r32[32];
+            tmem_ld32(tO + 32 * q4, r32);
+            float y[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(r32[e]) * (whole ? inv : 1.f);
+            if (valid) store_chunk32(whole ? c.o : c.part, whole ? ooff : prow * kD, whole ? c.kv.dt : kDtF32, q4, y);
+          }
+          if (valid) {
+            if (whole) c.lse[(static_cast<int64_t>(wk.pb) * c.H + h) * c.T + t] = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * kLn2;
+            else P.part_ml[prow] = make_float2(m_run, l_run);
+          }
+        }
+      } else {
+        // the two slots' accumulators come together: this group takes 64 columns
+        float2* ml = reinterpret_cast<float2*>(sm + L::ml);
+        ml[slot * 128 + r] = make_float2(m_run, l_run);
+        mbar_arrive(&bars[L::MlFull + slot]);
+        if (!(ok = wait_bar_warp(&bars[L::MlFull + (slot ^ 1)], n_piece & 1, abort_flag, budget))) break;
+        if (act) {
+          const float2 other = ml[(slot ^ 1) * 128 + r];
+          const float m = fmaxf(m_run, other.x), m_use = m == -INFINITY ? 0.f : m;
+          const float f0 = ex2(m_run - m_use), f1 = ex2(other.x - m_use);
+          const float l = f0 * l_run + f1 * other.y, inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+          const bool mine = steps > 1 || (g & 1) == slot, theirs = steps > 1 || (g & 1) != slot;
+          const int64_t ooff = wk.pb * c.o_sb + static_cast<int64_t>(t) * c.o_ss + static_cast<int64_t>(h) * c.o_sh;
+          const int64_t prow = pslot * P.part_rows + r;
+          const uint32_t tOther = tmem + 256 + (slot ^ 1) * 128 + lane;
+#pragma unroll 1
+          for (int q = 0; q < 2; ++q) {
+            const int q4 = 2 * slot + q;
+            uint32_t a[32], d[32];
+            float y[32];
+            if (mine) tmem_ld32(tO + 32 * q4, a);
+            if (theirs) tmem_ld32(tOther + 32 * q4, d);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              float v = mine ? __uint_as_float(a[e]) * f0 : 0.f;
+              if (theirs) v = fmaf(__uint_as_float(d[e]), f1, v);
+              y[e] = v * inv;
+            }
+            if (valid) store_chunk32(whole ? c.o : c.part, whole ? ooff : prow * kD, whole ? c.kv.dt : kDtF32, q4, y);
+          }
+          if (valid && slot == 0) {
+            if (whole) c.lse[(static_cast<int64_t>(wk.pb) * c.H + h) * c.T + t] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            else P.part_ml[prow] = make_float2(m, l);
+          }
+        }
+        // neither accumulator is overwritten before both groups have read it
+        tc_fence_before();
+        mbar_arrive(&bars[L::ORead + slot]);
+        if (!(ok = wait_bar_warp(&bars[L::ORead + (slot ^ 1)], n_piece & 1, abort_flag, budget))) break;
+      }
+      tc_fence_before();
+      g += steps;
+      vc += wk.kt1 - wk.kt0;
+      ++n_piece;
+    }
+  } else if (warp < kWarpQ0 + kQWarps) {
+    // ---------------------------------------------------------------- Q rows
+    const int qt = tid - kWarpQ0 * 32;
+    int n_piece = 0;
+    while (wk.next(P, NT)) {
+      if (n_piece > 0 && !wait_bar_warp(&bars[L::QEmpty], (n_piece - 1) & 1, abort_flag, budget)) break;
+#pragma unroll 1
+      for (int ti = 0; ti < NT; ++ti) {
+        const int t0 = (wk.pm * NT + ti) * P.tpt;
+        const int nv = max(0, min(P.tpt, wk.it.cnt - t0)) * G;     // rows that are there
+        const int fill = ((nv + 31) & ~31) * 16;                   // whole warps of rows: zeros behind them
+        uint8_t* tile = sm + L::q + ti * kTileBytes;
+#pragma unroll 1
+        for (int e0 = qt; e0 < fill; e0 += kQWarps * 32 * 8) {
+          uint4 x[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const int e = e0 + u * kQWarps * 32, row = e >> 4;
+            x[u] = make_uint4(0, 0, 0, 0);
+            if (row < nv) {
+              const int tt = t0 + row / G, h = wk.ph * G + row % G;
+              x[u] = ldg_nc_v4(static_cast<const uint16_t*>(c.q.p) + wk.pb * c.q.sb + tt * c.q.ss + h * c.q.sh + 8 * (e & 15));
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const int e = e0 + u * kQWarps * 32, row = e >> 4, ch = e & 15;
+            if (e < fill) *reinterpret_cast<uint4*>(tile + (ch >> 3) * kHalfBytes + sw128_off(row, ch & 7)) = x[u];
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&bars[L::QFull]);
+      ++n_piece;
+    }
+  } else if (warp == kWarpK || warp == kWarpV) {
+    // ------------------------------------------------------- TMA of K and V
+    const bool is_k = warp == kWarpK;
+    const int stages = is_k ? L::KS : L::VS;
+    uint64_t* full = &bars[is_k ? L::KFull : L::VFull];
+    uint64_t* empty = &bars[is_k ? L::KEmpty : L::VEmpty];
+    const CUtensorMap* map = is_k ? &P.tmap_k : &P.tmap_v;
+    const bool r_first = (is_k ? P.k_r_first : P.v_r_first) != 0;
+    uint8_t* ring = sm + (is_k ? L::k : L::v);
+    const int nb = kTile / P.box, half = lane_id / nb, bx = lane_id - half * nb;  // lanes 0 .. 2 nb - 1
+    int n = 0;
+    bool ok = true;
+    while (ok && wk.next(P, NT)) {
+      for (int kt = wk.kt0; kt < wk.kt1; ++kt, ++n) {
+        const int st = n % stages;
+        const int j = kt * kTile + bx * P.box;
+        const bool mine = half < 2 && j < wk.it.keys;
+        int pg = 0, row = 0;
+        if (mine && !kv_locate(c.kv, wk.pb, j, &pg, &row)) atomicOr(c.status, kStatusIndex);  // reads as zeros
+        const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, mine));
+        if (n >= stages && !(ok = wait_bar_warp(&empty[st], ((n / stages) - 1) & 1, abort_flag, budget))) break;
+        if (lane_id == 0) mbar_arrive_expect_tx(&full[st], boxes * P.box * 128);
+        __syncwarp();
+        if (mine) {
+          uint8_t* dst = ring + st * kTileBytes + half * kHalfBytes + bx * P.box * 128;
+          tma_load_4d(dst, map, &full[st], 64 * half, r_first ? row : wk.ph, r_first ? wk.ph : row, pg);
+        }
+      }
+    }
+    // every issued load lands before the CTA exits
+    for (int m = max(0, n - stages); m < n; ++m) mbar_wait(&full[m % stages], (m / stages) & 1, budget);
+  } else if (warp == kWarpMma) {
+    // ------------------------------------------------------------ MMA issue
+    if (lane_id == 0) {
+      const uint64_t dQ0 = sdesc_sw128(smem_u32(sm + L::q), 16, 1024);
+      const uint64_t dK0 = sdesc_sw128(smem_u32(sm + L::k), 16, 1024);
+      const uint64_t dV0 = sdesc_sw128(smem_u32(sm + L::v), kHalfBytes, 1024);
+      // the scores' stream runs two tiles ahead of PV's, each with a walk of its own
+      Walk ws = wk;
+      bool have_s = ws.next(P, NT), have_p = wk.next(P, NT), ok = true, issued = false;
+      int s_step = 0, s_piece = 0, s_tile = 0;  // next score tile of its piece; pieces and key tiles before
+      int p_step = 0, p_tile = 0;
+      long long gs = 0, gp = 0;
+      auto scores = [&]() -> bool {  // issues the next score tile
+        const int slot = gs & 1, kt = NT == 2 ? s_step >> 1 : s_step, kn = s_tile + kt;
+        if (s_step == 0 && !wait_bar(&bars[L::QFull], s_piece & 1, abort_flag, budget)) return false;
+        if ((NT == 1 || slot == 0) && !wait_bar(&bars[L::KFull + kn % L::KS], (kn / L::KS) & 1, abort_flag, budget)) return false;
+        tc_fence_after();
+        issue_s<F16>(tmem + slot * 128, sdesc_add(dQ0, NT == 2 ? slot * kTileBytes : 0), sdesc_add(dK0, (kn % L::KS) * kTileBytes));
+        issued = true;
+        mma_commit(&bars[L::SFull + slot]);
+        if (NT == 1 || slot == 1) mma_commit(&bars[L::KEmpty + kn % L::KS]);
+        ++gs;
+        if (++s_step == (ws.kt1 - ws.kt0) * NT) {
+          mma_commit(&bars[L::QEmpty]);
+          s_tile += ws.kt1 - ws.kt0;
+          s_step = 0;
+          ++s_piece;
+          have_s = ws.next(P, NT);
+        }
+        return true;
+      };
+      for (int i = 0; i < 2 && ok && have_s; ++i) ok = scores();
+      while (ok && have_p) {
+        const int slot = gp & 1, kt = NT == 2 ? p_step >> 1 : p_step, vn = p_tile + kt;
+        if (!(ok = wait_bar(&bars[L::VFull + vn % L::VS], (vn / L::VS) & 1, abort_flag, budget))) break;
+        if (!(ok = wait_bar(&bars[L::PFull + slot], (gp >> 1) & 1, abort_flag, budget))) break;
+        tc_fence_after();
+        issue_pv<F16>(tmem + 256 + slot * 128, tmem + slot * 128, sdesc_add(dV0, (vn % L::VS) * kTileBytes), p_step >= 2);
+        if (NT == 1 || slot == 1) mma_commit(&bars[L::VEmpty + vn % L::VS]);
+        ++gp;
+        if (++p_step == (wk.kt1 - wk.kt0) * NT) {
+          mma_commit(&bars[L::OFull]);
+          p_tile += wk.kt1 - wk.kt0;
+          p_step = 0;
+          have_p = wk.next(P, NT);
+        }
+        if (have_s && !(ok = scores())) break;
+      }
+      if (issued && !ok) {
+        // every MMA done before anyone frees TMEM or shared memory: the K
+        // stages' barriers are no use here, so a bounded pause on a commit of
+        // its own (QFull's phases do not matter any more)
+        mma_commit(&bars[L::QEmpty]);
+        const long long t0 = clock64();
+        const uint32_t ph = static_cast<uint32_t>(s_piece & 1);
+        while (!mbar_try_wait(&bars[L::QEmpty], ph) && clock64() - t0 < budget) {
+        }
+      }
+    }
+  }
+
+  __syncwarp();
+  if (*abort_flag && tid == 0) {
+    atomicOr(c.status, kStatusTimeout);
+    atomicAdd(c.counters + kCtrTimeouts, 1ull);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    __syncwarp();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of an item whose tiles several CTAs held: block (x, y) looks
+// at the border before CTA x + 1 and, if it is an item's first inner border,
+// at rows 32 y .. of that item. A warp takes a row, a lane four columns.
+constexpr int kJoinRows = 32;
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ TcAttnParams P, int nt) {
+  grid_dependency_wait();
+  const CacheAttnParams& c = P.c;
+  const int cta = blockIdx.x + 1;
+  const JoinMeta me = P.meta[cta];
+  if (me.n == 0) return;
+  const long long ctas = min(static_cast<long long>(P.ctas), me.total);
+  auto first_tile = [&](long long x) { return x * me.total / ctas; };
+  if (first_tile(cta - 1) > me.item_start) return;  // an earlier border lies inside the item
+  int last = cta;
+  while (last + 1 < ctas && first_tile(last + 1) < me.item_start + me.n) ++last;
+  const int parts = last - cta + 2;
+  const int64_t slot0 = 2 * static_cast<int64_t>(cta - 1) + (first_tile(cta - 1) == me.item_start ? 0 : 1);
+  const Item it = item_of(P, nt, me.b, me.m);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tile_rows = P.tpt * c.group;
+  for (int r = blockIdx.y * kJoinRows + warp; r < min((static_cast<int>(blockIdx.y) + 1) * kJoinRows, P.part_rows); r += 8) {
+    const int ti = r / tile_rows, rr = r - ti * tile_rows;
+    const int t = (me.m * nt + ti) * P.tpt + rr / c.group, h = me.h * c.group + rr % c.group;
+    if (t >= it.cnt) continue;
+    auto row_of = [&](int i) { return (i == 0 ? slot0 : 2 * static_cast<int64_t>(cta - 1 + i)) * P.part_rows + r; };
+    float m = -INFINITY;
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, P.part_ml[row_of(i)].x);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+    const float m_use = m == -INFINITY ? 0.f : m;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+      const int64_t row = row_of(i);
+      const float2 x = P.part_ml[row];
+      const float4 y = reinterpret_cast<const float4*>(c.part + row * kD)[lane];
+      const float f = ex2(x.x - m_use);
+      l = fmaf(f, x.y, l);
+      o.x = fmaf(f, y.x, o.x);
+      o.y = fmaf(f, y.y, o.y);
+      o.z = fmaf(f, y.z, o.z);
+      o.w = fmaf(f, y.w, o.w);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t off = me.b * c.o_sb + static_cast<int64_t>(t) * c.o_ss + static_cast<int64_t>(h) * c.o_sh + 4 * lane;
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(c.o) + off) =
+        make_uint2(pack_dt(c.kv.dt, o.x * inv, o.y * inv), pack_dt(c.kv.dt, o.z * inv, o.w * inv));
+    if (lane == 0) c.lse[(static_cast<int64_t>(me.b) * c.H + h) * c.T + t] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  }
+}
+
+template <int NT, bool F16, bool TREE>
+cudaError_t launch_t(const TcAttnParams& p, cudaStream_t stream) {
+  auto kern = tc_kernel<NT, F16, TREE>;
+  static std::atomic<uint64_t> configured{0};
+  cudaError_t e = opt_in_smem(kern, Lay<NT>::bytes, configured);
+  if (e != cudaSuccess) return e;
+  return launch_chained(kern, dim3(p.ctas), dim3(kTcThreads), Lay<NT>::bytes, stream, p);
+}
+template <int NT>
+cudaError_t launch_nt(const TcAttnParams& p, bool f16, cudaStream_t stream) {
+  if (p.c.parents) return f16 ? launch_t<NT, true, true>(p, stream) : launch_t<NT, false, true>(p, stream);
+  return f16 ? launch_t<NT, true, false>(p, stream) : launch_t<NT, false, false>(p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_attn_tc(const TcAttnParams& p, int nt, bool f16, cudaStream_t stream) {
+  return nt == 2 ? launch_nt<2>(p, f16, stream) : launch_nt<1>(p, f16, stream);
+}
+
+cudaError_t launch_cache_attn_join(const TcAttnParams& p, int nt, cudaStream_t stream) {
+  if (p.ctas < 2) return cudaSuccess;
+  return launch_chained(join_kernel, dim3(p.ctas - 1, (p.part_rows + kJoinRows - 1) / kJoinRows), dim3(256), 0, stream, p, nt);
+}
+
+}  // namespace st

@@ -67,5 +67,6 @@ st_status check_axes(const st_rope* rope, int D);
 void fill_table(const Ids& ids, const st_rope* rope, float2* out, __half2* out16, unsigned* ctrl, TableParams* t);
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+st_status encode_rows_map(const st_tensor* t, CUtensorMap* map, int* s_first, int box_rows = kTile);
 
 }  // namespace st

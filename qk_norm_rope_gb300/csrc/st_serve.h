@@ -96,6 +96,32 @@ inline int64_t simt_items(int B, int T, int H, int Hkv) {
 cudaError_t launch_cache_attn_simt(const CacheAttnParams& p, cudaStream_t stream);
 cudaError_t launch_cache_attn_simt_join(const CacheAttnParams& p, cudaStream_t stream);
 
+// Tensor-core kernel. A group is NT query tiles of 128 rows (tokens x heads of
+// one K/V head; NT = 2 where a sequence has more than 128 rows a head), an
+// item a (K/V head, sequence, group); its key tiles are dealt out to the CTAs
+// in one continuous range each.
+struct TcAttnParams {
+  CacheAttnParams c;
+  CUtensorMap tmap_k, tmap_v;  // cache pages, boxes of 64 columns x box rows
+  int k_r_first, v_r_first;    // map dims are (d, row, head, page) instead of (d, head, row, page)
+  int box;                     // rows per box: a power of two that divides the page size, 8..128
+  int tpt;                     // tokens per query tile (128 / group)
+  int n_groups;                // groups per sequence
+  int part_rows;               // rows of a partial result
+  int ctas;
+  struct JoinMeta* meta;       // [ctas], workspace
+  float2* part_ml;             // [2 ctas, part_rows] (reference, sum); c.part: [2 ctas, part_rows, D]
+};
+struct JoinMeta {
+  long long total;             // key tiles of the call
+  long long item_start;        // first tile of the item that this CTA's range begins inside of
+  int n;                       // its tiles; 0: the range begins with an item
+  int h, b, m;
+};
+inline int tc_tiles(int T, int group) { return static_cast<int64_t>(T) * group > 128 ? 2 : 1; }
+cudaError_t launch_cache_attn_tc(const TcAttnParams& p, int nt, bool f16, cudaStream_t stream);
+cudaError_t launch_cache_attn_join(const TcAttnParams& p, int nt, cudaStream_t stream);
+
 struct VerifyParams {
   const void* p;                   // target probabilities [B, T, V]
   const void* q;                   // draft probabilities, or null

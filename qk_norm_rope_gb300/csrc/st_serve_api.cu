@@ -105,13 +105,17 @@ st_status check_counts(const st_tensor* t, int B, const int32_t** out) {
 }
 
 struct AttnPlan {
-  CacheAttnParams p;
-  size_t bytes = 0;
+  TcAttnParams tc;        // c: the parameters of either kernel
+  bool tensor = false;    // the tensor-core kernel
+  int nt = 1;
+  size_t bytes = 0, off_ml = 0, off_meta = 0;
 };
 
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
 st_status plan_attn(const st_tensor* q, const st_kv_cache* cache, const st_tensor* parents, AttnPlan* P) {
-  memset(&P->p, 0, sizeof(P->p));
-  CacheAttnParams& p = P->p;
+  memset(&P->tc, 0, sizeof(P->tc));
+  CacheAttnParams& p = P->tc.c;
   st_status st;
   if ((st = check_new_rows(q, "q_rot", &p.B, &p.T, &p.H)) != ST_OK) return st;
   if ((st = check_cache(cache, p.B, &p.kv, "st_cache_attn")) != ST_OK) return st;
@@ -126,6 +130,31 @@ st_status plan_attn(const st_tensor* q, const st_kv_cache* cache, const st_tenso
   }
   P->bytes = 256;
   if (static_cast<int64_t>(p.B) * p.T * p.H == 0) return ST_OK;
+  // The tensor-core kernel takes every 16-bit cache whose pages are whole TMA
+  // boxes (at least one 8-row swizzle atom); fp32 caches and other page sizes
+  // take the CUDA cores.
+  P->tensor = p.kv.dt != ST_F32 && p.kv.page % 8 == 0 && p.kv.n_pages > 0 && p.kv.max_pages > 0;
+  if (P->tensor) {
+    TcAttnParams& t = P->tc;
+    P->nt = tc_tiles(p.T, p.group);
+    t.box = 8;
+    while (t.box < kTile && p.kv.page % (2 * t.box) == 0) t.box *= 2;
+    t.tpt = kTile / p.group;
+    const int64_t tpg = static_cast<int64_t>(t.tpt) * P->nt;
+    t.n_groups = static_cast<int>((p.T + tpg - 1) / tpg);
+    t.part_rows = static_cast<int>(std::min<int64_t>(p.T, tpg)) * p.group;
+    const int64_t cap_tiles = (static_cast<int64_t>(p.kv.max_pages) * p.kv.page + kTile - 1) / kTile;
+    const int64_t items = static_cast<int64_t>(p.B) * p.kv.Hkv * t.n_groups;
+    if (items > (1ll << 40)) return fail(ST_ERR_SHAPE, "too many query rows");
+    t.ctas = static_cast<int>(items >= kSmCount ? kSmCount : std::min<int64_t>(kSmCount, items * cap_tiles));
+    // a CTA leaves at most two parts: one at each end of its range
+    size_t off = align256(static_cast<size_t>(2) * t.ctas * t.part_rows * kD * sizeof(float));
+    P->off_ml = off;
+    off = align256(off + static_cast<size_t>(2) * t.ctas * t.part_rows * sizeof(float2));
+    P->off_meta = off;
+    P->bytes = align256(off + t.ctas * sizeof(JoinMeta));
+    return ST_OK;
+  }
   const int64_t items = simt_items(p.B, p.T, p.H, p.kv.Hkv);
   if (items > (1ll << 30)) return fail(ST_ERR_SHAPE, "too many query rows");
   const int64_t tiles = (static_cast<int64_t>(p.kv.max_pages) * p.kv.page + kSimtKeys - 1) / kSimtKeys;
@@ -204,7 +233,7 @@ st_status st_cache_attn(const st_tensor* q_rot, const st_kv_cache* cache, const 
   AttnPlan P;
   st_status st = plan_attn(q_rot, cache, parents, &P);
   if (st != ST_OK) return st;
-  CacheAttnParams& p = P.p;
+  CacheAttnParams& p = P.tc.c;
   if ((st = check_flat(lens, "lens", p.B, ST_I32)) != ST_OK) return st;
   if ((st = check_counts(counts, p.B, &p.counts)) != ST_OK) return st;
   if (!std::isfinite(scale)) return fail(ST_ERR_INVALID_ARG, "scale must be finite");
@@ -235,6 +264,19 @@ st_status st_cache_attn(const st_tensor* q_rot, const st_kv_cache* cache, const 
   p.counters = dev.counters;
   p.wait_budget = wait_budget();
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  if (P.tensor) {
+    TcAttnParams& t = P.tc;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    t.part_ml = reinterpret_cast<float2*>(ws + P.off_ml);
+    t.meta = reinterpret_cast<JoinMeta*>(ws + P.off_meta);
+    if ((st = encode_rows_map(cache->k, &t.tmap_k, &t.k_r_first, t.box)) != ST_OK) return st;
+    if ((st = encode_rows_map(cache->v, &t.tmap_v, &t.v_r_first, t.box)) != ST_OK) return st;
+    if ((st = cuda_check(launch_counted(ST_K_CACHE_ATTN, stream, [&] { return launch_cache_attn_tc(t, P.nt, p.kv.dt == ST_F16, stream); }),
+                         "cached attention launch")) != ST_OK)
+      return st;
+    return cuda_check(launch_counted(ST_K_CACHE_JOIN, stream, [&] { return launch_cache_attn_join(t, P.nt, stream); }),
+                      "cached attention join launch");
+  }
   if ((st = cuda_check(launch_counted(ST_K_CACHE_ATTN, stream, [&] { return launch_cache_attn_simt(p, stream); }),
                        "cached attention launch")) != ST_OK)
     return st;

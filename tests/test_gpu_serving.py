@@ -175,6 +175,27 @@ def test_attention(cuda_lib, dtype, B, T, H, Hkv, lens, counts, page, is_tree):
     assert torch.equal(bits(cache.k), bits(k)) and torch.equal(bits(cache.v), bits(v))
 
 
+@pytest.mark.parametrize("dtype,B,T,H,Hkv,most,page,is_tree", [
+    ("bf16", 40, 2, 16, 8, 900, 16, False),   # few rows a head: many short items, odd numbers of key tiles
+    ("fp16", 60, 1, 5, 5, 1500, 32, False),
+    ("bf16", 9, 70, 16, 8, 1400, 64, True),   # more than a tile of rows a head
+    ("fp16", 3, 300, 6, 3, 1000, 8, False),
+])
+def test_attention_many_items(cuda_lib, dtype, B, T, H, Hkv, most, page, is_tree):
+    """More key tiles than SMs, so that each SM works through several items, whole ones and parts."""
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, most, (B,), generator=g).tolist()
+    counts = torch.randint(0, T + 1, (B,), generator=g).tolist()
+    q, k, v, pages, parents = attn_case(dtype, B, T, H, Hkv, lens, counts, page, is_tree, seed=40)
+    cache = dev_cache(cuda_lib, k, v, pages)
+    o, lse = cuda_lib.st_cache_attn(q.cuda(), cache, i32(lens).cuda(), counts=i32(counts).cuda(),
+                                    parents=None if parents is None else parents.cuda())
+    cuda_lib.st_check_status()
+    ro, rl, bo, bl = R.attention(q, k, v, pages, lens, counts, parents)
+    R.close("o", o, ro, bo)
+    R.close("lse", lse, rl, bl)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 def test_attention_shared_tree_scale_and_repeat(cuda_lib, dtype):
     """One tree for the whole batch, a scale of its own, large scores (a running maximum that moves), and the same bits
