@@ -1,4 +1,4 @@
-"""Python binding of the st_rope_attn C-ABI (ctypes).
+"""Python binding of the st_rope_attn C-ABI (ctypes; the serving calls in C++).
 
 Argument marshalling only: every step of the computation runs in the CUDA
 library. PyTorch supplies device memory (outputs, workspace) and the current
@@ -19,6 +19,7 @@ pair-duplicated cos/sin tables: pass ``RopeTables(cos, sin)`` in place of
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
 import os
 import threading
@@ -108,6 +109,8 @@ LIB_PATH = _build.LIB
 def lib():
     """The loaded CUDA library (built in-tree on first use if missing)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.build()
@@ -135,16 +138,16 @@ def lib():
             L.st_timing_enable.restype = i
             L.st_timing_read.argtypes = [ctypes.POINTER(st_kernel_times)]
             L.st_timing_read.restype = i
-            K = ctypes.POINTER(st_kv_cache)
-            L.st_cache_append.argtypes = [T, T, T, T, T, fl, R, K, T, T, T, vp]
+            # the serving calls (their Python forms go through st_bind.so)
+            L.st_cache_append.argtypes = [vp] * 5 + [fl] + [vp] * 6
             L.st_cache_append.restype = i
-            L.st_cache_attn_workspace_size.argtypes = [T, K, T]
+            L.st_cache_attn_workspace_size.argtypes = [vp, vp, vp]
             L.st_cache_attn_workspace_size.restype = sz
-            L.st_cache_attn.argtypes = [T, K, T, T, T, fl, T, T, vp, sz, vp]
+            L.st_cache_attn.argtypes = [vp] * 5 + [fl] + [vp] * 3 + [sz, vp]
             L.st_cache_attn.restype = i
-            L.st_tree_verify.argtypes = [T] * 10 + [vp]
+            L.st_tree_verify.argtypes = [vp] * 11
             L.st_tree_verify.restype = i
-            L.st_cache_keep.argtypes = [K, T, T, T, T, vp]
+            L.st_cache_keep.argtypes = [vp] * 6
             L.st_cache_keep.restype = i
             _lib = L
     return _lib
@@ -324,55 +327,43 @@ def st_timing_read() -> dict:
 
 
 # ------------------------------------------------------------------ serving
-def _cache_struct(cache):
-    c = st_kv_cache()
-    c._keep = [_t(cache.k), _t(cache.v), _t(cache.pages)]
-    c.k, c.v, c.pages = (_p(x) for x in c._keep)
-    return c
+# A decoding step makes these calls for every layer on small tensors, so that
+# the host's share counts: they go through st_bind.so (C++) instead of ctypes.
+_bind_mod = None
 
 
-def _device_of(*ts):
-    """The one CUDA device that all given tensors live on."""
-    dev = None
-    for t in ts:
-        for x in (t.tensors() if isinstance(t, RopeTables) else [t.k, t.v, t.pages] if isinstance(t, KVCache) else [t]):
-            if x is None:
-                continue
-            if not x.is_cuda:
-                raise StError(ST_ERR_INVALID_ARG, "all tensors must live on a CUDA device")
-            if dev is None:
-                dev = x.device
-            elif x.device != dev:
-                raise StError(ST_ERR_INVALID_ARG, f"tensors live on {dev} and on {x.device}")
-    return dev
-
-
-def _launch(dev, call):
-    """Runs a C call with ``dev`` as the current device, on that device's
-    current torch stream."""
-    if dev.index == torch.cuda.current_device():
-        _check(call(ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)))
-    else:
-        with torch.cuda.device(dev):
-            _check(call(ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)))
+def _bind():
+    """The serving calls' C++ binding (built in-tree on first use if missing)."""
+    global _bind_mod
+    if _bind_mod is None:
+        lib()
+        with _lock:
+            if _bind_mod is None:
+                spec = importlib.util.spec_from_file_location("st_bind", _build.build_bind())
+                m = importlib.util.module_from_spec(spec)
+                spec.loader.exec_module(m)
+                m.init(StError)
+                _bind_mod = m
+    return _bind_mod
 
 
 def st_cache_append(q, k, v, q_norm_w, k_norm_w, eps, ids, axes_dim, theta, cache, lens, counts=None, q_rot=None):
     """New rows enter the cache: q [B,T,H,D], k, v [B,T,H_kv,D]; k normalised
     and rotated, and v, go to positions lens[b].. of each sequence. Returns the
     normalised, rotated q in the cache's dtype (zero in rows behind counts[b])."""
-    dev = _device_of(q, k, v, q_norm_w, k_norm_w, ids, cache, lens, counts, q_rot)
-    if q_rot is None:
-        q_rot = torch.empty(q.shape, dtype=cache.k.dtype, device=dev)
-    r, c = _rope(ids, axes_dim, theta, None), _cache_struct(cache)
-    _launch(dev, lambda s: lib().st_cache_append(
-        _p(_t(q)), _p(_t(k)), _p(_t(v)), _p(_t(q_norm_w)), _p(_t(k_norm_w)), float(eps), ctypes.byref(r),
-        ctypes.byref(c), _p(_t(lens)), _p(_t(counts)), _p(_t(q_rot)), s))
-    return q_rot
+    m = _bind_mod or _bind()
+    if isinstance(ids, RopeTables):
+        return m.cache_append(q, k, v, q_norm_w, k_norm_w, eps, None, ids.cos, ids.sin, ids.cos_k, ids.sin_k, (), 0.0,
+                              cache.k, cache.v, cache.pages, lens, counts, q_rot)
+    return m.cache_append(q, k, v, q_norm_w, k_norm_w, eps, ids, None, None, None, None, axes_dim, theta, cache.k, cache.v,
+                          cache.pages, lens, counts, q_rot)
 
 
 def st_cache_attn_workspace_size(q_rot, cache, parents=None) -> int:
-    n = lib().st_cache_attn_workspace_size(_p(_t(q_rot)), ctypes.byref(_cache_struct(cache)), _p(_t(parents)))
+    c = st_kv_cache()
+    keep = [_t(cache.k), _t(cache.v), _t(cache.pages)]
+    c.k, c.v, c.pages = (_p(x) for x in keep)
+    n = lib().st_cache_attn_workspace_size(_p(_t(q_rot)), ctypes.byref(c), _p(_t(parents)))
     if n == 0:
         raise StError(ST_ERR_INVALID_ARG, lib().st_last_error().decode())
     return int(n)
@@ -382,50 +373,22 @@ def st_cache_attn(q_rot, cache, lens, counts=None, parents=None, scale=None, o=N
     """Attention of the new rows over the cache (after st_cache_append):
     parents=None for a chain (single tokens, a prompt's chunk), [B|1, T] int32
     for trees of drafted tokens. Returns (o [B,T,H,D], lse [B,H,T] fp32)."""
-    dev = _device_of(q_rot, cache, lens, counts, parents, o, lse, workspace)
-    B, T, H, _ = q_rot.shape
-    if o is None:
-        o = torch.empty(q_rot.shape, dtype=q_rot.dtype, device=dev)
-    if lse is None:
-        lse = torch.empty((B, H, T), dtype=torch.float32, device=dev)
-    if workspace is None:
-        workspace = torch.empty(st_cache_attn_workspace_size(q_rot, cache, parents), dtype=torch.uint8, device=dev)
-    c = _cache_struct(cache)
-    _launch(dev, lambda s: lib().st_cache_attn(
-        _p(_t(q_rot)), ctypes.byref(c), _p(_t(lens)), _p(_t(counts)), _p(_t(parents)), float(scale) if scale else 0.0,
-        _p(_t(o)), _p(_t(lse)), ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size(), s))
-    return o, lse
+    return (_bind_mod or _bind()).cache_attn(q_rot, cache.k, cache.v, cache.pages, lens, counts, parents, scale or 0.0, o,
+                                             lse, workspace)
 
 
 def st_tree_verify(target_probs, draft_probs, tokens, parents, u_accept, u_sample, counts=None, path=None,
                    n_accepted=None, next_token=None):
     """Verification of drafted trees (see the C header): returns (path [B,T]
     int32, the accepted nodes then -1; n_accepted [B] int32; next_token [B])."""
-    dev = _device_of(target_probs, draft_probs, tokens, parents, u_accept, u_sample, counts, path, n_accepted,
-                     next_token)
-    B, T = tokens.shape
-    if path is None:
-        path = torch.empty((B, T), dtype=torch.int32, device=dev)
-    if n_accepted is None:
-        n_accepted = torch.empty((B,), dtype=torch.int32, device=dev)
-    if next_token is None:
-        next_token = torch.empty((B,), dtype=tokens.dtype, device=dev)
-    _launch(dev, lambda s: lib().st_tree_verify(
-        _p(_t(target_probs)), _p(_t(draft_probs)), _p(_t(tokens)), _p(_t(parents)), _p(_t(counts)), _p(_t(u_accept)),
-        _p(_t(u_sample)), _p(_t(path)), _p(_t(n_accepted)), _p(_t(next_token)), s))
-    return path, n_accepted, next_token
+    return (_bind_mod or _bind()).tree_verify(target_probs, draft_probs, tokens, parents, counts, u_accept, u_sample, path,
+                                              n_accepted, next_token)
 
 
 def st_cache_keep(cache, start, rows, n_rows, lens=None):
     """Row start[b] + rows[b, i] of each sequence moves to start[b] + i, for
     i < n_rows[b], in place. Returns the new lengths start + n_rows."""
-    dev = _device_of(cache, start, rows, n_rows, lens)
-    if lens is None:
-        lens = torch.empty(start.shape, dtype=torch.int32, device=dev)
-    c = _cache_struct(cache)
-    _launch(dev, lambda s: lib().st_cache_keep(ctypes.byref(c), _p(_t(start)), _p(_t(rows)), _p(_t(n_rows)),
-                                               _p(_t(lens)), s))
-    return lens
+    return (_bind_mod or _bind()).cache_keep(cache.k, cache.v, cache.pages, start, rows, n_rows, lens)
 
 
 class RopeAttention(torch.autograd.Function):

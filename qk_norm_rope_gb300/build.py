@@ -1,6 +1,7 @@
-"""Builds libst_rope_attn.so in-tree with nvcc for sm_103a (GB300).
+"""Builds libst_rope_attn.so in-tree with nvcc for sm_103a (GB300), and
+st_bind.so, the Python binding of the serving calls, with g++ against torch.
 
-The translation units compile in parallel; the shared object lands in
+The translation units compile in parallel; the shared objects land in
 ``qk_norm_rope_gb300/_build/``. Rebuilds only when a source is newer than the
 library.
 """
@@ -17,6 +18,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libst_rope_attn.so")
+BIND_SRC = os.path.join(CSRC, "st_bind.cpp")
+BIND = os.path.join(OUT, "st_bind.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -70,5 +73,55 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
+def _bind_object() -> str:
+    """Compiles st_bind.cpp against the installed torch; the object's name carries torch's version."""
+    import sysconfig
+
+    import torch
+    t = os.path.dirname(os.path.abspath(torch.__file__))
+    obj = os.path.join(OUT, f"st_bind.{torch.__version__}.o")
+    head = os.path.join(ROOT, "include", "st_rope_attn.h")
+    if os.path.exists(obj) and os.path.getmtime(obj) >= max(os.path.getmtime(BIND_SRC), os.path.getmtime(head)):
+        return obj
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{os.path.join(ROOT, 'include')}",
+           f"-I{sysconfig.get_paths()['include']}", f"-isystem{t}/include", f"-isystem{t}/include/torch/csrc/api/include",
+           f"-isystem{cuda}/include", "-c", BIND_SRC, "-o", obj + f".{os.getpid()}.tmp"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for st_bind.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(obj + f".{os.getpid()}.tmp", obj)
+    return obj
+
+
+def build_bind(obj: str | None = None) -> str:
+    """The Python binding of the serving calls, linked to libst_rope_attn.so beside it."""
+    import torch
+    build_lib = build()
+    obj = obj or _bind_object()
+    if os.path.exists(BIND) and os.path.getmtime(BIND) >= os.path.getmtime(obj):
+        return BIND
+    t = os.path.join(os.path.dirname(os.path.abspath(torch.__file__)), "lib")
+    tmp = BIND + f".{os.getpid()}.tmp"
+    cmd = ["g++", "-shared", obj, "-o", tmp, f"-L{t}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           f"-L{os.path.dirname(build_lib)}", "-l:libst_rope_attn.so", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{t}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed for st_bind.so:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BIND)
+    return BIND
+
+
+def build_all(force: bool = False, verbose: bool = False) -> None:
+    """The library and the binding, their compilers side by side."""
+    os.makedirs(OUT, exist_ok=True)
+    with ThreadPoolExecutor(max_workers=1) as ex:
+        obj = ex.submit(_bind_object)
+        build(force=force, verbose=verbose)
+        build_bind(obj.result())
+
+
 if __name__ == "__main__":
-    print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
+    build_all(force="--force" in sys.argv, verbose="-v" in sys.argv)
+    print(LIB)
