@@ -11,10 +11,10 @@
 // (O unnormalised, reference, sum) in the workspace, at most one such part at
 // each end of its range, and the join kernel puts them together.
 //
-// Roles (480 threads, one CTA per SM):
+// Roles (512 threads, one CTA per SM):
 //   warps 0-7   softmax, two groups of four warps; thread = query row = TMEM lane
 //   warps 8-11  Q rows of the next item into shared memory
-//   warp 12     TMEM allocation, tcgen05.mma issue (one thread)
+//   warp 12/15  tcgen05.mma issue for slot 0 / 1 (one thread each); TMEM allocation
 //   warp 13/14  TMA of K / V boxes, one lane per box
 // TMEM: S0 | S1 | O0 | O1, 128 fp32 columns each; P (16-bit) overwrites the
 // first half of its S and feeds PV from TMEM. The stream of score tiles
@@ -22,7 +22,8 @@
 // tile, with NT = 1 (decoding: few rows, bound by the reading of K and V) the
 // slots take alternate key tiles with accumulators of their own, which are
 // merged at the end; either way one slot's softmax runs under the other's
-// MMAs. The scores run two tiles ahead of PV, across the borders of items.
+// MMAs. A slot's scores run one tile ahead of its PV, across the borders of
+// items.
 #include <atomic>
 #include "st_kernels.h"
 #include "st_serve.h"
@@ -31,24 +32,35 @@ namespace st {
 
 namespace {
 
-constexpr int kSoftWarps = 8, kWarpQ0 = 8, kQWarps = 4, kWarpMma = 12, kWarpK = 13, kWarpV = 14;
-constexpr int kTcWarps = 15, kTcThreads = kTcWarps * 32;
+constexpr int kSoftWarps = 8, kWarpQ0 = 8, kQWarps = 4, kWarpMma = 12, kWarpK = 13, kWarpV = 14;  // warp 15: the second slot's MMAs
+constexpr int kTcWarps = 16, kTcThreads = kTcWarps * 32;
+// Registers per thread: the softmax threads hold a row of 128 scores. 256 * 184 + 256 * 72 = 512 * 128.
+constexpr int kRegsSoft = 184, kRegsRest = 72;
 constexpr float kRescale = 8.0f;  // O is rescaled when the running maximum grows by more than this (base 2)
 
 template <int NT>
 struct Lay {  // shared memory, offsets from a 1024-byte aligned base
-  static constexpr int KS = 3, VS = NT == 1 ? 3 : 2;
+  // With NT = 1 a stage belongs to one slot for good (even counts): a slot's
+  // thread waits for every phase of the stages that it uses, and a wait on
+  // parity says nothing where phases went by unseen.
+  static constexpr int KS = NT == 1 ? 2 : 3, VS = NT == 1 ? 4 : 2;
+  static_assert(NT == 2 || (KS % 2 == 0 && VS % 2 == 0), "stages of one slot");
   static constexpr uint32_t q = 0, k = NT * kTileBytes, v = k + KS * kTileBytes, bar = v + VS * kTileBytes;
   static constexpr uint32_t ml = bar + 512;          // [2][128] (reference, sum), NT = 1
   static constexpr uint32_t bytes = ml + (NT == 1 ? 2 * 128 * 8 : 0);
   enum { QFull = 0, QEmpty, KFull, KEmpty = KFull + KS, VFull = KEmpty + KS, VEmpty = VFull + VS, SFull = VEmpty + VS,
-         PFull = SFull + 2, OFull = PFull + 2, MlFull, ORead = MlFull + 2, Num = ORead + 2 };
+         PFull = SFull + 2, OFull = PFull + 2, MlFull, ORead = MlFull + 2, Drain = ORead + 2, Num = Drain + 2 };
 };
 static_assert(Lay<1>::bytes <= 232448 && Lay<2>::bytes <= 232448, "shared memory");
 static_assert(Lay<1>::Num * 8 + 128 <= 512 && Lay<2>::Num * 8 + 128 <= 512, "barrier area");
 
 __device__ __forceinline__ constexpr uint32_t kofs(int kk) { return (kk >> 2) * kHalfBytes + (kk & 3) * 32; }
 __device__ __forceinline__ constexpr uint32_t mofs(int kk) { return kk * 2048; }
+
+// Asynchronous 16-byte copy into shared memory; zeros when !there.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
 
 struct Item {
   int prefix, keys, cnt, n;  // n: key tiles
@@ -216,25 +228,22 @@ __device__ __forceinline__ uint32_t key_bits(int j0, const Item& it, int t, cons
 template <bool F16, bool MASK>
 __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float sc, const uint32_t (&mb)[4], bool first,
                                              float& m_run, float& l_run) {
-  uint32_t ra[16], rb[16];
+  uint32_t x[4][32];  // the whole row: TMEM is read once
+#pragma unroll
+  for (int i = 0; i < 4; ++i) tmem_ld32_issue(tS + 32 * i, x[i]);
   float m0 = -INFINITY, m1 = -INFINITY;
-  tmem_ld16_issue(tS, ra);
 #pragma unroll
-  for (int q8 = 0; q8 < 8; ++q8) {
-    uint32_t(&cur)[16] = (q8 & 1) ? rb : ra;
-    uint32_t(&nxt)[16] = (q8 & 1) ? ra : rb;
-    tmem_ld_wait16(cur);
-    if (q8 < 7) tmem_ld16_issue(tS + 16 * (q8 + 1), nxt);
+  for (int i = 0; i < 4; ++i) {
+    tmem_ld_wait32(x[i]);
     if constexpr (MASK) {
-      const uint32_t bits = mb[q8 >> 1] >> ((q8 & 1) * 16);
 #pragma unroll
-      for (int t = 0; t < 16; ++t)
-        if (!((bits >> t) & 1u)) cur[t] = 0xff800000u;
+      for (int t = 0; t < 32; ++t)
+        if (!((mb[i] >> t) & 1u)) x[i][t] = 0xff800000u;
     }
 #pragma unroll
-    for (int t = 0; t < 16; t += 4) {
-      m0 = fmax3(m0, __uint_as_float(cur[t]), __uint_as_float(cur[t + 1]));
-      m1 = fmax3(m1, __uint_as_float(cur[t + 2]), __uint_as_float(cur[t + 3]));
+    for (int t = 0; t < 32; t += 4) {
+      m0 = fmax3(m0, __uint_as_float(x[i][t]), __uint_as_float(x[i][t + 1]));
+      m1 = fmax3(m1, __uint_as_float(x[i][t + 2]), __uint_as_float(x[i][t + 3]));
     }
   }
   const float mt = fmaxf(m0, m1) * sc;
@@ -246,28 +255,17 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float sc,
   const float m_use = m_run == -INFINITY ? 0.f : m_run;
   const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-m_use, -m_use);
   float2 ls = make_float2(0.f, 0.f);
-  tmem_ld16_issue(tS, ra);
 #pragma unroll
-  for (int q8 = 0; q8 < 8; ++q8) {
-    uint32_t(&cur)[16] = (q8 & 1) ? rb : ra;
-    uint32_t(&nxt)[16] = (q8 & 1) ? ra : rb;
-    tmem_ld_wait16(cur);
-    if (q8 < 7) tmem_ld16_issue(tS + 16 * (q8 + 1), nxt);
-    if constexpr (MASK) {
-      const uint32_t bits = mb[q8 >> 1] >> ((q8 & 1) * 16);
+  for (int i = 0; i < 4; ++i) {
+    uint32_t pw[16];
 #pragma unroll
-      for (int t = 0; t < 16; ++t)
-        if (!((bits >> t) & 1u)) cur[t] = 0xff800000u;
-    }
-    uint32_t pw[8];
-#pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      const float2 x = __ffma2_rn(make_float2(__uint_as_float(cur[2 * t]), __uint_as_float(cur[2 * t + 1])), sc2, nm2);
-      const float p0 = ex2(x.x), p1 = ex2(x.y);
+    for (int t = 0; t < 16; ++t) {
+      const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[i][2 * t]), __uint_as_float(x[i][2 * t + 1])), sc2, nm2);
+      const float p0 = ex2(y.x), p1 = ex2(y.y);
       ls = __fadd2_rn(ls, make_float2(p0, p1));
       pw[t] = pack16<F16>(p0, p1);
     }
-    tmem_st8(tS + 8 * q8, pw);
+    tmem_st16(tS + 16 * i, pw);
   }
   l_run = l_run * corr + (ls.x + ls.y);
   if (!first && __any_sync(0xffffffffu, corr != 1.f)) {  // warp-uniform: tcgen05.ld/st are collective
@@ -297,7 +295,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::bar);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + L::Num);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
-  Start* start = reinterpret_cast<Start*>(tslot + 2);
+  int* pipe_lock = reinterpret_cast<int*>(tslot + 2);  // held by the slot that is issuing MMAs
+  Start* start = reinterpret_cast<Start*>(tslot + 4);
   const int tid = threadIdx.x, warp = tid >> 5, lane_id = tid & 31;
   const long long budget = c.wait_budget;
 
@@ -307,23 +306,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
   }
   if (tid == 0) {
     mbar_init(&bars[L::QFull], kQWarps * 32);
-    mbar_init(&bars[L::QEmpty], 1);
+    mbar_init(&bars[L::QEmpty], 2);
     for (int s = 0; s < L::KS; ++s) {
       mbar_init(&bars[L::KFull + s], 1);
-      mbar_init(&bars[L::KEmpty + s], 1);
+      mbar_init(&bars[L::KEmpty + s], NT);  // NT = 1: a tile is one slot's
     }
     for (int s = 0; s < L::VS; ++s) {
       mbar_init(&bars[L::VFull + s], 1);
-      mbar_init(&bars[L::VEmpty + s], 1);
+      mbar_init(&bars[L::VEmpty + s], NT);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars[L::SFull + s], 1);
       mbar_init(&bars[L::PFull + s], 128);
       mbar_init(&bars[L::MlFull + s], 128);
       mbar_init(&bars[L::ORead + s], 128);
+      mbar_init(&bars[L::Drain + s], 1);
     }
-    mbar_init(&bars[L::OFull], 1);
+    mbar_init(&bars[L::OFull], 2);
     *abort_flag = 0;
+    *pipe_lock = 0;
     fence_mbar_init();
   }
   if (tid == kWarpK * 32) tma_prefetch_desc(&P.tmap_k);
@@ -344,6 +345,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
 
   if (warp < kSoftWarps) {
     // -------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
     // padding rows, and every row of a sequence without room for keys
     if (c.counts || static_cast<int64_t>(c.kv.max_pages) * c.kv.page == 0) {
       for (int b = blockIdx.x; b < c.B; b += gridDim.x) {
@@ -408,9 +410,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
           }
         }
         first = false;
-        if (j0 + kTile > wk.it.keys && (NT == 1 || slot == 0)) {
+        if (j0 + kTile > wk.it.keys) {
           // rows of V behind the last key hold anything: zero weights do not
-          // silence infinities and NaN, zeros do
+          // silence infinities and NaN, zeros do (with NT = 2 both slots write
+          // the same zeros: neither waits for the other)
           const int st = (vc + kt - wk.kt0) % L::VS;
           if (!(ok = wait_bar_warp(&bars[L::VFull + st], ((vc + kt - wk.kt0) / L::VS) & 1, abort_flag, budget))) break;
           if (j0 + r >= wk.it.keys) zero_row(sm + L::v + st * kTileBytes, r);
@@ -466,13 +469,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
             const int q4 = 2 * slot + q;
             uint32_t a[32], d[32];
             float y[32];
-            if (mine) tmem_ld32(tO + 32 * q4, a);
-            if (theirs) tmem_ld32(tOther + 32 * q4, d);
+            tmem_ld32(tO + 32 * q4, a);
+            tmem_ld32(tOther + 32 * q4, d);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              float v = mine ? __uint_as_float(a[e]) * f0 : 0.f;
-              if (theirs) v = fmaf(__uint_as_float(d[e]), f1, v);
-              y[e] = v * inv;
+            for (int e = 0; e < 32; ++e) {  // a slot without tiles holds anything
+              const float v0 = mine ? __uint_as_float(a[e]) : 0.f, v1 = theirs ? __uint_as_float(d[e]) : 0.f;
+              y[e] = fmaf(v1, f1, v0 * f0) * inv;
             }
             if (valid) store_chunk32(whole ? c.o : c.part, whole ? ooff : prow * kD, whole ? c.kv.dt : kDtF32, q4, y);
           }
@@ -493,6 +495,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
     }
   } else if (warp < kWarpQ0 + kQWarps) {
     // ---------------------------------------------------------------- Q rows
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     const int qt = tid - kWarpQ0 * 32;
     int n_piece = 0;
     while (wk.next(P, NT)) {
@@ -503,116 +506,152 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
         const int nv = max(0, min(P.tpt, wk.it.cnt - t0)) * G;     // rows that are there
         const int fill = ((nv + 31) & ~31) * 16;                   // whole warps of rows: zeros behind them
         uint8_t* tile = sm + L::q + ti * kTileBytes;
-#pragma unroll 1
-        for (int e0 = qt; e0 < fill; e0 += kQWarps * 32 * 8) {
-          uint4 x[8];
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const int e = e0 + u * kQWarps * 32, row = e >> 4;
-            x[u] = make_uint4(0, 0, 0, 0);
-            if (row < nv) {
-              const int tt = t0 + row / G, h = wk.ph * G + row % G;
-              x[u] = ldg_nc_v4(static_cast<const uint16_t*>(c.q.p) + wk.pb * c.q.sb + tt * c.q.ss + h * c.q.sh + 8 * (e & 15));
-            }
-          }
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const int e = e0 + u * kQWarps * 32, row = e >> 4, ch = e & 15;
-            if (e < fill) *reinterpret_cast<uint4*>(tile + (ch >> 3) * kHalfBytes + sw128_off(row, ch & 7)) = x[u];
-          }
+        for (int e = qt; e < fill; e += kQWarps * 32) {
+          const int row = e >> 4, ch = e & 15, rr = row < nv ? row : 0;
+          const int tt = t0 + rr / G, h = wk.ph * G + rr % G;
+          cp_async16(tile + (ch >> 3) * kHalfBytes + sw128_off(row, ch & 7),
+                     static_cast<const uint16_t*>(c.q.p) + wk.pb * c.q.sb + tt * c.q.ss + h * c.q.sh + 8 * ch, row < nv);
         }
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async_smem();
       mbar_arrive(&bars[L::QFull]);
       ++n_piece;
     }
-  } else if (warp == kWarpK || warp == kWarpV) {
-    // ------------------------------------------------------- TMA of K and V
-    const bool is_k = warp == kWarpK;
-    const int stages = is_k ? L::KS : L::VS;
-    uint64_t* full = &bars[is_k ? L::KFull : L::VFull];
-    uint64_t* empty = &bars[is_k ? L::KEmpty : L::VEmpty];
-    const CUtensorMap* map = is_k ? &P.tmap_k : &P.tmap_v;
-    const bool r_first = (is_k ? P.k_r_first : P.v_r_first) != 0;
-    uint8_t* ring = sm + (is_k ? L::k : L::v);
-    const int nb = kTile / P.box, half = lane_id / nb, bx = lane_id - half * nb;  // lanes 0 .. 2 nb - 1
-    int n = 0;
-    bool ok = true;
-    while (ok && wk.next(P, NT)) {
-      for (int kt = wk.kt0; kt < wk.kt1; ++kt, ++n) {
-        const int st = n % stages;
-        const int j = kt * kTile + bx * P.box;
-        const bool mine = half < 2 && j < wk.it.keys;
-        int pg = 0, row = 0;
-        if (mine && !kv_locate(c.kv, wk.pb, j, &pg, &row)) atomicOr(c.status, kStatusIndex);  // reads as zeros
-        const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, mine));
-        if (n >= stages && !(ok = wait_bar_warp(&empty[st], ((n / stages) - 1) & 1, abort_flag, budget))) break;
-        if (lane_id == 0) mbar_arrive_expect_tx(&full[st], boxes * P.box * 128);
-        __syncwarp();
-        if (mine) {
-          uint8_t* dst = ring + st * kTileBytes + half * kHalfBytes + bx * P.box * 128;
-          tma_load_4d(dst, map, &full[st], 64 * half, r_first ? row : wk.ph, r_first ? wk.ph : row, pg);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (warp == kWarpK || warp == kWarpV) {
+      // ------------------------------------------------------- TMA of K and V
+      const bool is_k = warp == kWarpK;
+      const int stages = is_k ? L::KS : L::VS;
+      uint64_t* full = &bars[is_k ? L::KFull : L::VFull];
+      uint64_t* empty = &bars[is_k ? L::KEmpty : L::VEmpty];
+      const CUtensorMap* map = is_k ? &P.tmap_k : &P.tmap_v;
+      const bool r_first = (is_k ? P.k_r_first : P.v_r_first) != 0;
+      uint8_t* ring = sm + (is_k ? L::k : L::v);
+      const int nb = kTile / P.box, half = lane_id / nb, bx = lane_id - half * nb;  // lanes 0 .. 2 nb - 1
+      int n = 0;
+      bool ok = true;
+      while (ok && wk.next(P, NT)) {
+        for (int kt = wk.kt0; kt < wk.kt1; ++kt, ++n) {
+          const int st = n % stages;
+          const int j = kt * kTile + bx * P.box;
+          const bool mine = half < 2 && j < wk.it.keys;
+          int pg = 0, row = 0;
+          if (mine && !kv_locate(c.kv, wk.pb, j, &pg, &row)) atomicOr(c.status, kStatusIndex);  // reads as zeros
+          const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, mine));
+          if (n >= stages && !(ok = wait_bar_warp(&empty[st], ((n / stages) - 1) & 1, abort_flag, budget))) break;
+          if (lane_id == 0) mbar_arrive_expect_tx(&full[st], boxes * P.box * 128);
+          __syncwarp();
+          if (mine) {
+            uint8_t* dst = ring + st * kTileBytes + half * kHalfBytes + bx * P.box * 128;
+            tma_load_4d(dst, map, &full[st], 64 * half, r_first ? row : wk.ph, r_first ? wk.ph : row, pg);
+          }
         }
       }
-    }
-    // every issued load lands before the CTA exits
-    for (int m = max(0, n - stages); m < n; ++m) mbar_wait(&full[m % stages], (m / stages) & 1, budget);
-  } else if (warp == kWarpMma) {
-    // ------------------------------------------------------------ MMA issue
-    if (lane_id == 0) {
-      const uint64_t dQ0 = sdesc_sw128(smem_u32(sm + L::q), 16, 1024);
+      // every issued load lands before the CTA exits
+      for (int m = max(0, n - stages); m < n; ++m) mbar_wait(&full[m % stages], (m / stages) & 1, budget);
+    } else if (lane_id == 0) {
+      // ------------------------------------------------------------ MMA issue
+      // one thread per slot: its waits run under the other's MMAs
+      const int slot = warp == kWarpMma ? 0 : 1;
+      const uint32_t tS = tmem + slot * 128, tO = tmem + 256 + slot * 128;
+      const uint64_t dQ = sdesc_sw128(smem_u32(sm + L::q) + (NT == 2 ? slot * kTileBytes : 0), 16, 1024);
       const uint64_t dK0 = sdesc_sw128(smem_u32(sm + L::k), 16, 1024);
       const uint64_t dV0 = sdesc_sw128(smem_u32(sm + L::v), kHalfBytes, 1024);
-      // the scores' stream runs two tiles ahead of PV's, each with a walk of its own
+      // the scores' stream runs one of the slot's tiles ahead of PV's, each with
+      // a walk of its own; kn counts key tiles over all pieces
       Walk ws = wk;
-      bool have_s = ws.next(P, NT), have_p = wk.next(P, NT), ok = true, issued = false;
-      int s_step = 0, s_piece = 0, s_tile = 0;  // next score tile of its piece; pieces and key tiles before
-      int p_step = 0, p_tile = 0;
-      long long gs = 0, gp = 0;
-      auto scores = [&]() -> bool {  // issues the next score tile
-        const int slot = gs & 1, kt = NT == 2 ? s_step >> 1 : s_step, kn = s_tile + kt;
-        if (s_step == 0 && !wait_bar(&bars[L::QFull], s_piece & 1, abort_flag, budget)) return false;
-        if ((NT == 1 || slot == 0) && !wait_bar(&bars[L::KFull + kn % L::KS], (kn / L::KS) & 1, abort_flag, budget)) return false;
-        tc_fence_after();
-        issue_s<F16>(tmem + slot * 128, sdesc_add(dQ0, NT == 2 ? slot * kTileBytes : 0), sdesc_add(dK0, (kn % L::KS) * kTileBytes));
-        issued = true;
-        mma_commit(&bars[L::SFull + slot]);
-        if (NT == 1 || slot == 1) mma_commit(&bars[L::KEmpty + kn % L::KS]);
-        ++gs;
-        if (++s_step == (ws.kt1 - ws.kt0) * NT) {
-          mma_commit(&bars[L::QEmpty]);
-          s_tile += ws.kt1 - ws.kt0;
-          s_step = 0;
-          ++s_piece;
-          have_s = ws.next(P, NT);
-        }
+      bool ok = true, issued = false;
+      int s_left = 0, s_kn = 0, s_next = 0, s_piece = -1, p_left = 0, p_kn = 0, p_next = 0, p_done = 0, p_piece = 0;
+      // Enters the next piece: its first key tile and its number of tiles for
+      // this slot (none, where NT = 1 and its only tile is the other slot's).
+      auto enter = [&](Walk& w, int& kn, int& next, int& left) -> bool {
+        if (!w.next(P, NT)) return false;
+        const int tiles = w.kt1 - w.kt0;
+        // NT = 1: the slots take alternate tiles of the whole stream
+        const int skip = NT == 2 ? 0 : (slot ^ next) & 1;
+        kn = next + skip;
+        left = NT == 2 ? tiles : (tiles - skip + 1) / 2;
+        next += tiles;
         return true;
       };
-      for (int i = 0; i < 2 && ok && have_s; ++i) ok = scores();
-      while (ok && have_p) {
-        const int slot = gp & 1, kt = NT == 2 ? p_step >> 1 : p_step, vn = p_tile + kt;
-        if (!(ok = wait_bar(&bars[L::VFull + vn % L::VS], (vn / L::VS) & 1, abort_flag, budget))) break;
-        if (!(ok = wait_bar(&bars[L::PFull + slot], (gp >> 1) & 1, abort_flag, budget))) break;
-        tc_fence_after();
-        issue_pv<F16>(tmem + 256 + slot * 128, tmem + slot * 128, sdesc_add(dV0, (vn % L::VS) * kTileBytes), p_step >= 2);
-        if (NT == 1 || slot == 1) mma_commit(&bars[L::VEmpty + vn % L::VS]);
-        ++gp;
-        if (++p_step == (wk.kt1 - wk.kt0) * NT) {
-          mma_commit(&bars[L::OFull]);
-          p_tile += wk.kt1 - wk.kt0;
-          p_step = 0;
-          have_p = wk.next(P, NT);
+      bool more = true;
+      // makes the slot's next score tile ready to be issued, if any is left
+      auto find_scores = [&]() -> bool {
+        while (s_left == 0) {
+          if (!enter(ws, s_kn, s_next, s_left)) {
+            more = false;
+            return true;
+          }
+          ++s_piece;
+          if (!wait_bar(&bars[L::QFull], s_piece & 1, abort_flag, budget)) return false;
+          if (s_left == 0) mma_commit(&bars[L::QEmpty]);  // a piece of one tile, the other slot's
         }
-        if (have_s && !(ok = scores())) break;
+        return wait_bar(&bars[L::KFull + s_kn % L::KS], (s_kn / L::KS) & 1, abort_flag, budget);
+      };
+      auto scores = [&]() {
+        issue_s<F16>(tS, dQ, sdesc_add(dK0, (s_kn % L::KS) * kTileBytes));
+        issued = true;
+        mma_commit(&bars[L::SFull + slot]);
+        mma_commit(&bars[L::KEmpty + s_kn % L::KS]);
+        s_kn += NT == 2 ? 1 : 2;
+        if (--s_left == 0) mma_commit(&bars[L::QEmpty]);
+      };
+      // NT = 2: a slot's PV and next scores enter the tensor pipe as one batch:
+      // two threads' MMAs taken in turns end together, and the slots' softmax
+      // then runs side by side with the tensor pipe idle (2048-token chunk after
+      // 16384 tokens: 563 us without the lock, 465 with it).
+      auto batch = [&](auto&& issue) -> bool {
+        if constexpr (NT == 1) {
+          tc_fence_after();
+          issue();
+          return true;
+        }
+        const long long t0 = clock64();
+        while (atomicCAS(pipe_lock, 0, 1) != 0) {
+          if (*abort_flag || clock64() - t0 > budget) {
+            *abort_flag = 1;
+            return false;
+          }
+        }
+        tc_fence_after();
+        issue();
+        __threadfence_block();
+        atomicExch(pipe_lock, 0);
+        return true;
+      };
+      ok = find_scores() && (!more || batch(scores));
+      while (ok && enter(wk, p_kn, p_next, p_left)) {
+        for (int i = 0; i < p_left; ++i, ++p_done) {
+          const bool same = s_left > 0;  // the next scores are of the same piece: Q is there
+          if (same && !(ok = find_scores())) break;
+          if (!(ok = wait_bar(&bars[L::VFull + p_kn % L::VS], (p_kn / L::VS) & 1, abort_flag, budget))) break;
+          if (!(ok = wait_bar(&bars[L::PFull + slot], p_done & 1, abort_flag, budget))) break;
+          ok = batch([&] {
+            issue_pv<F16>(tO, tS, sdesc_add(dV0, (p_kn % L::VS) * kTileBytes), i > 0);
+            mma_commit(&bars[L::VEmpty + p_kn % L::VS]);
+            if (i + 1 == p_left) mma_commit(&bars[L::OFull]);
+            if (same) scores();
+          });
+          if (!ok) break;
+          p_kn += NT == 2 ? 1 : 2;
+          if (!same && more && !(ok = find_scores() && (!more || batch(scores)))) break;
+        }
+        if (!ok) break;
+        if (p_left == 0) {
+          // nothing of this piece is this slot's: its arrival must not fall
+          // into the phase of the piece before, which the other slot may be at
+          if (p_piece > 0 && !(ok = wait_bar(&bars[L::OFull], (p_piece - 1) & 1, abort_flag, budget))) break;
+          mma_commit(&bars[L::OFull]);
+        }
+        ++p_piece;
       }
       if (issued && !ok) {
-        // every MMA done before anyone frees TMEM or shared memory: the K
-        // stages' barriers are no use here, so a bounded pause on a commit of
-        // its own (QFull's phases do not matter any more)
-        mma_commit(&bars[L::QEmpty]);
+        // every MMA of this thread done before anyone frees TMEM or shared memory
+        mma_commit(&bars[L::Drain + slot]);
         const long long t0 = clock64();
-        const uint32_t ph = static_cast<uint32_t>(s_piece & 1);
-        while (!mbar_try_wait(&bars[L::QEmpty], ph) && clock64() - t0 < budget) {
+        while (!mbar_try_wait(&bars[L::Drain + slot], 0) && clock64() - t0 < budget) {
         }
       }
     }
