@@ -12,12 +12,11 @@ namespace {
 // ------------------------------------------------------------------ append
 // Per token and head: y = rotate(x / sqrt(mean x^2 + eps) * w), every product
 // in fp32 and one rounding to the cache's type; v is copied. Memory bound:
-// each row is read once and written once. A row belongs to a half-warp (16
-// lanes x 8 elements), a block to `tpb` tokens whose (cos, sin) it computes
-// once in shared memory for all of their heads, while the first rows' loads
-// are in flight.
-constexpr int kAppThreads = 256;
-constexpr int kAppBatch = 4;  // rows per half-warp whose loads are issued together
+// each row is read once and written once. A warp is a unit of its own (no
+// block barrier): 2 NI rows of one token, a half-warp (16 lanes x 8 elements)
+// per row, all NI loads of a half-warp in flight before the token's (cos, sin)
+// pairs, two per lane, are computed and shared through shared memory.
+constexpr int kAppWarps = 4;
 
 __device__ __forceinline__ void store_chunk8(void* base, int64_t off, int dt, int c, const float (&v)[8]) {
   if (dt == kDtF32) {
@@ -30,113 +29,107 @@ __device__ __forceinline__ void store_chunk8(void* base, int64_t off, int dt, in
   }
 }
 
-__global__ void __launch_bounds__(kAppThreads) append_kernel(const __grid_constant__ AppendParams p, int hpt) {
-  __shared__ float2 tab[4][kPairs];
-  __shared__ int loc[4][2];
-  grid_dependency_wait();
-  const int tpb = (kAppThreads / 16) / hpt;  // tokens per block: 1, 2 or 4
-  const int hw = threadIdx.x >> 4, l = threadIdx.x & 15;
-  const int slot = hw / hpt, r_first = hw - slot * hpt;
-  const int64_t n_tok = static_cast<int64_t>(p.B) * p.T;
-  const int64_t tok = static_cast<int64_t>(blockIdx.x) * tpb + slot;
-  const bool there = tok < n_tok;
-  const int b = there ? static_cast<int>(tok / p.T) : 0, t = there ? static_cast<int>(tok - static_cast<int64_t>(b) * p.T) : 0;
-  const int Hkv = p.kv.Hkv, n_rows = p.H + 2 * Hkv;
-  const bool live = there && t < row_count(p.counts, b, p.T);
-
-  float x[kAppBatch][8];
-  auto fetch = [&](int r0) {
-#pragma unroll
-    for (int u = 0; u < kAppBatch; ++u) {
-      const int r = r0 + u * hpt;
-      if (live && r < n_rows) {
-        const RowTensor& src = r < p.H ? p.q : (r < p.H + Hkv ? p.k : p.v);
-        const int h = r < p.H ? r : (r < p.H + Hkv ? r - p.H : r - p.H - Hkv);
-        load_chunk8(src.p, b * src.sb + t * src.ss + h * src.sh, src.dt, l, x[u]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[u][e] = 0.f;
-      }
-    }
-  };
-  fetch(r_first);
-
-  // (cos, sin) of the block's tokens: the angle reduced in fp64 so that far
-  // positions keep full fp32 accuracy; or entry 2j of the caller's tables
-  for (int e = threadIdx.x; e < tpb * kPairs; e += kAppThreads) {
-    const int sl = e / kPairs, pr = e % kPairs;
-    const int64_t tk = static_cast<int64_t>(blockIdx.x) * tpb + sl;
-    float2 cs = make_float2(1.f, 0.f);
-    if (tk < n_tok) {
-      const int bb = static_cast<int>(tk / p.T), tt = static_cast<int>(tk - static_cast<int64_t>(bb) * p.T);
-      const int bt = p.tab.Bt == 1 ? 0 : bb;
-      if (p.tab.cos) {
-        cs.x = table_elem(p.tab.cos, p.tab.tab_dtype, bt * p.tab.c_sb + static_cast<int64_t>(tt) * p.tab.c_ss + (2 * pr) * p.tab.c_sd);
-        cs.y = table_elem(p.tab.sin, p.tab.tab_dtype, bt * p.tab.s_sb + static_cast<int64_t>(tt) * p.tab.s_ss + (2 * pr) * p.tab.s_sd);
-      } else {
-        const int64_t off = bt * p.tab.i_sb + static_cast<int64_t>(tt) * p.tab.i_ss + p.tab.axis_of[pr] * p.tab.i_sa;
-        const double id = p.tab.ids_f32 ? static_cast<double>(static_cast<const float*>(p.tab.ids)[off])
-                                        : static_cast<double>(static_cast<const int32_t*>(p.tab.ids)[off]);
-        cs = pair_cos_sin(id, p.tab.omega[pr]);
-      }
-      if (pr == 0) {
-        int pg = -1, row = 0;
-        if (tt < row_count(p.counts, bb, p.T) &&
-            !kv_locate(p.kv, bb, static_cast<int64_t>(__ldg(p.lens + bb)) + tt, &pg, &row)) {
-          pg = -1;
-          atomicOr(p.status, kStatusIndex);
-        }
-        loc[sl][0] = pg;
-        loc[sl][1] = row;
-      }
-    }
-    tab[sl][pr] = cs;
+// (cos, sin) of pair `pr` at token (b, t). Integer positions: position times
+// the pair's turns per position in 64-bit fixed point, whose low 64 bits are
+// the fraction of a turn, exactly reduced however far the position.
+__device__ __forceinline__ float2 append_pair(const AppendParams& p, int b, int t, int pr) {
+  const TableParams& tab = p.tab;
+  const int bt = tab.Bt == 1 ? 0 : b;
+  float2 cs;
+  if (tab.cos) {
+    cs.x = table_elem(tab.cos, tab.tab_dtype, bt * tab.c_sb + static_cast<int64_t>(t) * tab.c_ss + (2 * pr) * tab.c_sd);
+    cs.y = table_elem(tab.sin, tab.tab_dtype, bt * tab.s_sb + static_cast<int64_t>(t) * tab.s_ss + (2 * pr) * tab.s_sd);
+    return cs;
   }
-  __syncthreads();
-  if (!there) return;
+  const int64_t off = bt * tab.i_sb + static_cast<int64_t>(t) * tab.i_ss + tab.axis_of[pr] * tab.i_sa;
+  if (tab.ids_f32) return pair_cos_sin(static_cast<double>(static_cast<const float*>(tab.ids)[off]), tab.omega[pr]);
+  const long long id = static_cast<const int32_t*>(tab.ids)[off];
+  const unsigned long long turn = static_cast<unsigned long long>(id) * p.turns[pr];
+  sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f, &cs.y, &cs.x);  // 2^-31
+  return cs;
+}
+
+template <int NI>
+__global__ void __launch_bounds__(kAppWarps * 32) append_kernel(const __grid_constant__ AppendParams p, int units) {
+  __shared__ float4 tab[kAppWarps][kPairs / 2];
+  grid_dependency_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kAppWarps + warp;
+  const int64_t tok = unit / units;
+  if (tok >= static_cast<int64_t>(p.B) * p.T) return;
+  const int r_base = static_cast<int>(unit - tok * units) * 2 * NI + half;
+  const int b = static_cast<int>(tok / p.T), t = static_cast<int>(tok - static_cast<int64_t>(b) * p.T);
+  const int Hkv = p.kv.Hkv, n_rows = p.H + 2 * Hkv;
+  const bool live = t < row_count(p.counts, b, p.T);
   if (!live) {  // a padded token: its q' rows are zero, nothing enters the cache
     const float z[8] = {};
-    for (int r = r_first; r < p.H; r += hpt) store_chunk8(p.qo, b * p.qo_sb + t * p.qo_ss + r * p.qo_sh, p.kv.dt, l, z);
+#pragma unroll
+    for (int u = 0; u < NI; ++u)
+      if (r_base + 2 * u < p.H) store_chunk8(p.qo, b * p.qo_sb + t * p.qo_ss + (r_base + 2 * u) * p.qo_sh, p.kv.dt, l, z);
     return;
   }
-  const int pg = loc[slot][0], prow = loc[slot][1];
-  const int64_t k_off = pg * p.kv.k_sp + prow * p.kv.k_sr, v_off = pg * p.kv.v_sp + prow * p.kv.v_sr;
-  float2 cs[4];
+  uint4 x[NI][2];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) cs[e] = tab[slot][4 * l + e];
-  float wq[8], wk[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    wq[e] = __ldg(p.wq + 8 * l + e);
-    wk[e] = __ldg(p.wk + 8 * l + e);
-  }
-  // the bound is that of the warp's first half: both halves take the shuffles
-  for (int r0 = r_first; r0 - (hw & 1) < n_rows; r0 += kAppBatch * hpt) {
-    if (r0 != r_first) fetch(r0);
-#pragma unroll
-    for (int u = 0; u < kAppBatch; ++u) {
-      const int r = r0 + u * hpt;
-      const bool is_v = r >= p.H + Hkv, is_q = r < p.H;
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(x[u][e], x[u][e], ss);
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (r >= n_rows) continue;
-      if (!is_v) {
-        const float inv = rsqrtf(ss * (1.0f / kD) + p.eps);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float n0 = x[u][2 * e] * inv * (is_q ? wq[2 * e] : wk[2 * e]);
-          const float n1 = x[u][2 * e + 1] * inv * (is_q ? wq[2 * e + 1] : wk[2 * e + 1]);
-          x[u][2 * e] = n0 * cs[e].x - n1 * cs[e].y;
-          x[u][2 * e + 1] = n0 * cs[e].y + n1 * cs[e].x;
-        }
+  for (int u = 0; u < NI; ++u) {
+    const int r = r_base + 2 * u;
+    x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
+    if (r < n_rows) {
+      const RowTensor& src = r < p.H ? p.q : (r < p.H + Hkv ? p.k : p.v);
+      const int h = r < p.H ? r : (r < p.H + Hkv ? r - p.H : r - p.H - Hkv);
+      const int64_t off = b * src.sb + t * src.ss + h * src.sh + 8 * l;
+      if (src.dt == kDtF32) {
+        x[u][0] = ldg_nc_v4(static_cast<const float*>(src.p) + off);
+        x[u][1] = ldg_nc_v4(static_cast<const float*>(src.p) + off + 4);
+      } else {
+        x[u][0] = ldg_nc_v4(static_cast<const uint16_t*>(src.p) + off);
       }
-      if (is_q) store_chunk8(p.qo, b * p.qo_sb + t * p.qo_ss + r * p.qo_sh, p.kv.dt, l, x[u]);
-      else if (pg >= 0 && !is_v) store_chunk8(p.kv.k, k_off + (r - p.H) * p.kv.k_sh, p.kv.dt, l, x[u]);
-      else if (pg >= 0) store_chunk8(p.kv.v, v_off + (r - p.H - Hkv) * p.kv.v_sh, p.kv.dt, l, x[u]);
     }
+  }
+  int pg = -1, prow = 0;
+  if (r_base - half + 2 * NI > p.H && !kv_locate(p.kv, b, static_cast<int64_t>(__ldg(p.lens + b)) + t, &pg, &prow)) {
+    pg = -1;
+    if (lane == 0) atomicOr(p.status, kStatusIndex);
+  }
+  const float2 c0 = append_pair(p, b, t, 2 * lane), c1 = append_pair(p, b, t, 2 * lane + 1);
+  tab[warp][lane] = make_float4(c0.x, c0.y, c1.x, c1.y);
+  __syncwarp();
+  const float4 ca = tab[warp][2 * l], cb = tab[warp][2 * l + 1];
+  const float2 cs[4] = {{ca.x, ca.y}, {ca.z, ca.w}, {cb.x, cb.y}, {cb.z, cb.w}};
+  const int64_t k_off = pg * p.kv.k_sp + prow * p.kv.k_sr, v_off = pg * p.kv.v_sp + prow * p.kv.v_sr;
+#pragma unroll
+  for (int u = 0; u < NI; ++u) {
+    const int r = r_base + 2 * u;
+    const bool is_q = r < p.H, is_v = r >= p.H + Hkv;
+    const int dt = is_v ? p.v.dt : p.q.dt;
+    const uint32_t w[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w, x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (dt == kDtF32) y[e] = __uint_as_float(w[e]);
+      else if (dt == kDtBF16) y[e] = e & 1 ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
+      else y[e] = e & 1 ? f16_hi(w[e >> 1]) : f16_lo(w[e >> 1]);
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (r >= n_rows) continue;
+    if (!is_v) {
+      const float inv = rsqrtf(ss * (1.0f / kD) + p.eps);
+      const float4* wp = reinterpret_cast<const float4*>(is_q ? p.wq : p.wk) + 2 * l;
+      const float4 wa = __ldg(wp), wb = __ldg(wp + 1);
+      const float wv[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float n0 = y[2 * e] * inv * wv[2 * e], n1 = y[2 * e + 1] * inv * wv[2 * e + 1];
+        y[2 * e] = n0 * cs[e].x - n1 * cs[e].y;
+        y[2 * e + 1] = n0 * cs[e].y + n1 * cs[e].x;
+      }
+    }
+    if (is_q) store_chunk8(p.qo, b * p.qo_sb + t * p.qo_ss + r * p.qo_sh, p.kv.dt, l, y);
+    else if (pg >= 0 && !is_v) store_chunk8(p.kv.k, k_off + (r - p.H) * p.kv.k_sh, p.kv.dt, l, y);
+    else if (pg >= 0) store_chunk8(p.kv.v, v_off + (r - p.H - Hkv) * p.kv.v_sh, p.kv.dt, l, y);
   }
 }
 
@@ -146,22 +139,43 @@ __global__ void __launch_bounds__(kAppThreads) append_kernel(const __grid_consta
 // order may move in place: the destinations of a chunk are rows that this and
 // earlier chunks have read. A CTA owns a column (part_lanes 16-byte lanes of
 // one K/V head, of K or of V) of one sequence, so no two CTAs touch the same
-// bytes. Memory bound; chunks are staged through a ring of shared memory by
-// asynchronous copies, kKeepStages chunks ahead of the one being written.
+// bytes. Memory bound. The addresses of kKeepTable rows at a time are worked
+// out ahead of their use into a table in shared memory (list entry -> page
+// number -> address is two dependent loads; done row by row in the copy loop it
+// held the whole kernel to 1.3 TB/s), and chunks are staged through a ring by
+// asynchronous copies, kKeepStages - 1 chunks ahead of the one being written.
 constexpr int kKeepThreads = 256;
 constexpr int kKeepPer = 4;     // 16-byte copies per thread and chunk
 constexpr int kKeepStages = 4;
-constexpr int kKeepSmem = kKeepStages * kKeepPer * kKeepThreads * 16;
+constexpr int kKeepTable = 1024;
+// Shared memory by the call's N (several CTAs per SM where a list is short):
+// the ring's chunks, then src and dst byte offsets of one table or two; src < 0:
+// the row does not move.
+struct KeepLay {
+  int stages, table, tables;
+  __host__ __device__ KeepLay(int N, int part_lanes) {
+    const int chunk = kKeepThreads / part_lanes * kKeepPer, chunks = (N + chunk - 1) / chunk;
+    stages = chunks < 1 ? 1 : (chunks < kKeepStages ? chunks : kKeepStages);
+    table = chunks * chunk < kKeepTable ? (chunks < 1 ? chunk : chunks * chunk) : kKeepTable;
+    tables = N > kKeepTable ? 2 : 1;
+  }
+  __host__ __device__ size_t ring() const { return static_cast<size_t>(stages) * kKeepPer * kKeepThreads * 16; }
+  __host__ __device__ size_t bytes() const { return ring() + static_cast<size_t>(2) * tables * table * 8; }
+};
 
 __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constant__ KeepParams p) {
-  extern __shared__ __align__(16) uint4 ring[];
+  extern __shared__ __align__(16) uint8_t raw[];
+  const KeepLay lay(p.N, p.part_lanes);
+  uint4* ring = reinterpret_cast<uint4*>(raw);
+  int64_t* t_src = reinterpret_cast<int64_t*>(raw + lay.ring());
+  int64_t* t_dst = t_src + lay.tables * lay.table;
   grid_dependency_wait();
-  const int b = blockIdx.z;
+  const int b = blockIdx.z, tid = threadIdx.x;
   const int64_t cap = static_cast<int64_t>(p.kv.max_pages) * p.kv.page;
   const int start = __ldg(p.start + b), n_said = __ldg(p.n_rows + b);
   const int n = static_cast<int>(min(static_cast<int64_t>(min(max(n_said, 0), p.N)), max(cap - max(start, 0), int64_t(0))));
-  const bool first = blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0;
-  if (first) {
+  const bool first = blockIdx.x == 0 && blockIdx.y == 0;
+  if (first && tid == 0) {
     if (n != n_said || start < 0) atomicOr(p.status, kStatusIndex);
     p.lens[b] = start < 0 ? start : start + n;
   }
@@ -172,51 +186,70 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constan
   const int h = is_v ? blockIdx.y - p.kv.Hkv : blockIdx.y;
   uint8_t* base = static_cast<uint8_t*>(is_v ? p.kv.v : p.kv.k) + h * (is_v ? p.kv.v_sh : p.kv.k_sh) * eb;
   const int64_t sp = (is_v ? p.kv.v_sp : p.kv.k_sp) * eb, sr = (is_v ? p.kv.v_sr : p.kv.k_sr) * eb;
-  const int lanes = p.part_lanes, lane = threadIdx.x % lanes;
-  const int rows_pass = kKeepThreads / lanes, chunk = rows_pass * kKeepPer;
+  const int lanes = p.part_lanes, lane = tid % lanes, row0 = tid / lanes;
+  const int rows_pass = kKeepThreads / lanes, chunk = rows_pass * kKeepPer;  // chunk divides kKeepTable
   const int64_t col = (static_cast<int64_t>(blockIdx.x) * lanes + lane) * 16;
-  const int n_chunks = (n + chunk - 1) / chunk;
+  const int n_chunks = (n + chunk - 1) / chunk, per_table = lay.table / chunk;
   const int32_t* rows = p.rows + b * p.r_sb;
 
-  auto load = [&](int c) {
-    uint4* st = ring + (c % kKeepStages) * kKeepPer * kKeepThreads + threadIdx.x;
+  auto build = [&](int tb) {  // the table of rows [tb kKeepTable, (tb + 1) kKeepTable)
+    constexpr int kPer = kKeepTable / kKeepThreads;
+    int r[kPer], before[kPer];
 #pragma unroll
-    for (int u = 0; u < kKeepPer; ++u) {
-      const int i = c * chunk + u * rows_pass + threadIdx.x / lanes;
-      if (c < n_chunks && i < n) {
-        const int r = __ldg(rows + i);
-        int pg, row;
-        if (r != i && r > i && kv_locate(p.kv, b, static_cast<int64_t>(start) + r, &pg, &row)) {
-          const void* src = base + pg * sp + row * sr + col;
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(st + u * kKeepThreads)), "l"(src) : "memory");
+    for (int u = 0; u < kPer; ++u) {
+      const int i = tb * lay.table + u * kKeepThreads + tid;
+      r[u] = i < n ? __ldg(rows + i) : -1;
+      before[u] = i < n && i > 0 ? __ldg(rows + i - 1) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const int e = u * kKeepThreads + tid, i = tb * lay.table + e;
+      if (e >= lay.table) break;
+      int64_t so = -1, dof = 0;
+      if (i < n) {
+        int pg, row, pg2, row2;
+        const bool ok = r[u] >= i && r[u] > before[u] && kv_locate(p.kv, b, static_cast<int64_t>(start) + r[u], &pg, &row) &&
+                        kv_locate(p.kv, b, static_cast<int64_t>(start) + i, &pg2, &row2);
+        if (!ok) {
+          if (first) atomicOr(p.status, kStatusIndex);
+        } else if (r[u] != i) {
+          so = pg * sp + row * sr;
+          dof = pg2 * sp + row2 * sr;
         }
+      }
+      t_src[(tb & 1) * lay.table + e] = so;
+      t_dst[(tb & 1) * lay.table + e] = dof;
+    }
+  };
+  auto load = [&](int c) {
+    if (c < n_chunks) {
+      const int64_t* src = t_src + ((c / per_table) & 1) * lay.table + (c % per_table) * chunk + row0;
+#pragma unroll
+      for (int u = 0; u < kKeepPer; ++u) {
+        const int64_t so = src[u * rows_pass];
+        if (so >= 0)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(ring + ((c % lay.stages) * kKeepPer + u) * kKeepThreads + tid)), "l"(base + so + col) : "memory");
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  build(0);
+  __syncthreads();
 #pragma unroll 1
   for (int c = 0; c < kKeepStages - 1; ++c) load(c);
 #pragma unroll 1
   for (int c = 0; c < n_chunks; ++c) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kKeepStages - 2) : "memory");
     __syncthreads();  // every source of chunk c has been read: its destinations may be written
-    const uint4* st = ring + (c % kKeepStages) * kKeepPer * kKeepThreads + threadIdx.x;
+    const int tb = c / per_table, within = c % per_table;
+    const int64_t* src = t_src + (tb & 1) * lay.table + within * chunk + row0;
+    const int64_t* dst = t_dst + (tb & 1) * lay.table + within * chunk + row0;
 #pragma unroll
-    for (int u = 0; u < kKeepPer; ++u) {
-      const int i = c * chunk + u * rows_pass + threadIdx.x / lanes;
-      if (i < n) {
-        const int r = __ldg(rows + i);
-        int pg, row, pg2, row2;
-        bool bad = r < i || (i > 0 && r <= __ldg(rows + i - 1)) ||
-                   !kv_locate(p.kv, b, static_cast<int64_t>(start) + r, &pg2, &row2);
-        if (!bad && r != i) {
-          if (kv_locate(p.kv, b, static_cast<int64_t>(start) + i, &pg, &row))
-            *reinterpret_cast<uint4*>(base + pg * sp + row * sr + col) = st[u * kKeepThreads];
-          else bad = true;
-        }
-        if (bad) atomicOr(p.status, kStatusIndex);
-      }
-    }
+    for (int u = 0; u < kKeepPer; ++u)
+      if (src[u * rows_pass] >= 0) *reinterpret_cast<uint4*>(base + dst[u * rows_pass] + col) = ring[((c % lay.stages) * kKeepPer + u) * kKeepThreads + tid];
+    // the next table goes where the last one was, which no thread reads any more
+    // (chunks ahead stay within it: a table holds at least kKeepStages chunks)
+    if (within == 0 && (tb + 1) * per_table < n_chunks) build(tb + 1);
     load(c + kKeepStages - 1);  // its slot was written out in the previous turn
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -226,19 +259,27 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constan
 
 cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t stream) {
   const int n_rows = p.H + 2 * p.kv.Hkv;
-  // half-warps per token: as many as it has rows, 16 at most
-  const int hpt = n_rows <= 4 ? 4 : (n_rows <= 8 ? 8 : 16);
-  const int tpb = 16 / hpt;
-  const int64_t blocks = (static_cast<int64_t>(p.B) * p.T + tpb - 1) / tpb;
-  return launch_chained(append_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kAppThreads), 0, stream, p, hpt);
+  const int64_t tokens = static_cast<int64_t>(p.B) * p.T;
+  auto go = [&](auto kern, int ni) {
+    const int units = (n_rows + 2 * ni - 1) / (2 * ni);
+    return launch_chained(kern, dim3(static_cast<unsigned>((tokens * units + kAppWarps - 1) / kAppWarps)), dim3(kAppWarps * 32), 0,
+                          stream, p, units);
+  };
+  // as many rows per warp as still leave every SM (152) 16 warps: rows in
+  // flight hide the reads, warps the rest
+  if (tokens * ((n_rows + 15) / 16) >= 152 * 16) return go(append_kernel<8>, 8);
+  if (tokens * ((n_rows + 3) / 4) >= 152 * 16) return go(append_kernel<2>, 2);
+  return go(append_kernel<1>, 1);
 }
 
 cudaError_t launch_cache_keep(const KeepParams& p, cudaStream_t stream) {
   static std::atomic<uint64_t> configured{0};
-  cudaError_t e = opt_in_smem(keep_kernel, kKeepSmem, configured);
+  const KeepLay lay(p.N, p.part_lanes);
+  constexpr size_t most = static_cast<size_t>(kKeepStages) * kKeepPer * kKeepThreads * 16 + 4 * kKeepTable * 8;
+  cudaError_t e = opt_in_smem(keep_kernel, static_cast<int>(most), configured);
   if (e != cudaSuccess) return e;
   const int row_lanes = kD * (p.kv.dt == kDtF32 ? 4 : 2) / 16;
-  return launch_chained(keep_kernel, dim3(row_lanes / p.part_lanes, 2 * p.kv.Hkv, p.B), dim3(kKeepThreads), kKeepSmem, stream, p);
+  return launch_chained(keep_kernel, dim3(row_lanes / p.part_lanes, 2 * p.kv.Hkv, p.B), dim3(kKeepThreads), lay.bytes(), stream, p);
 }
 
 }  // namespace st

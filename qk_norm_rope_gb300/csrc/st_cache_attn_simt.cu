@@ -27,6 +27,7 @@ struct Smem {
   float p[kR][kPadP];
   float corr[kR], m[kR], l[kR];
   uint32_t anc[kR][kTreeWords];
+  int64_t k_off[2][kN], v_off[2][kN];  // element offsets of a tile's rows, by its parity; < 0: no row
 };
 
 // Bit j of the result: node `first + j` is seen from a row whose ancestors
@@ -92,26 +93,69 @@ __global__ void __launch_bounds__(kThreads) simt_kernel(const __grid_constant__ 
   float o[4][4] = {};
   const int tr = tid >> 4, tc = tid & 15;   // scores: rows tr, tr + 16; keys tc + 16 i
   const int rg = tid >> 5, dg = tid & 31;   // outputs: rows 4 rg + i; dims 4 dg..
-  for (int jt = j_lo; jt < j_hi; ++jt) {
-    const int j0 = jt * kN;
-    __syncthreads();
-    for (int e = tid; e < kN * kD / 8; e += kThreads) {
-      const int r = e / (kD / 8), c = e % (kD / 8), j = j0 + r;
-      float x[8] = {}, y[8] = {};
+  const bool f32 = p.kv.dt == kDtF32;
+  auto locate = [&](int jt) {  // the rows of key tile jt
+    if (tid < kN && jt < j_hi) {
+      const int j = jt * kN + tid;
       int pg, prow;
+      int64_t ko = -1, vo = -1;
       if (j < keys) {
         if (kv_locate(p.kv, b, j, &pg, &prow)) {
-          load_chunk8(p.kv.k, pg * p.kv.k_sp + prow * p.kv.k_sr + hk * p.kv.k_sh, p.kv.dt, c, x);
-          load_chunk8(p.kv.v, pg * p.kv.v_sp + prow * p.kv.v_sr + hk * p.kv.v_sh, p.kv.dt, c, y);
+          ko = pg * p.kv.k_sp + prow * p.kv.k_sr + hk * p.kv.k_sh;
+          vo = pg * p.kv.v_sp + prow * p.kv.v_sr + hk * p.kv.v_sh;
         } else {
           atomicOr(p.status, kStatusIndex);
         }
       }
-      *reinterpret_cast<float4*>(&s.k[r][8 * c]) = make_float4(x[0], x[1], x[2], x[3]);
-      *reinterpret_cast<float4*>(&s.k[r][8 * c + 4]) = make_float4(x[4], x[5], x[6], x[7]);
-      *reinterpret_cast<float4*>(&s.v[r][8 * c]) = make_float4(y[0], y[1], y[2], y[3]);
-      *reinterpret_cast<float4*>(&s.v[r][8 * c + 4]) = make_float4(y[4], y[5], y[6], y[7]);
+      s.k_off[jt & 1][tid] = ko;
+      s.v_off[jt & 1][tid] = vo;
     }
+  };
+  // One of a tile's two operands into shared memory: asynchronous copies of
+  // fp32 rows, conversion of 16-bit ones; zeros where there is no row.
+  auto fetch = [&](const void* base, const int64_t* off, float* dst, int pad) {
+    if (f32) {
+#pragma unroll
+      for (int u = 0; u < kN * kD / 4 / kThreads; ++u) {
+        const int e = u * kThreads + tid, r = e / (kD / 4), c = e % (kD / 4);
+        const int64_t o = off[r];
+        const float* src = static_cast<const float*>(base) + (o < 0 ? 0 : o) + 4 * c;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst + r * pad + 4 * c)), "l"(o < 0 ? base : src), "r"(o < 0 ? 0 : 16) : "memory");
+      }
+    } else {
+      uint4 x[kN * kD / 8 / kThreads];
+#pragma unroll
+      for (int u = 0; u < kN * kD / 8 / kThreads; ++u) {
+        const int e = u * kThreads + tid, r = e / (kD / 8), c = e % (kD / 8);
+        const int64_t o = off[r];
+        x[u] = o < 0 ? make_uint4(0, 0, 0, 0) : ldg_nc_v4(static_cast<const uint16_t*>(base) + o + 8 * c);
+      }
+#pragma unroll
+      for (int u = 0; u < kN * kD / 8 / kThreads; ++u) {
+        const int e = u * kThreads + tid, r = e / (kD / 8), c = e % (kD / 8);
+        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          y[2 * i] = p.kv.dt == kDtF16 ? f16_lo(w[i]) : bf16_lo(w[i]);
+          y[2 * i + 1] = p.kv.dt == kDtF16 ? f16_hi(w[i]) : bf16_hi(w[i]);
+        }
+        *reinterpret_cast<float4*>(dst + r * pad + 8 * c) = make_float4(y[0], y[1], y[2], y[3]);
+        *reinterpret_cast<float4*>(dst + r * pad + 8 * c + 4) = make_float4(y[4], y[5], y[6], y[7]);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  locate(j_lo);
+  __syncthreads();
+  if (j_lo < j_hi) {
+    fetch(p.kv.k, s.k_off[j_lo & 1], &s.k[0][0], kPad);
+    fetch(p.kv.v, s.v_off[j_lo & 1], &s.v[0][0], kD);
+  }
+  for (int jt = j_lo; jt < j_hi; ++jt) {
+    const int j0 = jt * kN;
+    locate(jt + 1);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");  // K
     __syncthreads();
     float sc[2][4] = {};
 #pragma unroll 8
@@ -157,7 +201,9 @@ __global__ void __launch_bounds__(kThreads) simt_kernel(const __grid_constant__ 
         s.l[r] = s.l[r] * corr + sum;
       }
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");  // V
     __syncthreads();
+    if (jt + 1 < j_hi) fetch(p.kv.k, s.k_off[(jt + 1) & 1], &s.k[0][0], kPad);  // under this tile's PV
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float corr = s.corr[4 * rg + i];
@@ -182,6 +228,8 @@ __global__ void __launch_bounds__(kThreads) simt_kernel(const __grid_constant__ 
         }
       }
     }
+    __syncthreads();
+    if (jt + 1 < j_hi) fetch(p.kv.v, s.v_off[(jt + 1) & 1], &s.v[0][0], kD);
   }
   __syncthreads();
 #pragma unroll

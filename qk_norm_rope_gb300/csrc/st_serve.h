@@ -50,6 +50,7 @@ struct AppendParams {
   const float* wk;
   float eps;
   TableParams tab;                 // ids, or cos/sin tables
+  unsigned long long turns[kPairs];  // fraction of a turn per position, 2^-64 a unit
   PagedKV kv;
   const int32_t* lens;
   const int32_t* counts;           // or null
@@ -152,7 +153,7 @@ struct KeepParams {
   const int32_t* n_rows;           // [B]
   int32_t* lens;                   // [B], out
   int B, N;
-  int part_lanes;                  // 16-byte lanes of a row that one CTA moves (2, 4 or 8)
+  int part_lanes;                  // 16-byte lanes of a row that one CTA moves (4 or 8)
   unsigned* status;
 };
 cudaError_t launch_cache_keep(const KeepParams& p, cudaStream_t stream);

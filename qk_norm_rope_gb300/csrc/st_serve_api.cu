@@ -158,8 +158,8 @@ st_status plan_attn(const st_tensor* q, const st_kv_cache* cache, const st_tenso
   const int64_t items = simt_items(p.B, p.T, p.H, p.kv.Hkv);
   if (items > (1ll << 30)) return fail(ST_ERR_SHAPE, "too many query rows");
   const int64_t tiles = (static_cast<int64_t>(p.kv.max_pages) * p.kv.page + kSimtKeys - 1) / kSimtKeys;
-  // enough key ranges for four CTAs per SM, none shorter than a tile
-  p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({(4 * kSmCount + items - 1) / items, tiles, 128})));
+  // enough key ranges for two CTAs per SM (what fits), none shorter than a tile
+  p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({2 * kSmCount / items, tiles, 128})));
   if (p.splits > 1) P->bytes = static_cast<size_t>(items) * p.splits * kSimtRows * (kD + 2) * sizeof(float);
   return ST_OK;
 }
@@ -202,11 +202,15 @@ st_status st_cache_append(const st_tensor* q, const st_tensor* k, const st_tenso
   RowTensor ro;
   if ((st = check_bshd(q_rot, "q_rot", p.B, p.T, p.H, kD, bit(p.kv.dt), &ro)) != ST_OK) return st;
   const int64_t tokens = static_cast<int64_t>(p.B) * p.T;
-  if (tokens > (1ll << 30)) return fail(ST_ERR_SHAPE, "too many new rows");
+  if (tokens > (1ll << 30) || tokens * (p.H + 2 * p.kv.Hkv) > (1ll << 32)) return fail(ST_ERR_SHAPE, "too many new rows");
   if (tokens * p.H == 0) return ST_OK;
   Dev dev;
   if ((st = device_globals(&dev)) != ST_OK) return st;
   fill_table(ids, rope, nullptr, nullptr, nullptr, &p.tab);
+  for (int j = 0; j < kPairs; ++j) {
+    const double turn = p.tab.omega[j] * 0.15915494309189535;  // 1 / (2 pi)
+    p.turns[j] = static_cast<unsigned long long>((turn - std::floor(turn)) * 18446744073709551616.0);
+  }
   p.wq = static_cast<const float*>(q_norm_w->data);
   p.wk = static_cast<const float*>(k_norm_w->data);
   p.eps = eps;
@@ -395,7 +399,7 @@ st_status st_cache_keep(const st_kv_cache* cache, const st_tensor* start, const 
   p.lens = static_cast<int32_t*>(lens->data);
   // columns of 128 bytes, or narrower ones where that leaves SMs without work
   const int64_t chains = static_cast<int64_t>(p.B) * 2 * p.kv.Hkv * (kD * elem_bytes(p.kv.dt) / 128);
-  p.part_lanes = chains >= kSmCount ? 8 : (2 * chains >= kSmCount ? 4 : 2);
+  p.part_lanes = chains >= kSmCount ? 8 : 4;
   p.status = dev.status;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   return cuda_check(launch_counted(ST_K_CACHE_KEEP, stream, [&] { return launch_cache_keep(p, stream); }), "cache keep launch");
