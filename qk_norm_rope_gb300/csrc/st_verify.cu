@@ -34,6 +34,7 @@ namespace {
 
 constexpr int kVerThreads = 256;
 constexpr int kVerWarps = kVerThreads / 32;
+constexpr int kBatches = 64;    // batches of a warp's slice whose sums are kept for the draw (further ones are read again)
 constexpr int kRowBatch = 16;  // rows of 32 probabilities whose loads are issued together
 constexpr double kUnit = 1.0 / 8796093022208.0;  // 2^-43, the unit of a weight
 
@@ -55,47 +56,55 @@ __device__ __forceinline__ float prob(const void* p, int64_t e) {
 // cost twice the instructions of the rest of the sum).
 constexpr float kHi = 1.5f * 4.0f;                    // 1.5 * 2^(23 - 21)
 constexpr float kLo = 1.5f * 9.5367431640625e-7f;     // 1.5 * 2^(23 - 43)
-struct Limbs {
-  int hi, lo;
+struct Limbs {  // of two values, modulo 2^32; kHi's and kLo's own bits are still in them
+  uint32_t hi, lo;
 };
-__device__ __forceinline__ Limbs limbs(float v, float tail = 0.f) {  // of v + tail, |tail| <= 2^-23
-  const float t = __fadd_rn(v, kHi);
-  const float rem = __fadd_rn(__fsub_rn(v, __fsub_rn(t, kHi)), tail);
-  Limbs r;
-  r.hi = __float_as_int(t) - __float_as_int(kHi);
-  r.lo = __float_as_int(__fadd_rn(rem, kLo)) - __float_as_int(kLo);
-  return r;
+__device__ __forceinline__ Limbs limbs(float2 v, float2 tail) {  // of v + tail, |tail| <= 2^-23; both values added up
+  const float2 t = __fadd2_rn(v, make_float2(kHi, kHi));
+  const float2 back = __fadd2_rn(t, make_float2(-kHi, -kHi));
+  const float2 rem = __fadd2_rn(__fadd2_rn(v, make_float2(-back.x, -back.y)), tail);
+  const float2 l = __fadd2_rn(rem, make_float2(kLo, kLo));
+  return {__float_as_uint(t.x) + __float_as_uint(t.y), __float_as_uint(l.x) + __float_as_uint(l.y)};
 }
 // The limbs of max(p - a q, 0). a = 0 and a = 1 (before and after the first
 // rejection) need no product; else a = ah + al and the product is carried with
-// its rounding error.
+// its rounding error. A difference of p and something no larger is p - s = d
+// with the error (p - d) - s, exactly.
 struct Scale {
   float ah, al;
 };
 template <int A>  // 0: a = 0; 1: a = 1; 2: any a
-__device__ __forceinline__ Limbs weight(float p, float q, Scale a) {
-  if constexpr (A == 0) return limbs(p);
-  Limbs r{0, 0};
-  if constexpr (A == 1) {
-    const Limbs x = limbs(p), y = limbs(q);
-    if (p > q) {
-      r.hi = x.hi - y.hi;
-      r.lo = x.lo - y.lo;
-    }
+__device__ __forceinline__ Limbs weight(float2 p, float2 q, Scale a) {
+  if constexpr (A == 0) return limbs(p, make_float2(0.f, 0.f));
+  float2 s = q, tail = make_float2(0.f, 0.f);
+  if constexpr (A == 2) {
+    s = make_float2(__fmul_rn(a.ah, q.x), __fmul_rn(a.ah, q.y));
+    tail = make_float2(__fmaf_rn(a.al, q.x, __fmaf_rn(a.ah, q.x, -s.x)), __fmaf_rn(a.al, q.y, __fmaf_rn(a.ah, q.y, -s.y)));
+    // nothing is left where the product is p or more: then s = p, without a tail
+    const bool nx = s.x > p.x || (s.x == p.x && tail.x >= 0.f), ny = s.y > p.y || (s.y == p.y && tail.y >= 0.f);
+    s = make_float2(nx ? p.x : s.x, ny ? p.y : s.y);
+    tail = make_float2(nx ? 0.f : tail.x, ny ? 0.f : tail.y);
   } else {
-    const float sh = __fmul_rn(a.ah, q), sl = __fmaf_rn(a.al, q, __fmaf_rn(a.ah, q, -sh));
-    const float d = __fsub_rn(p, sh), bb = __fsub_rn(p, d);          // d + e = p - sh exactly
-    const float e = __fsub_rn(__fsub_rn(bb, sh), sl) + __fsub_rn(p, __fadd_rn(d, bb));
-    if (__fadd_rn(d, e) > 0.f && d <= 1.f) r = limbs(d, e);
+    s = make_float2(fminf(p.x, q.x), fminf(p.y, q.y));
   }
-  return r;
+  const float2 ns = make_float2(-s.x, -s.y);
+  float2 d = __fadd2_rn(p, ns);
+  float2 e = __fadd2_rn(__fadd2_rn(p, make_float2(-d.x, -d.y)), ns);
+  if constexpr (A == 2) {
+    e = __fadd2_rn(e, make_float2(-tail.x, -tail.y));
+    const bool zx = d.x + e.x <= 0.f, zy = d.y + e.y <= 0.f;
+    d = make_float2(zx ? 0.f : d.x, zy ? 0.f : d.y);
+    e = make_float2(zx ? 0.f : e.x, zy ? 0.f : e.y);
+  }
+  return limbs(d, e);
 }
-__device__ __forceinline__ unsigned long long whole(int hi, int lo) {
-  return static_cast<unsigned long long>((static_cast<long long>(hi) << 22) + lo);
+constexpr uint32_t kPairHi = 2u * 0x40c00000u, kPairLo = 2u * 0x35c00000u;  // kHi's and kLo's bits, twice
+__device__ __forceinline__ unsigned long long whole(uint32_t hi, uint32_t lo) {
+  return static_cast<unsigned long long>(static_cast<long long>(static_cast<int>(hi)) * 4194304 + static_cast<int>(lo));
 }
 __device__ __forceinline__ unsigned long long fix(float v) {
-  const Limbs x = limbs(v);
-  return whole(x.hi, x.lo);
+  const Limbs x = limbs(make_float2(v, 0.f), make_float2(0.f, 0.f));
+  return whole(x.hi - kPairHi, x.lo - kPairLo);
 }
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
 #pragma unroll
@@ -112,6 +121,7 @@ struct VerState {
   bool first_yes[kMaxVerify];    // accepted when no sibling was rejected before it
   int path[kMaxVerify];
   unsigned long long warp_tot[kVerWarps];
+  unsigned long long batch_tot[kVerWarps][kBatches];
   unsigned long long cta_tot[2][kMaxClusterVerify];  // by the parity of the exchange
   int rejected[kMaxVerify];
   int n_rejected;
@@ -160,21 +170,32 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
   const int w_lo = static_cast<int>(min(lo64, static_cast<int64_t>(V))), w_hi = static_cast<int>(min(lo64 + sub, static_cast<int64_t>(V)));
   int parity = 0;
 
-  // kRowBatch x 32 probabilities from v0 on, all loads in flight together
-  auto load_rows = [&](int64_t pe, int64_t qe, int v0, bool with_q, float (&pv)[kRowBatch], float (&qv)[kRowBatch]) {
+  // kRowBatch x 32 probabilities from v0 on, all loads in flight together; a
+  // whole batch takes constant offsets from one address
+  auto load_rows = [&](int64_t pe, int64_t qe, int v0, auto with_q, float (&pv)[kRowBatch], float (&qv)[kRowBatch]) {
+    constexpr bool Q = decltype(with_q)::value;
+    if (v0 + 32 * kRowBatch <= w_hi) {
+#pragma unroll
+      for (int u = 0; u < kRowBatch; ++u) {
+        pv[u] = prob<DT>(P.p, pe + v0 + lane + 32 * u);
+        qv[u] = Q ? prob<DT>(P.q, qe + v0 + lane + 32 * u) : 0.f;
+      }
+      return;
+    }
 #pragma unroll
     for (int u = 0; u < kRowBatch; ++u) {
       const int v = min(v0 + 32 * u + lane, w_hi - 1);  // no branch around a load
       pv[u] = prob<DT>(P.p, pe + v);
-      qv[u] = with_q ? prob<DT>(P.q, qe + v) : 0.f;
+      qv[u] = Q ? prob<DT>(P.q, qe + v) : 0.f;
     }
 #pragma unroll
     for (int u = 0; u < kRowBatch; ++u)
       if (v0 + 32 * u + lane >= w_hi) pv[u] = 0.f;  // weighs nothing, whatever q
   };
+
   // sum over V of the residual weights of node `cur` at `a`, less the removed
   // tokens; leaves the warps' totals in s.warp_tot and the CTAs' in s.cta_tot
-  auto sum_row = [&](int cur, double a, bool removed) -> unsigned long long {
+  auto sum_row = [&](int cur, double a, bool removed, bool keep) -> unsigned long long {
     const int64_t pe = b * P.p_sb + cur * P.p_st, qe = b * P.q_sb + cur * P.q_st;
     unsigned long long acc = 0;
     const Scale sc{static_cast<float>(a), static_cast<float>(a - static_cast<float>(a))};
@@ -182,15 +203,24 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
       constexpr int A = decltype(kind)::value;
       for (int v0 = w_lo; v0 < w_hi; v0 += 32 * kRowBatch) {
         float pv[kRowBatch], qv[kRowBatch];
-        load_rows(pe, qe, v0, A != 0, pv, qv);
-        int hi = 0, lo = 0;
+        load_rows(pe, qe, v0, std::integral_constant<bool, A != 0>(), pv, qv);
+        uint32_t hi = 0, lo = 0;  // modulo 2^32: the sums of 16 limbs are far below it
 #pragma unroll
-        for (int u = 0; u < kRowBatch; ++u) {
-          const Limbs x = weight<A>(pv[u], qv[u], sc);
-          hi += x.hi;
-          lo += x.lo;
+        for (int u = 0; u < kRowBatch; u += 2) {
+          const Limbs x = weight<A>(make_float2(pv[u], pv[u + 1]), make_float2(qv[u], qv[u + 1]), sc);
+          hi += x.hi - kPairHi;
+          lo += x.lo - kPairLo;
         }
-        acc += whole(hi, lo);
+        unsigned long long part = whole(hi, lo);
+        if (keep) {  // the batches' own sums, where the draw will look
+          const int batch = (v0 - w_lo) / (32 * kRowBatch);
+          if (batch < kBatches) {
+            part = warp_sum(part);
+            if (lane == 0) s.batch_tot[warp][batch] = part;
+            if (lane != 0) part = 0;
+          }
+        }
+        acc += part;
       }
     };
     if (!drafted || a == 0.0) pass(std::integral_constant<int, 0>());
@@ -202,7 +232,12 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
     if (removed) {
       for (int r = tid; r < s.n_rejected; r += kVerThreads) {
         const int x = s.tok[s.rejected[r]], w = x / sub - rank * kVerWarps;
-        if (w >= 0 && w < kVerWarps) atomicAdd(&s.warp_tot[w], 0ull - fix(s.pp[s.rejected[r]]));
+        if (w >= 0 && w < kVerWarps) {
+          const unsigned long long f = 0ull - fix(s.pp[s.rejected[r]]);
+          atomicAdd(&s.warp_tot[w], f);
+          const int batch = x % sub / (32 * kRowBatch);
+          if (keep && batch < kBatches) atomicAdd(&s.batch_tot[w][batch], f);
+        }
       }
       __syncthreads();
     }
@@ -283,7 +318,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
     }
     __syncthreads();
     if (!s.more) break;
-    const unsigned long long total = sum_row(s.cur, s.a, false);
+    const unsigned long long total = sum_row(s.cur, s.a, false, false);
     parity ^= 1;
     if (warp == 0) c = static_cast<double>(total) * kUnit;
     __syncthreads();
@@ -294,68 +329,73 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
     const int cur = s.cur;
     double aa = s.a;
     bool removed = s.n_rejected > 0;
-    unsigned long long total = sum_row(cur, aa, removed);
+    unsigned long long total = sum_row(cur, aa, removed, true);
     if (total == 0) {  // p <= a q everywhere: the target's own distribution
       parity ^= 1;
       aa = 0.0;
       removed = false;
       __syncthreads();
-      total = sum_row(cur, 0.0, false);
+      total = sum_row(cur, 0.0, false, true);
     }
     if (total > 0) {
       const float us = fminf(fmaxf(__ldg(P.u_sample + b), 0.f), 1.f);
       // u in 2^-64 units (below 1), so that thr = floor(u * total) < total
       const unsigned long long u64 = us >= 1.f ? ~0ull : __double2ull_rz(static_cast<double>(us) * 18446744073709551616.0);
       const unsigned long long thr = __umul64hi(u64, total);
-      unsigned long long before = 0;
-      for (int r = 0; r < rank; ++r) before += s.cta_tot[parity][r];
-      for (int w = 0; w < warp; ++w) before += s.warp_tot[w];
-      const unsigned long long mine = s.warp_tot[warp];
-      if (thr >= before && thr < before + mine) {  // one warp of the cluster
+      unsigned long long run = 0;
+      for (int r = 0; r < rank; ++r) run += s.cta_tot[parity][r];
+      if (thr >= run && thr < run + s.cta_tot[parity][rank]) {  // one CTA of the cluster
         const int64_t pe = b * P.p_sb + cur * P.p_st, qe = b * P.q_sb + cur * P.q_st;
-        const bool with_q = drafted && aa != 0.0;
         const Scale sc{static_cast<float>(aa), static_cast<float>(aa - static_cast<float>(aa))};
-        unsigned long long run = before;
-        int found = -1;
-        for (int v0 = w_lo; v0 < w_hi && found < 0; v0 += 32 * kRowBatch) {
-          float pv[kRowBatch], qv[kRowBatch];
-          load_rows(pe, qe, v0, with_q, pv, qv);
-          unsigned long long w[kRowBatch];
+        // the slice, then the batch, that holds it, by their sums
+        int w = 0;
+        while (w < kVerWarps - 1 && run + s.warp_tot[w] <= thr) run += s.warp_tot[w++];
+        const int64_t lo = static_cast<int64_t>(rank * kVerWarps + w) * sub;
+        const int end = static_cast<int>(min(lo + sub, static_cast<int64_t>(V)));
+        int v0 = static_cast<int>(min(lo, static_cast<int64_t>(V)));
+        for (int k = 0; k < kBatches && v0 < end && run + s.batch_tot[w][k] <= thr; ++k, v0 += 32 * kRowBatch) run += s.batch_tot[w][k];
+        __syncthreads();  // warp_tot serves the scans below
+        // two neighbours per thread: a batch at a time, usually one
+        auto find = [&](auto kind) {
+          constexpr int A = decltype(kind)::value;
+          static_assert(32 * kRowBatch == 2 * kVerThreads, "two tokens per thread");
+          for (bool found = false; v0 < end && !found; v0 += 32 * kRowBatch) {
+            unsigned long long x[2];
 #pragma unroll
-          for (int u = 0; u < kRowBatch; ++u) {
-            const Limbs x = !with_q ? weight<0>(pv[u], 0.f, sc) : aa == 1.0 ? weight<1>(pv[u], qv[u], sc) : weight<2>(pv[u], qv[u], sc);
-            w[u] = whole(x.hi, x.lo);
-            if (removed)
-              for (int r = 0; r < s.n_rejected; ++r)
-                if (s.tok[s.rejected[r]] == v0 + 32 * u + lane) w[u] = 0;
-          }
-          unsigned long long all = 0;
-#pragma unroll
-          for (int u = 0; u < kRowBatch; ++u) all += w[u];
-          all = warp_sum(all);
-          if (run + all <= thr) {  // not in this batch
-            run += all;
-            continue;
-          }
-#pragma unroll
-          for (int u = 0; u < kRowBatch; ++u) {
-            const unsigned long long sum = warp_sum(w[u]);
-            if (found < 0 && run + sum > thr) {  // uniform: the row of 32 that holds it
-              unsigned long long inc = w[u];
-#pragma unroll
-              for (int o = 1; o < 32; o <<= 1) {
-                const unsigned long long t = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += t;
-              }
-              found = v0 + 32 * u + __ffs(__ballot_sync(0xffffffffu, run + inc > thr)) - 1;
+            for (int u = 0; u < 2; ++u) {
+              const int e = v0 + 2 * tid + u, i = min(e, end - 1);
+              const Limbs y = weight<A>(make_float2(prob<DT>(P.p, pe + i), 0.f), make_float2(A != 0 ? prob<DT>(P.q, qe + i) : 0.f, 0.f), sc);
+              x[u] = e < end ? whole(y.hi - kPairHi, y.lo - kPairLo) : 0ull;
+              if (A == 0 && removed)
+                for (int r = 0; r < s.n_rejected; ++r)
+                  if (s.tok[s.rejected[r]] == e) x[u] = 0;
             }
-            run += sum;
+            unsigned long long inc = x[0] + x[1];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const unsigned long long t = __shfl_up_sync(0xffffffffu, inc, o);
+              if (lane >= o) inc += t;
+            }
+            if (lane == 31) s.warp_tot[warp] = inc;
+            __syncthreads();
+            unsigned long long at = run + inc - x[0] - x[1], all = 0;
+            for (int i = 0; i < kVerWarps; ++i) {
+              if (i < warp) at += s.warp_tot[i];
+              all += s.warp_tot[i];
+            }
+            if (thr >= at && thr < at + x[0] + x[1]) {  // one thread
+              const int token = v0 + 2 * tid + (thr < at + x[0] ? 0 : 1);
+              if (P.tok64) static_cast<long long*>(P.next_token)[b] = token;
+              else static_cast<int32_t*>(P.next_token)[b] = token;
+            }
+            found = thr < run + all;
+            run += all;
+            __syncthreads();
           }
-        }
-        if (lane == 0) {
-          if (P.tok64) static_cast<long long*>(P.next_token)[b] = found;
-          else static_cast<int32_t*>(P.next_token)[b] = found;
-        }
+        };
+        if (!drafted || aa == 0.0) find(std::integral_constant<int, 0>());
+        else if (aa == 1.0) find(std::integral_constant<int, 1>());
+        else find(std::integral_constant<int, 2>());
       }
     } else if (rank == 0 && tid == 0) {
       if (P.tok64) static_cast<long long*>(P.next_token)[b] = -1;

@@ -324,6 +324,7 @@ VERIFY = [
     (16, 61, 999, 6, True, "fp32"), (16, 61, 999, 6, False, "fp32"), (5, 40, 20011, 8, False, "bf16"),
     (6, 30, 8191, 8, True, "bf16"), (7, 30, 4097, 4, True, "fp16"), (2, 1024, 300, 5, True, "fp32"),
     (200, 9, 130, 8, True, "fp32"), (400, 5, 70, 4, False, "fp16"),
+    (310, 1, 300001, 1, False, "fp32"),  # one CTA per sequence, slices of more batches than have their sums kept
 ]
 
 
