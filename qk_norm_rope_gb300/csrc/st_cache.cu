@@ -13,21 +13,54 @@ namespace {
 // Per token and head: y = rotate(x / sqrt(mean x^2 + eps) * w), every product
 // in fp32 and one rounding to the cache's type; v is copied. Memory bound:
 // each row is read once and written once. A warp is a unit of its own (no
-// block barrier): 2 NI rows of one token, a half-warp (16 lanes x 8 elements)
-// per row, all NI loads of a half-warp in flight before the token's (cos, sin)
-// pairs, two per lane, are computed and shared through shared memory.
+// block barrier): 2 NI rows of one token and of one kind (q, k or v), a
+// half-warp (16 lanes x 8 elements) per row, all NI loads of a half-warp in
+// flight before the token's (cos, sin) pairs, two per lane, are computed and
+// shared through shared memory. Types are template arguments and the kind is
+// the warp's: with both decided row by row, the loads of a unit went out one
+// after the other and addresses took a third of the instructions (4608-token
+// prompts of two samples: 136 us against 83).
 constexpr int kAppWarps = 4;
 
-__device__ __forceinline__ void store_chunk8(void* base, int64_t off, int dt, int c, const float (&v)[8]) {
-  if (dt == kDtF32) {
-    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + off) + 2 * c;
-    p[0] = make_float4(v[0], v[1], v[2], v[3]);
-    p[1] = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-    uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + off) + c;
-    *p = make_uint4(pack_dt(dt, v[0], v[1]), pack_dt(dt, v[2], v[3]), pack_dt(dt, v[4], v[5]), pack_dt(dt, v[6], v[7]));
+template <int DT>
+struct Raw8 {  // eight elements as they lie in memory
+  uint4 a, b;  // b: fp32 only
+  __device__ __forceinline__ void load(const void* p, int64_t off) {
+    if constexpr (DT == kDtF32) {
+      a = ldg_nc_v4(static_cast<const float*>(p) + off);
+      b = ldg_nc_v4(static_cast<const float*>(p) + off + 4);
+    } else {
+      a = ldg_nc_v4(static_cast<const uint16_t*>(p) + off);
+    }
   }
-}
+  __device__ __forceinline__ void store(void* p, int64_t off) const {
+    if constexpr (DT == kDtF32) {
+      uint4* d = reinterpret_cast<uint4*>(static_cast<float*>(p) + off);
+      d[0] = a;
+      d[1] = b;
+    } else {
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + off) = a;
+    }
+  }
+  __device__ __forceinline__ void get(float (&y)[8]) const {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if constexpr (DT == kDtF32) y[e] = __uint_as_float(w[e]);
+      else if constexpr (DT == kDtBF16) y[e] = e & 1 ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
+      else y[e] = e & 1 ? f16_hi(w[e >> 1]) : f16_lo(w[e >> 1]);
+    }
+  }
+  __device__ __forceinline__ void set(const float (&y)[8]) {
+    if constexpr (DT == kDtF32) {
+      a = make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3]));
+      b = make_uint4(__float_as_uint(y[4]), __float_as_uint(y[5]), __float_as_uint(y[6]), __float_as_uint(y[7]));
+    } else {
+      a = make_uint4(pack16<DT == kDtF16>(y[0], y[1]), pack16<DT == kDtF16>(y[2], y[3]), pack16<DT == kDtF16>(y[4], y[5]),
+                     pack16<DT == kDtF16>(y[6], y[7]));
+    }
+  }
+};
 
 // (cos, sin) of pair `pr` at token (b, t). Integer positions: position times
 // the pair's turns per position in 64-bit fixed point, whose low 64 bits are
@@ -49,87 +82,94 @@ __device__ __forceinline__ float2 append_pair(const AppendParams& p, int b, int 
   return cs;
 }
 
-template <int NI>
-__global__ void __launch_bounds__(kAppWarps * 32) append_kernel(const __grid_constant__ AppendParams p, int units) {
+// SRC: type of q and k; DST: of v and the cache. u_q, u_k: units of a token's q
+// rows, and of its k (and v) rows.
+template <int NI, int SRC, int DST>
+__global__ void __launch_bounds__(kAppWarps * 32) append_kernel(const __grid_constant__ AppendParams p, int u_q, int u_k) {
   __shared__ float4 tab[kAppWarps][kPairs / 2];
   grid_dependency_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * kAppWarps + warp;
+  const int units = u_q + 2 * u_k;
   const int64_t tok = unit / units;
   if (tok >= static_cast<int64_t>(p.B) * p.T) return;
-  const int r_base = static_cast<int>(unit - tok * units) * 2 * NI + half;
+  const int u = static_cast<int>(unit - tok * units);
+  const int kind = u < u_q ? 0 : (u < u_q + u_k ? 1 : 2);  // q, k, v
+  const int h0 = (u - (kind == 0 ? 0 : (kind == 1 ? u_q : u_q + u_k))) * 2 * NI + half;
+  const int heads = kind == 0 ? p.H : p.kv.Hkv;
   const int b = static_cast<int>(tok / p.T), t = static_cast<int>(tok - static_cast<int64_t>(b) * p.T);
-  const int Hkv = p.kv.Hkv, n_rows = p.H + 2 * Hkv;
   const bool live = t < row_count(p.counts, b, p.T);
+  const int64_t q_off = b * p.qo_sb + t * p.qo_ss + 8 * l;
   if (!live) {  // a padded token: its q' rows are zero, nothing enters the cache
-    const float z[8] = {};
-#pragma unroll
-    for (int u = 0; u < NI; ++u)
-      if (r_base + 2 * u < p.H) store_chunk8(p.qo, b * p.qo_sb + t * p.qo_ss + (r_base + 2 * u) * p.qo_sh, p.kv.dt, l, z);
+    Raw8<DST> z;
+    z.a = z.b = make_uint4(0, 0, 0, 0);
+    if (kind == 0)
+      for (int h = h0; h < min(h0 + 2 * NI, heads); h += 2) z.store(p.qo, q_off + h * p.qo_sh);
     return;
   }
-  uint4 x[NI][2];
+  // where the rows go: q', or the token's slot of the cache
+  void* out = p.qo;
+  int64_t o_off = q_off, o_sh = p.qo_sh;
+  bool room = true;
+  auto find_slot = [&]() {
+    int pg = 0, row = 0;
+    room = kv_locate(p.kv, b, static_cast<int64_t>(__ldg(p.lens + b)) + t, &pg, &row);
+    if (!room && lane == 0) atomicOr(p.status, kStatusIndex);
+    out = kind == 1 ? p.kv.k : p.kv.v;
+    o_sh = kind == 1 ? p.kv.k_sh : p.kv.v_sh;
+    o_off = kind == 1 ? pg * p.kv.k_sp + row * p.kv.k_sr : pg * p.kv.v_sp + row * p.kv.v_sr;
+    o_off += 8 * l;
+  };
+  if (kind == 2) {
+    const int64_t off = b * p.v.sb + t * p.v.ss + 8 * l;
+    Raw8<DST> x[NI];
 #pragma unroll
-  for (int u = 0; u < NI; ++u) {
-    const int r = r_base + 2 * u;
-    x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
-    if (r < n_rows) {
-      const RowTensor& src = r < p.H ? p.q : (r < p.H + Hkv ? p.k : p.v);
-      const int h = r < p.H ? r : (r < p.H + Hkv ? r - p.H : r - p.H - Hkv);
-      const int64_t off = b * src.sb + t * src.ss + h * src.sh + 8 * l;
-      if (src.dt == kDtF32) {
-        x[u][0] = ldg_nc_v4(static_cast<const float*>(src.p) + off);
-        x[u][1] = ldg_nc_v4(static_cast<const float*>(src.p) + off + 4);
-      } else {
-        x[u][0] = ldg_nc_v4(static_cast<const uint16_t*>(src.p) + off);
-      }
-    }
+    for (int i = 0; i < NI; ++i)
+      if (h0 + 2 * i < heads) x[i].load(p.v.p, off + (h0 + 2 * i) * p.v.sh);
+    find_slot();
+    if (!room) return;
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      if (h0 + 2 * i < heads) x[i].store(out, o_off + (h0 + 2 * i) * o_sh);
+    return;
   }
-  int pg = -1, prow = 0;
-  if (r_base - half + 2 * NI > p.H && !kv_locate(p.kv, b, static_cast<int64_t>(__ldg(p.lens + b)) + t, &pg, &prow)) {
-    pg = -1;
-    if (lane == 0) atomicOr(p.status, kStatusIndex);
+  const void* src = kind == 0 ? p.q.p : p.k.p;
+  const int64_t sh = kind == 0 ? p.q.sh : p.k.sh;
+  const int64_t off = (kind == 0 ? b * p.q.sb + t * p.q.ss : b * p.k.sb + t * p.k.ss) + 8 * l;
+  Raw8<SRC> x[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int h = min(h0 + 2 * i, heads - 1);  // the shuffles below want every lane
+    x[i].load(src, off + h * sh);
   }
+  const float4* wp = reinterpret_cast<const float4*>(kind == 0 ? p.wq : p.wk) + 2 * l;
+  const float4 wa = __ldg(wp), wb = __ldg(wp + 1);
+  if (kind == 1) find_slot();
   const float2 c0 = append_pair(p, b, t, 2 * lane), c1 = append_pair(p, b, t, 2 * lane + 1);
   tab[warp][lane] = make_float4(c0.x, c0.y, c1.x, c1.y);
   __syncwarp();
   const float4 ca = tab[warp][2 * l], cb = tab[warp][2 * l + 1];
   const float2 cs[4] = {{ca.x, ca.y}, {ca.z, ca.w}, {cb.x, cb.y}, {cb.z, cb.w}};
-  const int64_t k_off = pg * p.kv.k_sp + prow * p.kv.k_sr, v_off = pg * p.kv.v_sp + prow * p.kv.v_sr;
+  const float wv[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
-  for (int u = 0; u < NI; ++u) {
-    const int r = r_base + 2 * u;
-    const bool is_q = r < p.H, is_v = r >= p.H + Hkv;
-    const int dt = is_v ? p.v.dt : p.q.dt;
-    const uint32_t w[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w, x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
+  for (int i = 0; i < NI; ++i) {
     float y[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (dt == kDtF32) y[e] = __uint_as_float(w[e]);
-      else if (dt == kDtBF16) y[e] = e & 1 ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
-      else y[e] = e & 1 ? f16_hi(w[e >> 1]) : f16_lo(w[e >> 1]);
-    }
+    x[i].get(y);
     float ss = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (r >= n_rows) continue;
-    if (!is_v) {
-      const float inv = rsqrtf(ss * (1.0f / kD) + p.eps);
-      const float4* wp = reinterpret_cast<const float4*>(is_q ? p.wq : p.wk) + 2 * l;
-      const float4 wa = __ldg(wp), wb = __ldg(wp + 1);
-      const float wv[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
+    const float inv = rsqrtf(ss * (1.0f / kD) + p.eps);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float n0 = y[2 * e] * inv * wv[2 * e], n1 = y[2 * e + 1] * inv * wv[2 * e + 1];
-        y[2 * e] = n0 * cs[e].x - n1 * cs[e].y;
-        y[2 * e + 1] = n0 * cs[e].y + n1 * cs[e].x;
-      }
+    for (int e = 0; e < 4; ++e) {
+      const float n0 = y[2 * e] * inv * wv[2 * e], n1 = y[2 * e + 1] * inv * wv[2 * e + 1];
+      y[2 * e] = n0 * cs[e].x - n1 * cs[e].y;
+      y[2 * e + 1] = n0 * cs[e].y + n1 * cs[e].x;
     }
-    if (is_q) store_chunk8(p.qo, b * p.qo_sb + t * p.qo_ss + r * p.qo_sh, p.kv.dt, l, y);
-    else if (pg >= 0 && !is_v) store_chunk8(p.kv.k, k_off + (r - p.H) * p.kv.k_sh, p.kv.dt, l, y);
-    else if (pg >= 0) store_chunk8(p.kv.v, v_off + (r - p.H - Hkv) * p.kv.v_sh, p.kv.dt, l, y);
+    Raw8<DST> r;
+    r.set(y);
+    if (room && h0 + 2 * i < heads) r.store(out, o_off + (h0 + 2 * i) * o_sh);
   }
 }
 
@@ -257,19 +297,29 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constan
 
 }  // namespace
 
-cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t stream) {
-  const int n_rows = p.H + 2 * p.kv.Hkv;
-  const int64_t tokens = static_cast<int64_t>(p.B) * p.T;
-  auto go = [&](auto kern, int ni) {
-    const int units = (n_rows + 2 * ni - 1) / (2 * ni);
-    return launch_chained(kern, dim3(static_cast<unsigned>((tokens * units + kAppWarps - 1) / kAppWarps)), dim3(kAppWarps * 32), 0,
-                          stream, p, units);
-  };
-  // as many rows per warp as still leave every SM (152) 16 warps: rows in
+template <int NI, int SRC, int DST>
+cudaError_t launch_append_t(const AppendParams& p, cudaStream_t stream) {
+  const int u_q = (p.H + 2 * NI - 1) / (2 * NI), u_k = (p.kv.Hkv + 2 * NI - 1) / (2 * NI);
+  const int64_t units = static_cast<int64_t>(p.B) * p.T * (u_q + 2 * u_k);
+  return launch_chained(append_kernel<NI, SRC, DST>, dim3(static_cast<unsigned>((units + kAppWarps - 1) / kAppWarps)),
+                        dim3(kAppWarps * 32), 0, stream, p, u_q, u_k);
+}
+template <int SRC, int DST>
+cudaError_t launch_append_types(const AppendParams& p, cudaStream_t stream) {
+  // as many rows per warp as still leave every SM (152) 32 warps: rows in
   // flight hide the reads, warps the rest
-  if (tokens * ((n_rows + 15) / 16) >= 152 * 16) return go(append_kernel<8>, 8);
-  if (tokens * ((n_rows + 3) / 4) >= 152 * 16) return go(append_kernel<2>, 2);
-  return go(append_kernel<1>, 1);
+  const int64_t rows = static_cast<int64_t>(p.B) * p.T * (p.H + 2 * p.kv.Hkv);
+  if (rows >= 152 * 32 * 8) return launch_append_t<4, SRC, DST>(p, stream);
+  return launch_append_t<1, SRC, DST>(p, stream);
+}
+
+cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t stream) {
+  const bool f32 = p.q.dt == kDtF32;
+  switch (p.kv.dt) {
+    case kDtBF16: return f32 ? launch_append_types<kDtF32, kDtBF16>(p, stream) : launch_append_types<kDtBF16, kDtBF16>(p, stream);
+    case kDtF16: return f32 ? launch_append_types<kDtF32, kDtF16>(p, stream) : launch_append_types<kDtF16, kDtF16>(p, stream);
+    default: return launch_append_types<kDtF32, kDtF32>(p, stream);
+  }
 }
 
 cudaError_t launch_cache_keep(const KeepParams& p, cudaStream_t stream) {
