@@ -117,24 +117,51 @@ struct Walk {
   __device__ __forceinline__ bool whole() const { return kt0 == 0 && kt1 == it.n; }
 };
 
+// The deal: CTA x has the tiles [first(x), first(x + 1)) of the call's, shares
+// that differ by one at most. 32-bit division where the numbers allow it.
+struct Deal {
+  long long total, share;
+  int ctas, extra;
+  __device__ __forceinline__ void make(long long tiles, int most) {
+    total = tiles;
+    ctas = static_cast<int>(min(static_cast<long long>(most), tiles));
+    share = ctas == 0 ? 0 : div(tiles, ctas);
+    extra = static_cast<int>(tiles - share * ctas);
+  }
+  static __device__ __forceinline__ long long div(long long a, long long b) {
+    if (((a | b) >> 31) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+  }
+  __device__ __forceinline__ long long first(int x) const { return x * share + min(x, extra); }
+  // the CTA that has tile t
+  __device__ __forceinline__ int holder(long long t) const {
+    const long long big = (share + 1) * extra;
+    return static_cast<int>(t < big ? div(t, share + 1) : extra + div(t - big, share));
+  }
+};
+
 struct Start {  // found by the block, read by every role
   int h, b, m, off;
-  long long left, total;
+  long long left;
 };
 
 // Where the CTA's range begins: every thread sums the key tiles of a run of
 // (sequence, group) pairs, a block scan places the runs.
 __device__ __forceinline__ void find_start(const TcAttnParams& p, int nt, long long* scan, Start* st) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t pairs = static_cast<int64_t>(p.c.B) * p.n_groups;
-  const int64_t per = (pairs + kTcThreads - 1) / kTcThreads, lo = min(pairs, tid * per), hi = min(pairs, lo + per);
+  const int pairs = p.c.B * p.n_groups;  // at most 2^30
+  const int per = (pairs + kTcThreads - 1) / kTcThreads, lo = min(pairs, tid * per), hi = min(pairs, lo + per);
+  const int b0 = p.n_groups == 1 ? lo : lo / p.n_groups, m0 = lo - b0 * p.n_groups;
   long long sum = 0;
-  for (int64_t e = lo; e < hi; ++e) {
-    const int b = static_cast<int>(e / p.n_groups), m = static_cast<int>(e - static_cast<int64_t>(b) * p.n_groups);
+  for (int e = lo, b = b0, m = m0; e < hi; ++e) {
     const Item it = item_of(p, nt, b, m);
     sum += it.n;
     if (m == 0 && blockIdx.x == 0 && (__ldg(p.c.lens + b) < 0 || static_cast<int64_t>(__ldg(p.c.lens + b)) + it.cnt > it.keys))
       atomicOr(p.c.status, kStatusIndex);
+    if (++m == p.n_groups) {
+      m = 0;
+      ++b;
+    }
   }
   long long inc = sum;
 #pragma unroll
@@ -146,41 +173,46 @@ __device__ __forceinline__ void find_start(const TcAttnParams& p, int nt, long l
   if (tid == 0) st->left = 0;
   __syncthreads();
   long long before = 0, one = 0;
+#pragma unroll
   for (int w = 0; w < kTcWarps; ++w) {
     if (w < warp) before += scan[w];
     one += scan[w];
   }
-  const long long total = one * p.c.kv.Hkv;
-  const long long ctas = min(static_cast<long long>(p.ctas), total);
-  if (tid == 0) st->total = total;
-  if (blockIdx.x < ctas) {
-    const long long s0 = blockIdx.x * total / ctas, s1 = (blockIdx.x + 1) * total / ctas;
-    const int h = static_cast<int>(s0 / one);
+  Deal d;
+  d.make(one * p.c.kv.Hkv, p.ctas);
+  if (blockIdx.x < d.ctas) {
+    const long long s0 = d.first(blockIdx.x);
+    const int h = static_cast<int>(Deal::div(s0, one));
     long long rem = s0 - h * one - (before + inc - sum);
     if (rem >= 0 && rem < sum) {  // one thread
-      for (int64_t e = lo; e < hi; ++e) {
-        const int b = static_cast<int>(e / p.n_groups), m = static_cast<int>(e - static_cast<int64_t>(b) * p.n_groups);
+      for (int e = lo, b = b0, m = m0; e < hi; ++e) {
         const Item it = item_of(p, nt, b, m);
         if (rem < it.n) {
           st->h = h;
           st->b = b;
           st->m = m;
           st->off = static_cast<int>(rem);
-          st->left = s1 - s0;
-          JoinMeta& meta = p.meta[blockIdx.x];
-          meta.total = total;
-          meta.item_start = s0 - rem;
-          meta.n = rem > 0 ? it.n : 0;
-          meta.h = h;
-          meta.b = b;
-          meta.m = m;
+          st->left = d.first(blockIdx.x + 1) - s0;
+          // for the join: is this border the first inside of its item, and
+          // who has the item's tiles?
+          JoinMeta meta{0, 0, h, b, m, it.cnt};
+          const long long item = s0 - rem;
+          if (rem > 0 && d.first(blockIdx.x - 1) <= item) {
+            meta.parts = d.holder(item + it.n - 1) - static_cast<int>(blockIdx.x) + 2;
+            meta.slot0 = 2 * (static_cast<int>(blockIdx.x) - 1) + (d.first(blockIdx.x - 1) == item ? 0 : 1);
+          }
+          p.meta[blockIdx.x] = meta;
           break;
         }
         rem -= it.n;
+        if (++m == p.n_groups) {
+          m = 0;
+          ++b;
+        }
       }
     }
   } else if (tid == 0) {
-    p.meta[blockIdx.x].n = 0;
+    p.meta[blockIdx.x].parts = 0;
   }
   __syncthreads();
 }
@@ -674,44 +706,50 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
 // at the border before CTA x + 1 and, if it is an item's first inner border,
 // at rows 32 y .. of that item. A warp takes a row, a lane four columns.
 constexpr int kJoinRows = 32;
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ TcAttnParams P, int nt) {
+__global__ void __launch_bounds__(256, 6) join_kernel(const __grid_constant__ TcAttnParams P, int nt) {
   grid_dependency_wait();
   const CacheAttnParams& c = P.c;
   const int cta = blockIdx.x + 1;
   const JoinMeta me = P.meta[cta];
-  if (me.n == 0) return;
-  const long long ctas = min(static_cast<long long>(P.ctas), me.total);
-  auto first_tile = [&](long long x) { return x * me.total / ctas; };
-  if (first_tile(cta - 1) > me.item_start) return;  // an earlier border lies inside the item
-  int last = cta;
-  while (last + 1 < ctas && first_tile(last + 1) < me.item_start + me.n) ++last;
-  const int parts = last - cta + 2;
-  const int64_t slot0 = 2 * static_cast<int64_t>(cta - 1) + (first_tile(cta - 1) == me.item_start ? 0 : 1);
-  const Item it = item_of(P, nt, me.b, me.m);
+  if (me.parts == 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tile_rows = P.tpt * c.group;
   for (int r = blockIdx.y * kJoinRows + warp; r < min((static_cast<int>(blockIdx.y) + 1) * kJoinRows, P.part_rows); r += 8) {
     const int ti = r / tile_rows, rr = r - ti * tile_rows;
     const int t = (me.m * nt + ti) * P.tpt + rr / c.group, h = me.h * c.group + rr % c.group;
-    if (t >= it.cnt) continue;
-    auto row_of = [&](int i) { return (i == 0 ? slot0 : 2 * static_cast<int64_t>(cta - 1 + i)) * P.part_rows + r; };
-    float m = -INFINITY;
-    for (int i = lane; i < parts; i += 32) m = fmaxf(m, P.part_ml[row_of(i)].x);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-    const float m_use = m == -INFINITY ? 0.f : m;
+    if (t >= me.cnt) continue;
+    // the running maximum and sum over the parts, four of them in flight
+    float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < parts; ++i) {
-      const int64_t row = row_of(i);
-      const float2 x = P.part_ml[row];
-      const float4 y = reinterpret_cast<const float4*>(c.part + row * kD)[lane];
-      const float f = ex2(x.x - m_use);
-      l = fmaf(f, x.y, l);
-      o.x = fmaf(f, y.x, o.x);
-      o.y = fmaf(f, y.y, o.y);
-      o.z = fmaf(f, y.z, o.z);
-      o.w = fmaf(f, y.w, o.w);
+    for (int i0 = 0; i0 < me.parts; i0 += 4) {
+      float2 x[4];
+      float4 y[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u;
+        x[u] = make_float2(-INFINITY, 0.f);
+        y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < me.parts) {  // the same for the whole block
+          const int64_t row = (i == 0 ? me.slot0 : 2 * static_cast<int64_t>(cta - 1 + i)) * P.part_rows + r;
+          x[u] = P.part_ml[row];
+          y[u] = reinterpret_cast<const float4*>(c.part + row * kD)[lane];
+        }
+      }
+      float top = m;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) top = fmaxf(top, x[u].x);
+      const float use = top == -INFINITY ? 0.f : top, f0 = ex2(m - use);
+      m = top;
+      l *= f0;
+      o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float f = ex2(x[u].x - use);
+        l = fmaf(f, x[u].y, l);
+        o.x = fmaf(f, y[u].x, o.x);
+        o.y = fmaf(f, y[u].y, o.y);
+        o.z = fmaf(f, y[u].z, o.z);
+        o.w = fmaf(f, y[u].w, o.w);
+      }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const int64_t off = me.b * c.o_sb + static_cast<int64_t>(t) * c.o_ss + static_cast<int64_t>(h) * c.o_sh + 4 * lane;

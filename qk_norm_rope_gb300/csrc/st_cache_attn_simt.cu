@@ -7,8 +7,11 @@
 // p.splits CTAs, since a decoding step has few rows and many keys. Each CTA
 // leaves (O unnormalised, running maximum, sum) in the workspace and a second
 // kernel joins them; with one split it writes O and LSE itself. Bound by the
-// fp32 FMA rate and shared-memory reads: a thread holds 2 x 4 scores and 4 x 4
-// outputs, so that one 16-byte read feeds 5 to 8 FMAs.
+// fp32 FMA rate: a thread holds 4 x 4 scores and 8 x 4 outputs, so that shared
+// memory (8 and 12 16-byte reads, mostly broadcasts, for 64 and 128 FMAs) keeps
+// up; with half as many rows (2 x 4 and 4 x 4) it did not, 47 us against 37 for
+// four trees of 13 nodes after up to 2001 tokens. The weights P take K's place
+// in shared memory once the scores are done, so that two CTAs fit on an SM.
 #include <atomic>
 #include "st_kernels.h"
 #include "st_serve.h"
@@ -21,10 +24,12 @@ constexpr int kR = kSimtRows, kN = kSimtKeys, kThreads = 256;
 constexpr int kPad = kD + 4, kPadP = kN + 4;
 
 struct Smem {
-  float q[kR][kPad];
-  float k[kN][kPad];
+  float q[kR][kD];  // read as broadcasts
+  union {
+    float k[kN][kPad];
+    float p[kR][kPadP];
+  };
   float v[kN][kD];
-  float p[kR][kPadP];
   float corr[kR], m[kR], l[kR];
   uint32_t anc[kR][kTreeWords];
   int64_t k_off[2][kN], v_off[2][kN];  // element offsets of a tile's rows, by its parity; < 0: no row
@@ -36,63 +41,57 @@ __device__ __forceinline__ bool tree_sees(const uint32_t* anc, int node) {
   return node < kMaxTree && ((anc[node >> 5] >> (node & 31)) & 1u);
 }
 
-__global__ void __launch_bounds__(kThreads) simt_kernel(const __grid_constant__ CacheAttnParams p, int n_rt) {
+__global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant__ CacheAttnParams p, int n_rt) {
   extern __shared__ __align__(16) uint8_t raw[];
   Smem& s = *reinterpret_cast<Smem*>(raw);
   grid_dependency_wait();
   const int tid = threadIdx.x;
   const int64_t item = blockIdx.x;
   const int split = blockIdx.y;
-  const int rt = static_cast<int>(item % n_rt), hk = static_cast<int>(item / n_rt % p.kv.Hkv);
-  const int b = static_cast<int>(item / n_rt / p.kv.Hkv);
+  const unsigned it32 = blockIdx.x;  // items are at most 2^30
+  const int rt = static_cast<int>(it32 % n_rt), hk = static_cast<int>(it32 / n_rt % p.kv.Hkv);
+  const int b = static_cast<int>(it32 / n_rt / p.kv.Hkv);
   const int G = p.group;
   const int64_t rows = static_cast<int64_t>(p.T) * G;
   const int64_t row0 = static_cast<int64_t>(rt) * kR;
+  // row r of the item: token t0 + (g0 + r) / G, head (g0 + r) % G of the group
+  const int t0 = static_cast<int>(row0 / G), g0 = static_cast<int>(row0 - static_cast<int64_t>(t0) * G);
+  const int n_here = static_cast<int>(min(rows - row0, static_cast<int64_t>(kR)));
   const int cnt = row_count(p.counts, b, p.T);
   int prefix;
   const int keys = key_count(p, b, cnt, &prefix);
   if (tid == 0 && split == 0 && (__ldg(p.lens + b) < 0 || static_cast<int64_t>(__ldg(p.lens + b)) + cnt > keys)) atomicOr(p.status, kStatusIndex);
 
   // the last key that any row of the item sees
-  const int t_last = static_cast<int>(min((row0 + kR - 1) / G, static_cast<int64_t>(p.T) - 1));
+  const int t_last = t0 + (g0 + n_here - 1) / G;
   const int end = p.parents ? keys : min(keys, prefix + min(t_last + 1, cnt));
-  const int n_tiles = row0 / G < cnt ? (end + kN - 1) / kN : 0;
+  const int n_tiles = t0 < cnt ? (end + kN - 1) / kN : 0;
   const int j_lo = static_cast<int>(static_cast<int64_t>(n_tiles) * split / p.splits);
   const int j_hi = static_cast<int>(static_cast<int64_t>(n_tiles) * (split + 1) / p.splits);
 
-  for (int e = tid; e < kR * kD / 8; e += kThreads) {
-    const int r = e / (kD / 8), c = e % (kD / 8);
-    const int64_t row = row0 + r;
-    float x[8] = {};
-    if (row < rows) {
-      const int t = static_cast<int>(row / G), h = hk * G + static_cast<int>(row % G);
-      if (t < cnt) load_chunk8(p.q.p, b * p.q.sb + t * p.q.ss + h * p.q.sh, p.q.dt, c, x);
-    }
-#pragma unroll
-    for (int u = 0; u < 8; ++u) s.q[r][8 * c + u] = x[u] * p.scale_log2;
-  }
-  if (tid < kR) {
-    s.m[tid] = -INFINITY;
-    s.l[tid] = 0.f;
-    if (p.parents) {  // a walk up from the row's node; parents come before children
-      const int64_t row = row0 + tid;
-      for (int w = 0; w < kTreeWords; ++w) s.anc[tid][w] = 0;
-      int node = row < rows ? static_cast<int>(row / G) : -1;
-      if (node >= cnt) node = -1;
-      while (node >= 0) {
-        s.anc[tid][node >> 5] |= 1u << (node & 31);
-        const int up = __ldg(p.parents + b * p.par_sb + node);
-        if (up >= node || up < -1) {
-          atomicOr(p.status, kStatusIndex);
-          break;
-        }
-        node = up;
+  if (tid < kR && p.parents) {  // a walk up from the row's node; parents come before children
+    for (int w = 0; w < kTreeWords; ++w) s.anc[tid][w] = 0;
+    int node = tid < n_here ? t0 + (g0 + tid) / G : -1;
+    if (node >= cnt) node = -1;
+    while (node >= 0) {
+      s.anc[tid][node >> 5] |= 1u << (node & 31);
+      const int up = __ldg(p.parents + b * p.par_sb + node);
+      if (up >= node || up < -1) {
+        atomicOr(p.status, kStatusIndex);
+        break;
       }
+      node = up;
     }
   }
-  float o[4][4] = {};
-  const int tr = tid >> 4, tc = tid & 15;   // scores: rows tr, tr + 16; keys tc + 16 i
-  const int rg = tid >> 5, dg = tid & 31;   // outputs: rows 4 rg + i; dims 4 dg..
+  float o[8][4] = {};
+  float m_run[4], l_run[4];  // of the thread's score rows: the maximum, and the sum over the thread's own keys
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    m_run[w] = -INFINITY;
+    l_run[w] = 0.f;
+  }
+  const int tr = tid >> 4, tc = tid & 15;   // scores: rows tr + 16 w; keys tc + 16 i
+  const int rg = tid >> 5, dg = tid & 31;   // outputs: rows 8 rg + i; dims 4 dg..
   const bool f32 = p.kv.dt == kDtF32;
   auto locate = [&](int jt) {  // the rows of key tile jt
     if (tid < kN && jt < j_hi) {
@@ -147,77 +146,92 @@ __global__ void __launch_bounds__(kThreads) simt_kernel(const __grid_constant__ 
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   locate(j_lo);
+  if (tid < kR) {  // the offsets of the query rows, where the second tile's will be
+    const int t = t0 + (g0 + tid) / G, h = hk * G + (g0 + tid) % G;
+    s.k_off[(j_lo + 1) & 1][tid] = tid < n_here && t < cnt ? b * p.q.sb + t * p.q.ss + h * p.q.sh : -1;
+  }
   __syncthreads();
   if (j_lo < j_hi) {
+    fetch(p.q.p, s.k_off[(j_lo + 1) & 1], &s.q[0][0], kD);
     fetch(p.kv.k, s.k_off[j_lo & 1], &s.k[0][0], kPad);
     fetch(p.kv.v, s.v_off[j_lo & 1], &s.v[0][0], kD);
   }
   for (int jt = j_lo; jt < j_hi; ++jt) {
     const int j0 = jt * kN;
-    locate(jt + 1);
-    asm volatile("cp.async.wait_group 1;" ::: "memory");  // K
+    asm volatile("cp.async.wait_group 1;" ::: "memory");  // Q and K
     __syncthreads();
-    float sc[2][4] = {};
-#pragma unroll 8
+    locate(jt + 1);
+    float sc[4][4] = {};
+#pragma unroll 4
     for (int d = 0; d < kD; d += 4) {
-      const float4 q0 = *reinterpret_cast<const float4*>(&s.q[tr][d]), q1 = *reinterpret_cast<const float4*>(&s.q[tr + 16][d]);
+      float4 qq[4], kk[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 kk = *reinterpret_cast<const float4*>(&s.k[tc + 16 * i][d]);
-        sc[0][i] = fmaf(q0.x, kk.x, fmaf(q0.y, kk.y, fmaf(q0.z, kk.z, fmaf(q0.w, kk.w, sc[0][i]))));
-        sc[1][i] = fmaf(q1.x, kk.x, fmaf(q1.y, kk.y, fmaf(q1.z, kk.z, fmaf(q1.w, kk.w, sc[1][i]))));
+      for (int w = 0; w < 4; ++w) qq[w] = *reinterpret_cast<const float4*>(&s.q[tr + 16 * w][d]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) kk[i] = *reinterpret_cast<const float4*>(&s.k[tc + 16 * i][d]);
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          sc[w][i] = fmaf(qq[w].x, kk[i].x, fmaf(qq[w].y, kk[i].y, fmaf(qq[w].z, kk[i].z, fmaf(qq[w].w, kk[i].w, sc[w][i]))));
+    }
+    __syncthreads();  // K is read: P takes its place
+    const float sl = p.scale_log2;
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sc[w][i] *= sl;
+    if (j0 + kN > prefix) {  // rows of padding see anything here: they are dropped at the end
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const int r = tr + 16 * w, t = t0 + (g0 + r) / G;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = j0 + tc + 16 * i, node = j - prefix;
+          const bool sees = j < keys && (node < 0 || (p.parents ? tree_sees(s.anc[r], node) : node <= t));
+          if (!sees) sc[w][i] = -INFINITY;
+        }
       }
     }
+    float mt[4], sum[4];
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
+    for (int w = 0; w < 4; ++w) mt[w] = fmaxf(fmaxf(sc[w][0], sc[w][1]), fmaxf(sc[w][2], sc[w][3]));
+#pragma unroll
+    for (int x = 8; x > 0; x >>= 1)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) mt[w] = fmaxf(mt[w], __shfl_xor_sync(0xffffffffu, mt[w], x));
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
       const int r = tr + 16 * w;
-      const int64_t row = row0 + r;
-      const int t = row < rows ? static_cast<int>(row / G) : p.T;
-      float mt = -INFINITY;
+      const float m_new = fmaxf(m_run[w], mt[w]), m_use = m_new == -INFINITY ? 0.f : m_new;
+      if (tc == 0) s.corr[r] = ex2(m_run[w] - m_use);  // 0 while the row has seen nothing
+      l_run[w] *= ex2(m_run[w] - m_use);
+      m_run[w] = m_new;
+      sum[w] = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int j = j0 + tc + 16 * i, node = j - prefix;
-        const bool sees = t < cnt && j < keys && (node < 0 || (p.parents ? tree_sees(s.anc[r], node) : node <= t));
-        if (!sees) sc[w][i] = -INFINITY;
-        mt = fmaxf(mt, sc[w][i]);
-      }
-#pragma unroll
-      for (int x = 8; x > 0; x >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
-      const float m_old = s.m[r], m_new = fmaxf(m_old, mt), m_use = m_new == -INFINITY ? 0.f : m_new;
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float e = exp2f(sc[w][i] - m_use);
+        const float e = ex2(sc[w][i] - m_use);
         s.p[r][tc + 16 * i] = e;
-        sum += e;
+        sum[w] += e;
       }
-#pragma unroll
-      for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-      __syncwarp();  // every lane has read the row's old maximum
-      if (tc == 0) {
-        const float corr = exp2f(m_old - m_use);  // 0 while the row has seen nothing
-        s.corr[r] = corr;
-        s.m[r] = m_new;
-        s.l[r] = s.l[r] * corr + sum;
-      }
+      l_run[w] += sum[w];  // this lane's keys
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");  // V
     __syncthreads();
-    if (jt + 1 < j_hi) fetch(p.kv.k, s.k_off[(jt + 1) & 1], &s.k[0][0], kPad);  // under this tile's PV
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float corr = s.corr[4 * rg + i];
+    for (int i = 0; i < 8; ++i) {
+      const float corr = s.corr[8 * rg + i];
 #pragma unroll
       for (int u = 0; u < 4; ++u) o[i][u] *= corr;
     }
-#pragma unroll 4
+#pragma unroll 2
     for (int k = 0; k < kN; k += 4) {
       float4 vv[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) vv[u] = *reinterpret_cast<const float4*>(&s.v[k + u][4 * dg]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 pp = *reinterpret_cast<const float4*>(&s.p[4 * rg + i][k]);
+      for (int i = 0; i < 8; ++i) {
+        const float4 pp = *reinterpret_cast<const float4*>(&s.p[8 * rg + i][k]);
         const float pw[4] = {pp.x, pp.y, pp.z, pp.w};
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -229,14 +243,27 @@ __global__ void __launch_bounds__(kThreads) simt_kernel(const __grid_constant__ 
       }
     }
     __syncthreads();
-    if (jt + 1 < j_hi) fetch(p.kv.v, s.v_off[(jt + 1) & 1], &s.v[0][0], kD);
+    if (jt + 1 < j_hi) {
+      fetch(p.kv.k, s.k_off[(jt + 1) & 1], &s.k[0][0], kPad);
+      fetch(p.kv.v, s.v_off[(jt + 1) & 1], &s.v[0][0], kD);
+    }
+  }
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+#pragma unroll
+    for (int x = 8; x > 0; x >>= 1) l_run[w] += __shfl_xor_sync(0xffffffffu, l_run[w], x);
+    const int r = tr + 16 * w;
+    const bool there = r < n_here && t0 + (g0 + r) / G < cnt;  // padding: nothing seen
+    if (tc == 0) {
+      s.m[r] = there ? m_run[w] : -INFINITY;
+      s.l[r] = there ? l_run[w] : 0.f;
+    }
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 4 * rg + i;
-    const int64_t row = row0 + r;
-    if (row >= rows) continue;
+  for (int i = 0; i < 8; ++i) {
+    const int r = 8 * rg + i;
+    if (r >= n_here) continue;
     if (p.splits > 1) {
       const int64_t slot = (item * p.splits + split) * kR + r;
       *reinterpret_cast<float4*>(p.part + slot * kD + 4 * dg) = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
@@ -247,7 +274,7 @@ __global__ void __launch_bounds__(kThreads) simt_kernel(const __grid_constant__ 
       continue;
     }
     const float l = s.l[r], inv = l == 0.f ? 0.f : 1.f / l;
-    const int t = static_cast<int>(row / G), h = hk * G + static_cast<int>(row % G);
+    const int t = t0 + (g0 + r) / G, h = hk * G + (g0 + r) % G;
     const int64_t off = b * p.o_sb + t * p.o_ss + h * p.o_sh + 4 * dg;
     if (p.kv.dt == kDtF32)
       *reinterpret_cast<float4*>(static_cast<float*>(p.o) + off) = make_float4(o[i][0] * inv, o[i][1] * inv, o[i][2] * inv, o[i][3] * inv);

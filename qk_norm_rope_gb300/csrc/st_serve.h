@@ -90,7 +90,7 @@ __device__ __forceinline__ int key_count(const CacheAttnParams& p, int b, int co
 }
 
 // SIMT kernel: items of kSimtRows query rows of one K/V head.
-constexpr int kSimtRows = 32, kSimtKeys = 64;
+constexpr int kSimtRows = 64, kSimtKeys = 64;
 inline int64_t simt_items(int B, int T, int H, int Hkv) {
   return static_cast<int64_t>(B) * Hkv * ((static_cast<int64_t>(T) * (H / Hkv) + kSimtRows - 1) / kSimtRows);
 }
@@ -113,11 +113,11 @@ struct TcAttnParams {
   struct JoinMeta* meta;       // [ctas], workspace
   float2* part_ml;             // [2 ctas, part_rows] (reference, sum); c.part: [2 ctas, part_rows, D]
 };
+// Of each CTA: the item whose first inner border is the CTA's beginning. Its
+// parts lie in slot0 and then in the slots 2 x of the CTAs x from this one on.
 struct JoinMeta {
-  long long total;             // key tiles of the call
-  long long item_start;        // first tile of the item that this CTA's range begins inside of
-  int n;                       // its tiles; 0: the range begins with an item
-  int h, b, m;
+  int parts, slot0;            // parts = 0: there is no such item
+  int h, b, m, cnt;
 };
 inline int tc_tiles(int T, int group) { return static_cast<int64_t>(T) * group > 128 ? 2 : 1; }
 cudaError_t launch_cache_attn_tc(const TcAttnParams& p, int nt, bool f16, cudaStream_t stream);

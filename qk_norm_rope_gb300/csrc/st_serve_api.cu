@@ -145,7 +145,7 @@ st_status plan_attn(const st_tensor* q, const st_kv_cache* cache, const st_tenso
     t.part_rows = static_cast<int>(std::min<int64_t>(p.T, tpg)) * p.group;
     const int64_t cap_tiles = (static_cast<int64_t>(p.kv.max_pages) * p.kv.page + kTile - 1) / kTile;
     const int64_t items = static_cast<int64_t>(p.B) * p.kv.Hkv * t.n_groups;
-    if (items > (1ll << 40)) return fail(ST_ERR_SHAPE, "too many query rows");
+    if (items > (1ll << 40) || static_cast<int64_t>(p.B) * t.n_groups > (1ll << 30)) return fail(ST_ERR_SHAPE, "too many query rows");
     t.ctas = static_cast<int>(items >= kSmCount ? kSmCount : std::min<int64_t>(kSmCount, items * cap_tiles));
     // a CTA leaves at most two parts: one at each end of its range
     size_t off = align256(static_cast<size_t>(2) * t.ctas * t.part_rows * kD * sizeof(float));
