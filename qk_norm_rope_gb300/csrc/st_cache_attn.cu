@@ -11,6 +11,11 @@
 // (O unnormalised, reference, sum) in the workspace, at most one such part at
 // each end of its range, and the join kernel puts them together.
 //
+// Few items with short caches (CL, below): instead of the deal, a cluster of
+// CTAs per item shares its key tiles out evenly and joins its parts through
+// distributed shared memory, which saves the scan for the range's beginning
+// and the second launch.
+//
 // Roles (512 threads, one CTA per SM):
 //   warps 0-7   softmax, two groups of four warps; thread = query row = TMEM lane
 //   warps 8-11  Q rows of the next item into shared memory
@@ -313,13 +318,30 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float sc,
   tmem_st_wait();
 }
 
-template <int NT, bool F16, bool TREE>
+// Reads of a peer CTA's shared memory (cluster addresses from mapa).
+__device__ __forceinline__ float4 ld_peer_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ld_peer_f2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+  return v;
+}
+
+// A part in shared memory: 128 rows of 128 floats over the K stages, the
+// 16-byte chunks of a row permuted so that neither a thread per row (writing)
+// nor a warp per row (reading) meets bank conflicts; (reference, sum) of the
+// rows over the V stages.
+__device__ __forceinline__ uint32_t stage_off(int row, int chunk) { return row * 512u + ((chunk ^ (row & 31)) << 4); }
+
+template <int NT, bool F16, bool TREE, bool CL>
 __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant__ TcAttnParams P) {
   using L = Lay<NT>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw;
   const CacheAttnParams& c = P.c;
-  grid_dependency_wait();
   if (smem_u32(sm) & 1023u) {
     if (threadIdx.x == 0) atomicOr(c.status, kStatusLayout);
     return;
@@ -361,18 +383,32 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
   }
   if (tid == kWarpK * 32) tma_prefetch_desc(&P.tmap_k);
   if (tid == kWarpV * 32) tma_prefetch_desc(&P.tmap_v);
-  // the scan's scratch lies in the Q tile, which is written later
-  find_start(P, NT, reinterpret_cast<long long*>(sm + L::q), start);
+  grid_dependency_wait();  // what came before touches no global memory
+  Walk wk;
+  if constexpr (CL) {
+    const int rank = static_cast<int>(cluster_rank()), item = blockIdx.x / P.cluster;
+    wk.m = item % P.n_groups;
+    wk.b = item / P.n_groups % c.B;
+    wk.h = item / P.n_groups / c.B;
+    const Item it = item_of(P, NT, wk.b, wk.m);
+    wk.off = it.n * rank / P.cluster;
+    wk.left = it.n * (rank + 1) / P.cluster - wk.off;
+    if (tid == 0 && rank == 0 && wk.h == 0 && wk.m == 0 &&
+        (__ldg(c.lens + wk.b) < 0 || static_cast<int64_t>(__ldg(c.lens + wk.b)) + it.cnt > it.keys))
+      atomicOr(c.status, kStatusIndex);
+  } else {
+    // the scan's scratch lies in the Q tile, which is written later
+    find_start(P, NT, reinterpret_cast<long long*>(sm + L::q), start);
+    wk.h = start->h;
+    wk.b = start->b;
+    wk.m = start->m;
+    wk.off = start->off;
+    wk.left = start->left;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tslot;
-  Walk wk;
-  wk.h = start->h;
-  wk.b = start->b;
-  wk.m = start->m;
-  wk.off = start->off;
-  wk.left = start->left;
   const int G = c.group, tile_rows = P.tpt * G;
 
   if (warp < kSoftWarps) {
@@ -491,7 +527,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
           const float2 other = ml[(slot ^ 1) * 128 + r];
           const float m = fmaxf(m_run, other.x), m_use = m == -INFINITY ? 0.f : m;
           const float f0 = ex2(m_run - m_use), f1 = ex2(other.x - m_use);
-          const float l = f0 * l_run + f1 * other.y, inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+          const float l = f0 * l_run + f1 * other.y, inv = whole && !CL ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
           const bool mine = steps > 1 || (g & 1) == slot, theirs = steps > 1 || (g & 1) != slot;
           const int64_t ooff = wk.pb * c.o_sb + static_cast<int64_t>(t) * c.o_ss + static_cast<int64_t>(h) * c.o_sh;
           const int64_t prow = pslot * P.part_rows + r;
@@ -508,9 +544,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
               const float v0 = mine ? __uint_as_float(a[e]) : 0.f, v1 = theirs ? __uint_as_float(d[e]) : 0.f;
               y[e] = fmaf(v1, f1, v0 * f0) * inv;
             }
+            if constexpr (CL) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                *reinterpret_cast<float4*>(sm + L::k + stage_off(r, 8 * q4 + e)) = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+              continue;
+            }
             if (valid) store_chunk32(whole ? c.o : c.part, whole ? ooff : prow * kD, whole ? c.kv.dt : kDtF32, q4, y);
           }
-          if (valid && slot == 0) {
+          if (CL && slot == 0) reinterpret_cast<float2*>(sm + L::v)[r] = make_float2(m, l);
+          if (!CL && valid && slot == 0) {
             if (whole) c.lse[(static_cast<int64_t>(wk.pb) * c.H + h) * c.T + t] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
             else P.part_ml[prow] = make_float2(m, l);
           }
@@ -525,6 +568,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
       vc += wk.kt1 - wk.kt0;
       ++n_piece;
     }
+    if (CL && n_piece == 0 && slot == 0) reinterpret_cast<float2*>(sm + L::v)[r] = make_float2(-INFINITY, 0.f);
   } else if (warp < kWarpQ0 + kQWarps) {
     // ---------------------------------------------------------------- Q rows
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
@@ -695,7 +739,48 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
     atomicAdd(c.counters + kCtrTimeouts, 1ull);
   }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (CL) {
+    static_assert(NT == 1 && L::KS * kTileBytes >= 128 * 512, "a part fits over the K stages");
+    cluster_sync();  // every CTA's part is in place
+    const int rank = static_cast<int>(cluster_rank()), item = blockIdx.x / P.cluster;
+    const int m = item % P.n_groups, b = item / P.n_groups % c.B, h = item / P.n_groups / c.B;
+    const int rows = max(0, min(P.tpt, row_count(c.counts, b, c.T) - m * P.tpt)) * G;
+    for (int r = rank * kTcWarps + warp; r < rows; r += P.cluster * kTcWarps) {
+      float2 x[kMaxClusterAttn];
+      float4 y[kMaxClusterAttn];
+#pragma unroll
+      for (int i = 0; i < kMaxClusterAttn; ++i) {
+        x[i] = make_float2(-INFINITY, 0.f);
+        y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < P.cluster) {
+          x[i] = ld_peer_f2(mapa_shared(smem_u32(sm + L::v) + 8 * r, i));
+          y[i] = ld_peer_f4(mapa_shared(smem_u32(sm + L::k) + stage_off(r, lane_id), i));
+        }
+      }
+      float top = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int i = 0; i < kMaxClusterAttn; ++i) top = fmaxf(top, x[i].x);
+      const float use = top == -INFINITY ? 0.f : top;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kMaxClusterAttn; ++i) {
+        if (x[i].x == -INFINITY) continue;  // a CTA without tiles left nothing there
+        const float f = ex2(x[i].x - use);
+        l = fmaf(f, x[i].y, l);
+        o = make_float4(fmaf(f, y[i].x, o.x), fmaf(f, y[i].y, o.y), fmaf(f, y[i].z, o.z), fmaf(f, y[i].w, o.w));
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const int t = m * P.tpt + r / G, hq = h * G + r % G;
+      const int64_t off = b * c.o_sb + static_cast<int64_t>(t) * c.o_ss + static_cast<int64_t>(hq) * c.o_sh + 4 * lane_id;
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(c.o) + off) =
+          make_uint2(pack16<F16>(o.x * inv, o.y * inv), pack16<F16>(o.z * inv, o.w * inv));
+      if (lane_id == 0) c.lse[(static_cast<int64_t>(b) * c.H + hq) * c.T + t] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
+    }
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while a peer reads its part
+  } else {
+    __syncthreads();
+  }
   if (warp == kWarpMma) {
     __syncwarp();
     tmem_dealloc(tmem, 512);
@@ -704,9 +789,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
 
 // Joins the parts of an item whose tiles several CTAs held: block (x, y) looks
 // at the border before CTA x + 1 and, if it is an item's first inner border,
-// at rows 32 y .. of that item. A warp takes a row, a lane four columns.
+// at rows 32 y .. of that item. A warp takes a row, a lane four columns; U
+// parts are in flight: many where there are few rows (a decoding step, whose
+// items are spread over many CTAs), few and more warps per SM where there are
+// many rows.
 constexpr int kJoinRows = 32;
-__global__ void __launch_bounds__(256, 6) join_kernel(const __grid_constant__ TcAttnParams P, int nt) {
+template <int U>
+__global__ void __launch_bounds__(256, U > 4 ? 2 : 6) join_kernel(const __grid_constant__ TcAttnParams P, int nt) {
   grid_dependency_wait();
   const CacheAttnParams& c = P.c;
   const int cta = blockIdx.x + 1;
@@ -717,14 +806,14 @@ __global__ void __launch_bounds__(256, 6) join_kernel(const __grid_constant__ Tc
     const int ti = r / tile_rows, rr = r - ti * tile_rows;
     const int t = (me.m * nt + ti) * P.tpt + rr / c.group, h = me.h * c.group + rr % c.group;
     if (t >= me.cnt) continue;
-    // the running maximum and sum over the parts, four of them in flight
+    // the running maximum and sum over the parts
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < me.parts; i0 += 4) {
-      float2 x[4];
-      float4 y[4];
+    for (int i0 = 0; i0 < me.parts; i0 += U) {
+      float2 x[U];
+      float4 y[U];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < U; ++u) {
         const int i = i0 + u;
         x[u] = make_float2(-INFINITY, 0.f);
         y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -736,13 +825,13 @@ __global__ void __launch_bounds__(256, 6) join_kernel(const __grid_constant__ Tc
       }
       float top = m;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) top = fmaxf(top, x[u].x);
+      for (int u = 0; u < U; ++u) top = fmaxf(top, x[u].x);
       const float use = top == -INFINITY ? 0.f : top, f0 = ex2(m - use);
       m = top;
       l *= f0;
       o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < U; ++u) {
         const float f = ex2(x[u].x - use);
         l = fmaf(f, x[u].y, l);
         o.x = fmaf(f, y[u].x, o.x);
@@ -759,29 +848,46 @@ __global__ void __launch_bounds__(256, 6) join_kernel(const __grid_constant__ Tc
   }
 }
 
-template <int NT, bool F16, bool TREE>
+template <int NT, bool F16, bool TREE, bool CL>
 cudaError_t launch_t(const TcAttnParams& p, cudaStream_t stream) {
-  auto kern = tc_kernel<NT, F16, TREE>;
+  auto kern = tc_kernel<NT, F16, TREE, CL>;
   static std::atomic<uint64_t> configured{0};
   cudaError_t e = opt_in_smem(kern, Lay<NT>::bytes, configured);
   if (e != cudaSuccess) return e;
+  if constexpr (CL) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.ctas);
+    cfg.blockDim = dim3(kTcThreads);
+    cfg.dynamicSmemBytes = Lay<NT>::bytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+  }
   return launch_chained(kern, dim3(p.ctas), dim3(kTcThreads), Lay<NT>::bytes, stream, p);
 }
-template <int NT>
+template <int NT, bool CL>
 cudaError_t launch_nt(const TcAttnParams& p, bool f16, cudaStream_t stream) {
-  if (p.c.parents) return f16 ? launch_t<NT, true, true>(p, stream) : launch_t<NT, false, true>(p, stream);
-  return f16 ? launch_t<NT, true, false>(p, stream) : launch_t<NT, false, false>(p, stream);
+  if (p.c.parents) return f16 ? launch_t<NT, true, true, CL>(p, stream) : launch_t<NT, false, true, CL>(p, stream);
+  return f16 ? launch_t<NT, true, false, CL>(p, stream) : launch_t<NT, false, false, CL>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_attn_tc(const TcAttnParams& p, int nt, bool f16, cudaStream_t stream) {
-  return nt == 2 ? launch_nt<2>(p, f16, stream) : launch_nt<1>(p, f16, stream);
+  if (p.cluster > 0) return launch_nt<1, true>(p, f16, stream);
+  return nt == 2 ? launch_nt<2, false>(p, f16, stream) : launch_nt<1, false>(p, f16, stream);
 }
 
 cudaError_t launch_cache_attn_join(const TcAttnParams& p, int nt, cudaStream_t stream) {
   if (p.ctas < 2) return cudaSuccess;
-  return launch_chained(join_kernel, dim3(p.ctas - 1, (p.part_rows + kJoinRows - 1) / kJoinRows), dim3(256), 0, stream, p, nt);
+  return launch_chained(p.part_rows <= kJoinRows ? join_kernel<16> : join_kernel<4>, dim3(p.ctas - 1, (p.part_rows + kJoinRows - 1) / kJoinRows), dim3(256), 0, stream, p, nt);
 }
 
 }  // namespace st

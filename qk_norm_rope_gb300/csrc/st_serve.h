@@ -13,6 +13,7 @@ constexpr int kTreeWords = kMaxTree / 32;
 constexpr int kMaxVerify = 1024;     // nodes of a drafted tree that the verification takes
 constexpr int kMaxGroup = 128;       // query heads per K/V head
 constexpr int kMaxClusterVerify = 8;
+constexpr int kMaxClusterAttn = 8;
 
 // A paged K/V cache: token `pos` of sequence b lies in row pos % page of page
 // pages[b][pos / page].
@@ -110,6 +111,7 @@ struct TcAttnParams {
   int n_groups;                // groups per sequence
   int part_rows;               // rows of a partial result
   int ctas;
+  int cluster;                 // CTAs per item of the clustered form (NT = 1), 0: the dealt form
   struct JoinMeta* meta;       // [ctas], workspace
   float2* part_ml;             // [2 ctas, part_rows] (reference, sum); c.part: [2 ctas, part_rows, D]
 };

@@ -146,6 +146,26 @@ st_status plan_attn(const st_tensor* q, const st_kv_cache* cache, const st_tenso
     const int64_t cap_tiles = (static_cast<int64_t>(p.kv.max_pages) * p.kv.page + kTile - 1) / kTile;
     const int64_t items = static_cast<int64_t>(p.B) * p.kv.Hkv * t.n_groups;
     if (items > (1ll << 40) || static_cast<int64_t>(p.B) * t.n_groups > (1ll << 30)) return fail(ST_ERR_SHAPE, "too many query rows");
+    // The clustered form: as many CTAs per item as let all clusters run at once
+    // (15 clusters of 8 such CTAs, 36 of 4, 76 of 2 fit the GPU; 16 of 8 took
+    // two turns: 18.3 us against 11.0 with 4). Its shares are even per item
+    // instead of over the call: up to room * (1 / cluster - mean * items / SMs)
+    // key tiles more for a CTA, of ~0.75 us each (mean: the mean length over the
+    // room, taken as 1 for one sequence and 1/2 for a batch, whose lengths
+    // differ); it saves the scan and the join, ~2.5 us and a launch (one token,
+    // 8 K/V heads, 777 keys: 10.9 us dealt, 9.1 clustered; 4000 keys: 15.7 and
+    // 12.6; 8 sequences of up to 8000 keys: 36 and 49).
+    t.cluster = 0;
+    if (P->nt == 1) {
+      const int cl = items <= 15 ? 8 : (items <= 36 ? 4 : (items <= 76 ? 2 : 1));
+      static_assert(kMaxClusterAttn == 8, "the largest cluster");
+      const int64_t mean = p.B == 1 ? 2 : 1;  // halves
+      if (cl > 1 && cap_tiles * (2 * kSmCount - mean * items * cl) <= static_cast<int64_t>(10) * cl * kSmCount) t.cluster = cl;
+    }
+    if (t.cluster > 0) {
+      t.ctas = static_cast<int>(items) * t.cluster;
+      return ST_OK;  // no workspace
+    }
     t.ctas = static_cast<int>(items >= kSmCount ? kSmCount : std::min<int64_t>(kSmCount, items * cap_tiles));
     // a CTA leaves at most two parts: one at each end of its range
     size_t off = align256(static_cast<size_t>(2) * t.ctas * t.part_rows * kD * sizeof(float));
@@ -278,6 +298,7 @@ st_status st_cache_attn(const st_tensor* q_rot, const st_kv_cache* cache, const 
     if ((st = cuda_check(launch_counted(ST_K_CACHE_ATTN, stream, [&] { return launch_cache_attn_tc(t, P.nt, p.kv.dt == ST_F16, stream); }),
                          "cached attention launch")) != ST_OK)
       return st;
+    if (t.cluster > 0) return ST_OK;
     return cuda_check(launch_counted(ST_K_CACHE_JOIN, stream, [&] { return launch_cache_attn_join(t, P.nt, stream); }),
                       "cached attention join launch");
   }

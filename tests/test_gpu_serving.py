@@ -161,9 +161,14 @@ def attn_case(dtype, B, T, H, Hkv, lens, counts, page, is_tree, seed=0, one_tree
     return q, k, v, pages, parents
 
 
+@pytest.mark.parametrize("room", ["tight", "wide"])
 @pytest.mark.parametrize("dtype,B,T,H,Hkv,lens,counts,page,is_tree", ATTN)
-def test_attention(cuda_lib, dtype, B, T, H, Hkv, lens, counts, page, is_tree):
+def test_attention(cuda_lib, dtype, B, T, H, Hkv, lens, counts, page, is_tree, room):
+    """With page tables that fit the lengths and with ones that leave room for far more (the calls are planned by the
+    room, the lengths being on the device)."""
     q, k, v, pages, parents = attn_case(dtype, B, T, H, Hkv, lens, counts, page, is_tree)
+    if room == "wide":
+        pages = torch.cat((pages, torch.full((B, 200000 // page), -7, dtype=torch.int32)), 1)
     cache = dev_cache(cuda_lib, k, v, pages)
     cnt = None if counts is None else i32(counts)
     cu = lambda t: None if t is None else t.cuda()
@@ -178,6 +183,8 @@ def test_attention(cuda_lib, dtype, B, T, H, Hkv, lens, counts, page, is_tree):
 @pytest.mark.parametrize("dtype,B,T,H,Hkv,most,page,is_tree", [
     ("bf16", 40, 2, 16, 8, 900, 16, False),   # few rows a head: many short items, odd numbers of key tiles
     ("fp16", 60, 1, 5, 5, 1500, 32, False),
+    ("bf16", 7, 1, 20, 5, 600, 16, False),    # clusters of four and of two
+    ("fp16", 12, 3, 30, 6, 400, 64, True),
     ("bf16", 9, 70, 16, 8, 1400, 64, True),   # more than a tile of rows a head
     ("fp16", 3, 300, 6, 3, 1000, 8, False),
 ])
