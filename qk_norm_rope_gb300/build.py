@@ -104,7 +104,7 @@ def build_bind(obj: str | None = None) -> str:
         return BIND
     t = os.path.join(os.path.dirname(os.path.abspath(torch.__file__)), "lib")
     tmp = BIND + f".{os.getpid()}.tmp"
-    cmd = ["g++", "-shared", obj, "-o", tmp, f"-L{t}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+    cmd = ["g++", "-shared", obj, "-o", tmp, f"-L{t}", "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10", "-lc10_cuda",
            f"-L{os.path.dirname(build_lib)}", "-l:libst_rope_attn.so", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{t}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

@@ -435,6 +435,16 @@ void fill_common(const Plan& P, const st_tensor* qw, const st_tensor* kw, float 
 
 namespace st {
 
+void fill_ids(const Ids& ids, TableParams* t) {
+  t->Bt = ids.Bt;
+  t->S = ids.S;
+  t->ids = ids.t->data;
+  t->ids_f32 = ids.t->dtype == ST_F32;
+  t->i_sb = ids.t->stride[0];
+  t->i_ss = ids.t->stride[1];
+  t->i_sa = ids.t->stride[2];
+}
+
 void fill_table(const Ids& ids, const st_rope* rope, float2* out, __half2* out16, unsigned* ctrl, TableParams* t) {
   memset(t, 0, sizeof(*t));
   t->Bt = ids.Bt;
@@ -456,11 +466,7 @@ void fill_table(const Ids& ids, const st_rope* rope, float2* out, __half2* out16
     t->s_sd = sn->stride[o + 1];
     return;
   }
-  t->ids = ids.t->data;
-  t->ids_f32 = ids.t->dtype == ST_F32;
-  t->i_sb = ids.t->stride[0];
-  t->i_ss = ids.t->stride[1];
-  t->i_sa = ids.t->stride[2];
+  fill_ids(ids, t);
   int pair = 0;
   for (int a = 0; a < rope->n_axes; ++a) {
     const int da = rope->axes_dim[a];

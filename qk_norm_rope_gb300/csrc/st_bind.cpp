@@ -5,7 +5,7 @@
 // defaults); errors raise the StError class given to init().
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -71,6 +71,13 @@ struct Call {
   }
 };
 
+// torch.empty on a CUDA device (its allocator, the device's current stream)
+// without the way through the dispatcher.
+at::Tensor new_tensor(at::IntArrayRef shape, at::ScalarType ty, int dev) {
+  if (dev < 0) throw Refused(ST_ERR_INVALID_ARG, "no tensor was given");
+  return at::Tensor(at::detail::empty_cuda(shape, ty, at::Device(at::kCUDA, static_cast<at::DeviceIndex>(dev)), std::nullopt));
+}
+
 // An output: the caller's tensor, or a new one.
 struct Out {
   at::Tensor t;
@@ -81,7 +88,7 @@ struct Out {
       given = o;
       Call::fill(*c.tensor(o, name), &s, name);
     } else {
-      t = at::empty(shape, at::TensorOptions().dtype(ty).device(at::kCUDA, c.dev));
+      t = new_tensor(shape, ty, c.dev);
       Call::fill(t, &s, name);
     }
   }
@@ -219,7 +226,7 @@ PyObject* cache_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (a[10] == Py_None) {
       wn = st_cache_attn_workspace_size(q, &kv.c, par);
       if (wn == 0) throw Refused(ST_ERR_INVALID_ARG, st_last_error());
-      ws = at::empty({static_cast<int64_t>(wn)}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, c.dev));
+      ws = new_tensor({static_cast<int64_t>(wn)}, at::kByte, c.dev);
       wp = ws.data_ptr();
     } else {
       const at::Tensor* w = c.tensor(a[10], "workspace");

@@ -64,6 +64,7 @@ st_status check_ids(const st_tensor* t, const char* name, int B, int S, int n_ax
 st_status check_tables(const st_tensor* c, const st_tensor* sn, const char* name, int B, int S, Ids* out);
 // Axis widths and theta of the position-id form (widths must sum to D).
 st_status check_axes(const st_rope* rope, int D);
+void fill_ids(const Ids& ids, TableParams* t);  // the position-id form's tensor
 void fill_table(const Ids& ids, const st_rope* rope, float2* out, __half2* out16, unsigned* ctrl, TableParams* t);
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();

@@ -226,10 +226,34 @@ st_status st_cache_append(const st_tensor* q, const st_tensor* k, const st_tenso
   if (tokens * p.H == 0) return ST_OK;
   Dev dev;
   if ((st = device_globals(&dev)) != ST_OK) return st;
-  fill_table(ids, rope, nullptr, nullptr, nullptr, &p.tab);
-  for (int j = 0; j < kPairs; ++j) {
-    const double turn = p.tab.omega[j] * 0.15915494309189535;  // 1 / (2 pi)
-    p.turns[j] = static_cast<unsigned long long>((turn - std::floor(turn)) * 18446744073709551616.0);
+  if (ids.table) {
+    fill_table(ids, rope, nullptr, nullptr, nullptr, &p.tab);
+  } else {
+    // the pairs' frequencies depend on the widths and theta alone, which a
+    // model never changes: a thread keeps its last ones (64 powers a call
+    // otherwise)
+    struct Freq {
+      int n = 0, axes[8];
+      double theta;
+      TableParams tab;
+      unsigned long long turns[kPairs];
+    };
+    static thread_local Freq f;
+    if (f.n != rope->n_axes || f.theta != rope->theta || memcmp(f.axes, rope->axes_dim, sizeof(int) * f.n) != 0) {
+      f.n = 0;
+      fill_table(ids, rope, nullptr, nullptr, nullptr, &f.tab);
+      for (int j = 0; j < kPairs; ++j) {
+        const double turn = f.tab.omega[j] * 0.15915494309189535;  // 1 / (2 pi)
+        f.turns[j] = static_cast<unsigned long long>((turn - std::floor(turn)) * 18446744073709551616.0);
+      }
+      memcpy(f.axes, rope->axes_dim, sizeof(int) * rope->n_axes);
+      f.theta = rope->theta;
+      f.n = rope->n_axes;
+    }
+    memcpy(p.tab.omega, f.tab.omega, sizeof(p.tab.omega));
+    memcpy(p.tab.axis_of, f.tab.axis_of, sizeof(p.tab.axis_of));
+    memcpy(p.turns, f.turns, sizeof(p.turns));
+    fill_ids(ids, &p.tab);
   }
   p.wq = static_cast<const float*>(q_norm_w->data);
   p.wk = static_cast<const float*>(k_norm_w->data);
