@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
         const int e = u * kThreads + tid, r = e / (kD / 4), c = e % (kD / 4);
         const int64_t o = off[r];
         const float* src = static_cast<const float*>(base) + (o < 0 ? 0 : o) + 4 * c;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst + r * pad + 4 * c)), "l"(o < 0 ? base : src), "r"(o < 0 ? 0 : 16) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst + r * pad + 4 * c)), "l"(o < 0 ? p.q.p : static_cast<const void*>(src)), "r"(o < 0 ? 0 : 16) : "memory");
       }
     } else {
       uint4 x[kN * kD / 8 / kThreads];

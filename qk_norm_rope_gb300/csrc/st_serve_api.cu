@@ -54,6 +54,11 @@ st_status check_cache(const st_kv_cache* c, int64_t B, PagedKV* out, const char*
   st_status st;
   if ((st = check_bshd(k, "cache.k", n, page, H, kD, kCacheTypes, &rk)) != ST_OK) return st;
   if ((st = check_bshd(c->v, "cache.v", n, page, H, kD, bit(k->dtype), &rv)) != ST_OK) return st;
+  // the rows of a cache are written: none may stand for several positions
+  for (const st_tensor* t : {k, c->v})
+    for (int a = 0; a < 3; ++a)
+      if (t->shape[a] > 1 && t->stride[a] <= 0)
+        return fail(ST_ERR_ALIGN, "%s must not be expanded (stride[%d]=%lld)", t == k ? "cache.k" : "cache.v", a, (long long)t->stride[a]);
   if (pt->ndim != 2 || (B >= 0 && pt->shape[0] != B)) return fail(ST_ERR_SHAPE, "cache.pages must be [%lld, max_pages]", (long long)B);
   if (pt->shape[0] < 0 || pt->shape[0] > 65535 || pt->shape[1] < 0) return fail(ST_ERR_SHAPE, "cache.pages sizes out of range");
   if (pt->dtype != ST_I32) return fail(ST_ERR_DTYPE, "cache.pages must be int32");

@@ -302,6 +302,72 @@ def test_attention_on_a_side_stream(cuda_lib, dtype):
     R.close("lse", lse, rl, bl)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_attention_without_room(cuda_lib, dtype):
+    """A page table without columns, and a cache without pages: nothing is seen, and the status says so."""
+    dt = DT[dtype]
+    q = rand(1, 2, 3, 4, D, dtype=dt).cuda()
+    kc = torch.zeros(2, 16, 2, D, dtype=dt, device="cuda")
+    for cache in (cuda_lib.KVCache(kc, kc.clone(), torch.zeros(2, 0, dtype=torch.int32, device="cuda")),):
+        o, lse = cuda_lib.st_cache_attn(q, cache, i32([0, 5]).cuda())
+        with pytest.raises(cuda_lib.StError):
+            cuda_lib.st_check_status()
+        assert not o.any() and torch.isinf(lse).all() and (lse < 0).all()
+    none = cuda_lib.KVCache(kc[:0], kc[:0].clone(), i32([[0], [1]]).cuda())
+    o, lse = cuda_lib.st_cache_attn(q, none, i32([0, 5]).cuda())
+    with pytest.raises(cuda_lib.StError):
+        cuda_lib.st_check_status()
+    assert not o.any()  # pages that do not exist read as zeros
+    cuda_lib.st_check_status()
+
+
+def test_two_streams_at_once(cuda_lib):
+    """Calls that overlap on the GPU, each with outputs and a workspace of its own, over one cache that both read."""
+    lens = [2900, 1000, 17, 640]
+    q, k, v, pages, parents = attn_case("bf16", 4, 20, 16, 8, lens, None, 16, True, seed=120)
+    cache = dev_cache(cuda_lib, k, v, pages)
+    qd, ln, pd = q.cuda(), i32(lens).cuda(), parents.cuda()
+    want, want_lse = cuda_lib.st_cache_attn(qd, cache, ln, parents=pd)
+    wide = cuda_lib.KVCache(cache.k, cache.v, torch.cat((cache.pages, torch.zeros(4, 20000, dtype=torch.int32, device="cuda")), 1))
+    want2, _ = cuda_lib.st_cache_attn(qd, wide, ln, parents=pd)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = []
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append((i, cuda_lib.st_cache_attn(qd, wide if i == 1 else cache, ln, parents=pd)))
+    torch.cuda.synchronize()
+    cuda_lib.st_check_status()
+    for i, (o, lse) in got:
+        assert torch.equal(bits(o), bits(want2 if i == 1 else want))
+    ro, _, bo, _ = R.attention(q, k, v, pages, lens, None, parents)
+    R.close("o", want, ro, bo)
+    R.close("o", want2, ro, bo)
+
+
+def test_attention_rows_do_not_depend_on_the_batch(cuda_lib):
+    """A sequence alone and the same one in a batch of other lengths agree within their bounds, padded rows are zero and
+    untouched neighbours of strided outputs stay."""
+    lens = [350, 3, 900]
+    q, k, v, pages, parents = attn_case("fp16", 3, 5, 8, 2, lens, [5, 2, 4], 32, True, seed=130)
+    cache = dev_cache(cuda_lib, k, v, pages)
+    room = torch.full((3, 7, 10, D), 7.0, dtype=torch.float16, device="cuda")
+    o, lse = cuda_lib.st_cache_attn(q.cuda(), cache, i32(lens).cuda(), counts=i32([5, 2, 4]).cuda(), parents=parents.cuda(),
+                                    o=room[:, 1:6, 1:9])
+    cuda_lib.st_check_status()
+    ro, rl, bo, bl = R.attention(q, k, v, pages, lens, [5, 2, 4], parents)
+    R.close("o", o, ro, bo)
+    R.close("lse", lse, rl, bl)
+    room[:, 1:6, 1:9] = 7.0
+    assert (room == 7.0).all()
+    for b in range(3):
+        one = cuda_lib.KVCache(cache.k, cache.v, cache.pages[b:b + 1])
+        ob, _ = cuda_lib.st_cache_attn(q[b:b + 1].cuda(), one, i32(lens[b:b + 1]).cuda(), counts=i32([[5, 2, 4][b]]).cuda(),
+                                       parents=parents[b:b + 1].cuda())
+        R.close("o", ob[0], ro[b], bo[b])
+
+
 # ------------------------------------------------------------ verification
 def probs(seed, *shape, sharp=2.0, dtype=torch.float32):
     return torch.softmax(rand(seed, *shape) * sharp, -1).to(dtype)
@@ -456,6 +522,14 @@ def test_keep(cuda_lib, dtype, B, Hkv, page, start, N, n_rows, T):
         wk[dpg, drow], wv[dpg, drow] = k[spg, srow], v[spg, srow]
     assert torch.equal(bits(cache.k), bits(wk)) and torch.equal(bits(cache.v), bits(wv))
     assert lens.tolist() == [s + n for s, n in zip(start, n_rows)]
+
+
+def test_keep_nothing(cuda_lib):
+    k, v, pages = R.make_cache(2, [32] * 2, 1, 16, torch.float16, 8, fill=3.0)
+    cache = dev_cache(cuda_lib, k, v, pages)
+    lens = cuda_lib.st_cache_keep(cache, i32([4, 9]).cuda(), torch.zeros(2, 0, dtype=torch.int32, device="cuda"), i32([0, 0]).cuda())
+    cuda_lib.st_check_status()
+    assert lens.tolist() == [4, 9] and torch.equal(bits(cache.k), bits(k)) and torch.equal(bits(cache.v), bits(v))
 
 
 def test_keep_bad_rows(cuda_lib):

@@ -118,6 +118,8 @@ def test_cache_refusals(call):
     check(call, E.ST_ERR_ALIGN, "unit stride", ck=T([9, 16, 2, 128], strides=[4096, 256, 1, 2]))
     check(call, E.ST_ERR_ALIGN, "aligned", cv=T([9, 16, 2, 128], data=FAKE + 8))
     check(call, E.ST_ERR_ALIGN, "multiple of 16", cv=T([9, 16, 2, 128], strides=[4100, 256, 128, 1]))
+    check(call, E.ST_ERR_ALIGN, "expanded", ck=T([9, 16, 2, 128], strides=[4096, 256, 0, 1]))
+    check(call, E.ST_ERR_ALIGN, "expanded", cv=T([9, 16, 2, 128], strides=[0, 256, 128, 1]))
     check(call, E.ST_ERR_DTYPE, "pages", pages=T([2, 4], E.ST_I64))
     check(call, E.ST_ERR_ALIGN, "pages", pages=T([2, 4], E.ST_I32, strides=[8, 2]))
     check(call, E.ST_ERR_SHAPE, "pages", pages=T([2, 4, 1], E.ST_I32))
