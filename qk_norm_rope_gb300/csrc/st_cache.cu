@@ -184,28 +184,34 @@ __global__ void __launch_bounds__(kAppWarps * 32) append_kernel(const __grid_con
 // number -> address is two dependent loads; done row by row in the copy loop it
 // held the whole kernel to 1.3 TB/s), and chunks are staged through a ring by
 // asynchronous copies, kKeepStages - 1 chunks ahead of the one being written.
-constexpr int kKeepThreads = 256;
-constexpr int kKeepPer = 4;     // 16-byte copies per thread and chunk
+// A chunk costs a CTA about a microsecond whatever its size, so that few long
+// columns want wide CTAs: moving 28672 rows of 4 sequences of 8 heads takes
+// 162 us (5.1 TB/s, reads and writes) with 128 columns of 128 bytes and 1024
+// threads, 177 with 256 of 64 bytes and 256 threads, 211 with 128 and 256;
+// a path of 8 rows takes 5.2 us with 256 threads and 18 with 1024.
 constexpr int kKeepStages = 4;
 constexpr int kKeepTable = 1024;
 // Shared memory by the call's N (several CTAs per SM where a list is short):
 // the ring's chunks, then src and dst byte offsets of one table or two; src < 0:
 // the row does not move.
+template <int THREADS, int PER>  // PER: 16-byte copies per thread and chunk
 struct KeepLay {
+  static constexpr int kChunkBytes = THREADS * PER * 16;
   int stages, table, tables;
   __host__ __device__ KeepLay(int N, int part_lanes) {
-    const int chunk = kKeepThreads / part_lanes * kKeepPer, chunks = (N + chunk - 1) / chunk;
+    const int chunk = THREADS / part_lanes * PER, chunks = (N + chunk - 1) / chunk;
     stages = chunks < 1 ? 1 : (chunks < kKeepStages ? chunks : kKeepStages);
     table = chunks * chunk < kKeepTable ? (chunks < 1 ? chunk : chunks * chunk) : kKeepTable;
     tables = N > kKeepTable ? 2 : 1;
   }
-  __host__ __device__ size_t ring() const { return static_cast<size_t>(stages) * kKeepPer * kKeepThreads * 16; }
+  __host__ __device__ size_t ring() const { return static_cast<size_t>(stages) * kChunkBytes; }
   __host__ __device__ size_t bytes() const { return ring() + static_cast<size_t>(2) * tables * table * 8; }
 };
 
-__global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constant__ KeepParams p) {
+template <int THREADS, int PER>
+__global__ void __launch_bounds__(THREADS) keep_kernel(const __grid_constant__ KeepParams p) {
   extern __shared__ __align__(16) uint8_t raw[];
-  const KeepLay lay(p.N, p.part_lanes);
+  const KeepLay<THREADS, PER> lay(p.N, p.part_lanes);
   uint4* ring = reinterpret_cast<uint4*>(raw);
   int64_t* t_src = reinterpret_cast<int64_t*>(raw + lay.ring());
   int64_t* t_dst = t_src + lay.tables * lay.table;
@@ -227,23 +233,23 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constan
   uint8_t* base = static_cast<uint8_t*>(is_v ? p.kv.v : p.kv.k) + h * (is_v ? p.kv.v_sh : p.kv.k_sh) * eb;
   const int64_t sp = (is_v ? p.kv.v_sp : p.kv.k_sp) * eb, sr = (is_v ? p.kv.v_sr : p.kv.k_sr) * eb;
   const int lanes = p.part_lanes, lane = tid % lanes, row0 = tid / lanes;
-  const int rows_pass = kKeepThreads / lanes, chunk = rows_pass * kKeepPer;  // chunk divides kKeepTable
+  const int rows_pass = THREADS / lanes, chunk = rows_pass * PER;  // chunk divides kKeepTable
   const int64_t col = (static_cast<int64_t>(blockIdx.x) * lanes + lane) * 16;
   const int n_chunks = (n + chunk - 1) / chunk, per_table = lay.table / chunk;
   const int32_t* rows = p.rows + b * p.r_sb;
 
   auto build = [&](int tb) {  // the table of rows [tb kKeepTable, (tb + 1) kKeepTable)
-    constexpr int kPer = kKeepTable / kKeepThreads;
+    constexpr int kPer = (kKeepTable + THREADS - 1) / THREADS;
     int r[kPer], before[kPer];
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
-      const int i = tb * lay.table + u * kKeepThreads + tid;
+      const int i = tb * lay.table + u * THREADS + tid;
       r[u] = i < n ? __ldg(rows + i) : -1;
       before[u] = i < n && i > 0 ? __ldg(rows + i - 1) : -1;
     }
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
-      const int e = u * kKeepThreads + tid, i = tb * lay.table + e;
+      const int e = u * THREADS + tid, i = tb * lay.table + e;
       if (e >= lay.table) break;
       int64_t so = -1, dof = 0;
       if (i < n) {
@@ -265,10 +271,10 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constan
     if (c < n_chunks) {
       const int64_t* src = t_src + ((c / per_table) & 1) * lay.table + (c % per_table) * chunk + row0;
 #pragma unroll
-      for (int u = 0; u < kKeepPer; ++u) {
+      for (int u = 0; u < PER; ++u) {
         const int64_t so = src[u * rows_pass];
         if (so >= 0)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(ring + ((c % lay.stages) * kKeepPer + u) * kKeepThreads + tid)), "l"(base + so + col) : "memory");
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(ring + ((c % lay.stages) * PER + u) * THREADS + tid)), "l"(base + so + col) : "memory");
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -285,8 +291,8 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constan
     const int64_t* src = t_src + (tb & 1) * lay.table + within * chunk + row0;
     const int64_t* dst = t_dst + (tb & 1) * lay.table + within * chunk + row0;
 #pragma unroll
-    for (int u = 0; u < kKeepPer; ++u)
-      if (src[u * rows_pass] >= 0) *reinterpret_cast<uint4*>(base + dst[u * rows_pass] + col) = ring[((c % lay.stages) * kKeepPer + u) * kKeepThreads + tid];
+    for (int u = 0; u < PER; ++u)
+      if (src[u * rows_pass] >= 0) *reinterpret_cast<uint4*>(base + dst[u * rows_pass] + col) = ring[((c % lay.stages) * PER + u) * THREADS + tid];
     // the next table goes where the last one was, which no thread reads any more
     // (chunks ahead stay within it: a table holds at least kKeepStages chunks)
     if (within == 0 && (tb + 1) * per_table < n_chunks) build(tb + 1);
@@ -322,14 +328,21 @@ cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t stream) {
   }
 }
 
-cudaError_t launch_cache_keep(const KeepParams& p, cudaStream_t stream) {
+template <int THREADS, int PER>
+cudaError_t launch_keep_t(const KeepParams& p, cudaStream_t stream) {
   static std::atomic<uint64_t> configured{0};
-  const KeepLay lay(p.N, p.part_lanes);
-  constexpr size_t most = static_cast<size_t>(kKeepStages) * kKeepPer * kKeepThreads * 16 + 4 * kKeepTable * 8;
-  cudaError_t e = opt_in_smem(keep_kernel, static_cast<int>(most), configured);
+  using Lay = KeepLay<THREADS, PER>;
+  // the least part_lanes: 4, or 8 in wide CTAs
+  static_assert(kKeepTable >= kKeepStages * (THREADS / (THREADS > 256 ? 8 : 4) * PER), "a table holds the chunks ahead");
+  cudaError_t e = opt_in_smem(keep_kernel<THREADS, PER>, kKeepStages * Lay::kChunkBytes + 4 * kKeepTable * 8, configured);
   if (e != cudaSuccess) return e;
   const int row_lanes = kD * (p.kv.dt == kDtF32 ? 4 : 2) / 16;
-  return launch_chained(keep_kernel, dim3(row_lanes / p.part_lanes, 2 * p.kv.Hkv, p.B), dim3(kKeepThreads), lay.bytes(), stream, p);
+  return launch_chained(keep_kernel<THREADS, PER>, dim3(row_lanes / p.part_lanes, 2 * p.kv.Hkv, p.B), dim3(THREADS),
+                        Lay(p.N, p.part_lanes).bytes(), stream, p);
+}
+
+cudaError_t launch_cache_keep(const KeepParams& p, cudaStream_t stream) {
+  return p.wide ? launch_keep_t<1024, 2>(p, stream) : launch_keep_t<256, 4>(p, stream);
 }
 
 }  // namespace st

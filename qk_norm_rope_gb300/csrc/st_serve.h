@@ -156,6 +156,7 @@ struct KeepParams {
   int32_t* lens;                   // [B], out
   int B, N;
   int part_lanes;                  // 16-byte lanes of a row that one CTA moves (4 or 8)
+  int wide;                        // 1: CTAs of 1024 threads (part_lanes 8)
   unsigned* status;
 };
 cudaError_t launch_cache_keep(const KeepParams& p, cudaStream_t stream);

@@ -447,9 +447,11 @@ st_status st_cache_keep(const st_kv_cache* cache, const st_tensor* start, const 
   p.rows = static_cast<const int32_t*>(rows->data);
   p.n_rows = static_cast<const int32_t*>(n_rows->data);
   p.lens = static_cast<int32_t*>(lens->data);
-  // columns of 128 bytes, or narrower ones where that leaves SMs without work
+  // columns of 128 bytes; where there are fewer of them than SMs, long lists
+  // take wide CTAs and short ones narrower columns
   const int64_t chains = static_cast<int64_t>(p.B) * 2 * p.kv.Hkv * (kD * elem_bytes(p.kv.dt) / 128);
-  p.part_lanes = chains >= kSmCount ? 8 : 4;
+  p.wide = chains < kSmCount && p.N > 2048;
+  p.part_lanes = p.wide || chains >= kSmCount ? 8 : 4;
   p.status = dev.status;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   return cuda_check(launch_counted(ST_K_CACHE_KEEP, stream, [&] { return launch_cache_keep(p, stream); }), "cache keep launch");
