@@ -102,8 +102,22 @@ struct Walk {
       }
     }
   }
+  // a range that is one piece of the item (h, b, m, it)
+  __device__ __forceinline__ void alone(int t0, int t1) {
+    left = t1 - t0;
+    ph = h;
+    pb = b;
+    pm = m;
+    kt0 = t0;
+    kt1 = t1;
+  }
+  template <bool ONE>
   __device__ __forceinline__ bool next(const TcAttnParams& p, int nt) {
     if (left <= 0) return false;
+    if constexpr (ONE) {
+      left = 0;
+      return true;
+    }
     while (true) {
       it = item_of(p, nt, b, m);
       if (off < it.n) break;
@@ -330,6 +344,21 @@ __device__ __forceinline__ float2 ld_peer_f2(uint32_t a) {
   return v;
 }
 
+// The page and row of a TMA lane's box of key tile kt: lane = (64-column half,
+// box of keys).
+struct Box {
+  bool mine;  // the lane has a box, and keys lie in it
+  int pg, row;
+};
+__device__ __forceinline__ Box find_box(const TcAttnParams& P, const Walk& wk, int kt, int lane) {
+  const int nb = kTile >> P.box_shift, j = kt * kTile + ((lane & (nb - 1)) << P.box_shift);
+  Box b;
+  b.mine = lane < 2 * nb && j < wk.it.keys;
+  b.pg = b.row = 0;
+  if (b.mine && !kv_locate(P.c.kv, wk.pb, j, &b.pg, &b.row)) atomicOr(P.c.status, kStatusIndex);  // reads as zeros
+  return b;
+}
+
 // A part in shared memory: 128 rows of 128 floats over the K stages, the
 // 16-byte chunks of a row permuted so that neither a thread per row (writing)
 // nor a warp per row (reading) meets bank conflicts; (reference, sum) of the
@@ -383,18 +412,26 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
   }
   if (tid == kWarpK * 32) tma_prefetch_desc(&P.tmap_k);
   if (tid == kWarpV * 32) tma_prefetch_desc(&P.tmap_v);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tslot;
   grid_dependency_wait();  // what came before touches no global memory
-  Walk wk;
+  Walk wk;  // with CL every role finds its way alone from here on
   if constexpr (CL) {
-    const int rank = static_cast<int>(cluster_rank()), item = blockIdx.x / P.cluster;
-    wk.m = item % P.n_groups;
-    wk.b = item / P.n_groups % c.B;
-    wk.h = item / P.n_groups / c.B;
-    const Item it = item_of(P, NT, wk.b, wk.m);
-    wk.off = it.n * rank / P.cluster;
-    wk.left = it.n * (rank + 1) / P.cluster - wk.off;
+    // grid (cluster x K/V heads, sequences x groups)
+    const int rank = static_cast<int>(cluster_rank());
+    wk.h = blockIdx.x >> P.cluster_shift;
+    wk.b = blockIdx.y;
+    wk.m = 0;
+    if (P.n_groups > 1) {
+      wk.b = blockIdx.y / P.n_groups;
+      wk.m = blockIdx.y - wk.b * P.n_groups;
+    }
+    wk.it = item_of(P, NT, wk.b, wk.m);
+    wk.alone((wk.it.n * rank) >> P.cluster_shift, (wk.it.n * (rank + 1)) >> P.cluster_shift);
     if (tid == 0 && rank == 0 && wk.h == 0 && wk.m == 0 &&
-        (__ldg(c.lens + wk.b) < 0 || static_cast<int64_t>(__ldg(c.lens + wk.b)) + it.cnt > it.keys))
+        (__ldg(c.lens + wk.b) < 0 || static_cast<int64_t>(__ldg(c.lens + wk.b)) + wk.it.cnt > wk.it.keys))
       atomicOr(c.status, kStatusIndex);
   } else {
     // the scan's scratch lies in the Q tile, which is written later
@@ -405,10 +442,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
     wk.off = start->off;
     wk.left = start->left;
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tslot;
   const int G = c.group, tile_rows = P.tpt * G;
 
   if (warp < kSoftWarps) {
@@ -416,7 +449,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
     // padding rows, and every row of a sequence without room for keys
     if (c.counts || static_cast<int64_t>(c.kv.max_pages) * c.kv.page == 0) {
-      for (int b = blockIdx.x; b < c.B; b += gridDim.x) {
+      for (int b = CL ? blockIdx.y * gridDim.x + blockIdx.x : blockIdx.x; b < c.B; b += CL ? gridDim.x * gridDim.y : gridDim.x) {
         const Item it = item_of(P, NT, b, 0);
         const int t0 = it.keys == 0 ? 0 : it.cnt;
         for (int64_t e = tid; e < static_cast<int64_t>(c.T - t0) * c.H * 16; e += kSoftWarps * 32) {
@@ -437,7 +470,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
     int vc = 0;         // key tiles before the present piece
     int n_piece = 0;
     bool ok = true, at_start = true;
-    while (ok && wk.next(P, NT)) {
+    while (ok && wk.next<CL>(P, NT)) {
       const int steps = (wk.kt1 - wk.kt0) * NT;
       const int t = (wk.pm * NT + (NT == 2 ? slot : 0)) * P.tpt + rt;
       const bool valid = r < tile_rows && t < wk.it.cnt;
@@ -574,7 +607,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     const int qt = tid - kWarpQ0 * 32;
     int n_piece = 0;
-    while (wk.next(P, NT)) {
+    while (wk.next<CL>(P, NT)) {
       if (n_piece > 0 && !wait_bar_warp(&bars[L::QEmpty], (n_piece - 1) & 1, abort_flag, budget)) break;
 #pragma unroll 1
       for (int ti = 0; ti < NT; ++ti) {
@@ -605,25 +638,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
       const CUtensorMap* map = is_k ? &P.tmap_k : &P.tmap_v;
       const bool r_first = (is_k ? P.k_r_first : P.v_r_first) != 0;
       uint8_t* ring = sm + (is_k ? L::k : L::v);
-      const int nb = kTile / P.box, half = lane_id / nb, bx = lane_id - half * nb;  // lanes 0 .. 2 nb - 1
+      const int half = lane_id >> (7 - P.box_shift), x = half * 64;  // a lane per box: two halves of 128 / box
+      const uint32_t dst = half * kHalfBytes + ((lane_id & ((kTile >> P.box_shift) - 1)) << P.box_shift) * 128;
       int n = 0;
-      bool ok = true;
-      while (ok && wk.next(P, NT)) {
-        for (int kt = wk.kt0; kt < wk.kt1; ++kt, ++n) {
-          const int st = n % stages;
-          const int j = kt * kTile + bx * P.box;
-          const bool mine = half < 2 && j < wk.it.keys;
-          int pg = 0, row = 0;
-          if (mine && !kv_locate(c.kv, wk.pb, j, &pg, &row)) atomicOr(c.status, kStatusIndex);  // reads as zeros
-          const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, mine));
-          if (n >= stages && !(ok = wait_bar_warp(&empty[st], ((n / stages) - 1) & 1, abort_flag, budget))) break;
-          if (lane_id == 0) mbar_arrive_expect_tx(&full[st], boxes * P.box * 128);
-          __syncwarp();
-          if (mine) {
-            uint8_t* dst = ring + st * kTileBytes + half * kHalfBytes + bx * P.box * 128;
-            tma_load_4d(dst, map, &full[st], 64 * half, r_first ? row : wk.ph, r_first ? wk.ph : row, pg);
-          }
+      bool ok = true, have = wk.next<CL>(P, NT);
+      int kt = wk.kt0;
+      Box box{false, 0, 0};
+      if (have) box = find_box(P, wk, kt, lane_id);
+      while (ok && have) {
+        const int st = n % stages;
+        const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, box.mine));
+        if (n >= stages && !(ok = wait_bar_warp(&empty[st], ((n / stages) - 1) & 1, abort_flag, budget))) break;
+        if (lane_id == 0) mbar_arrive_expect_tx(&full[st], (boxes << P.box_shift) * 128);
+        __syncwarp();
+        if (box.mine)
+          tma_load_4d(ring + st * kTileBytes + dst, map, &full[st], x, r_first ? box.row : wk.ph, r_first ? wk.ph : box.row, box.pg);
+        // the next tile's pages are looked up while its stage is in use
+        if (++kt == wk.kt1) {
+          have = wk.next<CL>(P, NT);
+          kt = wk.kt0;
         }
+        if (have) box = find_box(P, wk, kt, lane_id);
+        ++n;
       }
       // every issued load lands before the CTA exits
       for (int m = max(0, n - stages); m < n; ++m) mbar_wait(&full[m % stages], (m / stages) & 1, budget);
@@ -643,7 +679,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
       // Enters the next piece: its first key tile and its number of tiles for
       // this slot (none, where NT = 1 and its only tile is the other slot's).
       auto enter = [&](Walk& w, int& kn, int& next, int& left) -> bool {
-        if (!w.next(P, NT)) return false;
+        if (!w.next<CL>(P, NT)) return false;
         const int tiles = w.kt1 - w.kt0;
         // NT = 1: the slots take alternate tiles of the whole stream
         const int skip = NT == 2 ? 0 : (slot ^ next) & 1;
@@ -742,10 +778,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
   if constexpr (CL) {
     static_assert(NT == 1 && L::KS * kTileBytes >= 128 * 512, "a part fits over the K stages");
     cluster_sync();  // every CTA's part is in place
-    const int rank = static_cast<int>(cluster_rank()), item = blockIdx.x / P.cluster;
-    const int m = item % P.n_groups, b = item / P.n_groups % c.B, h = item / P.n_groups / c.B;
-    const int rows = max(0, min(P.tpt, row_count(c.counts, b, c.T) - m * P.tpt)) * G;
-    for (int r = rank * kTcWarps + warp; r < rows; r += P.cluster * kTcWarps) {
+    const int rank = static_cast<int>(cluster_rank()), m = wk.m, b = wk.b, h = wk.h;
+    const int rows = max(0, min(P.tpt, wk.it.cnt - m * P.tpt)) * G;
+    for (int r = (warp << P.cluster_shift) + rank; r < rows; r += kTcWarps << P.cluster_shift) {
       float2 x[kMaxClusterAttn];
       float4 y[kMaxClusterAttn];
 #pragma unroll
@@ -777,7 +812,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
       if (lane_id == 0) c.lse[(static_cast<int64_t>(b) * c.H + hq) * c.T + t] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
     }
     __syncwarp();
-    cluster_sync();  // no CTA leaves while a peer reads its part
+    // no CTA leaves while a peer reads its part (nothing is published here: a
+    // releasing arrival would wait for the results' way to memory)
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
   } else {
     __syncthreads();
   }
@@ -856,7 +893,7 @@ cudaError_t launch_t(const TcAttnParams& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if constexpr (CL) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.ctas);
+    cfg.gridDim = dim3(p.cluster * p.c.kv.Hkv, p.c.B * p.n_groups);
     cfg.blockDim = dim3(kTcThreads);
     cfg.dynamicSmemBytes = Lay<NT>::bytes;
     cfg.stream = stream;

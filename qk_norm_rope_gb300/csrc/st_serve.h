@@ -26,6 +26,7 @@ struct PagedKV {
   const int32_t* pages;
   int64_t p_sb, p_sj;              // element strides of the page table
   int n_pages, page, max_pages;
+  int page_shift;                  // log2 of page, -1 where it is no power of two
   int Hkv;
 };
 
@@ -34,7 +35,7 @@ struct PagedKV {
 __device__ __forceinline__ bool kv_locate(const PagedKV& c, int b, int64_t pos, int* pg, int* row) {
   if (pos < 0 || pos >= static_cast<int64_t>(c.max_pages) * c.page) return false;
   const unsigned p = static_cast<unsigned>(pos);  // capacity <= 2^30
-  const unsigned j = p / static_cast<unsigned>(c.page);
+  const unsigned j = c.page_shift >= 0 ? p >> c.page_shift : p / static_cast<unsigned>(c.page);
   *row = static_cast<int>(p - j * static_cast<unsigned>(c.page));
   *pg = __ldg(c.pages + b * c.p_sb + j * c.p_sj);
   return static_cast<unsigned>(*pg) < static_cast<unsigned>(c.n_pages);
@@ -106,12 +107,13 @@ struct TcAttnParams {
   CacheAttnParams c;
   CUtensorMap tmap_k, tmap_v;  // cache pages, boxes of 64 columns x box rows
   int k_r_first, v_r_first;    // map dims are (d, row, head, page) instead of (d, head, row, page)
-  int box;                     // rows per box: a power of two that divides the page size, 8..128
+  int box_shift;               // log2 of the rows per box: a power of two that divides the page size, 8..128
   int tpt;                     // tokens per query tile (128 / group)
   int n_groups;                // groups per sequence
   int part_rows;               // rows of a partial result
   int ctas;
-  int cluster;                 // CTAs per item of the clustered form (NT = 1), 0: the dealt form
+  int cluster;                 // CTAs per item of the clustered form (NT = 1): 2, 4 or 8; 0: the dealt form
+  int cluster_shift;
   struct JoinMeta* meta;       // [ctas], workspace
   float2* part_ml;             // [2 ctas, part_rows] (reference, sum); c.part: [2 ctas, part_rows, D]
 };

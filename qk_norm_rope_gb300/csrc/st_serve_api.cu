@@ -77,6 +77,9 @@ st_status check_cache(const st_kv_cache* c, int64_t B, PagedKV* out, const char*
   out->p_sj = 1;
   out->n_pages = n;
   out->page = page;
+  out->page_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (page == 1 << i) out->page_shift = i;
   out->max_pages = static_cast<int>(pt->shape[1]);
   out->Hkv = H;
   return ST_OK;
@@ -142,8 +145,8 @@ st_status plan_attn(const st_tensor* q, const st_kv_cache* cache, const st_tenso
   if (P->tensor) {
     TcAttnParams& t = P->tc;
     P->nt = tc_tiles(p.T, p.group);
-    t.box = 8;
-    while (t.box < kTile && p.kv.page % (2 * t.box) == 0) t.box *= 2;
+    t.box_shift = 3;
+    while ((1 << t.box_shift) < kTile && p.kv.page % (2 << t.box_shift) == 0) ++t.box_shift;
     t.tpt = kTile / p.group;
     const int64_t tpg = static_cast<int64_t>(t.tpt) * P->nt;
     t.n_groups = static_cast<int>((p.T + tpg - 1) / tpg);
@@ -169,6 +172,7 @@ st_status plan_attn(const st_tensor* q, const st_kv_cache* cache, const st_tenso
     }
     if (t.cluster > 0) {
       t.ctas = static_cast<int>(items) * t.cluster;
+      t.cluster_shift = t.cluster == 8 ? 3 : t.cluster / 2;
       return ST_OK;  // no workspace
     }
     t.ctas = static_cast<int>(items >= kSmCount ? kSmCount : std::min<int64_t>(kSmCount, items * cap_tiles));
@@ -322,8 +326,8 @@ st_status st_cache_attn(const st_tensor* q_rot, const st_kv_cache* cache, const 
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     t.part_ml = reinterpret_cast<float2*>(ws + P.off_ml);
     t.meta = reinterpret_cast<JoinMeta*>(ws + P.off_meta);
-    if ((st = encode_rows_map(cache->k, &t.tmap_k, &t.k_r_first, t.box)) != ST_OK) return st;
-    if ((st = encode_rows_map(cache->v, &t.tmap_v, &t.v_r_first, t.box)) != ST_OK) return st;
+    if ((st = encode_rows_map(cache->k, &t.tmap_k, &t.k_r_first, 1 << t.box_shift)) != ST_OK) return st;
+    if ((st = encode_rows_map(cache->v, &t.tmap_v, &t.v_r_first, 1 << t.box_shift)) != ST_OK) return st;
     if ((st = cuda_check(launch_counted(ST_K_CACHE_ATTN, stream, [&] { return launch_cache_attn_tc(t, P.nt, p.kv.dt == ST_F16, stream); }),
                          "cached attention launch")) != ST_OK)
       return st;
