@@ -272,9 +272,11 @@ ST_API st_status st_rope_attn_fwd_noalloc(const st_tensor* q, const st_tensor* k
  *
  * Lengths, counts, page numbers, parents, rows and tokens live on the device
  * and are read there, so that no call waits for the GPU and every call can be
- * captured into a CUDA graph and replayed with other lengths. What is out of
- * range there cannot be refused by the call: it is left out as each call says,
- * and the next st_check_status returns ST_ERR_INVALID_ARG.
+ * captured into a CUDA graph and replayed with other lengths (the first call of
+ * each kind on a device loads its kernels: make it outside a capture). What is
+ * out of range there cannot be refused by the call: it is left out as each call
+ * says, and the next st_check_status returns ST_ERR_INVALID_ARG. Nothing here
+ * is differentiated.
  *
  * st_kv_cache: token `pos` of sequence b lies in row pos % page of page
  *   pages[b, pos / page]. k, v: [N_pages, page, H_kv, D] of one dtype (bf16,

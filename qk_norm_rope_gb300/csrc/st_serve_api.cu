@@ -158,17 +158,18 @@ st_status plan_attn(const st_tensor* q, const st_kv_cache* cache, const st_tenso
     // (15 clusters of 8 such CTAs, 36 of 4, 76 of 2 fit the GPU; 16 of 8 took
     // two turns: 18.3 us against 11.0 with 4). Its shares are even per item
     // instead of over the call: up to room * (1 / cluster - mean * items / SMs)
-    // key tiles more for a CTA, of ~0.75 us each (mean: the mean length over the
-    // room, taken as 1 for one sequence and 1/2 for a batch, whose lengths
-    // differ); it saves the scan and the join, ~2.5 us and a launch (one token,
-    // 8 K/V heads, 777 keys: 10.9 us dealt, 9.1 clustered; 4000 keys: 15.7 and
-    // 12.6; 8 sequences of up to 8000 keys: 36 and 49).
+    // key tiles more for a CTA (mean: the mean length over the room, taken as 1
+    // for one sequence and 1/2 for a batch, whose lengths differ); it saves the
+    // scan for the beginning and the join, as much as about 8 tiles. One token,
+    // 8 K/V heads: 777 keys 10.5 us dealt, 7.1 clustered; 8000 keys 17.9 and
+    // 14.4; 16000 keys 18.8 and 22.3; 8 sequences of up to 1000 keys 16.6 and
+    // 10.9, of up to 8000 keys 36 and 43.
     t.cluster = 0;
     if (P->nt == 1) {
       const int cl = items <= 15 ? 8 : (items <= 36 ? 4 : (items <= 76 ? 2 : 1));
       static_assert(kMaxClusterAttn == 8, "the largest cluster");
       const int64_t mean = p.B == 1 ? 2 : 1;  // halves
-      if (cl > 1 && cap_tiles * (2 * kSmCount - mean * items * cl) <= static_cast<int64_t>(10) * cl * kSmCount) t.cluster = cl;
+      if (cl > 1 && cap_tiles * (2 * kSmCount - mean * items * cl) <= static_cast<int64_t>(16) * cl * kSmCount) t.cluster = cl;
     }
     if (t.cluster > 0) {
       t.ctas = static_cast<int>(items) * t.cluster;
