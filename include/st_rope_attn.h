@@ -322,7 +322,8 @@ ST_API size_t st_cache_attn_workspace_size(const st_tensor* q_rot, const st_kv_c
  *           and its ancestors. parents[t] < t, -1 for a node that follows the
  *           prefix; anything else ends the walk up at that node.
  *  scale:   score scale; <= 0 selects 1/sqrt(D).
- *  o:       [B, T, H, D], the cache's dtype; lse: [B, H, T] fp32, contiguous.
+ *  o:       [B, T, H, D], the cache's dtype, not overlapping q_rot; lse:
+ *           [B, H, T] fp32, contiguous.
  *           Padding rows get O = 0, LSE = -inf.
  *  workspace: 256-byte aligned; its contents need no initialisation. Calls
  *           that may overlap on the GPU need workspaces of their own.

@@ -27,10 +27,10 @@ struct Raw8 {  // eight elements as they lie in memory
   uint4 a, b;  // b: fp32 only
   __device__ __forceinline__ void load(const void* p, int64_t off) {
     if constexpr (DT == kDtF32) {
-      a = ldg_nc_v4(static_cast<const float*>(p) + off);
-      b = ldg_nc_v4(static_cast<const float*>(p) + off + 4);
+      a = ld_v4(static_cast<const float*>(p) + off);
+      b = ld_v4(static_cast<const float*>(p) + off + 4);
     } else {
-      a = ldg_nc_v4(static_cast<const uint16_t*>(p) + off);
+      a = ld_v4(static_cast<const uint16_t*>(p) + off);
     }
   }
   __device__ __forceinline__ void store(void* p, int64_t off) const {
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kAppWarps * 32) append_kernel(const __grid_con
   bool room = true;
   auto find_slot = [&]() {
     int pg = 0, row = 0;
-    room = kv_locate(p.kv, b, static_cast<int64_t>(__ldg(p.lens + b)) + t, &pg, &row);
+    room = kv_locate(p.kv, b, static_cast<int64_t>(ld_now(p.lens + b)) + t, &pg, &row);
     if (!room && lane == 0) atomicOr(p.status, kStatusIndex);
     out = kind == 1 ? p.kv.k : p.kv.v;
     o_sh = kind == 1 ? p.kv.k_sh : p.kv.v_sh;
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kAppWarps * 32) append_kernel(const __grid_con
     x[i].load(src, off + h * sh);
   }
   const float4* wp = reinterpret_cast<const float4*>(kind == 0 ? p.wq : p.wk) + 2 * l;
-  const float4 wa = __ldg(wp), wb = __ldg(wp + 1);
+  const float4 wa = ld_now(wp), wb = ld_now(wp + 1);
   if (kind == 1) find_slot();
   const float2 c0 = append_pair(p, b, t, 2 * lane), c1 = append_pair(p, b, t, 2 * lane + 1);
   tab[warp][lane] = make_float4(c0.x, c0.y, c1.x, c1.y);
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(THREADS) keep_kernel(const __grid_constant__ K
   grid_dependency_wait();
   const int b = blockIdx.z, tid = threadIdx.x;
   const int64_t cap = static_cast<int64_t>(p.kv.max_pages) * p.kv.page;
-  const int start = __ldg(p.start + b), n_said = __ldg(p.n_rows + b);
+  const int start = ld_now(p.start + b), n_said = ld_now(p.n_rows + b);
   const int n = static_cast<int>(min(static_cast<int64_t>(min(max(n_said, 0), p.N)), max(cap - max(start, 0), int64_t(0))));
   const bool first = blockIdx.x == 0 && blockIdx.y == 0;
   if (first && tid == 0) {
@@ -244,8 +244,8 @@ __global__ void __launch_bounds__(THREADS) keep_kernel(const __grid_constant__ K
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
       const int i = tb * lay.table + u * THREADS + tid;
-      r[u] = i < n ? __ldg(rows + i) : -1;
-      before[u] = i < n && i > 0 ? __ldg(rows + i - 1) : -1;
+      r[u] = i < n ? ld_now(rows + i) : -1;
+      before[u] = i < n && i > 0 ? ld_now(rows + i - 1) : -1;
     }
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {

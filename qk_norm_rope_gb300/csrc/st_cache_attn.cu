@@ -122,6 +122,10 @@ struct Walk {
       it = item_of(p, nt, b, m);
       if (off < it.n) break;
       advance(p);
+      if (h >= p.c.kv.Hkv) {  // lengths that changed under the kernel: no tiles are left
+        left = 0;
+        return false;
+      }
     }
     ph = h;
     pb = b;
@@ -175,7 +179,7 @@ __device__ __forceinline__ void find_start(const TcAttnParams& p, int nt, long l
   for (int e = lo, b = b0, m = m0; e < hi; ++e) {
     const Item it = item_of(p, nt, b, m);
     sum += it.n;
-    if (m == 0 && blockIdx.x == 0 && (__ldg(p.c.lens + b) < 0 || static_cast<int64_t>(__ldg(p.c.lens + b)) + it.cnt > it.keys))
+    if (m == 0 && blockIdx.x == 0 && (ld_now(p.c.lens + b) < 0 || static_cast<int64_t>(ld_now(p.c.lens + b)) + it.cnt > it.keys))
       atomicOr(p.c.status, kStatusIndex);
     if (++m == p.n_groups) {
       m = 0;
@@ -431,7 +435,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
     wk.it = item_of(P, NT, wk.b, wk.m);
     wk.alone((wk.it.n * rank) >> P.cluster_shift, (wk.it.n * (rank + 1)) >> P.cluster_shift);
     if (tid == 0 && rank == 0 && wk.h == 0 && wk.m == 0 &&
-        (__ldg(c.lens + wk.b) < 0 || static_cast<int64_t>(__ldg(c.lens + wk.b)) + wk.it.cnt > wk.it.keys))
+        (ld_now(c.lens + wk.b) < 0 || static_cast<int64_t>(ld_now(c.lens + wk.b)) + wk.it.cnt > wk.it.keys))
       atomicOr(c.status, kStatusIndex);
   } else {
     // the scan's scratch lies in the Q tile, which is written later
@@ -482,7 +486,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
 #pragma unroll
           for (int i = 0; i < kTreeWords; ++i)
             if (i == (node >> 5)) anc[i] |= 1u << (node & 31);
-          const int up = __ldg(c.parents + wk.pb * c.par_sb + node);
+          const int up = ld_now(c.parents + wk.pb * c.par_sb + node);
           if (up >= node || up < -1) {
             atomicOr(c.status, kStatusIndex);
             break;

@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
   const int cnt = row_count(p.counts, b, p.T);
   int prefix;
   const int keys = key_count(p, b, cnt, &prefix);
-  if (tid == 0 && split == 0 && (__ldg(p.lens + b) < 0 || static_cast<int64_t>(__ldg(p.lens + b)) + cnt > keys)) atomicOr(p.status, kStatusIndex);
+  if (tid == 0 && split == 0 && (ld_now(p.lens + b) < 0 || static_cast<int64_t>(ld_now(p.lens + b)) + cnt > keys)) atomicOr(p.status, kStatusIndex);
 
   // the last key that any row of the item sees
   const int t_last = t0 + (g0 + n_here - 1) / G;
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
     if (node >= cnt) node = -1;
     while (node >= 0) {
       s.anc[tid][node >> 5] |= 1u << (node & 31);
-      const int up = __ldg(p.parents + b * p.par_sb + node);
+      const int up = ld_now(p.parents + b * p.par_sb + node);
       if (up >= node || up < -1) {
         atomicOr(p.status, kStatusIndex);
         break;
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
       for (int u = 0; u < kN * kD / 8 / kThreads; ++u) {
         const int e = u * kThreads + tid, r = e / (kD / 8), c = e % (kD / 8);
         const int64_t o = off[r];
-        x[u] = o < 0 ? make_uint4(0, 0, 0, 0) : ldg_nc_v4(static_cast<const uint16_t*>(base) + o + 8 * c);
+        x[u] = o < 0 ? make_uint4(0, 0, 0, 0) : ld_v4(static_cast<const uint16_t*>(base) + o + 8 * c);
       }
 #pragma unroll
       for (int u = 0; u < kN * kD / 8 / kThreads; ++u) {

@@ -15,6 +15,19 @@ constexpr int kMaxGroup = 128;       // query heads per K/V head
 constexpr int kMaxClusterVerify = 8;
 constexpr int kMaxClusterAttn = 8;
 
+// Ordinary loads, not the read-only path: with programmatic launches a kernel
+// may be resident while the one before it still writes what is read here (after
+// the dependency wait).
+template <class T>
+__device__ __forceinline__ T ld_now(const T* p) {
+  return *p;
+}
+__device__ __forceinline__ uint4 ld_v4(const void* p) {  // volatile: stays where it stands among other volatile asm
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
+
 // A paged K/V cache: token `pos` of sequence b lies in row pos % page of page
 // pages[b][pos / page].
 struct PagedKV {
@@ -37,13 +50,13 @@ __device__ __forceinline__ bool kv_locate(const PagedKV& c, int b, int64_t pos, 
   const unsigned p = static_cast<unsigned>(pos);  // capacity <= 2^30
   const unsigned j = c.page_shift >= 0 ? p >> c.page_shift : p / static_cast<unsigned>(c.page);
   *row = static_cast<int>(p - j * static_cast<unsigned>(c.page));
-  *pg = __ldg(c.pages + b * c.p_sb + j * c.p_sj);
+  *pg = ld_now(c.pages + b * c.p_sb + j * c.p_sj);
   return static_cast<unsigned>(*pg) < static_cast<unsigned>(c.n_pages);
 }
 
 // The number of sequence b's T rows that are there.
 __device__ __forceinline__ int row_count(const int32_t* counts, int b, int T) {
-  return counts ? min(max(__ldg(counts + b), 0), T) : T;
+  return counts ? min(max(ld_now(counts + b), 0), T) : T;
 }
 
 struct AppendParams {
@@ -86,7 +99,7 @@ struct CacheAttnParams {
 // page table has room for.
 __device__ __forceinline__ int key_count(const CacheAttnParams& p, int b, int count, int* prefix) {
   const int64_t cap = static_cast<int64_t>(p.kv.max_pages) * p.kv.page;
-  const int64_t len = max(__ldg(p.lens + b), 0);
+  const int64_t len = max(ld_now(p.lens + b), 0);
   *prefix = static_cast<int>(min(len, cap));
   return static_cast<int>(min(len + count, cap));
 }

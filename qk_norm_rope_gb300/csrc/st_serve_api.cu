@@ -297,6 +297,8 @@ st_status st_cache_attn(const st_tensor* q_rot, const st_kv_cache* cache, const 
   if (!std::isfinite(scale)) return fail(ST_ERR_INVALID_ARG, "scale must be finite");
   RowTensor ro;
   if ((st = check_bshd(o, "o", p.B, p.T, p.H, kD, bit(p.kv.dt), &ro)) != ST_OK) return st;
+  if (static_cast<int64_t>(p.B) * p.T * p.H > 0 && o->data == q_rot->data)
+    return fail(ST_ERR_INVALID_ARG, "o must not be q_rot: its rows are read until the call ends");
   if (!lse || lse->ndim != 3 || lse->shape[0] != p.B || lse->shape[1] != p.H || lse->shape[2] != p.T)
     return fail(ST_ERR_SHAPE, "lse must be [B,H,T] = [%d,%d,%d]", p.B, p.H, p.T);
   if (lse->dtype != ST_F32) return fail(ST_ERR_DTYPE, "lse must be fp32");

@@ -44,9 +44,9 @@ constexpr double kUnit = 1.0 / 8796093022208.0;  // 2^-43, the unit of a weight
 template <int DT>
 __device__ __forceinline__ float prob(const void* p, int64_t e) {
   float v;
-  if constexpr (DT == kDtF32) v = __ldg(static_cast<const float*>(p) + e);
-  else if constexpr (DT == kDtBF16) v = __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(p) + e));
-  else v = __half2float(__ldg(static_cast<const __half*>(p) + e));
+  if constexpr (DT == kDtF32) v = ld_now(static_cast<const float*>(p) + e);
+  else if constexpr (DT == kDtBF16) v = __bfloat162float(ld_now(static_cast<const __nv_bfloat16*>(p) + e));
+  else v = __half2float(ld_now(static_cast<const __half*>(p) + e));
   return __saturatef(v);  // [0, 1]; NaN: 0
 }
 // A value in [-1, 1] as two integer limbs of 21 and 22 bits, value =
@@ -141,8 +141,8 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
 
   for (int i = tid; i < cnt; i += kVerThreads) {
     const int64_t te = b * P.tok_sb + i * P.tok_st;
-    const int64_t t64 = P.tok64 ? __ldg(static_cast<const long long*>(P.tokens) + te) : __ldg(static_cast<const int32_t*>(P.tokens) + te);
-    const int par = __ldg(P.parents + b * P.par_sb + i);
+    const int64_t t64 = P.tok64 ? ld_now(static_cast<const long long*>(P.tokens) + te) : ld_now(static_cast<const int32_t*>(P.tokens) + te);
+    const int par = ld_now(P.parents + b * P.par_sb + i);
     const bool ok = i > 0 && par >= 0 && par < i && t64 >= 0 && t64 < V;
     // the root has no parent; -1 stands for a node that nothing leads to
     if (!ok && (i > 0 ? (par >= i || par < -1 || t64 < 0 || t64 >= V) : par >= 0) && rank == 0) atomicOr(P.status, kStatusIndex);
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
     s.tok[i] = x;
     s.pp[i] = ok ? prob<DT>(P.p, b * P.p_sb + par * P.p_st + x) : 0.f;
     s.qq[i] = ok && drafted ? prob<DT>(P.q, b * P.q_sb + par * P.q_st + x) : 1.f;
-    s.uu[i] = ok ? __ldg(P.u_accept + static_cast<int64_t>(b) * P.T + i) : 0.f;
+    s.uu[i] = ok ? ld_now(P.u_accept + static_cast<int64_t>(b) * P.T + i) : 0.f;
     s.first_yes[i] = static_cast<double>(s.uu[i]) * s.qq[i] < static_cast<double>(s.pp[i]);
   }
   if (tid == 0) {
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
       total = sum_row(cur, 0.0, false, true);
     }
     if (total > 0) {
-      const float us = fminf(fmaxf(__ldg(P.u_sample + b), 0.f), 1.f);
+      const float us = fminf(fmaxf(ld_now(P.u_sample + b), 0.f), 1.f);
       // u in 2^-64 units (below 1), so that thr = floor(u * total) < total
       const unsigned long long u64 = us >= 1.f ? ~0ull : __double2ull_rz(static_cast<double>(us) * 18446744073709551616.0);
       const unsigned long long thr = __umul64hi(u64, total);

@@ -230,11 +230,13 @@ def test_attention_strided_views(cuda_lib, dtype):
     kv = torch.stack((k, v), 1).transpose(2, 3).contiguous().cuda()  # N, 2, Hkv, page, D
     cache = cuda_lib.KVCache(kv[:, 0].transpose(1, 2), kv[:, 1].transpose(1, 2), pages.cuda())
     qv = q.transpose(1, 2).contiguous().cuda().transpose(1, 2)
-    o = torch.empty(B, H, T, D, dtype=dt, device="cuda").transpose(1, 2)
-    cuda_lib.st_cache_attn(qv, cache, i32(lens).cuda(), o=o)
-    cuda_lib.st_check_status()
     ro, _, bo, _ = R.attention(q, k, v, pages, lens, None, None)
-    R.close("o", o, ro, bo)
+    turned = [t.permute(1, 2, 0, 3).contiguous().cuda().permute(2, 0, 1, 3) for t in (k, v)]  # pages innermost but D
+    for c in (cache, cuda_lib.KVCache(turned[0], turned[1], pages.cuda())):
+        o = torch.empty(B, H, T, D, dtype=dt, device="cuda").transpose(1, 2)
+        cuda_lib.st_cache_attn(qv, c, i32(lens).cuda(), o=o)
+        cuda_lib.st_check_status()
+        R.close("o", o, ro, bo)
 
 
 def test_attention_far_pages(cuda_lib):

@@ -25,7 +25,7 @@ class Serve:
         self.lens, self.counts = T([B], api.ST_I32), None
         self.q_rot = T([B, T_, H, 128], dt)
         self.parents = None
-        self.o, self.lse = T([B, T_, H, 128], dt), T([B, H, T_], api.ST_F32)
+        self.o, self.lse = T([B, T_, H, 128], dt, data=FAKE + (1 << 30)), T([B, H, T_], api.ST_F32)
         self.scale, self.ws, self.ws_bytes = 0.0, FAKE, 1 << 40
         self.target, self.draft = T([B, T_, V], api.ST_F32), T([B, T_, V], api.ST_F32)
         self.tokens, self.vpar = T([B, T_], api.ST_I32), T([B, T_], api.ST_I32)
@@ -172,6 +172,7 @@ def test_attn_refusals():
     check(c, E.ST_ERR_UNSUPPORTED, "256", sizes=dict(T_=257), parents=T([2, 257], E.ST_I32))
     check(c, E.ST_ERR_INVALID_ARG, "scale", scale=float("inf"))
     check(c, E.ST_ERR_SHAPE, "o has shape", o=T([2, 4, 8, 128]))
+    check(c, E.ST_ERR_INVALID_ARG, "must not be q_rot", o=T([2, 5, 8, 128]))
     check(c, E.ST_ERR_DTYPE, "o has", o=T([2, 5, 8, 128], E.ST_F32))
     check(c, E.ST_ERR_SHAPE, "lse", lse=T([2, 5, 8], E.ST_F32))
     check(c, E.ST_ERR_DTYPE, "lse", lse=T([2, 8, 5]))
