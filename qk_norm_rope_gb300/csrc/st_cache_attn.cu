@@ -830,11 +830,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
 
 // Joins the parts of an item whose tiles several CTAs held: block (x, y) looks
 // at the border before CTA x + 1 and, if it is an item's first inner border,
-// at rows 32 y .. of that item. A warp takes a row, a lane four columns; U
+// at rows kJoinRows y .. of that item. A warp takes a row, a lane four columns; U
 // parts are in flight: many where there are few rows (a decoding step, whose
 // items are spread over many CTAs), few and more warps per SM where there are
 // many rows.
-constexpr int kJoinRows = 32;
+constexpr int kJoinRows = 16;
 template <int U>
 __global__ void __launch_bounds__(256, U > 4 ? 2 : 6) join_kernel(const __grid_constant__ TcAttnParams P, int nt) {
   grid_dependency_wait();
@@ -928,7 +928,7 @@ cudaError_t launch_cache_attn_tc(const TcAttnParams& p, int nt, bool f16, cudaSt
 
 cudaError_t launch_cache_attn_join(const TcAttnParams& p, int nt, cudaStream_t stream) {
   if (p.ctas < 2) return cudaSuccess;
-  return launch_chained(p.part_rows <= kJoinRows ? join_kernel<16> : join_kernel<4>, dim3(p.ctas - 1, (p.part_rows + kJoinRows - 1) / kJoinRows), dim3(256), 0, stream, p, nt);
+  return launch_chained(p.part_rows <= 32 ? join_kernel<16> : join_kernel<4>, dim3(p.ctas - 1, (p.part_rows + kJoinRows - 1) / kJoinRows), dim3(256), 0, stream, p, nt);
 }
 
 }  // namespace st
