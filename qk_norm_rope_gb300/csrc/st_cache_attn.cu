@@ -240,11 +240,11 @@ __device__ __forceinline__ void find_start(const TcAttnParams& p, int nt, long l
   __syncthreads();
 }
 
-template <bool F16>
+template <bool F16, int K0, int K1>  // of the eight K-steps of 16 head dims
 __device__ __forceinline__ void issue_s(uint32_t tS, uint64_t dQ, uint64_t dK) {
   constexpr uint32_t idesc = idesc16(F16, 128, 128, 0, 0);
 #pragma unroll
-  for (int kk = 0; kk < 8; ++kk) mma_ss(tS, sdesc_add(dQ, kofs(kk)), sdesc_add(dK, kofs(kk)), idesc, kk > 0);
+  for (int kk = K0; kk < K1; ++kk) mma_ss(tS, sdesc_add(dQ, kofs(kk)), sdesc_add(dK, kofs(kk)), idesc, kk > 0);
 }
 template <bool F16>
 __device__ __forceinline__ void issue_pv(uint32_t tO, uint32_t tP, uint64_t dV, bool acc) {
@@ -706,8 +706,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
         }
         return wait_bar(&bars[L::KFull + s_kn % L::KS], (s_kn / L::KS) & 1, abort_flag, budget);
       };
-      auto scores = [&]() {
-        issue_s<F16>(tS, dQ, sdesc_add(dK0, (s_kn % L::KS) * kTileBytes));
+      constexpr int kHold = 6;  // K-steps of the scores under the lock (8: 468 us, 6 and 7: 459, 4: 464, 2: 481, 0: 514)
+      auto scores = [&](auto&& release) {
+        issue_s<F16, 0, kHold>(tS, dQ, sdesc_add(dK0, (s_kn % L::KS) * kTileBytes));
+        release();
+        issue_s<F16, kHold, 8>(tS, dQ, sdesc_add(dK0, (s_kn % L::KS) * kTileBytes));
         issued = true;
         mma_commit(&bars[L::SFull + slot]);
         mma_commit(&bars[L::KEmpty + s_kn % L::KS]);
@@ -717,11 +720,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
       // NT = 2: a slot's PV and next scores enter the tensor pipe as one batch:
       // two threads' MMAs taken in turns end together, and the slots' softmax
       // then runs side by side with the tensor pipe idle (2048-token chunk after
-      // 16384 tokens: 563 us without the lock, 465 with it).
+      // 16384 tokens: 563 us without the lock, 459 with it).
+      // The lock is let go before the last MMAs, so that it has changed hands
+      // when the pipe has done them.
       auto batch = [&](auto&& issue) -> bool {
         if constexpr (NT == 1) {
           tc_fence_after();
-          issue();
+          issue([] {});
           return true;
         }
         const long long t0 = clock64();
@@ -732,9 +737,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
           }
         }
         tc_fence_after();
-        issue();
-        __threadfence_block();
-        atomicExch(pipe_lock, 0);
+        issue([&] {
+          __threadfence_block();
+          atomicExch(pipe_lock, 0);
+        });
         return true;
       };
       ok = find_scores() && (!more || batch(scores));
@@ -744,11 +750,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
           if (same && !(ok = find_scores())) break;
           if (!(ok = wait_bar(&bars[L::VFull + p_kn % L::VS], (p_kn / L::VS) & 1, abort_flag, budget))) break;
           if (!(ok = wait_bar(&bars[L::PFull + slot], p_done & 1, abort_flag, budget))) break;
-          ok = batch([&] {
+          ok = batch([&](auto&& release) {
             issue_pv<F16>(tO, tS, sdesc_add(dV0, (p_kn % L::VS) * kTileBytes), i > 0);
             mma_commit(&bars[L::VEmpty + p_kn % L::VS]);
             if (i + 1 == p_left) mma_commit(&bars[L::OFull]);
-            if (same) scores();
+            if (same) scores(release);
+            else release();
           });
           if (!ok) break;
           p_kn += NT == 2 ? 1 : 2;
