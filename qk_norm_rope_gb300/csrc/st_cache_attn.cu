@@ -363,11 +363,16 @@ __device__ __forceinline__ Box find_box(const TcAttnParams& P, const Walk& wk, i
   return b;
 }
 
-// A part in shared memory: 128 rows of 128 floats over the K stages, the
-// 16-byte chunks of a row permuted so that neither a thread per row (writing)
-// nor a warp per row (reading) meets bank conflicts; (reference, sum) of the
-// rows over the V stages.
+// A part in shared memory: NT x 128 rows of 128 floats over the K stages (and
+// on over the V stages), the 16-byte chunks of a row permuted so that neither a
+// thread per row (writing) nor a warp per row (reading) meets bank conflicts;
+// behind them (reference, sum) of the rows.
 __device__ __forceinline__ uint32_t stage_off(int row, int chunk) { return row * 512u + ((chunk ^ (row & 31)) << 4); }
+__device__ __forceinline__ void stage_chunk32(uint8_t* base, int row, int q4, const float (&y)[32]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    *reinterpret_cast<float4*>(base + stage_off(row, 8 * q4 + e)) = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+}
 
 template <int NT, bool F16, bool TREE, bool CL>
 __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant__ TcAttnParams P) {
@@ -447,6 +452,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
     wk.left = start->left;
   }
   const int G = c.group, tile_rows = P.tpt * G;
+  float2* part_ml = reinterpret_cast<float2*>(sm + L::k + NT * 65536);  // CL
+  static_assert(NT * (65536 + 1024) <= (L::KS + L::VS) * kTileBytes, "a part fits over the K and V stages");
 
   if (warp < kSoftWarps) {
     // -------------------------------------------------------------- softmax
@@ -546,10 +553,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
             tmem_ld32(tO + 32 * q4, r32);
             float y[32];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(r32[e]) * (whole ? inv : 1.f);
+            for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(r32[e]) * (whole && !CL ? inv : 1.f);
+            if constexpr (CL) {
+              stage_chunk32(sm + L::k, slot * 128 + r, q4, y);
+              continue;
+            }
             if (valid) store_chunk32(whole ? c.o : c.part, whole ? ooff : prow * kD, whole ? c.kv.dt : kDtF32, q4, y);
           }
-          if (valid) {
+          if (CL) part_ml[slot * 128 + r] = make_float2(m_run, l_run);
+          if (!CL && valid) {
             if (whole) c.lse[(static_cast<int64_t>(wk.pb) * c.H + h) * c.T + t] = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * kLn2;
             else P.part_ml[prow] = make_float2(m_run, l_run);
           }
@@ -582,14 +594,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
               y[e] = fmaf(v1, f1, v0 * f0) * inv;
             }
             if constexpr (CL) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                *reinterpret_cast<float4*>(sm + L::k + stage_off(r, 8 * q4 + e)) = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+              stage_chunk32(sm + L::k, r, q4, y);
               continue;
             }
             if (valid) store_chunk32(whole ? c.o : c.part, whole ? ooff : prow * kD, whole ? c.kv.dt : kDtF32, q4, y);
           }
-          if (CL && slot == 0) reinterpret_cast<float2*>(sm + L::v)[r] = make_float2(m, l);
+          if (CL && slot == 0) part_ml[r] = make_float2(m, l);
           if (!CL && valid && slot == 0) {
             if (whole) c.lse[(static_cast<int64_t>(wk.pb) * c.H + h) * c.T + t] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
             else P.part_ml[prow] = make_float2(m, l);
@@ -605,7 +615,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
       vc += wk.kt1 - wk.kt0;
       ++n_piece;
     }
-    if (CL && n_piece == 0 && slot == 0) reinterpret_cast<float2*>(sm + L::v)[r] = make_float2(-INFINITY, 0.f);
+    if (CL && n_piece == 0 && (NT == 2 || slot == 0)) part_ml[(NT == 2 ? slot * 128 : 0) + r] = make_float2(-INFINITY, 0.f);
   } else if (warp < kWarpQ0 + kQWarps) {
     // ---------------------------------------------------------------- Q rows
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
@@ -787,11 +797,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
   }
   tc_fence_before();
   if constexpr (CL) {
-    static_assert(NT == 1 && L::KS * kTileBytes >= 128 * 512, "a part fits over the K stages");
     cluster_sync();  // every CTA's part is in place
     const int rank = static_cast<int>(cluster_rank()), m = wk.m, b = wk.b, h = wk.h;
-    const int rows = max(0, min(P.tpt, wk.it.cnt - m * P.tpt)) * G;
-    for (int r = (warp << P.cluster_shift) + rank; r < rows; r += kTcWarps << P.cluster_shift) {
+    const int there = max(0, min(NT * P.tpt, wk.it.cnt - m * NT * P.tpt)) * G;  // rows, tile after tile
+    for (int e = (warp << P.cluster_shift) + rank; e < there; e += kTcWarps << P.cluster_shift) {
+      const int r = NT == 2 && e >= tile_rows ? 128 + e - tile_rows : e;  // in the part
       float2 x[kMaxClusterAttn];
       float4 y[kMaxClusterAttn];
 #pragma unroll
@@ -799,7 +809,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
         x[i] = make_float2(-INFINITY, 0.f);
         y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (i < P.cluster) {
-          x[i] = ld_peer_f2(mapa_shared(smem_u32(sm + L::v) + 8 * r, i));
+          x[i] = ld_peer_f2(mapa_shared(smem_u32(part_ml + r), i));
           y[i] = ld_peer_f4(mapa_shared(smem_u32(sm + L::k) + stage_off(r, lane_id), i));
         }
       }
@@ -816,7 +826,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
         o = make_float4(fmaf(f, y[i].x, o.x), fmaf(f, y[i].y, o.y), fmaf(f, y[i].z, o.z), fmaf(f, y[i].w, o.w));
       }
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const int t = m * P.tpt + r / G, hq = h * G + r % G;
+      const int t = m * NT * P.tpt + e / G, hq = h * G + e % G;
       const int64_t off = b * c.o_sb + static_cast<int64_t>(t) * c.o_ss + static_cast<int64_t>(hq) * c.o_sh + 4 * lane_id;
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(c.o) + off) =
           make_uint2(pack16<F16>(o.x * inv, o.y * inv), pack16<F16>(o.z * inv, o.w * inv));
@@ -929,13 +939,15 @@ cudaError_t launch_nt(const TcAttnParams& p, bool f16, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_cache_attn_tc(const TcAttnParams& p, int nt, bool f16, cudaStream_t stream) {
-  if (p.cluster > 0) return launch_nt<1, true>(p, f16, stream);
+  if (p.cluster > 0) return nt == 2 ? launch_nt<2, true>(p, f16, stream) : launch_nt<1, true>(p, f16, stream);
   return nt == 2 ? launch_nt<2, false>(p, f16, stream) : launch_nt<1, false>(p, f16, stream);
 }
 
 cudaError_t launch_cache_attn_join(const TcAttnParams& p, int nt, cudaStream_t stream) {
   if (p.ctas < 2) return cudaSuccess;
-  return launch_chained(p.part_rows <= 32 ? join_kernel<16> : join_kernel<4>, dim3(p.ctas - 1, (p.part_rows + kJoinRows - 1) / kJoinRows), dim3(256), 0, stream, p, nt);
+  // few rows, or few items, whose parts are then many
+  const bool deep = p.part_rows <= 32 || static_cast<int64_t>(p.c.B) * p.c.kv.Hkv * p.n_groups * 4 <= p.ctas;
+  return launch_chained(deep ? join_kernel<16> : join_kernel<4>, dim3(p.ctas - 1, (p.part_rows + kJoinRows - 1) / kJoinRows), dim3(256), 0, stream, p, nt);
 }
 
 }  // namespace st

@@ -125,7 +125,7 @@ struct TcAttnParams {
   int n_groups;                // groups per sequence
   int part_rows;               // rows of a partial result
   int ctas;
-  int cluster;                 // CTAs per item of the clustered form (NT = 1): 2, 4 or 8; 0: the dealt form
+  int cluster;                 // CTAs per item of the clustered form: 2, 4 or 8; 0: the dealt form
   int cluster_shift;
   struct JoinMeta* meta;       // [ctas], workspace
   float2* part_ml;             // [2 ctas, part_rows] (reference, sum); c.part: [2 ctas, part_rows, D]

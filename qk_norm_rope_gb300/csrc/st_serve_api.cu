@@ -164,12 +164,15 @@ st_status plan_attn(const st_tensor* q, const st_kv_cache* cache, const st_tenso
     // 8 K/V heads: 777 keys 10.5 us dealt, 7.1 clustered; 8000 keys 17.9 and
     // 14.4; 16000 keys 18.8 and 22.3; 8 sequences of up to 1000 keys 16.6 and
     // 10.9, of up to 8000 keys 36 and 43.
+    // With more than 128 rows a head the join is the larger part: as much as 16
+    // tiles (a tree of 61 nodes, 32 / 8 heads: 1000 keys 22 us dealt, 15.6
+    // clustered; 8000 keys 41 and 26; 32000 keys 61 and 69).
     t.cluster = 0;
-    if (P->nt == 1) {
+    {
       const int cl = items <= 15 ? 8 : (items <= 36 ? 4 : (items <= 76 ? 2 : 1));
       static_assert(kMaxClusterAttn == 8, "the largest cluster");
-      const int64_t mean = p.B == 1 ? 2 : 1;  // halves
-      if (cl > 1 && cap_tiles * (2 * kSmCount - mean * items * cl) <= static_cast<int64_t>(16) * cl * kSmCount) t.cluster = cl;
+      const int64_t mean = p.B == 1 ? 2 : 1, saved = P->nt == 1 ? 16 : 32;  // halves of the room; of tiles
+      if (cl > 1 && cap_tiles * (2 * kSmCount - mean * items * cl) <= saved * cl * kSmCount) t.cluster = cl;
     }
     if (t.cluster > 0) {
       t.ctas = static_cast<int>(items) * t.cluster;
