@@ -336,6 +336,41 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float sc,
   tmem_st_wait();
 }
 
+// 32 bytes of a thread in one store: a thread per row writes whole sectors, in
+// half as many instructions of 32 sectors each as with 16-byte stores.
+__device__ __forceinline__ void st_v8(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+// Columns [32 q4, 32 q4 + 32) of a row: fp32 into a part, or 16 bits into the
+// result (`wide`: its rows start on 32 bytes).
+__device__ __forceinline__ void store_part32(float* row, int q4, const float (&y)[32]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(y[8 * i + e]);
+    st_v8(row + 32 * q4 + 8 * i, w);
+  }
+}
+template <bool F16>
+__device__ __forceinline__ void store_out32(void* o, int64_t off, bool wide, int q4, const float (&y)[32]) {
+  uint16_t* row = static_cast<uint16_t*>(o) + off + 32 * q4;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = pack16<F16>(y[16 * i + 2 * e], y[16 * i + 2 * e + 1]);
+    if (wide) {
+      st_v8(row + 16 * i, w);
+    } else {
+      reinterpret_cast<uint4*>(row + 16 * i)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      reinterpret_cast<uint4*>(row + 16 * i)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+  }
+}
+
 // Reads of a peer CTA's shared memory (cluster addresses from mapa).
 __device__ __forceinline__ float4 ld_peer_f4(uint32_t a) {
   float4 v;
@@ -558,7 +593,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
               stage_chunk32(sm + L::k, slot * 128 + r, q4, y);
               continue;
             }
-            if (valid) store_chunk32(whole ? c.o : c.part, whole ? ooff : prow * kD, whole ? c.kv.dt : kDtF32, q4, y);
+            if (valid && whole) store_out32<F16>(c.o, ooff, P.o_wide != 0, q4, y);
+            else if (valid) store_part32(c.part + prow * kD, q4, y);
           }
           if (CL) part_ml[slot * 128 + r] = make_float2(m_run, l_run);
           if (!CL && valid) {
@@ -597,7 +633,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
               stage_chunk32(sm + L::k, r, q4, y);
               continue;
             }
-            if (valid) store_chunk32(whole ? c.o : c.part, whole ? ooff : prow * kD, whole ? c.kv.dt : kDtF32, q4, y);
+            if (valid && whole) store_out32<F16>(c.o, ooff, P.o_wide != 0, q4, y);
+            else if (valid) store_part32(c.part + prow * kD, q4, y);
           }
           if (CL && slot == 0) part_ml[r] = make_float2(m, l);
           if (!CL && valid && slot == 0) {

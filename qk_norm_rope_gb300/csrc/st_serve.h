@@ -124,6 +124,7 @@ struct TcAttnParams {
   int tpt;                     // tokens per query tile (128 / group)
   int n_groups;                // groups per sequence
   int part_rows;               // rows of a partial result
+  int o_wide;                  // 1: o's rows start on 32 bytes
   int ctas;
   int cluster;                 // CTAs per item of the clustered form: 2, 4 or 8; 0: the dealt form
   int cluster_shift;

@@ -332,6 +332,7 @@ st_status st_cache_attn(const st_tensor* q_rot, const st_kv_cache* cache, const 
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     t.part_ml = reinterpret_cast<float2*>(ws + P.off_ml);
     t.meta = reinterpret_cast<JoinMeta*>(ws + P.off_meta);
+    t.o_wide = (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0 && p.o_sb % 16 == 0 && p.o_ss % 16 == 0 && p.o_sh % 16 == 0;
     if ((st = encode_rows_map(cache->k, &t.tmap_k, &t.k_r_first, 1 << t.box_shift)) != ST_OK) return st;
     if ((st = encode_rows_map(cache->v, &t.tmap_v, &t.v_r_first, 1 << t.box_shift)) != ST_OK) return st;
     if ((st = cuda_check(launch_counted(ST_K_CACHE_ATTN, stream, [&] { return launch_cache_attn_tc(t, P.nt, p.kv.dt == ST_F16, stream); }),
