@@ -9,7 +9,7 @@
 // kernel joins them; with one split it writes O and LSE itself. Bound by the
 // fp32 FMA rate: a thread holds 4 x 4 scores and 8 x 4 outputs, so that shared
 // memory (8 and 12 16-byte reads, mostly broadcasts, for 64 and 128 FMAs) keeps
-// up; with half as many rows (2 x 4 and 4 x 4) it did not, 47 us against 37 for
+// up; with half as many rows (2 x 4 and 4 x 4) it did not, 47 us against 37 (34 with packed FMAs) for
 // four trees of 13 nodes after up to 2001 tokens. The weights P take K's place
 // in shared memory once the scores are done, so that two CTAs fit on an SM.
 #include <atomic>
@@ -83,7 +83,9 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
       node = up;
     }
   }
-  float o[8][4] = {};
+  float2 o[8][2];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = make_float2(0.f, 0.f);
   float m_run[4], l_run[4];  // of the thread's score rows: the maximum, and the sum over the thread's own keys
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
@@ -161,7 +163,11 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
     asm volatile("cp.async.wait_group 1;" ::: "memory");  // Q and K
     __syncthreads();
     locate(jt + 1);
-    float sc[4][4] = {};
+    float2 acc[4][4];  // even and odd head dims: two products per instruction
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[w][i] = make_float2(0.f, 0.f);
 #pragma unroll 4
     for (int d = 0; d < kD; d += 4) {
       float4 qq[4], kk[4];
@@ -173,14 +179,16 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
       for (int w = 0; w < 4; ++w)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          sc[w][i] = fmaf(qq[w].x, kk[i].x, fmaf(qq[w].y, kk[i].y, fmaf(qq[w].z, kk[i].z, fmaf(qq[w].w, kk[i].w, sc[w][i]))));
+          acc[w][i] = __ffma2_rn(make_float2(qq[w].x, qq[w].y), make_float2(kk[i].x, kk[i].y),
+                                 __ffma2_rn(make_float2(qq[w].z, qq[w].w), make_float2(kk[i].z, kk[i].w), acc[w][i]));
     }
     __syncthreads();  // K is read: P takes its place
     const float sl = p.scale_log2;
+    float sc[4][4];
 #pragma unroll
     for (int w = 0; w < 4; ++w)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sc[w][i] *= sl;
+      for (int i = 0; i < 4; ++i) sc[w][i] = (acc[w][i].x + acc[w][i].y) * sl;
     if (j0 + kN > prefix) {  // rows of padding see anything here: they are dropped at the end
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
@@ -221,8 +229,8 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float corr = s.corr[8 * rg + i];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) o[i][u] *= corr;
+      o[i][0] = make_float2(o[i][0].x * corr, o[i][0].y * corr);
+      o[i][1] = make_float2(o[i][1].x * corr, o[i][1].y * corr);
     }
 #pragma unroll 2
     for (int k = 0; k < kN; k += 4) {
@@ -235,10 +243,9 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
         const float pw[4] = {pp.x, pp.y, pp.z, pp.w};
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          o[i][0] = fmaf(pw[u], vv[u].x, o[i][0]);
-          o[i][1] = fmaf(pw[u], vv[u].y, o[i][1]);
-          o[i][2] = fmaf(pw[u], vv[u].z, o[i][2]);
-          o[i][3] = fmaf(pw[u], vv[u].w, o[i][3]);
+          const float2 pp2 = make_float2(pw[u], pw[u]);
+          o[i][0] = __ffma2_rn(pp2, make_float2(vv[u].x, vv[u].y), o[i][0]);
+          o[i][1] = __ffma2_rn(pp2, make_float2(vv[u].z, vv[u].w), o[i][1]);
         }
       }
     }
@@ -266,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
     if (r >= n_here) continue;
     if (p.splits > 1) {
       const int64_t slot = (item * p.splits + split) * kR + r;
-      *reinterpret_cast<float4*>(p.part + slot * kD + 4 * dg) = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+      *reinterpret_cast<float4*>(p.part + slot * kD + 4 * dg) = make_float4(o[i][0].x, o[i][0].y, o[i][1].x, o[i][1].y);
       if (dg == 0) {
         float2* ml = reinterpret_cast<float2*>(p.part + static_cast<int64_t>(gridDim.x) * p.splits * kR * kD);
         ml[slot] = make_float2(s.m[r], s.l[r]);
@@ -277,10 +284,10 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
     const int t = t0 + (g0 + r) / G, h = hk * G + (g0 + r) % G;
     const int64_t off = b * p.o_sb + t * p.o_ss + h * p.o_sh + 4 * dg;
     if (p.kv.dt == kDtF32)
-      *reinterpret_cast<float4*>(static_cast<float*>(p.o) + off) = make_float4(o[i][0] * inv, o[i][1] * inv, o[i][2] * inv, o[i][3] * inv);
+      *reinterpret_cast<float4*>(static_cast<float*>(p.o) + off) = make_float4(o[i][0].x * inv, o[i][0].y * inv, o[i][1].x * inv, o[i][1].y * inv);
     else
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + off) =
-          make_uint2(pack_dt(p.kv.dt, o[i][0] * inv, o[i][1] * inv), pack_dt(p.kv.dt, o[i][2] * inv, o[i][3] * inv));
+          make_uint2(pack_dt(p.kv.dt, o[i][0].x * inv, o[i][0].y * inv), pack_dt(p.kv.dt, o[i][1].x * inv, o[i][1].y * inv));
     if (dg == 0) p.lse[(static_cast<int64_t>(b) * p.H + h) * p.T + t] = l == 0.f ? -INFINITY : (s.m[r] + log2f(l)) * kLn2;
   }
 }
