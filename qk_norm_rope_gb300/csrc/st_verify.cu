@@ -36,7 +36,8 @@ constexpr int kVerThreads = 256;
 constexpr int kVerWarps = kVerThreads / 32;
 constexpr int kBatches = 64;    // batches of a warp's slice whose sums are kept for the draw (further ones are read again)
 constexpr int kRowBatch = 16;  // rows of 32 probabilities whose loads are issued together
-constexpr double kUnit = 1.0 / 8796093022208.0;  // 2^-43, the unit of a weight
+constexpr float kUnit = 1.0f / 8796093022208.0f;       // 2^-43, the unit of a weight
+constexpr unsigned long long kOne = 8796093022208ull;  // 1 in it
 
 // The type is the kernel's template argument: a branch on it per element would
 // keep the loads of a batch from being issued together (60000 cycles for a sum
@@ -59,44 +60,53 @@ constexpr float kLo = 1.5f * 9.5367431640625e-7f;     // 1.5 * 2^(23 - 43)
 struct Limbs {  // of two values, modulo 2^32; kHi's and kLo's own bits are still in them
   uint32_t hi, lo;
 };
+__device__ __forceinline__ float2 pair(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 less(float2 x, float2 y) { return __ffma2_rn(y, pair(-1.f), x); }  // x - y, without negating y first
 __device__ __forceinline__ Limbs limbs(float2 v, float2 tail) {  // of v + tail, |tail| <= 2^-23; both values added up
-  const float2 t = __fadd2_rn(v, make_float2(kHi, kHi));
-  const float2 back = __fadd2_rn(t, make_float2(-kHi, -kHi));
-  const float2 rem = __fadd2_rn(__fadd2_rn(v, make_float2(-back.x, -back.y)), tail);
-  const float2 l = __fadd2_rn(rem, make_float2(kLo, kLo));
+  const float2 t = __fadd2_rn(v, pair(kHi));
+  const float2 rem = __fadd2_rn(less(v, __fadd2_rn(t, pair(-kHi))), tail);
+  const float2 l = __fadd2_rn(rem, pair(kLo));
   return {__float_as_uint(t.x) + __float_as_uint(t.y), __float_as_uint(l.x) + __float_as_uint(l.y)};
 }
 // The limbs of max(p - a q, 0). a = 0 and a = 1 (before and after the first
-// rejection) need no product; else a = ah + al and the product is carried with
-// its rounding error. A difference of p and something no larger is p - s = d
-// with the error (p - d) - s, exactly.
+// rejection) need no product; else a = ah + al and the product is s with the
+// error r. For s <= p the difference d of p and s has the error (p - d) - s
+// exactly; for p < s <= 2 p it is exact, and that term 0; beyond it is below
+// -s/2 and its sign stands whatever the error.
 struct Scale {
   float ah, al;
 };
+// A sum in two floats. (fp64 arithmetic would serve, at a hundredth of the rate:
+// a wave of it in every warp costs 1 us a turn.)
+__device__ __forceinline__ Scale split(unsigned long long x) {
+  const float h = __ull2float_rn(x);
+  const long long rest = static_cast<long long>(x - __float2ull_rn(h));
+  return {h * kUnit, __ll2float_rn(rest) * kUnit};
+}
 template <int A>  // 0: a = 0; 1: a = 1; 2: any a
 __device__ __forceinline__ Limbs weight(float2 p, float2 q, Scale a) {
-  if constexpr (A == 0) return limbs(p, make_float2(0.f, 0.f));
-  float2 s = q, tail = make_float2(0.f, 0.f);
-  if constexpr (A == 2) {
-    s = make_float2(__fmul_rn(a.ah, q.x), __fmul_rn(a.ah, q.y));
-    tail = make_float2(__fmaf_rn(a.al, q.x, __fmaf_rn(a.ah, q.x, -s.x)), __fmaf_rn(a.al, q.y, __fmaf_rn(a.ah, q.y, -s.y)));
-    // nothing is left where the product is p or more: then s = p, without a tail
-    const bool nx = s.x > p.x || (s.x == p.x && tail.x >= 0.f), ny = s.y > p.y || (s.y == p.y && tail.y >= 0.f);
-    s = make_float2(nx ? p.x : s.x, ny ? p.y : s.y);
-    tail = make_float2(nx ? 0.f : tail.x, ny ? 0.f : tail.y);
-  } else {
-    s = make_float2(fminf(p.x, q.x), fminf(p.y, q.y));
+  if constexpr (A == 0) return limbs(p, pair(0.f));
+  if constexpr (A == 1) {
+    const float2 s = make_float2(fminf(p.x, q.x), fminf(p.y, q.y));
+    const float2 d = less(p, s);
+    return limbs(d, less(less(p, d), s));
   }
-  const float2 ns = make_float2(-s.x, -s.y);
+  const float2 ns = __fmul2_rn(q, pair(-a.ah)), r = __ffma2_rn(q, pair(a.ah), ns);
   float2 d = __fadd2_rn(p, ns);
-  float2 e = __fadd2_rn(__fadd2_rn(p, make_float2(-d.x, -d.y)), ns);
-  if constexpr (A == 2) {
-    e = __fadd2_rn(e, make_float2(-tail.x, -tail.y));
-    const bool zx = d.x + e.x <= 0.f, zy = d.y + e.y <= 0.f;
-    d = make_float2(zx ? 0.f : d.x, zy ? 0.f : d.y);
-    e = make_float2(zx ? 0.f : e.x, zy ? 0.f : e.y);
-  }
+  float2 e = __ffma2_rn(q, pair(-a.al), less(__fadd2_rn(less(p, d), ns), r));
+  const float2 x = __fadd2_rn(d, e);
+  d = make_float2(x.x > 0.f ? d.x : 0.f, x.y > 0.f ? d.y : 0.f);
+  e = make_float2(x.x > 0.f ? e.x : 0.f, x.y > 0.f ? e.y : 0.f);
   return limbs(d, e);
+}
+// u q C < max(p - a q, 0), the acceptance of a child with siblings rejected
+// before: both sides in two floats, the differences of their parts added up.
+__device__ __forceinline__ bool accepts(float u, float p, float q, Scale a, Scale c) {
+  const float s = __fmul_rn(a.ah, q), d = __fsub_rn(p, s);
+  const float e = __fmaf_rn(-a.al, q, __fsub_rn(__fsub_rn(__fsub_rn(p, d), s), __fmaf_rn(a.ah, q, -s)));
+  const float t = __fmul_rn(u, q), t2 = __fmaf_rn(u, q, -t), w = __fmul_rn(t, c.ah);
+  const float w2 = __fadd_rn(__fmaf_rn(t, c.ah, -w), __fmaf_rn(t, c.al, __fmul_rn(t2, c.ah)));
+  return __fadd_rn(d, e) > 0.f && __fadd_rn(__fsub_rn(w, d), __fsub_rn(w2, e)) < 0.f;
 }
 constexpr uint32_t kPairHi = 2u * 0x40c00000u, kPairLo = 2u * 0x35c00000u;  // kHi's and kLo's bits, twice
 __device__ __forceinline__ unsigned long long whole(uint32_t hi, uint32_t lo) {
@@ -123,10 +133,7 @@ struct VerState {
   unsigned long long warp_tot[kVerWarps];
   unsigned long long batch_tot[kVerWarps][kBatches];
   unsigned long long cta_tot[2][kMaxClusterVerify];  // by the parity of the exchange
-  int rejected[kMaxVerify];
-  int n_rejected;
-  int cur, n_path, more;         // more: a rejected child has a sibling left
-  double a;
+  int rejected[kMaxVerify];      // of the node where the walk ended, without draft probabilities
 };
 
 template <int DT>
@@ -154,12 +161,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
     s.uu[i] = ok ? ld_now(P.u_accept + static_cast<int64_t>(b) * P.T + i) : 0.f;
     s.first_yes[i] = static_cast<double>(s.uu[i]) * s.qq[i] < static_cast<double>(s.pp[i]);
   }
-  if (tid == 0) {
-    s.cur = 0;
-    s.n_path = cnt > 0 ? 1 : 0;
-    s.path[0] = 0;
-    s.n_rejected = 0;
-  }
+  if (tid == 0) s.path[0] = 0;
   // also: every CTA of the cluster runs before another writes into its memory
   if (C > 1) cluster_sync();
   else __syncthreads();
@@ -195,10 +197,10 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
 
   // sum over V of the residual weights of node `cur` at `a`, less the removed
   // tokens; leaves the warps' totals in s.warp_tot and the CTAs' in s.cta_tot
-  auto sum_row = [&](int cur, double a, bool removed, bool keep) -> unsigned long long {
+  auto sum_row = [&](int cur, unsigned long long a, int removed, bool keep) -> unsigned long long {
     const int64_t pe = b * P.p_sb + cur * P.p_st, qe = b * P.q_sb + cur * P.q_st;
     unsigned long long acc = 0;
-    const Scale sc{static_cast<float>(a), static_cast<float>(a - static_cast<float>(a))};
+    const Scale sc = split(a);
     auto pass = [&](auto kind) {
       constexpr int A = decltype(kind)::value;
       for (int v0 = w_lo; v0 < w_hi; v0 += 32 * kRowBatch) {
@@ -208,10 +210,10 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
 #pragma unroll
         for (int u = 0; u < kRowBatch; u += 2) {
           const Limbs x = weight<A>(make_float2(pv[u], pv[u + 1]), make_float2(qv[u], qv[u + 1]), sc);
-          hi += x.hi - kPairHi;
-          lo += x.lo - kPairLo;
+          hi += x.hi;
+          lo += x.lo;
         }
-        unsigned long long part = whole(hi, lo);
+        unsigned long long part = whole(hi - kRowBatch / 2 * kPairHi, lo - kRowBatch / 2 * kPairLo);
         if (keep) {  // the batches' own sums, where the draw will look
           const int batch = (v0 - w_lo) / (32 * kRowBatch);
           if (batch < kBatches) {
@@ -223,14 +225,14 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
         acc += part;
       }
     };
-    if (!drafted || a == 0.0) pass(std::integral_constant<int, 0>());
-    else if (a == 1.0) pass(std::integral_constant<int, 1>());
+    if (!drafted || a == 0) pass(std::integral_constant<int, 0>());
+    else if (a == kOne) pass(std::integral_constant<int, 1>());
     else pass(std::integral_constant<int, 2>());
     acc = warp_sum(acc);
     if (lane == 0) s.warp_tot[warp] = acc;
     __syncthreads();
-    if (removed) {
-      for (int r = tid; r < s.n_rejected; r += kVerThreads) {
+    if (removed > 0) {
+      for (int r = tid; r < removed; r += kVerThreads) {
         const int x = s.tok[s.rejected[r]], w = x / sub - rank * kVerWarps;
         if (w >= 0 && w < kVerWarps) {
           const unsigned long long f = 0ull - fix(s.pp[s.rejected[r]]);
@@ -255,87 +257,68 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
     return total;
   };
 
-  int last = 0;                       // warp 0: the last child tried
-  double a = 0.0, c = 1.0;            // warp 0
-  while (cnt > 0) {  // every turn tries further nodes: at most cnt turns
-    if (warp == 0) {
-      int cur = s.cur, n = s.n_path, n_rej = s.n_rejected, more = 0;
-      // the next child of `cur` behind node `from`, or cnt
-      auto next_child = [&](int from) {
-        for (int base = from + 1; base < cnt; base += 32) {
-          const int i = base + lane;
-          const unsigned m = __ballot_sync(0xffffffffu, i < cnt && s.par[i] == cur);
-          if (m) return base + __ffs(m) - 1;
-        }
-        return cnt;
-      };
-      int i = next_child(last);
-      while (i < cnt) {
-        const float u = s.uu[i], px = s.pp[i], qx = s.qq[i];
-        bool yes;
-        bool again = false;  // a token that was already removed here
-        if (drafted) {
-          yes = a == 0.0 ? s.first_yes[i]
-                         : static_cast<double>(u) * qx * c < fmax(static_cast<double>(px) - a * qx, 0.0);
-        } else {
-          for (int r0 = 0; r0 < n_rej; r0 += 32)
-            again |= __any_sync(0xffffffffu, r0 + lane < n_rej && s.tok[s.rejected[min(r0 + lane, n_rej - 1)]] == s.tok[i]);
-          yes = !again && (n_rej == 0 ? s.first_yes[i] : static_cast<double>(u) * c < static_cast<double>(px));
-        }
-        last = i;
-        if (yes) {
-          cur = i;
-          if (lane == 0) s.path[n] = i;
-          ++n;
-          a = 0.0;
-          c = 1.0;
-          n_rej = 0;
-          i = next_child(last);
-          continue;
-        }
-        i = next_child(last);
-        if (drafted) {
-          a += c;
-          if (i < cnt) {  // the next sibling needs the residual's sum
-            more = 1;
-            break;
-          }
-        } else if (!again) {
-          c -= px;
-          if (lane == 0) s.rejected[n_rej] = last;
-          ++n_rej;
-          __syncwarp();
-        }
-      }
-      __syncwarp();
-      if (lane == 0) {
-        s.cur = cur;
-        s.n_path = n;
-        s.n_rejected = drafted ? 0 : n_rej;
-        s.a = a;
-        s.more = more;
-      }
+  // the walk, by every warp for itself
+  int cur = 0, n = cnt > 0 ? 1 : 0, n_rej = 0;
+  unsigned long long a = 0, c = kOne;  // a and C, in 2^-43
+  double left = 1.0;                   // C without draft probabilities
+  // the next child of `cur` behind node `from`, or cnt
+  auto next_child = [&](int from) {
+    for (int base = from + 1; base < cnt; base += 32) {
+      const int i = base + lane;
+      const unsigned m = __ballot_sync(0xffffffffu, i < cnt && s.par[i] == cur);
+      if (m) return base + __ffs(m) - 1;
     }
-    __syncthreads();
-    if (!s.more) break;
-    const unsigned long long total = sum_row(s.cur, s.a, false, false);
-    parity ^= 1;
-    if (warp == 0) c = static_cast<double>(total) * kUnit;
-    __syncthreads();
+    return cnt;
+  };
+  // a child of `cur` before node i has i's token
+  auto tried = [&](int i) {
+    bool again = false;
+    for (int base = 0; base < i; base += 32) again |= base + lane < i && s.par[base + lane] == cur && s.tok[base + lane] == s.tok[i];
+    return __any_sync(0xffffffffu, again) != 0;
+  };
+  for (int i = next_child(0); i < cnt;) {
+    const float u = s.uu[i], px = s.pp[i], qx = s.qq[i];
+    const bool again = !drafted && n_rej > 0 && tried(i);  // a token that was already removed here
+    bool yes;
+    if (drafted)
+      yes = a == 0 ? s.first_yes[i] : accepts(u, px, qx, split(a), split(c));
+    else
+      yes = !again && (n_rej == 0 ? s.first_yes[i] : static_cast<double>(u) * left < static_cast<double>(px));
+    const int last = i;
+    if (yes) {
+      cur = i;
+      if (tid == 0) s.path[n] = i;
+      ++n;
+      a = 0;
+      c = kOne;
+      left = 1.0;
+      n_rej = 0;
+      i = next_child(last);
+      continue;
+    }
+    i = next_child(last);
+    if (drafted) {
+      a += c;
+      if (i < cnt) {  // the next sibling needs the residual's sum
+        c = sum_row(cur, a, 0, false);
+        parity ^= 1;
+      }
+    } else if (!again) {
+      left -= px;
+      if (tid == 0) s.rejected[n_rej] = last;
+      ++n_rej;
+    }
   }
 
   // the draw
   if (cnt > 0) {
-    const int cur = s.cur;
-    double aa = s.a;
-    bool removed = s.n_rejected > 0;
-    unsigned long long total = sum_row(cur, aa, removed, true);
+    unsigned long long total = sum_row(cur, a, n_rej, true);
     if (total == 0) {  // p <= a q everywhere: the target's own distribution
       parity ^= 1;
-      aa = 0.0;
-      removed = false;
+      a = 0;
+      n_rej = 0;
       __syncthreads();
-      total = sum_row(cur, 0.0, false, true);
+      total = sum_row(cur, 0, 0, true);
     }
     if (total > 0) {
       const float us = fminf(fmaxf(ld_now(P.u_sample + b), 0.f), 1.f);
@@ -346,7 +329,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
       for (int r = 0; r < rank; ++r) run += s.cta_tot[parity][r];
       if (thr >= run && thr < run + s.cta_tot[parity][rank]) {  // one CTA of the cluster
         const int64_t pe = b * P.p_sb + cur * P.p_st, qe = b * P.q_sb + cur * P.q_st;
-        const Scale sc{static_cast<float>(aa), static_cast<float>(aa - static_cast<float>(aa))};
+        const Scale sc = split(a);
         // the slice, then the batch, that holds it, by their sums
         int w = 0;
         while (w < kVerWarps - 1 && run + s.warp_tot[w] <= thr) run += s.warp_tot[w++];
@@ -366,8 +349,8 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
               const int e = v0 + 2 * tid + u, i = min(e, end - 1);
               const Limbs y = weight<A>(make_float2(prob<DT>(P.p, pe + i), 0.f), make_float2(A != 0 ? prob<DT>(P.q, qe + i) : 0.f, 0.f), sc);
               x[u] = e < end ? whole(y.hi - kPairHi, y.lo - kPairLo) : 0ull;
-              if (A == 0 && removed)
-                for (int r = 0; r < s.n_rejected; ++r)
+              if (A == 0)
+                for (int r = 0; r < n_rej; ++r)
                   if (s.tok[s.rejected[r]] == e) x[u] = 0;
             }
             unsigned long long inc = x[0] + x[1];
@@ -393,8 +376,8 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
             __syncthreads();
           }
         };
-        if (!drafted || aa == 0.0) find(std::integral_constant<int, 0>());
-        else if (aa == 1.0) find(std::integral_constant<int, 1>());
+        if (!drafted || a == 0) find(std::integral_constant<int, 0>());
+        else if (a == kOne) find(std::integral_constant<int, 1>());
         else find(std::integral_constant<int, 2>());
       }
     } else if (rank == 0 && tid == 0) {
@@ -406,7 +389,6 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
     else static_cast<int32_t*>(P.next_token)[b] = -1;
   }
   if (rank == 0) {
-    const int n = s.n_path;
     for (int i = tid; i < P.T; i += kVerThreads) P.path[static_cast<int64_t>(b) * P.T + i] = i < n ? s.path[i] : -1;
     if (tid == 0) P.n_accepted[b] = n;
   }
