@@ -9,9 +9,10 @@
 // kernel joins them; with one split it writes O and LSE itself. Bound by the
 // fp32 FMA rate: a thread holds 4 x 4 scores and 8 x 4 outputs, so that shared
 // memory (8 and 12 16-byte reads, mostly broadcasts, for 64 and 128 FMAs) keeps
-// up; with half as many rows (2 x 4 and 4 x 4) it did not, 47 us against 37 (34 with packed FMAs) for
-// four trees of 13 nodes after up to 2001 tokens. The weights P take K's place
-// in shared memory once the scores are done, so that two CTAs fit on an SM.
+// up; with half as many rows (2 x 4 and 4 x 4) it did not, 47 us against 37 (34
+// with packed FMAs) for four trees of 13 nodes after up to 2001 tokens. The
+// weights P take K's place in shared memory once the scores are done, so that
+// two CTAs fit on an SM.
 #include <atomic>
 #include "st_kernels.h"
 #include "st_serve.h"

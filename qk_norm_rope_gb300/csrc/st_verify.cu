@@ -24,6 +24,13 @@
 // probabilities at once, walks redundantly (the same integers in every CTA),
 // owns a slice of V in the sums, and exchanges its slice's total through
 // distributed shared memory.
+//
+// 32 trees of 61 nodes over 131072 tokens in fp32 take 18 us: 7 for a walk without
+// rejections (launch, gather, one sum of p, the draw), 2 for a first rejection's
+// sum (a = 1), 5 for each further one and for the draw behind it; 16-bit
+// probabilities take as long. Instructions bound it (about 45 per two weights of
+// p - a q). What was slower: the next batch's loads ahead of a batch's sums, in
+// registers (spills, 26) or through shared memory (21); 512 threads (25).
 #include <type_traits>
 #include "st_kernels.h"
 #include "st_serve.h"
@@ -49,6 +56,24 @@ __device__ __forceinline__ float prob(const void* p, int64_t e) {
   else if constexpr (DT == kDtBF16) v = __bfloat162float(ld_now(static_cast<const __nv_bfloat16*>(p) + e));
   else v = __half2float(ld_now(static_cast<const __half*>(p) + e));
   return __saturatef(v);  // [0, 1]; NaN: 0
+}
+// Four neighbours that start on four elements, in one load.
+template <int DT>
+__device__ __forceinline__ void prob4(const void* p, int64_t e, float* v) {
+  if constexpr (DT == kDtF32) {
+    const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + e);
+    v[0] = __saturatef(x.x), v[1] = __saturatef(x.y), v[2] = __saturatef(x.z), v[3] = __saturatef(x.w);
+  } else {
+    const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + e);
+    const uint32_t w[2] = {x.x, x.y};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float2 y;
+      if constexpr (DT == kDtBF16) y = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+      else y = __half22float2(__halves2half2(__ushort_as_half(static_cast<unsigned short>(w[i])), __ushort_as_half(static_cast<unsigned short>(w[i] >> 16))));
+      v[2 * i] = __saturatef(y.x), v[2 * i + 1] = __saturatef(y.y);
+    }
+  }
 }
 // A value in [-1, 1] as two integer limbs of 21 and 22 bits, value =
 // (hi 2^22 + lo) 2^-43 rounded to nearest. Adding 1.5 * 2^(23 - b) leaves the
@@ -173,9 +198,18 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
   int parity = 0;
 
   // kRowBatch x 32 probabilities from v0 on, all loads in flight together; a
-  // whole batch takes constant offsets from one address
-  auto load_rows = [&](int64_t pe, int64_t qe, int v0, auto with_q, float (&pv)[kRowBatch], float (&qv)[kRowBatch]) {
+  // whole batch takes constant offsets from one address, and four tokens per
+  // load where its rows allow it (sums do not care which thread has which)
+  auto load_rows = [&](int64_t pe, int64_t qe, bool wide, int v0, auto with_q, float (&pv)[kRowBatch], float (&qv)[kRowBatch]) {
     constexpr bool Q = decltype(with_q)::value;
+    if (v0 + 32 * kRowBatch <= w_hi && wide) {
+#pragma unroll
+      for (int u = 0; u < kRowBatch; u += 4) {
+        prob4<DT>(P.p, pe + v0 + 4 * lane + 32 * u, pv + u);
+        if (Q) prob4<DT>(P.q, qe + v0 + 4 * lane + 32 * u, qv + u);
+      }
+      return;
+    }
     if (v0 + 32 * kRowBatch <= w_hi) {
 #pragma unroll
       for (int u = 0; u < kRowBatch; ++u) {
@@ -200,12 +234,14 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
   auto sum_row = [&](int cur, unsigned long long a, int removed, bool keep) -> unsigned long long {
     const int64_t pe = b * P.p_sb + cur * P.p_st, qe = b * P.q_sb + cur * P.q_st;
     unsigned long long acc = 0;
+    constexpr int kSize = DT == kDtF32 ? 4 : 2;
+    const bool wide = ((reinterpret_cast<uintptr_t>(P.p) + pe * kSize) | (drafted ? reinterpret_cast<uintptr_t>(P.q) + qe * kSize : 0)) % (4 * kSize) == 0;
     const Scale sc = split(a);
     auto pass = [&](auto kind) {
       constexpr int A = decltype(kind)::value;
       for (int v0 = w_lo; v0 < w_hi; v0 += 32 * kRowBatch) {
         float pv[kRowBatch], qv[kRowBatch];
-        load_rows(pe, qe, v0, std::integral_constant<bool, A != 0>(), pv, qv);
+        load_rows(pe, qe, wide, v0, std::integral_constant<bool, A != 0>(), pv, qv);
         uint32_t hi = 0, lo = 0;  // modulo 2^32: the sums of 16 limbs are far below it
 #pragma unroll
         for (int u = 0; u < kRowBatch; u += 2) {

@@ -460,6 +460,24 @@ def test_verify_borders(cuda_lib):
         assert torch.equal(g, w)
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+def test_verify_rows_of_any_alignment(cuda_lib, dtype):
+    """Rows that start on any element, and the same rows on 16 bytes: the same walk and the same token."""
+    B, T, V = 3, 9, 20001
+    target, draft, tokens, parents, ua, us = verify_case(B, T, V, 4, True, DT[dtype], seed=11)
+    for d in (draft, None):
+        want = R.verify(target, d, tokens, parents, ua, us)
+        for pad in (0, 1, 2, 7):
+            wide = torch.full((2, B, T, V + pad), 0.5, dtype=DT[dtype])
+            wide[0, :, :, :V], wide[1, :, :, :V] = target, draft
+            wide = wide.cuda()
+            got = cuda_lib.st_tree_verify(wide[0, :, :, :V], None if d is None else wide[1, :, :, :V], tokens.cuda(), parents.cuda(),
+                                          ua.cuda(), us.cuda())
+            for g, w in zip(got, want):
+                assert torch.equal(g.cpu(), w), pad
+    cuda_lib.st_check_status()
+
+
 def test_verify_bad_values(cuda_lib):
     target, draft, tokens, parents, ua, us = verify_case(3, 8, 50, 2, True, seed=21)
     tokens[0, 3], parents[1, 4], tokens[0, 0] = 50, 6, -9  # the root's token is not read
