@@ -28,8 +28,9 @@
 // 32 trees of 61 nodes over 131072 tokens in fp32 take 18 us: 7 for a walk without
 // rejections (launch, gather, one sum of p, the draw), 2 for a first rejection's
 // sum (a = 1), 5 for each further one and for the draw behind it; 16-bit
-// probabilities take as long. Instructions bound it (about 45 per two weights of
-// p - a q). What was slower: the next batch's loads ahead of a batch's sums, in
+// probabilities take as long. The busiest SMs issue half of the time (about 45
+// instructions for two weights of p - a q); the rest are waits for loads, the
+// cluster's barriers and the walk. What was slower: the next batch's loads ahead of a batch's sums, in
 // registers (spills, 26) or through shared memory (21); 512 threads (25).
 #include <type_traits>
 #include "st_kernels.h"
