@@ -3,17 +3,24 @@
 // fit (page sizes that are no multiple of 8).
 //
 // An item is kSimtRows query rows (token x head of the group) of one K/V head
-// of one sequence; its keys are walked in tiles of kSimtKeys and split over
-// p.splits CTAs, since a decoding step has few rows and many keys. Each CTA
-// leaves (O unnormalised, running maximum, sum) in the workspace and a second
-// kernel joins them; with one split it writes O and LSE itself. Bound by the
-// fp32 FMA rate: a thread holds 4 x 4 scores and 8 x 4 outputs, so that shared
-// memory (8 and 12 16-byte reads, mostly broadcasts, for 64 and 128 FMAs) keeps
-// up; with half as many rows (2 x 4 and 4 x 4) it did not, 47 us against 37 (34
-// with packed FMAs) for four trees of 13 nodes after up to 2001 tokens. The
+// of one sequence; its keys are walked in tiles of kSimtKeys. Few items are split
+// over the keys: the p.splits ranges that there are CTAs for are dealt to the
+// sequences by their lengths, which only the device knows (an equal number each
+// left the CTAs of short sequences idle). Each CTA leaves (O unnormalised,
+// running maximum, sum) in the workspace and a second kernel joins them; without
+// a split it writes O and LSE itself.
+//
+// Bound by the FMA rate and shared memory's: a thread holds 4 x 4 scores and
+// 8 x 4 outputs (8 and 12 16-byte reads for 64 and 128 FMAs); with half as many
+// rows (2 x 4 and 4 x 4) four trees of 13 nodes after up to 2001 tokens took 47 us
+// instead of 37, 34 with packed FMAs, 33 with ranges dealt by length. Those were
+// for uneven lengths: 8 single tokens after up to 4000 keys 58 -> 37 us, 30 after
+// up to 1000 116 -> 85 us. Long and even ones run at 58% of the FMA rate. The
 // weights P take K's place in shared memory once the scores are done, so that
 // two CTAs fit on an SM.
+#include <algorithm>
 #include <atomic>
+#include <type_traits>
 #include "st_kernels.h"
 #include "st_serve.h"
 
@@ -42,16 +49,59 @@ __device__ __forceinline__ bool tree_sees(const uint32_t* anc, int node) {
   return node < kMaxTree && ((anc[node >> 5] >> (node & 31)) & 1u);
 }
 
+// The ranges of sequence b's items, `n` from `first` on among the call's
+// p.splits: one, and a share of the others in proportion to the sequence's keys,
+// but none shorter than two units of kUnit keys (a token after 100 keys takes
+// 13.5 us so, 21 with four units, as a second tile costs more than a part).
+struct Ranges {
+  int b, first, n;
+};
+constexpr int kUnit = 16;
+constexpr int kMaxRanges = 128;  // of an item: the join goes through them
+// By a whole warp: the sequence that range y belongs to (b = -1: none), or, with
+// y < 0, the ranges of sequence b.
+__device__ Ranges find_ranges(const CacheAttnParams& p, int y, int b) {
+  const int lane = threadIdx.x & 31;
+  auto units = [&](int i) {
+    int prefix;
+    return i < p.B ? (key_count(p, i, row_count(p.counts, i, p.T), &prefix) + kUnit - 1) / kUnit : 0;
+  };
+  const int mine = units(lane);
+  long long all = mine;
+  for (int i = 32 + lane; i < p.B; i += 32) all += units(i);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) all += __shfl_xor_sync(0xffffffffu, all, x);
+  int first = 0;
+  for (int base = 0; base < p.B; base += 32) {
+    const int u = base == 0 ? mine : units(base + lane);
+    const int more = static_cast<int>(min(static_cast<long long>(p.splits - p.B) * u / max(all, 1ll), static_cast<long long>(kMaxRanges - 1)));
+    const int n = base + lane < p.B ? 1 + min(more, max(u / 2 - 1, 0)) : 0;
+    int upto = n;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, upto, x);
+      if (lane >= x) upto += t;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, y >= 0 ? y < first + upto : base + lane == b);
+    if (hit != 0) {
+      const int at = __ffs(hit) - 1, count = __shfl_sync(0xffffffffu, n, at);
+      return {base + at, first + __shfl_sync(0xffffffffu, upto, at) - count, count};
+    }
+    first += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return {-1, 0, 0};
+}
+
 __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant__ CacheAttnParams p, int n_rt) {
   extern __shared__ __align__(16) uint8_t raw[];
   Smem& s = *reinterpret_cast<Smem*>(raw);
   grid_dependency_wait();
   const int tid = threadIdx.x;
-  const int64_t item = blockIdx.x;
-  const int split = blockIdx.y;
-  const unsigned it32 = blockIdx.x;  // items are at most 2^30
+  const unsigned it32 = blockIdx.x;  // items are at most 2^30: of a sequence, or (no split) of all
   const int rt = static_cast<int>(it32 % n_rt), hk = static_cast<int>(it32 / n_rt % p.kv.Hkv);
-  const int b = static_cast<int>(it32 / n_rt / p.kv.Hkv);
+  const Ranges range = p.splits > 0 ? find_ranges(p, blockIdx.y, 0) : Ranges{static_cast<int>(it32 / n_rt / p.kv.Hkv), 0, 1};
+  const int b = range.b, split = blockIdx.y - range.first;
+  if (b < 0) return;  // short sequences need fewer ranges
   const int G = p.group;
   const int64_t rows = static_cast<int64_t>(p.T) * G;
   const int64_t row0 = static_cast<int64_t>(rt) * kR;
@@ -66,9 +116,10 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
   // the last key that any row of the item sees
   const int t_last = t0 + (g0 + n_here - 1) / G;
   const int end = p.parents ? keys : min(keys, prefix + min(t_last + 1, cnt));
-  const int n_tiles = t0 < cnt ? (end + kN - 1) / kN : 0;
-  const int j_lo = static_cast<int>(static_cast<int64_t>(n_tiles) * split / p.splits);
-  const int j_hi = static_cast<int>(static_cast<int64_t>(n_tiles) * (split + 1) / p.splits);
+  const int units = t0 < cnt ? (end + kUnit - 1) / kUnit : 0;
+  const int key_lo = static_cast<int>(static_cast<int64_t>(units) * split / range.n) * kUnit;
+  const int key_hi = static_cast<int>(static_cast<int64_t>(units) * (split + 1) / range.n) * kUnit;
+  const int n_tiles = (key_hi - key_lo + kN - 1) / kN;
 
   if (tid < kR && p.parents) {  // a walk up from the row's node; parents come before children
     for (int w = 0; w < kTreeWords; ++w) s.anc[tid][w] = 0;
@@ -97,11 +148,11 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
   const int rg = tid >> 5, dg = tid & 31;   // outputs: rows 8 rg + i; dims 4 dg..
   const bool f32 = p.kv.dt == kDtF32;
   auto locate = [&](int jt) {  // the rows of key tile jt
-    if (tid < kN && jt < j_hi) {
-      const int j = jt * kN + tid;
+    if (tid < kN && jt < n_tiles) {
+      const int j = key_lo + jt * kN + tid;
       int pg, prow;
       int64_t ko = -1, vo = -1;
-      if (j < keys) {
+      if (j < min(keys, key_hi)) {
         if (kv_locate(p.kv, b, j, &pg, &prow)) {
           ko = pg * p.kv.k_sp + prow * p.kv.k_sr + hk * p.kv.k_sh;
           vo = pg * p.kv.v_sp + prow * p.kv.v_sr + hk * p.kv.v_sh;
@@ -148,19 +199,19 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  locate(j_lo);
+  locate(0);
   if (tid < kR) {  // the offsets of the query rows, where the second tile's will be
     const int t = t0 + (g0 + tid) / G, h = hk * G + (g0 + tid) % G;
-    s.k_off[(j_lo + 1) & 1][tid] = tid < n_here && t < cnt ? b * p.q.sb + t * p.q.ss + h * p.q.sh : -1;
+    s.k_off[1][tid] = tid < n_here && t < cnt ? b * p.q.sb + t * p.q.ss + h * p.q.sh : -1;
   }
   __syncthreads();
-  if (j_lo < j_hi) {
-    fetch(p.q.p, s.k_off[(j_lo + 1) & 1], &s.q[0][0], kD);
-    fetch(p.kv.k, s.k_off[j_lo & 1], &s.k[0][0], kPad);
-    fetch(p.kv.v, s.v_off[j_lo & 1], &s.v[0][0], kD);
+  if (n_tiles > 0) {
+    fetch(p.q.p, s.k_off[1], &s.q[0][0], kD);
+    fetch(p.kv.k, s.k_off[0], &s.k[0][0], kPad);
+    fetch(p.kv.v, s.v_off[0], &s.v[0][0], kD);
   }
-  for (int jt = j_lo; jt < j_hi; ++jt) {
-    const int j0 = jt * kN;
+  for (int jt = 0; jt < n_tiles; ++jt) {
+    const int j0 = key_lo + jt * kN, n_units = min(kN, key_hi - j0) / kUnit;  // a range's last tile: only what it has
     asm volatile("cp.async.wait_group 1;" ::: "memory");  // Q and K
     __syncthreads();
     locate(jt + 1);
@@ -169,20 +220,27 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
     for (int w = 0; w < 4; ++w)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[w][i] = make_float2(0.f, 0.f);
+    auto scores = [&](auto count) {  // of the first kUnit * count keys
+      constexpr int N = decltype(count)::value;
 #pragma unroll 4
-    for (int d = 0; d < kD; d += 4) {
-      float4 qq[4], kk[4];
+      for (int d = 0; d < kD; d += 4) {
+        float4 qq[4], kk[N];
 #pragma unroll
-      for (int w = 0; w < 4; ++w) qq[w] = *reinterpret_cast<const float4*>(&s.q[tr + 16 * w][d]);
+        for (int w = 0; w < 4; ++w) qq[w] = *reinterpret_cast<const float4*>(&s.q[tr + 16 * w][d]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) kk[i] = *reinterpret_cast<const float4*>(&s.k[tc + 16 * i][d]);
+        for (int i = 0; i < N; ++i) kk[i] = *reinterpret_cast<const float4*>(&s.k[tc + 16 * i][d]);
 #pragma unroll
-      for (int w = 0; w < 4; ++w)
+        for (int w = 0; w < 4; ++w)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          acc[w][i] = __ffma2_rn(make_float2(qq[w].x, qq[w].y), make_float2(kk[i].x, kk[i].y),
-                                 __ffma2_rn(make_float2(qq[w].z, qq[w].w), make_float2(kk[i].z, kk[i].w), acc[w][i]));
-    }
+          for (int i = 0; i < N; ++i)
+            acc[w][i] = __ffma2_rn(make_float2(qq[w].x, qq[w].y), make_float2(kk[i].x, kk[i].y),
+                                   __ffma2_rn(make_float2(qq[w].z, qq[w].w), make_float2(kk[i].z, kk[i].w), acc[w][i]));
+      }
+    };
+    if (n_units == 4) scores(std::integral_constant<int, 4>());
+    else if (n_units == 3) scores(std::integral_constant<int, 3>());
+    else if (n_units == 2) scores(std::integral_constant<int, 2>());
+    else scores(std::integral_constant<int, 1>());
     __syncthreads();  // K is read: P takes its place
     const float sl = p.scale_log2;
     float sc[4][4];
@@ -190,14 +248,14 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
     for (int w = 0; w < 4; ++w)
 #pragma unroll
       for (int i = 0; i < 4; ++i) sc[w][i] = (acc[w][i].x + acc[w][i].y) * sl;
-    if (j0 + kN > prefix) {  // rows of padding see anything here: they are dropped at the end
+    if (j0 + kN > min(prefix, key_hi)) {  // rows of padding see anything here: they are dropped at the end
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         const int r = tr + 16 * w, t = t0 + (g0 + r) / G;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int j = j0 + tc + 16 * i, node = j - prefix;
-          const bool sees = j < keys && (node < 0 || (p.parents ? tree_sees(s.anc[r], node) : node <= t));
+          const bool sees = j < min(keys, key_hi) && (node < 0 || (p.parents ? tree_sees(s.anc[r], node) : node <= t));
           if (!sees) sc[w][i] = -INFINITY;
         }
       }
@@ -234,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
       o[i][1] = make_float2(o[i][1].x * corr, o[i][1].y * corr);
     }
 #pragma unroll 2
-    for (int k = 0; k < kN; k += 4) {
+    for (int k = 0; k < kUnit * n_units; k += 4) {
       float4 vv[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) vv[u] = *reinterpret_cast<const float4*>(&s.v[k + u][4 * dg]);
@@ -251,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
       }
     }
     __syncthreads();
-    if (jt + 1 < j_hi) {
+    if (jt + 1 < n_tiles) {
       fetch(p.kv.k, s.k_off[(jt + 1) & 1], &s.k[0][0], kPad);
       fetch(p.kv.v, s.v_off[(jt + 1) & 1], &s.v[0][0], kD);
     }
@@ -272,11 +330,11 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
   for (int i = 0; i < 8; ++i) {
     const int r = 8 * rg + i;
     if (r >= n_here) continue;
-    if (p.splits > 1) {
-      const int64_t slot = (item * p.splits + split) * kR + r;
+    if (p.splits > 0) {
+      const int64_t slot = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * kR + r;
       *reinterpret_cast<float4*>(p.part + slot * kD + 4 * dg) = make_float4(o[i][0].x, o[i][0].y, o[i][1].x, o[i][1].y);
       if (dg == 0) {
-        float2* ml = reinterpret_cast<float2*>(p.part + static_cast<int64_t>(gridDim.x) * p.splits * kR * kD);
+        float2* ml = reinterpret_cast<float2*>(p.part + static_cast<int64_t>(gridDim.x) * gridDim.y * kR * kD);
         ml[slot] = make_float2(s.m[r], s.l[r]);
       }
       continue;
@@ -293,38 +351,68 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
   }
 }
 
-// One warp per query row: the splits' parts, brought to their common maximum.
+// W warps per query row, 1 or 8: each brings every W-th range's part to their
+// common maximum, four in flight, and the first one the warps' results.
+template <int W>
 __global__ void __launch_bounds__(256) simt_join_kernel(const __grid_constant__ CacheAttnParams p, int n_rt, int64_t items) {
+  __shared__ float4 so[W][kD / 4];
+  __shared__ float2 sml[W];
   grid_dependency_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t w = (static_cast<int64_t>(blockIdx.x) * 8 + warp) / W;
   const int64_t item = w / kR;
-  const int r = static_cast<int>(w % kR);
-  if (item >= items) return;
+  const int r = static_cast<int>(w % kR), part0 = warp % W;
+  if (item >= items) return;  // with W = 8 these hold for the whole block
   const int rt = static_cast<int>(item % n_rt), hk = static_cast<int>(item / n_rt % p.kv.Hkv);
   const int b = static_cast<int>(item / n_rt / p.kv.Hkv);
   const int64_t row = static_cast<int64_t>(rt) * kR + r;
   if (row >= static_cast<int64_t>(p.T) * p.group) return;
-  const float2* ml = reinterpret_cast<const float2*>(p.part + items * p.splits * kR * kD);
-  const int64_t slot0 = item * p.splits * kR + r;
-  float m = -INFINITY;
-  for (int s = lane; s < p.splits; s += 32) m = fmaxf(m, ml[slot0 + static_cast<int64_t>(s) * kR].x);
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-  const float m_use = m == -INFINITY ? 0.f : m;
+  const Ranges range = find_ranges(p, -1, b);
+  const int64_t per_seq = static_cast<int64_t>(n_rt) * p.kv.Hkv, step = per_seq * kR;  // items; rows from a range to the next
+  const float2* ml = reinterpret_cast<const float2*>(p.part + per_seq * p.splits * kR * kD);
+  const int64_t slot0 = (range.first * per_seq + item % per_seq) * kR + r;
+  float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-#pragma unroll 4
-  for (int s = 0; s < p.splits; ++s) {
-    const int64_t slot = slot0 + static_cast<int64_t>(s) * kR;
-    const float2 x = ml[slot];
-    const float4 y = reinterpret_cast<const float4*>(p.part + slot * kD)[lane];
-    const float f = exp2f(x.x - m_use);
-    l = fmaf(f, x.y, l);
-    o.x = fmaf(f, y.x, o.x);
-    o.y = fmaf(f, y.y, o.y);
-    o.z = fmaf(f, y.z, o.z);
-    o.w = fmaf(f, y.w, o.w);
+  auto merge = [&](const float2 (&x)[4], const float4 (&y)[4]) {
+    const float top = fmaxf(fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x)), m), use = top == -INFINITY ? 0.f : top;
+    const float f0 = ex2(m - use);
+    m = top;
+    l *= f0;
+    o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float f = ex2(x[u].x - use);
+      l = fmaf(f, x[u].y, l);
+      o = make_float4(fmaf(f, y[u].x, o.x), fmaf(f, y[u].y, o.y), fmaf(f, y[u].z, o.z), fmaf(f, y[u].w, o.w));
+    }
+  };
+  for (int s0 = part0; s0 < range.n; s0 += 4 * W) {
+    float2 x[4];
+    float4 y[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = s0 + u * W;
+      const int64_t slot = slot0 + min(i, range.n - 1) * step;  // no branch around a load
+      x[u] = ml[slot];
+      y[u] = reinterpret_cast<const float4*>(p.part + slot * kD)[lane];
+      if (i >= range.n) x[u] = make_float2(-INFINITY, 0.f);
+    }
+    merge(x, y);
+  }
+  if constexpr (W > 1) {
+    so[warp][lane] = o;
+    if (lane == 0) sml[warp] = make_float2(m, l);
+    __syncthreads();
+    if (warp > 0) return;
+    m = -INFINITY;
+    l = 0.f;
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int s0 = 0; s0 < W; s0 += 4) {
+      const float2 x[4] = {sml[s0], sml[s0 + 1], sml[s0 + 2], sml[s0 + 3]};
+      const float4 y[4] = {so[s0][lane], so[s0 + 1][lane], so[s0 + 2][lane], so[s0 + 3][lane]};
+      merge(x, y);
+    }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int t = static_cast<int>(row / p.group), h = hk * p.group + static_cast<int>(row % p.group);
@@ -344,14 +432,18 @@ cudaError_t launch_cache_attn_simt(const CacheAttnParams& p, cudaStream_t stream
   cudaError_t e = opt_in_smem(simt_kernel, sizeof(Smem), configured);
   if (e != cudaSuccess) return e;
   const int n_rt = static_cast<int>((static_cast<int64_t>(p.T) * p.group + kR - 1) / kR);
-  return launch_chained(simt_kernel, dim3(static_cast<unsigned>(simt_items(p.B, p.T, p.H, p.kv.Hkv)), p.splits), dim3(kThreads),
-                        sizeof(Smem), stream, p, n_rt);
+  const int64_t items = simt_items(p.splits > 0 ? 1 : p.B, p.T, p.H, p.kv.Hkv);
+  return launch_chained(simt_kernel, dim3(static_cast<unsigned>(items), std::max(p.splits, 1)), dim3(kThreads), sizeof(Smem), stream, p, n_rt);
 }
 
 cudaError_t launch_cache_attn_simt_join(const CacheAttnParams& p, cudaStream_t stream) {
   const int n_rt = static_cast<int>((static_cast<int64_t>(p.T) * p.group + kR - 1) / kR);
   const int64_t items = simt_items(p.B, p.T, p.H, p.kv.Hkv);
-  return launch_chained(simt_join_kernel, dim3(static_cast<unsigned>((items * kR + 7) / 8)), dim3(256), 0, stream, p, n_rt, items);
+  // several warps a row where its parts are many: with one, 125 parts took 27 us
+  // more than one (10 us in all with eight)
+  const int warps = p.splits > 4 * p.B ? 8 : 1;
+  return launch_chained(warps == 8 ? simt_join_kernel<8> : simt_join_kernel<1>, dim3(static_cast<unsigned>((items * kR * warps + 7) / 8)),
+                        dim3(256), 0, stream, p, n_rt, items);
 }
 
 }  // namespace st

@@ -89,7 +89,7 @@ struct CacheAttnParams {
   float* lse;                      // [B, H, T]
   int B, T, H, group;
   float* part;                     // partial results (workspace)
-  int splits;                      // SIMT kernel: key ranges per item
+  int splits;                      // SIMT kernel: key ranges over all sequences (0: an item's keys stay together)
   unsigned* status;
   unsigned long long* counters;
   long long wait_budget;

@@ -191,9 +191,13 @@ st_status plan_attn(const st_tensor* q, const st_kv_cache* cache, const st_tenso
   const int64_t items = simt_items(p.B, p.T, p.H, p.kv.Hkv);
   if (items > (1ll << 30)) return fail(ST_ERR_SHAPE, "too many query rows");
   const int64_t tiles = (static_cast<int64_t>(p.kv.max_pages) * p.kv.page + kSimtKeys - 1) / kSimtKeys;
-  // enough key ranges for two CTAs per SM (what fits), none shorter than a tile
-  p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({2 * kSmCount / items, tiles, 128})));
-  if (p.splits > 1) P->bytes = static_cast<size_t>(items) * p.splits * kSimtRows * (kD + 2) * sizeof(float);
+  // few items: as many key ranges as give two CTAs per SM (what fits), dealt to
+  // the sequences by their lengths
+  if (2 * kSmCount / items >= 2 && tiles > 1) {
+    const int64_t per_seq = items / p.B;
+    p.splits = static_cast<int>(2 * kSmCount / per_seq);
+    P->bytes = static_cast<size_t>(per_seq) * p.splits * kSimtRows * (kD + 2) * sizeof(float);
+  }
   return ST_OK;
 }
 
@@ -345,7 +349,7 @@ st_status st_cache_attn(const st_tensor* q_rot, const st_kv_cache* cache, const 
   if ((st = cuda_check(launch_counted(ST_K_CACHE_ATTN, stream, [&] { return launch_cache_attn_simt(p, stream); }),
                        "cached attention launch")) != ST_OK)
     return st;
-  if (p.splits == 1) return ST_OK;
+  if (p.splits == 0) return ST_OK;
   return cuda_check(launch_counted(ST_K_CACHE_JOIN, stream, [&] { return launch_cache_attn_simt_join(p, stream); }),
                     "cached attention join launch");
 }

@@ -148,6 +148,10 @@ ATTN = [
     ("fp32", 1, 70, 2, 2, [5], None, 5, False),
     ("bf16", 2, 6, 8, 4, [100, 31], None, 7, True),                     # pages of 7 rows
     ("fp16", 1, 2, 2, 1, [40], None, 1, False),                         # pages of one row
+    ("fp32", 5, 1, 8, 2, [0, 3000, 17, 900, 64], [1, 1, 1, 1, 0], 7, False),   # key ranges dealt by length
+    ("fp32", 40, 2, 2, 1, [(37 * i * i) % 700 for i in range(40)], None, 16, True),
+    ("fp16", 36, 1, 4, 1, [5 * i for i in range(36)], [i % 2 for i in range(36)], 5, False),
+    ("fp32", 1, 1, 2, 2, [9000], None, 64, False),                      # as many ranges as an item may have
 ]
 
 
