@@ -305,7 +305,8 @@ typedef struct {
  *  q_rot:   [B, T, H, D] output in the cache's dtype: normalised, rotated q
  *           (zero in padding rows). It may be q itself when the dtypes match.
  * Rows whose position lies beyond the page table, or whose page number is not
- * in [0, N_pages), are not written. Padding rows write nothing. */
+ * in [0, N_pages), are not written; with lens[b] < 0 none of sequence b's are.
+ * Padding rows write nothing. */
 ST_API st_status st_cache_append(const st_tensor* q, const st_tensor* k, const st_tensor* v, const st_tensor* q_norm_w,
                                  const st_tensor* k_norm_w, float eps, const st_rope* rope, const st_kv_cache* cache,
                                  const st_tensor* lens, const st_tensor* counts, st_tensor* q_rot, void* stream);

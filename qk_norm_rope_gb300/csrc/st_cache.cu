@@ -113,7 +113,9 @@ __global__ void __launch_bounds__(kAppWarps * 32) append_kernel(const __grid_con
   bool room = true;
   auto find_slot = [&]() {
     int pg = 0, row = 0;
-    room = kv_locate(p.kv, b, static_cast<int64_t>(ld_now(p.lens + b)) + t, &pg, &row);
+    const int len = ld_now(p.lens + b);
+    // a negative length names no position, also where adding t would reach one
+    room = len >= 0 && kv_locate(p.kv, b, static_cast<int64_t>(len) + t, &pg, &row);
     if (!room && lane == 0) atomicOr(p.status, kStatusIndex);
     out = kind == 1 ? p.kv.k : p.kv.v;
     o_sh = kind == 1 ? p.kv.k_sh : p.kv.v_sh;

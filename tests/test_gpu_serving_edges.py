@@ -1,0 +1,39 @@
+"""Serving calls on the GPU at the edges of what they allow: values in device memory out of their range, statuses, and
+inputs that ask for more bits than ordinary ones."""
+import pytest
+import torch
+
+import _serving as R
+from test_gpu_serving import D, DT, bits, dev_cache, i32, rand
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_append_negative_length_writes_nothing(cuda_lib, dtype):
+    """No row of a sequence of negative length enters the cache, not even those whose lens[b] + t is a position; the
+    other sequences' rows do, q comes back for all, and the status says so."""
+    B, T, H, Hkv, page = 3, 6, 4, 2, 8
+    lens = [-1, 5, -4]
+    q, k, v = (rand(s, B, T, h, D, dtype=DT[dtype]) for s, h in ((1, H), (2, Hkv), (3, Hkv)))
+    kc, vc, pages = R.make_cache(B, [T, 5 + T, T], Hkv, page, DT[dtype], 4, fill=0.5)
+    cache = dev_cache(cuda_lib, kc, vc, pages)
+    w = torch.ones(D)
+    ids = torch.arange(T, dtype=torch.int32)[None, :, None].contiguous()
+    got = cuda_lib.st_cache_append(q.cuda(), k.cuda(), v.cuda(), w.cuda(), w.cuda(), 1e-6, ids.cuda(), (128,), 1e4, cache,
+                                   i32(lens).cuda())
+    with pytest.raises(cuda_lib.StError) as e:
+        cuda_lib.st_check_status()
+    assert e.value.status == cuda_lib.ST_ERR_INVALID_ARG
+    ang = R.angles(ids, (128,), 1e4)
+    yq, sq = R.rotate(q, w, ang, 1e-6)
+    yk, sk = R.rotate(k, w, ang, 1e-6)
+    # as the append's other tests: one rounding; angle, sincosf, rsqrt and five fp32 products below 2^-19 of the terms
+    tol = lambda y, s: R.HALF[DT[dtype]] * y.abs() + 2.0 ** -19 * s * (1 + R.HALF[DT[dtype]]) + 2.0 ** -25
+    R.close("q_rot", got, yq, tol(yq, sq))
+    pg, row = R.slots(pages, page, 1, 5 + torch.arange(T))
+    R.close("k", cache.k.cpu()[pg, row], yk[1], tol(yk, sk)[1])
+    assert torch.equal(cache.v.cpu()[pg, row], v[1])
+    k2, v2 = cache.k.cpu(), cache.v.cpu()
+    k2[pg, row], v2[pg, row] = kc[pg, row], vc[pg, row]
+    assert torch.equal(bits(k2), bits(kc)) and torch.equal(bits(v2), bits(vc))
