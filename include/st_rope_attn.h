@@ -407,8 +407,8 @@ ST_API st_status st_selftest_wait_timeout(long long budget_cycles, void* stream)
 /* Synchronises `stream` and reports ST_ERR_TIMEOUT if any kernel recorded a
  * bounded-wait timeout since the previous check (the record is then cleared),
  * ST_ERR_INVALID_ARG if a serving kernel met a value out of its range in device
- * memory (likewise), or ST_ERR_CUDA if the stream holds an error. For tests and
- * debugging. */
+ * memory (likewise; after a timeout the next check reports it), or ST_ERR_CUDA
+ * if the stream holds an error. For tests and debugging. */
 ST_API st_status st_check_status(void* stream);
 
 #ifdef __cplusplus

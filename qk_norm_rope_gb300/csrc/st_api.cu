@@ -1105,13 +1105,16 @@ st_status st_check_status(void* stream_) {
   if (st != ST_OK) return st;
   Dev dev;
   if ((st = device_globals(&dev)) != ST_OK) return st;
-  unsigned s = 0, z = 0;
+  unsigned s = 0;
   if ((st = cuda_check(cudaMemcpy(&s, dev.status, sizeof(s), cudaMemcpyDeviceToHost), "read status")) != ST_OK)
     return st;
-  if (s & (kStatusTimeout | kStatusLayout | kStatusIndex)) {
-    cudaMemcpy(dev.status, &z, sizeof(z), cudaMemcpyHostToDevice);
-    if (s & kStatusLayout) return fail(ST_ERR_CUDA, "a kernel found its shared memory misaligned and did nothing");
-    if (s & kStatusTimeout) return fail(ST_ERR_TIMEOUT, "a kernel's bounded wait ran out");
+  // one kind is reported and cleared, the gravest first; the next check reports the others
+  const unsigned bits = s & kStatusLayout ? kStatusLayout | kStatusTimeout : s & kStatusTimeout ? kStatusTimeout : s & kStatusIndex;
+  if (bits) {
+    s &= ~bits;
+    if ((st = cuda_check(cudaMemcpy(dev.status, &s, sizeof(s), cudaMemcpyHostToDevice), "clear status")) != ST_OK) return st;
+    if (bits & kStatusLayout) return fail(ST_ERR_CUDA, "a kernel found its shared memory misaligned and did nothing");
+    if (bits & kStatusTimeout) return fail(ST_ERR_TIMEOUT, "a kernel's bounded wait ran out");
     return fail(ST_ERR_INVALID_ARG,
                 "a serving kernel met a length, count, page, row, parent or token out of its range");
   }

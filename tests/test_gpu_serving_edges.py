@@ -37,3 +37,17 @@ def test_append_negative_length_writes_nothing(cuda_lib, dtype):
     k2, v2 = cache.k.cpu(), cache.v.cpu()
     k2[pg, row], v2[pg, row] = kc[pg, row], vc[pg, row]
     assert torch.equal(bits(k2), bits(kc)) and torch.equal(bits(v2), bits(vc))
+
+
+def test_status_reports_a_timeout_and_then_the_index(cuda_lib):
+    """A bounded wait that ran out does not hide a value out of range met in between: one check reports each."""
+    kc = torch.zeros(2, 8, 1, D, dtype=torch.bfloat16, device="cuda")
+    cache = cuda_lib.KVCache(kc, kc.clone(), i32([[0, 1]]).cuda())
+    cuda_lib.st_check_status()
+    cuda_lib.st_cache_keep(cache, i32([0]).cuda(), i32([[2, 1]]).cuda(), i32([2]).cuda())  # the second row does not ascend
+    cuda_lib.st_selftest_wait_timeout(2_000_000)
+    for want in (cuda_lib.ST_ERR_TIMEOUT, cuda_lib.ST_ERR_INVALID_ARG):
+        with pytest.raises(cuda_lib.StError) as e:
+            cuda_lib.st_check_status()
+        assert e.value.status == want
+    cuda_lib.st_check_status()
