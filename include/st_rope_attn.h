@@ -144,7 +144,8 @@ typedef struct {
   uint64_t kernel_launches;       /* kernels this library enqueued (host count) */
 } st_stats;
 
-/* Kernel kinds reported by st_timing_read. */
+/* Kernel kinds. st_timing_read reports those below ST_K_COUNT (the size of
+ * st_kernel_times is part of the ABI), st_timing_read_kinds all of them. */
 enum {
   ST_K_TABLE = 0,     /* rotary (cos, sin) table */
   ST_K_CLASSIFY = 1,  /* bool mask tile classification */
@@ -156,12 +157,13 @@ enum {
   ST_K_DW = 6,        /* norm-weight gradient reduction */
   ST_K_QPRIME = 7,    /* Q' rows for a backward without a forward's workspace */
   ST_K_PROBE = 8,     /* bounded-wait self-test */
+  ST_K_COUNT = 9,
   ST_K_CACHE_APPEND = 9,  /* st_cache_append */
   ST_K_CACHE_ATTN = 10,   /* st_cache_attn: attention over the cache */
   ST_K_CACHE_JOIN = 11,   /* st_cache_attn: joining the parts of split rows */
   ST_K_VERIFY = 12,       /* st_tree_verify */
   ST_K_CACHE_KEEP = 13,   /* st_cache_keep */
-  ST_K_COUNT = 14
+  ST_K_KINDS = 14
 };
 
 /* Per-kernel device time between two st_timing_read calls. */
@@ -396,6 +398,11 @@ ST_API void st_reset_stats(void);
  * starts a new accumulation. Off by default. */
 ST_API st_status st_timing_enable(int on);
 ST_API st_status st_timing_read(st_kernel_times* out);
+
+/* The same for the kernel kinds 0 .. n - 1, serving kernels included: launches
+ * and ms hold n entries each. Kinds from n on are dropped, and entries from
+ * ST_K_KINDS on are 0. */
+ST_API st_status st_timing_read_kinds(uint64_t* launches, double* ms, int n);
 
 /* Self-test of the bounded-wait mechanism: enqueues one tiny kernel that waits
  * on an mbarrier nothing arrives on and gives up after `budget_cycles`

@@ -91,7 +91,8 @@ KERNEL_KINDS = ["table", "classify", "fwd", "bwd_pre", "bwd", "dq_post", "dw_red
 
 
 class st_kernel_times(ctypes.Structure):
-    _fields_ = [("launches", ctypes.c_uint64 * len(KERNEL_KINDS)), ("ms", ctypes.c_double * len(KERNEL_KINDS))]
+    """What the C call st_timing_read fills: the kinds up to "probe"."""
+    _fields_ = [("launches", ctypes.c_uint64 * 9), ("ms", ctypes.c_double * 9)]
 
 
 class StError(RuntimeError):
@@ -138,6 +139,8 @@ def lib():
             L.st_timing_enable.restype = i
             L.st_timing_read.argtypes = [ctypes.POINTER(st_kernel_times)]
             L.st_timing_read.restype = i
+            L.st_timing_read_kinds.argtypes = [ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(ctypes.c_double), i]
+            L.st_timing_read_kinds.restype = i
             # the serving calls (their Python forms go through st_bind.so)
             L.st_cache_append.argtypes = [vp] * 5 + [fl] + [vp] * 6
             L.st_cache_append.restype = i
@@ -321,9 +324,10 @@ def st_timing_enable(on: bool) -> None:
 
 def st_timing_read() -> dict:
     """{kernel kind: (launches, total ms)} since the previous read (synchronises)."""
-    t = st_kernel_times()
-    _check(lib().st_timing_read(ctypes.byref(t)))
-    return {n: (int(t.launches[i]), float(t.ms[i])) for i, n in enumerate(KERNEL_KINDS)}
+    n = len(KERNEL_KINDS)
+    launches, ms = (ctypes.c_uint64 * n)(), (ctypes.c_double * n)()
+    _check(lib().st_timing_read_kinds(launches, ms, n))
+    return {k: (int(launches[i]), float(ms[i])) for i, k in enumerate(KERNEL_KINDS)}
 
 
 # ------------------------------------------------------------------ serving

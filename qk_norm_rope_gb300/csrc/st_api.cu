@@ -1062,7 +1062,15 @@ st_status st_timing_enable(int on) {
 
 st_status st_timing_read(st_kernel_times* out) {
   if (!out) return fail(ST_ERR_INVALID_ARG, "out is NULL");
-  memset(out, 0, sizeof(*out));
+  return st_timing_read_kinds(out->launches, out->ms, ST_K_COUNT);
+}
+
+st_status st_timing_read_kinds(uint64_t* launches, double* ms_out, int n) {
+  if (n < 0 || (n > 0 && (!launches || !ms_out))) return fail(ST_ERR_INVALID_ARG, "launches and ms must hold n >= 0 entries");
+  for (int i = 0; i < n; ++i) {
+    launches[i] = 0;
+    ms_out[i] = 0.0;
+  }
   std::vector<TimedLaunch> done;
   {
     std::lock_guard<std::mutex> lk(g_tmu);
@@ -1074,9 +1082,9 @@ st_status st_timing_read(st_kernel_times* out) {
     cudaError_t e = cudaEventSynchronize(t.b);
     if (e == cudaSuccess) e = cudaEventElapsedTime(&ms, t.a, t.b);
     if (e != cudaSuccess && st == ST_OK) st = fail(ST_ERR_CUDA, "event timing: %s", cudaGetErrorString(e));
-    if (t.kind >= 0 && t.kind < ST_K_COUNT) {
-      out->launches[t.kind] += 1;
-      out->ms[t.kind] += ms;
+    if (t.kind >= 0 && t.kind < n) {
+      launches[t.kind] += 1;
+      ms_out[t.kind] += ms;
     }
   }
   std::lock_guard<std::mutex> lk(g_tmu);

@@ -51,3 +51,24 @@ def test_status_reports_a_timeout_and_then_the_index(cuda_lib):
             cuda_lib.st_check_status()
         assert e.value.status == want
     cuda_lib.st_check_status()
+
+
+def test_timing_reports_the_serving_kernels(cuda_lib):
+    """The Python reader has every kind; the C struct's reader has the first nine and drops the others."""
+    import ctypes
+    kc = torch.zeros(2, 8, 1, D, dtype=torch.bfloat16, device="cuda")
+    cache = cuda_lib.KVCache(kc, kc.clone(), i32([[0, 1]]).cuda())
+    keep = lambda: cuda_lib.st_cache_keep(cache, i32([0]).cuda(), i32([[1, 2]]).cuda(), i32([2]).cuda())
+    keep()
+    cuda_lib.st_timing_enable(True)
+    try:
+        cuda_lib.st_timing_read()
+        keep()
+        got = cuda_lib.st_timing_read()
+        assert got["cache_keep"][0] == 1 and got["cache_keep"][1] > 0 and sum(n for n, _ in got.values()) == 1
+        keep()
+        t = cuda_lib.st_kernel_times()
+        assert cuda_lib.lib().st_timing_read(ctypes.byref(t)) == cuda_lib.ST_OK and list(t.launches) == [0] * 9
+        assert sum(n for n, _ in cuda_lib.st_timing_read().values()) == 0
+    finally:
+        cuda_lib.st_timing_enable(False)
