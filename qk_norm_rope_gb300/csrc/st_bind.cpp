@@ -225,7 +225,12 @@ PyObject* cache_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     size_t wn;
     if (a[10] == Py_None) {
       wn = st_cache_attn_workspace_size(q, &kv.c, par);
-      if (wn == 0) throw Refused(ST_ERR_INVALID_ARG, st_last_error());
+      // a size of 0: refused arguments, for which the call itself has the status (it
+      // plans first and needs no workspace to refuse)
+      if (wn == 0) {
+        check(st_cache_attn(q, &kv.c, lens, counts, par, scale, &o.s, &lse.s, nullptr, 0, nullptr));
+        throw Refused(ST_ERR_INVALID_ARG, "the workspace has no size");
+      }
       ws = new_tensor({static_cast<int64_t>(wn)}, at::kByte, c.dev);
       wp = ws.data_ptr();
     } else {

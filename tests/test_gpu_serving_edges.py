@@ -72,3 +72,29 @@ def test_timing_reports_the_serving_kernels(cuda_lib):
         assert sum(n for n, _ in cuda_lib.st_timing_read().values()) == 0
     finally:
         cuda_lib.st_timing_enable(False)
+
+
+def test_attention_refusals_keep_their_status_in_python(cuda_lib):
+    """What the C call refuses has the same status through Python, with the caller's workspace and without one."""
+    E = cuda_lib
+    z = lambda *s, dtype=torch.bfloat16: torch.zeros(*s, dtype=dtype, device="cuda")
+    lens = z(1, dtype=torch.int32)
+    cache = E.KVCache(z(2, 16, 2, D), z(2, 16, 2, D), z(1, 2, dtype=torch.int32))
+    par = lambda t: z(1, t, dtype=torch.int32)
+    cases = [
+        (E.ST_ERR_UNSUPPORTED, "256", z(1, 257, 2, D), cache, par(257)),
+        (E.ST_ERR_UNSUPPORTED, "D=128", z(1, 1, 2, 64), cache, None),
+        (E.ST_ERR_UNSUPPORTED, "query heads", z(1, 1, 258, D), cache, None),
+        (E.ST_ERR_DTYPE, "q_rot", z(1, 1, 2, D, dtype=torch.float16), cache, None),
+        (E.ST_ERR_DTYPE, "parents", z(1, 3, 2, D), cache, par(3).long()),
+        (E.ST_ERR_SHAPE, "divide", z(1, 1, 3, D), cache, None),
+        (E.ST_ERR_SHAPE, "parents", z(1, 3, 2, D), cache, par(4)),
+        (E.ST_ERR_ALIGN, "unit stride", z(1, 1, 2, 2 * D)[..., ::2], cache, None),
+        (E.ST_ERR_ALIGN, "expanded", z(1, 1, 2, D), E.KVCache(cache.k[:1].expand(2, -1, -1, -1), cache.v, cache.pages), None),
+    ]
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    for status, text, q, c, parents in cases:
+        for w in (None, ws):
+            with pytest.raises(E.StError, match=text) as e:
+                E.st_cache_attn(q, c, lens, parents=parents, workspace=w)
+            assert e.value.status == status, (text, w is None, e.value.status)
