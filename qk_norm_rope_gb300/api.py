@@ -141,7 +141,7 @@ def lib():
             L.st_timing_read.restype = i
             L.st_timing_read_kinds.argtypes = [ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(ctypes.c_double), i]
             L.st_timing_read_kinds.restype = i
-            # the serving calls (their Python forms go through st_bind.so)
+            # the serving calls (their Python forms go through st_bind.cpp)
             L.st_cache_append.argtypes = [vp] * 5 + [fl] + [vp] * 6
             L.st_cache_append.restype = i
             L.st_cache_attn_workspace_size.argtypes = [vp, vp, vp]
@@ -332,7 +332,7 @@ def st_timing_read() -> dict:
 
 # ------------------------------------------------------------------ serving
 # A decoding step makes these calls for every layer on small tensors, so that
-# the host's share counts: they go through st_bind.so (C++) instead of ctypes.
+# the host's share counts: they go through st_bind.cpp instead of ctypes.
 _bind_mod = None
 
 

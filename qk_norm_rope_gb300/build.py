@@ -1,5 +1,5 @@
 """Builds libst_rope_attn.so in-tree with nvcc for sm_103a (GB300), and
-st_bind.so, the Python binding of the serving calls, with g++ against torch.
+st_bind.*.so, the Python binding of the serving calls, with g++ against torch.
 
 The translation units compile in parallel; the shared objects land in
 ``qk_norm_rope_gb300/_build/``. Rebuilds only when a source is newer than the
@@ -19,7 +19,6 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libst_rope_attn.so")
 BIND_SRC = os.path.join(CSRC, "st_bind.cpp")
-BIND = os.path.join(OUT, "st_bind.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -73,13 +72,22 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
+def _bind_name() -> str:
+    """Path without suffix of the binding's object and library: the torch and the Python (version and machine) whose
+    headers it is compiled against are in it, as neither takes what another's layouts were compiled into."""
+    import sysconfig
+
+    import torch
+    return os.path.join(OUT, f"st_bind.{torch.__version__}.{sysconfig.get_config_var('SOABI')}")
+
+
 def _bind_object() -> str:
-    """Compiles st_bind.cpp against the installed torch; the object's name carries torch's version."""
+    """Compiles st_bind.cpp against the running Python and the installed torch."""
     import sysconfig
 
     import torch
     t = os.path.dirname(os.path.abspath(torch.__file__))
-    obj = os.path.join(OUT, f"st_bind.{torch.__version__}.o")
+    obj = _bind_name() + ".o"
     head = os.path.join(ROOT, "include", "st_rope_attn.h")
     if os.path.exists(obj) and os.path.getmtime(obj) >= max(os.path.getmtime(BIND_SRC), os.path.getmtime(head)):
         return obj
@@ -100,17 +108,18 @@ def build_bind(obj: str | None = None) -> str:
     import torch
     build_lib = build()
     obj = obj or _bind_object()
-    if os.path.exists(BIND) and os.path.getmtime(BIND) >= os.path.getmtime(obj):
-        return BIND
+    so = _bind_name() + ".so"
+    if os.path.exists(so) and os.path.getmtime(so) >= os.path.getmtime(obj):
+        return so
     t = os.path.join(os.path.dirname(os.path.abspath(torch.__file__)), "lib")
-    tmp = BIND + f".{os.getpid()}.tmp"
+    tmp = so + f".{os.getpid()}.tmp"
     cmd = ["g++", "-shared", obj, "-o", tmp, f"-L{t}", "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10", "-lc10_cuda",
            f"-L{os.path.dirname(build_lib)}", "-l:libst_rope_attn.so", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{t}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed for st_bind.so:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BIND)
-    return BIND
+    os.replace(tmp, so)
+    return so
 
 
 def build_all(force: bool = False, verbose: bool = False) -> None:
