@@ -42,6 +42,12 @@ constexpr int kTcWarps = 16, kTcThreads = kTcWarps * 32;
 // Registers per thread: the softmax threads hold a row of 128 scores. 256 * 184 + 256 * 72 = 512 * 128.
 constexpr int kRegsSoft = 184, kRegsRest = 72;
 constexpr float kRescale = 8.0f;  // O is rescaled when the running maximum grows by more than this (base 2)
+// How far the reference stays below the running maximum (base 2). fp16 weights
+// end at 2^-25 of 1, and a long row's many small ones would leave PV but stay in
+// the sum; with the maximum's at 2^7, at most 2^15 while the reference lags,
+// they end 2^-32 below it. bf16 has fp32's range.
+template <bool F16>
+constexpr float kLift = F16 ? 7.0f : 0.0f;
 
 template <int NT>
 struct Lay {  // shared memory, offsets from a 1024-byte aligned base
@@ -301,7 +307,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float sc,
       m1 = fmax3(m1, __uint_as_float(x[i][t + 2]), __uint_as_float(x[i][t + 3]));
     }
   }
-  const float mt = fmaxf(m0, m1) * sc;
+  const float mt = fmaf(fmaxf(m0, m1), sc, -kLift<F16>);
   float corr = 1.f;
   if (mt > m_run + kRescale || (m_run == -INFINITY && mt > -INFINITY)) {
     corr = ex2(m_run - mt);  // 0 when m_run is -inf

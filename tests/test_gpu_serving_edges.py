@@ -98,3 +98,33 @@ def test_attention_refusals_keep_their_status_in_python(cuda_lib):
             with pytest.raises(E.StError, match=text) as e:
                 E.st_cache_attn(q, c, lens, parents=parents, workspace=w)
             assert e.value.status == status, (text, w is None, e.value.status)
+
+
+def test_fp16_attention_keeps_a_long_tail(cuda_lib):
+    """One key far ahead of 41000 others: together they still weigh what they should. Sequences share their pages, so
+    that each has a CTA or two of its own for its whole length."""
+    n, B, page = 41000, 160, 40
+    g = torch.Generator().manual_seed(5)
+    k = torch.zeros(n // page + 1, page, 1, D, dtype=torch.float16)
+    v = (1 + 0.25 * torch.rand(n // page + 1, page, 1, D, generator=g)).to(torch.float16)
+    k[0, 0, 0, 0] = 1
+    v[0, 0] = 0
+    ahead = torch.tensor([22.0, 24.0, 25.0, 25.5, 26.0, 28.0, 31.0, 33.0])  # in bits, exact in fp16
+    q = torch.zeros(B, 1, 1, D, dtype=torch.float16)
+    q[:, 0, 0, 0] = ahead.repeat(B // 8).half()
+    pages = torch.arange(n // page + 1, dtype=torch.int32).expand(B, -1).contiguous()
+    cache = dev_cache(cuda_lib, k, v, pages)
+    ln2 = 0.6931471805599453
+    o, lse = cuda_lib.st_cache_attn(q.cuda(), cache, torch.full((B,), n - 1, dtype=torch.int32).cuda(), scale=ln2)
+    cuda_lib.st_check_status()
+    vv = v.reshape(-1, D)[:n].double()
+    w = 2.0 ** -ahead.double()[:, None]
+    total = 1 + w * (n - 1)
+    want = (w * vv.sum(0) / total).repeat(B // 8, 1)[:, None, None]
+    # of the sum's terms: half a step of a weight, the scores' fp32 rounding (33 bits: 2^-18 together with ex2), the sums;
+    # weights below fp16's range, 2^-25 where the largest is 2^7; the output's half step
+    size = want.abs()
+    bound = size * (2.0 ** -11 + 2 * 2.0 ** -18 + 2 * (n + 64) * 2.0 ** -24) + n * 2.0 ** -32 * vv.max() + 2.0 ** -11 * size + 2.0 ** -25
+    R.close("o", o, want, bound)
+    want_lse = (ahead.double() * ln2 + total[:, 0].log()).repeat(B // 8)[:, None, None]
+    R.close("lse", lse, want_lse, 2.0 ** -18 + (n + 64) * 2.0 ** -24 + 2.0 ** -22 * (1 + want_lse.abs()))
