@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import _serving as R
-from test_gpu_serving import D, DT, bits, dev_cache, i32, rand
+from test_gpu_serving import D, DT, Loop, bits, dev_cache, i32, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -128,3 +128,50 @@ def test_fp16_attention_keeps_a_long_tail(cuda_lib):
     R.close("o", o, want, bound)
     want_lse = (ahead.double() * ln2 + total[:, 0].log()).repeat(B // 8)[:, None, None]
     R.close("lse", lse, want_lse, 2.0 ** -18 + (n + 64) * 2.0 ** -24 + 2.0 ** -22 * (1 + want_lse.abs()))
+
+
+@pytest.mark.parametrize("dtype,H,Hkv,page", [("bf16", 8, 2, 16), ("fp16", 3, 1, 24), ("fp32", 4, 4, 10), ("bf16", 6, 2, 7), ("fp16", 32, 8, 8)])
+def test_decoding_loop_step_by_step(cuda_lib, dtype, H, Hkv, page):
+    """A decoding loop in which every call is held to its own bound: q' and the new rows of the cache to one rounding of
+    the exact ones, and the attention to the 64-bit form on the very q' and cache that it was given."""
+    B, T = 3, 10
+    L = Loop(cuda_lib, dtype, B, T, H, Hkv, page, [0, 37, 250], 3, 40, seed=2000)
+    cache = dev_cache(cuda_lib, L.k, L.v, L.pages)
+    lens = i32(L.lens0).cuda()
+    half = R.HALF[L.dt]
+    tol = lambda y, s: half * y.abs() + 2.0 ** -19 * s * (1 + half) + 2.0 ** -25  # as the append's own tests
+    for c, d in zip(L.steps, L.to_dev()):
+        before = lens.tolist()
+        k0, v0 = cache.k.cpu(), cache.v.cpu()
+        ids = (lens[:, None] + d["depth"])[..., None]
+        q = cuda_lib.st_cache_append(d["q"], d["k"], d["v"], L.wq_, L.wk_, 1e-6, ids, (128,), 1e4, cache, lens)
+        k1, v1 = cache.k.cpu(), cache.v.cpu()
+        o, lse = cuda_lib.st_cache_attn(q, cache, lens, parents=d["parents"])
+        path, n, nxt = cuda_lib.st_tree_verify(d["target"], d["draft"], d["tokens"], d["parents"], d["ua"], d["us"])
+        new = cuda_lib.st_cache_keep(cache, lens, path, n)
+        cuda_lib.st_check_status()
+
+        ang = R.angles(ids.cpu(), (128,), 1e4)
+        yq, sq = R.rotate(c["q"], L.wq, ang, 1e-6)
+        yk, sk = R.rotate(c["k"], L.wk, ang, 1e-6)
+        R.close("q_rot", q, yq, tol(yq, sq))
+        want_k, tol_k, want_v = k0.double(), torch.zeros(k0.shape, dtype=torch.float64), v0.clone()
+        for b in range(B):
+            pg, row = R.slots(L.pages, page, b, before[b] + torch.arange(T))
+            want_k[pg, row], tol_k[pg, row], want_v[pg, row] = yk[b], tol(yk, sk)[b], c["v"][b]
+        R.close("cache.k", k1, want_k, tol_k)
+        assert torch.equal(bits(v1), bits(want_v))
+        ro, rl, bo, bl = R.attention(q.cpu(), k1, v1, L.pages, before, None, c["parents"])
+        R.close("o", o, ro, bo)
+        R.close("lse", lse, rl, bl)
+        for got, want in zip((path, n, nxt), R.verify(c["target"], c["draft"], c["tokens"], c["parents"], c["ua"], c["us"])):
+            assert torch.equal(got.cpu(), want)
+        for b in range(B):  # the accepted rows moved, everything else kept its bits
+            keep = path[b, : n[b]].long().cpu()
+            spg, srow = R.slots(L.pages, page, b, before[b] + keep)
+            dpg, drow = R.slots(L.pages, page, b, before[b] + torch.arange(keep.numel()))
+            moved_k, moved_v = k1[spg, srow].clone(), v1[spg, srow].clone()
+            k1[dpg, drow], v1[dpg, drow] = moved_k, moved_v
+        assert torch.equal(bits(cache.k), bits(k1)) and torch.equal(bits(cache.v), bits(v1))
+        assert new.tolist() == [x + y for x, y in zip(before, n.tolist())]
+        lens = new

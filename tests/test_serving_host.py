@@ -62,3 +62,38 @@ def test_binding_is_kept_apart_by_torch_and_python(monkeypatch, tmp_path):
         monkeypatch.setattr(torch, "__version__", torch_version)
         for _ in range(2):
             assert open(build.build_bind()).read() == f"{torch_version} {abi}"
+
+
+@pytest.mark.parametrize("mistake", ["chain", "no self", "zero"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_attention_bound_finds_planted_mistakes(dtype, mistake):
+    """The bound that cached attention is held to is far below what a wrong mask or a missing result changes."""
+    import torch
+
+    import _serving as R
+    dt = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}[dtype]
+    B, T, H, Hkv, page, lens = 3, 10, 4, 2, 16, [0, 37, 250]
+    full = [n + T for n in lens]
+    k, v, pages = R.make_cache(B, full, Hkv, page, dt, 1, fill=0.0)
+    R.fill_prefix(k, v, pages, full, 2)
+    q = torch.randn(B, T, H, 128, generator=torch.Generator().manual_seed(3)).to(dt)
+    parents = R.tree(B, T, 3, 4)
+    o, _, bound, _ = R.attention(q, k, v, pages, lens, None, parents)
+    if mistake == "chain":
+        wrong = R.attention(q, k, v, pages, lens, None, None)[0]
+    elif mistake == "zero":
+        wrong = torch.zeros_like(o)
+    else:  # the last node's own key taken from another row
+        k2 = k.clone()
+        for b in range(B):
+            pg, row = R.slots(pages, page, b, torch.tensor([lens[b] + T - 1, lens[b]]))
+            k2[pg[0], row[0]] = k[pg[1], row[1]]
+        wrong = R.attention(q, k2, v, pages, lens, None, parents)[0]
+    changed = (wrong - o).abs() > 0
+    assert changed.any()
+    # The last node's own key is one of up to 260 of its row, so that its weight moves outputs by 0.4%, the size of the
+    # bf16 bound: some elements have to be found. The others change whole rows: most have to be.
+    share = 0.0 if mistake == "no self" else 0.5
+    for b in range(B):
+        found = ((wrong[b] - o[b]).abs() > bound[b])[changed[b]]
+        assert found.double().mean() > share, (b, float(found.double().mean()))
