@@ -360,7 +360,9 @@ ST_API st_status st_cache_attn(const st_tensor* q_rot, const st_kv_cache* cache,
  * Without draft_probs q(x) = 1 and a rejection removes x: w(x) = 0, C_{k+1} =
  * C_k - p(x). At the end the next token is the first v whose running sum of w
  * exceeds u_sample * sum w (of p when w is zero everywhere, -1 when p is too).
- * Weights are rounded to multiples of 2^-43 for the sums, which are exact.
+ * Weights are rounded for the sums, which are exact: to multiples of 2^-43, or,
+ * where a node's sum to less than 2^-12 (a draft close to its target), to
+ * multiples of 2^-34 of the sum or less.
  *  path:    [B, T] int32, contiguous: the accepted nodes from the root on, then
  *           -1. n_accepted: [B] int32 (the root included; 0 where counts is 0).
  *  next_token: [B], the dtype of tokens.

@@ -17,7 +17,11 @@
 // Weights are held as integers, 2^-43 a unit (rounded to nearest), and summed
 // in integer arithmetic: sums do not depend on their order, so a row may be
 // split over any number of threads and CTAs and the drawn token is the same. A
-// running sum over 2^17 tokens is off by about 2^-37 of the total.
+// running sum over V tokens is off by V 2^-44 at most, by about 2^-36 over 2^17
+// tokens, whose roundings are independent. What is left of a row whose draft is
+// close to its target sums to far less than 1, and loses its small weights in
+// that unit: after a sum below 2^-12 (finish_small) the rest of the sequence is
+// done with weights in fp64 and a unit that goes by the sum.
 //
 // The walk is latency, the residual sums and the draw read two rows of V. One
 // cluster of CTAs serves a sequence: each CTA gathers every node's two
@@ -162,6 +166,143 @@ struct VerState {
   int rejected[kMaxVerify];      // of the node where the walk ended, without draft probabilities
 };
 
+// The tokens of a warp's slice of V, rounded up to whole rows of 32.
+__device__ __forceinline__ int slice_of(int V, int C) { return ((V + C * kVerWarps - 1) / (C * kVerWarps) + 31) & ~31; }
+// The next child of `cur` behind node `from`, or cnt; by a whole warp.
+__device__ __forceinline__ int next_child(const VerState& s, int cur, int from, int cnt) {
+  const int lane = threadIdx.x & 31;
+  for (int base = from + 1; base < cnt; base += 32) {
+    const int i = base + lane;
+    const unsigned m = __ballot_sync(0xffffffffu, i < cnt && s.par[i] == cur);
+    if (m) return base + __ffs(m) - 1;
+  }
+  return cnt;
+}
+// floor(u_sample * total): the draw takes the first token whose running sum is above it.
+__device__ __forceinline__ unsigned long long draw_at(const VerifyParams& P, int b, unsigned long long total) {
+  const float us = fminf(fmaxf(ld_now(P.u_sample + b), 0.f), 1.f);
+  // u in 2^-64 units (below 1), so that the result is below total
+  const unsigned long long u64 = us >= 1.f ? ~0ull : __double2ull_rz(static_cast<double>(us) * 18446744073709551616.0);
+  return __umul64hi(u64, total);
+}
+__device__ __forceinline__ void put_token(const VerifyParams& P, int b, int token) {
+  if (P.tok64) static_cast<long long*>(P.next_token)[b] = token;
+  else static_cast<int32_t*>(P.next_token)[b] = token;
+}
+
+// ------------------------------------------------------ residuals of small sums
+// The rest of a sequence's walk and its draw once a residual has summed to less
+// than kSmall units: weights by one fp64 product and sum each, in the unit
+// 2^-(43 + shift), with shift raised until the sum has kEnough units or nothing is
+// left. A step leaves room for what was rounded off before: (2^34 + V / 2) 2^25 <
+// 2^60 for V <= 2^30. Residuals only shrink from one rejection to the next, so a
+// node's shift stays good. A function of its own and plain code, as few sequences
+// need it; built into the ordinary passes it cost all of them 6 to 8%.
+constexpr unsigned long long kSmall = 1ull << 31, kEnough = 1ull << 34;
+constexpr int kShiftStep = 25, kShiftMost = 125;  // to 2^-168: fp32's smallest number is 2^-149
+constexpr unsigned long long kAnyLeft = 1ull << 60;  // in a CTA's total: it has weights above 0
+
+// From the child i of node `cur` on (cnt: none is left), `n` nodes being accepted,
+// at `a` with n_rej removed tokens; `parity`: of the next exchange. Returns the accepted nodes and writes the token.
+template <int DT>
+__device__ __noinline__ int finish_small(const VerifyParams& P, VerState& s, int b, int rank, int cnt, int cur, int i, int n, int n_rej,
+                                         unsigned long long a_units, int parity) {
+  const int C = P.cluster, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, V = P.V, sub = slice_of(V, C);
+  const bool drafted = P.q != nullptr;
+  double a = static_cast<double>(a_units) * kUnit, c = 1.0;
+  int shift = kShiftStep;
+  auto weight = [&](int64_t pe, int64_t qe, int v) {
+    const double p = prob<DT>(P.p, pe + v);
+    double w = drafted && a != 0.0 ? fma(-a, static_cast<double>(prob<DT>(P.q, qe + v)), p) : p;
+    for (int r = 0; r < n_rej; ++r)
+      if (s.tok[s.rejected[r]] == v) w = 0.0;
+    return w;
+  };
+  auto units = [&](double w) { return static_cast<unsigned long long>(__double2ll_rn(scalbn(fmax(w, 0.0), 43 + shift))); };
+  // the sum over the row of node `cur`; the warps' totals stay in s.warp_tot, the CTAs' in s.cta_tot[parity ^ 1]
+  auto sum_row = [&]() -> unsigned long long {
+    const int64_t pe = b * P.p_sb + cur * P.p_st, qe = b * P.q_sb + cur * P.q_st, lo = static_cast<int64_t>(rank * kVerWarps + warp) * sub;
+    while (true) {
+      unsigned long long acc = 0;
+      bool any = false;
+      for (int64_t v = lo + lane; v < min(lo + sub, static_cast<int64_t>(V)); v += 32) {
+        const double w = weight(pe, qe, static_cast<int>(v));
+        any |= w > 0.0;
+        acc += units(w);
+      }
+      acc = warp_sum(acc);
+      if (lane == 0) s.warp_tot[warp] = acc;
+      any = __syncthreads_or(any) != 0;
+      unsigned long long cta = any ? kAnyLeft : 0;
+      for (int w = 0; w < kVerWarps; ++w) cta += s.warp_tot[w];
+      if (C == 1) {
+        if (tid == 0) s.cta_tot[parity][0] = cta;
+        __syncthreads();
+      } else {
+        if (tid < C) st_cluster_u64(mapa_shared(smem_u32(&s.cta_tot[parity][rank]), tid), cta);
+        cluster_sync();
+      }
+      unsigned long long total = 0;
+      for (int r = 0; r < C; ++r) total += s.cta_tot[parity][r];
+      const bool left = total >= kAnyLeft;
+      total &= kAnyLeft - 1;
+      parity ^= 1;
+      if (total >= kEnough || !left || shift >= kShiftMost) return total;
+      shift += kShiftStep;
+    }
+  };
+  if (i < cnt) c = scalbn(static_cast<double>(sum_row()), -43 - shift);  // only with draft probabilities
+  while (i < cnt) {
+    const double px = s.pp[i], qx = s.qq[i];
+    const bool yes = static_cast<double>(s.uu[i]) * qx * c < fmax(fma(-a, qx, px), 0.0);
+    const int last = i;
+    if (yes) {
+      if (tid == 0) s.path[n] = i;
+      cur = i;
+      ++n;
+      a = 0.0;
+      c = 1.0;
+      shift = 0;
+    } else {
+      a += c;
+    }
+    i = next_child(s, cur, last, cnt);
+    if (!yes && i < cnt) c = scalbn(static_cast<double>(sum_row()), -43 - shift);
+  }
+  unsigned long long total = sum_row();
+  if (total == 0) {  // p <= a q everywhere: the target's own distribution
+    a = 0.0;
+    shift = 0;
+    n_rej = 0;
+    total = sum_row();
+  }
+  if (total == 0) {
+    if (rank == 0 && tid == 0) put_token(P, b, -1);
+    return n;
+  }
+  const unsigned long long thr = draw_at(P, b, total);
+  unsigned long long run = 0;
+  for (int r = 0; r < rank; ++r) run += s.cta_tot[parity ^ 1][r] & (kAnyLeft - 1);
+  for (int w = 0; w < warp; ++w) run += s.warp_tot[w];
+  if (thr < run || thr >= run + s.warp_tot[warp]) return n;
+  // one warp of the cluster: 32 tokens at a time
+  const int64_t pe = b * P.p_sb + cur * P.p_st, qe = b * P.q_sb + cur * P.q_st, lo = static_cast<int64_t>(rank * kVerWarps + warp) * sub;
+  const int end = static_cast<int>(min(lo + sub, static_cast<int64_t>(V)));
+  for (int v0 = static_cast<int>(lo); v0 < end; v0 += 32) {
+    const unsigned long long x = v0 + lane < end ? units(weight(pe, qe, v0 + lane)) : 0ull;
+    unsigned long long inc = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long t = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += t;
+    }
+    if (thr >= run + inc - x && thr < run + inc) put_token(P, b, v0 + lane);  // one thread
+    run += __shfl_sync(0xffffffffu, inc, 31);
+    if (thr < run) break;
+  }
+  return n;
+}
+
 template <int DT>
 __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_constant__ VerifyParams P) {
   __shared__ VerState s;
@@ -193,7 +334,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
   else __syncthreads();
 
   // slice of V of this CTA, and of each warp of it
-  const int sub = ((V + C * kVerWarps - 1) / (C * kVerWarps) + 31) & ~31;
+  const int sub = slice_of(V, C);
   const int64_t lo64 = static_cast<int64_t>(rank * kVerWarps + warp) * sub;
   const int w_lo = static_cast<int>(min(lo64, static_cast<int64_t>(V))), w_hi = static_cast<int>(min(lo64 + sub, static_cast<int64_t>(V)));
   int parity = 0;
@@ -298,22 +439,15 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
   int cur = 0, n = cnt > 0 ? 1 : 0, n_rej = 0;
   unsigned long long a = 0, c = kOne;  // a and C, in 2^-43
   double left = 1.0;                   // C without draft probabilities
-  // the next child of `cur` behind node `from`, or cnt
-  auto next_child = [&](int from) {
-    for (int base = from + 1; base < cnt; base += 32) {
-      const int i = base + lane;
-      const unsigned m = __ballot_sync(0xffffffffu, i < cnt && s.par[i] == cur);
-      if (m) return base + __ffs(m) - 1;
-    }
-    return cnt;
-  };
   // a child of `cur` before node i has i's token
   auto tried = [&](int i) {
     bool again = false;
     for (int base = 0; base < i; base += 32) again |= base + lane < i && s.par[base + lane] == cur && s.tok[base + lane] == s.tok[i];
     return __any_sync(0xffffffffu, again) != 0;
   };
-  for (int i = next_child(0); i < cnt;) {
+  bool small = false;                  // a residual's sum was too small for the unit
+  int i = next_child(s, cur, 0, cnt);
+  while (i < cnt) {
     const float u = s.uu[i], px = s.pp[i], qx = s.qq[i];
     const bool again = !drafted && n_rej > 0 && tried(i);  // a token that was already removed here
     bool yes;
@@ -330,15 +464,16 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
       c = kOne;
       left = 1.0;
       n_rej = 0;
-      i = next_child(last);
+      i = next_child(s, cur, last, cnt);
       continue;
     }
-    i = next_child(last);
+    i = next_child(s, cur, last, cnt);
     if (drafted) {
       a += c;
       if (i < cnt) {  // the next sibling needs the residual's sum
         c = sum_row(cur, a, 0, false);
         parity ^= 1;
+        if ((small = c < kSmall)) break;
       }
     } else if (!again) {
       left -= px;
@@ -349,19 +484,15 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
 
   // the draw
   if (cnt > 0) {
-    unsigned long long total = sum_row(cur, a, n_rej, true);
-    if (total == 0) {  // p <= a q everywhere: the target's own distribution
-      parity ^= 1;
-      a = 0;
-      n_rej = 0;
-      __syncthreads();
-      total = sum_row(cur, 0, 0, true);
+    unsigned long long total = 0;
+    if (!small) {
+      total = sum_row(cur, a, n_rej, true);
+      if ((small = total < kSmall)) parity ^= 1;
     }
-    if (total > 0) {
-      const float us = fminf(fmaxf(ld_now(P.u_sample + b), 0.f), 1.f);
-      // u in 2^-64 units (below 1), so that thr = floor(u * total) < total
-      const unsigned long long u64 = us >= 1.f ? ~0ull : __double2ull_rz(static_cast<double>(us) * 18446744073709551616.0);
-      const unsigned long long thr = __umul64hi(u64, total);
+    if (small) {
+      n = finish_small<DT>(P, s, b, rank, cnt, cur, i, n, n_rej, a, parity);
+    } else {
+      const unsigned long long thr = draw_at(P, b, total);
       unsigned long long run = 0;
       for (int r = 0; r < rank; ++r) run += s.cta_tot[parity][r];
       if (thr >= run && thr < run + s.cta_tot[parity][rank]) {  // one CTA of the cluster
@@ -404,9 +535,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
               all += s.warp_tot[i];
             }
             if (thr >= at && thr < at + x[0] + x[1]) {  // one thread
-              const int token = v0 + 2 * tid + (thr < at + x[0] ? 0 : 1);
-              if (P.tok64) static_cast<long long*>(P.next_token)[b] = token;
-              else static_cast<int32_t*>(P.next_token)[b] = token;
+              put_token(P, b, v0 + 2 * tid + (thr < at + x[0] ? 0 : 1));
             }
             found = thr < run + all;
             run += all;
@@ -417,13 +546,9 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
         else if (a == kOne) find(std::integral_constant<int, 1>());
         else find(std::integral_constant<int, 2>());
       }
-    } else if (rank == 0 && tid == 0) {
-      if (P.tok64) static_cast<long long*>(P.next_token)[b] = -1;
-      else static_cast<int32_t*>(P.next_token)[b] = -1;
     }
   } else if (rank == 0 && tid == 0) {
-    if (P.tok64) static_cast<long long*>(P.next_token)[b] = -1;
-    else static_cast<int32_t*>(P.next_token)[b] = -1;
+    put_token(P, b, -1);
   }
   if (rank == 0) {
     for (int i = tid; i < P.T; i += kVerThreads) P.path[static_cast<int64_t>(b) * P.T + i] = i < n ? s.path[i] : -1;

@@ -175,3 +175,112 @@ def test_decoding_loop_step_by_step(cuda_lib, dtype, H, Hkv, page):
         assert torch.equal(bits(cache.k), bits(k1)) and torch.equal(bits(cache.v), bits(v1))
         assert new.tolist() == [x + y for x, y in zip(before, n.tolist())]
         lens = new
+
+
+def near_case(B, T, V, near, dtype, seed):
+    """Trees whose root's children are guesses that the draft overrates: all are rejected, and what is left of the row is
+    as small as target and draft are close."""
+    g = torch.Generator().manual_seed(seed)
+    target = torch.softmax(torch.randn(B, T, V, generator=g) * 2, -1)
+    draft = target * (1 + near * torch.randn(B, T, V, generator=g)).clamp(min=0.05)
+    draft = draft / draft.sum(-1, keepdim=True)
+    target, draft = target.to(dtype), draft.to(dtype)
+    tokens = torch.zeros(B, T, dtype=torch.int32)
+    for b in range(B):
+        over = (draft[b, 0].double() * (1 - 2.0 ** -24) > target[b, 0].double()).nonzero()[:, 0]
+        tokens[b, 1:] = over[torch.randperm(over.numel(), generator=g)[: T - 1]].to(torch.int32)
+    parents = torch.zeros(B, T, dtype=torch.int32)
+    parents[:, 0] = -1
+    ua = torch.full((B, T), 1 - 2.0 ** -24)
+    return target, draft, tokens, parents, ua, (torch.arange(B) + 0.5) / B
+
+
+@pytest.mark.parametrize("near,dtype", [(0.3, "fp32"), (1e-2, "fp32"), (1e-4, "fp32"), (1e-6, "fp32"), (1e-2, "bf16"), (2e-3, "fp16")])
+@pytest.mark.parametrize("B,T,V", [(24, 2, 131072), (24, 5, 20001), (320, 3, 701)])
+def test_verify_draft_close_to_the_target(cuda_lib, near, dtype, B, T, V):
+    """One to four rejections, and the draw from a residual of 2^-3 to 2^-21: the same token as in 64 bits. (A running sum
+    of 2^17 weights is off by about 2^-30 of such a total at most, and a draw among 2^17 borders within that of one hardly
+    ever; these inputs have none.)"""
+    case = near_case(B, T, V, near, DT[dtype], seed=T)
+    want = R.verify(*case)
+    assert want[1].tolist() == [1] * B  # all guesses are rejected
+    got = cuda_lib.st_tree_verify(*(t.cuda() for t in case))
+    cuda_lib.st_check_status()
+    for name, x, w in zip(("path", "n_accepted", "next_token"), got, want):
+        assert torch.equal(x.cpu(), w), (name, (x.cpu() != w).sum().item())
+
+
+def test_verify_residual_of_tiny_weights(cuda_lib):
+    """All that is left are tokens far below 2^-44: the next token is one of them, in proportion, not one of the target's
+    likely ones. With a draft, and without one after the only likely token's rejection."""
+    V, B = 5000, 64
+    target = torch.zeros(B, 3, V)
+    target[:, :, 7], target[:, :, 9] = 0.5, 0.5
+    tiny = torch.arange(100, 140)
+    target[:, :, tiny] = 2.0 ** -60 * torch.arange(1, 41)
+    draft = target.clone()
+    draft[:, :, tiny] = 0
+    draft[:, :, 9] = 0.5 + 2.0 ** -20
+    us = (torch.arange(B) + 0.5) / B
+    case = (target, draft, i32([[0, 9, 9]] * B), i32([[-1, 0, 0]]), torch.full((B, 3), 1 - 2.0 ** -24), us)
+    weight = torch.arange(1, 41).double()
+    want = 100 + (weight.cumsum(0)[None] <= us.double()[:, None] * weight.sum()).sum(-1)
+    path, n, nxt = (t.cpu() for t in cuda_lib.st_tree_verify(*(t.cuda() for t in case)))
+    assert n.tolist() == [1] * B and nxt.tolist() == want.tolist()
+    for first in (0.999, 1 - 2.0 ** -24):  # every weight counts, the largest is removed
+        alone = target.clone()
+        alone[:, :, 7], alone[:, :, 9] = first, 0
+        path, n, nxt = (t.cpu() for t in cuda_lib.st_tree_verify(alone.cuda(), None, i32([[0, 7, 7]] * B).cuda(), i32([[-1, 0, 0]]).cuda(),
+                                                                 case[4].cuda(), us.cuda()))
+        assert n.tolist() == [1] * B and nxt.tolist() == want.tolist()
+    # subnormal numbers, and a draft that is the target's very self but for them
+    sub = target.clone()
+    sub[:, :, tiny] = 2.0 ** -149 * torch.arange(1, 41)
+    path, n, nxt = (t.cpu() for t in cuda_lib.st_tree_verify(sub.cuda(), draft.cuda(), *(t.cuda() for t in case[2:])))
+    assert n.tolist() == [1] * B and nxt.tolist() == want.tolist()
+
+
+@pytest.mark.parametrize("near,dtype", [(1e-3, "fp32"), (1e-6, "fp32"), (2e-2, "bf16")])
+@pytest.mark.parametrize("B,V", [(48, 3001), (320, 257)])
+def test_verify_walk_behind_a_small_residual(cuda_lib, near, dtype, B, V):
+    """Trees whose nodes have a child that is rejected, one that what is left accepts or not, and children of their own:
+    the walk goes on behind residuals of any size."""
+    T = 24
+    target, draft, tokens, _, _, us = near_case(B, T, V, near, DT[dtype], seed=31)
+    g = torch.Generator().manual_seed(32)
+    parents = R.tree(B, T, 5, 33)
+    ua = torch.rand(B, T, generator=g)
+    for b in range(B):
+        first = {}
+        for i in range(1, T):
+            par = int(parents[b, i])
+            more = draft[b, par].double() > target[b, par].double()
+            if par not in first:  # overrated, and asked for with the largest u: rejected
+                more = draft[b, par].double() * (1 - 2.0 ** -24) > target[b, par].double()
+                ua[b, i] = 1 - 2.0 ** -24
+            elif i % 3:
+                more = ~more
+            first.setdefault(par, i)
+            pick = more.nonzero()[:, 0]
+            tokens[b, i] = int(pick[torch.randint(pick.numel(), (1,), generator=g)])
+    case = (target, draft, tokens, parents, ua, us)
+    want = R.verify(*case)
+    assert int(want[1].max()) > 1  # some walks go on
+    got = cuda_lib.st_tree_verify(*(t.cuda() for t in case))
+    cuda_lib.st_check_status()
+    for name, x, w in zip(("path", "n_accepted", "next_token"), got, want):
+        assert torch.equal(x.cpu(), w), (name, (x.cpu() != w).sum().item())
+
+
+def test_verify_greedy_with_nothing_left(cuda_lib):
+    """Target and draft both sure of one token: a guess of another one, tried first, is rejected and leaves nothing; then
+    the sure token is not accepted either, and the next one is the target's."""
+    B, V = 9, 40000
+    one = torch.zeros(B, 3, V)
+    one[:, :, 31234] = 1.0
+    for order in ([0, 5, 31234], [0, 31234, 5]):
+        case = (one, one, i32([order] * B), i32([[-1, 0, 0]]), torch.full((B, 3), 0.5), torch.full((B,), 0.25))
+        got = [t.cpu() for t in cuda_lib.st_tree_verify(*(t.cuda() for t in case))]
+        for x, w in zip(got, R.verify(*case)):
+            assert torch.equal(x, w)
+        assert got[1].tolist() == [1 if order[1] == 5 else 2] * B and got[2].tolist() == [31234] * B
