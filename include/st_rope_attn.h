@@ -305,7 +305,8 @@ typedef struct {
  *           the same rotation for q and k (ids_k, cos_k and sin_k must be
  *           NULL).
  *  q_rot:   [B, T, H, D] output in the cache's dtype: normalised, rotated q
- *           (zero in padding rows). It may be q itself when the dtypes match.
+ *           (zero in padding rows), not expanded. It may be q itself when the
+ *           dtypes match.
  * Rows whose position lies beyond the page table, or whose page number is not
  * in [0, N_pages), are not written; with lens[b] < 0 none of sequence b's are.
  * Padding rows write nothing. */
@@ -325,8 +326,8 @@ ST_API size_t st_cache_attn_workspace_size(const st_tensor* q_rot, const st_kv_c
  *           and its ancestors. parents[t] < t, -1 for a node that follows the
  *           prefix; anything else ends the walk up at that node.
  *  scale:   score scale; <= 0 selects 1/sqrt(D).
- *  o:       [B, T, H, D], the cache's dtype, not overlapping q_rot; lse:
- *           [B, H, T] fp32, contiguous.
+ *  o:       [B, T, H, D], the cache's dtype, not expanded and not overlapping
+ *           q_rot; lse: [B, H, T] fp32, contiguous.
  *           Padding rows get O = 0, LSE = -inf.
  *  workspace: 256-byte aligned; its contents need no initialisation. Calls
  *           that may overlap on the GPU need workspaces of their own.

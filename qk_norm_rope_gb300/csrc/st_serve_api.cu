@@ -40,6 +40,14 @@ st_status check_rows(const st_tensor* t, const char* name, int64_t B, int64_t n,
   return ST_OK;
 }
 
+// Rows that are written: none may stand for several.
+st_status check_own_rows(const st_tensor* t, const char* name) {
+  if (t->shape[0] * t->shape[1] * t->shape[2] == 0) return ST_OK;
+  for (int a = 0; a < 3; ++a)
+    if (t->shape[a] > 1 && t->stride[a] <= 0) return fail(ST_ERR_ALIGN, "%s must not be expanded (stride[%d]=%lld)", name, a, (long long)t->stride[a]);
+  return ST_OK;
+}
+
 // B < 0: the page table's own batch size is taken.
 st_status check_cache(const st_kv_cache* c, int64_t B, PagedKV* out, const char* who) {
   if (!c || !c->k || !c->v || !c->pages) return fail(ST_ERR_INVALID_ARG, "%s: the cache needs k, v and pages", who);
@@ -54,11 +62,8 @@ st_status check_cache(const st_kv_cache* c, int64_t B, PagedKV* out, const char*
   st_status st;
   if ((st = check_bshd(k, "cache.k", n, page, H, kD, kCacheTypes, &rk)) != ST_OK) return st;
   if ((st = check_bshd(c->v, "cache.v", n, page, H, kD, bit(k->dtype), &rv)) != ST_OK) return st;
-  // the rows of a cache are written: none may stand for several positions
-  for (const st_tensor* t : {k, c->v})
-    for (int a = 0; a < 3; ++a)
-      if (t->shape[a] > 1 && t->stride[a] <= 0)
-        return fail(ST_ERR_ALIGN, "%s must not be expanded (stride[%d]=%lld)", t == k ? "cache.k" : "cache.v", a, (long long)t->stride[a]);
+  if ((st = check_own_rows(k, "cache.k")) != ST_OK) return st;
+  if ((st = check_own_rows(c->v, "cache.v")) != ST_OK) return st;
   if (pt->ndim != 2 || (B >= 0 && pt->shape[0] != B)) return fail(ST_ERR_SHAPE, "cache.pages must be [%lld, max_pages]", (long long)B);
   if (pt->shape[0] < 0 || pt->shape[0] > 65535 || pt->shape[1] < 0) return fail(ST_ERR_SHAPE, "cache.pages sizes out of range");
   if (pt->dtype != ST_I32) return fail(ST_ERR_DTYPE, "cache.pages must be int32");
@@ -238,6 +243,7 @@ st_status st_cache_append(const st_tensor* q, const st_tensor* k, const st_tenso
   if ((st = check_counts(counts, p.B, &p.counts)) != ST_OK) return st;
   RowTensor ro;
   if ((st = check_bshd(q_rot, "q_rot", p.B, p.T, p.H, kD, bit(p.kv.dt), &ro)) != ST_OK) return st;
+  if ((st = check_own_rows(q_rot, "q_rot")) != ST_OK) return st;
   const int64_t tokens = static_cast<int64_t>(p.B) * p.T;
   if (tokens > (1ll << 30) || tokens * (p.H + 2 * p.kv.Hkv) > (1ll << 32)) return fail(ST_ERR_SHAPE, "too many new rows");
   if (tokens * p.H == 0) return ST_OK;
@@ -304,6 +310,7 @@ st_status st_cache_attn(const st_tensor* q_rot, const st_kv_cache* cache, const 
   if (!std::isfinite(scale)) return fail(ST_ERR_INVALID_ARG, "scale must be finite");
   RowTensor ro;
   if ((st = check_bshd(o, "o", p.B, p.T, p.H, kD, bit(p.kv.dt), &ro)) != ST_OK) return st;
+  if ((st = check_own_rows(o, "o")) != ST_OK) return st;
   if (static_cast<int64_t>(p.B) * p.T * p.H > 0 && o->data == q_rot->data)
     return fail(ST_ERR_INVALID_ARG, "o must not be q_rot: its rows are read until the call ends");
   if (!lse || lse->ndim != 3 || lse->shape[0] != p.B || lse->shape[1] != p.H || lse->shape[2] != p.T)

@@ -97,3 +97,18 @@ def test_attention_bound_finds_planted_mistakes(dtype, mistake):
     for b in range(B):
         found = ((wrong[b] - o[b]).abs() > bound[b])[changed[b]]
         assert found.double().mean() > share, (b, float(found.double().mean()))
+
+
+@pytest.mark.parametrize("dim", [0, 1, 2])
+def test_outputs_must_not_be_expanded(dim):
+    """An output whose rows lie in one place (q itself, broadcast over heads, as q_rot) would keep any of them."""
+    from test_abi import FAKE, T
+    from test_serving_abi import check
+    strides = [5 * 8 * 128, 8 * 128, 128, 1]
+    strides[dim] = 0
+    check("append", api.ST_ERR_ALIGN, "q_rot must not be expanded", q_rot=T([2, 5, 8, 128], strides=strides))
+    check("attn", api.ST_ERR_ALIGN, "o must not be expanded", o=T([2, 5, 8, 128], data=FAKE + (1 << 30), strides=strides))
+    one = dict(B=1, T_=1, H=1, Hkv=1)  # a stride of nothing is no expansion
+    import torch
+    if not torch.cuda.is_available():
+        check("append", api.ST_ERR_CUDA, sizes=one, q_rot=T([1, 1, 1, 128], strides=[0, 0, 0, 1]))
