@@ -499,11 +499,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
   if (warp < kSoftWarps) {
     // -------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
-    // padding rows, and every row of a sequence without room for keys
-    if (c.counts || static_cast<int64_t>(c.kv.max_pages) * c.kv.page == 0) {
+    // padding rows (a cache without room for keys is not this kernel's)
+    if (c.counts) {
       for (int b = CL ? blockIdx.y * gridDim.x + blockIdx.x : blockIdx.x; b < c.B; b += CL ? gridDim.x * gridDim.y : gridDim.x) {
-        const Item it = item_of(P, NT, b, 0);
-        const int t0 = it.keys == 0 ? 0 : it.cnt;
+        const int t0 = row_count(c.counts, b, c.T);
         for (int64_t e = tid; e < static_cast<int64_t>(c.T - t0) * c.H * 16; e += kSoftWarps * 32) {
           const int64_t row = e >> 4;
           const int t = t0 + static_cast<int>(row / c.H), h = static_cast<int>(row % c.H);
@@ -987,7 +986,6 @@ cudaError_t launch_cache_attn_tc(const TcAttnParams& p, int nt, bool f16, cudaSt
 }
 
 cudaError_t launch_cache_attn_join(const TcAttnParams& p, int nt, cudaStream_t stream) {
-  if (p.ctas < 2) return cudaSuccess;
   // few rows, or few items, whose parts are then many
   const bool deep = p.part_rows <= 32 || static_cast<int64_t>(p.c.B) * p.c.kv.Hkv * p.n_groups * 4 <= p.ctas;
   return launch_chained(deep ? join_kernel<16> : join_kernel<4>, dim3(p.ctas - 1, (p.part_rows + kJoinRows - 1) / kJoinRows), dim3(256), 0, stream, p, nt);
