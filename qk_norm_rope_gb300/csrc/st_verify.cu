@@ -192,14 +192,17 @@ __device__ __forceinline__ void put_token(const VerifyParams& P, int b, int toke
 
 // ------------------------------------------------------ residuals of small sums
 // The rest of a sequence's walk and its draw once a residual has summed to less
-// than kSmall units: weights by one fp64 product and sum each, in the unit
+// than kSmall units: weights to the last bit that fp64 gives, in the unit
 // 2^-(43 + shift), with shift raised until the sum has kEnough units or nothing is
 // left. A step leaves room for what was rounded off before: (2^34 + V / 2) 2^25 <
 // 2^60 for V <= 2^30. Residuals only shrink from one rejection to the next, so a
 // node's shift stays good. A function of its own and plain code, as few sequences
-// need it; built into the ordinary passes it cost all of them 6 to 8%.
+// need it (a first residual below 2^-12 means that less than one guess in 4096 was
+// rejected): built into the ordinary passes it cost all of them 6 to 8%. 24
+// sequences over 131072 tokens take 42 us with one such rejection and 75 more with
+// each further one (fp64), 13 with ordinary residuals.
 constexpr unsigned long long kSmall = 1ull << 31, kEnough = 1ull << 34;
-constexpr int kShiftStep = 25, kShiftMost = 125;  // to 2^-168: fp32's smallest number is 2^-149
+constexpr int kFineBatch = 8, kShiftStep = 25, kShiftMost = 125;  // to 2^-168: fp32's smallest number is 2^-149
 constexpr unsigned long long kAnyLeft = 1ull << 60;  // in a CTA's total: it has weights above 0
 
 // From the child i of node `cur` on (cnt: none is left), `n` nodes being accepted,
@@ -211,24 +214,59 @@ __device__ __noinline__ int finish_small(const VerifyParams& P, VerState& s, int
   const bool drafted = P.q != nullptr;
   double a = static_cast<double>(a_units) * kUnit, c = 1.0;
   int shift = kShiftStep;
-  auto weight = [&](int64_t pe, int64_t qe, int v) {
-    const double p = prob<DT>(P.p, pe + v);
-    double w = drafted && a != 0.0 ? fma(-a, static_cast<double>(prob<DT>(P.q, qe + v)), p) : p;
-    for (int r = 0; r < n_rej; ++r)
-      if (s.tok[s.rejected[r]] == v) w = 0.0;
-    return w;
+  const int64_t lo = static_cast<int64_t>(rank * kVerWarps + warp) * sub, end = min(lo + sub, static_cast<int64_t>(V));  // the warp's slice
+  // tokens v0 + 32 u of the row of node `cur`, their loads in flight together, in
+  // units. Returns whether any is above 0. For a = 0 and a = 1 the first shift
+  // needs no fp64: p - min(p, q) is a float and its error, 2^56 units at most.
+  auto batch = [&](int64_t v0, unsigned long long (&x)[kFineBatch]) {
+    const int64_t pe = b * P.p_sb + cur * P.p_st, qe = b * P.q_sb + cur * P.q_st;
+    const bool with_q = drafted && a != 0.0, plain = shift == kShiftStep && (!with_q || a == 1.0);
+    float pv[kFineBatch], qv[kFineBatch];
+#pragma unroll
+    for (int u = 0; u < kFineBatch; ++u) {
+      const int64_t v = min(v0 + 32 * u, end - 1);
+      pv[u] = prob<DT>(P.p, pe + v);
+      qv[u] = with_q ? prob<DT>(P.q, qe + v) : 0.f;
+    }
+    for (int r = 0; r < n_rej; ++r) {
+      const int64_t gone = s.tok[s.rejected[r]] - v0;
+#pragma unroll
+      for (int u = 0; u < kFineBatch; ++u)
+        if (gone == 32 * u) pv[u] = 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < kFineBatch; ++u)
+      if (v0 + 32 * u >= end) pv[u] = 0.f;  // weighs nothing, whatever q
+    bool any = false;
+    if (plain) {
+      constexpr float kScale = 295147905179352825856.f;  // 2^(43 + kShiftStep)
+#pragma unroll
+      for (int u = 0; u < kFineBatch; ++u) {
+        const float m = fminf(pv[u], qv[u]), d = __fsub_rn(pv[u], m), e = __fsub_rn(__fsub_rn(pv[u], d), m);
+        x[u] = __float2ull_rn(d * kScale) + static_cast<unsigned long long>(__float2ll_rn(e * kScale));
+        any |= d > 0.f;
+      }
+    } else {
+      const double scale = scalbn(1.0, 43 + shift);
+#pragma unroll
+      for (int u = 0; u < kFineBatch; ++u) {
+        const double w = fmax(fma(-a, static_cast<double>(qv[u]), static_cast<double>(pv[u])), 0.0);
+        x[u] = static_cast<unsigned long long>(__double2ll_rn(w * scale));
+        any |= w > 0.0;
+      }
+    }
+    return any;
   };
-  auto units = [&](double w) { return static_cast<unsigned long long>(__double2ll_rn(scalbn(fmax(w, 0.0), 43 + shift))); };
   // the sum over the row of node `cur`; the warps' totals stay in s.warp_tot, the CTAs' in s.cta_tot[parity ^ 1]
   auto sum_row = [&]() -> unsigned long long {
-    const int64_t pe = b * P.p_sb + cur * P.p_st, qe = b * P.q_sb + cur * P.q_st, lo = static_cast<int64_t>(rank * kVerWarps + warp) * sub;
     while (true) {
       unsigned long long acc = 0;
       bool any = false;
-      for (int64_t v = lo + lane; v < min(lo + sub, static_cast<int64_t>(V)); v += 32) {
-        const double w = weight(pe, qe, static_cast<int>(v));
-        any |= w > 0.0;
-        acc += units(w);
+      for (int64_t v0 = lo + lane; v0 < end; v0 += 32 * kFineBatch) {
+        unsigned long long x[kFineBatch];
+        any |= batch(v0, x);
+#pragma unroll
+        for (int u = 0; u < kFineBatch; ++u) acc += x[u];
       }
       acc = warp_sum(acc);
       if (lane == 0) s.warp_tot[warp] = acc;
@@ -251,7 +289,11 @@ __device__ __noinline__ int finish_small(const VerifyParams& P, VerState& s, int
       shift += kShiftStep;
     }
   };
-  if (i < cnt) c = scalbn(static_cast<double>(sum_row()), -43 - shift);  // only with draft probabilities
+  auto residual = [&]() {
+    const unsigned long long total = sum_row();  // which may raise the shift
+    return scalbn(static_cast<double>(total), -43 - shift);
+  };
+  if (i < cnt) c = residual();  // only with draft probabilities
   while (i < cnt) {
     const double px = s.pp[i], qx = s.qq[i];
     const bool yes = static_cast<double>(s.uu[i]) * qx * c < fmax(fma(-a, qx, px), 0.0);
@@ -267,7 +309,7 @@ __device__ __noinline__ int finish_small(const VerifyParams& P, VerState& s, int
       a += c;
     }
     i = next_child(s, cur, last, cnt);
-    if (!yes && i < cnt) c = scalbn(static_cast<double>(sum_row()), -43 - shift);
+    if (!yes && i < cnt) c = residual();
   }
   unsigned long long total = sum_row();
   if (total == 0) {  // p <= a q everywhere: the target's own distribution
@@ -286,19 +328,21 @@ __device__ __noinline__ int finish_small(const VerifyParams& P, VerState& s, int
   for (int w = 0; w < warp; ++w) run += s.warp_tot[w];
   if (thr < run || thr >= run + s.warp_tot[warp]) return n;
   // one warp of the cluster: 32 tokens at a time
-  const int64_t pe = b * P.p_sb + cur * P.p_st, qe = b * P.q_sb + cur * P.q_st, lo = static_cast<int64_t>(rank * kVerWarps + warp) * sub;
-  const int end = static_cast<int>(min(lo + sub, static_cast<int64_t>(V)));
-  for (int v0 = static_cast<int>(lo); v0 < end; v0 += 32) {
-    const unsigned long long x = v0 + lane < end ? units(weight(pe, qe, v0 + lane)) : 0ull;
-    unsigned long long inc = x;
+  for (int64_t v0 = lo; v0 < end && thr >= run; v0 += 32 * kFineBatch) {
+    unsigned long long y[kFineBatch];
+    batch(v0 + lane, y);
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long t = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += t;
+    for (int u = 0; u < kFineBatch; ++u) {
+      const unsigned long long x = y[u];
+      unsigned long long inc = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long t = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += t;
+      }
+      if (thr >= run + inc - x && thr < run + inc) put_token(P, b, static_cast<int>(v0) + 32 * u + lane);  // one thread
+      run += __shfl_sync(0xffffffffu, inc, 31);
     }
-    if (thr >= run + inc - x && thr < run + inc) put_token(P, b, v0 + lane);  // one thread
-    run += __shfl_sync(0xffffffffu, inc, 31);
-    if (thr < run) break;
   }
   return n;
 }
