@@ -192,35 +192,45 @@ __device__ __forceinline__ void put_token(const VerifyParams& P, int b, int toke
 
 // ------------------------------------------------------ residuals of small sums
 // The rest of a sequence's walk and its draw once a residual has summed to less
-// than kSmall units: weights to the last bit that fp64 gives, in the unit
-// 2^-(43 + shift), with shift raised until the sum has kEnough units or nothing is
-// left. A step leaves room for what was rounded off before: (2^34 + V / 2) 2^25 <
-// 2^60 for V <= 2^30. Residuals only shrink from one rejection to the next, so a
+// than kSmall units, from the present node's first child on: what the ordinary
+// sums rounded off weighs in such a residual. Weights are to the last bit that
+// fp64 gives, in the unit 2^-(43 + shift), with shift raised until the sum has
+// kEnough units or nothing is left; a raise leaves room for what was rounded off
+// before, V / 2 units. Residuals only shrink from one rejection to the next, so a
 // node's shift stays good. A function of its own and plain code, as few sequences
 // need it (a first residual below 2^-12 means that less than one guess in 4096 was
-// rejected): built into the ordinary passes it cost all of them 6 to 8%. 24
-// sequences over 131072 tokens take 42 us with one such rejection and 75 more with
-// each further one (fp64), 13 with ordinary residuals.
-constexpr unsigned long long kSmall = 1ull << 31, kEnough = 1ull << 34;
-constexpr int kFineBatch = 8, kShiftStep = 25, kShiftMost = 125;  // to 2^-168: fp32's smallest number is 2^-149
+// rejected): built into the ordinary passes it cost all of them 6 to 8%, as it is
+// 0.15 us of a chain's 5.9. 24 sequences over 131072 tokens take 45 us with
+// one such rejection and 75 more with each further one (fp64), 13 with ordinary
+// residuals.
+constexpr unsigned long long kSmall = 1ull << 31, kEnough = 1ull << 50;
+constexpr int kFineBatch = 8;
+constexpr int kShiftFirst = -16, kShiftMost = 125;   // rows of any sum up to 2^30; 2^-168: fp32's smallest number is 2^-149
+constexpr int kRoom = 59;                            // a CTA's and the row's sums stay below 2^59
 constexpr unsigned long long kAnyLeft = 1ull << 60;  // in a CTA's total: it has weights above 0
 
-// From the child i of node `cur` on (cnt: none is left), `n` nodes being accepted,
-// at `a` with n_rej removed tokens; `parity`: of the next exchange. Returns the accepted nodes and writes the token.
+// `n` nodes being accepted, the last of them `cur`; without draft probabilities
+// its children are done with and n_rej tokens removed. The small sum was `found`,
+// at `found_a`. `parity`: of the next exchange. Returns the accepted nodes and
+// writes the token.
 template <int DT>
-__device__ __noinline__ int finish_small(const VerifyParams& P, VerState& s, int b, int rank, int cnt, int cur, int i, int n, int n_rej,
-                                         unsigned long long a_units, int parity) {
+__device__ __noinline__ int finish_small(const VerifyParams& P, VerState& s, int b, int rank, int cnt, int cur, int n, int n_rej,
+                                         unsigned long long found_a, unsigned long long found, int parity) {
   const int C = P.cluster, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, V = P.V, sub = slice_of(V, C);
   const bool drafted = P.q != nullptr;
-  double a = static_cast<double>(a_units) * kUnit, c = 1.0;
-  int shift = kShiftStep;
   const int64_t lo = static_cast<int64_t>(rank * kVerWarps + warp) * sub, end = min(lo + sub, static_cast<int64_t>(V));  // the warp's slice
+  const int found_at = cur, found_rej = n_rej;
+  double a = 0.0, c = 1.0;
+  int shift = kShiftFirst;
+  auto raise = [&](unsigned long long total) {  // for a sum of `total` units
+    shift = min(shift + kRoom - (64 - __clzll(static_cast<long long>(total + V / 2 + 1))), kShiftMost);
+  };
   // tokens v0 + 32 u of the row of node `cur`, their loads in flight together, in
-  // units. Returns whether any is above 0. For a = 0 and a = 1 the first shift
-  // needs no fp64: p - min(p, q) is a float and its error, 2^56 units at most.
+  // units. Returns whether any is above 0. a = 0 and a = 1 need no fp64: p - min(p, q)
+  // is a float and its error.
   auto batch = [&](int64_t v0, unsigned long long (&x)[kFineBatch]) {
     const int64_t pe = b * P.p_sb + cur * P.p_st, qe = b * P.q_sb + cur * P.q_st;
-    const bool with_q = drafted && a != 0.0, plain = shift == kShiftStep && (!with_q || a == 1.0);
+    const bool with_q = drafted && a != 0.0, plain = shift <= 80 && (!with_q || a == 1.0);
     float pv[kFineBatch], qv[kFineBatch];
 #pragma unroll
     for (int u = 0; u < kFineBatch; ++u) {
@@ -239,11 +249,11 @@ __device__ __noinline__ int finish_small(const VerifyParams& P, VerState& s, int
       if (v0 + 32 * u >= end) pv[u] = 0.f;  // weighs nothing, whatever q
     bool any = false;
     if (plain) {
-      constexpr float kScale = 295147905179352825856.f;  // 2^(43 + kShiftStep)
+      const float scale = scalbnf(1.f, 43 + shift);
 #pragma unroll
       for (int u = 0; u < kFineBatch; ++u) {
         const float m = fminf(pv[u], qv[u]), d = __fsub_rn(pv[u], m), e = __fsub_rn(__fsub_rn(pv[u], d), m);
-        x[u] = __float2ull_rn(d * kScale) + static_cast<unsigned long long>(__float2ll_rn(e * kScale));
+        x[u] = __float2ull_rn(d * scale) + static_cast<unsigned long long>(__float2ll_rn(e * scale));
         any |= d > 0.f;
       }
     } else {
@@ -259,6 +269,10 @@ __device__ __noinline__ int finish_small(const VerifyParams& P, VerState& s, int
   };
   // the sum over the row of node `cur`; the warps' totals stay in s.warp_tot, the CTAs' in s.cta_tot[parity ^ 1]
   auto sum_row = [&]() -> unsigned long long {
+    if (shift == kShiftFirst && cur == found_at && n_rej == found_rej && a == static_cast<double>(found_a) * kUnit) {  // that very sum
+      shift = 0;
+      raise(found);
+    }
     while (true) {
       unsigned long long acc = 0;
       bool any = false;
@@ -286,15 +300,10 @@ __device__ __noinline__ int finish_small(const VerifyParams& P, VerState& s, int
       total &= kAnyLeft - 1;
       parity ^= 1;
       if (total >= kEnough || !left || shift >= kShiftMost) return total;
-      shift += kShiftStep;
+      raise(total);
     }
   };
-  auto residual = [&]() {
-    const unsigned long long total = sum_row();  // which may raise the shift
-    return scalbn(static_cast<double>(total), -43 - shift);
-  };
-  if (i < cnt) c = residual();  // only with draft probabilities
-  while (i < cnt) {
+  for (int i = drafted ? next_child(s, cur, cur, cnt) : cnt; i < cnt;) {
     const double px = s.pp[i], qx = s.qq[i];
     const bool yes = static_cast<double>(s.uu[i]) * qx * c < fmax(fma(-a, qx, px), 0.0);
     const int last = i;
@@ -304,17 +313,20 @@ __device__ __noinline__ int finish_small(const VerifyParams& P, VerState& s, int
       ++n;
       a = 0.0;
       c = 1.0;
-      shift = 0;
+      shift = kShiftFirst;
     } else {
       a += c;
     }
     i = next_child(s, cur, last, cnt);
-    if (!yes && i < cnt) c = residual();
+    if (!yes && i < cnt) {
+      const unsigned long long total = sum_row();  // which may raise the shift
+      c = scalbn(static_cast<double>(total), -43 - shift);
+    }
   }
   unsigned long long total = sum_row();
   if (total == 0) {  // p <= a q everywhere: the target's own distribution
     a = 0.0;
-    shift = 0;
+    shift = kShiftFirst;
     n_rej = 0;
     total = sum_row();
   }
@@ -333,14 +345,13 @@ __device__ __noinline__ int finish_small(const VerifyParams& P, VerState& s, int
     batch(v0 + lane, y);
 #pragma unroll
     for (int u = 0; u < kFineBatch; ++u) {
-      const unsigned long long x = y[u];
-      unsigned long long inc = x;
+      unsigned long long inc = y[u];
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const unsigned long long t = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += t;
       }
-      if (thr >= run + inc - x && thr < run + inc) put_token(P, b, static_cast<int>(v0) + 32 * u + lane);  // one thread
+      if (thr >= run + inc - y[u] && thr < run + inc) put_token(P, b, static_cast<int>(v0) + 32 * u + lane);  // one thread
       run += __shfl_sync(0xffffffffu, inc, 31);
     }
   }
@@ -528,13 +539,13 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
 
   // the draw
   if (cnt > 0) {
-    unsigned long long total = 0;
+    unsigned long long total = c;
     if (!small) {
       total = sum_row(cur, a, n_rej, true);
       if ((small = total < kSmall)) parity ^= 1;
     }
     if (small) {
-      n = finish_small<DT>(P, s, b, rank, cnt, cur, i, n, n_rej, a, parity);
+      n = finish_small<DT>(P, s, b, rank, cnt, cur, n, n_rej, a, total, parity);
     } else {
       const unsigned long long thr = draw_at(P, b, total);
       unsigned long long run = 0;

@@ -284,3 +284,25 @@ def test_verify_greedy_with_nothing_left(cuda_lib):
         for x, w in zip(got, R.verify(*case)):
             assert torch.equal(x, w)
         assert got[1].tolist() == [1 if order[1] == 5 else 2] * B and got[2].tolist() == [31234] * B
+
+
+def test_verify_every_token_removed(cuda_lib):
+    """Without a draft, rows that sum to less than 1: both of their tokens are guessed and rejected, which leaves nothing,
+    and the next token is the target's. And rows of far more than 1 (scores instead of probabilities), whose draft is the
+    same: some token of them."""
+    V, B = 20000, 8
+    p = torch.zeros(B, 3, V)
+    p[:, :, 70], p[:, :, 15000] = 0.3, 0.3
+    us = (torch.arange(B) + 0.5) / B
+    case = (p, None, i32([[0, 70, 15000]] * B), i32([[-1, 0, 0]]), torch.full((B, 3), 0.9), us)
+    got = [t.cpu() for t in cuda_lib.st_tree_verify(*(None if t is None else t.cuda() for t in case))]
+    for x, w in zip(got, R.verify(*case)):
+        assert torch.equal(x, w)
+    assert got[2].tolist() == [70] * 4 + [15000] * 4
+    V = 150000
+    ones = torch.ones(B, 2, V)
+    ones[:, :, 0] = 0
+    case = (ones, ones, i32([[0, 0]] * B), i32([[-1, 0]]), torch.full((B, 2), 0.5), us)
+    got = [t.cpu() for t in cuda_lib.st_tree_verify(*(t.cuda() for t in case))]
+    for x, w in zip(got, R.verify(*case)):
+        assert torch.equal(x, w)
