@@ -278,7 +278,7 @@ ST_API st_status st_rope_attn_fwd_noalloc(const st_tensor* q, const st_tensor* k
  * each kind on a device loads its kernels: make it outside a capture). What is
  * out of range there cannot be refused by the call: it is left out as each call
  * says, and the next st_check_status returns ST_ERR_INVALID_ARG. Nothing here
- * is differentiated.
+ * is differentiated: outputs carry no gradient, whatever the inputs ask for.
  *
  * st_kv_cache: token `pos` of sequence b lies in row pos % page of page
  *   pages[b, pos / page]. k, v: [N_pages, page, H_kv, D] of one dtype (bf16,
@@ -297,7 +297,10 @@ typedef struct {
   const st_tensor* pages;
 } st_kv_cache;
 
-/* New rows enter the cache.
+/* New rows enter the cache. The norm is always taken, and the rotation turns
+ * neighbouring elements (2 p, 2 p + 1) of a head, as everywhere in this library:
+ * a model that rotates halves permutes its projections' rows and its norm
+ * weights once.
  *  q, k, v: [B, T, H, D], [B, T, H_kv, D] (twice); v of the cache's dtype, q
  *           and k of that dtype or both fp32 (then rounded to it after norm
  *           and rotation). H_kv divides H.
@@ -336,7 +339,12 @@ ST_API size_t st_cache_attn_workspace_size(const st_tensor* q_rot, const st_kv_c
  * row does not see must be finite where their position is below lens[b] +
  * counts[b]; what lies behind is never used. bf16 and fp16 caches: products of
  * 16-bit operands, the softmax weights rounded to that type, all sums in fp32.
- * fp32 caches: fp32 throughout. Results do not depend on the run. */
+ * fp32 caches: fp32 throughout. Results do not depend on the run.
+ * The call is planned by the room of the page table (max_pages * page), as the
+ * lengths are on the device. Few sequences with short contexts run faster with a
+ * view of the table that is narrowed to a bound on their lengths (fewer columns,
+ * the same strides). 16-bit caches want pages of a multiple of 8 rows: others
+ * take a kernel without tensor cores. */
 ST_API st_status st_cache_attn(const st_tensor* q_rot, const st_kv_cache* cache, const st_tensor* lens,
                                const st_tensor* counts, const st_tensor* parents, float scale, st_tensor* o,
                                st_tensor* lse, void* workspace, size_t workspace_bytes, void* stream);

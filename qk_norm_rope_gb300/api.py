@@ -9,7 +9,8 @@ Names follow the C-ABI: ``st_rope_attn_fwd``, ``st_rope_attn_bwd``,
 ``st_rope_attn_workspace_size``, ``st_get_stats``, ``st_reset_stats``,
 ``st_check_status``, ``st_last_error``. ``rope_attention`` wraps the pair in a
 ``torch.autograd.Function``. The serving calls, over a paged ``KVCache``:
-``st_cache_append``, ``st_cache_attn``, ``st_tree_verify``, ``st_cache_keep``.
+``st_cache_append``, ``st_cache_attn``, ``st_tree_verify``, ``st_cache_keep``
+(forward only: their results carry no gradient, also where inputs require one).
 
 The rotation is given either by position ids (``ids``, ``axes_dim``,
 ``theta``) or, in the form of the "Fused RoPE + SDPA" entry point, by
@@ -354,7 +355,8 @@ def _bind():
 def st_cache_append(q, k, v, q_norm_w, k_norm_w, eps, ids, axes_dim, theta, cache, lens, counts=None, q_rot=None):
     """New rows enter the cache: q [B,T,H,D], k, v [B,T,H_kv,D]; k normalised
     and rotated, and v, go to positions lens[b].. of each sequence. Returns the
-    normalised, rotated q in the cache's dtype (zero in rows behind counts[b])."""
+    normalised, rotated q in the cache's dtype (zero in rows behind counts[b]),
+    without a gradient."""
     m = _bind_mod or _bind()
     if isinstance(ids, RopeTables):
         return m.cache_append(q, k, v, q_norm_w, k_norm_w, eps, None, ids.cos, ids.sin, ids.cos_k, ids.sin_k, (), 0.0,
@@ -376,7 +378,9 @@ def st_cache_attn_workspace_size(q_rot, cache, parents=None) -> int:
 def st_cache_attn(q_rot, cache, lens, counts=None, parents=None, scale=None, o=None, lse=None, workspace=None):
     """Attention of the new rows over the cache (after st_cache_append):
     parents=None for a chain (single tokens, a prompt's chunk), [B|1, T] int32
-    for trees of drafted tokens. Returns (o [B,T,H,D], lse [B,H,T] fp32)."""
+    for trees of drafted tokens. Returns (o [B,T,H,D], lse [B,H,T] fp32),
+    without gradients. Planned by the room of cache.pages: a table narrowed to
+    a bound on the lengths is faster for few sequences."""
     return (_bind_mod or _bind()).cache_attn(q_rot, cache.k, cache.v, cache.pages, lens, counts, parents, scale or 0.0, o,
                                              lse, workspace)
 

@@ -64,7 +64,8 @@ struct Raw8 {  // eight elements as they lie in memory
 
 // (cos, sin) of pair `pr` at token (b, t). Integer positions: position times
 // the pair's turns per position in 64-bit fixed point, whose low 64 bits are
-// the fraction of a turn, exactly reduced however far the position.
+// the fraction of a turn, exactly reduced however far the position. fp32 positions
+// are reduced in fp64 (4608 tokens of two samples, 24 + 24 heads: 81 us against 76).
 __device__ __forceinline__ float2 append_pair(const AppendParams& p, int b, int t, int pr) {
   const TableParams& tab = p.tab;
   const int bt = tab.Bt == 1 ? 0 : b;

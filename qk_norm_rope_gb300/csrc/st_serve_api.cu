@@ -164,9 +164,11 @@ st_status plan_attn(const st_tensor* q, const st_kv_cache* cache, const st_tenso
     // two turns: 18.3 us against 11.0 with 4). Its shares are even per item
     // instead of over the call: up to room * (1 / cluster - mean * items / SMs)
     // key tiles more for a CTA (mean: the mean length over the room, taken as 1
-    // for one sequence and 1/2 for a batch, whose lengths differ); it saves the
-    // scan for the beginning and the join, as much as about 8 tiles. One token,
-    // 8 K/V heads: 777 keys 10.5 us dealt, 7.1 clustered; 8000 keys 17.9 and
+    // for one sequence and 1/2 for a batch, whose lengths differ: the lengths are on
+    // the device, so a table with room for far more than they need is dealt, 777
+    // keys with room for 16384 or more 11.5 us, 8 sequences of up to 1000 16.9);
+    // it saves the scan for the beginning and the join, as much as about 8 tiles.
+    // One token, 8 K/V heads: 777 keys 10.5 us dealt, 7.1 clustered; 8000 keys 17.9 and
     // 14.4; 16000 keys 18.8 and 22.3; 8 sequences of up to 1000 keys 16.6 and
     // 10.9, of up to 8000 keys 36 and 43.
     // With more than 128 rows a head the join is the larger part: as much as 16
@@ -197,7 +199,8 @@ st_status plan_attn(const st_tensor* q, const st_kv_cache* cache, const st_tenso
   if (items > (1ll << 30)) return fail(ST_ERR_SHAPE, "too many query rows");
   const int64_t tiles = (static_cast<int64_t>(p.kv.max_pages) * p.kv.page + kSimtKeys - 1) / kSimtKeys;
   // few items: as many key ranges as give two CTAs per SM (what fits), dealt to
-  // the sequences by their lengths
+  // the sequences by their lengths (fp32, 8 K/V heads, single tokens after 2000
+  // keys each: 19 sequences 234 us with their two ranges each, 20 without 449)
   if (2 * kSmCount / items >= 2 && tiles > 1) {
     const int64_t per_seq = items / p.B;
     p.splits = static_cast<int>(2 * kSmCount / per_seq);

@@ -21,7 +21,7 @@
 // tokens, whose roundings are independent. What is left of a row whose draft is
 // close to its target sums to far less than 1, and loses its small weights in
 // that unit: after a sum below 2^-12 (finish_small) the rest of the sequence is
-// done with weights in fp64 and a unit that goes by the sum.
+// done with exact weights and a unit that goes by the sum.
 //
 // The walk is latency, the residual sums and the draw read two rows of V. One
 // cluster of CTAs serves a sequence: each CTA gathers every node's two
@@ -29,13 +29,15 @@
 // owns a slice of V in the sums, and exchanges its slice's total through
 // distributed shared memory.
 //
-// 32 trees of 61 nodes over 131072 tokens in fp32 take 18 us: 7 for a walk without
+// 32 trees of 61 nodes over 131072 tokens in fp32 take 18 to 23 us (six sets of
+// inputs) by the rejections of the longest walk: 7 for a walk without
 // rejections (launch, gather, one sum of p, the draw), 2 for a first rejection's
 // sum (a = 1), 5 for each further one and for the draw behind it; 16-bit
 // probabilities take as long. The busiest SMs issue half of the time (about 45
 // instructions for two weights of p - a q); the rest are waits for loads, the
-// cluster's barriers and the walk. What was slower: the next batch's loads ahead of a batch's sums, in
-// registers (spills, 26) or through shared memory (21); 512 threads (25).
+// cluster's barriers and the walk. What was slower: the next batch's loads ahead
+// of a batch's sums, in registers (spills, 26) or through shared memory (21); 512
+// threads (25).
 #include <type_traits>
 #include "st_kernels.h"
 #include "st_serve.h"

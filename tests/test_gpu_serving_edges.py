@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import _serving as R
-from test_gpu_serving import D, DT, Loop, bits, dev_cache, i32, rand
+from test_gpu_serving import D, DT, Loop, attn_case, bits, dev_cache, i32, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -306,3 +306,28 @@ def test_verify_every_token_removed(cuda_lib):
     got = [t.cpu() for t in cuda_lib.st_tree_verify(*(t.cuda() for t in case))]
     for x, w in zip(got, R.verify(*case)):
         assert torch.equal(x, w)
+
+
+@pytest.mark.parametrize("dtype,page,T,is_tree", [("bf16", 16, 1, False), ("fp16", 64, 61, True), ("fp32", 16, 5, True), ("bf16", 7, 3, False)])
+def test_narrowed_page_table(cuda_lib, dtype, page, T, is_tree):
+    """A view of a wide page table's first columns, in all three calls that read one: what the table itself gives, within
+    the bound (the two may be planned in different forms), and the same writes."""
+    B, H, Hkv, lens = 3, 8, 2, [777, 5, 300]
+    full = [n + T for n in lens]
+    q, k, v, pages, parents = attn_case(dtype, B, T, H, Hkv, lens, None, page, is_tree, seed=60)
+    wide = torch.cat((pages, torch.full((B, 150000 // page), -5, dtype=torch.int32)), 1).cuda()
+    bound = -(-max(full) // page)
+    ro, rl, bo, bl = R.attention(q, k, v, pages, lens, None, parents)
+    w, ids = torch.ones(D, device="cuda"), torch.arange(T, dtype=torch.int32, device="cuda")[None, :, None].contiguous()
+    new = rand(61, B, T, Hkv, D, dtype=DT[dtype]).cuda()
+    after = []
+    for table in (wide, wide[:, :bound]):
+        cache = cuda_lib.KVCache(k.cuda(), v.cuda(), table)
+        o, lse = cuda_lib.st_cache_attn(q.cuda(), cache, i32(lens).cuda(), parents=None if parents is None else parents.cuda())
+        R.close("o", o, ro, bo)
+        R.close("lse", lse, rl, bl)
+        qr = cuda_lib.st_cache_append(q.cuda(), new, new, w, w, 1e-6, ids, (128,), 1e4, cache, i32(lens).cuda())
+        got = cuda_lib.st_cache_keep(cache, i32([0, 0, 0]).cuda(), i32([[1, 4]] * B).cuda(), i32([2, 2, 0]).cuda())
+        cuda_lib.st_check_status()
+        after.append([bits(t) for t in (qr, cache.k, cache.v, got)])
+    assert all(torch.equal(x, y) for x, y in zip(*after))
