@@ -369,9 +369,10 @@ def st_cache_attn_workspace_size(q_rot, cache, parents=None) -> int:
     c = st_kv_cache()
     keep = [_t(cache.k), _t(cache.v), _t(cache.pages)]
     c.k, c.v, c.pages = (_p(x) for x in keep)
-    n = lib().st_cache_attn_workspace_size(_p(_t(q_rot)), ctypes.byref(c), _p(_t(parents)))
-    if n == 0:
-        raise StError(ST_ERR_INVALID_ARG, lib().st_last_error().decode())
+    q, par = _t(q_rot), _t(parents)
+    n = lib().st_cache_attn_workspace_size(_p(q), ctypes.byref(c), _p(par))
+    if n == 0:  # refused arguments: the call, which plans first, has the status
+        _check(lib().st_cache_attn(_p(q), ctypes.byref(c), None, None, _p(par), 0.0, None, None, None, 0, None))
     return int(n)
 
 

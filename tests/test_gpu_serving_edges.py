@@ -98,6 +98,9 @@ def test_attention_refusals_keep_their_status_in_python(cuda_lib):
             with pytest.raises(E.StError, match=text) as e:
                 E.st_cache_attn(q, c, lens, parents=parents, workspace=w)
             assert e.value.status == status, (text, w is None, e.value.status)
+        with pytest.raises(E.StError, match=text) as e:
+            E.st_cache_attn_workspace_size(q, c, parents)
+        assert e.value.status == status, (text, e.value.status)
 
 
 def test_fp16_attention_keeps_a_long_tail(cuda_lib):
