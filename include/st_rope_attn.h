@@ -81,7 +81,9 @@ typedef enum {
   ST_ERR_UNSUPPORTED = 8  /* valid request outside what this build implements */
 } st_status;
 
-typedef enum { ST_BF16 = 0, ST_F16 = 1, ST_F32 = 2, ST_BOOL = 3, ST_I32 = 4, ST_I64 = 5 } st_dtype;
+/* ST_E4M3 (8-bit floats: 4 exponent and 3 mantissa bits, no infinities) and
+ * ST_I8 are types of caches only. */
+typedef enum { ST_BF16 = 0, ST_F16 = 1, ST_F32 = 2, ST_BOOL = 3, ST_I32 = 4, ST_I64 = 5, ST_E4M3 = 6, ST_I8 = 7 } st_dtype;
 
 /* A strided view. Strides are in elements. Unused trailing dims are ignored. */
 typedef struct {
@@ -162,7 +164,7 @@ enum {
   ST_K_CACHE_ATTN = 10,   /* st_cache_attn: attention over the cache */
   ST_K_CACHE_JOIN = 11,   /* st_cache_attn: joining the parts of split rows */
   ST_K_VERIFY = 12,       /* st_tree_verify */
-  ST_K_CACHE_KEEP = 13,   /* st_cache_keep */
+  ST_K_CACHE_KEEP = 13,   /* st_cache_keep, st_cache_read */
   ST_K_KINDS = 14
 };
 
@@ -290,12 +292,23 @@ ST_API st_status st_rope_attn_fwd_noalloc(const st_tensor* q, const st_tensor* k
  * lens:   [B] int32, contiguous: tokens of each sequence in the cache before
  *   the new rows, which take the positions lens[b], lens[b] + 1, ...
  * counts: [B] int32, contiguous, or NULL (all T): how many of the T new rows
- *   sequence b has (0..T); the rows behind them are padding. */
+ *   sequence b has (0..T); the rows behind them are padding.
+ * A cache of 8 bits (k, v of ST_E4M3 or ST_I8) comes with its scales and goes
+ * to the calls that take them: st_cache_append_held, st_cache_attn_opt,
+ * st_cache_read and st_cache_keep_held. */
 typedef struct {
   const st_tensor* k;
   const st_tensor* v;
   const st_tensor* pages;
 } st_kv_cache;
+
+/* The scales of a cache of 8 bits: [N_pages, H_kv, page] fp32 each, unit stride
+ * on page. Element d of the row of token and head with scale s and held values c
+ * stands for s * c[d]. */
+typedef struct {
+  const st_tensor* k;
+  const st_tensor* v;
+} st_kv_scales;
 
 /* New rows enter the cache. The norm is always taken, and the rotation turns
  * neighbouring elements (2 p, 2 p + 1) of a head, as everywhere in this library:
@@ -316,6 +329,28 @@ typedef struct {
 ST_API st_status st_cache_append(const st_tensor* q, const st_tensor* k, const st_tensor* v, const st_tensor* q_norm_w,
                                  const st_tensor* k_norm_w, float eps, const st_rope* rope, const st_kv_cache* cache,
                                  const st_tensor* lens, const st_tensor* counts, st_tensor* q_rot, void* stream);
+
+/* The same into a cache of 8 bits (scales = NULL: st_cache_append). v may be
+ * bf16, fp16 or fp32, q and k of that type or both fp32, and q_rot is of v's
+ * type. A row (a token and K/V head) of the rotated k, in fp32, and of v is held
+ * as c[d] = x[d] / s rounded to nearest even, with s = max |x[d]| / 448 (E4M3) or
+ * / 127 (I8): each value is off by at most half a step of what is held. Rows
+ * whose s would be below 2^-100 are held as zeros with s = 0; a row with an
+ * infinity or NaN has it in its scale and reads as NaN. */
+ST_API st_status st_cache_append_held(const st_tensor* q, const st_tensor* k, const st_tensor* v, const st_tensor* q_norm_w,
+                                      const st_tensor* k_norm_w, float eps, const st_rope* rope, const st_kv_cache* cache,
+                                      const st_kv_scales* scales, const st_tensor* lens, const st_tensor* counts,
+                                      st_tensor* q_rot, void* stream);
+
+/* Rows leave the cache: positions start[b] .. start[b] + T - 1 of each sequence
+ * into k and v, [B, T, H_kv, D] both, not expanded, in the cache's dtype or, from
+ * a cache of 8 bits, in bf16, fp16 or fp32 (s * c[d] in fp32, rounded once).
+ *  start:   [B] int32, contiguous; counts: [B] int32 or NULL (all T): the rows
+ *           that are wanted; those behind them are zero.
+ * Rows whose position is negative or beyond the page table, or whose page number
+ * is out of range, are zero, too. */
+ST_API st_status st_cache_read(const st_kv_cache* cache, const st_kv_scales* scales, const st_tensor* start,
+                               const st_tensor* counts, st_tensor* k, st_tensor* v, void* stream);
 
 /* Bytes of device workspace that st_cache_attn needs (0 on invalid arguments,
  * the error then in st_last_error; a call without rows needs 256). */
@@ -348,6 +383,42 @@ ST_API size_t st_cache_attn_workspace_size(const st_tensor* q_rot, const st_kv_c
 ST_API st_status st_cache_attn(const st_tensor* q_rot, const st_kv_cache* cache, const st_tensor* lens,
                                const st_tensor* counts, const st_tensor* parents, float scale, st_tensor* o,
                                st_tensor* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* st_cache_attn with more: a cache of 8 bits, a sliding window, a prefix that all
+ * sequences share. opts = NULL, or all zero, is st_cache_attn; its words hold
+ * here too. The workspace of a call is that of st_cache_attn_opt_workspace_size
+ * for the same opts.
+ *  scales:  the scales of a cache of 8 bits, else NULL. q_rot is then bf16, fp16
+ *           or fp32 and o of its type; the held values enter the products exactly,
+ *           scales and sums are fp32, the softmax weights times V's scales are
+ *           rounded to fp16 (relative to the largest scale of 128 keys; scales of
+ *           V are good from 2^-80 to 2^80), with fp32 rows nothing is. The scales
+ *           of keys that no row sees are not used.
+ *  window:  0: none. Else a row at position p sees, of the keys that it would see
+ *           without, those at positions above p - window and those below sinks.
+ *           Positions are lens[b] + t for a chain, lens[b] plus the number of its
+ *           ancestors for a node of a tree. Keys that no row sees are not read,
+ *           nor are pages that hold no other: their table entries may be anything.
+ *  sinks:   first tokens that stay visible (only with a window).
+ *  shared:  [1] int32 on the device, or NULL: the first shared[0] tokens of every
+ *           sequence that has rows lie in the same pages. What is a multiple of
+ *           128 of them (at most of the least of those lens) is read once for all
+ *           rows, from the first such sequence's pages, by the tensor-core kernel;
+ *           it changes the time, not what is computed. Not used with a window, and
+ *           by the kernel without tensor cores. */
+typedef struct {
+  const st_kv_scales* scales;
+  int32_t window;
+  int32_t sinks;
+  const st_tensor* shared;
+} st_cache_attn_opts;
+
+ST_API size_t st_cache_attn_opt_workspace_size(const st_tensor* q_rot, const st_kv_cache* cache, const st_cache_attn_opts* opts,
+                                               const st_tensor* parents);
+
+ST_API st_status st_cache_attn_opt(const st_tensor* q_rot, const st_kv_cache* cache, const st_cache_attn_opts* opts,
+                                   const st_tensor* lens, const st_tensor* counts, const st_tensor* parents, float scale,
+                                   st_tensor* o, st_tensor* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Verification of drafted tokens by speculative rejection sampling from given
  * random numbers.
@@ -394,6 +465,9 @@ ST_API st_status st_tree_verify(const st_tensor* target_probs, const st_tensor* 
  * not be shared. */
 ST_API st_status st_cache_keep(const st_kv_cache* cache, const st_tensor* start, const st_tensor* rows,
                                const st_tensor* n_rows, st_tensor* lens, void* stream);
+/* The same for a cache of 8 bits: scales move with their rows. */
+ST_API st_status st_cache_keep_held(const st_kv_cache* cache, const st_kv_scales* scales, const st_tensor* start,
+                                    const st_tensor* rows, const st_tensor* n_rows, st_tensor* lens, void* stream);
 
 /* Message of the last failing call on this thread ("" if none). */
 ST_API const char* st_last_error(void);

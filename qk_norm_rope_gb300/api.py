@@ -9,8 +9,10 @@ Names follow the C-ABI: ``st_rope_attn_fwd``, ``st_rope_attn_bwd``,
 ``st_rope_attn_workspace_size``, ``st_get_stats``, ``st_reset_stats``,
 ``st_check_status``, ``st_last_error``. ``rope_attention`` wraps the pair in a
 ``torch.autograd.Function``. The serving calls, over a paged ``KVCache``:
-``st_cache_append``, ``st_cache_attn``, ``st_tree_verify``, ``st_cache_keep``
-(forward only: their results carry no gradient, also where inputs require one).
+``st_cache_append``, ``st_cache_attn``, ``st_tree_verify``, ``st_cache_keep``,
+``st_cache_read`` (forward only: their results carry no gradient, also where
+inputs require one). The C calls with ``_held`` and ``_opt`` in their names are
+these with a cache of 8 bits or with a window or shared prefix.
 
 The rotation is given either by position ids (``ids``, ``axes_dim``,
 ``theta``) or, in the form of the "Fused RoPE + SDPA" entry point, by
@@ -31,9 +33,9 @@ from . import build as _build
 
 ST_OK, ST_ERR_INVALID_ARG, ST_ERR_DTYPE, ST_ERR_SHAPE, ST_ERR_ALIGN, ST_ERR_WORKSPACE, ST_ERR_CUDA, \
     ST_ERR_TIMEOUT, ST_ERR_UNSUPPORTED = range(9)
-ST_BF16, ST_F16, ST_F32, ST_BOOL, ST_I32, ST_I64 = range(6)
+ST_BF16, ST_F16, ST_F32, ST_BOOL, ST_I32, ST_I64, ST_E4M3, ST_I8 = range(8)
 _DTYPES = {torch.bfloat16: ST_BF16, torch.float16: ST_F16, torch.float32: ST_F32, torch.bool: ST_BOOL,
-           torch.int32: ST_I32, torch.int64: ST_I64}
+           torch.int32: ST_I32, torch.int64: ST_I64, torch.float8_e4m3fn: ST_E4M3, torch.int8: ST_I8}
 STATUS_NAMES = ["ST_OK", "ST_ERR_INVALID_ARG", "ST_ERR_DTYPE", "ST_ERR_SHAPE", "ST_ERR_ALIGN", "ST_ERR_WORKSPACE",
                 "ST_ERR_CUDA", "ST_ERR_TIMEOUT", "ST_ERR_UNSUPPORTED"]
 
@@ -70,15 +72,26 @@ class st_kv_cache(ctypes.Structure):
                 ("pages", ctypes.POINTER(st_tensor))]
 
 
+class st_kv_scales(ctypes.Structure):
+    _fields_ = [("k", ctypes.POINTER(st_tensor)), ("v", ctypes.POINTER(st_tensor))]
+
+
+class st_cache_attn_opts(ctypes.Structure):
+    _fields_ = [("scales", ctypes.POINTER(st_kv_scales)), ("window", ctypes.c_int32), ("sinks", ctypes.c_int32),
+                ("shared", ctypes.POINTER(st_tensor))]
+
+
 class KVCache:
     """A paged K/V cache: ``k``, ``v`` [N_pages, page, H_kv, D] (bf16, fp16 or
-    fp32) and the page table ``pages`` [B, max_pages] int32; token ``pos`` of
-    sequence ``b`` lies in row ``pos % page`` of page ``pages[b, pos // page]``.
-    Holds references only: allocating pages and filling the table is the
-    caller's."""
+    fp32; 8-bit: float8_e4m3fn or int8) and the page table ``pages``
+    [B, max_pages] int32; token ``pos`` of sequence ``b`` lies in row
+    ``pos % page`` of page ``pages[b, pos // page]``. A cache of 8 bits has
+    ``k_scale`` and ``v_scale``, [N_pages, H_kv, page] fp32: a row stands for
+    its scale times what it holds. Holds references only: allocating pages and
+    filling the table is the caller's."""
 
-    def __init__(self, k, v, pages):
-        self.k, self.v, self.pages = k, v, pages
+    def __init__(self, k, v, pages, k_scale=None, v_scale=None):
+        self.k, self.v, self.pages, self.k_scale, self.v_scale = k, v, pages, k_scale, v_scale
 
 
 class st_stats(ctypes.Structure):
@@ -149,6 +162,16 @@ def lib():
             L.st_cache_attn_workspace_size.restype = sz
             L.st_cache_attn.argtypes = [vp] * 5 + [fl] + [vp] * 3 + [sz, vp]
             L.st_cache_attn.restype = i
+            L.st_cache_append_held.argtypes = [vp] * 5 + [fl] + [vp] * 7
+            L.st_cache_append_held.restype = i
+            L.st_cache_attn_opt_workspace_size.argtypes = [vp] * 4
+            L.st_cache_attn_opt_workspace_size.restype = sz
+            L.st_cache_attn_opt.argtypes = [vp] * 6 + [fl] + [vp] * 3 + [sz, vp]
+            L.st_cache_attn_opt.restype = i
+            L.st_cache_read.argtypes = [vp] * 7
+            L.st_cache_read.restype = i
+            L.st_cache_keep_held.argtypes = [vp] * 7
+            L.st_cache_keep_held.restype = i
             L.st_tree_verify.argtypes = [vp] * 11
             L.st_tree_verify.restype = i
             L.st_cache_keep.argtypes = [vp] * 6
@@ -356,34 +379,44 @@ def st_cache_append(q, k, v, q_norm_w, k_norm_w, eps, ids, axes_dim, theta, cach
     """New rows enter the cache: q [B,T,H,D], k, v [B,T,H_kv,D]; k normalised
     and rotated, and v, go to positions lens[b].. of each sequence. Returns the
     normalised, rotated q in the cache's dtype (zero in rows behind counts[b]),
-    without a gradient."""
+    without a gradient. Into a cache of 8 bits k' and v are quantised row by row,
+    and q comes back in v's dtype (bf16, fp16 or fp32)."""
     m = _bind_mod or _bind()
     if isinstance(ids, RopeTables):
         return m.cache_append(q, k, v, q_norm_w, k_norm_w, eps, None, ids.cos, ids.sin, ids.cos_k, ids.sin_k, (), 0.0,
-                              cache.k, cache.v, cache.pages, lens, counts, q_rot)
+                              cache.k, cache.v, cache.pages, cache.k_scale, cache.v_scale, lens, counts, q_rot)
     return m.cache_append(q, k, v, q_norm_w, k_norm_w, eps, ids, None, None, None, None, axes_dim, theta, cache.k, cache.v,
-                          cache.pages, lens, counts, q_rot)
+                          cache.pages, cache.k_scale, cache.v_scale, lens, counts, q_rot)
 
 
-def st_cache_attn_workspace_size(q_rot, cache, parents=None) -> int:
-    c = st_kv_cache()
-    keep = [_t(cache.k), _t(cache.v), _t(cache.pages)]
-    c.k, c.v, c.pages = (_p(x) for x in keep)
+def st_cache_attn_workspace_size(q_rot, cache, parents=None, window=0, sinks=0, shared=None) -> int:
+    c, opts, sc = st_kv_cache(), st_cache_attn_opts(), st_kv_scales()
+    keep = [_t(x) for x in (cache.k, cache.v, cache.pages, cache.k_scale, cache.v_scale, shared)]
+    c.k, c.v, c.pages, sc.k, sc.v, opts.shared = (_p(x) for x in keep)
+    opts.window, opts.sinks = window, sinks
+    if keep[3] or keep[4] or keep[0].dtype in (ST_E4M3, ST_I8):
+        opts.scales = ctypes.pointer(sc)
     q, par = _t(q_rot), _t(parents)
-    n = lib().st_cache_attn_workspace_size(_p(q), ctypes.byref(c), _p(par))
+    n = lib().st_cache_attn_opt_workspace_size(_p(q), ctypes.byref(c), ctypes.byref(opts), _p(par))
     if n == 0:  # refused arguments: the call, which plans first, has the status
-        _check(lib().st_cache_attn(_p(q), ctypes.byref(c), None, None, _p(par), 0.0, None, None, None, 0, None))
+        _check(lib().st_cache_attn_opt(_p(q), ctypes.byref(c), ctypes.byref(opts), None, None, _p(par), 0.0, None, None, None, 0,
+                                       None))
     return int(n)
 
 
-def st_cache_attn(q_rot, cache, lens, counts=None, parents=None, scale=None, o=None, lse=None, workspace=None):
+def st_cache_attn(q_rot, cache, lens, counts=None, parents=None, scale=None, o=None, lse=None, workspace=None, window=0,
+                  sinks=0, shared=None):
     """Attention of the new rows over the cache (after st_cache_append):
     parents=None for a chain (single tokens, a prompt's chunk), [B|1, T] int32
     for trees of drafted tokens. Returns (o [B,T,H,D], lse [B,H,T] fp32),
     without gradients. Planned by the room of cache.pages: a table narrowed to
-    a bound on the lengths is faster for few sequences."""
-    return (_bind_mod or _bind()).cache_attn(q_rot, cache.k, cache.v, cache.pages, lens, counts, parents, scale or 0.0, o,
-                                             lse, workspace)
+    a bound on the lengths is faster for few sequences.
+
+    window > 0: a row at position p sees keys at positions above p - window and
+    below sinks only. shared ([1] int32): that many first tokens lie in the same
+    pages for all sequences and are read once for the batch."""
+    return (_bind_mod or _bind()).cache_attn(q_rot, cache.k, cache.v, cache.pages, cache.k_scale, cache.v_scale, lens, counts,
+                                             parents, scale or 0.0, o, lse, workspace, window, sinks, shared)
 
 
 def st_tree_verify(target_probs, draft_probs, tokens, parents, u_accept, u_sample, counts=None, path=None,
@@ -397,7 +430,16 @@ def st_tree_verify(target_probs, draft_probs, tokens, parents, u_accept, u_sampl
 def st_cache_keep(cache, start, rows, n_rows, lens=None):
     """Row start[b] + rows[b, i] of each sequence moves to start[b] + i, for
     i < n_rows[b], in place. Returns the new lengths start + n_rows."""
-    return (_bind_mod or _bind()).cache_keep(cache.k, cache.v, cache.pages, start, rows, n_rows, lens)
+    return (_bind_mod or _bind()).cache_keep(cache.k, cache.v, cache.pages, cache.k_scale, cache.v_scale, start, rows, n_rows,
+                                             lens)
+
+
+def st_cache_read(cache, start, n_rows, counts=None, dtype=None, k=None, v=None):
+    """Rows start[b] .. start[b] + n_rows - 1 of each sequence out of the cache,
+    zero behind counts[b]: (k, v), [B, n_rows, H_kv, D] both, in the cache's
+    dtype, from a cache of 8 bits in ``dtype`` (bf16 unless given)."""
+    return (_bind_mod or _bind()).cache_read(cache.k, cache.v, cache.pages, cache.k_scale, cache.v_scale, start, n_rows, counts,
+                                             dtype, k, v)
 
 
 class RopeAttention(torch.autograd.Function):

@@ -93,7 +93,7 @@ int elem_bytes(int dt) {
     case ST_BF16: case ST_F16: return 2;
     case ST_F32: case ST_I32: return 4;
     case ST_I64: return 8;
-    case ST_BOOL: return 1;
+    case ST_BOOL: case ST_E4M3: case ST_I8: return 1;
     default: return 0;
   }
 }

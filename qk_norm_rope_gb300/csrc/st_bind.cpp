@@ -8,6 +8,7 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstring>
@@ -50,6 +51,8 @@ struct Call {
       case at::kBool: s->dtype = ST_BOOL; break;
       case at::kInt: s->dtype = ST_I32; break;
       case at::kLong: s->dtype = ST_I64; break;
+      case at::kFloat8_e4m3fn: s->dtype = ST_E4M3; break;
+      case at::kChar: s->dtype = ST_I8; break;
       default: throw Refused(ST_ERR_DTYPE, std::string("unsupported dtype of ") + name);
     }
     const int64_t n = t.dim();
@@ -155,9 +158,12 @@ void launch(int dev, F&& fn) {
 }
 
 struct Cache {
-  st_tensor k, v, pages;
+  st_tensor k, v, pages, ks, vs;
   st_kv_cache c;
+  st_kv_scales sc;
+  const st_kv_scales* scales;  // NULL where neither is given
   at::ScalarType type;
+  // a: k, v, pages, k_scale, v_scale
   void take(Call& call, PyObject* const* a) {
     const at::Tensor* kt = call.tensor(a[0], "cache.k");
     if (!kt) throw Refused(ST_ERR_INVALID_ARG, "cache.k is None");
@@ -166,12 +172,16 @@ struct Cache {
     c.k = &k;
     c.v = call.view(a[1], &v, "cache.v");
     c.pages = call.view(a[2], &pages, "cache.pages");
+    sc.k = call.view(a[3], &ks, "cache.k_scale");
+    sc.v = call.view(a[4], &vs, "cache.v_scale");
+    scales = sc.k || sc.v || held() ? &sc : nullptr;
   }
+  bool held() const { return type == at::kFloat8_e4m3fn || type == at::kChar; }
 };
 
-// q, k, v, wq, wk, eps, ids, cos, sin, cos_k, sin_k, axes, theta, cache (3), lens, counts, q_rot
+// q, k, v, wq, wk, eps, ids, cos, sin, cos_k, sin_k, axes, theta, cache (5), lens, counts, q_rot
 PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 19, [&]() -> PyObject* {
+  return guarded(n, 21, [&]() -> PyObject* {
     Call c;
     st_tensor s[12];
     Cache kv;
@@ -196,50 +206,58 @@ PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     r.n_axes = static_cast<int32_t>(na);
     r.theta = number(a[12]);
     kv.take(c, a + 13);
-    st_tensor *lens = c.view(a[16], &s[10], "lens"), *counts = c.view(a[17], &s[11], "counts");
+    st_tensor *lens = c.view(a[18], &s[10], "lens"), *counts = c.view(a[19], &s[11], "counts");
     Out o;
-    o.take(c, a[18], "q_rot", qt->sizes(), kv.type);
-    launch(c.dev, [&](void* st) { return st_cache_append(q, k, v, wq, wk, eps, &r, &kv.c, lens, counts, &o.s, st); });
+    o.take(c, a[20], "q_rot", qt->sizes(), kv.held() && v ? c.tensor(a[2], "v")->scalar_type() : kv.type);
+    launch(c.dev, [&](void* st) { return st_cache_append_held(q, k, v, wq, wk, eps, &r, &kv.c, kv.scales, lens, counts, &o.s, st); });
     return o.py();
   });
 }
 
-// q_rot, cache (3), lens, counts, parents, scale, o, lse, workspace
+int32_t count(PyObject* o, const char* name) {
+  const long v = PyLong_AsLong(o);
+  if (v == -1 && PyErr_Occurred()) throw Refused(-1, "");
+  if (v != static_cast<int32_t>(v)) throw Refused(ST_ERR_INVALID_ARG, std::string(name) + " is out of range");
+  return static_cast<int32_t>(v);
+}
+
+// q_rot, cache (5), lens, counts, parents, scale, o, lse, workspace, window, sinks, shared
 PyObject* cache_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 11, [&]() -> PyObject* {
+  return guarded(n, 16, [&]() -> PyObject* {
     Call c;
-    st_tensor s[4];
+    st_tensor s[5];
     Cache kv;
     const at::Tensor* qt = c.tensor(a[0], "q_rot");
     if (!qt) throw Refused(ST_ERR_INVALID_ARG, "q_rot is None");
     st_tensor* q = c.view(a[0], &s[0], "q_rot");
     kv.take(c, a + 1);
-    st_tensor *lens = c.view(a[4], &s[1], "lens"), *counts = c.view(a[5], &s[2], "counts"), *par = c.view(a[6], &s[3], "parents");
-    const float scale = static_cast<float>(number(a[7]));
+    st_tensor *lens = c.view(a[6], &s[1], "lens"), *counts = c.view(a[7], &s[2], "counts"), *par = c.view(a[8], &s[3], "parents");
+    const float scale = static_cast<float>(number(a[9]));
+    const st_cache_attn_opts opts{kv.scales, count(a[13], "window"), count(a[14], "sinks"), c.view(a[15], &s[4], "shared")};
     const int64_t B = dim_of(*qt, 0, "q_rot"), T = dim_of(*qt, 1, "q_rot"), H = dim_of(*qt, 2, "q_rot");
     Out o, lse;
-    o.take(c, a[8], "o", qt->sizes(), qt->scalar_type());
-    lse.take(c, a[9], "lse", {B, H, T}, at::kFloat);
+    o.take(c, a[10], "o", qt->sizes(), qt->scalar_type());
+    lse.take(c, a[11], "lse", {B, H, T}, at::kFloat);
     at::Tensor ws;
     void* wp;
     size_t wn;
-    if (a[10] == Py_None) {
-      wn = st_cache_attn_workspace_size(q, &kv.c, par);
+    if (a[12] == Py_None) {
+      wn = st_cache_attn_opt_workspace_size(q, &kv.c, &opts, par);
       // a size of 0: refused arguments, for which the call itself has the status (it
       // plans first and needs no workspace to refuse)
       if (wn == 0) {
-        check(st_cache_attn(q, &kv.c, lens, counts, par, scale, &o.s, &lse.s, nullptr, 0, nullptr));
+        check(st_cache_attn_opt(q, &kv.c, &opts, lens, counts, par, scale, &o.s, &lse.s, nullptr, 0, nullptr));
         throw Refused(ST_ERR_INVALID_ARG, "the workspace has no size");
       }
       ws = new_tensor({static_cast<int64_t>(wn)}, at::kByte, c.dev);
       wp = ws.data_ptr();
     } else {
-      const at::Tensor* w = c.tensor(a[10], "workspace");
+      const at::Tensor* w = c.tensor(a[12], "workspace");
       if (!w->is_contiguous()) throw Refused(ST_ERR_INVALID_ARG, "the workspace must be contiguous");
       wp = w->numel() > 0 ? w->data_ptr() : nullptr;
       wn = w->nbytes();
     }
-    launch(c.dev, [&](void* st) { return st_cache_attn(q, &kv.c, lens, counts, par, scale, &o.s, &lse.s, wp, wn, st); });
+    launch(c.dev, [&](void* st) { return st_cache_attn_opt(q, &kv.c, &opts, lens, counts, par, scale, &o.s, &lse.s, wp, wn, st); });
     PyObject *x = o.py(), *y = lse.py();
     PyObject* r = x && y ? PyTuple_Pack(2, x, y) : nullptr;
     Py_XDECREF(x);
@@ -274,20 +292,49 @@ PyObject* tree_verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// cache (3), start, rows, n_rows, lens
+// cache (5), start, rows, n_rows, lens
 PyObject* cache_keep(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 7, [&]() -> PyObject* {
+  return guarded(n, 9, [&]() -> PyObject* {
     Call c;
     st_tensor s[3];
     Cache kv;
     kv.take(c, a);
-    const at::Tensor* st0 = c.tensor(a[3], "start");
+    const at::Tensor* st0 = c.tensor(a[5], "start");
     if (!st0) throw Refused(ST_ERR_INVALID_ARG, "start is None");
-    st_tensor *start = c.view(a[3], &s[0], "start"), *rows = c.view(a[4], &s[1], "rows"), *cnt = c.view(a[5], &s[2], "n_rows");
+    st_tensor *start = c.view(a[5], &s[0], "start"), *rows = c.view(a[6], &s[1], "rows"), *cnt = c.view(a[7], &s[2], "n_rows");
     Out lens;
-    lens.take(c, a[6], "lens", st0->sizes(), at::kInt);
-    launch(c.dev, [&](void* st) { return st_cache_keep(&kv.c, start, rows, cnt, &lens.s, st); });
+    lens.take(c, a[8], "lens", st0->sizes(), at::kInt);
+    launch(c.dev, [&](void* st) { return st_cache_keep_held(&kv.c, kv.scales, start, rows, cnt, &lens.s, st); });
     return lens.py();
+  });
+}
+
+// cache (5), start, T, counts, dtype (a torch.dtype or None), k, v
+PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 11, [&]() -> PyObject* {
+    Call c;
+    st_tensor s[2];
+    Cache kv;
+    kv.take(c, a);
+    st_tensor *start = c.view(a[5], &s[0], "start"), *counts = c.view(a[7], &s[1], "counts");
+    const int64_t T = count(a[6], "n_rows");
+    if (T < 0) throw Refused(ST_ERR_INVALID_ARG, "n_rows must be at least 0");
+    at::ScalarType ty = kv.held() ? at::kBFloat16 : kv.type;
+    if (a[8] != Py_None) {
+      if (!THPDtype_Check(a[8])) throw Refused(ST_ERR_INVALID_ARG, "dtype must be a torch.dtype");
+      ty = reinterpret_cast<THPDtype*>(a[8])->scalar_type;
+    }
+    const int64_t B = dim_of(*c.tensor(a[2], "cache.pages"), 0, "cache.pages"), H = dim_of(*c.tensor(a[0], "cache.k"), 2, "cache.k");
+    const int64_t D = dim_of(*c.tensor(a[0], "cache.k"), 3, "cache.k");
+    Out k, v;
+    k.take(c, a[9], "k", {B, T, H, D}, ty);
+    v.take(c, a[10], "v", {B, T, H, D}, ty);
+    launch(c.dev, [&](void* st) { return st_cache_read(&kv.c, kv.scales, start, counts, &k.s, &v.s, st); });
+    PyObject *x = k.py(), *y = v.py();
+    PyObject* r = x && y ? PyTuple_Pack(2, x, y) : nullptr;
+    Py_XDECREF(x);
+    Py_XDECREF(y);
+    return r;
   });
 }
 
@@ -303,6 +350,7 @@ PyMethodDef kMethods[] = {{"init", init, METH_O, nullptr},
                           {"cache_attn", ST_FAST(cache_attn)},
                           {"tree_verify", ST_FAST(tree_verify)},
                           {"cache_keep", ST_FAST(cache_keep)},
+                          {"cache_read", ST_FAST(cache_read)},
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "st_bind", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,5 +1,6 @@
 // The cache's writers: append (RMS norm + rotation of new q/k rows, k' and v
-// into their pages) and keep (rows of a sequence move up).
+// into their pages) and keep (rows of a sequence move up); and read, which
+// brings rows back.
 #include <algorithm>
 #include <atomic>
 #include "st_kernels.h"
@@ -83,9 +84,43 @@ __device__ __forceinline__ float2 append_pair(const AppendParams& p, int b, int 
   return cs;
 }
 
-// SRC: type of q and k; DST: of v and the cache. u_q, u_k: units of a token's q
-// rows, and of its k (and v) rows.
-template <int NI, int SRC, int DST>
+// A row of a cache of 8 bits, eight of its elements per lane of a half-warp: its
+// scale s = max |x| / top and x / s rounded to nearest even, so that each value
+// is off by half a step of the held type. The magnitudes are compared as
+// integers, where NaN stands above infinity and that above every number: a row
+// with one of them gets it as its scale and reads as NaN.
+template <int KV>
+__device__ __forceinline__ uint2 hold_row(const float (&y)[8], float* scale) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(y[e]) & 0x7fffffffu);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float s = __uint_as_float(top) / top_of(KV);
+  const bool none = s < kMinScale;
+  const float inv = none ? 0.f : 1.f / s;
+  *scale = none ? 0.f : s;
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float *x = y + 4 * i;
+    if constexpr (KV == kDtE4M3) {
+      asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\tmov.b32 %0, {a, b};\n}"
+          : "=r"(w[i]) : "f"(x[0] * inv), "f"(x[1] * inv), "f"(x[2] * inv), "f"(x[3] * inv));
+    } else {
+      uint32_t v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = static_cast<uint32_t>(__float2int_rn(x[e] * inv));
+      w[i] = __byte_perm(__byte_perm(v[0], v[1], 0x0040), __byte_perm(v[2], v[3], 0x0040), 0x5410);
+    }
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// SRC: type of q and k; DST: of v, q' and (KV = 0) the cache; KV: kDtE4M3 or
+// kDtI8, a cache of that type. u_q, u_k: units of a token's q rows, and of its k
+// (and v) rows.
+template <int NI, int SRC, int DST, int KV>
 __global__ void __launch_bounds__(kAppWarps * 32) append_kernel(const __grid_constant__ AppendParams p, int u_q, int u_k) {
   __shared__ float4 tab[kAppWarps][kPairs / 2];
   grid_dependency_wait();
@@ -112,6 +147,8 @@ __global__ void __launch_bounds__(kAppWarps * 32) append_kernel(const __grid_con
   void* out = p.qo;
   int64_t o_off = q_off, o_sh = p.qo_sh;
   bool room = true;
+  float* sc_out = nullptr;  // the rows' scales
+  int64_t sc_sh = 0;
   auto find_slot = [&]() {
     int pg = 0, row = 0;
     const int len = ld_now(p.lens + b);
@@ -122,14 +159,36 @@ __global__ void __launch_bounds__(kAppWarps * 32) append_kernel(const __grid_con
     o_sh = kind == 1 ? p.kv.k_sh : p.kv.v_sh;
     o_off = kind == 1 ? pg * p.kv.k_sp + row * p.kv.k_sr : pg * p.kv.v_sp + row * p.kv.v_sr;
     o_off += 8 * l;
+    if constexpr (KV != 0) {
+      sc_out = kind == 1 ? p.kv.ks + pg * p.kv.ks_sp + row : p.kv.vs + pg * p.kv.vs_sp + row;
+      sc_sh = kind == 1 ? p.kv.ks_sh : p.kv.vs_sh;
+    }
+  };
+  auto hold = [&](const float (&y)[8], int h) {  // every lane calls it
+    if constexpr (KV != 0) {
+      float s;
+      const uint2 w = hold_row<KV>(y, &s);
+      if (!room || h >= heads) return;
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(out) + o_off + h * o_sh) = w;
+      if (l == 0) sc_out[h * sc_sh] = s;
+    }
   };
   if (kind == 2) {
     const int64_t off = b * p.v.sb + t * p.v.ss + 8 * l;
     Raw8<DST> x[NI];
 #pragma unroll
     for (int i = 0; i < NI; ++i)
-      if (h0 + 2 * i < heads) x[i].load(p.v.p, off + (h0 + 2 * i) * p.v.sh);
+      if (KV != 0 || h0 + 2 * i < heads) x[i].load(p.v.p, off + min(h0 + 2 * i, heads - 1) * p.v.sh);
     find_slot();
+    if constexpr (KV != 0) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        float y[8];
+        x[i].get(y);
+        hold(y, h0 + 2 * i);
+      }
+      return;
+    }
     if (!room) return;
 #pragma unroll
     for (int i = 0; i < NI; ++i)
@@ -169,6 +228,10 @@ __global__ void __launch_bounds__(kAppWarps * 32) append_kernel(const __grid_con
       const float n0 = y[2 * e] * inv * wv[2 * e], n1 = y[2 * e + 1] * inv * wv[2 * e + 1];
       y[2 * e] = n0 * cs[e].x - n1 * cs[e].y;
       y[2 * e + 1] = n0 * cs[e].y + n1 * cs[e].x;
+    }
+    if (KV != 0 && kind == 1) {
+      hold(y, h0 + 2 * i);
+      continue;
     }
     Raw8<DST> r;
     r.set(y);
@@ -211,7 +274,10 @@ struct KeepLay {
   __host__ __device__ size_t bytes() const { return ring() + static_cast<size_t>(2) * tables * table * 8; }
 };
 
-template <int THREADS, int PER>
+// SC: a cache of 8 bits. Blocks from 2 Hkv on move the scales of one head, K's
+// and then V's: THREADS rows at a time are read, and written once all are read
+// (a later turn's rows lie behind all that this one writes).
+template <int THREADS, int PER, bool SC>
 __global__ void __launch_bounds__(THREADS) keep_kernel(const __grid_constant__ KeepParams p) {
   extern __shared__ __align__(16) uint8_t raw[];
   const KeepLay<THREADS, PER> lay(p.N, p.part_lanes);
@@ -229,8 +295,29 @@ __global__ void __launch_bounds__(THREADS) keep_kernel(const __grid_constant__ K
     p.lens[b] = start < 0 ? start : start + n;
   }
   if (start < 0) return;
+  if constexpr (SC) {
+    if (blockIdx.y >= 2 * p.kv.Hkv) {
+      if (blockIdx.x > 0) return;
+      const int u = blockIdx.y - 2 * p.kv.Hkv;
+      const bool v = u >= p.kv.Hkv;
+      float* sc = v ? p.kv.vs + (u - p.kv.Hkv) * p.kv.vs_sh : p.kv.ks + u * p.kv.ks_sh;
+      const int64_t sp = v ? p.kv.vs_sp : p.kv.ks_sp;
+      const int32_t* list = p.rows + b * p.r_sb;
+      for (int i0 = 0; i0 < n; i0 += THREADS) {
+        const int i = i0 + tid, r = i < n ? ld_now(list + i) : -1, before = i < n && i > 0 ? ld_now(list + i - 1) : -1;
+        int pg, row, pg2, row2;
+        const bool moves = i < n && r > i && r > before && kv_locate(p.kv, b, static_cast<int64_t>(start) + r, &pg, &row) &&
+                           kv_locate(p.kv, b, static_cast<int64_t>(start) + i, &pg2, &row2);
+        float s = 0.f;
+        if (moves) s = ld_now(sc + pg * sp + row);
+        __syncthreads();
+        if (moves) sc[pg2 * sp + row2] = s;
+      }
+      return;
+    }
+  }
 
-  const int eb = p.kv.dt == kDtF32 ? 4 : 2;
+  const int eb = p.kv.dt == kDtF32 ? 4 : (SC ? 1 : 2);
   const bool is_v = blockIdx.y >= p.kv.Hkv;
   const int h = is_v ? blockIdx.y - p.kv.Hkv : blockIdx.y;
   uint8_t* base = static_cast<uint8_t*>(is_v ? p.kv.v : p.kv.k) + h * (is_v ? p.kv.v_sh : p.kv.k_sh) * eb;
@@ -304,48 +391,156 @@ __global__ void __launch_bounds__(THREADS) keep_kernel(const __grid_constant__ K
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
+// -------------------------------------------------------------------- read
+// Rows of a cache into dense tensors: memory bound, each byte read and written
+// once. Eight lanes take a row, a warp 16 rows, K's and V's of one token where
+// these are so many: four rows are in flight per lane and the token's page is
+// looked up once. KV: 8-bit type of the cache, or 0: rows of type OUT are copied.
+constexpr int kReadWarps = 8, kReadRows = 16;
+template <int KV, int OUT>
+__global__ void __launch_bounds__(kReadWarps * 32) read_kernel(const __grid_constant__ ReadParams p, int tokens, int groups) {
+  // a unit: `tokens` tokens (where a token has fewer rows than 16), or a group of 16 rows of one
+  constexpr int kEs = OUT == kDtF32 ? 4 : 2, kPieces = KV != 0 ? 1 : kEs;  // 16-byte pieces a lane reads of a row
+  grid_dependency_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane & 7;
+  const unsigned unit = blockIdx.x * kReadWarps + warp, at = unit / static_cast<unsigned>(groups);
+  const int group = static_cast<int>(unit - at * groups), per = 2 * p.kv.Hkv;  // rows of a token
+  const unsigned all = static_cast<unsigned>(p.B) * p.T, tok0 = at * tokens;  // at most 2^30
+  if (tok0 >= all) return;
+  uint4 x[kReadRows / 4][kPieces];
+  float s[kReadRows / 4];
+  int where[kReadRows / 4];      // (head or Hkv + head), -1: no row of this unit
+  unsigned tok[kReadRows / 4];
+#pragma unroll
+  for (int u = 0; u < kReadRows / 4; ++u) {
+    const int r = 4 * u + (lane >> 3), step = tokens > 1 ? r / per : 0;
+    const int i = tokens > 1 ? r - step * per : group * kReadRows + r;
+    tok[u] = tok0 + step;
+    where[u] = i < per && step < tokens && tok[u] < all ? i : -1;
+    s[u] = 0.f;
+#pragma unroll
+    for (int c = 0; c < kPieces; ++c) x[u][c] = make_uint4(0, 0, 0, 0);
+    if (where[u] < 0) continue;
+    const int b = static_cast<int>(tok[u] / static_cast<unsigned>(p.T)), t = static_cast<int>(tok[u] - static_cast<unsigned>(b) * p.T);
+    if (t >= row_count(p.counts, b, p.T)) continue;
+    const int start = ld_now(p.start + b);
+    int pg, row;
+    if (start < 0 || !kv_locate(p.kv, b, static_cast<int64_t>(start) + t, &pg, &row)) {
+      if (l == 0) atomicOr(p.status, kStatusIndex);
+      continue;  // zeros
+    }
+    const bool v = i >= p.kv.Hkv;
+    const int h = v ? i - p.kv.Hkv : i;
+    const int64_t off = v ? pg * p.kv.v_sp + row * p.kv.v_sr + h * p.kv.v_sh : pg * p.kv.k_sp + row * p.kv.k_sr + h * p.kv.k_sh;
+    const uint8_t* src = static_cast<const uint8_t*>(v ? p.kv.v : p.kv.k) + off * (KV != 0 ? 1 : kEs);
+#pragma unroll
+    for (int c = 0; c < kPieces; ++c) x[u][c] = ld_v4(src + 16 * (l + 8 * c));
+    if constexpr (KV != 0) s[u] = v ? ld_now(p.kv.vs + pg * p.kv.vs_sp + h * p.kv.vs_sh + row) : ld_now(p.kv.ks + pg * p.kv.ks_sp + h * p.kv.ks_sh + row);
+  }
+#pragma unroll
+  for (int u = 0; u < kReadRows / 4; ++u) {
+    if (where[u] < 0) continue;
+    const int b = static_cast<int>(tok[u] / static_cast<unsigned>(p.T)), t = static_cast<int>(tok[u] - static_cast<unsigned>(b) * p.T);
+    const bool v = where[u] >= p.kv.Hkv;
+    const int h = v ? where[u] - p.kv.Hkv : where[u];
+    const int64_t off = v ? b * p.v_sb + t * p.v_ss + h * p.v_sh : b * p.k_sb + t * p.k_ss + h * p.k_sh;
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(v ? p.v : p.k) + off * kEs);
+    if constexpr (KV != 0) {
+      const uint32_t w[4] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w};
+      float y[16];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float z[4];
+        held4<KV>(w[e], z);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[4 * e + k] = z[k] * s[u];
+      }
+      if constexpr (OUT == kDtF32) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          dst[4 * l + c] = make_uint4(__float_as_uint(y[4 * c]), __float_as_uint(y[4 * c + 1]), __float_as_uint(y[4 * c + 2]), __float_as_uint(y[4 * c + 3]));
+      } else {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          dst[2 * l + c] = make_uint4(pack16<OUT == kDtF16>(y[8 * c], y[8 * c + 1]), pack16<OUT == kDtF16>(y[8 * c + 2], y[8 * c + 3]),
+                                      pack16<OUT == kDtF16>(y[8 * c + 4], y[8 * c + 5]), pack16<OUT == kDtF16>(y[8 * c + 6], y[8 * c + 7]));
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < kPieces; ++c) dst[l + 8 * c] = x[u][c];
+    }
+  }
+}
+
 }  // namespace
 
-template <int NI, int SRC, int DST>
+template <int NI, int SRC, int DST, int KV>
 cudaError_t launch_append_t(const AppendParams& p, cudaStream_t stream) {
   const int u_q = (p.H + 2 * NI - 1) / (2 * NI), u_k = (p.kv.Hkv + 2 * NI - 1) / (2 * NI);
   const int64_t units = static_cast<int64_t>(p.B) * p.T * (u_q + 2 * u_k);
-  return launch_chained(append_kernel<NI, SRC, DST>, dim3(static_cast<unsigned>((units + kAppWarps - 1) / kAppWarps)),
+  return launch_chained(append_kernel<NI, SRC, DST, KV>, dim3(static_cast<unsigned>((units + kAppWarps - 1) / kAppWarps)),
                         dim3(kAppWarps * 32), 0, stream, p, u_q, u_k);
 }
-template <int SRC, int DST>
+template <int SRC, int DST, int KV>
 cudaError_t launch_append_types(const AppendParams& p, cudaStream_t stream) {
   // as many rows per warp as still leave every SM (152) 32 warps: rows in
   // flight hide the reads, warps the rest
   const int64_t rows = static_cast<int64_t>(p.B) * p.T * (p.H + 2 * p.kv.Hkv);
-  if (rows >= 152 * 32 * 8) return launch_append_t<4, SRC, DST>(p, stream);
-  return launch_append_t<1, SRC, DST>(p, stream);
+  if (rows >= 152 * 32 * 8) return launch_append_t<4, SRC, DST, KV>(p, stream);
+  return launch_append_t<1, SRC, DST, KV>(p, stream);
 }
-
-cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t stream) {
+template <int KV>
+cudaError_t launch_append_kv(const AppendParams& p, cudaStream_t stream) {
   const bool f32 = p.q.dt == kDtF32;
-  switch (p.kv.dt) {
-    case kDtBF16: return f32 ? launch_append_types<kDtF32, kDtBF16>(p, stream) : launch_append_types<kDtBF16, kDtBF16>(p, stream);
-    case kDtF16: return f32 ? launch_append_types<kDtF32, kDtF16>(p, stream) : launch_append_types<kDtF16, kDtF16>(p, stream);
-    default: return launch_append_types<kDtF32, kDtF32>(p, stream);
+  switch (p.v.dt) {
+    case kDtBF16: return f32 ? launch_append_types<kDtF32, kDtBF16, KV>(p, stream) : launch_append_types<kDtBF16, kDtBF16, KV>(p, stream);
+    case kDtF16: return f32 ? launch_append_types<kDtF32, kDtF16, KV>(p, stream) : launch_append_types<kDtF16, kDtF16, KV>(p, stream);
+    default: return launch_append_types<kDtF32, kDtF32, KV>(p, stream);
   }
 }
 
-template <int THREADS, int PER>
+cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t stream) {
+  if (p.kv.dt == kDtE4M3) return launch_append_kv<kDtE4M3>(p, stream);
+  return p.kv.dt == kDtI8 ? launch_append_kv<kDtI8>(p, stream) : launch_append_kv<0>(p, stream);
+}
+
+template <int THREADS, int PER, bool SC>
 cudaError_t launch_keep_t(const KeepParams& p, cudaStream_t stream) {
   static std::atomic<uint64_t> configured{0};
   using Lay = KeepLay<THREADS, PER>;
   // the least part_lanes: 4, or 8 in wide CTAs
   static_assert(kKeepTable >= kKeepStages * (THREADS / (THREADS > 256 ? 8 : 4) * PER), "a table holds the chunks ahead");
-  cudaError_t e = opt_in_smem(keep_kernel<THREADS, PER>, kKeepStages * Lay::kChunkBytes + 4 * kKeepTable * 8, configured);
+  cudaError_t e = opt_in_smem(keep_kernel<THREADS, PER, SC>, kKeepStages * Lay::kChunkBytes + 4 * kKeepTable * 8, configured);
   if (e != cudaSuccess) return e;
-  const int row_lanes = kD * (p.kv.dt == kDtF32 ? 4 : 2) / 16;
-  return launch_chained(keep_kernel<THREADS, PER>, dim3(row_lanes / p.part_lanes, 2 * p.kv.Hkv, p.B), dim3(THREADS),
+  const int row_lanes = kD * (p.kv.dt == kDtF32 ? 4 : (SC ? 1 : 2)) / 16;
+  return launch_chained(keep_kernel<THREADS, PER, SC>, dim3(row_lanes / p.part_lanes, (SC ? 4 : 2) * p.kv.Hkv, p.B), dim3(THREADS),
                         Lay(p.N, p.part_lanes).bytes(), stream, p);
 }
 
 cudaError_t launch_cache_keep(const KeepParams& p, cudaStream_t stream) {
-  return p.wide ? launch_keep_t<1024, 2>(p, stream) : launch_keep_t<256, 4>(p, stream);
+  if (p.kv.ks) return p.wide ? launch_keep_t<1024, 2, true>(p, stream) : launch_keep_t<256, 4, true>(p, stream);
+  return p.wide ? launch_keep_t<1024, 2, false>(p, stream) : launch_keep_t<256, 4, false>(p, stream);
+}
+
+template <int KV, int OUT>
+cudaError_t launch_read_t(const ReadParams& p, cudaStream_t stream) {
+  const int per = 2 * p.kv.Hkv, tokens = per < kReadRows ? kReadRows / per : 1, groups = tokens > 1 ? 1 : (per + kReadRows - 1) / kReadRows;
+  const int64_t units = (static_cast<int64_t>(p.B) * p.T + tokens - 1) / tokens * groups;
+  return launch_chained(read_kernel<KV, OUT>, dim3(static_cast<unsigned>((units + kReadWarps - 1) / kReadWarps)), dim3(kReadWarps * 32), 0,
+                        stream, p, tokens, groups);
+}
+template <int KV>
+cudaError_t launch_read_kv(const ReadParams& p, cudaStream_t stream) {
+  switch (p.dt) {
+    case kDtBF16: return launch_read_t<KV, kDtBF16>(p, stream);
+    case kDtF16: return launch_read_t<KV, kDtF16>(p, stream);
+    default: return launch_read_t<KV, kDtF32>(p, stream);
+  }
+}
+
+cudaError_t launch_cache_read(const ReadParams& p, cudaStream_t stream) {
+  if (p.kv.dt == kDtE4M3) return launch_read_kv<kDtE4M3>(p, stream);
+  return p.kv.dt == kDtI8 ? launch_read_kv<kDtI8>(p, stream) : launch_read_kv<0>(p, stream);
 }
 
 }  // namespace st

@@ -1,6 +1,12 @@
 // Cached attention on the CUDA cores: fp32 caches (every product and sum in
-// fp32), and 16-bit caches whose pages the tensor-core kernel's boxes do not
-// fit (page sizes that are no multiple of 8).
+// fp32), 16-bit and 8-bit caches whose pages the tensor-core kernel's boxes do
+// not fit (page sizes that are no multiple of 8), and fp32 rows over 8-bit caches.
+//
+// EXT: the forms with a window or an 8-bit cache. A window's keys are two runs,
+// the first tokens and what the rows' windows hold; they are walked as one list
+// of units of 16 keys with a gap in it, and the mask goes by each key's position.
+// Values of 8 bits become fp32, times their row's scale, on their way into shared
+// memory. (Kept apart from the other form, whose code is as it was.)
 //
 // An item is kSimtRows query rows (token x head of the group) of one K/V head
 // of one sequence; its keys are walked in tiles of kSimtKeys. Few items are split
@@ -42,6 +48,10 @@ struct Smem {
   uint32_t anc[kR][kTreeWords];
   int64_t k_off[2][kN], v_off[2][kN];  // element offsets of a tile's rows, by its parity; < 0: no row
 };
+struct SmemExt : Smem {
+  int low[kR];                         // where the rows' windows begin
+  float ks[2][kN], vs[2][kN];          // scales
+};
 
 // Bit j of the result: node `first + j` is seen from a row whose ancestors
 // (itself included) are `anc`.
@@ -60,11 +70,17 @@ constexpr int kUnit = 16;
 constexpr int kMaxRanges = 128;  // of an item: the join goes through them
 // By a whole warp: the sequence that range y belongs to (b = -1: none), or, with
 // y < 0, the ranges of sequence b.
+template <bool EXT>
 __device__ Ranges find_ranges(const CacheAttnParams& p, int y, int b) {
   const int lane = threadIdx.x & 31;
   auto units = [&](int i) {
     int prefix;
-    return i < p.B ? (key_count(p, i, row_count(p.counts, i, p.T), &prefix) + kUnit - 1) / kUnit : 0;
+    if (i >= p.B) return 0;
+    const int n = (key_count(p, i, row_count(p.counts, i, p.T), &prefix) + kUnit - 1) / kUnit;
+    if constexpr (EXT) {
+      if (p.window > 0) return n - window_gap<kUnit>(p, window_low(p, i, 0), n).gap;
+    }
+    return n;
   };
   const int mine = units(lane);
   long long all = mine;
@@ -92,14 +108,17 @@ __device__ Ranges find_ranges(const CacheAttnParams& p, int y, int b) {
   return {-1, 0, 0};
 }
 
+// KV: kDtE4M3 or kDtI8 for a cache of that type, else 0 (p.kv.dt says).
+template <bool EXT, int KV>
 __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant__ CacheAttnParams p, int n_rt) {
   extern __shared__ __align__(16) uint8_t raw[];
-  Smem& s = *reinterpret_cast<Smem*>(raw);
+  using S = std::conditional_t<EXT, SmemExt, Smem>;
+  S& s = *reinterpret_cast<S*>(raw);
   grid_dependency_wait();
   const int tid = threadIdx.x;
   const unsigned it32 = blockIdx.x;  // items are at most 2^30: of a sequence, or (no split) of all
   const int rt = static_cast<int>(it32 % n_rt), hk = static_cast<int>(it32 / n_rt % p.kv.Hkv);
-  const Ranges range = p.splits > 0 ? find_ranges(p, blockIdx.y, 0) : Ranges{static_cast<int>(it32 / n_rt / p.kv.Hkv), 0, 1};
+  const Ranges range = p.splits > 0 ? find_ranges<EXT>(p, blockIdx.y, 0) : Ranges{static_cast<int>(it32 / n_rt / p.kv.Hkv), 0, 1};
   const int b = range.b, split = blockIdx.y - range.first;
   if (b < 0) return;  // short sequences need fewer ranges
   const int G = p.group;
@@ -116,7 +135,18 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
   // the last key that any row of the item sees
   const int t_last = t0 + (g0 + n_here - 1) / G;
   const int end = p.parents ? keys : min(keys, prefix + min(t_last + 1, cnt));
-  const int units = t0 < cnt ? (end + kUnit - 1) / kUnit : 0;
+  int units = t0 < cnt ? (end + kUnit - 1) / kUnit : 0;
+  Gap gap{0, 0};
+  int low = 0;  // keys before it, first tokens aside, are in no row's window
+  if constexpr (EXT) {
+    if (p.window > 0 && units > 0) {
+      low = window_low(p, b, p.parents ? 0 : t0);
+      gap = window_gap<kUnit>(p, low, units);
+      units -= gap.gap;
+    }
+  }
+  // the key at place `at` of the list of units
+  auto key_at = [&](int at) { return EXT && at >= gap.lead * kUnit ? at + gap.gap * kUnit : at; };
   const int key_lo = static_cast<int>(static_cast<int64_t>(units) * split / range.n) * kUnit;
   const int key_hi = static_cast<int>(static_cast<int64_t>(units) * (split + 1) / range.n) * kUnit;
   const int n_tiles = (key_hi - key_lo + kN - 1) / kN;
@@ -125,8 +155,15 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
     for (int w = 0; w < kTreeWords; ++w) s.anc[tid][w] = 0;
     int node = tid < n_here ? t0 + (g0 + tid) / G : -1;
     if (node >= cnt) node = -1;
+    int depth = 0, k = 0;
+    if constexpr (EXT) {
+      if (p.window > 0) {
+        if (node >= 0) depth = node_depth(p, b, node);
+        s.low[tid] = window_low(p, b, depth);
+      }
+    }
     while (node >= 0) {
-      s.anc[tid][node >> 5] |= 1u << (node & 31);
+      if (!EXT || p.window == 0 || window_sees(p, b, depth, k++)) s.anc[tid][node >> 5] |= 1u << (node & 31);
       const int up = ld_now(p.parents + b * p.par_sb + node);
       if (up >= node || up < -1) {
         atomicOr(p.status, kStatusIndex);
@@ -134,6 +171,9 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
       }
       node = up;
     }
+  }
+  if constexpr (EXT) {
+    if (tid < kR && p.window > 0 && !p.parents) s.low[tid] = window_low(p, b, t0 + (g0 + tid) / G);
   }
   float2 o[8][2];
 #pragma unroll
@@ -146,16 +186,26 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
   }
   const int tr = tid >> 4, tc = tid & 15;   // scores: rows tr + 16 w; keys tc + 16 i
   const int rg = tid >> 5, dg = tid & 31;   // outputs: rows 8 rg + i; dims 4 dg..
-  const bool f32 = p.kv.dt == kDtF32;
+  const bool f32 = KV == 0 && p.kv.dt == kDtF32, q_f32 = EXT ? p.q.dt == kDtF32 : f32;
+  const int row_dt = EXT ? p.q.dt : p.kv.dt;  // of q and o
   auto locate = [&](int jt) {  // the rows of key tile jt
     if (tid < kN && jt < n_tiles) {
-      const int j = key_lo + jt * kN + tid;
+      const int at = key_lo + jt * kN + tid, j = key_at(at);
       int pg, prow;
       int64_t ko = -1, vo = -1;
-      if (j < min(keys, key_hi)) {
+      bool there = at < key_hi && j < keys;
+      if constexpr (EXT) {
+        there = there && (j >= low || j < p.sinks);
+        s.ks[jt & 1][tid] = s.vs[jt & 1][tid] = 0.f;
+      }
+      if (there) {
         if (kv_locate(p.kv, b, j, &pg, &prow)) {
           ko = pg * p.kv.k_sp + prow * p.kv.k_sr + hk * p.kv.k_sh;
           vo = pg * p.kv.v_sp + prow * p.kv.v_sr + hk * p.kv.v_sh;
+          if constexpr (KV != 0) {
+            s.ks[jt & 1][tid] = ld_now(p.kv.ks + pg * p.kv.ks_sp + hk * p.kv.ks_sh + prow);
+            s.vs[jt & 1][tid] = ld_now(p.kv.vs + pg * p.kv.vs_sp + hk * p.kv.vs_sh + prow);
+          }
         } else {
           atomicOr(p.status, kStatusIndex);
         }
@@ -166,8 +216,8 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
   };
   // One of a tile's two operands into shared memory: asynchronous copies of
   // fp32 rows, conversion of 16-bit ones; zeros where there is no row.
-  auto fetch = [&](const void* base, const int64_t* off, float* dst, int pad) {
-    if (f32) {
+  auto fetch = [&](const void* base, const int64_t* off, float* dst, int pad, bool wide, bool f16) {
+    if (wide) {
 #pragma unroll
       for (int u = 0; u < kN * kD / 4 / kThreads; ++u) {
         const int e = u * kThreads + tid, r = e / (kD / 4), c = e % (kD / 4);
@@ -190,14 +240,49 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
         float y[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          y[2 * i] = p.kv.dt == kDtF16 ? f16_lo(w[i]) : bf16_lo(w[i]);
-          y[2 * i + 1] = p.kv.dt == kDtF16 ? f16_hi(w[i]) : bf16_hi(w[i]);
+          y[2 * i] = f16 ? f16_lo(w[i]) : bf16_lo(w[i]);
+          y[2 * i + 1] = f16 ? f16_hi(w[i]) : bf16_hi(w[i]);
         }
         *reinterpret_cast<float4*>(dst + r * pad + 8 * c) = make_float4(y[0], y[1], y[2], y[3]);
         *reinterpret_cast<float4*>(dst + r * pad + 8 * c + 4) = make_float4(y[4], y[5], y[6], y[7]);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // The same from 8 bits, a scale to a row.
+  auto fetch8 = [&](const void* base, const int64_t* off, const float* scale, float* dst, int pad) {
+    if constexpr (KV != 0) {
+      constexpr int kN8 = kN * kD / 16 / kThreads;
+      uint4 x[kN8];
+#pragma unroll
+      for (int u = 0; u < kN8; ++u) {
+        const int e = u * kThreads + tid, r = e / (kD / 16), c = e % (kD / 16);
+        const int64_t o = off[r];
+        x[u] = o < 0 ? make_uint4(0, 0, 0, 0) : ld_v4(static_cast<const uint8_t*>(base) + o + 16 * c);
+      }
+#pragma unroll
+      for (int u = 0; u < kN8; ++u) {
+        const int e = u * kThreads + tid, r = e / (kD / 16), c = e % (kD / 16);
+        const float f = scale[r];
+        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float y[4];
+          held4<KV>(w[i], y);
+          *reinterpret_cast<float4*>(dst + r * pad + 16 * c + 4 * i) = make_float4(y[0] * f, y[1] * f, y[2] * f, y[3] * f);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto fetch_kv = [&](int jt) {
+    if constexpr (KV != 0) {
+      fetch8(p.kv.k, s.k_off[jt & 1], s.ks[jt & 1], &s.k[0][0], kPad);
+      fetch8(p.kv.v, s.v_off[jt & 1], s.vs[jt & 1], &s.v[0][0], kD);
+    } else {
+      fetch(p.kv.k, s.k_off[jt & 1], &s.k[0][0], kPad, f32, p.kv.dt == kDtF16);
+      fetch(p.kv.v, s.v_off[jt & 1], &s.v[0][0], kD, f32, p.kv.dt == kDtF16);
+    }
   };
   locate(0);
   if (tid < kR) {  // the offsets of the query rows, where the second tile's will be
@@ -206,9 +291,8 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
   }
   __syncthreads();
   if (n_tiles > 0) {
-    fetch(p.q.p, s.k_off[1], &s.q[0][0], kD);
-    fetch(p.kv.k, s.k_off[0], &s.k[0][0], kPad);
-    fetch(p.kv.v, s.v_off[0], &s.v[0][0], kD);
+    fetch(p.q.p, s.k_off[1], &s.q[0][0], kD, q_f32, row_dt == kDtF16);
+    fetch_kv(0);
   }
   for (int jt = 0; jt < n_tiles; ++jt) {
     const int j0 = key_lo + jt * kN, n_units = min(kN, key_hi - j0) / kUnit;  // a range's last tile: only what it has
@@ -248,7 +332,21 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
     for (int w = 0; w < 4; ++w)
 #pragma unroll
       for (int i = 0; i < 4; ++i) sc[w][i] = (acc[w][i].x + acc[w][i].y) * sl;
-    if (j0 + kN > min(prefix, key_hi)) {  // rows of padding see anything here: they are dropped at the end
+    if (EXT && p.window > 0) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const int r = tr + 16 * w, t = t0 + (g0 + r) / G;
+        int r_low = 0;
+        if constexpr (EXT) r_low = s.low[r];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int at = j0 + tc + 16 * i, j = key_at(at), node = j - prefix;
+          const bool near = j >= r_low || j < p.sinks;
+          const bool sees = at < key_hi && j < keys && (p.parents && node >= 0 ? tree_sees(s.anc[r], node) : near && node <= t);
+          if (!sees) sc[w][i] = -INFINITY;
+        }
+      }
+    } else if (j0 + kN > min(prefix, key_hi)) {  // rows of padding see anything here: they are dropped at the end
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         const int r = tr + 16 * w, t = t0 + (g0 + r) / G;
@@ -310,8 +408,7 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
     }
     __syncthreads();
     if (jt + 1 < n_tiles) {
-      fetch(p.kv.k, s.k_off[(jt + 1) & 1], &s.k[0][0], kPad);
-      fetch(p.kv.v, s.v_off[(jt + 1) & 1], &s.v[0][0], kD);
+      fetch_kv(jt + 1);
     }
   }
 #pragma unroll
@@ -342,18 +439,18 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
     const float l = s.l[r], inv = l == 0.f ? 0.f : 1.f / l;
     const int t = t0 + (g0 + r) / G, h = hk * G + (g0 + r) % G;
     const int64_t off = b * p.o_sb + t * p.o_ss + h * p.o_sh + 4 * dg;
-    if (p.kv.dt == kDtF32)
+    if (row_dt == kDtF32)
       *reinterpret_cast<float4*>(static_cast<float*>(p.o) + off) = make_float4(o[i][0].x * inv, o[i][0].y * inv, o[i][1].x * inv, o[i][1].y * inv);
     else
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + off) =
-          make_uint2(pack_dt(p.kv.dt, o[i][0].x * inv, o[i][0].y * inv), pack_dt(p.kv.dt, o[i][1].x * inv, o[i][1].y * inv));
+          make_uint2(pack_dt(row_dt, o[i][0].x * inv, o[i][0].y * inv), pack_dt(row_dt, o[i][1].x * inv, o[i][1].y * inv));
     if (dg == 0) p.lse[(static_cast<int64_t>(b) * p.H + h) * p.T + t] = l == 0.f ? -INFINITY : (s.m[r] + log2f(l)) * kLn2;
   }
 }
 
 // W warps per query row, 1 or 8: each brings every W-th range's part to their
 // common maximum, four in flight, and the first one the warps' results.
-template <int W>
+template <int W, bool EXT>
 __global__ void __launch_bounds__(256) simt_join_kernel(const __grid_constant__ CacheAttnParams p, int n_rt, int64_t items) {
   __shared__ float4 so[W][kD / 4];
   __shared__ float2 sml[W];
@@ -367,7 +464,7 @@ __global__ void __launch_bounds__(256) simt_join_kernel(const __grid_constant__ 
   const int b = static_cast<int>(item / n_rt / p.kv.Hkv);
   const int64_t row = static_cast<int64_t>(rt) * kR + r;
   if (row >= static_cast<int64_t>(p.T) * p.group) return;
-  const Ranges range = find_ranges(p, -1, b);
+  const Ranges range = find_ranges<EXT>(p, -1, b);
   const int64_t per_seq = static_cast<int64_t>(n_rt) * p.kv.Hkv, step = per_seq * kR;  // items; rows from a range to the next
   const float2* ml = reinterpret_cast<const float2*>(p.part + per_seq * p.splits * kR * kD);
   const int64_t slot0 = (range.first * per_seq + item % per_seq) * kR + r;
@@ -417,23 +514,32 @@ __global__ void __launch_bounds__(256) simt_join_kernel(const __grid_constant__ 
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int t = static_cast<int>(row / p.group), h = hk * p.group + static_cast<int>(row % p.group);
   const int64_t off = b * p.o_sb + t * p.o_ss + h * p.o_sh + 4 * lane;
-  if (p.kv.dt == kDtF32)
+  const int row_dt = EXT ? p.q.dt : p.kv.dt;
+  if (row_dt == kDtF32)
     *reinterpret_cast<float4*>(static_cast<float*>(p.o) + off) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
   else
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + off) =
-        make_uint2(pack_dt(p.kv.dt, o.x * inv, o.y * inv), pack_dt(p.kv.dt, o.z * inv, o.w * inv));
+        make_uint2(pack_dt(row_dt, o.x * inv, o.y * inv), pack_dt(row_dt, o.z * inv, o.w * inv));
   if (lane == 0) p.lse[(static_cast<int64_t>(b) * p.H + h) * p.T + t] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+template <bool EXT, int KV>
+cudaError_t launch_t(const CacheAttnParams& p, cudaStream_t stream) {
+  static std::atomic<uint64_t> configured{0};
+  constexpr size_t smem = EXT ? sizeof(SmemExt) : sizeof(Smem);
+  cudaError_t e = opt_in_smem(simt_kernel<EXT, KV>, smem, configured);
+  if (e != cudaSuccess) return e;
+  const int n_rt = static_cast<int>((static_cast<int64_t>(p.T) * p.group + kR - 1) / kR);
+  const int64_t items = simt_items(p.splits > 0 ? 1 : p.B, p.T, p.H, p.kv.Hkv);
+  return launch_chained(simt_kernel<EXT, KV>, dim3(static_cast<unsigned>(items), std::max(p.splits, 1)), dim3(kThreads), smem, stream, p, n_rt);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_attn_simt(const CacheAttnParams& p, cudaStream_t stream) {
-  static std::atomic<uint64_t> configured{0};
-  cudaError_t e = opt_in_smem(simt_kernel, sizeof(Smem), configured);
-  if (e != cudaSuccess) return e;
-  const int n_rt = static_cast<int>((static_cast<int64_t>(p.T) * p.group + kR - 1) / kR);
-  const int64_t items = simt_items(p.splits > 0 ? 1 : p.B, p.T, p.H, p.kv.Hkv);
-  return launch_chained(simt_kernel, dim3(static_cast<unsigned>(items), std::max(p.splits, 1)), dim3(kThreads), sizeof(Smem), stream, p, n_rt);
+  if (p.kv.dt == kDtE4M3) return launch_t<true, kDtE4M3>(p, stream);
+  if (p.kv.dt == kDtI8) return launch_t<true, kDtI8>(p, stream);
+  return p.window > 0 ? launch_t<true, 0>(p, stream) : launch_t<false, 0>(p, stream);
 }
 
 cudaError_t launch_cache_attn_simt_join(const CacheAttnParams& p, cudaStream_t stream) {
@@ -442,8 +548,10 @@ cudaError_t launch_cache_attn_simt_join(const CacheAttnParams& p, cudaStream_t s
   // several warps a row where its parts are many: with one, 125 parts took 27 us
   // more than one (10 us in all with eight)
   const int warps = p.splits > 4 * p.B ? 8 : 1;
-  return launch_chained(warps == 8 ? simt_join_kernel<8> : simt_join_kernel<1>, dim3(static_cast<unsigned>((items * kR * warps + 7) / 8)),
-                        dim3(256), 0, stream, p, n_rt, items);
+  const bool ext = p.kv.ks || p.window > 0;
+  const auto kern = ext ? (warps == 8 ? simt_join_kernel<8, true> : simt_join_kernel<1, true>)
+                        : (warps == 8 ? simt_join_kernel<8, false> : simt_join_kernel<1, false>);
+  return launch_chained(kern, dim3(static_cast<unsigned>((items * kR * warps + 7) / 8)), dim3(256), 0, stream, p, n_rt, items);
 }
 
 }  // namespace st

@@ -1,5 +1,5 @@
-// Parameter blocks and launchers of the serving kernels: cache append, cached
-// attention, tree verification and cache compaction.
+// Parameter blocks and launchers of the serving kernels: cache append and read,
+// cached attention, tree verification and cache compaction.
 #pragma once
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -14,6 +14,15 @@ constexpr int kMaxVerify = 1024;     // nodes of a drafted tree that the verific
 constexpr int kMaxGroup = 128;       // query heads per K/V head
 constexpr int kMaxClusterVerify = 8;
 constexpr int kMaxClusterAttn = 8;
+
+// Element types of a cache of 8 bits (the codes of st_dtype): value = scale of
+// the row (a token and K/V head) times what is held.
+enum : int { kDtE4M3 = 6, kDtI8 = 7 };
+// What a row's largest magnitude is held as.
+__host__ __device__ constexpr float top_of(int dt) { return dt == kDtE4M3 ? 448.f : 127.f; }
+// Rows whose scale would be below this are held as zeros: its reciprocal, and
+// every value's product with it, is a normal number.
+constexpr float kMinScale = 7.888609052210118e-31f;  // 2^-100
 
 // Ordinary loads, not the read-only path: with programmatic launches a kernel
 // may be resident while the one before it still writes what is read here (after
@@ -41,7 +50,23 @@ struct PagedKV {
   int n_pages, page, max_pages;
   int page_shift;                  // log2 of page, -1 where it is no power of two
   int Hkv;
+  float* ks;                       // caches of 8 bits: scales [n_pages, Hkv, page], unit stride on page
+  float* vs;
+  int64_t ks_sp, ks_sh, vs_sp, vs_sh;
 };
+
+// Four held bytes (the lowest first) as numbers.
+template <int DT>
+__device__ __forceinline__ void held4(uint32_t w, float (&y)[4]) {
+  if constexpr (DT == kDtE4M3) {
+    uint32_t lo, hi;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n}" : "=r"(lo), "=r"(hi) : "r"(w));
+    y[0] = f16_lo(lo); y[1] = f16_hi(lo); y[2] = f16_lo(hi); y[3] = f16_hi(hi);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = static_cast<float>(static_cast<int8_t>(w >> (8 * e)));
+  }
+}
 
 // Page and row of token `pos` of sequence b; false when the position or the
 // table's entry is out of range.
@@ -69,7 +94,7 @@ struct AppendParams {
   PagedKV kv;
   const int32_t* lens;
   const int32_t* counts;           // or null
-  void* qo;                        // rotated q, [B, T, H, D] in the cache's type
+  void* qo;                        // rotated q, [B, T, H, D] in v's type (the cache's, unless that is of 8 bits)
   int64_t qo_sb, qo_ss, qo_sh;
   int B, T, H;
   unsigned* status;
@@ -77,7 +102,7 @@ struct AppendParams {
 cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t stream);
 
 struct CacheAttnParams {
-  RowTensor q;                     // rotated q, the cache's type
+  RowTensor q;                     // rotated q, the cache's type (any with a cache of 8 bits), as o
   PagedKV kv;
   const int32_t* lens;
   const int32_t* counts;           // or null
@@ -90,6 +115,8 @@ struct CacheAttnParams {
   int B, T, H, group;
   float* part;                     // partial results (workspace)
   int splits;                      // SIMT kernel: key ranges over all sequences (0: an item's keys stay together)
+  int window, sinks;               // window > 0: a row at position p sees keys at positions above p - window or below sinks
+  const int32_t* shared;           // [1]: tokens that all sequences have in the same pages, or null
   unsigned* status;
   unsigned long long* counters;
   long long wait_budget;
@@ -102,6 +129,39 @@ __device__ __forceinline__ int key_count(const CacheAttnParams& p, int b, int co
   const int64_t len = max(ld_now(p.lens + b), 0);
   *prefix = static_cast<int>(min(len, cap));
   return static_cast<int>(min(len + count, cap));
+}
+
+// The lowest position in the window of a row at lens[b] + step, at least 0 and
+// at most 2^30 (no key lies there). `sinks` aside.
+__device__ __forceinline__ int window_low(const CacheAttnParams& p, int b, int64_t step) {
+  const int64_t low = max(ld_now(p.lens + b), 0) + step - p.window + 1;
+  return static_cast<int>(min(max(low, int64_t(0)), int64_t(1) << 30));
+}
+// With a window, how many nodes are above `node` of sequence b's tree (parents
+// come before children; anything else ends the walk).
+__device__ __forceinline__ int node_depth(const CacheAttnParams& p, int b, int node) {
+  int depth = 0;
+  while (true) {
+    const int up = ld_now(p.parents + b * p.par_sb + node);
+    if (up >= node || up < 0) return depth;
+    node = up;
+    ++depth;
+  }
+}
+// The k-th ancestor of a row of that depth is seen.
+__device__ __forceinline__ bool window_sees(const CacheAttnParams& p, int b, int depth, int k) {
+  return k < p.window || static_cast<int64_t>(max(ld_now(p.lens + b), 0)) + depth - k < p.sinks;
+}
+// Keys that a window leaves out, in units of U keys: the first `lead` units and
+// those from lead + gap on hold every key that a row whose window begins at
+// `low` or higher sees.
+struct Gap {
+  int lead, gap;
+};
+template <int U>
+__device__ __forceinline__ Gap window_gap(const CacheAttnParams& p, int low, int units) {
+  const int lead = min(units, (min(p.sinks, 1 << 30) + U - 1) / U);
+  return {lead, max(0, min(low / U, units) - lead)};
 }
 
 // SIMT kernel: items of kSimtRows query rows of one K/V head.
@@ -140,6 +200,20 @@ struct JoinMeta {
 inline int tc_tiles(int T, int group) { return static_cast<int64_t>(T) * group > 128 ? 2 : 1; }
 cudaError_t launch_cache_attn_tc(const TcAttnParams& p, int nt, bool f16, cudaStream_t stream);
 cudaError_t launch_cache_attn_join(const TcAttnParams& p, int nt, cudaStream_t stream);
+
+// Rows of a cache into dense tensors [B, T, Hkv, D].
+struct ReadParams {
+  PagedKV kv;
+  const int32_t* start;            // [B]
+  const int32_t* counts;           // or null
+  void* k;
+  void* v;
+  int64_t k_sb, k_ss, k_sh, v_sb, v_ss, v_sh;
+  int dt;                          // of k and v
+  int B, T;
+  unsigned* status;
+};
+cudaError_t launch_cache_read(const ReadParams& p, cudaStream_t stream);
 
 struct VerifyParams {
   const void* p;                   // target probabilities [B, T, V]

@@ -12,7 +12,8 @@ namespace {
 
 using namespace st;
 
-constexpr unsigned kCacheTypes = bit(ST_BF16) | bit(ST_F16) | bit(ST_F32);
+constexpr unsigned kRowTypes = bit(ST_BF16) | bit(ST_F16) | bit(ST_F32), kHeldTypes = bit(ST_E4M3) | bit(ST_I8);
+static_assert(ST_E4M3 == kDtE4M3 && ST_I8 == kDtI8, "type codes");
 constexpr int kSmCount = 152;
 
 // A contiguous int32 or fp32 vector [B].
@@ -48,8 +49,25 @@ st_status check_own_rows(const st_tensor* t, const char* name) {
   return ST_OK;
 }
 
-// B < 0: the page table's own batch size is taken.
-st_status check_cache(const st_kv_cache* c, int64_t B, PagedKV* out, const char* who) {
+// The scales of K or V of a cache of 8 bits.
+st_status check_scales(const st_tensor* t, const char* name, int n, int Hkv, int page, float** p, int64_t* sp, int64_t* sh) {
+  if (!t) return fail(ST_ERR_INVALID_ARG, "%s is NULL: a cache of 8 bits needs its scales", name);
+  if (t->ndim != 3 || t->shape[0] != n || t->shape[1] != Hkv || t->shape[2] != page)
+    return fail(ST_ERR_SHAPE, "%s must be [N_pages, H_kv, page] = [%d, %d, %d]", name, n, Hkv, page);
+  if (t->dtype != ST_F32) return fail(ST_ERR_DTYPE, "%s must be fp32", name);
+  if (static_cast<int64_t>(n) * Hkv > 0 && !t->data) return fail(ST_ERR_INVALID_ARG, "%s data is NULL", name);
+  if (page > 1 && t->stride[2] != 1) return fail(ST_ERR_ALIGN, "%s must have unit stride on page", name);
+  if (reinterpret_cast<uintptr_t>(t->data) & 3u) return fail(ST_ERR_ALIGN, "%s data pointer is not 4-byte aligned", name);
+  if ((n > 1 && t->stride[0] <= 0) || (Hkv > 1 && t->stride[1] <= 0)) return fail(ST_ERR_ALIGN, "%s must not be expanded", name);
+  *p = static_cast<float*>(t->data);
+  *sp = n > 1 ? t->stride[0] : 0;
+  *sh = Hkv > 1 ? t->stride[1] : 0;
+  return ST_OK;
+}
+
+// B < 0: the page table's own batch size is taken. sc: the scales of a cache of
+// 8 bits, or NULL.
+st_status check_cache(const st_kv_cache* c, const st_kv_scales* sc, int64_t B, PagedKV* out, const char* who) {
   if (!c || !c->k || !c->v || !c->pages) return fail(ST_ERR_INVALID_ARG, "%s: the cache needs k, v and pages", who);
   const st_tensor *k = c->k, *pt = c->pages;
   if (k->ndim != 4) return fail(ST_ERR_SHAPE, "cache.k must be 4-D [N_pages, page, H_kv, D]");
@@ -60,7 +78,7 @@ st_status check_cache(const st_kv_cache* c, int64_t B, PagedKV* out, const char*
   RowTensor rk, rv;
   const int n = static_cast<int>(k->shape[0]), page = static_cast<int>(k->shape[1]), H = static_cast<int>(k->shape[2]);
   st_status st;
-  if ((st = check_bshd(k, "cache.k", n, page, H, kD, kCacheTypes, &rk)) != ST_OK) return st;
+  if ((st = check_bshd(k, "cache.k", n, page, H, kD, sc ? kRowTypes | kHeldTypes : kRowTypes, &rk)) != ST_OK) return st;
   if ((st = check_bshd(c->v, "cache.v", n, page, H, kD, bit(k->dtype), &rv)) != ST_OK) return st;
   if ((st = check_own_rows(k, "cache.k")) != ST_OK) return st;
   if ((st = check_own_rows(c->v, "cache.v")) != ST_OK) return st;
@@ -87,8 +105,12 @@ st_status check_cache(const st_kv_cache* c, int64_t B, PagedKV* out, const char*
     if (page == 1 << i) out->page_shift = i;
   out->max_pages = static_cast<int>(pt->shape[1]);
   out->Hkv = H;
-  return ST_OK;
+  if (!sc) return ST_OK;
+  if (!(bit(k->dtype) & kHeldTypes)) return fail(ST_ERR_INVALID_ARG, "%s: scales belong to a cache of 8 bits", who);
+  if ((st = check_scales(sc->k, "k_scale", n, H, page, &out->ks, &out->ks_sp, &out->ks_sh)) != ST_OK) return st;
+  return check_scales(sc->v, "v_scale", n, H, page, &out->vs, &out->vs_sp, &out->vs_sh);
 }
+bool held(const PagedKV& kv) { return kv.dt == kDtE4M3 || kv.dt == kDtI8; }
 
 // Sizes of a new-rows tensor [B, T, H, D].
 st_status check_new_rows(const st_tensor* q, const char* name, int* B, int* T, int* H) {
@@ -126,13 +148,13 @@ struct AttnPlan {
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
-st_status plan_attn(const st_tensor* q, const st_kv_cache* cache, const st_tensor* parents, AttnPlan* P) {
+st_status plan_attn(const st_tensor* q, const st_kv_cache* cache, const st_cache_attn_opts* opts, const st_tensor* parents, AttnPlan* P) {
   memset(&P->tc, 0, sizeof(P->tc));
   CacheAttnParams& p = P->tc.c;
   st_status st;
   if ((st = check_new_rows(q, "q_rot", &p.B, &p.T, &p.H)) != ST_OK) return st;
-  if ((st = check_cache(cache, p.B, &p.kv, "st_cache_attn")) != ST_OK) return st;
-  if ((st = check_bshd(q, "q_rot", p.B, p.T, p.H, kD, bit(p.kv.dt), &p.q)) != ST_OK) return st;
+  if ((st = check_cache(cache, opts ? opts->scales : nullptr, p.B, &p.kv, "st_cache_attn")) != ST_OK) return st;
+  if ((st = check_bshd(q, "q_rot", p.B, p.T, p.H, kD, held(p.kv) ? kRowTypes : bit(p.kv.dt), &p.q)) != ST_OK) return st;
   if ((st = check_heads(p.H, p.kv.Hkv)) != ST_OK) return st;
   p.group = p.kv.Hkv > 0 ? p.H / p.kv.Hkv : 1;
   if (p.group > kMaxGroup) return fail(ST_ERR_UNSUPPORTED, "%d query heads per K/V head: at most %d are supported", p.group, kMaxGroup);
@@ -141,12 +163,22 @@ st_status plan_attn(const st_tensor* q, const st_kv_cache* cache, const st_tenso
     if (p.T > kMaxTree) return fail(ST_ERR_UNSUPPORTED, "a tree of %d nodes: at most %d are supported", p.T, kMaxTree);
     p.parents = static_cast<const int32_t*>(parents->data);
   }
+  if (opts) {
+    if (opts->window < 0 || opts->sinks < 0) return fail(ST_ERR_INVALID_ARG, "window and sinks must be at least 0");
+    p.window = opts->window;
+    p.sinks = opts->window > 0 ? opts->sinks : 0;
+    if (opts->shared) {
+      if ((st = check_flat(opts->shared, "shared", 1, ST_I32)) != ST_OK) return st;
+      // with a window a sequence has few keys, and the rows see different ones
+      if (p.window == 0) p.shared = static_cast<const int32_t*>(opts->shared->data);
+    }
+  }
   P->bytes = 256;
   if (static_cast<int64_t>(p.B) * p.T * p.H == 0) return ST_OK;
   // The tensor-core kernel takes every 16-bit cache whose pages are whole TMA
   // boxes (at least one 8-row swizzle atom); fp32 caches and other page sizes
   // take the CUDA cores.
-  P->tensor = p.kv.dt != ST_F32 && p.kv.page % 8 == 0 && p.kv.n_pages > 0 && p.kv.max_pages > 0;
+  P->tensor = p.kv.dt != ST_F32 && p.kv.page % 8 == 0 && p.kv.n_pages > 0 && p.kv.max_pages > 0 && !held(p.kv) && p.window == 0;
   if (P->tensor) {
     TcAttnParams& t = P->tc;
     P->nt = tc_tiles(p.T, p.group);
@@ -216,17 +248,26 @@ extern "C" {
 st_status st_cache_append(const st_tensor* q, const st_tensor* k, const st_tensor* v, const st_tensor* q_norm_w,
                           const st_tensor* k_norm_w, float eps, const st_rope* rope, const st_kv_cache* cache,
                           const st_tensor* lens, const st_tensor* counts, st_tensor* q_rot, void* stream_) {
+  return st_cache_append_held(q, k, v, q_norm_w, k_norm_w, eps, rope, cache, nullptr, lens, counts, q_rot, stream_);
+}
+
+st_status st_cache_append_held(const st_tensor* q, const st_tensor* k, const st_tensor* v, const st_tensor* q_norm_w,
+                               const st_tensor* k_norm_w, float eps, const st_rope* rope, const st_kv_cache* cache,
+                               const st_kv_scales* scales, const st_tensor* lens, const st_tensor* counts, st_tensor* q_rot,
+                               void* stream_) {
   clear_error();
   AppendParams p;
   memset(&p, 0, sizeof(p));
   st_status st;
   if ((st = check_new_rows(q, "q", &p.B, &p.T, &p.H)) != ST_OK) return st;
-  if ((st = check_cache(cache, p.B, &p.kv, "st_cache_append")) != ST_OK) return st;
+  if ((st = check_cache(cache, scales, p.B, &p.kv, "st_cache_append")) != ST_OK) return st;
   if ((st = check_heads(p.H, p.kv.Hkv)) != ST_OK) return st;
-  const unsigned qk = bit(p.kv.dt) | bit(ST_F32);
+  // the type of v and q': the cache's, with one of 8 bits any
+  const unsigned row = held(p.kv) ? kRowTypes : bit(p.kv.dt);
+  if ((st = check_bshd(v, "v", p.B, p.T, p.kv.Hkv, kD, row, &p.v)) != ST_OK) return st;
+  const unsigned qk = bit(v->dtype) | bit(ST_F32);
   if ((st = check_bshd(q, "q", p.B, p.T, p.H, kD, qk, &p.q)) != ST_OK) return st;
   if ((st = check_bshd(k, "k", p.B, p.T, p.kv.Hkv, kD, qk, &p.k)) != ST_OK) return st;
-  if ((st = check_bshd(v, "v", p.B, p.T, p.kv.Hkv, kD, bit(p.kv.dt), &p.v)) != ST_OK) return st;
   if (q->dtype != k->dtype) return fail(ST_ERR_DTYPE, "q and k must have the same dtype");
   if ((st = check_vec(q_norm_w, "q_norm_w", kD)) != ST_OK) return st;
   if ((st = check_vec(k_norm_w, "k_norm_w", kD)) != ST_OK) return st;
@@ -245,7 +286,7 @@ st_status st_cache_append(const st_tensor* q, const st_tensor* k, const st_tenso
   if ((st = check_flat(lens, "lens", p.B, ST_I32)) != ST_OK) return st;
   if ((st = check_counts(counts, p.B, &p.counts)) != ST_OK) return st;
   RowTensor ro;
-  if ((st = check_bshd(q_rot, "q_rot", p.B, p.T, p.H, kD, bit(p.kv.dt), &ro)) != ST_OK) return st;
+  if ((st = check_bshd(q_rot, "q_rot", p.B, p.T, p.H, kD, bit(v->dtype), &ro)) != ST_OK) return st;
   if ((st = check_own_rows(q_rot, "q_rot")) != ST_OK) return st;
   const int64_t tokens = static_cast<int64_t>(p.B) * p.T;
   if (tokens > (1ll << 30) || tokens * (p.H + 2 * p.kv.Hkv) > (1ll << 32)) return fail(ST_ERR_SHAPE, "too many new rows");
@@ -294,25 +335,36 @@ st_status st_cache_append(const st_tensor* q, const st_tensor* k, const st_tenso
 }
 
 size_t st_cache_attn_workspace_size(const st_tensor* q_rot, const st_kv_cache* cache, const st_tensor* parents) {
+  return st_cache_attn_opt_workspace_size(q_rot, cache, nullptr, parents);
+}
+
+size_t st_cache_attn_opt_workspace_size(const st_tensor* q_rot, const st_kv_cache* cache, const st_cache_attn_opts* opts,
+                                        const st_tensor* parents) {
   clear_error();
   AttnPlan P;
-  if (plan_attn(q_rot, cache, parents, &P) != ST_OK) return 0;
+  if (plan_attn(q_rot, cache, opts, parents, &P) != ST_OK) return 0;
   return P.bytes;
 }
 
 st_status st_cache_attn(const st_tensor* q_rot, const st_kv_cache* cache, const st_tensor* lens, const st_tensor* counts,
                         const st_tensor* parents, float scale, st_tensor* o, st_tensor* lse, void* workspace,
                         size_t workspace_bytes, void* stream_) {
+  return st_cache_attn_opt(q_rot, cache, nullptr, lens, counts, parents, scale, o, lse, workspace, workspace_bytes, stream_);
+}
+
+st_status st_cache_attn_opt(const st_tensor* q_rot, const st_kv_cache* cache, const st_cache_attn_opts* opts, const st_tensor* lens,
+                            const st_tensor* counts, const st_tensor* parents, float scale, st_tensor* o, st_tensor* lse,
+                            void* workspace, size_t workspace_bytes, void* stream_) {
   clear_error();
   AttnPlan P;
-  st_status st = plan_attn(q_rot, cache, parents, &P);
+  st_status st = plan_attn(q_rot, cache, opts, parents, &P);
   if (st != ST_OK) return st;
   CacheAttnParams& p = P.tc.c;
   if ((st = check_flat(lens, "lens", p.B, ST_I32)) != ST_OK) return st;
   if ((st = check_counts(counts, p.B, &p.counts)) != ST_OK) return st;
   if (!std::isfinite(scale)) return fail(ST_ERR_INVALID_ARG, "scale must be finite");
   RowTensor ro;
-  if ((st = check_bshd(o, "o", p.B, p.T, p.H, kD, bit(p.kv.dt), &ro)) != ST_OK) return st;
+  if ((st = check_bshd(o, "o", p.B, p.T, p.H, kD, bit(p.q.dt), &ro)) != ST_OK) return st;
   if ((st = check_own_rows(o, "o")) != ST_OK) return st;
   if (static_cast<int64_t>(p.B) * p.T * p.H > 0 && o->data == q_rot->data)
     return fail(ST_ERR_INVALID_ARG, "o must not be q_rot: its rows are read until the call ends");
@@ -443,11 +495,16 @@ st_status st_tree_verify(const st_tensor* target, const st_tensor* draft, const 
 
 st_status st_cache_keep(const st_kv_cache* cache, const st_tensor* start, const st_tensor* rows, const st_tensor* n_rows,
                         st_tensor* lens, void* stream_) {
+  return st_cache_keep_held(cache, nullptr, start, rows, n_rows, lens, stream_);
+}
+
+st_status st_cache_keep_held(const st_kv_cache* cache, const st_kv_scales* scales, const st_tensor* start, const st_tensor* rows,
+                             const st_tensor* n_rows, st_tensor* lens, void* stream_) {
   clear_error();
   KeepParams p;
   memset(&p, 0, sizeof(p));
   st_status st;
-  if ((st = check_cache(cache, -1, &p.kv, "st_cache_keep")) != ST_OK) return st;
+  if ((st = check_cache(cache, scales, -1, &p.kv, "st_cache_keep")) != ST_OK) return st;
   p.B = static_cast<int>(cache->pages->shape[0]);
   if (!rows || rows->ndim != 2 || rows->shape[1] < 0 || rows->shape[1] > (1ll << 30)) return fail(ST_ERR_SHAPE, "rows must be [%d, N]", p.B);
   if ((st = check_flat(start, "start", p.B, ST_I32)) != ST_OK) return st;
@@ -480,6 +537,41 @@ st_status st_cache_keep(const st_kv_cache* cache, const st_tensor* start, const 
   p.status = dev.status;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   return cuda_check(launch_counted(ST_K_CACHE_KEEP, stream, [&] { return launch_cache_keep(p, stream); }), "cache keep launch");
+}
+
+st_status st_cache_read(const st_kv_cache* cache, const st_kv_scales* scales, const st_tensor* start, const st_tensor* counts,
+                        st_tensor* k, st_tensor* v, void* stream_) {
+  clear_error();
+  ReadParams p;
+  memset(&p, 0, sizeof(p));
+  st_status st;
+  if ((st = check_cache(cache, scales, -1, &p.kv, "st_cache_read")) != ST_OK) return st;
+  p.B = static_cast<int>(cache->pages->shape[0]);
+  if (!k || !v) return fail(ST_ERR_INVALID_ARG, "%s is NULL", k ? "v" : "k");
+  if (k->ndim != 4) return fail(ST_ERR_SHAPE, "k must be 4-D [B,T,H_kv,D], got ndim=%d", k->ndim);
+  if (k->shape[1] < 0 || k->shape[1] > (1ll << 30)) return fail(ST_ERR_SHAPE, "k sizes out of range");
+  p.T = static_cast<int>(k->shape[1]);
+  RowTensor rk, rv;
+  if ((st = check_bshd(k, "k", p.B, p.T, p.kv.Hkv, kD, held(p.kv) ? kRowTypes : bit(p.kv.dt), &rk)) != ST_OK) return st;
+  if ((st = check_bshd(v, "v", p.B, p.T, p.kv.Hkv, kD, bit(k->dtype), &rv)) != ST_OK) return st;
+  if ((st = check_own_rows(k, "k")) != ST_OK) return st;
+  if ((st = check_own_rows(v, "v")) != ST_OK) return st;
+  if ((st = check_flat(start, "start", p.B, ST_I32)) != ST_OK) return st;
+  if ((st = check_counts(counts, p.B, &p.counts)) != ST_OK) return st;
+  const int64_t tokens = static_cast<int64_t>(p.B) * p.T;
+  if (tokens > (1ll << 30) || tokens * 2 * p.kv.Hkv > (1ll << 32)) return fail(ST_ERR_SHAPE, "too many rows");
+  if (tokens * p.kv.Hkv == 0) return ST_OK;
+  Dev dev;
+  if ((st = device_globals(&dev)) != ST_OK) return st;
+  p.start = static_cast<const int32_t*>(start->data);
+  p.k = k->data;
+  p.v = v->data;
+  p.k_sb = rk.sb; p.k_ss = rk.ss; p.k_sh = rk.sh;
+  p.v_sb = rv.sb; p.v_ss = rv.ss; p.v_sh = rv.sh;
+  p.dt = k->dtype;
+  p.status = dev.status;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  return cuda_check(launch_counted(ST_K_CACHE_KEEP, stream, [&] { return launch_cache_read(p, stream); }), "cache read launch");
 }
 
 }  // extern "C"
