@@ -190,6 +190,13 @@ struct TcAttnParams {
   int cluster_shift;
   struct JoinMeta* meta;       // [ctas], workspace
   float2* part_ml;             // [2 ctas, part_rows] (reference, sum); c.part: [2 ctas, part_rows, D]
+  int sc_wide;                 // 1: four scales of neighbouring keys lie on 16 bytes
+  // With a shared prefix: parts are [2 ctas, split_rows], then a result of pre_rows
+  // or part_rows for each item that one CTA has whole.
+  int n_pre;                   // groups of the prefix's rows
+  int pre_rows, split_rows;    // rows of such a group, of a split part
+  int2* item_meta;             // [items] (parts, slot of the first or -1: whole)
+  int* p0;                     // [1] tiles of the prefix
 };
 // Of each CTA: the item whose first inner border is the CTA's beginning. Its
 // parts lie in slot0 and then in the slots 2 x of the CTAs x from this one on.
@@ -199,6 +206,9 @@ struct JoinMeta {
 };
 inline int tc_tiles(int T, int group) { return static_cast<int64_t>(T) * group > 128 ? 2 : 1; }
 cudaError_t launch_cache_attn_tc(const TcAttnParams& p, int nt, bool f16, cudaStream_t stream);
+cudaError_t launch_cache_attn_ext(const TcAttnParams& p, int nt, bool f16, cudaStream_t stream);   // the forms, each in a file of its own
+cudaError_t launch_cache_attn_e4m3(const TcAttnParams& p, int nt, bool f16, cudaStream_t stream);
+cudaError_t launch_cache_attn_i8(const TcAttnParams& p, int nt, bool f16, cudaStream_t stream);
 cudaError_t launch_cache_attn_join(const TcAttnParams& p, int nt, cudaStream_t stream);
 
 // Rows of a cache into dense tensors [B, T, Hkv, D].

@@ -143,7 +143,7 @@ struct AttnPlan {
   TcAttnParams tc;        // c: the parameters of either kernel
   bool tensor = false;    // the tensor-core kernel
   int nt = 1;
-  size_t bytes = 0, off_ml = 0, off_meta = 0;
+  size_t bytes = 0, off_ml = 0, off_meta = 0, off_p0 = 0;
 };
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
@@ -178,19 +178,31 @@ st_status plan_attn(const st_tensor* q, const st_kv_cache* cache, const st_cache
   // The tensor-core kernel takes every 16-bit cache whose pages are whole TMA
   // boxes (at least one 8-row swizzle atom); fp32 caches and other page sizes
   // take the CUDA cores.
-  P->tensor = p.kv.dt != ST_F32 && p.kv.page % 8 == 0 && p.kv.n_pages > 0 && p.kv.max_pages > 0 && !held(p.kv) && p.window == 0;
+  P->tensor = p.kv.dt != ST_F32 && p.kv.page % 8 == 0 && p.kv.n_pages > 0 && p.kv.max_pages > 0 && p.q.dt != ST_F32;
   if (P->tensor) {
     TcAttnParams& t = P->tc;
     P->nt = tc_tiles(p.T, p.group);
     t.box_shift = 3;
-    while ((1 << t.box_shift) < kTile && p.kv.page % (2 << t.box_shift) == 0) ++t.box_shift;
+    while ((1 << t.box_shift) < (held(p.kv) ? kTile / 2 : kTile) && p.kv.page % (2 << t.box_shift) == 0) ++t.box_shift;
     t.tpt = kTile / p.group;
     const int64_t tpg = static_cast<int64_t>(t.tpt) * P->nt;
     t.n_groups = static_cast<int>((p.T + tpg - 1) / tpg);
     t.part_rows = static_cast<int>(std::min<int64_t>(p.T, tpg)) * p.group;
-    const int64_t cap_tiles = (static_cast<int64_t>(p.kv.max_pages) * p.kv.page + kTile - 1) / kTile;
-    const int64_t items = static_cast<int64_t>(p.B) * p.kv.Hkv * t.n_groups;
-    if (items > (1ll << 40) || static_cast<int64_t>(p.B) * t.n_groups > (1ll << 30)) return fail(ST_ERR_SHAPE, "too many query rows");
+    int64_t cap_tiles = (static_cast<int64_t>(p.kv.max_pages) * p.kv.page + kTile - 1) / kTile;
+    // a window's tiles: the first tokens', the window's and its rows', one for the window's edge
+    if (p.window > 0)
+      cap_tiles = std::min(cap_tiles, (static_cast<int64_t>(p.sinks) + kTile - 1) / kTile +
+                                          (static_cast<int64_t>(p.window) + std::min<int64_t>(p.T, p.parents ? p.T : tpg) + kTile - 1) / kTile + 1);
+    int64_t items = static_cast<int64_t>(p.B) * p.kv.Hkv * t.n_groups;
+    if (p.shared) {
+      const int64_t tokens = static_cast<int64_t>(p.B) * p.T;
+      if (tokens > (1ll << 30)) return fail(ST_ERR_SHAPE, "too many query rows");
+      t.n_pre = static_cast<int>((tokens + tpg - 1) / tpg);
+      t.pre_rows = static_cast<int>(std::min<int64_t>(tokens, tpg)) * p.group;
+      t.split_rows = std::max(t.pre_rows, t.part_rows);
+      items += static_cast<int64_t>(p.kv.Hkv) * t.n_pre;
+    }
+    if (items > (1ll << 40) || static_cast<int64_t>(p.B) * t.n_groups + t.n_pre > (1ll << 30)) return fail(ST_ERR_SHAPE, "too many query rows");
     // The clustered form: as many CTAs per item as let all clusters run at once
     // (15 clusters of 8 such CTAs, 36 of 4, 76 of 2 fit the GPU; 16 of 8 took
     // two turns: 18.3 us against 11.0 with 4). Its shares are even per item
@@ -211,7 +223,7 @@ st_status plan_attn(const st_tensor* q, const st_kv_cache* cache, const st_cache
       const int cl = items <= 15 ? 8 : (items <= 36 ? 4 : (items <= 76 ? 2 : 1));
       static_assert(kMaxClusterAttn == 8, "the largest cluster");
       const int64_t mean = p.B == 1 ? 2 : 1, saved = P->nt == 1 ? 16 : 32;  // halves of the room; of tiles
-      if (cl > 1 && cap_tiles * (2 * kSmCount - mean * items * cl) <= saved * cl * kSmCount) t.cluster = cl;
+      if (cl > 1 && !p.shared && cap_tiles * (2 * kSmCount - mean * items * cl) <= saved * cl * kSmCount) t.cluster = cl;
     }
     if (t.cluster > 0) {
       t.ctas = static_cast<int>(items) * t.cluster;
@@ -219,6 +231,17 @@ st_status plan_attn(const st_tensor* q, const st_kv_cache* cache, const st_cache
       return ST_OK;  // no workspace
     }
     t.ctas = static_cast<int>(items >= kSmCount ? kSmCount : std::min<int64_t>(kSmCount, items * cap_tiles));
+    if (p.shared) {
+      const int64_t own = items - static_cast<int64_t>(p.kv.Hkv) * t.n_pre;
+      const size_t rows = static_cast<size_t>(2) * t.ctas * t.split_rows + static_cast<size_t>(items - own) * t.pre_rows + static_cast<size_t>(own) * t.part_rows;
+      size_t off = align256(rows * kD * sizeof(float));
+      P->off_ml = off;
+      off = align256(off + rows * sizeof(float2));
+      P->off_meta = off;
+      P->off_p0 = align256(off + items * sizeof(int2));
+      P->bytes = P->off_p0 + 256;
+      return ST_OK;
+    }
     // a CTA leaves at most two parts: one at each end of its range
     size_t off = align256(static_cast<size_t>(2) * t.ctas * t.part_rows * kD * sizeof(float));
     P->off_ml = off;
@@ -398,10 +421,15 @@ st_status st_cache_attn_opt(const st_tensor* q_rot, const st_kv_cache* cache, co
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     t.part_ml = reinterpret_cast<float2*>(ws + P.off_ml);
     t.meta = reinterpret_cast<JoinMeta*>(ws + P.off_meta);
+    t.item_meta = reinterpret_cast<int2*>(ws + P.off_meta);
+    t.p0 = reinterpret_cast<int*>(ws + P.off_p0);
+    const PagedKV& kv = p.kv;
+    t.sc_wide = ((reinterpret_cast<uintptr_t>(kv.ks) | reinterpret_cast<uintptr_t>(kv.vs)) & 15u) == 0 &&
+                (kv.ks_sp | kv.ks_sh | kv.vs_sp | kv.vs_sh) % 4 == 0;
     t.o_wide = (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0 && p.o_sb % 16 == 0 && p.o_ss % 16 == 0 && p.o_sh % 16 == 0;
     if ((st = encode_rows_map(cache->k, &t.tmap_k, &t.k_r_first, 1 << t.box_shift)) != ST_OK) return st;
     if ((st = encode_rows_map(cache->v, &t.tmap_v, &t.v_r_first, 1 << t.box_shift)) != ST_OK) return st;
-    if ((st = cuda_check(launch_counted(ST_K_CACHE_ATTN, stream, [&] { return launch_cache_attn_tc(t, P.nt, p.kv.dt == ST_F16, stream); }),
+    if ((st = cuda_check(launch_counted(ST_K_CACHE_ATTN, stream, [&] { return launch_cache_attn_tc(t, P.nt, p.q.dt == ST_F16, stream); }),
                          "cached attention launch")) != ST_OK)
       return st;
     if (t.cluster > 0) return ST_OK;
