@@ -568,8 +568,8 @@ st_status encode_rows_map(const st_tensor* t, CUtensorMap* map, int* s_first, in
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc) return fail(ST_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   const int64_t B = t->shape[0], S = t->shape[1], H = t->shape[2];
-  const bool f32 = t->dtype == ST_F32, held = t->dtype == ST_E4M3 || t->dtype == ST_I8;
-  const int64_t eb = f32 ? 4 : (held ? 1 : 2);
+  const bool f32 = t->dtype == ST_F32;
+  const int64_t eb = f32 ? 4 : 2;
   // strides in bytes; a size-1 dim gets the packed stride (any valid value works)
   int64_t ss = S > 1 ? t->stride[1] * eb : H * kD * eb;
   int64_t sh = H > 1 ? t->stride[2] * eb : kD * eb;
@@ -579,7 +579,7 @@ st_status encode_rows_map(const st_tensor* t, CUtensorMap* map, int* s_first, in
   if (sb == 0) sb = S * H * kD * eb;
   *s_first = ss < sh;
   cuuint64_t dims[4], strides[3];
-  cuuint32_t box[4] = {f32 ? 32u : (held ? 128u : 64u), 1, 1, 1}, es[4] = {1, 1, 1, 1};
+  cuuint32_t box[4] = {f32 ? 32u : 64u, 1, 1, 1}, es[4] = {1, 1, 1, 1};
   dims[0] = kD;
   if (*s_first) {
     dims[1] = S; dims[2] = H; strides[0] = ss; strides[1] = sh; box[1] = box_rows;
@@ -588,11 +588,10 @@ st_status encode_rows_map(const st_tensor* t, CUtensorMap* map, int* s_first, in
   }
   dims[3] = B;
   strides[2] = sb;
-  const CUtensorMapDataType ty = f32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                 : held ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                        : (t->dtype == ST_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
+  const CUtensorMapDataType ty = f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : (t->dtype == ST_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
   CUresult r = enc(map, ty, 4, t->data, dims,
-                   strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, held ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                   strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(ST_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled rejected the layout (error %d)", (int)r);
   return ST_OK;

@@ -68,10 +68,11 @@ __global__ void __launch_bounds__(256, U > 4 ? 2 : 6) join_kernel(const __grid_c
   }
 }
 
-// With a shared prefix: a row's results over the prefix's tiles and over its own
-// keys come together, each whole or in the parts that CTAs left of it. A warp takes
-// a row, a lane four columns; four parts are in flight.
-__global__ void __launch_bounds__(256) join_shared_kernel(const __grid_constant__ TcAttnParams P, int nt) {
+// By items (a shared prefix, FEW): a row's results over the prefix's tiles and over
+// its own keys come together, each whole or in the parts that CTAs left of it, these
+// in four copies with FEW. A warp takes a row, a lane four columns; four parts are in
+// flight.
+__global__ void __launch_bounds__(256) join_items_kernel(const __grid_constant__ TcAttnParams P, int nt) {
   grid_dependency_wait();
   const CacheAttnParams& c = P.c;
   const int lane = threadIdx.x & 31;
@@ -80,7 +81,7 @@ __global__ void __launch_bounds__(256) join_shared_kernel(const __grid_constant_
   const int64_t tok = row / c.H;  // at most 2^30
   const int hq = static_cast<int>(row - tok * c.H), b = static_cast<int>(tok / c.T), t = static_cast<int>(tok - static_cast<int64_t>(b) * c.T);
   if (t >= row_count(c.counts, b, c.T)) return;  // the attention kernel wrote it
-  const int h = hq / c.group, g = hq - h * c.group, tpg = P.tpt * nt, p0 = ld_now(P.p0);
+  const int h = hq / c.group, g = hq - h * c.group, tpg = P.tpt * nt, p0 = c.shared ? ld_now(P.p0) : 0;
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
@@ -88,19 +89,20 @@ __global__ void __launch_bounds__(256) join_shared_kernel(const __grid_constant_
     const int ib = which == 0 ? -1 : b, at = which == 0 ? static_cast<int>(tok) : t, im = at / tpg;
     if (item_of<true>(P, nt, ib, im, p0).n == 0) continue;
     const int in = at - im * tpg, r = in * c.group + g;  // tiles of tpt tokens follow one another without gaps
+    const int copies = P.few && which == 1 ? 4 : 1;
     const int2 meta = P.item_meta[item_index(P, h, ib, im)];
     const int64_t first = meta.y < 0 ? whole_part(P, h, ib, im) : static_cast<int64_t>(meta.y) * P.split_rows;
     const int64_t cta = meta.y >> 1;
-    for (int i0 = 0; i0 < meta.x; i0 += 4) {
+    for (int i0 = 0; i0 < meta.x * copies; i0 += 4) {
       float2 x[4];
       float4 y[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const int i = min(i0 + u, meta.x - 1);
-        const int64_t at_row = (i == 0 ? first : 2 * (cta + i) * P.split_rows) + r;
+        const int v = min(i0 + u, meta.x * copies - 1), i = copies == 4 ? v >> 2 : v, copy = copies == 4 ? v & 3 : 0;
+        const int64_t at_row = (i == 0 ? first : 2 * (cta + i) * P.split_rows) + copy * P.part_rows + r;
         x[u] = P.part_ml[at_row];
         y[u] = reinterpret_cast<const float4*>(c.part + at_row * kD)[lane];
-        if (i0 + u >= meta.x) x[u] = make_float2(-INFINITY, 0.f);
+        if (i0 + u >= meta.x * copies) x[u] = make_float2(-INFINITY, 0.f);
       }
       const float top = fmaxf(fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x)), m), use = top == -INFINITY ? 0.f : top;
       const float f0 = ex2(m - use);
@@ -131,9 +133,9 @@ cudaError_t launch_cache_attn_tc(const TcAttnParams& p, int nt, bool f16, cudaSt
 }
 
 cudaError_t launch_cache_attn_join(const TcAttnParams& p, int nt, cudaStream_t stream) {
-  if (p.c.shared) {
+  if (p.item_meta) {
     const int64_t rows = static_cast<int64_t>(p.c.B) * p.c.T * p.c.H;
-    return launch_chained(join_shared_kernel, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, stream, p, nt);
+    return launch_chained(join_items_kernel, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, stream, p, nt);
   }
   // few rows, or few items, whose parts are then many
   const bool deep = p.part_rows <= 32 || static_cast<int64_t>(p.c.B) * p.c.kv.Hkv * p.n_groups * 4 <= p.ctas;

@@ -29,18 +29,27 @@
 // values are the operands, as fp16, and the scales enter in fp32: K's multiply the
 // scores, V's the weights P before these are rounded. bf16 rows of q come to fp16
 // by a power of two of their own (what is lost is 2^-39 of the row's largest
-// element or less). TMA brings the bytes into a ring of 64-key pieces, four warps
-// turn them into the 16-bit operand tiles (K one tile ahead of V, so that scores
-// do not wait for V's turn), and one warp lays out the scales. Half the bytes are
-// read for each key; the conversion runs under the reading (16 KB of a tile take
-// a CTA 370 ns at its share of the HBM rate, their conversion about 250).
+// element or less). Four warps each bring K's and V's bytes into shared memory and
+// turn them into the 16-bit operand tiles; a thread fetches just the 16-byte pieces
+// that it converts later, by asynchronous copies, so that nothing is handed over in
+// between, and pages may be of any size. (With TMA boxes their issue set the pace:
+// 64-key stages of 16-row boxes took the TMA warp 2900 cycles a tile.) Half the
+// bytes are read for each key; all else has half the time of the 16-bit form.
 //
-// Roles (512 threads, one CTA per SM):
+// FEW (KV, at most 32 rows of one query tile: decoding): a thread per row left
+// seven of eight warps idle and 128 scores of a tile to one after the other. The
+// rows are put into all four lane groups of the tile (the MMA has room for 128) and
+// each warp takes a quarter of the tile's keys, its weights of the others being
+// zero; every group has sums and accumulators of its own, which are joined at the
+// end like parts of the keys.
+//
+// Roles (512 threads, KV: 640; one CTA per SM):
 //   warps 0-7   softmax, two groups of four warps; thread = query row = TMEM lane
-//   warps 8-11  Q rows of the next item into shared memory; KV: the conversion
-//   warp 12/15  tcgen05.mma issue for slot 0 / 1 (one thread each); TMEM allocation
-//   warp 13/14  TMA of K / V boxes, one lane per box; KV: of both / scales (and,
-//               with one query tile, Q rows)
+//   warps 8-11  Q rows of the next item into shared memory; KV: also K's conversion,
+//               and four more warps V's
+//   then        tcgen05.mma issue for slot 0 (one thread; TMEM allocation); TMA of K
+//               boxes, one lane per box; TMA of V boxes (KV: neither); tcgen05.mma
+//               issue for slot 1
 // TMEM: S0 | S1 | O0 | O1, 128 fp32 columns each; P (16-bit) overwrites the
 // first half of its S and feeds PV from TMEM. The stream of score tiles
 // alternates between the two halves ("slots"): with NT = 2 a slot is a query
@@ -51,6 +60,7 @@
 // items.
 #pragma once
 #include <atomic>
+#include <type_traits>
 #include "st_kernels.h"
 #include "st_serve.h"
 
@@ -58,10 +68,16 @@ namespace st {
 
 namespace {
 
-constexpr int kSoftWarps = 8, kWarpQ0 = 8, kQWarps = 4, kWarpMma = 12, kWarpK = 13, kWarpV = 14;  // warp 15: the second slot's MMAs
-constexpr int kTcWarps = 16, kTcThreads = kTcWarps * 32;
-// Registers per thread: the softmax threads hold a row of 128 scores. 256 * 184 + 256 * 72 = 512 * 128.
-constexpr int kRegsSoft = 184, kRegsRest = 72;
+constexpr int kSoftWarps = 8, kWarpQ0 = 8, kQWarps = 4;
+template <bool HELD>
+struct Roles {
+  static constexpr int kWarpMma = HELD ? 16 : 12, kWarpK = kWarpMma + 1, kWarpV = kWarpMma + 2;  // kWarpMma + 3: the second slot's MMAs
+  static constexpr int kWarps = kWarpMma + 4, kThreads = kWarps * 32;
+  // Registers per thread. The 16-bit form's softmax threads hold a row of 128 scores:
+  // 256 * 184 + 256 * 72 = 512 * 128. KV reads the scores from TMEM twice instead and
+  // holds 64: 256 * 128 + 384 * 72 <= 640 * 96.
+  static constexpr int kRegsSoft = HELD ? 128 : 184, kRegsRest = 72;
+};
 constexpr float kRescale = 8.0f;  // O is rescaled when the running maximum grows by more than this (base 2)
 // How far the reference stays below the running maximum (base 2). fp16 weights
 // end at 2^-25 of 1, and a long row's many small ones would leave PV but stay in
@@ -70,24 +86,24 @@ constexpr float kRescale = 8.0f;  // O is rescaled when the running maximum grow
 template <bool F16>
 constexpr float kLift = F16 ? 7.0f : 0.0f;
 
-constexpr int kRawRows = 64;                         // keys of a stage of bytes (KV)
-constexpr uint32_t kRawBytes = kRawRows * kD;
-
 template <int NT, bool HELD = false>
 struct Lay {  // shared memory, offsets from a 1024-byte aligned base
   // With NT = 1 a stage belongs to one slot for good (even counts): a slot's
   // thread waits for every phase of the stages that it uses, and a wait on
   // parity says nothing where phases went by unseen.
   static constexpr int KS = NT == 1 || HELD ? 2 : 3, VS = NT == 1 && !HELD ? 4 : 2;
-  static constexpr int RS = !HELD ? 0 : (NT == 1 ? 7 : 3);  // stages of bytes: 56 KB in flight where reading bounds
-  static_assert(NT == 2 || (KS % 2 == 0 && VS % 2 == 0), "stages of one slot");
-  static constexpr uint32_t q = 0, k = NT * kTileBytes, v = k + KS * kTileBytes, raw = v + VS * kTileBytes, bar = raw + RS * kRawBytes;
+  static constexpr int SS = HELD ? 6 : 0;                   // stages of scales (NT = 1: of one slot, as above)
+  // stages of bytes, of K and of V, and their keys: 56 KB in flight where reading bounds
+  static constexpr int RK = !HELD ? 0 : (NT == 1 ? 4 : 3), RV = !HELD ? 0 : 3, kRawRows = NT == 1 ? 64 : 32;
+  static constexpr uint32_t kRawBytes = kRawRows * kD;
+  static_assert(NT == 2 || (KS % 2 == 0 && VS % 2 == 0 && SS % 2 == 0), "stages of one slot");
+  static constexpr uint32_t q = 0, k = NT * kTileBytes, v = k + KS * kTileBytes, raw = v + VS * kTileBytes, bar = raw + (RK + RV) * kRawBytes;
   static constexpr uint32_t ml = bar + 512;          // [2][128] (reference, sum), NT = 1
-  static constexpr uint32_t sc = ml + (NT == 1 ? 2 * 128 * 8 : 0);  // HELD: [2] Scales
-  static constexpr uint32_t bytes = sc + (HELD ? 2 * 1040 : 0);
+  static constexpr uint32_t sc = ml + (NT == 1 ? 2 * 128 * 8 : 0);  // [SS] Scales
+  static constexpr uint32_t walk = sc + SS * 1040;   // HELD: [2][warps] places of the roles' walks
+  static constexpr uint32_t bytes = walk + (HELD ? 2 * Roles<true>::kWarps * 24 : 0);
   enum { QFull = 0, QEmpty, KFull, KEmpty = KFull + KS, VFull = KEmpty + KS, VEmpty = VFull + VS, SFull = VEmpty + VS,
-         PFull = SFull + 2, OFull = PFull + 2, MlFull, ORead = MlFull + 2, Drain = ORead + 2, RawFull = Drain + 2,
-         RawEmpty = RawFull + RS, ScFull = RawEmpty + RS, ScEmpty = ScFull + (HELD ? 2 : 0), Num = ScEmpty + (HELD ? 2 : 0) };
+         PFull = SFull + 2, OFull = PFull + 2, MlFull, ORead = MlFull + 2, Drain = ORead + 2, ScFull = Drain + 2, ScEmpty = ScFull + SS, Num = ScEmpty + SS };
 };
 static_assert(Lay<1>::bytes <= 232448 && Lay<2>::bytes <= 232448, "shared memory");
 static_assert(Lay<1, true>::bytes <= 232448 && Lay<2, true>::bytes <= 232448, "shared memory");
@@ -95,10 +111,10 @@ static_assert(Lay<1>::Num * 8 + 128 <= 512 && Lay<2>::Num * 8 + 128 <= 512, "bar
 static_assert(Lay<1, true>::Num * 8 + 128 <= 512 && Lay<2, true>::Num * 8 + 128 <= 512, "barrier area");
 
 // The scales of a key tile; those of keys that no row sees are 0. top: log2 of
-// V's largest.
+// V's largest, of the keys that each of four warps fetched.
 struct Scales {
   float k[kTile], v[kTile];
-  float top, pad[3];
+  float top[4];
 };
 static_assert(sizeof(Scales) == 1040, "layout");
 // V's scales are good in this range (base 2).
@@ -110,6 +126,11 @@ __device__ __forceinline__ constexpr uint32_t mofs(int kk) { return kk * 2048; }
 // Asynchronous 16-byte copy into shared memory; zeros when !there.
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+
+// The same of one fp32 number.
+__device__ __forceinline__ void cp_async4(void* dst, const void* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 4 : 0) : "memory");
 }
 
 struct Item {
@@ -213,6 +234,29 @@ struct Walk {
     return true;
   }
   __device__ __forceinline__ bool whole() const { return kt0 == 0 && kt1 == it.n; }
+  // HELD: what the walk goes on from lies in shared memory between pieces, so that
+  // the roles' 72 registers hold the present piece only (with two walks in
+  // registers they spilled in their loops: 64 tokens after up to 8191 keys in
+  // e4m3 395 us).
+  struct Place {
+    int h, b, m, off;
+    long long left;
+  };
+  __device__ __forceinline__ void save(Place* at) const { *at = {h, b, m, off, left}; }
+  template <bool ONE, bool WARP>
+  __device__ __forceinline__ bool next_from(const TcAttnParams& p, int nt, Place* at) {
+    const Place x = *at;
+    h = x.h;
+    b = x.b;
+    m = x.m;
+    off = x.off;
+    left = x.left;
+    const bool more = next<ONE>(p, nt);
+    if (WARP) __syncwarp();  // every lane has read
+    if (!WARP || (threadIdx.x & 31) == 0) save(at);
+    if (WARP) __syncwarp();
+    return more;
+  }
 };
 
 // The deal: CTA x has the tiles [first(x), first(x + 1)) of the call's, shares
@@ -247,10 +291,11 @@ struct Start {  // found by the block, read by every role
 
 // The shared prefix: whole tiles of what the least of the sequences that have
 // rows reaches, and the first of these sequences.
+template <int W>  // warps
 __device__ __forceinline__ void find_shared(const TcAttnParams& p, int* scratch, Start* st) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int least = 0x7fffffff, first = 0x7fffffff;
-  for (int b = tid; b < p.c.B; b += kTcThreads)
+  for (int b = tid; b < p.c.B; b += W * 32)
     if (row_count(p.c.counts, b, p.c.T) > 0) {
       least = min(least, max(ld_now(p.c.lens + b), 0));
       first = min(first, b);
@@ -259,13 +304,13 @@ __device__ __forceinline__ void find_shared(const TcAttnParams& p, int* scratch,
   first = __reduce_min_sync(0xffffffffu, first);
   if (lane == 0) {
     scratch[warp] = least;
-    scratch[kTcWarps + warp] = first;
+    scratch[W + warp] = first;
   }
   __syncthreads();
   if (tid == 0) {
-    for (int w = 1; w < kTcWarps; ++w) {
+    for (int w = 1; w < W; ++w) {
       least = min(least, scratch[w]);
-      first = min(first, scratch[kTcWarps + w]);
+      first = min(first, scratch[W + w]);
     }
     const int cap = p.c.kv.max_pages * p.c.kv.page;  // at most 2^30
     st->p0 = first == 0x7fffffff ? 0 : min(min(max(ld_now(p.c.shared), 0), least), cap) / kTile;
@@ -278,18 +323,18 @@ __device__ __forceinline__ void find_shared(const TcAttnParams& p, int* scratch,
 // Where the CTA's range begins: every thread sums the key tiles of a run of
 // (sequence, group) pairs (the shared prefix's groups first), a block scan places
 // the runs.
-template <bool EXT>
+template <bool EXT, int W>
 __device__ __forceinline__ void find_start(const TcAttnParams& p, int nt, long long* scan, Start* st) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int p0 = 0;
   if constexpr (EXT) {
     if (p.c.shared) {
-      find_shared(p, reinterpret_cast<int*>(scan), st);
+      find_shared<W>(p, reinterpret_cast<int*>(scan), st);
       p0 = st->p0;
     }
   }
   const int pre = p0 > 0 ? p.n_pre : 0, pairs = pre + p.c.B * p.n_groups;  // at most 2^30
-  const int per = (pairs + kTcThreads - 1) / kTcThreads, lo = min(pairs, tid * per), hi = min(pairs, lo + per);
+  const int per = (pairs + W * 32 - 1) / (W * 32), lo = min(pairs, tid * per), hi = min(pairs, lo + per);
   int b0, m0;
   if (EXT && lo < pre) {
     b0 = -1;
@@ -320,7 +365,7 @@ __device__ __forceinline__ void find_start(const TcAttnParams& p, int nt, long l
   __syncthreads();
   long long before = 0, one = 0;
 #pragma unroll
-  for (int w = 0; w < kTcWarps; ++w) {
+  for (int w = 0; w < W; ++w) {
     if (w < warp) before += scan[w];
     one += scan[w];
   }
@@ -345,7 +390,7 @@ __device__ __forceinline__ void find_start(const TcAttnParams& p, int nt, long l
           st->m = m;
           st->off = static_cast<int>(rem);
           st->left = d.first(blockIdx.x + 1) - s0;
-          if (EXT && p.c.shared) break;
+          if (EXT && p.item_meta) break;
           // for the join: is this border the first inside of its item, and
           // who has the item's tiles?
           JoinMeta meta{0, 0, h, b, m, it.cnt};
@@ -364,7 +409,7 @@ __device__ __forceinline__ void find_start(const TcAttnParams& p, int nt, long l
         }
       }
     }
-  } else if (tid == 0 && !(EXT && p.c.shared)) {
+  } else if (tid == 0 && !(EXT && p.item_meta)) {
     p.meta[blockIdx.x].parts = 0;
   }
   __syncthreads();
@@ -477,70 +522,123 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float sc,
   tmem_st_wait();
 }
 
-// The same over a cache of 8 bits. Scores are s ks sc: ks the key's scale, sc the
-// row's factor. The weights are rounded as P vs, vs V's scale, and so that they end
-// at 2^15 the reference has log2 of the tile's largest vs added to it; sums and
-// accumulators alike are in its units.
-template <bool MASK>
-__device__ __forceinline__ void softmax_held(uint32_t tS, uint32_t tO, float sc, const Scales& scales, const uint32_t (&mb)[4], bool first,
-                                             float& m_run, float& l_run) {
-  uint32_t x[4][32];
+// The same over a cache of 8 bits, over the chunks [c0, c1) of 32 keys (with FEW one;
+// the weights of the others are zero). Scores are s ks sc: ks the key's scale, sc
+// the row's factor. The weights are rounded as P vs, vs V's scale, and so that they
+// end at 2^15 the reference has log2 of the tile's largest vs added to it; sums and
+// accumulators alike are in its units. The scores are read from TMEM twice, for the
+// maximum and for the weights, which take the place of scores that have been read.
+__device__ __forceinline__ void scale_chunk(uint32_t (&x)[32], const float* ks, bool mask, uint32_t mb) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) tmem_ld32_issue(tS + 32 * i, x[i]);
+  for (int t = 0; t < 32; t += 4) {
+    const float4 k4 = *reinterpret_cast<const float4*>(ks + t);
+    const float2 a = __fmul2_rn(make_float2(__uint_as_float(x[t]), __uint_as_float(x[t + 1])), make_float2(k4.x, k4.y));
+    const float2 b = __fmul2_rn(make_float2(__uint_as_float(x[t + 2]), __uint_as_float(x[t + 3])), make_float2(k4.z, k4.w));
+    x[t] = __float_as_uint(a.x);
+    x[t + 1] = __float_as_uint(a.y);
+    x[t + 2] = __float_as_uint(b.x);
+    x[t + 3] = __float_as_uint(b.y);
+  }
+  if (mask) {
+#pragma unroll
+    for (int t = 0; t < 32; ++t)
+      if (!((mb >> t) & 1u)) x[t] = 0xff800000u;
+  }
+}
+__device__ __forceinline__ float max_chunk(const uint32_t (&x)[32]) {
   float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    tmem_ld_wait32(x[i]);
+  for (int t = 0; t < 32; t += 4) {
+    m0 = fmax3(m0, __uint_as_float(x[t]), __uint_as_float(x[t + 1]));
+    m1 = fmax3(m1, __uint_as_float(x[t + 2]), __uint_as_float(x[t + 3]));
+  }
+  return fmaxf(m0, m1);
+}
+// The weights of a chunk into its 16 columns of P; their sum before V's scales.
+__device__ __forceinline__ float2 weigh_chunk(uint32_t tP, const uint32_t (&x)[32], const float* vs, float sc, float m_use, float2 ls) {
+  const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-m_use, -m_use);
+  uint32_t pw[16];
 #pragma unroll
-    for (int t = 0; t < 32; t += 4) {
-      const float4 ks = *reinterpret_cast<const float4*>(&scales.k[32 * i + t]);
-      const float2 a = __fmul2_rn(make_float2(__uint_as_float(x[i][t]), __uint_as_float(x[i][t + 1])), make_float2(ks.x, ks.y));
-      const float2 c = __fmul2_rn(make_float2(__uint_as_float(x[i][t + 2]), __uint_as_float(x[i][t + 3])), make_float2(ks.z, ks.w));
-      float y[4] = {a.x, a.y, c.x, c.y};
+  for (int t = 0; t < 16; t += 2) {
+    const float4 v4 = *reinterpret_cast<const float4*>(vs + 2 * t);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (MASK && !((mb[i] >> (t + e)) & 1u)) y[e] = -INFINITY;
-        x[i][t + e] = __float_as_uint(y[e]);
-      }
-      m0 = fmax3(m0, y[0], y[1]);
-      m1 = fmax3(m1, y[2], y[3]);
+    for (int e = 0; e < 2; ++e) {
+      const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[2 * (t + e)]), __uint_as_float(x[2 * (t + e) + 1])), sc2, nm2);
+      const float2 p = make_float2(ex2(y.x), ex2(y.y));
+      ls = __fadd2_rn(ls, p);
+      const float2 w = __fmul2_rn(p, e == 0 ? make_float2(v4.x, v4.y) : make_float2(v4.z, v4.w));
+      pw[t + e] = pack16<true>(w.x, w.y);
     }
   }
-  const float mt = fmaf(fmaxf(m0, m1), sc, scales.top - kLift<true>);
+  tmem_st16(tP, pw);
+  return ls;
+}
+__device__ __forceinline__ void softmax_held(uint32_t tS, uint32_t tO, float sc, const Scales& scales, bool mask, const uint32_t (&mb)[4], bool few,
+                                             int quarter, bool first, float& m_run, float& l_run) {
+  uint32_t x[32], z[32];
+  float top;
+  if (few) {  // the warp's chunk stays in registers
+    tmem_ld32(tS + 32 * quarter, x);
+    scale_chunk(x, scales.k + 32 * quarter, mask, mb[0]);
+    top = max_chunk(x);
+  } else {
+    tmem_ld32_issue(tS, x);
+    tmem_ld32_issue(tS + 32, z);
+    tmem_ld_wait32(x);
+    scale_chunk(x, scales.k, mask, mb[0]);
+    top = max_chunk(x);
+    tmem_ld32_issue(tS + 64, x);
+    tmem_ld_wait32(z);
+    scale_chunk(z, scales.k + 32, mask, mb[1]);
+    top = fmaxf(top, max_chunk(z));
+    tmem_ld32_issue(tS + 96, z);
+    tmem_ld_wait32(x);
+    scale_chunk(x, scales.k + 64, mask, mb[2]);
+    top = fmaxf(top, max_chunk(x));
+    tmem_ld32_issue(tS, x);  // for the weights
+    tmem_ld_wait32(z);
+    scale_chunk(z, scales.k + 96, mask, mb[3]);
+    top = fmaxf(top, max_chunk(z));
+  }
+  const float4 vt = *reinterpret_cast<const float4*>(scales.top);
+  const float mt = fmaf(top, sc, fmaxf(fmaxf(vt.x, vt.y), fmaxf(vt.z, vt.w)) - kLift<true>);
   float corr = 1.f;
   if (mt > m_run + kRescale || (m_run == -INFINITY && mt > -INFINITY)) {
     corr = ex2(m_run - mt);  // 0 when m_run is -inf
     m_run = mt;
   }
   const float m_use = m_run == -INFINITY ? 0.f : m_run;
-  const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-m_use, -m_use);
   float2 ls = make_float2(0.f, 0.f);
+  if (few) {
+    ls = weigh_chunk(tS + 16 * quarter, x, scales.v + 32 * quarter, sc, m_use, ls);
+    const uint32_t none[16] = {};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t pw[16];
-#pragma unroll
-    for (int t = 0; t < 16; t += 2) {
-      const float4 vs = *reinterpret_cast<const float4*>(&scales.v[32 * i + 2 * t]);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[i][2 * (t + e)]), __uint_as_float(x[i][2 * (t + e) + 1])), sc2, nm2);
-        const float2 p = make_float2(ex2(y.x), ex2(y.y));
-        ls = __fadd2_rn(ls, p);
-        const float2 w = __fmul2_rn(p, e == 0 ? make_float2(vs.x, vs.y) : make_float2(vs.z, vs.w));
-        pw[t + e] = pack16<true>(w.x, w.y);
-      }
-    }
-    tmem_st16(tS + 16 * i, pw);
+    for (int i = 1; i < 4; ++i) tmem_st16(tS + 16 * ((quarter + i) & 3), none);
+  } else {
+    tmem_ld_wait32(x);
+    scale_chunk(x, scales.k, mask, mb[0]);
+    tmem_ld32_issue(tS + 32, z);
+    ls = weigh_chunk(tS, x, scales.v, sc, m_use, ls);
+    tmem_ld_wait32(z);
+    tmem_ld32_issue(tS + 64, x);
+    scale_chunk(z, scales.k + 32, mask, mb[1]);
+    ls = weigh_chunk(tS + 16, z, scales.v + 32, sc, m_use, ls);
+    tmem_ld_wait32(x);
+    tmem_ld32_issue(tS + 96, z);
+    scale_chunk(x, scales.k + 64, mask, mb[2]);
+    ls = weigh_chunk(tS + 32, x, scales.v + 64, sc, m_use, ls);
+    tmem_ld_wait32(z);
+    scale_chunk(z, scales.k + 96, mask, mb[3]);
+    ls = weigh_chunk(tS + 48, z, scales.v + 96, sc, m_use, ls);
   }
   l_run = l_run * corr + (ls.x + ls.y);
   if (!first && __any_sync(0xffffffffu, corr != 1.f)) {  // warp-uniform: tcgen05.ld/st are collective
 #pragma unroll 1
     for (int q4 = 0; q4 < 4; ++q4) {
-      uint32_t r32[32];
-      tmem_ld32(tO + 32 * q4, r32);
+      tmem_ld32(tO + 32 * q4, x);
 #pragma unroll
-      for (int t = 0; t < 32; ++t) r32[t] = __float_as_uint(__uint_as_float(r32[t]) * corr);
-      tmem_st32(tO + 32 * q4, r32);
+      for (int t = 0; t < 32; ++t) x[t] = __float_as_uint(__uint_as_float(x[t]) * corr);
+      tmem_st32(tO + 32 * q4, x);
     }
   }
   tmem_st_wait();
@@ -635,11 +733,11 @@ struct Box {
   bool mine;  // the lane has a box, and keys lie in it
   int pg, row;
 };
-template <bool EXT, bool HELD>
+template <bool EXT>
 __device__ __forceinline__ Box find_box(const TcAttnParams& P, const Walk<EXT>& wk, int kt, int lane, int pre_b) {
   const int nb = kTile >> P.box_shift, j = tile_key<EXT>(wk.it, kt) + ((lane & (nb - 1)) << P.box_shift);
   Box b;
-  b.mine = lane < (HELD ? nb : 2 * nb) && j < wk.it.keys;
+  b.mine = lane < 2 * nb && j < wk.it.keys;
   if constexpr (EXT) b.mine = b.mine && (j + (1 << P.box_shift) > wk.it.low || j < P.c.sinks);
   b.pg = b.row = 0;
   if (b.mine && !kv_locate(P.c.kv, EXT && wk.pb < 0 ? pre_b : wk.pb, j, &b.pg, &b.row)) atomicOr(P.c.status, kStatusIndex);  // reads as zeros
@@ -661,7 +759,7 @@ __device__ __forceinline__ RowAt row_at(const TcAttnParams& P, int b, int t) {
 }
 
 // Q rows of the present piece into shared memory, by N threads.
-template <int NT, bool F16, int KV, bool EXT, int N>
+template <int NT, bool EXT, int N>
 __device__ __forceinline__ void load_q(const TcAttnParams& P, const Walk<EXT>& wk, uint8_t* sm, int qt) {
   const CacheAttnParams& c = P.c;
   const int G = c.group;
@@ -680,24 +778,51 @@ __device__ __forceinline__ void load_q(const TcAttnParams& P, const Walk<EXT>& w
     }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
-  if constexpr (KV != 0 && !F16) {
-    // bf16 to fp16 in place: 16 lanes have a row, each the piece that it fetched
-    static_assert(N % 16 == 0, "a row's lanes are together");
+  fence_proxy_async_smem();
+}
+// The same over caches of 8 bits, as fp16 and by way of registers (16 lanes have a
+// row, and other copies of theirs stay in flight). few: every 32 rows of the tile
+// are the same ones.
+template <int NT, bool F16, bool EXT, int N>
+__device__ __forceinline__ void load_q_held(const TcAttnParams& P, const Walk<EXT>& wk, uint8_t* sm, int qt, bool few) {
+  const CacheAttnParams& c = P.c;
+  const int G = c.group;
 #pragma unroll 1
-    for (int ti = 0; ti < NT; ++ti) {
-      const int nv = max(0, min(P.tpt, wk.it.cnt - (wk.pm * NT + ti) * P.tpt)) * G, fill = ((nv + 31) & ~31) * 16;
-#pragma unroll 2
-      for (int e = qt; e < fill; e += N) {
-        const int row = e >> 4, ch = e & 15;
-        uint4* at = reinterpret_cast<uint4*>(sm + ti * kTileBytes + (ch >> 3) * kHalfBytes + sw128_off(row, ch & 7));
-        const uint4 x = *at;
-        uint32_t top = top_bits(x);
+  for (int ti = 0; ti < NT; ++ti) {
+    const int t0 = (wk.pm * NT + ti) * P.tpt;
+    const int nv = max(0, min(P.tpt, wk.it.cnt - t0)) * G, fill = ((nv + 31) & ~31) * 16;
+    uint8_t* tile = sm + ti * kTileBytes;
+    constexpr int U = 4;
+#pragma unroll 1
+    for (int e0 = qt; e0 < fill; e0 += U * N) {  // fill: a multiple of U N
+      uint4 x[U];
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        *at = to_f16(x, __int_as_float((row_shift(top) + 127) << 23));
+      for (int u = 0; u < U; ++u) {
+        const int e = e0 + u * N, row = e >> 4;
+        x[u] = make_uint4(0, 0, 0, 0);
+        if (row < nv) {
+          const RowAt at = row_at<EXT>(P, wk.pb, t0 + row / G);
+          x[u] = ld_v4(static_cast<const uint16_t*>(c.q.p) + at.b * c.q.sb + at.t * c.q.ss + (wk.ph * G + row % G) * c.q.sh + 8 * (e & 15));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int e = e0 + u * N, row = e >> 4, ch = e & 15;
+        if constexpr (!F16) {
+          uint32_t top = top_bits(x[u]);
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          x[u] = to_f16(x[u], __int_as_float((row_shift(top) + 127) << 23));
+        }
+        uint8_t* at = tile + (ch >> 3) * kHalfBytes + sw128_off(row, ch & 7);
+        *reinterpret_cast<uint4*>(at) = x[u];
+        if (few)
+#pragma unroll
+          for (int i = 1; i < 4; ++i) *reinterpret_cast<uint4*>(at + i * 32 * 128) = x[u];
       }
     }
   }
+  static_assert(N * 4 == 512, "32 rows a turn");
   fence_proxy_async_smem();
 }
 
@@ -713,21 +838,23 @@ __device__ __forceinline__ void stage_chunk32(uint8_t* base, int row, int q4, co
 }
 
 // The place of an item in the list of the call's items, and, where one CTA has
-// all of its tiles, of its result's first row (the call has a shared prefix).
+// all of its tiles, of its result's first row (calls that join by items).
 __device__ __forceinline__ int64_t item_index(const TcAttnParams& p, int h, int b, int m) {
   if (b < 0) return static_cast<int64_t>(h) * p.n_pre + m;
   return static_cast<int64_t>(p.c.kv.Hkv) * p.n_pre + (static_cast<int64_t>(h) * p.c.B + b) * p.n_groups + m;
 }
 __device__ __forceinline__ int64_t whole_part(const TcAttnParams& p, int h, int b, int m) {
   const int64_t first = 2 * static_cast<int64_t>(p.ctas) * p.split_rows, pre = static_cast<int64_t>(p.c.kv.Hkv) * p.n_pre, i = item_index(p, h, b, m);
-  return b < 0 ? first + i * p.pre_rows : first + pre * p.pre_rows + (i - pre) * p.part_rows;
+  return b < 0 ? first + i * p.pre_rows : first + pre * p.pre_rows + (i - pre) * p.part_rows * (p.few ? 4 : 1);
 }
 
 // F16: the type of q and o (and of a 16-bit cache). KV: 0, kDtE4M3 or kDtI8.
 template <int NT, bool F16, bool TREE, bool CL, int KV, bool EXT>
-__global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant__ TcAttnParams P) {
+__global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const __grid_constant__ TcAttnParams P) {
   constexpr bool HELD = KV != 0, OP16 = F16 || HELD;  // fp16 operands
   using L = Lay<NT, HELD>;
+  constexpr int kWarpMma = Roles<HELD>::kWarpMma, kWarpK = Roles<HELD>::kWarpK, kWarpV = Roles<HELD>::kWarpV, kTcWarps = Roles<HELD>::kWarps;
+  constexpr int kRegsSoft = Roles<HELD>::kRegsSoft, kRegsRest = Roles<HELD>::kRegsRest;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw;
   const CacheAttnParams& c = P.c;
@@ -748,15 +875,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
     tmem_relinquish();
   }
   if (tid == 0) {
-    mbar_init(&bars[L::QFull], HELD && NT == 1 ? 32 : kQWarps * 32);
+    mbar_init(&bars[L::QFull], kQWarps * 32);
     mbar_init(&bars[L::QEmpty], 2);
-    for (int s = 0; s < L::RS; ++s) {
-      mbar_init(&bars[L::RawFull + s], 1);
-      mbar_init(&bars[L::RawEmpty + s], kQWarps);
-    }
     if constexpr (HELD)
-      for (int s = 0; s < 2; ++s) {
-        mbar_init(&bars[L::ScFull + s], 32);
+      for (int s = 0; s < L::SS; ++s) {
+        mbar_init(&bars[L::ScFull + s], 2 * kQWarps);
         mbar_init(&bars[L::ScEmpty + s], 4 * NT);  // NT = 1: a slot's own
       }
     for (int s = 0; s < L::KS; ++s) {
@@ -779,8 +902,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
     *pipe_lock = 0;
     fence_mbar_init();
   }
-  if (tid == kWarpK * 32) tma_prefetch_desc(&P.tmap_k);
-  if (tid == kWarpV * 32) tma_prefetch_desc(&P.tmap_v);
+  if (!HELD && tid == kWarpK * 32) tma_prefetch_desc(&P.tmap_k);
+  if (!HELD && tid == kWarpV * 32) tma_prefetch_desc(&P.tmap_v);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -806,7 +929,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
       atomicOr(c.status, kStatusIndex);
   } else {
     // the scan's scratch lies in the Q tile, which is written later
-    find_start<EXT>(P, NT, reinterpret_cast<long long*>(sm + L::q), start);
+    find_start<EXT, kTcWarps>(P, NT, reinterpret_cast<long long*>(sm + L::q), start);
     wk.h = start->h;
     wk.b = start->b;
     wk.m = start->m;
@@ -817,10 +940,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
       pre_b = start->pre_b;
     }
   }
-  const bool shared = EXT && !CL && c.shared;
+  const bool by_items = EXT && !CL && P.item_meta;  // every result is joined
+  using Place = typename Walk<EXT>::Place;
+  static_assert(sizeof(Place) == 24, "layout");
+  Place* place = reinterpret_cast<Place*>(sm + L::walk) + warp;  // HELD: this warp's, and a second one kTcWarps further on
+  if constexpr (HELD && !CL) {
+    if (lane_id == 0) {
+      wk.save(place);
+      wk.save(place + kTcWarps);
+    }
+    __syncwarp();
+  }
+  // the next piece of walk `w` (second: the warp's other walk)
+  auto next_piece = [&](Walk<EXT>& w, auto warp_wide, bool second) -> bool {
+    if constexpr (HELD && !CL) return w.template next_from<CL, decltype(warp_wide)::value>(P, NT, place + (second ? kTcWarps : 0));
+    else return w.template next<CL>(P, NT);
+  };
+  constexpr std::true_type all_lanes;
+  constexpr std::false_type one_lane;
   const int G = c.group, tile_rows = P.tpt * G;
   float2* part_ml = reinterpret_cast<float2*>(sm + L::k + NT * 65536);  // CL
-  static_assert(NT * (65536 + 1024) <= (L::KS + L::VS) * kTileBytes + L::RS * kRawBytes, "a part fits over the stages");
+  static_assert(NT * (65536 + 1024) <= (L::KS + L::VS) * kTileBytes + (L::RK + L::RV) * L::kRawBytes, "a part fits over the stages");
 
   if (warp < kSoftWarps) {
     // -------------------------------------------------------------- softmax
@@ -841,17 +981,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
     const int r = (warp & 3) * 32 + lane_id;
     const uint32_t lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + slot * 128 + lane, tO = tmem + 256 + slot * 128 + lane;
-    const int rt = r / G, rg = r - rt * G;
+    const int r_few = r & 31;  // FEW: the row, of which this warp has a quarter of the keys
+    const bool call_few = HELD && NT == 1 && P.few;
+    int rt = r / G, rg = r - rt * G;
     const float sc = c.scale_log2;
     long long g = 0;    // score tiles before the present piece
     int vc = 0;         // key tiles before the present piece
     int n_piece = 0;
     bool ok = true, at_start = true;
-    long long tile_at = shared ? start->first : 0;  // of the call's
-    while (ok && wk.template next<CL>(P, NT)) {
+    long long tile_at = by_items ? start->first : 0;  // of the call's
+    while (ok && next_piece(wk, all_lanes, false)) {
       const int steps = (wk.kt1 - wk.kt0) * NT;
+      const bool few = call_few && wk.pb >= 0;
+      if constexpr (HELD && NT == 1) {
+        const int rr = few ? r_few : r;
+        rt = rr / G;
+        rg = rr - rt * G;
+      }
       const int t = (wk.pm * NT + (NT == 2 ? slot : 0)) * P.tpt + rt;
-      const bool valid = r < tile_rows && t < wk.it.cnt;
+      const bool valid = (few ? r_few : r) < tile_rows && t < wk.it.cnt;
       const bool act = __any_sync(0xffffffffu, valid);  // this warp has rows
       uint32_t anc[kTreeWords] = {};
       int low = 0, low_last = 0;  // where the row's window begins, and the last of the warp's
@@ -899,9 +1047,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
         if (!(ok = wait_bar_warp(&bars[L::SFull + slot], (gg >> 1) & 1, abort_flag, budget))) break;
         const int sc_at = NT == 2 ? vc + kt - wk.kt0 : static_cast<int>(gg);  // HELD: the tile, counted by the CTA
         if constexpr (HELD) {
-          if (!(ok = wait_bar_warp(&bars[L::ScFull + (sc_at & 1)], (sc_at >> 1) & 1, abort_flag, budget))) break;
+          if (!(ok = wait_bar_warp(&bars[L::ScFull + sc_at % L::SS], (sc_at / L::SS) & 1, abort_flag, budget))) break;
         }
-        const Scales& scales = reinterpret_cast<const Scales*>(sm + L::sc)[sc_at & 1];
+        const Scales& scales = reinterpret_cast<const Scales*>(sm + L::sc)[HELD ? sc_at % (HELD ? L::SS : 1) : 0];
         tc_fence_after();
         if (act) {
           // the first node that the warp's first token does not see
@@ -910,23 +1058,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
           if constexpr (EXT) all = all && (c.window == 0 || j0 >= low_last || j0 + kTile <= c.sinks);
           if (all) {
             const uint32_t mb[4] = {~0u, ~0u, ~0u, ~0u};
-            if constexpr (HELD) softmax_held<false>(tS, tO, row_sc, scales, mb, first, m_run, l_run);
+            if constexpr (HELD) softmax_held(tS, tO, row_sc, scales, false, mb, few, warp & 3, first, m_run, l_run);
             else softmax_tile<F16, false>(tS, tO, sc, mb, first, m_run, l_run);
           } else {
-            uint32_t mb[4];
+            uint32_t mb[4] = {};
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              mb[w] = valid ? key_bits<TREE>(j0 + 32 * w, wk.it, t, anc) : 0u;
-              if (EXT && c.window > 0) mb[w] &= window_bits<TREE>(j0 + 32 * w, low, c.sinks, wk.it.prefix);
+              if (HELD && few && w > 0) break;  // mb[0]: the warp's own quarter
+              const int j = j0 + 32 * (HELD && few ? warp & 3 : w);
+              mb[w] = valid ? key_bits<TREE>(j, wk.it, t, anc) : 0u;
+              if (EXT && c.window > 0) mb[w] &= window_bits<TREE>(j, low, c.sinks, wk.it.prefix);
             }
-            if constexpr (HELD) softmax_held<true>(tS, tO, row_sc, scales, mb, first, m_run, l_run);
+            if constexpr (HELD) softmax_held(tS, tO, row_sc, scales, true, mb, few, warp & 3, first, m_run, l_run);
             else softmax_tile<F16, true>(tS, tO, sc, mb, first, m_run, l_run);
           }
         }
         first = false;
         if constexpr (HELD) {
           __syncwarp();
-          if (lane_id == 0) mbar_arrive(&bars[L::ScEmpty + (sc_at & 1)]);
+          if (lane_id == 0) mbar_arrive(&bars[L::ScEmpty + sc_at % L::SS]);
         }
         if (!HELD && (j0 + kTile > wk.it.keys || (EXT && j0 < wk.it.low && j0 + kTile > c.sinks))) {
           // rows of V behind the last key (or before every window) hold anything:
@@ -943,12 +1093,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
       if (!ok) break;
       // ---- the piece's result
       const int h = wk.ph * G + rg;
-      const bool whole = wk.whole() && !shared;
+      const bool whole = wk.whole() && !by_items;
       const int64_t pslot = 2 * static_cast<int64_t>(blockIdx.x) + (at_start ? 0 : 1);
       at_start = false;
       int64_t prow0 = pslot * P.part_rows;  // the part's first row
       if constexpr (EXT && !CL) {
-        if (shared) {
+        if (by_items) {
           prow0 = pslot * P.split_rows;
           if (wk.whole()) prow0 = whole_part(P, wk.ph, wk.pb, wk.pm);
           if (tid == 0 && wk.kt0 == 0) {
@@ -1001,7 +1151,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
           const float l = f0 * l_run + f1 * other.y, inv = whole && !CL ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
           const bool mine = steps > 1 || (g & 1) == slot, theirs = steps > 1 || (g & 1) != slot;
           const int64_t ooff = wk.pb * c.o_sb + static_cast<int64_t>(t) * c.o_ss + static_cast<int64_t>(h) * c.o_sh;
-          const int64_t prow = prow0 + r;
+          const int64_t prow = prow0 + (few ? (warp & 3) * P.part_rows + r_few : r);
           const uint32_t tOther = tmem + 256 + (slot ^ 1) * 128 + lane;
 #pragma unroll 1
           for (int q = 0; q < 2; ++q) {
@@ -1039,198 +1189,155 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
       ++n_piece;
     }
     if (CL && n_piece == 0 && (NT == 2 || slot == 0)) part_ml[(NT == 2 ? slot * 128 : 0) + r] = make_float2(-INFINITY, 0.f);
-  } else if (warp < kWarpQ0 + kQWarps) {
+  } else if (warp < kWarpMma) {
     // ---------------------------------------------------------------- Q rows
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     const int qt = tid - kWarpQ0 * 32;
     int n_piece = 0;
     if constexpr (HELD) {
       // ------------------------------------------------- bytes into operands
-      // in the order of the TMA: K of tile i, then V of tile i - 1
-      Walk<EXT> wv = wk;  // V's
-      const int cg = qt & 7, r0 = qt >> 3;  // 16 columns of rows r0 + 16 u of a stage
-      bool ok = true;
-      int raw = 0;
-      // One operand tile; V: rows that no row sees become zeros.
-      auto convert = [&](uint8_t* tile, uint64_t* empty, bool used, uint32_t parity, auto&& sees) -> bool {
-#pragma unroll 1
-        for (int half = 0; half < kTile / kRawRows; ++half, ++raw) {
-          const int st = raw % L::RS;
-          if (!wait_bar_warp(&bars[L::RawFull + st], (raw / L::RS) & 1, abort_flag, budget)) return false;
-          uint4 x[kRawRows / 16];
-#pragma unroll
-          for (int u = 0; u < kRawRows / 16; ++u)
-            x[u] = *reinterpret_cast<const uint4*>(sm + L::raw + st * kRawBytes + (r0 + 16 * u) * kD + 16 * cg);
-          if (half == 0 && used && !wait_bar_warp(empty, parity, abort_flag, budget)) return false;
-#pragma unroll
-          for (int u = 0; u < kRawRows / 16; ++u) {
-            const int row = half * kRawRows + r0 + 16 * u;
-            if (!sees(row)) x[u] = make_uint4(0, 0, 0, 0);
-            uint4 a, b;
-            held_f16<KV>(x[u].x, a.x, a.y);
-            held_f16<KV>(x[u].y, a.z, a.w);
-            held_f16<KV>(x[u].z, b.x, b.y);
-            held_f16<KV>(x[u].w, b.z, b.w);
-            // columns 16 cg .. + 16 are chunks 2 cg and 2 cg + 1; the upper four
-            // lanes of a row write theirs the other way round: no bank twice
-            const int ch = (cg & 3) * 2, first = cg >> 2;
-            uint8_t* dst = tile + (cg >> 2) * kHalfBytes;
-            *reinterpret_cast<uint4*>(dst + sw128_off(row, ch + first)) = first ? b : a;
-            *reinterpret_cast<uint4*>(dst + sw128_off(row, ch + 1 - first)) = first ? a : b;
-          }
-          // after the bytes' last use: let go right after the loads, the stage was
-          // overwritten under them (64 keys of K with V's numbers)
-          __syncwarp();
-          if (lane_id == 0) mbar_arrive(&bars[L::RawEmpty + st]);
+      const bool is_v = warp >= kWarpQ0 + kQWarps;
+      constexpr int kParts = kTile / L::kRawRows, kU = L::kRawRows / 16;  // stages of a tile, a thread's pieces of a stage
+      const PagedKV& kv = c.kv;
+      const int gw = warp & 3, cg = lane_id & 7, r0 = 4 * gw + (lane_id >> 3);  // 16 columns of rows r0 + 16 u
+      uint64_t* full = &bars[is_v ? L::VFull : L::KFull];
+      uint64_t* empty = &bars[is_v ? L::VEmpty : L::KEmpty];
+      uint8_t* tiles = sm + (is_v ? L::v : L::k);
+      static_assert(L::KS == L::VS, "one count");
+      uint8_t* raw = sm + L::raw + (is_v ? L::RK : 0) * L::kRawBytes + r0 * kD + 16 * cg;
+      const int n_raw = is_v ? L::RV : L::RK;
+      // ---- the stream of fetches, up to n_raw stages ahead of the conversion. A
+      // lane looks up the place of one of its warp's 32 rows of a tile, a tile ahead
+      // of the fetch, and has that row's scale.
+      const int my_row = 4 * gw + (lane_id & 3) + 16 * (lane_id >> 2);
+      Walk<EXT> wl = wk;
+      bool l_have = next_piece(wl, all_lanes, true), l_in = false;
+      int lt = wl.kt0, l_pg = 0, l_row = 0, l_h = 0;
+      auto look = [&]() {  // the next tile
+        const int j = tile_key<EXT>(wl.it, lt) + my_row;
+        l_in = j < wl.it.keys && (!EXT || j >= wl.it.low || j < c.sinks);  // (keys lie within the table)
+        l_h = wl.ph;
+        if (l_in) {
+          const int at = kv.page_shift >= 0 ? j >> kv.page_shift : j / kv.page;
+          l_row = j - at * kv.page;
+          l_pg = ld_now(kv.pages + (EXT && wl.pb < 0 ? pre_b : wl.pb) * kv.p_sb + at);
         }
-        fence_proxy_async_smem();
+        if (++lt == wl.kt1) {
+          l_have = next_piece(wl, all_lanes, true);
+          lt = wl.kt0;
+        }
+      };
+      bool there = l_have;  // a tile was looked up
+      if (there) look();
+      int i_tile = 0, i_part = 0, i_slot = 0;
+      bool i_have = false;
+      int64_t off = -1;  // of the lane's row, < 0: no row
+      auto fetch = [&]() -> bool {
+        if (i_part == 0) {
+          i_have = there;
+          if (there) {
+            off = -1;
+            const float* sc_at = nullptr;
+            if (l_in && static_cast<unsigned>(l_pg) >= static_cast<unsigned>(kv.n_pages)) atomicOr(c.status, kStatusIndex);  // reads as zeros
+            else if (l_in) {
+              off = is_v ? l_pg * kv.v_sp + l_row * kv.v_sr + l_h * kv.v_sh : l_pg * kv.k_sp + l_row * kv.k_sr + l_h * kv.k_sh;
+              sc_at = is_v ? kv.vs + l_pg * kv.vs_sp + l_h * kv.vs_sh + l_row : kv.ks + l_pg * kv.ks_sp + l_h * kv.ks_sh + l_row;
+            }
+            there = l_have;
+            if (there) look();
+            const int st = i_tile % L::SS;
+            if (i_tile >= L::SS && !wait_bar_warp(&bars[L::ScEmpty + st], ((i_tile / L::SS) - 1) & 1, abort_flag, budget)) return false;
+            Scales& s = reinterpret_cast<Scales*>(sm + L::sc)[st];
+            cp_async4(is_v ? &s.v[my_row] : &s.k[my_row], sc_at ? sc_at : kv.ks, sc_at != nullptr);
+            ++i_tile;
+          }
+        }
+        if (i_have) {
+          uint8_t* dst = raw + i_slot * L::kRawBytes;
+          const uint8_t* base = static_cast<const uint8_t*>(is_v ? kv.v : kv.k);
+#pragma unroll
+          for (int u = 0; u < kU; ++u) {
+            const long long o = __shfl_sync(0xffffffffu, static_cast<long long>(off), (lane_id >> 3) + 4 * (i_part * kU + u));
+            cp_async16(dst + u * 16 * kD, base + (o < 0 ? 0 : o + 16 * cg), o >= 0);
+          }
+          if (++i_part == kParts) i_part = 0;
+          if (++i_slot == n_raw) i_slot = 0;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
         return true;
       };
-      bool have = wk.template next<CL>(P, NT), have_v = wv.template next<CL>(P, NT);
-      int kt = wk.kt0, vt = wv.kt0, kn = 0, vn = 0;
-      while (ok && have_v) {
-        if (have) {
-          if (NT == 2 && kt == wk.kt0) {
-            // a new piece: its rows, once the last one's scores are done (all that
-            // these wait for, V of the last tile but one among it, is there)
-            if (n_piece > 0 && !(ok = wait_bar_warp(&bars[L::QEmpty], (n_piece - 1) & 1, abort_flag, budget))) break;
-            load_q<NT, F16, KV, EXT, kQWarps * 32>(P, wk, sm + L::q, qt);
-            mbar_arrive(&bars[L::QFull]);
-            ++n_piece;
-          }
-          const int st = kn % L::KS;
-          if (!(ok = convert(sm + L::k + st * kTileBytes, &bars[L::KEmpty + st], kn >= L::KS, ((kn / L::KS) - 1) & 1, [](int) { return true; }))) break;
-          mbar_arrive(&bars[L::KFull + st]);
-          ++kn;
-          if (++kt == wk.kt1) {
-            have = wk.template next<CL>(P, NT);
-            kt = wk.kt0;
-          }
+#pragma unroll 1
+      for (int i = 0; i < n_raw; ++i) fetch();  // fewer tiles than SS: no wait
+      // ---- the conversion. Columns 16 cg .. + 16 are chunks 2 cg and 2 cg + 1; the
+      // upper four lanes of a row write theirs the other way round: no bank twice.
+      // Rows r0 + 16 u have the swizzle of r0.
+      const uint32_t ch = (cg & 3) * 2, odd = cg >> 2;
+      const uint32_t at0 = (cg >> 2) * kHalfBytes + sw128_off(r0, ch + odd), at1 = (cg >> 2) * kHalfBytes + sw128_off(r0, ch + 1 - odd);
+      bool ok = true, have = next_piece(wk, all_lanes, false);
+      int kt = wk.kt0, n = 0, slot = 0;
+      while (ok && have) {
+        if (!is_v && kt == wk.kt0) {
+          // a new piece: its rows, once the last one's scores are done
+          if (n_piece > 0 && !(ok = wait_bar_warp(&bars[L::QEmpty], (n_piece - 1) & 1, abort_flag, budget))) break;
+          load_q_held<NT, F16, EXT, kQWarps * 32>(P, wk, sm + L::q, qt, NT == 1 && P.few && wk.pb >= 0);
+          mbar_arrive(&bars[L::QFull]);
+          ++n_piece;
         }
-        if (kn < vn + 2 && have) continue;  // K is one tile ahead
-        const int st = vn % L::VS, j0 = tile_key<EXT>(wv.it, vt);
-        const int n_low = EXT ? wv.it.low - j0 : 0, n_sink = EXT ? min(c.sinks, 1 << 30) - j0 : 0, n_keys = wv.it.keys - j0;
-        if (!(ok = convert(sm + L::v + st * kTileBytes, &bars[L::VEmpty + st], vn >= L::VS, ((vn / L::VS) - 1) & 1,
-                           [&](int row) { return row < n_keys && (row >= n_low || row < n_sink); })))
-          break;
-        mbar_arrive(&bars[L::VFull + st]);
-        ++vn;
-        if (++vt == wv.kt1) {
-          have_v = wv.template next<CL>(P, NT);
-          vt = wv.kt0;
+        const int op = n % L::KS;
+        uint8_t* dst = tiles + op * kTileBytes;
+#pragma unroll 1
+        for (int part = 0; part < kParts; ++part) {
+          if (is_v) asm volatile("cp.async.wait_group %0;" ::"n"(HELD ? L::RV - 1 : 0) : "memory");
+          else asm volatile("cp.async.wait_group %0;" ::"n"(HELD ? L::RK - 1 : 0) : "memory");
+          if (part == 0) {
+            const int st = n % L::SS;
+            Scales& s = reinterpret_cast<Scales*>(sm + L::sc)[st];
+            if (is_v) {
+              const float v = fabsf(s.v[my_row]);
+              const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, v == v ? __float_as_uint(v) : 0u));
+              if (lane_id == 0) s.top[gw] = fminf(fmaxf(log2f(top), -kTopRange), kTopRange);
+            }
+            __syncwarp();
+            if (lane_id == 0) mbar_arrive(&bars[L::ScFull + st]);
+            if (n >= L::KS && !(ok = wait_bar_warp(&empty[op], ((n / L::KS) - 1) & 1, abort_flag, budget))) break;
+          }
+          const uint8_t* src = raw + slot * L::kRawBytes;
+#pragma unroll
+          for (int u = 0; u < kU; ++u) {
+            const uint4 x = *reinterpret_cast<const uint4*>(src + u * 16 * kD);
+            uint4 a, b;
+            held_f16<KV>(x.x, a.x, a.y);
+            held_f16<KV>(x.y, a.z, a.w);
+            held_f16<KV>(x.z, b.x, b.y);
+            held_f16<KV>(x.w, b.z, b.w);
+            *reinterpret_cast<uint4*>(dst + at0 + (part * kU + u) * 16 * 128) = odd ? b : a;
+            *reinterpret_cast<uint4*>(dst + at1 + (part * kU + u) * 16 * 128) = odd ? a : b;
+          }
+          if (!(ok = fetch())) break;  // into the stage that has just been read, by this thread
+          if (++slot == n_raw) slot = 0;
+        }
+        if (!ok) break;
+        fence_proxy_async_smem();
+        mbar_arrive(&full[op]);
+        ++n;
+        if (++kt == wk.kt1) {
+          have = next_piece(wk, all_lanes, false);
+          kt = wk.kt0;
         }
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
       while (wk.template next<CL>(P, NT)) {
         if (n_piece > 0 && !wait_bar_warp(&bars[L::QEmpty], (n_piece - 1) & 1, abort_flag, budget)) break;
-        load_q<NT, F16, KV, EXT, kQWarps * 32>(P, wk, sm + L::q, qt);
+        load_q<NT, EXT, kQWarps * 32>(P, wk, sm + L::q, qt);
         mbar_arrive(&bars[L::QFull]);
         ++n_piece;
       }
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-    if (HELD && warp == kWarpK) {
-      // ------------------------------------------------------- TMA of bytes
-      // K of tile i, then V of tile i - 1: a box per lane, 64 keys a stage
-      const int nb = kTile >> P.box_shift, half = (lane_id << P.box_shift) / kRawRows;
-      const uint32_t dst = ((lane_id << P.box_shift) % kRawRows) * kD;
-      int raw = 0;
-      bool ok = true;
-      auto fetch = [&](const Box& box, int h, const CUtensorMap* map, bool r_first) -> bool {
-        const uint32_t boxes = __ballot_sync(0xffffffffu, box.mine);
-        const int per = kRawRows >> P.box_shift;  // boxes of a stage
-#pragma unroll 1
-        for (int i = 0; i < kTile / kRawRows; ++i, ++raw) {
-          const int st = raw % L::RS;
-          if (raw >= L::RS && !wait_bar_warp(&bars[L::RawEmpty + st], ((raw / L::RS) - 1) & 1, abort_flag, budget)) return false;
-          const uint32_t here = (boxes >> (i * per)) & ((1u << per) - 1u);
-          if (lane_id == 0) mbar_arrive_expect_tx(&bars[L::RawFull + st], (__popc(here) << P.box_shift) * kD);
-          __syncwarp();
-          if (box.mine && lane_id < nb && half == i)
-            tma_load_4d(sm + L::raw + st * kRawBytes + dst, map, &bars[L::RawFull + st], 0, r_first ? box.row : h, r_first ? h : box.row, box.pg);
-        }
-        return true;
-      };
-      bool have = wk.template next<CL>(P, NT), last = false;  // last: the tile before is there
-      int kt = wk.kt0, h_last = 0;
-      Box box{false, 0, 0}, box_last{false, 0, 0};
-      if (have) box = find_box<EXT, true>(P, wk, kt, lane_id, pre_b);
-      while (ok && (have || last)) {
-        const Box now = box;
-        const int h = wk.ph;
-        const bool there = have;
-        if (there) {
-          if (!(ok = fetch(now, h, &P.tmap_k, P.k_r_first != 0))) break;
-          if (++kt == wk.kt1) {
-            have = wk.template next<CL>(P, NT);
-            kt = wk.kt0;
-          }
-          if (have) box = find_box<EXT, true>(P, wk, kt, lane_id, pre_b);
-        }
-        if (last && !(ok = fetch(box_last, h_last, &P.tmap_v, P.v_r_first != 0))) break;
-        box_last = now;
-        h_last = h;
-        last = there;
-      }
-      for (int m = max(0, raw - L::RS); m < raw; ++m) mbar_wait(&bars[L::RawFull + m % (HELD ? L::RS : 1)], (m / (HELD ? L::RS : 1)) & 1, budget);
-    } else if (HELD && warp == kWarpV) {
-      // --------------------------------------- scales, and Q rows where few
-      Scales* ring = reinterpret_cast<Scales*>(sm + L::sc);
-      const PagedKV& kv = c.kv;
-      float4 ks, vs;
-      auto fetch = [&](int kt) {  // a lane's four keys: pages are multiples of 8
-        const int j = tile_key<EXT>(wk.it, kt) + 4 * lane_id;
-        ks = vs = make_float4(0.f, 0.f, 0.f, 0.f);
-        int pg, row;
-        if (j >= wk.it.keys || (EXT && j + 4 <= wk.it.low && j >= c.sinks)) return;
-        if (!kv_locate(kv, EXT && wk.pb < 0 ? pre_b : wk.pb, j, &pg, &row)) return;  // zeros; the boxes' warp reports it
-        const float* a = kv.ks + pg * kv.ks_sp + wk.ph * kv.ks_sh + row;
-        const float* b = kv.vs + pg * kv.vs_sp + wk.ph * kv.vs_sh + row;
-        if (P.sc_wide) {
-          ks = ld_now(reinterpret_cast<const float4*>(a));
-          vs = ld_now(reinterpret_cast<const float4*>(b));
-        } else {
-          ks = make_float4(ld_now(a), ld_now(a + 1), ld_now(a + 2), ld_now(a + 3));
-          vs = make_float4(ld_now(b), ld_now(b + 1), ld_now(b + 2), ld_now(b + 3));
-        }
-      };
-      // keys that no row sees have the scale 0
-      auto cut = [&](float4 x, int j) {
-        float y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (j + e >= wk.it.keys || (EXT && j + e < wk.it.low && j + e >= c.sinks)) y[e] = 0.f;
-        return make_float4(y[0], y[1], y[2], y[3]);
-      };
-      bool ok = true, have = wk.template next<CL>(P, NT);
-      int n = 0, kt = wk.kt0, n_piece = 0;
-      if (have) fetch(kt);
-      while (ok && have) {
-        if (NT == 1 && kt == wk.kt0) {
-          if (n_piece > 0 && !(ok = wait_bar_warp(&bars[L::QEmpty], (n_piece - 1) & 1, abort_flag, budget))) break;
-          load_q<NT, F16, KV, EXT, 32>(P, wk, sm + L::q, lane_id);
-          mbar_arrive(&bars[L::QFull]);
-          ++n_piece;
-        }
-        const int j = tile_key<EXT>(wk.it, kt) + 4 * lane_id;
-        const float4 k4 = cut(ks, j), v4 = cut(vs, j);
-        float top = fmaxf(fmaxf(fabsf(v4.x), fabsf(v4.y)), fmaxf(fabsf(v4.z), fabsf(v4.w)));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (n >= 2 && !(ok = wait_bar_warp(&bars[L::ScEmpty + (n & 1)], ((n >> 1) - 1) & 1, abort_flag, budget))) break;
-        Scales& s = ring[n & 1];
-        *reinterpret_cast<float4*>(&s.k[4 * lane_id]) = k4;
-        *reinterpret_cast<float4*>(&s.v[4 * lane_id]) = v4;
-        if (lane_id == 0) s.top = fminf(fmaxf(log2f(top), -kTopRange), kTopRange);
-        mbar_arrive(&bars[L::ScFull + (n & 1)]);
-        ++n;
-        if (++kt == wk.kt1) {
-          have = wk.template next<CL>(P, NT);
-          kt = wk.kt0;
-        }
-        if (have) fetch(kt);
-      }
+    if (HELD && (warp == kWarpK || warp == kWarpV)) {
+      // nothing: registers are split by groups of four warps
     } else if (warp == kWarpK || warp == kWarpV) {
       // ------------------------------------------------------- TMA of K and V
       const bool is_k = warp == kWarpK;
@@ -1246,7 +1353,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
       bool ok = true, have = wk.template next<CL>(P, NT);
       int kt = wk.kt0;
       Box box{false, 0, 0};
-      if (have) box = find_box<EXT, false>(P, wk, kt, lane_id, pre_b);
+      if (have) box = find_box<EXT>(P, wk, kt, lane_id, pre_b);
       while (ok && have) {
         const int st = n % stages;
         const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, box.mine));
@@ -1260,7 +1367,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
           have = wk.template next<CL>(P, NT);
           kt = wk.kt0;
         }
-        if (have) box = find_box<EXT, false>(P, wk, kt, lane_id, pre_b);
+        if (have) box = find_box<EXT>(P, wk, kt, lane_id, pre_b);
         ++n;
       }
       // every issued load lands before the CTA exits
@@ -1280,8 +1387,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
       int s_left = 0, s_kn = 0, s_next = 0, s_piece = -1, p_left = 0, p_kn = 0, p_next = 0, p_done = 0, p_piece = 0;
       // Enters the next piece: its first key tile and its number of tiles for
       // this slot (none, where NT = 1 and its only tile is the other slot's).
-      auto enter = [&](Walk<EXT>& w, int& kn, int& next, int& left) -> bool {
-        if (!w.template next<CL>(P, NT)) return false;
+      auto enter = [&](Walk<EXT>& w, bool second, int& kn, int& next, int& left) -> bool {
+        if (!next_piece(w, one_lane, second)) return false;
         const int tiles = w.kt1 - w.kt0;
         // NT = 1: the slots take alternate tiles of the whole stream
         const int skip = NT == 2 ? 0 : (slot ^ next) & 1;
@@ -1294,7 +1401,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
       // makes the slot's next score tile ready to be issued, if any is left
       auto find_scores = [&]() -> bool {
         while (s_left == 0) {
-          if (!enter(ws, s_kn, s_next, s_left)) {
+          if (!enter(ws, true, s_kn, s_next, s_left)) {
             more = false;
             return true;
           }
@@ -1342,7 +1449,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
         return true;
       };
       ok = find_scores() && (!more || batch(scores));
-      while (ok && enter(wk, p_kn, p_next, p_left)) {
+      while (ok && enter(wk, false, p_kn, p_next, p_left)) {
         for (int i = 0; i < p_left; ++i, ++p_done) {
           const bool same = s_left > 0;  // the next scores are of the same piece: Q is there
           if (same && !(ok = find_scores())) break;
@@ -1385,6 +1492,36 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_kernel(const __grid_constant
   }
   tc_fence_before();
   if constexpr (CL) {
+    if constexpr (HELD && NT == 1) {
+      // FEW: the four groups' results become one
+      if (P.few && warp < kSoftWarps) {
+        named_bar(1, kSoftWarps * 32);
+        const int there = max(0, min(P.tpt, wk.it.cnt - wk.m * P.tpt)) * G;
+        for (int e = warp; e < there; e += kSoftWarps) {
+          float2 x[4];
+          float4 y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[i] = part_ml[32 * i + e];
+            y[i] = *reinterpret_cast<const float4*>(sm + L::k + stage_off(32 * i + e, lane_id));
+          }
+          const float top = fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x)), use = top == -INFINITY ? 0.f : top;
+          float l = 0.f;
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (x[i].x == -INFINITY) continue;
+            const float f = ex2(x[i].x - use);
+            l = fmaf(f, x[i].y, l);
+            o = make_float4(fmaf(f, y[i].x, o.x), fmaf(f, y[i].y, o.y), fmaf(f, y[i].z, o.z), fmaf(f, y[i].w, o.w));
+          }
+          __syncwarp();
+          *reinterpret_cast<float4*>(sm + L::k + stage_off(e, lane_id)) = o;
+          if (lane_id == 0) part_ml[e] = make_float2(top, l);
+        }
+        __syncwarp();
+      }
+    }
     cluster_sync();  // every CTA's part is in place
     const int rank = static_cast<int>(cluster_rank()), m = wk.m, b = wk.b, h = wk.h;
     const int there = max(0, min(NT * P.tpt, wk.it.cnt - m * NT * P.tpt)) * G;  // rows, tile after tile
@@ -1443,7 +1580,7 @@ cudaError_t launch_t(const TcAttnParams& p, cudaStream_t stream) {
   if constexpr (CL) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.cluster * p.c.kv.Hkv, p.c.B * p.n_groups);
-    cfg.blockDim = dim3(kTcThreads);
+    cfg.blockDim = dim3(Roles<KV != 0>::kThreads);
     cfg.dynamicSmemBytes = bytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -1456,7 +1593,7 @@ cudaError_t launch_t(const TcAttnParams& p, cudaStream_t stream) {
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, p);
   }
-  return launch_chained(kern, dim3(p.ctas), dim3(kTcThreads), bytes, stream, p);
+  return launch_chained(kern, dim3(p.ctas), dim3(Roles<KV != 0>::kThreads), bytes, stream, p);
 }
 template <int NT, bool CL, int KV, bool EXT>
 cudaError_t launch_nt(const TcAttnParams& p, bool f16, cudaStream_t stream) {

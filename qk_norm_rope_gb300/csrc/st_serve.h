@@ -190,12 +190,12 @@ struct TcAttnParams {
   int cluster_shift;
   struct JoinMeta* meta;       // [ctas], workspace
   float2* part_ml;             // [2 ctas, part_rows] (reference, sum); c.part: [2 ctas, part_rows, D]
-  int sc_wide;                 // 1: four scales of neighbouring keys lie on 16 bytes
-  // With a shared prefix: parts are [2 ctas, split_rows], then a result of pre_rows
-  // or part_rows for each item that one CTA has whole.
+  int few;                     // 8-bit caches: 1: at most 32 rows, their keys shared by four lane groups
+  // Joined by items (a shared prefix, few): parts are [2 ctas, split_rows], then a
+  // result of pre_rows or part_rows (few: four times) for each item that one CTA has whole.
   int n_pre;                   // groups of the prefix's rows
   int pre_rows, split_rows;    // rows of such a group, of a split part
-  int2* item_meta;             // [items] (parts, slot of the first or -1: whole)
+  int2* item_meta;             // [items] (parts, slot of the first or -1: whole); null: not by items
   int* p0;                     // [1] tiles of the prefix
 };
 // Of each CTA: the item whose first inner border is the CTA's beginning. Its

@@ -176,14 +176,14 @@ st_status plan_attn(const st_tensor* q, const st_kv_cache* cache, const st_cache
   P->bytes = 256;
   if (static_cast<int64_t>(p.B) * p.T * p.H == 0) return ST_OK;
   // The tensor-core kernel takes every 16-bit cache whose pages are whole TMA
-  // boxes (at least one 8-row swizzle atom); fp32 caches and other page sizes
-  // take the CUDA cores.
-  P->tensor = p.kv.dt != ST_F32 && p.kv.page % 8 == 0 && p.kv.n_pages > 0 && p.kv.max_pages > 0 && p.q.dt != ST_F32;
+  // boxes (at least one 8-row swizzle atom), and caches of 8 bits; fp32 rows and
+  // other page sizes take the CUDA cores.
+  P->tensor = p.kv.dt != ST_F32 && (held(p.kv) || p.kv.page % 8 == 0) && p.kv.n_pages > 0 && p.kv.max_pages > 0 && p.q.dt != ST_F32;
   if (P->tensor) {
     TcAttnParams& t = P->tc;
     P->nt = tc_tiles(p.T, p.group);
     t.box_shift = 3;
-    while ((1 << t.box_shift) < (held(p.kv) ? kTile / 2 : kTile) && p.kv.page % (2 << t.box_shift) == 0) ++t.box_shift;
+    while ((1 << t.box_shift) < kTile && p.kv.page % (2 << t.box_shift) == 0) ++t.box_shift;
     t.tpt = kTile / p.group;
     const int64_t tpg = static_cast<int64_t>(t.tpt) * P->nt;
     t.n_groups = static_cast<int>((p.T + tpg - 1) / tpg);
@@ -194,12 +194,14 @@ st_status plan_attn(const st_tensor* q, const st_kv_cache* cache, const st_cache
       cap_tiles = std::min(cap_tiles, (static_cast<int64_t>(p.sinks) + kTile - 1) / kTile +
                                           (static_cast<int64_t>(p.window) + std::min<int64_t>(p.T, p.parents ? p.T : tpg) + kTile - 1) / kTile + 1);
     int64_t items = static_cast<int64_t>(p.B) * p.kv.Hkv * t.n_groups;
+    t.few = held(p.kv) && t.part_rows <= 32;
+    t.split_rows = t.part_rows * (t.few ? 4 : 1);
     if (p.shared) {
       const int64_t tokens = static_cast<int64_t>(p.B) * p.T;
       if (tokens > (1ll << 30)) return fail(ST_ERR_SHAPE, "too many query rows");
       t.n_pre = static_cast<int>((tokens + tpg - 1) / tpg);
       t.pre_rows = static_cast<int>(std::min<int64_t>(tokens, tpg)) * p.group;
-      t.split_rows = std::max(t.pre_rows, t.part_rows);
+      t.split_rows = std::max(t.pre_rows, t.split_rows);
       items += static_cast<int64_t>(p.kv.Hkv) * t.n_pre;
     }
     if (items > (1ll << 40) || static_cast<int64_t>(p.B) * t.n_groups + t.n_pre > (1ll << 30)) return fail(ST_ERR_SHAPE, "too many query rows");
@@ -231,9 +233,9 @@ st_status plan_attn(const st_tensor* q, const st_kv_cache* cache, const st_cache
       return ST_OK;  // no workspace
     }
     t.ctas = static_cast<int>(items >= kSmCount ? kSmCount : std::min<int64_t>(kSmCount, items * cap_tiles));
-    if (p.shared) {
+    if (p.shared || t.few) {
       const int64_t own = items - static_cast<int64_t>(p.kv.Hkv) * t.n_pre;
-      const size_t rows = static_cast<size_t>(2) * t.ctas * t.split_rows + static_cast<size_t>(items - own) * t.pre_rows + static_cast<size_t>(own) * t.part_rows;
+      const size_t rows = static_cast<size_t>(2) * t.ctas * t.split_rows + static_cast<size_t>(items - own) * t.pre_rows + static_cast<size_t>(own) * t.part_rows * (t.few ? 4 : 1);
       size_t off = align256(rows * kD * sizeof(float));
       P->off_ml = off;
       off = align256(off + rows * sizeof(float2));
@@ -421,14 +423,11 @@ st_status st_cache_attn_opt(const st_tensor* q_rot, const st_kv_cache* cache, co
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     t.part_ml = reinterpret_cast<float2*>(ws + P.off_ml);
     t.meta = reinterpret_cast<JoinMeta*>(ws + P.off_meta);
-    t.item_meta = reinterpret_cast<int2*>(ws + P.off_meta);
+    t.item_meta = P.off_p0 > 0 ? reinterpret_cast<int2*>(ws + P.off_meta) : nullptr;  // by items
     t.p0 = reinterpret_cast<int*>(ws + P.off_p0);
-    const PagedKV& kv = p.kv;
-    t.sc_wide = ((reinterpret_cast<uintptr_t>(kv.ks) | reinterpret_cast<uintptr_t>(kv.vs)) & 15u) == 0 &&
-                (kv.ks_sp | kv.ks_sh | kv.vs_sp | kv.vs_sh) % 4 == 0;
     t.o_wide = (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0 && p.o_sb % 16 == 0 && p.o_ss % 16 == 0 && p.o_sh % 16 == 0;
-    if ((st = encode_rows_map(cache->k, &t.tmap_k, &t.k_r_first, 1 << t.box_shift)) != ST_OK) return st;
-    if ((st = encode_rows_map(cache->v, &t.tmap_v, &t.v_r_first, 1 << t.box_shift)) != ST_OK) return st;
+    if (!held(p.kv) && (st = encode_rows_map(cache->k, &t.tmap_k, &t.k_r_first, 1 << t.box_shift)) != ST_OK) return st;
+    if (!held(p.kv) && (st = encode_rows_map(cache->v, &t.tmap_v, &t.v_r_first, 1 << t.box_shift)) != ST_OK) return st;
     if ((st = cuda_check(launch_counted(ST_K_CACHE_ATTN, stream, [&] { return launch_cache_attn_tc(t, P.nt, p.q.dt == ST_F16, stream); }),
                          "cached attention launch")) != ST_OK)
       return st;
