@@ -43,12 +43,12 @@
 // zero; every group has sums and accumulators of its own, which are joined at the
 // end like parts of the keys.
 //
-// Roles (512 threads, KV: 640; one CTA per SM):
+// Roles (512 threads, KV: 576; one CTA per SM):
 //   warps 0-7   softmax, two groups of four warps; thread = query row = TMEM lane
 //   warps 8-11  Q rows of the next item into shared memory; KV: also K's conversion,
 //               and four more warps V's
 //   then        tcgen05.mma issue for slot 0 (one thread; TMEM allocation); TMA of K
-//               boxes, one lane per box; TMA of V boxes (KV: neither); tcgen05.mma
+//               boxes, one lane per box, and of V boxes (KV: neither); tcgen05.mma
 //               issue for slot 1
 // TMEM: S0 | S1 | O0 | O1, 128 fp32 columns each; P (16-bit) overwrites the
 // first half of its S and feeds PV from TMEM. The stream of score tiles
@@ -71,13 +71,13 @@ namespace {
 constexpr int kSoftWarps = 8, kWarpQ0 = 8, kQWarps = 4;
 template <bool HELD>
 struct Roles {
-  static constexpr int kWarpMma = HELD ? 16 : 12, kWarpK = kWarpMma + 1, kWarpV = kWarpMma + 2;  // kWarpMma + 3: the second slot's MMAs
-  static constexpr int kWarps = kWarpMma + 4, kThreads = kWarps * 32;
-  // Registers per thread. The 16-bit form's softmax threads hold a row of 128 scores:
-  // 256 * 184 + 256 * 72 = 512 * 128. KV reads the scores from TMEM twice instead and
-  // holds 64: 256 * 128 + 384 * 72 <= 640 * 96.
-  static constexpr int kRegsSoft = HELD ? 128 : 184, kRegsRest = 72;
+  static constexpr int kWarpMma = HELD ? 16 : 12, kWarpK = HELD ? 99 : 13, kWarpV = HELD ? 99 : 14;  // the last warp: the second slot's MMAs
+  static constexpr int kWarps = HELD ? 18 : 16, kThreads = kWarps * 32;
 };
+// Registers per thread of the 16-bit form: its softmax threads hold a row of 128
+// scores. 256 * 184 + 256 * 72 = 512 * 128. KV reads the scores from TMEM twice
+// instead and has 112 everywhere.
+constexpr int kRegsSoft = 184, kRegsRest = 72;
 constexpr float kRescale = 8.0f;  // O is rescaled when the running maximum grows by more than this (base 2)
 // How far the reference stays below the running maximum (base 2). fp16 weights
 // end at 2^-25 of 1, and a long row's many small ones would leave PV but stay in
@@ -85,6 +85,8 @@ constexpr float kRescale = 8.0f;  // O is rescaled when the running maximum grow
 // they end 2^-32 below it. bf16 has fp32's range.
 template <bool F16>
 constexpr float kLift = F16 ? 7.0f : 0.0f;
+
+constexpr int kPlaceBytes = 80;
 
 template <int NT, bool HELD = false>
 struct Lay {  // shared memory, offsets from a 1024-byte aligned base
@@ -100,8 +102,8 @@ struct Lay {  // shared memory, offsets from a 1024-byte aligned base
   static constexpr uint32_t q = 0, k = NT * kTileBytes, v = k + KS * kTileBytes, raw = v + VS * kTileBytes, bar = raw + (RK + RV) * kRawBytes;
   static constexpr uint32_t ml = bar + 512;          // [2][128] (reference, sum), NT = 1
   static constexpr uint32_t sc = ml + (NT == 1 ? 2 * 128 * 8 : 0);  // [SS] Scales
-  static constexpr uint32_t walk = sc + SS * 1040;   // HELD: [2][warps] places of the roles' walks
-  static constexpr uint32_t bytes = walk + (HELD ? 2 * Roles<true>::kWarps * 24 : 0);
+  static constexpr uint32_t walk = sc + SS * 1040;   // HELD: places of the roles' walks
+  static constexpr uint32_t bytes = walk + (HELD ? (2 * Roles<true>::kWarps - kSoftWarps) * kPlaceBytes : 0);
   enum { QFull = 0, QEmpty, KFull, KEmpty = KFull + KS, VFull = KEmpty + KS, VEmpty = VFull + VS, SFull = VEmpty + VS,
          PFull = SFull + 2, OFull = PFull + 2, MlFull, ORead = MlFull + 2, Drain = ORead + 2, ScFull = Drain + 2, ScEmpty = ScFull + SS, Num = ScEmpty + SS };
 };
@@ -234,30 +236,41 @@ struct Walk {
     return true;
   }
   __device__ __forceinline__ bool whole() const { return kt0 == 0 && kt1 == it.n; }
-  // HELD: what the walk goes on from lies in shared memory between pieces, so that
-  // the roles' 72 registers hold the present piece only (with two walks in
-  // registers they spilled in their loops: 64 tokens after up to 8191 keys in
-  // e4m3 395 us).
+  // HELD: what the walk goes on from lies in shared memory between pieces, and the
+  // step is a function of its own (below).
   struct Place {
     int h, b, m, off;
     long long left;
+    int p0, ph, pb, pm, kt0, kt1;
+    Item it;
   };
-  __device__ __forceinline__ void save(Place* at) const { *at = {h, b, m, off, left}; }
-  template <bool ONE, bool WARP>
-  __device__ __forceinline__ bool next_from(const TcAttnParams& p, int nt, Place* at) {
-    const Place x = *at;
-    h = x.h;
-    b = x.b;
-    m = x.m;
-    off = x.off;
-    left = x.left;
-    const bool more = next<ONE>(p, nt);
-    if (WARP) __syncwarp();  // every lane has read
-    if (!WARP || (threadIdx.x & 31) == 0) save(at);
-    if (WARP) __syncwarp();
-    return more;
+  __device__ __forceinline__ void save(Place* at) const { *at = {h, b, m, off, left, p0, 0, 0, 0, 0, 0, {}}; }
+  __device__ __forceinline__ void take(const Place* at) {
+    ph = at->ph;
+    pb = at->pb;
+    pm = at->pm;
+    kt0 = at->kt0;
+    kt1 = at->kt1;
+    it = at->it;
   }
 };
+// The next piece of the walk at `at`, by one thread. Inlined into every role, with
+// the rest unrolled, it made a kernel of 197 KB, which the instruction cache did
+// not hold: every role was held up by its own instructions (64 tokens after up to
+// 8191 keys in e4m3 253 us).
+template <bool EXT>
+__device__ __noinline__ bool next_piece_of(const TcAttnParams& p, int nt, typename Walk<EXT>::Place* at) {
+  Walk<EXT> w;
+  w.h = at->h;
+  w.b = at->b;
+  w.m = at->m;
+  w.off = at->off;
+  w.left = at->left;
+  w.p0 = at->p0;
+  if (!w.template next<false>(p, nt)) return false;
+  *at = {w.h, w.b, w.m, w.off, w.left, w.p0, w.ph, w.pb, w.pm, w.kt0, w.kt1, w.it};
+  return true;
+}
 
 // The deal: CTA x has the tiles [first(x), first(x + 1)) of the call's, shares
 // that differ by one at most. 32-bit division where the numbers allow it.
@@ -573,32 +586,16 @@ __device__ __forceinline__ float2 weigh_chunk(uint32_t tP, const uint32_t (&x)[3
   tmem_st16(tP, pw);
   return ls;
 }
-__device__ __forceinline__ void softmax_held(uint32_t tS, uint32_t tO, float sc, const Scales& scales, bool mask, const uint32_t (&mb)[4], bool few,
+__device__ __forceinline__ void softmax_held(uint32_t tS, uint32_t tO, float sc, const Scales& scales, bool mask, uint32_t mb0, uint32_t mb1, uint32_t mb2, uint32_t mb3, bool few,
                                              int quarter, bool first, float& m_run, float& l_run) {
-  uint32_t x[32], z[32];
-  float top;
-  if (few) {  // the warp's chunk stays in registers
-    tmem_ld32(tS + 32 * quarter, x);
-    scale_chunk(x, scales.k + 32 * quarter, mask, mb[0]);
-    top = max_chunk(x);
-  } else {
-    tmem_ld32_issue(tS, x);
-    tmem_ld32_issue(tS + 32, z);
-    tmem_ld_wait32(x);
-    scale_chunk(x, scales.k, mask, mb[0]);
-    top = max_chunk(x);
-    tmem_ld32_issue(tS + 64, x);
-    tmem_ld_wait32(z);
-    scale_chunk(z, scales.k + 32, mask, mb[1]);
-    top = fmaxf(top, max_chunk(z));
-    tmem_ld32_issue(tS + 96, z);
-    tmem_ld_wait32(x);
-    scale_chunk(x, scales.k + 64, mask, mb[2]);
+  uint32_t x[32];
+  const int c0 = few ? quarter : 0, c1 = few ? quarter + 1 : 4;
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int i = c0; i < c1; ++i) {  // rolled, here and below, for the instruction cache
+    tmem_ld32(tS + 32 * i, x);
+    scale_chunk(x, scales.k + 32 * i, mask, i & 2 ? (i & 1 ? mb3 : mb2) : (i & 1 ? mb1 : mb0));
     top = fmaxf(top, max_chunk(x));
-    tmem_ld32_issue(tS, x);  // for the weights
-    tmem_ld_wait32(z);
-    scale_chunk(z, scales.k + 96, mask, mb[3]);
-    top = fmaxf(top, max_chunk(z));
   }
   const float4 vt = *reinterpret_cast<const float4*>(scales.top);
   const float mt = fmaf(top, sc, fmaxf(fmaxf(vt.x, vt.y), fmaxf(vt.z, vt.w)) - kLift<true>);
@@ -609,27 +606,18 @@ __device__ __forceinline__ void softmax_held(uint32_t tS, uint32_t tO, float sc,
   }
   const float m_use = m_run == -INFINITY ? 0.f : m_run;
   float2 ls = make_float2(0.f, 0.f);
+#pragma unroll 1
+  for (int i = c0; i < c1; ++i) {
+    if (!few) {  // else they are still here
+      tmem_ld32(tS + 32 * i, x);
+      scale_chunk(x, scales.k + 32 * i, mask, i & 2 ? (i & 1 ? mb3 : mb2) : (i & 1 ? mb1 : mb0));
+    }
+    ls = weigh_chunk(tS + 16 * i, x, scales.v + 32 * i, sc, m_use, ls);
+  }
   if (few) {
-    ls = weigh_chunk(tS + 16 * quarter, x, scales.v + 32 * quarter, sc, m_use, ls);
     const uint32_t none[16] = {};
-#pragma unroll
+#pragma unroll 1
     for (int i = 1; i < 4; ++i) tmem_st16(tS + 16 * ((quarter + i) & 3), none);
-  } else {
-    tmem_ld_wait32(x);
-    scale_chunk(x, scales.k, mask, mb[0]);
-    tmem_ld32_issue(tS + 32, z);
-    ls = weigh_chunk(tS, x, scales.v, sc, m_use, ls);
-    tmem_ld_wait32(z);
-    tmem_ld32_issue(tS + 64, x);
-    scale_chunk(z, scales.k + 32, mask, mb[1]);
-    ls = weigh_chunk(tS + 16, z, scales.v + 32, sc, m_use, ls);
-    tmem_ld_wait32(x);
-    tmem_ld32_issue(tS + 96, z);
-    scale_chunk(x, scales.k + 64, mask, mb[2]);
-    ls = weigh_chunk(tS + 32, x, scales.v + 64, sc, m_use, ls);
-    tmem_ld_wait32(z);
-    scale_chunk(z, scales.k + 96, mask, mb[3]);
-    ls = weigh_chunk(tS + 48, z, scales.v + 96, sc, m_use, ls);
   }
   l_run = l_run * corr + (ls.x + ls.y);
   if (!first && __any_sync(0xffffffffu, corr != 1.f)) {  // warp-uniform: tcgen05.ld/st are collective
@@ -854,7 +842,6 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
   constexpr bool HELD = KV != 0, OP16 = F16 || HELD;  // fp16 operands
   using L = Lay<NT, HELD>;
   constexpr int kWarpMma = Roles<HELD>::kWarpMma, kWarpK = Roles<HELD>::kWarpK, kWarpV = Roles<HELD>::kWarpV, kTcWarps = Roles<HELD>::kWarps;
-  constexpr int kRegsSoft = Roles<HELD>::kRegsSoft, kRegsRest = Roles<HELD>::kRegsRest;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw;
   const CacheAttnParams& c = P.c;
@@ -942,19 +929,35 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
   }
   const bool by_items = EXT && !CL && P.item_meta;  // every result is joined
   using Place = typename Walk<EXT>::Place;
-  static_assert(sizeof(Place) == 24, "layout");
-  Place* place = reinterpret_cast<Place*>(sm + L::walk) + warp;  // HELD: this warp's, and a second one kTcWarps further on
+  static_assert(sizeof(Place) == kPlaceBytes, "layout");
+  // HELD: this warp's place, and behind all of them a second one of each warp that
+  // is no softmax warp
+  Place* place = reinterpret_cast<Place*>(sm + L::walk) + warp;
+  constexpr int kSecond = kTcWarps - kSoftWarps;
   if constexpr (HELD && !CL) {
     if (lane_id == 0) {
       wk.save(place);
-      wk.save(place + kTcWarps);
+      if (warp >= kSoftWarps) wk.save(place + kSecond);
     }
     __syncwarp();
   }
   // the next piece of walk `w` (second: the warp's other walk)
   auto next_piece = [&](Walk<EXT>& w, auto warp_wide, bool second) -> bool {
-    if constexpr (HELD && !CL) return w.template next_from<CL, decltype(warp_wide)::value>(P, NT, place + (second ? kTcWarps : 0));
-    else return w.template next<CL>(P, NT);
+    if constexpr (HELD && !CL) {
+      Place* at = place + (second ? kSecond : 0);
+      bool more = false;
+      if constexpr (decltype(warp_wide)::value) {
+        __syncwarp();  // every lane has what it wants of the last piece
+        if (lane_id == 0) more = next_piece_of<EXT>(P, NT, at);
+        more = __shfl_sync(0xffffffffu, more, 0);
+      } else {
+        more = next_piece_of<EXT>(P, NT, at);
+      }
+      if (more) w.take(at);
+      return more;
+    } else {
+      return w.template next<CL>(P, NT);
+    }
   };
   constexpr std::true_type all_lanes;
   constexpr std::false_type one_lane;
@@ -964,7 +967,7 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
 
   if (warp < kSoftWarps) {
     // -------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+    if constexpr (!HELD) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
     // padding rows (a cache without room for keys is not this kernel's)
     if (c.counts) {
       for (int b = CL ? blockIdx.y * gridDim.x + blockIdx.x : blockIdx.x; b < c.B; b += CL ? gridDim.x * gridDim.y : gridDim.x) {
@@ -1058,18 +1061,18 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
           if constexpr (EXT) all = all && (c.window == 0 || j0 >= low_last || j0 + kTile <= c.sinks);
           if (all) {
             const uint32_t mb[4] = {~0u, ~0u, ~0u, ~0u};
-            if constexpr (HELD) softmax_held(tS, tO, row_sc, scales, false, mb, few, warp & 3, first, m_run, l_run);
+            if constexpr (HELD) softmax_held(tS, tO, row_sc, scales, false, 0u, 0u, 0u, 0u, few, warp & 3, first, m_run, l_run);
             else softmax_tile<F16, false>(tS, tO, sc, mb, first, m_run, l_run);
           } else {
             uint32_t mb[4] = {};
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              if (HELD && few && w > 0) break;  // mb[0]: the warp's own quarter
-              const int j = j0 + 32 * (HELD && few ? warp & 3 : w);
+              if (HELD && few && w != (warp & 3)) continue;  // the warp's own quarter only
+              const int j = j0 + 32 * w;
               mb[w] = valid ? key_bits<TREE>(j, wk.it, t, anc) : 0u;
               if (EXT && c.window > 0) mb[w] &= window_bits<TREE>(j, low, c.sinks, wk.it.prefix);
             }
-            if constexpr (HELD) softmax_held(tS, tO, row_sc, scales, true, mb, few, warp & 3, first, m_run, l_run);
+            if constexpr (HELD) softmax_held(tS, tO, row_sc, scales, true, mb[0], mb[1], mb[2], mb[3], few, warp & 3, first, m_run, l_run);
             else softmax_tile<F16, true>(tS, tO, sc, mb, first, m_run, l_run);
           }
         }
@@ -1191,7 +1194,7 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
     if (CL && n_piece == 0 && (NT == 2 || slot == 0)) part_ml[(NT == 2 ? slot * 128 : 0) + r] = make_float2(-INFINITY, 0.f);
   } else if (warp < kWarpMma) {
     // ---------------------------------------------------------------- Q rows
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if constexpr (!HELD) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     const int qt = tid - kWarpQ0 * 32;
     int n_piece = 0;
     if constexpr (HELD) {
@@ -1206,6 +1209,12 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
       static_assert(L::KS == L::VS, "one count");
       uint8_t* raw = sm + L::raw + (is_v ? L::RK : 0) * L::kRawBytes + r0 * kD + 16 * cg;
       const int n_raw = is_v ? L::RV : L::RK;
+      // places in 32 bits: of rows in units of 16 bytes, of scales in numbers (the
+      // host has seen that they fit)
+      const HeldAt at = is_v ? P.held_v : P.held_k;
+      const uint8_t* base = static_cast<const uint8_t*>(is_v ? kv.v : kv.k) + 16 * cg;
+      const float* sc_base = is_v ? kv.vs : kv.ks;
+      constexpr uint32_t kNowhere = ~0u;
       // ---- the stream of fetches, up to n_raw stages ahead of the conversion. A
       // lane looks up the place of one of its warp's 32 rows of a tile, a tile ahead
       // of the fetch, and has that row's scale.
@@ -1218,9 +1227,9 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
         l_in = j < wl.it.keys && (!EXT || j >= wl.it.low || j < c.sinks);  // (keys lie within the table)
         l_h = wl.ph;
         if (l_in) {
-          const int at = kv.page_shift >= 0 ? j >> kv.page_shift : j / kv.page;
-          l_row = j - at * kv.page;
-          l_pg = ld_now(kv.pages + (EXT && wl.pb < 0 ? pre_b : wl.pb) * kv.p_sb + at);
+          const int page = kv.page_shift >= 0 ? j >> kv.page_shift : j / kv.page;
+          l_row = j - page * kv.page;
+          l_pg = ld_now(kv.pages + (EXT && wl.pb < 0 ? pre_b : wl.pb) * kv.p_sb + page);
         }
         if (++lt == wl.kt1) {
           l_have = next_piece(wl, all_lanes, true);
@@ -1231,34 +1240,34 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
       if (there) look();
       int i_tile = 0, i_part = 0, i_slot = 0;
       bool i_have = false;
-      int64_t off = -1;  // of the lane's row, < 0: no row
+      uint32_t off = kNowhere;  // of the lane's row
       auto fetch = [&]() -> bool {
         if (i_part == 0) {
           i_have = there;
           if (there) {
-            off = -1;
-            const float* sc_at = nullptr;
-            if (l_in && static_cast<unsigned>(l_pg) >= static_cast<unsigned>(kv.n_pages)) atomicOr(c.status, kStatusIndex);  // reads as zeros
-            else if (l_in) {
-              off = is_v ? l_pg * kv.v_sp + l_row * kv.v_sr + l_h * kv.v_sh : l_pg * kv.k_sp + l_row * kv.k_sr + l_h * kv.k_sh;
-              sc_at = is_v ? kv.vs + l_pg * kv.vs_sp + l_h * kv.vs_sh + l_row : kv.ks + l_pg * kv.ks_sp + l_h * kv.ks_sh + l_row;
+            off = kNowhere;
+            uint32_t sc_at = 0;
+            if (l_in && static_cast<unsigned>(l_pg) >= static_cast<unsigned>(kv.n_pages)) {
+              atomicOr(c.status, kStatusIndex);  // reads as zeros
+            } else if (l_in) {
+              off = l_pg * at.sp + l_row * at.sr + l_h * at.sh;
+              sc_at = l_pg * at.sc_sp + l_h * at.sc_sh + l_row;
             }
             there = l_have;
             if (there) look();
             const int st = i_tile % L::SS;
             if (i_tile >= L::SS && !wait_bar_warp(&bars[L::ScEmpty + st], ((i_tile / L::SS) - 1) & 1, abort_flag, budget)) return false;
             Scales& s = reinterpret_cast<Scales*>(sm + L::sc)[st];
-            cp_async4(is_v ? &s.v[my_row] : &s.k[my_row], sc_at ? sc_at : kv.ks, sc_at != nullptr);
+            cp_async4(is_v ? &s.v[my_row] : &s.k[my_row], sc_base + sc_at, off != kNowhere);
             ++i_tile;
           }
         }
         if (i_have) {
           uint8_t* dst = raw + i_slot * L::kRawBytes;
-          const uint8_t* base = static_cast<const uint8_t*>(is_v ? kv.v : kv.k);
 #pragma unroll
           for (int u = 0; u < kU; ++u) {
-            const long long o = __shfl_sync(0xffffffffu, static_cast<long long>(off), (lane_id >> 3) + 4 * (i_part * kU + u));
-            cp_async16(dst + u * 16 * kD, base + (o < 0 ? 0 : o + 16 * cg), o >= 0);
+            const uint32_t o = __shfl_sync(0xffffffffu, off, (lane_id >> 3) + 4 * (i_part * kU + u));
+            cp_async16(dst + u * 16 * kD, base + (o == kNowhere ? 0u : o) * static_cast<uint64_t>(16), o != kNowhere);
           }
           if (++i_part == kParts) i_part = 0;
           if (++i_slot == n_raw) i_slot = 0;
@@ -1304,14 +1313,15 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
           const uint8_t* src = raw + slot * L::kRawBytes;
 #pragma unroll
           for (int u = 0; u < kU; ++u) {
-            const uint4 x = *reinterpret_cast<const uint4*>(src + u * 16 * kD);
+            uint4 x = *reinterpret_cast<const uint4*>(src + u * 16 * kD);
+            if (odd) x = make_uint4(x.z, x.w, x.x, x.y);
             uint4 a, b;
             held_f16<KV>(x.x, a.x, a.y);
             held_f16<KV>(x.y, a.z, a.w);
             held_f16<KV>(x.z, b.x, b.y);
             held_f16<KV>(x.w, b.z, b.w);
-            *reinterpret_cast<uint4*>(dst + at0 + (part * kU + u) * 16 * 128) = odd ? b : a;
-            *reinterpret_cast<uint4*>(dst + at1 + (part * kU + u) * 16 * 128) = odd ? a : b;
+            *reinterpret_cast<uint4*>(dst + at0 + (part * kU + u) * 16 * 128) = a;
+            *reinterpret_cast<uint4*>(dst + at1 + (part * kU + u) * 16 * 128) = b;
           }
           if (!(ok = fetch())) break;  // into the stage that has just been read, by this thread
           if (++slot == n_raw) slot = 0;
@@ -1335,10 +1345,8 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-    if (HELD && (warp == kWarpK || warp == kWarpV)) {
-      // nothing: registers are split by groups of four warps
-    } else if (warp == kWarpK || warp == kWarpV) {
+    if constexpr (!HELD) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (!HELD && (warp == kWarpK || warp == kWarpV)) {
       // ------------------------------------------------------- TMA of K and V
       const bool is_k = warp == kWarpK;
       const int stages = is_k ? L::KS : L::VS;

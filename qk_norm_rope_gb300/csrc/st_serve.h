@@ -176,6 +176,11 @@ cudaError_t launch_cache_attn_simt_join(const CacheAttnParams& p, cudaStream_t s
 // one K/V head; NT = 2 where a sequence has more than 128 rows a head), an
 // item a (K/V head, sequence, group); its key tiles are dealt out to the CTAs
 // in one continuous range each.
+// Strides of pages, rows and heads of K or V in units of 16 bytes, and of the
+// scales' pages and heads in numbers.
+struct HeldAt {
+  uint32_t sp, sr, sh, sc_sp, sc_sh;
+};
 struct TcAttnParams {
   CacheAttnParams c;
   CUtensorMap tmap_k, tmap_v;  // cache pages, boxes of 64 columns x box rows
@@ -190,6 +195,7 @@ struct TcAttnParams {
   int cluster_shift;
   struct JoinMeta* meta;       // [ctas], workspace
   float2* part_ml;             // [2 ctas, part_rows] (reference, sum); c.part: [2 ctas, part_rows, D]
+  HeldAt held_k, held_v;       // 8-bit caches
   int few;                     // 8-bit caches: 1: at most 32 rows, their keys shared by four lane groups
   // Joined by items (a shared prefix, few): parts are [2 ctas, split_rows], then a
   // result of pre_rows or part_rows (few: four times) for each item that one CTA has whole.

@@ -13,7 +13,7 @@ namespace {
 using namespace st;
 
 constexpr unsigned kRowTypes = bit(ST_BF16) | bit(ST_F16) | bit(ST_F32), kHeldTypes = bit(ST_E4M3) | bit(ST_I8);
-static_assert(ST_E4M3 == kDtE4M3 && ST_I8 == kDtI8, "type codes");
+static_assert(static_cast<int>(ST_E4M3) == kDtE4M3 && static_cast<int>(ST_I8) == kDtI8, "type codes");
 constexpr int kSmCount = 152;
 
 // A contiguous int32 or fp32 vector [B].
@@ -146,6 +146,18 @@ struct AttnPlan {
   size_t bytes = 0, off_ml = 0, off_meta = 0, off_p0 = 0;
 };
 
+// Strides for 32-bit places of rows and scales; false where these do not fit.
+bool held_at(const PagedKV& kv, TcAttnParams* t) {
+  const int64_t n = kv.n_pages - 1, r = kv.page - 1, h = kv.Hkv - 1, most = (1ll << 32) - 2;
+  if ((n * kv.k_sp + r * kv.k_sr + h * kv.k_sh) / 16 > most || (n * kv.v_sp + r * kv.v_sr + h * kv.v_sh) / 16 > most ||
+      n * kv.ks_sp + h * kv.ks_sh + r > most || n * kv.vs_sp + h * kv.vs_sh + r > most)
+    return false;
+  auto u = [](int64_t x) { return static_cast<uint32_t>(x); };
+  t->held_k = {u(kv.k_sp / 16), u(kv.k_sr / 16), u(kv.k_sh / 16), u(kv.ks_sp), u(kv.ks_sh)};
+  t->held_v = {u(kv.v_sp / 16), u(kv.v_sr / 16), u(kv.v_sh / 16), u(kv.vs_sp), u(kv.vs_sh)};
+  return true;
+}
+
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 st_status plan_attn(const st_tensor* q, const st_kv_cache* cache, const st_cache_attn_opts* opts, const st_tensor* parents, AttnPlan* P) {
@@ -176,9 +188,10 @@ st_status plan_attn(const st_tensor* q, const st_kv_cache* cache, const st_cache
   P->bytes = 256;
   if (static_cast<int64_t>(p.B) * p.T * p.H == 0) return ST_OK;
   // The tensor-core kernel takes every 16-bit cache whose pages are whole TMA
-  // boxes (at least one 8-row swizzle atom), and caches of 8 bits; fp32 rows and
-  // other page sizes take the CUDA cores.
-  P->tensor = p.kv.dt != ST_F32 && (held(p.kv) || p.kv.page % 8 == 0) && p.kv.n_pages > 0 && p.kv.max_pages > 0 && p.q.dt != ST_F32;
+  // boxes (at least one 8-row swizzle atom), and caches of 8 bits whose K and V
+  // span at most 64 GB each; fp32 rows and what is left take the CUDA cores.
+  P->tensor = p.kv.dt != ST_F32 && (held(p.kv) ? held_at(p.kv, &P->tc) : p.kv.page % 8 == 0) && p.kv.n_pages > 0 && p.kv.max_pages > 0 &&
+              p.q.dt != ST_F32;
   if (P->tensor) {
     TcAttnParams& t = P->tc;
     P->nt = tc_tiles(p.T, p.group);
