@@ -70,20 +70,37 @@ __global__ void __launch_bounds__(256, U > 4 ? 2 : 6) join_kernel(const __grid_c
 
 // By items (a shared prefix, FEW): a row's results over the prefix's tiles and over
 // its own keys come together, each whole or in the parts that CTAs left of it, these
-// in four copies with FEW. A warp takes a row, a lane four columns; four parts are in
-// flight.
+// in four copies with FEW. W warps take a row, a lane four columns; four parts are in
+// flight for each, and the first warp brings the warps' results together. (One token
+// of 8 K/V heads after 30000 keys in 8 bits has 76 parts a row: 18 us of one warp.)
+template <int W>
 __global__ void __launch_bounds__(256) join_items_kernel(const __grid_constant__ TcAttnParams P, int nt) {
+  __shared__ float4 so[W][kD / 4];
+  __shared__ float2 sml[W];
   grid_dependency_wait();
   const CacheAttnParams& c = P.c;
-  const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (row >= static_cast<int64_t>(c.B) * c.T * c.H) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % W;
+  const int64_t row = (static_cast<int64_t>(blockIdx.x) * 8 + warp) / W;
+  if (row >= static_cast<int64_t>(c.B) * c.T * c.H) return;  // with W = 8 these hold for the whole block
   const int64_t tok = row / c.H;  // at most 2^30
   const int hq = static_cast<int>(row - tok * c.H), b = static_cast<int>(tok / c.T), t = static_cast<int>(tok - static_cast<int64_t>(b) * c.T);
   if (t >= row_count(c.counts, b, c.T)) return;  // the attention kernel wrote it
   const int h = hq / c.group, g = hq - h * c.group, tpg = P.tpt * nt, p0 = c.shared ? ld_now(P.p0) : 0;
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto merge = [&](const float2 (&x)[4], const float4 (&y)[4]) {
+    const float top = fmaxf(fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x)), m), use = top == -INFINITY ? 0.f : top;
+    const float f0 = ex2(m - use);
+    m = top;
+    l *= f0;
+    o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float f = ex2(x[u].x - use);
+      l = fmaf(f, x[u].y, l);
+      o = make_float4(fmaf(f, y[u].x, o.x), fmaf(f, y[u].y, o.y), fmaf(f, y[u].z, o.z), fmaf(f, y[u].w, o.w));
+    }
+  };
 #pragma unroll 1
   for (int which = p0 > 0 ? 0 : 1; which < 2; ++which) {
     const int ib = which == 0 ? -1 : b, at = which == 0 ? static_cast<int>(tok) : t, im = at / tpg;
@@ -93,28 +110,34 @@ __global__ void __launch_bounds__(256) join_items_kernel(const __grid_constant__
     const int2 meta = P.item_meta[item_index(P, h, ib, im)];
     const int64_t first = meta.y < 0 ? whole_part(P, h, ib, im) : static_cast<int64_t>(meta.y) * P.split_rows;
     const int64_t cta = meta.y >> 1;
-    for (int i0 = 0; i0 < meta.x * copies; i0 += 4) {
+    const int n = meta.x * copies;
+    for (int i0 = 4 * part; i0 < n; i0 += 4 * W) {
       float2 x[4];
       float4 y[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const int v = min(i0 + u, meta.x * copies - 1), i = copies == 4 ? v >> 2 : v, copy = copies == 4 ? v & 3 : 0;
+        const int v = min(i0 + u, n - 1), i = copies == 4 ? v >> 2 : v, copy = copies == 4 ? v & 3 : 0;
         const int64_t at_row = (i == 0 ? first : 2 * (cta + i) * P.split_rows) + copy * P.part_rows + r;
         x[u] = P.part_ml[at_row];
         y[u] = reinterpret_cast<const float4*>(c.part + at_row * kD)[lane];
-        if (i0 + u >= meta.x * copies) x[u] = make_float2(-INFINITY, 0.f);
+        if (i0 + u >= n) x[u] = make_float2(-INFINITY, 0.f);
       }
-      const float top = fmaxf(fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x)), m), use = top == -INFINITY ? 0.f : top;
-      const float f0 = ex2(m - use);
-      m = top;
-      l *= f0;
-      o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
+      merge(x, y);
+    }
+  }
+  if constexpr (W > 1) {
+    so[warp][lane] = o;
+    if (lane == 0) sml[warp] = make_float2(m, l);
+    __syncthreads();
+    if (warp > 0) return;
+    m = -INFINITY;
+    l = 0.f;
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float f = ex2(x[u].x - use);
-        l = fmaf(f, x[u].y, l);
-        o = make_float4(fmaf(f, y[u].x, o.x), fmaf(f, y[u].y, o.y), fmaf(f, y[u].z, o.z), fmaf(f, y[u].w, o.w));
-      }
+    for (int w = 0; w < W; w += 4) {
+      const float2 x[4] = {sml[w], sml[w + 1], sml[w + 2], sml[w + 3]};
+      const float4 y[4] = {so[w][lane], so[w + 1][lane], so[w + 2][lane], so[w + 3][lane]};
+      merge(x, y);
     }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -135,7 +158,11 @@ cudaError_t launch_cache_attn_tc(const TcAttnParams& p, int nt, bool f16, cudaSt
 cudaError_t launch_cache_attn_join(const TcAttnParams& p, int nt, cudaStream_t stream) {
   if (p.item_meta) {
     const int64_t rows = static_cast<int64_t>(p.c.B) * p.c.T * p.c.H;
-    return launch_chained(join_items_kernel, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, stream, p, nt);
+    // few items, whose parts are then many, and not many rows: eight warps a row
+    const int64_t items = (static_cast<int64_t>(p.c.B) * p.n_groups + p.n_pre) * p.c.kv.Hkv;
+    const int warps = items * 4 <= p.ctas * 3 && rows <= 8192 ? 8 : 1;
+    return launch_chained(warps == 8 ? join_items_kernel<8> : join_items_kernel<1>, dim3(static_cast<unsigned>((rows * warps + 7) / 8)), dim3(256),
+                          0, stream, p, nt);
   }
   // few rows, or few items, whose parts are then many
   const bool deep = p.part_rows <= 32 || static_cast<int64_t>(p.c.B) * p.c.kv.Hkv * p.n_groups * 4 <= p.ctas;

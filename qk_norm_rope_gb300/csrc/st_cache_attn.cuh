@@ -94,7 +94,7 @@ struct Lay {  // shared memory, offsets from a 1024-byte aligned base
   // thread waits for every phase of the stages that it uses, and a wait on
   // parity says nothing where phases went by unseen.
   static constexpr int KS = NT == 1 || HELD ? 2 : 3, VS = NT == 1 && !HELD ? 4 : 2;
-  static constexpr int SS = HELD ? 6 : 0;                   // stages of scales (NT = 1: of one slot, as above)
+  static constexpr int SS = HELD ? 4 : 0;                   // stages of scales (NT = 1: of one slot, as above)
   // stages of bytes, of K and of V, and their keys: 56 KB in flight where reading bounds
   static constexpr int RK = !HELD ? 0 : (NT == 1 ? 4 : 3), RV = !HELD ? 0 : 3, kRawRows = NT == 1 ? 64 : 32;
   static constexpr uint32_t kRawBytes = kRawRows * kD;
@@ -1202,12 +1202,16 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
       const bool is_v = warp >= kWarpQ0 + kQWarps;
       constexpr int kParts = kTile / L::kRawRows, kU = L::kRawRows / 16;  // stages of a tile, a thread's pieces of a stage
       const PagedKV& kv = c.kv;
-      const int gw = warp & 3, cg = lane_id & 7, r0 = 4 * gw + (lane_id >> 3);  // 16 columns of rows r0 + 16 u
+      const int gw = warp & 3;
+      // A lane has 16 columns (cg) of the rows r0 + 16 u. Eight lanes write two
+      // rows' 64 columns of one half of the operand tile, whose swizzles differ: no
+      // bank twice. (In the ring a thread's pieces lie anywhere: it alone reads them.)
+      const int half = (lane_id >> 3) & 1, cg = 4 * half + (lane_id & 3), r_in = ((lane_id >> 4) << 1) | ((lane_id >> 2) & 1), r0 = 4 * gw + r_in;
       uint64_t* full = &bars[is_v ? L::VFull : L::KFull];
       uint64_t* empty = &bars[is_v ? L::VEmpty : L::KEmpty];
       uint8_t* tiles = sm + (is_v ? L::v : L::k);
       static_assert(L::KS == L::VS, "one count");
-      uint8_t* raw = sm + L::raw + (is_v ? L::RK : 0) * L::kRawBytes + r0 * kD + 16 * cg;
+      uint8_t* raw = sm + L::raw + (is_v ? L::RK : 0) * L::kRawBytes + (gw * 32 + lane_id) * 16;  // + 2048 u
       const int n_raw = is_v ? L::RV : L::RK;
       // places in 32 bits: of rows in units of 16 bytes, of scales in numbers (the
       // host has seen that they fit)
@@ -1264,11 +1268,11 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
         }
         if (i_have) {
           uint8_t* dst = raw + i_slot * L::kRawBytes;
+          uint32_t o[kU];
 #pragma unroll
-          for (int u = 0; u < kU; ++u) {
-            const uint32_t o = __shfl_sync(0xffffffffu, off, (lane_id >> 3) + 4 * (i_part * kU + u));
-            cp_async16(dst + u * 16 * kD, base + (o == kNowhere ? 0u : o) * static_cast<uint64_t>(16), o != kNowhere);
-          }
+          for (int u = 0; u < kU; ++u) o[u] = __shfl_sync(0xffffffffu, off, r_in + 4 * (i_part * kU + u));
+#pragma unroll
+          for (int u = 0; u < kU; ++u) cp_async16(dst + u * 2048, base + (o[u] == kNowhere ? 0u : o[u]) * static_cast<uint64_t>(16), o[u] != kNowhere);
           if (++i_part == kParts) i_part = 0;
           if (++i_slot == n_raw) i_slot = 0;
         }
@@ -1277,11 +1281,9 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
       };
 #pragma unroll 1
       for (int i = 0; i < n_raw; ++i) fetch();  // fewer tiles than SS: no wait
-      // ---- the conversion. Columns 16 cg .. + 16 are chunks 2 cg and 2 cg + 1; the
-      // upper four lanes of a row write theirs the other way round: no bank twice.
-      // Rows r0 + 16 u have the swizzle of r0.
-      const uint32_t ch = (cg & 3) * 2, odd = cg >> 2;
-      const uint32_t at0 = (cg >> 2) * kHalfBytes + sw128_off(r0, ch + odd), at1 = (cg >> 2) * kHalfBytes + sw128_off(r0, ch + 1 - odd);
+      // ---- the conversion. Columns 16 cg .. + 16 are chunks 2 cg and 2 cg + 1; rows
+      // r0 + 16 u have the swizzle of r0.
+      const uint32_t at0 = half * kHalfBytes + sw128_off(r0, 2 * (lane_id & 3)), at1 = half * kHalfBytes + sw128_off(r0, 2 * (lane_id & 3) + 1);
       bool ok = true, have = next_piece(wk, all_lanes, false);
       int kt = wk.kt0, n = 0, slot = 0;
       while (ok && have) {
@@ -1294,7 +1296,7 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
         }
         const int op = n % L::KS;
         uint8_t* dst = tiles + op * kTileBytes;
-#pragma unroll 1
+#pragma unroll
         for (int part = 0; part < kParts; ++part) {
           if (is_v) asm volatile("cp.async.wait_group %0;" ::"n"(HELD ? L::RV - 1 : 0) : "memory");
           else asm volatile("cp.async.wait_group %0;" ::"n"(HELD ? L::RK - 1 : 0) : "memory");
@@ -1311,15 +1313,16 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
             if (n >= L::KS && !(ok = wait_bar_warp(&empty[op], ((n / L::KS) - 1) & 1, abort_flag, budget))) break;
           }
           const uint8_t* src = raw + slot * L::kRawBytes;
+          uint4 x[kU];  // all reads before the first write: the compiler keeps their order
+#pragma unroll
+          for (int u = 0; u < kU; ++u) x[u] = *reinterpret_cast<const uint4*>(src + u * 2048);
 #pragma unroll
           for (int u = 0; u < kU; ++u) {
-            uint4 x = *reinterpret_cast<const uint4*>(src + u * 16 * kD);
-            if (odd) x = make_uint4(x.z, x.w, x.x, x.y);
             uint4 a, b;
-            held_f16<KV>(x.x, a.x, a.y);
-            held_f16<KV>(x.y, a.z, a.w);
-            held_f16<KV>(x.z, b.x, b.y);
-            held_f16<KV>(x.w, b.z, b.w);
+            held_f16<KV>(x[u].x, a.x, a.y);
+            held_f16<KV>(x[u].y, a.z, a.w);
+            held_f16<KV>(x[u].z, b.x, b.y);
+            held_f16<KV>(x[u].w, b.z, b.w);
             *reinterpret_cast<uint4*>(dst + at0 + (part * kU + u) * 16 * 128) = a;
             *reinterpret_cast<uint4*>(dst + at1 + (part * kU + u) * 16 * 128) = b;
           }
