@@ -103,7 +103,9 @@ struct Lay {  // shared memory, offsets from a 1024-byte aligned base
   static constexpr uint32_t ml = bar + 512;          // [2][128] (reference, sum), NT = 1
   static constexpr uint32_t sc = ml + (NT == 1 ? 2 * 128 * 8 : 0);  // [SS] Scales
   static constexpr uint32_t walk = sc + SS * 1040;   // HELD: places of the roles' walks
-  static constexpr uint32_t bytes = walk + (HELD ? (2 * Roles<true>::kWarps - kSoftWarps) * kPlaceBytes : 0);
+  static constexpr uint32_t lens = walk + (HELD ? (2 * Roles<true>::kWarps - kSoftWarps) * kPlaceBytes : 0);
+  static constexpr uint32_t qs = lens + (HELD ? 144 : 0);  // HELD: [2][NT][128] the rows' factors, by the parity of the piece
+  static constexpr uint32_t bytes = qs + (HELD ? 2 * NT * 128 * 4 : 0);
   enum { QFull = 0, QEmpty, KFull, KEmpty = KFull + KS, VFull = KEmpty + KS, VEmpty = VFull + VS, SFull = VEmpty + VS,
          PFull = SFull + 2, OFull = PFull + 2, MlFull, ORead = MlFull + 2, Drain = ORead + 2, ScFull = Drain + 2, ScEmpty = ScFull + SS, Num = ScEmpty + SS };
 };
@@ -141,19 +143,13 @@ struct Item {
   // tokens aside, are in no row's window
   int lead, gap, low;
 };
-// b < 0: the shared prefix, p0 tiles.
+// An item of a sequence of that length (of the cache) and number of rows.
 template <bool EXT>
-__device__ __forceinline__ Item item_of(const TcAttnParams& p, int nt, int b, int m, int p0) {
+__device__ __forceinline__ Item item_from(const TcAttnParams& p, int nt, int m, int p0, int len, int cnt) {
   Item it;
   it.lead = it.gap = it.low = 0;
-  if (EXT && b < 0) {
-    it.cnt = p.c.B * p.c.T;
-    it.prefix = it.keys = p0 * kTile;
-    it.n = p0;
-    return it;
-  }
-  it.cnt = row_count(p.c.counts, b, p.c.T);
-  it.keys = key_count(p.c, b, it.cnt, &it.prefix);
+  it.cnt = cnt;
+  it.keys = keys_of(p.c, len, cnt, &it.prefix);
   const int64_t t0 = static_cast<int64_t>(m) * nt * p.tpt;
   if (t0 >= it.cnt) {
     it.n = 0;
@@ -163,7 +159,7 @@ __device__ __forceinline__ Item item_of(const TcAttnParams& p, int nt, int b, in
     it.n = static_cast<int>((end + kTile - 1) / kTile);
     if constexpr (EXT) {
       if (p.c.window > 0) {
-        it.low = window_low(p.c, b, p.c.parents ? 0 : t0);
+        it.low = window_low_of(p.c, len, p.c.parents ? 0 : t0);
         const Gap g = window_gap<kTile>(p.c, it.low, it.n);
         it.lead = g.lead;
         it.gap = g.gap;
@@ -175,6 +171,27 @@ __device__ __forceinline__ Item item_of(const TcAttnParams& p, int nt, int b, in
   }
   return it;
 }
+// b < 0: the shared prefix, p0 tiles.
+template <bool EXT>
+__device__ __forceinline__ Item item_of(const TcAttnParams& p, int nt, int b, int m, int p0) {
+  if (EXT && b < 0) {
+    Item it;
+    it.lead = it.gap = it.low = 0;
+    it.cnt = p.c.B * p.c.T;
+    it.prefix = it.keys = p0 * kTile;
+    it.n = p0;
+    return it;
+  }
+  const int cnt = row_count(p.c.counts, b, p.c.T);
+  return item_from<EXT>(p, nt, m, p0, ld_now(p.c.lens + b), cnt);
+}
+// Lengths of sequences that a CTA comes to, in shared memory: from memory they are
+// two round trips at each piece, for every role (64 tokens of short sequences: 10 us
+// a piece with them, and with the rows' factors read from q by the softmax).
+constexpr int kLens = 16;
+struct Lens {
+  int b0, len[kLens], cnt[kLens];
+};
 // The first key of the item's kt-th tile.
 template <bool EXT>
 __device__ __forceinline__ int tile_key(const Item& it, int kt) {
@@ -210,14 +227,19 @@ struct Walk {
     kt1 = t1;
   }
   template <bool ONE>
-  __device__ __forceinline__ bool next(const TcAttnParams& p, int nt) {
+  __device__ __forceinline__ bool next(const TcAttnParams& p, int nt, const Lens* lens = nullptr) {
     if (left <= 0) return false;
     if constexpr (ONE) {
       left = 0;
       return true;
     }
     while (true) {
-      it = item_of<EXT>(p, nt, b, m, p0);
+      int i = kLens;
+      if (lens && b >= 0) {
+        i = b - lens->b0;
+        if (i < 0) i += p.c.B;
+      }
+      it = i < kLens ? item_from<EXT>(p, nt, m, p0, lens->len[i], lens->cnt[i]) : item_of<EXT>(p, nt, b, m, p0);
       if (off < it.n) break;
       advance(p);
       if (h >= p.c.kv.Hkv) {  // lengths that changed under the kernel: no tiles are left
@@ -259,7 +281,7 @@ struct Walk {
 // not hold: every role was held up by its own instructions (64 tokens after up to
 // 8191 keys in e4m3 253 us).
 template <bool EXT>
-__device__ __noinline__ bool next_piece_of(const TcAttnParams& p, int nt, typename Walk<EXT>::Place* at) {
+__device__ __noinline__ bool next_piece_of(const TcAttnParams& p, int nt, typename Walk<EXT>::Place* at, const Lens* lens) {
   Walk<EXT> w;
   w.h = at->h;
   w.b = at->b;
@@ -267,7 +289,7 @@ __device__ __noinline__ bool next_piece_of(const TcAttnParams& p, int nt, typena
   w.off = at->off;
   w.left = at->left;
   w.p0 = at->p0;
-  if (!w.template next<false>(p, nt)) return false;
+  if (!w.template next<false>(p, nt, lens)) return false;
   *at = {w.h, w.b, w.m, w.off, w.left, w.p0, w.ph, w.pb, w.pm, w.kt0, w.kt1, w.it};
   return true;
 }
@@ -541,7 +563,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float sc,
 // end at 2^15 the reference has log2 of the tile's largest vs added to it; sums and
 // accumulators alike are in its units. The scores are read from TMEM twice, for the
 // maximum and for the weights, which take the place of scores that have been read.
-__device__ __forceinline__ void scale_chunk(uint32_t (&x)[32], const float* ks, bool mask, uint32_t mb) {
+__device__ __forceinline__ void scale_chunk(uint32_t (&x)[32], const float* ks) {
 #pragma unroll
   for (int t = 0; t < 32; t += 4) {
     const float4 k4 = *reinterpret_cast<const float4*>(ks + t);
@@ -552,11 +574,11 @@ __device__ __forceinline__ void scale_chunk(uint32_t (&x)[32], const float* ks, 
     x[t + 2] = __float_as_uint(b.x);
     x[t + 3] = __float_as_uint(b.y);
   }
-  if (mask) {
+}
+__device__ __forceinline__ void mask_chunk(uint32_t (&x)[32], uint32_t mb) {
 #pragma unroll
-    for (int t = 0; t < 32; ++t)
-      if (!((mb >> t) & 1u)) x[t] = 0xff800000u;
-  }
+  for (int t = 0; t < 32; ++t)
+    if (!((mb >> t) & 1u)) x[t] = 0xff800000u;
 }
 __device__ __forceinline__ float max_chunk(const uint32_t (&x)[32]) {
   float m0 = -INFINITY, m1 = -INFINITY;
@@ -586,15 +608,18 @@ __device__ __forceinline__ float2 weigh_chunk(uint32_t tP, const uint32_t (&x)[3
   tmem_st16(tP, pw);
   return ls;
 }
-__device__ __forceinline__ void softmax_held(uint32_t tS, uint32_t tO, float sc, const Scales& scales, bool mask, uint32_t mb0, uint32_t mb1, uint32_t mb2, uint32_t mb3, bool few,
-                                             int quarter, bool first, float& m_run, float& l_run) {
+// bits(i): the keys of chunk i that the row sees, where a mask is needed.
+template <class Bits>
+__device__ __forceinline__ void softmax_held(uint32_t tS, uint32_t tO, float sc, const Scales& scales, bool mask, Bits&& bits, bool few, int quarter,
+                                             bool first, float& m_run, float& l_run) {
   uint32_t x[32];
   const int c0 = few ? quarter : 0, c1 = few ? quarter + 1 : 4;
   float top = -INFINITY;
 #pragma unroll 1
   for (int i = c0; i < c1; ++i) {  // rolled, here and below, for the instruction cache
     tmem_ld32(tS + 32 * i, x);
-    scale_chunk(x, scales.k + 32 * i, mask, i & 2 ? (i & 1 ? mb3 : mb2) : (i & 1 ? mb1 : mb0));
+    scale_chunk(x, scales.k + 32 * i);
+    if (mask) mask_chunk(x, bits(i));
     top = fmaxf(top, max_chunk(x));
   }
   const float4 vt = *reinterpret_cast<const float4*>(scales.top);
@@ -610,7 +635,8 @@ __device__ __forceinline__ void softmax_held(uint32_t tS, uint32_t tO, float sc,
   for (int i = c0; i < c1; ++i) {
     if (!few) {  // else they are still here
       tmem_ld32(tS + 32 * i, x);
-      scale_chunk(x, scales.k + 32 * i, mask, i & 2 ? (i & 1 ? mb3 : mb2) : (i & 1 ? mb1 : mb0));
+      scale_chunk(x, scales.k + 32 * i);
+      if (mask) mask_chunk(x, bits(i));
     }
     ls = weigh_chunk(tS + 16 * i, x, scales.v + 32 * i, sc, m_use, ls);
   }
@@ -770,48 +796,55 @@ __device__ __forceinline__ void load_q(const TcAttnParams& P, const Walk<EXT>& w
 }
 // The same over caches of 8 bits, as fp16 and by way of registers (16 lanes have a
 // row, and other copies of theirs stay in flight). few: every 32 rows of the tile
-// are the same ones.
-template <int NT, bool F16, bool EXT, int N>
-__device__ __forceinline__ void load_q_held(const TcAttnParams& P, const Walk<EXT>& wk, uint8_t* sm, int qt, bool few) {
+// are the same ones. The first 32 rows are read before the wait for the tile; qs:
+// the rows' factors.
+template <int NT, bool F16, bool EXT, int N, class Wait>
+__device__ __forceinline__ bool load_q_held(const TcAttnParams& P, const Walk<EXT>& wk, uint8_t* sm, float* qs, int qt, bool few, Wait&& wait) {
   const CacheAttnParams& c = P.c;
   const int G = c.group;
+  static_assert(N * 4 == 512, "32 rows a turn");
+  const uint32_t inv = (65536u + G - 1) / G;  // row / G = row inv / 2^16 for rows below 256
+  bool first = true;
 #pragma unroll 1
-  for (int ti = 0; ti < NT; ++ti) {
-    const int t0 = (wk.pm * NT + ti) * P.tpt;
-    const int nv = max(0, min(P.tpt, wk.it.cnt - t0)) * G, fill = ((nv + 31) & ~31) * 16;
-    uint8_t* tile = sm + ti * kTileBytes;
-    constexpr int U = 4;
-#pragma unroll 1
-    for (int e0 = qt; e0 < fill; e0 += U * N) {  // fill: a multiple of U N
-      uint4 x[U];
+  for (int r0 = 0; r0 < NT * kTile; r0 += 32) {
+    const int ti = r0 / kTile, in0 = r0 - ti * kTile, t0 = (wk.pm * NT + ti) * P.tpt;
+    const int nv = max(0, min(P.tpt, wk.it.cnt - t0)) * G;
+    if (in0 >= nv && !first) continue;
+    uint4 x[4];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int e = e0 + u * N, row = e >> 4;
-        x[u] = make_uint4(0, 0, 0, 0);
-        if (row < nv) {
-          const RowAt at = row_at<EXT>(P, wk.pb, t0 + row / G);
-          x[u] = ld_v4(static_cast<const uint16_t*>(c.q.p) + at.b * c.q.sb + at.t * c.q.ss + (wk.ph * G + row % G) * c.q.sh + 8 * (e & 15));
-        }
+    for (int u = 0; u < 4; ++u) {
+      const int row = in0 + ((qt + u * N) >> 4);
+      const uint32_t tok = (row * inv) >> 16;
+      x[u] = make_uint4(0, 0, 0, 0);
+      if (row < nv) {
+        const RowAt at = row_at<EXT>(P, wk.pb, t0 + tok);
+        x[u] = ld_v4(static_cast<const uint16_t*>(c.q.p) + at.b * c.q.sb + at.t * c.q.ss + (wk.ph * G + row - tok * G) * c.q.sh + 8 * (qt & 15));
       }
+    }
+    if (first && !wait()) return false;
+    first = false;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int e = e0 + u * N, row = e >> 4, ch = e & 15;
-        if constexpr (!F16) {
-          uint32_t top = top_bits(x[u]);
+    for (int u = 0; u < 4; ++u) {
+      const int row = in0 + ((qt + u * N) >> 4), ch = qt & 15;
+      uint4 y = x[u];
+      if constexpr (!F16) {
+        uint32_t top = top_bits(y);
 #pragma unroll
-          for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-          x[u] = to_f16(x[u], __int_as_float((row_shift(top) + 127) << 23));
-        }
-        uint8_t* at = tile + (ch >> 3) * kHalfBytes + sw128_off(row, ch & 7);
-        *reinterpret_cast<uint4*>(at) = x[u];
-        if (few)
+        for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int shift = row_shift(top);
+        y = to_f16(y, __int_as_float((shift + 127) << 23));
+        if (ch == 0) qs[ti * 128 + row] = c.scale_log2 * __int_as_float((127 - shift) << 23);
+      }
+      uint8_t* at = sm + ti * kTileBytes + (ch >> 3) * kHalfBytes + sw128_off(row, ch & 7);
+      *reinterpret_cast<uint4*>(at) = y;
+      if (few) {
 #pragma unroll
-          for (int i = 1; i < 4; ++i) *reinterpret_cast<uint4*>(at + i * 32 * 128) = x[u];
+        for (int i = 1; i < 4; ++i) *reinterpret_cast<uint4*>(at + i * 32 * 128) = y;
       }
     }
   }
-  static_assert(N * 4 == 512, "32 rows a turn");
   fence_proxy_async_smem();
+  return true;
 }
 
 // A part in shared memory: NT x 128 rows of 128 floats over the K stages (and
@@ -934,7 +967,17 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
   // is no softmax warp
   Place* place = reinterpret_cast<Place*>(sm + L::walk) + warp;
   constexpr int kSecond = kTcWarps - kSoftWarps;
+  Lens* lens = reinterpret_cast<Lens*>(sm + L::lens);
+  static_assert(sizeof(Lens) <= 144, "layout");
   if constexpr (HELD && !CL) {
+    const int b0 = max(wk.b, 0);
+    if (tid < kLens) {
+      const int b = (b0 + tid) % c.B;
+      lens->len[tid] = ld_now(c.lens + b);
+      lens->cnt[tid] = row_count(c.counts, b, c.T);
+      lens->b0 = b0;
+    }
+    __syncthreads();
     if (lane_id == 0) {
       wk.save(place);
       if (warp >= kSoftWarps) wk.save(place + kSecond);
@@ -948,10 +991,10 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
       bool more = false;
       if constexpr (decltype(warp_wide)::value) {
         __syncwarp();  // every lane has what it wants of the last piece
-        if (lane_id == 0) more = next_piece_of<EXT>(P, NT, at);
+        if (lane_id == 0) more = next_piece_of<EXT>(P, NT, at, lens);
         more = __shfl_sync(0xffffffffu, more, 0);
       } else {
-        more = next_piece_of<EXT>(P, NT, at);
+        more = next_piece_of<EXT>(P, NT, at, lens);
       }
       if (more) w.take(at);
       return more;
@@ -1030,18 +1073,6 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
         low_last = __reduce_max_sync(0xffffffffu, low);
       }
       float row_sc = sc;
-      if constexpr (HELD && !F16) {
-        // the power of two that the row was brought to fp16 with: found again, as
-        // the row's way into shared memory is another warp's
-        if (valid) {
-          const RowAt at = row_at<EXT>(P, wk.pb, t);
-          const uint16_t* row = static_cast<const uint16_t*>(c.q.p) + at.b * c.q.sb + at.t * c.q.ss + (wk.ph * G + rg) * c.q.sh;
-          uint32_t top = 0;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) top = max(top, top_bits(ld_v4(row + 8 * i)));
-          row_sc = sc * __int_as_float((127 - row_shift(top)) << 23);
-        }
-      }
       float m_run = -INFINITY, l_run = 0.f;
       bool first = true;
       for (int j = static_cast<int>((slot ^ g) & 1); j < steps; j += 2) {
@@ -1053,27 +1084,33 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
           if (!(ok = wait_bar_warp(&bars[L::ScFull + sc_at % L::SS], (sc_at / L::SS) & 1, abort_flag, budget))) break;
         }
         const Scales& scales = reinterpret_cast<const Scales*>(sm + L::sc)[HELD ? sc_at % (HELD ? L::SS : 1) : 0];
+        // the row's factor: its way into shared memory ends before its warps say that
+        // the piece's first scales are there, and the next but one comes after this
+        // slot's weights
+        if (HELD && !F16 && first && valid) row_sc = reinterpret_cast<const float*>(sm + L::qs)[((n_piece & 1) * NT + (NT == 2 ? slot : 0)) * 128 + (few ? r_few : r)];
         tc_fence_after();
         if (act) {
           // the first node that the warp's first token does not see
           const int open = TREE ? wk.it.prefix : wk.it.prefix + __shfl_sync(0xffffffffu, t, 0) + 1;
           bool all = j0 + kTile <= min(open, wk.it.keys);
           if constexpr (EXT) all = all && (c.window == 0 || j0 >= low_last || j0 + kTile <= c.sinks);
-          if (all) {
+          if constexpr (HELD) {
+            softmax_held(tS, tO, row_sc, scales, !all, [&](int i) {
+              uint32_t w = valid ? key_bits<TREE>(j0 + 32 * i, wk.it, t, anc) : 0u;
+              if (EXT && c.window > 0) w &= window_bits<TREE>(j0 + 32 * i, low, c.sinks, wk.it.prefix);
+              return w;
+            }, few, warp & 3, first, m_run, l_run);
+          } else if (all) {
             const uint32_t mb[4] = {~0u, ~0u, ~0u, ~0u};
-            if constexpr (HELD) softmax_held(tS, tO, row_sc, scales, false, 0u, 0u, 0u, 0u, few, warp & 3, first, m_run, l_run);
-            else softmax_tile<F16, false>(tS, tO, sc, mb, first, m_run, l_run);
+            softmax_tile<F16, false>(tS, tO, sc, mb, first, m_run, l_run);
           } else {
-            uint32_t mb[4] = {};
+            uint32_t mb[4];
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              if (HELD && few && w != (warp & 3)) continue;  // the warp's own quarter only
-              const int j = j0 + 32 * w;
-              mb[w] = valid ? key_bits<TREE>(j, wk.it, t, anc) : 0u;
-              if (EXT && c.window > 0) mb[w] &= window_bits<TREE>(j, low, c.sinks, wk.it.prefix);
+              mb[w] = valid ? key_bits<TREE>(j0 + 32 * w, wk.it, t, anc) : 0u;
+              if (EXT && c.window > 0) mb[w] &= window_bits<TREE>(j0 + 32 * w, low, c.sinks, wk.it.prefix);
             }
-            if constexpr (HELD) softmax_held(tS, tO, row_sc, scales, true, mb[0], mb[1], mb[2], mb[3], few, warp & 3, first, m_run, l_run);
-            else softmax_tile<F16, true>(tS, tO, sc, mb, first, m_run, l_run);
+            softmax_tile<F16, true>(tS, tO, sc, mb, first, m_run, l_run);
           }
         }
         first = false;
@@ -1279,25 +1316,33 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
         asm volatile("cp.async.commit_group;" ::: "memory");
         return true;
       };
-#pragma unroll 1
-      for (int i = 0; i < n_raw; ++i) fetch();  // fewer tiles than SS: no wait
       // ---- the conversion. Columns 16 cg .. + 16 are chunks 2 cg and 2 cg + 1; rows
       // r0 + 16 u have the swizzle of r0.
       const uint32_t at0 = half * kHalfBytes + sw128_off(r0, 2 * (lane_id & 3)), at1 = half * kHalfBytes + sw128_off(r0, 2 * (lane_id & 3) + 1);
       bool ok = true, have = next_piece(wk, all_lanes, false);
-      int kt = wk.kt0, n = 0, slot = 0;
-      while (ok && have) {
-        if (!is_v && kt == wk.kt0) {
-          // a new piece: its rows, once the last one's scores are done
-          if (n_piece > 0 && !(ok = wait_bar_warp(&bars[L::QEmpty], (n_piece - 1) & 1, abort_flag, budget))) break;
-          load_q_held<NT, F16, EXT, kQWarps * 32>(P, wk, sm + L::q, qt, NT == 1 && P.few && wk.pb >= 0);
-          mbar_arrive(&bars[L::QFull]);
-          ++n_piece;
-        }
+      int kt = wk.kt0, n = 0, slot = 0, part = 0;
+      int ahead = n_raw;  // stages to be fetched before the first is converted (fewer tiles than SS: no wait)
+      // One stage a turn, in one copy of the code: unrolled, and with a fetch for
+      // the beginning, it was 36 KB of the instruction cache's.
+#pragma unroll 1
+      while (have) {
         const int op = n % L::KS;
-        uint8_t* dst = tiles + op * kTileBytes;
-#pragma unroll
-        for (int part = 0; part < kParts; ++part) {
+        if (ahead > 0) {
+          --ahead;
+        } else {
+          if (part == 0) {
+            if (!is_v && kt == wk.kt0) {
+              // a new piece: its rows, once the last one's scores are done
+              const bool q_few = NT == 1 && P.few && wk.pb >= 0;
+              float* qs = reinterpret_cast<float*>(sm + L::qs) + (n_piece & 1) * NT * 128;
+              if (!load_q_held<NT, F16, EXT, kQWarps * 32>(P, wk, sm + L::q, qs, qt, q_few, [&]() -> bool {
+                    return n_piece == 0 || wait_bar_warp(&bars[L::QEmpty], (n_piece - 1) & 1, abort_flag, budget);
+                  }))
+                break;
+              mbar_arrive(&bars[L::QFull]);
+              ++n_piece;
+            }
+          }
           if (is_v) asm volatile("cp.async.wait_group %0;" ::"n"(HELD ? L::RV - 1 : 0) : "memory");
           else asm volatile("cp.async.wait_group %0;" ::"n"(HELD ? L::RK - 1 : 0) : "memory");
           if (part == 0) {
@@ -1313,6 +1358,7 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
             if (n >= L::KS && !(ok = wait_bar_warp(&empty[op], ((n / L::KS) - 1) & 1, abort_flag, budget))) break;
           }
           const uint8_t* src = raw + slot * L::kRawBytes;
+          uint8_t* dst = tiles + op * kTileBytes + part * kU * 16 * 128;
           uint4 x[kU];  // all reads before the first write: the compiler keeps their order
 #pragma unroll
           for (int u = 0; u < kU; ++u) x[u] = *reinterpret_cast<const uint4*>(src + u * 2048);
@@ -1323,20 +1369,22 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
             held_f16<KV>(x[u].y, a.z, a.w);
             held_f16<KV>(x[u].z, b.x, b.y);
             held_f16<KV>(x[u].w, b.z, b.w);
-            *reinterpret_cast<uint4*>(dst + at0 + (part * kU + u) * 16 * 128) = a;
-            *reinterpret_cast<uint4*>(dst + at1 + (part * kU + u) * 16 * 128) = b;
+            *reinterpret_cast<uint4*>(dst + at0 + u * 16 * 128) = a;
+            *reinterpret_cast<uint4*>(dst + at1 + u * 16 * 128) = b;
           }
-          if (!(ok = fetch())) break;  // into the stage that has just been read, by this thread
           if (++slot == n_raw) slot = 0;
+          if (++part == kParts) {
+            part = 0;
+            fence_proxy_async_smem();
+            mbar_arrive(&full[op]);
+            ++n;
+            if (++kt == wk.kt1) {
+              have = next_piece(wk, all_lanes, false);
+              kt = wk.kt0;
+            }
+          }
         }
-        if (!ok) break;
-        fence_proxy_async_smem();
-        mbar_arrive(&full[op]);
-        ++n;
-        if (++kt == wk.kt1) {
-          have = next_piece(wk, all_lanes, false);
-          kt = wk.kt0;
-        }
+        if (!fetch()) break;  // into the stage that has just been read, by this thread
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
     } else {

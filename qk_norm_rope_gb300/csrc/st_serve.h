@@ -124,19 +124,23 @@ struct CacheAttnParams {
 
 // Number of keys of sequence b: its prefix and its new rows, at most what the
 // page table has room for.
-__device__ __forceinline__ int key_count(const CacheAttnParams& p, int b, int count, int* prefix) {
+__device__ __forceinline__ int keys_of(const CacheAttnParams& p, int length, int count, int* prefix) {
   const int64_t cap = static_cast<int64_t>(p.kv.max_pages) * p.kv.page;
-  const int64_t len = max(ld_now(p.lens + b), 0);
+  const int64_t len = max(length, 0);
   *prefix = static_cast<int>(min(len, cap));
   return static_cast<int>(min(len + count, cap));
+}
+__device__ __forceinline__ int key_count(const CacheAttnParams& p, int b, int count, int* prefix) {
+  return keys_of(p, ld_now(p.lens + b), count, prefix);
 }
 
 // The lowest position in the window of a row at lens[b] + step, at least 0 and
 // at most 2^30 (no key lies there). `sinks` aside.
-__device__ __forceinline__ int window_low(const CacheAttnParams& p, int b, int64_t step) {
-  const int64_t low = max(ld_now(p.lens + b), 0) + step - p.window + 1;
+__device__ __forceinline__ int window_low_of(const CacheAttnParams& p, int length, int64_t step) {
+  const int64_t low = max(length, 0) + step - p.window + 1;
   return static_cast<int>(min(max(low, int64_t(0)), int64_t(1) << 30));
 }
+__device__ __forceinline__ int window_low(const CacheAttnParams& p, int b, int64_t step) { return window_low_of(p, ld_now(p.lens + b), step); }
 // With a window, how many nodes are above `node` of sequence b's tree (parents
 // come before children; anything else ends the walk).
 __device__ __forceinline__ int node_depth(const CacheAttnParams& p, int b, int node) {
