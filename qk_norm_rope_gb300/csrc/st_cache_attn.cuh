@@ -95,11 +95,11 @@ struct Lay {  // shared memory, offsets from a 1024-byte aligned base
   // parity says nothing where phases went by unseen.
   static constexpr int KS = NT == 1 || HELD ? 2 : 3, VS = NT == 1 && !HELD ? 4 : 2;
   static constexpr int SS = HELD ? 4 : 0;                   // stages of scales (NT = 1: of one slot, as above)
-  // stages of bytes, of K and of V, and their keys: 56 KB in flight where reading bounds
-  static constexpr int RK = !HELD ? 0 : (NT == 1 ? 4 : 3), RV = !HELD ? 0 : 3, kRawRows = NT == 1 ? 64 : 32;
+  // stages of bytes, of K and of V each, and their keys: 48 KB where reading bounds
+  static constexpr int RS = HELD ? 3 : 0, kRawRows = NT == 1 ? 64 : 32;
   static constexpr uint32_t kRawBytes = kRawRows * kD;
   static_assert(NT == 2 || (KS % 2 == 0 && VS % 2 == 0 && SS % 2 == 0), "stages of one slot");
-  static constexpr uint32_t q = 0, k = NT * kTileBytes, v = k + KS * kTileBytes, raw = v + VS * kTileBytes, bar = raw + (RK + RV) * kRawBytes;
+  static constexpr uint32_t q = 0, k = NT * kTileBytes, v = k + KS * kTileBytes, raw = v + VS * kTileBytes, bar = raw + 2 * RS * kRawBytes;
   static constexpr uint32_t ml = bar + 512;          // [2][128] (reference, sum), NT = 1
   static constexpr uint32_t sc = ml + (NT == 1 ? 2 * 128 * 8 : 0);  // [SS] Scales
   static constexpr uint32_t walk = sc + SS * 1040;   // HELD: places of the roles' walks
@@ -1006,7 +1006,7 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
   constexpr std::false_type one_lane;
   const int G = c.group, tile_rows = P.tpt * G;
   float2* part_ml = reinterpret_cast<float2*>(sm + L::k + NT * 65536);  // CL
-  static_assert(NT * (65536 + 1024) <= (L::KS + L::VS) * kTileBytes + (L::RK + L::RV) * L::kRawBytes, "a part fits over the stages");
+  static_assert(NT * (65536 + 1024) <= (L::KS + L::VS) * kTileBytes + 2 * L::RS * L::kRawBytes, "a part fits over the stages");
 
   if (warp < kSoftWarps) {
     // -------------------------------------------------------------- softmax
@@ -1248,15 +1248,14 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
       uint64_t* empty = &bars[is_v ? L::VEmpty : L::KEmpty];
       uint8_t* tiles = sm + (is_v ? L::v : L::k);
       static_assert(L::KS == L::VS, "one count");
-      uint8_t* raw = sm + L::raw + (is_v ? L::RK : 0) * L::kRawBytes + (gw * 32 + lane_id) * 16;  // + 2048 u
-      const int n_raw = is_v ? L::RV : L::RK;
+      uint8_t* raw = sm + L::raw + (is_v ? L::RS : 0) * L::kRawBytes + (gw * 32 + lane_id) * 16;  // + 2048 u
       // places in 32 bits: of rows in units of 16 bytes, of scales in numbers (the
       // host has seen that they fit)
       const HeldAt at = is_v ? P.held_v : P.held_k;
       const uint8_t* base = static_cast<const uint8_t*>(is_v ? kv.v : kv.k) + 16 * cg;
       const float* sc_base = is_v ? kv.vs : kv.ks;
       constexpr uint32_t kNowhere = ~0u;
-      // ---- the stream of fetches, up to n_raw stages ahead of the conversion. A
+      // ---- the stream of fetches, RS stages ahead of the conversion. A
       // lane looks up the place of one of its warp's 32 rows of a tile, a tile ahead
       // of the fetch, and has that row's scale.
       const int my_row = 4 * gw + (lane_id & 3) + 16 * (lane_id >> 2);
@@ -1279,10 +1278,10 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
       };
       bool there = l_have;  // a tile was looked up
       if (there) look();
-      int i_tile = 0, i_part = 0, i_slot = 0;
+      int i_tile = 0;
       bool i_have = false;
       uint32_t off = kNowhere;  // of the lane's row
-      auto fetch = [&]() -> bool {
+      auto fetch = [&](int i_part, uint8_t* dst) -> bool {
         if (i_part == 0) {
           i_have = there;
           if (there) {
@@ -1304,14 +1303,11 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
           }
         }
         if (i_have) {
-          uint8_t* dst = raw + i_slot * L::kRawBytes;
           uint32_t o[kU];
 #pragma unroll
           for (int u = 0; u < kU; ++u) o[u] = __shfl_sync(0xffffffffu, off, r_in + 4 * (i_part * kU + u));
 #pragma unroll
           for (int u = 0; u < kU; ++u) cp_async16(dst + u * 2048, base + (o[u] == kNowhere ? 0u : o[u]) * static_cast<uint64_t>(16), o[u] != kNowhere);
-          if (++i_part == kParts) i_part = 0;
-          if (++i_slot == n_raw) i_slot = 0;
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         return true;
@@ -1320,31 +1316,27 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
       // r0 + 16 u have the swizzle of r0.
       const uint32_t at0 = half * kHalfBytes + sw128_off(r0, 2 * (lane_id & 3)), at1 = half * kHalfBytes + sw128_off(r0, 2 * (lane_id & 3) + 1);
       bool ok = true, have = next_piece(wk, all_lanes, false);
-      int kt = wk.kt0, n = 0, slot = 0, part = 0;
-      int ahead = n_raw;  // stages to be fetched before the first is converted (fewer tiles than SS: no wait)
-      // One stage a turn, in one copy of the code: unrolled, and with a fetch for
-      // the beginning, it was 36 KB of the instruction cache's.
+      int kt = wk.kt0, n = 0, slot = 0;
+#pragma unroll
+      for (int i = 0; i < L::RS; ++i) fetch(i % kParts, raw + i * L::kRawBytes);  // fewer tiles than SS: no wait
 #pragma unroll 1
-      while (have) {
+      while (ok && have) {
+        if (!is_v && kt == wk.kt0) {
+          // a new piece: its rows, once the last one's scores are done
+          const bool q_few = NT == 1 && P.few && wk.pb >= 0;
+          float* qs = reinterpret_cast<float*>(sm + L::qs) + (n_piece & 1) * NT * 128;
+          if (!load_q_held<NT, F16, EXT, kQWarps * 32>(P, wk, sm + L::q, qs, qt, q_few, [&]() -> bool {
+                return n_piece == 0 || wait_bar_warp(&bars[L::QEmpty], (n_piece - 1) & 1, abort_flag, budget);
+              }))
+            break;
+          mbar_arrive(&bars[L::QFull]);
+          ++n_piece;
+        }
         const int op = n % L::KS;
-        if (ahead > 0) {
-          --ahead;
-        } else {
-          if (part == 0) {
-            if (!is_v && kt == wk.kt0) {
-              // a new piece: its rows, once the last one's scores are done
-              const bool q_few = NT == 1 && P.few && wk.pb >= 0;
-              float* qs = reinterpret_cast<float*>(sm + L::qs) + (n_piece & 1) * NT * 128;
-              if (!load_q_held<NT, F16, EXT, kQWarps * 32>(P, wk, sm + L::q, qs, qt, q_few, [&]() -> bool {
-                    return n_piece == 0 || wait_bar_warp(&bars[L::QEmpty], (n_piece - 1) & 1, abort_flag, budget);
-                  }))
-                break;
-              mbar_arrive(&bars[L::QFull]);
-              ++n_piece;
-            }
-          }
-          if (is_v) asm volatile("cp.async.wait_group %0;" ::"n"(HELD ? L::RV - 1 : 0) : "memory");
-          else asm volatile("cp.async.wait_group %0;" ::"n"(HELD ? L::RK - 1 : 0) : "memory");
+        uint8_t* dst = tiles + op * kTileBytes;
+#pragma unroll
+        for (int part = 0; part < kParts; ++part) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(HELD ? L::RS - 1 : 0) : "memory");
           if (part == 0) {
             const int st = n % L::SS;
             Scales& s = reinterpret_cast<Scales*>(sm + L::sc)[st];
@@ -1357,8 +1349,7 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
             if (lane_id == 0) mbar_arrive(&bars[L::ScFull + st]);
             if (n >= L::KS && !(ok = wait_bar_warp(&empty[op], ((n / L::KS) - 1) & 1, abort_flag, budget))) break;
           }
-          const uint8_t* src = raw + slot * L::kRawBytes;
-          uint8_t* dst = tiles + op * kTileBytes + part * kU * 16 * 128;
+          uint8_t* src = raw + slot * L::kRawBytes;
           uint4 x[kU];  // all reads before the first write: the compiler keeps their order
 #pragma unroll
           for (int u = 0; u < kU; ++u) x[u] = *reinterpret_cast<const uint4*>(src + u * 2048);
@@ -1369,22 +1360,20 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
             held_f16<KV>(x[u].y, a.z, a.w);
             held_f16<KV>(x[u].z, b.x, b.y);
             held_f16<KV>(x[u].w, b.z, b.w);
-            *reinterpret_cast<uint4*>(dst + at0 + u * 16 * 128) = a;
-            *reinterpret_cast<uint4*>(dst + at1 + u * 16 * 128) = b;
+            *reinterpret_cast<uint4*>(dst + at0 + (part * kU + u) * 16 * 128) = a;
+            *reinterpret_cast<uint4*>(dst + at1 + (part * kU + u) * 16 * 128) = b;
           }
-          if (++slot == n_raw) slot = 0;
-          if (++part == kParts) {
-            part = 0;
-            fence_proxy_async_smem();
-            mbar_arrive(&full[op]);
-            ++n;
-            if (++kt == wk.kt1) {
-              have = next_piece(wk, all_lanes, false);
-              kt = wk.kt0;
-            }
-          }
+          if (!(ok = fetch((part + L::RS) % kParts, src))) break;  // into the stage that has just been read, by this thread
+          slot = slot == L::RS - 1 ? 0 : slot + 1;
         }
-        if (!fetch()) break;  // into the stage that has just been read, by this thread
+        if (!ok) break;
+        fence_proxy_async_smem();
+        mbar_arrive(&full[op]);
+        ++n;
+        if (++kt == wk.kt1) {
+          have = next_piece(wk, all_lanes, false);
+          kt = wk.kt0;
+        }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
