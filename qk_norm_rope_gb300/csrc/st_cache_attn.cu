@@ -149,9 +149,10 @@ __global__ void __launch_bounds__(256) join_items_kernel(const __grid_constant__
 }  // namespace
 
 cudaError_t launch_cache_attn_tc(const TcAttnParams& p, int nt, bool f16, cudaStream_t stream) {
-  if (p.c.kv.dt == kDtE4M3) return launch_cache_attn_e4m3(p, nt, f16, stream);
-  if (p.c.kv.dt == kDtI8) return launch_cache_attn_i8(p, nt, f16, stream);
-  if (p.c.window > 0 || p.c.shared) return launch_cache_attn_ext(p, nt, f16, stream);
+  const bool ext = p.c.window > 0 || p.c.shared;
+  if (p.c.kv.dt == kDtE4M3) return ext ? launch_cache_attn_e4m3_ext(p, nt, f16, stream) : launch_cache_attn_e4m3(p, nt, f16, stream);
+  if (p.c.kv.dt == kDtI8) return ext ? launch_cache_attn_i8_ext(p, nt, f16, stream) : launch_cache_attn_i8(p, nt, f16, stream);
+  if (ext) return launch_cache_attn_ext(p, nt, f16, stream);
   return launch_form<0, false>(p, nt, f16, stream);
 }
 

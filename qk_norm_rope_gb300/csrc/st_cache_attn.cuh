@@ -321,7 +321,7 @@ struct Start {  // found by the block, read by every role
   int h, b, m, off;
   long long left;
   int p0, pre_b;           // EXT: tiles of the shared prefix, the sequence whose pages hold it
-  long long first, total;  // EXT: the range's first tile, the call's tiles
+  long long first, total;  // joined by items: the range's first tile, the call's tiles
 };
 
 // The shared prefix: whole tiles of what the least of the sequences that have
@@ -358,7 +358,7 @@ __device__ __forceinline__ void find_shared(const TcAttnParams& p, int* scratch,
 // Where the CTA's range begins: every thread sums the key tiles of a run of
 // (sequence, group) pairs (the shared prefix's groups first), a block scan places
 // the runs.
-template <bool EXT, int W>
+template <bool EXT, int W, bool ITEMS>  // ITEMS: the call may join by items
 __device__ __forceinline__ void find_start(const TcAttnParams& p, int nt, long long* scan, Start* st) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int p0 = 0;
@@ -406,7 +406,7 @@ __device__ __forceinline__ void find_start(const TcAttnParams& p, int nt, long l
   }
   Deal d;
   d.make(one * p.c.kv.Hkv, p.ctas);
-  if constexpr (EXT) {
+  if constexpr (ITEMS) {
     if (tid == 0) {
       st->first = blockIdx.x < d.ctas ? d.first(blockIdx.x) : 0;
       st->total = d.total;
@@ -425,7 +425,7 @@ __device__ __forceinline__ void find_start(const TcAttnParams& p, int nt, long l
           st->m = m;
           st->off = static_cast<int>(rem);
           st->left = d.first(blockIdx.x + 1) - s0;
-          if (EXT && p.item_meta) break;
+          if (ITEMS && p.item_meta) break;
           // for the join: is this border the first inside of its item, and
           // who has the item's tiles?
           JoinMeta meta{0, 0, h, b, m, it.cnt};
@@ -444,7 +444,7 @@ __device__ __forceinline__ void find_start(const TcAttnParams& p, int nt, long l
         }
       }
     }
-  } else if (tid == 0 && !(EXT && p.item_meta)) {
+  } else if (tid == 0 && !(ITEMS && p.item_meta)) {
     p.meta[blockIdx.x].parts = 0;
   }
   __syncthreads();
@@ -949,7 +949,7 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
       atomicOr(c.status, kStatusIndex);
   } else {
     // the scan's scratch lies in the Q tile, which is written later
-    find_start<EXT, kTcWarps>(P, NT, reinterpret_cast<long long*>(sm + L::q), start);
+    find_start<EXT, kTcWarps, EXT || HELD>(P, NT, reinterpret_cast<long long*>(sm + L::q), start);
     wk.h = start->h;
     wk.b = start->b;
     wk.m = start->m;
@@ -960,7 +960,7 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
       pre_b = start->pre_b;
     }
   }
-  const bool by_items = EXT && !CL && P.item_meta;  // every result is joined
+  const bool by_items = (EXT || HELD) && !CL && P.item_meta;  // every result is joined
   using Place = typename Walk<EXT>::Place;
   static_assert(sizeof(Place) == kPlaceBytes, "layout");
   // HELD: this warp's place, and behind all of them a second one of each warp that
@@ -1137,7 +1137,7 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
       const int64_t pslot = 2 * static_cast<int64_t>(blockIdx.x) + (at_start ? 0 : 1);
       at_start = false;
       int64_t prow0 = pslot * P.part_rows;  // the part's first row
-      if constexpr (EXT && !CL) {
+      if constexpr ((EXT || HELD) && !CL) {
         if (by_items) {
           prow0 = pslot * P.split_rows;
           if (wk.whole()) prow0 = whole_part(P, wk.ph, wk.pb, wk.pm);

@@ -218,7 +218,9 @@ inline int tc_tiles(int T, int group) { return static_cast<int64_t>(T) * group >
 cudaError_t launch_cache_attn_tc(const TcAttnParams& p, int nt, bool f16, cudaStream_t stream);
 cudaError_t launch_cache_attn_ext(const TcAttnParams& p, int nt, bool f16, cudaStream_t stream);   // the forms, each in a file of its own
 cudaError_t launch_cache_attn_e4m3(const TcAttnParams& p, int nt, bool f16, cudaStream_t stream);
+cudaError_t launch_cache_attn_e4m3_ext(const TcAttnParams& p, int nt, bool f16, cudaStream_t stream);
 cudaError_t launch_cache_attn_i8(const TcAttnParams& p, int nt, bool f16, cudaStream_t stream);
+cudaError_t launch_cache_attn_i8_ext(const TcAttnParams& p, int nt, bool f16, cudaStream_t stream);
 cudaError_t launch_cache_attn_join(const TcAttnParams& p, int nt, cudaStream_t stream);
 
 // Rows of a cache into dense tensors [B, T, Hkv, D].
