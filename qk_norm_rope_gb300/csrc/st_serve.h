@@ -214,7 +214,7 @@ struct JoinMeta {
   int parts, slot0;            // parts = 0: there is no such item
   int h, b, m, cnt;
 };
-inline int tc_tiles(int T, int group) { return static_cast<int64_t>(T) * group > 128 ? 2 : 1; }
+inline int tc_tiles(int64_t T, int group) { return T * group > 128 ? 2 : 1; }
 cudaError_t launch_cache_attn_tc(const TcAttnParams& p, int nt, bool f16, cudaStream_t stream);
 cudaError_t launch_cache_attn_ext(const TcAttnParams& p, int nt, bool f16, cudaStream_t stream);   // the forms, each in a file of its own
 cudaError_t launch_cache_attn_e4m3(const TcAttnParams& p, int nt, bool f16, cudaStream_t stream);
