@@ -392,7 +392,7 @@ ST_API st_status st_cache_attn(const st_tensor* q_rot, const st_kv_cache* cache,
  *           or fp32 and o of its type; the held values enter the products exactly,
  *           scales and sums are fp32, the softmax weights times V's scales are
  *           rounded to fp16 (relative to the largest scale of 128 keys; scales of
- *           V are good from 2^-80 to 2^80), with fp32 rows nothing is. The scales
+ *           V are good from 2^-50 to 2^50), with fp32 rows nothing is. The scales
  *           of keys that no row sees are not used.
  *  window:  0: none. Else a row at position p sees, of the keys that it would see
  *           without, those at positions above p - window and those below sinks.

@@ -121,8 +121,10 @@ struct Scales {
   float top[4];
 };
 static_assert(sizeof(Scales) == 1040, "layout");
-// V's scales are good in this range (base 2).
-constexpr float kTopRange = 80.f;
+// V's scales are good in this range (base 2): between its ends a row's sum, in
+// units of them, may shrink by 2^-100, and a share of it above 2^-26 stays in ex2's
+// range.
+constexpr float kTopRange = 50.f;
 
 __device__ __forceinline__ constexpr uint32_t kofs(int kk) { return (kk >> 2) * kHalfBytes + (kk & 3) * 32; }
 __device__ __forceinline__ constexpr uint32_t mofs(int kk) { return kk * 2048; }
@@ -162,7 +164,9 @@ __device__ __forceinline__ Item item_from(const TcAttnParams& p, int nt, int m, 
         it.low = window_low_of(p.c, len, p.c.parents ? 0 : t0);
         const Gap g = window_gap<kTile>(p.c, it.low, it.n);
         it.lead = g.lead;
-        it.gap = g.gap;
+        // (a length beyond the table leaves no key in the window: one tile, all masked,
+        // gives the rows their zeros)
+        it.gap = g.gap == it.n ? it.n - 1 : g.gap;
       } else {
         it.gap = min(p0, it.n);
       }

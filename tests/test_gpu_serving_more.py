@@ -388,6 +388,28 @@ def test_lengths_out_of_range(cuda_lib, dtype, kv, page, window):
     assert bool((o[1] == 0).all()) and bool((lse[1] == -math.inf).all())  # no key of these windows is in the table
 
 
+@pytest.mark.parametrize("dtype,kv,T", [("bf16", "bf16", 1), ("fp16", "fp16", 70), ("bf16", "e4m3", 1), ("fp16", "int8", 40)])
+def test_windows_behind_the_table_of_many_sequences(cuda_lib, dtype, kv, T):
+    """More items than SMs: rows whose window has no key of the table are zeros all the same."""
+    B, far = 90, 1 << 30
+    lens = [(b * 37) % 200 for b in range(B)]
+    q, c, _, _ = attend_inputs(dtype, kv, B, T, 4, 2, lens, None, 16, False, 0, 0)
+    some = [0, 41, 89]
+    lens_far = [far if b in some else n for b, n in enumerate(lens)]
+    scales = None if c[3] is None else (c[3], c[4])
+    cache = dev_cache(cuda_lib, c)
+    need = cuda_lib.st_cache_attn_workspace_size(q.cuda(), cache, window=30)
+    o, lse = torch.full_like(q, 7.0).cuda(), torch.full((B, 4, T), 7.0).cuda()
+    cuda_lib.st_cache_attn(q.cuda(), cache, i32(lens_far).cuda(), window=30, o=o, lse=lse, workspace=torch.empty(need, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(cuda_lib.StError):
+        cuda_lib.st_check_status()
+    assert bool((o[some] == 0).all()) and bool((lse[some] == -math.inf).all())
+    want = M.attention(q, c[0], c[1], c[2], lens, None, None, 30, 0, scales)
+    rest = [b for b in range(B) if b not in some]
+    R.close("o", o[rest], want[0][rest], want[2][rest])
+    R.close("lse", lse[rest], want[1][rest], want[3][rest])
+
+
 # ------------------------------------------------------------ shared prefix
 SHARED = [
     # dtype, cache, B, T, H, Hkv, shared, own lengths, counts, page, tree
@@ -480,6 +502,22 @@ def test_scales_of_every_size(cuda_lib, dtype, kv):
     c[4][pg, :, row] = 0.0
     if dtype == "bf16":  # (fp16 holds no such numbers)
         q = (q.float() * torch.exp2(torch.arange(-30, 2, 4).float())[None, :, None, None]).to(q.dtype)
+    o, lse = cuda_lib.st_cache_attn(q.cuda(), dev_cache(cuda_lib, c), i32(lens).cuda())
+    want = M.attention(q, c[0], c[1], c[2], lens, None, None, scales=(c[3], c[4]))
+    R.close("o", o, want[0], want[2])
+    R.close("lse", lse, want[1], want[3])
+
+
+@pytest.mark.parametrize("kv", HELD)
+@pytest.mark.parametrize("T", [1, 20, 80])
+def test_scales_at_the_ends_of_their_range(cuda_lib, kv, T):
+    """Tiles of V rows near 2^-48 before, between and behind others near 2^48: none is lost from the sums."""
+    B, H, Hkv, lens = 2, 4, 2, [700, 640]
+    q, c, _, _ = attend_inputs("bf16", kv, B, T, H, Hkv, lens, None, 16, False, 0, 0)
+    for b, n in enumerate(lens):
+        at = torch.arange(n + T)
+        pg, row = R.slots(c[2], 16, b, at)
+        c[4][pg, :, row] *= torch.exp2(torch.where((at // 128) % 2 == b, -48.0, 48.0))[:, None]
     o, lse = cuda_lib.st_cache_attn(q.cuda(), dev_cache(cuda_lib, c), i32(lens).cuda())
     want = M.attention(q, c[0], c[1], c[2], lens, None, None, scales=(c[3], c[4]))
     R.close("o", o, want[0], want[2])
