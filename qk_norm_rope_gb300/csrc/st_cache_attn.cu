@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(256, U > 4 ? 2 : 6) join_kernel(const __grid_c
 // its own keys come together, each whole or in the parts that CTAs left of it, these
 // in four copies with FEW. W warps take a row, a lane four columns; four parts are in
 // flight for each, and the first warp brings the warps' results together. (One token
-// of 8 K/V heads after 30000 keys in 8 bits has 76 parts a row: 18 us of one warp.)
+// of 8 K/V heads after 30000 keys in 8 bits has 76 parts a row.)
 template <int W>
 __global__ void __launch_bounds__(256) join_items_kernel(const __grid_constant__ TcAttnParams P, int nt) {
   __shared__ float4 so[W][kD / 4];
@@ -159,9 +159,10 @@ cudaError_t launch_cache_attn_tc(const TcAttnParams& p, int nt, bool f16, cudaSt
 cudaError_t launch_cache_attn_join(const TcAttnParams& p, int nt, cudaStream_t stream) {
   if (p.item_meta) {
     const int64_t rows = static_cast<int64_t>(p.c.B) * p.c.T * p.c.H;
-    // few items, whose parts are then many, and not many rows: eight warps a row
-    const int64_t items = (static_cast<int64_t>(p.c.B) * p.n_groups + p.n_pre) * p.c.kv.Hkv;
-    const int warps = items * 4 <= p.ctas * 3 && rows <= 8192 ? 8 : 1;
+    // eight warps a row where the rows' blocks then run at once (one token of 8 K/V
+    // heads after 240000 keys 22 us with one warp and 10 with eight, 512 rows 11.7 and
+    // 9.7, 1152 rows 12.2 and 12.4, 4608 rows 12 and 31)
+    const int warps = rows <= 1024 ? 8 : 1;
     return launch_chained(warps == 8 ? join_items_kernel<8> : join_items_kernel<1>, dim3(static_cast<unsigned>((rows * warps + 7) / 8)), dim3(256),
                           0, stream, p, nt);
   }

@@ -76,7 +76,7 @@ struct Roles {
 };
 // Registers per thread of the 16-bit form: its softmax threads hold a row of 128
 // scores. 256 * 184 + 256 * 72 = 512 * 128. KV reads the scores from TMEM twice
-// instead and has 112 everywhere.
+// instead and has 96 everywhere (five warps on one of the SM's four register files).
 constexpr int kRegsSoft = 184, kRegsRest = 72;
 constexpr float kRescale = 8.0f;  // O is rescaled when the running maximum grows by more than this (base 2)
 // How far the reference stays below the running maximum (base 2). fp16 weights
@@ -561,15 +561,19 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float sc,
   tmem_st_wait();
 }
 
-// The same over a cache of 8 bits, over the chunks [c0, c1) of 32 keys (with FEW one;
-// the weights of the others are zero). Scores are s ks sc: ks the key's scale, sc
-// the row's factor. The weights are rounded as P vs, vs V's scale, and so that they
-// end at 2^15 the reference has log2 of the tile's largest vs added to it; sums and
-// accumulators alike are in its units. The scores are read from TMEM twice, for the
-// maximum and for the weights, which take the place of scores that have been read.
-__device__ __forceinline__ void scale_chunk(uint32_t (&x)[32], const float* ks) {
+// The same over a cache of 8 bits, in chunks of 32 keys (FEW: a warp has one, and its
+// weights of the others are zero). Scores are s ks sc: ks the key's scale, sc the row's
+// factor. The weights are rounded as P vs, vs V's scale, and so that they end at 2^15
+// the reference has log2 of the tile's largest vs added to it; sums and accumulators
+// alike are in its units. There are no registers for a row of 128 scores: they go back
+// to TMEM, scaled and masked, while the maximum is found, and come again for the
+// weights, which take the place of scores that have been read. (Scaled and masked a
+// second time instead, 2048 tokens after 16384 took 926 us over e4m3, now 751: the
+// reads of the scales from shared memory stand in line with the MMAs' operands.)
+template <int N>
+__device__ __forceinline__ void scale_chunk(uint32_t (&x)[N], const float* ks) {
 #pragma unroll
-  for (int t = 0; t < 32; t += 4) {
+  for (int t = 0; t < N; t += 4) {
     const float4 k4 = *reinterpret_cast<const float4*>(ks + t);
     const float2 a = __fmul2_rn(make_float2(__uint_as_float(x[t]), __uint_as_float(x[t + 1])), make_float2(k4.x, k4.y));
     const float2 b = __fmul2_rn(make_float2(__uint_as_float(x[t + 2]), __uint_as_float(x[t + 3])), make_float2(k4.z, k4.w));
@@ -584,21 +588,23 @@ __device__ __forceinline__ void mask_chunk(uint32_t (&x)[32], uint32_t mb) {
   for (int t = 0; t < 32; ++t)
     if (!((mb >> t) & 1u)) x[t] = 0xff800000u;
 }
-__device__ __forceinline__ float max_chunk(const uint32_t (&x)[32]) {
+template <int N>
+__device__ __forceinline__ float max_chunk(const uint32_t (&x)[N]) {
   float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-  for (int t = 0; t < 32; t += 4) {
+  for (int t = 0; t < N; t += 4) {
     m0 = fmax3(m0, __uint_as_float(x[t]), __uint_as_float(x[t + 1]));
     m1 = fmax3(m1, __uint_as_float(x[t + 2]), __uint_as_float(x[t + 3]));
   }
   return fmaxf(m0, m1);
 }
-// The weights of a chunk into its 16 columns of P; their sum before V's scales.
-__device__ __forceinline__ float2 weigh_chunk(uint32_t tP, const uint32_t (&x)[32], const float* vs, float sc, float m_use, float2 ls) {
+// The weights of N keys into their N / 2 columns of P; their sum before V's scales.
+template <int N>
+__device__ __forceinline__ float2 weigh_chunk(uint32_t tP, const uint32_t (&x)[N], const float* vs, float sc, float m_use, float2 ls) {
   const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-m_use, -m_use);
-  uint32_t pw[16];
+  uint32_t pw[N / 2];
 #pragma unroll
-  for (int t = 0; t < 16; t += 2) {
+  for (int t = 0; t < N / 2; t += 2) {
     const float4 v4 = *reinterpret_cast<const float4*>(vs + 2 * t);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -609,23 +615,53 @@ __device__ __forceinline__ float2 weigh_chunk(uint32_t tP, const uint32_t (&x)[3
       pw[t + e] = pack16<true>(w.x, w.y);
     }
   }
-  tmem_st16(tP, pw);
+  if constexpr (N == 32) tmem_st16(tP, pw);
+  else tmem_st8(tP, pw);
   return ls;
 }
-// bits(i): the keys of chunk i that the row sees, where a mask is needed.
-template <class Bits>
+// The eight runs of 16 columns from tS on, each on its way from TMEM while f works on
+// the one before it.
+template <class F>
+__device__ __forceinline__ void for_halves(uint32_t tS, F&& f) {
+  uint32_t a[16], b[16];
+  tmem_ld16_issue(tS, a);
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    tmem_ld_wait16(a);
+    tmem_ld16_issue(tS + 16 * i + 16, b);
+    f(a, i);
+    tmem_ld_wait16(b);
+    if (i < 6) tmem_ld16_issue(tS + 16 * i + 32, a);
+    f(b, i + 1);
+  }
+}
+// bits(i): the keys of chunk i that the row sees, where a mask is needed. With two
+// query tiles a softmax thread's own time is what bounds (a tile of 2048 tokens after
+// 16384 751 us rolled, 685 by halves), with one the kernel's size and its registers
+// (64 tokens after up to 8191 keys 181 and 186 us).
+template <int NT, class Bits>
 __device__ __forceinline__ void softmax_held(uint32_t tS, uint32_t tO, float sc, const Scales& scales, bool mask, Bits&& bits, bool few, int quarter,
                                              bool first, float& m_run, float& l_run) {
   uint32_t x[32];
   const int c0 = few ? quarter : 0, c1 = few ? quarter + 1 : 4;
   float top = -INFINITY;
+  if (NT == 2 && !mask) {
+    for_halves(tS, [&](uint32_t (&y)[16], int i) {
+      scale_chunk(y, scales.k + 16 * i);
+      top = fmaxf(top, max_chunk(y));
+      tmem_st16(tS + 16 * i, y);
+    });
+  } else {
 #pragma unroll 1
-  for (int i = c0; i < c1; ++i) {  // rolled, here and below, for the instruction cache
-    tmem_ld32(tS + 32 * i, x);
-    scale_chunk(x, scales.k + 32 * i);
-    if (mask) mask_chunk(x, bits(i));
-    top = fmaxf(top, max_chunk(x));
+    for (int i = c0; i < c1; ++i) {  // rolled, here and below, for the instruction cache
+      tmem_ld32(tS + 32 * i, x);
+      scale_chunk(x, scales.k + 32 * i);
+      if (mask) mask_chunk(x, bits(i));
+      top = fmaxf(top, max_chunk(x));
+      if (!few) tmem_st32(tS + 32 * i, x);
+    }
   }
+  if (!few) tmem_st_wait();
   const float4 vt = *reinterpret_cast<const float4*>(scales.top);
   const float mt = fmaf(top, sc, fmaxf(fmaxf(vt.x, vt.y), fmaxf(vt.z, vt.w)) - kLift<true>);
   float corr = 1.f;
@@ -635,19 +671,19 @@ __device__ __forceinline__ void softmax_held(uint32_t tS, uint32_t tO, float sc,
   }
   const float m_use = m_run == -INFINITY ? 0.f : m_run;
   float2 ls = make_float2(0.f, 0.f);
+  if constexpr (NT == 2) {
+    for_halves(tS, [&](const uint32_t (&y)[16], int i) { ls = weigh_chunk(tS + 8 * i, y, scales.v + 16 * i, sc, m_use, ls); });
+  } else {
 #pragma unroll 1
-  for (int i = c0; i < c1; ++i) {
-    if (!few) {  // else they are still here
-      tmem_ld32(tS + 32 * i, x);
-      scale_chunk(x, scales.k + 32 * i);
-      if (mask) mask_chunk(x, bits(i));
+    for (int i = c0; i < c1; ++i) {
+      if (!few) tmem_ld32(tS + 32 * i, x);  // else they are still here
+      ls = weigh_chunk(tS + 16 * i, x, scales.v + 32 * i, sc, m_use, ls);
     }
-    ls = weigh_chunk(tS + 16 * i, x, scales.v + 32 * i, sc, m_use, ls);
-  }
-  if (few) {
-    const uint32_t none[16] = {};
+    if (few) {
+      const uint32_t none[16] = {};
 #pragma unroll 1
-    for (int i = 1; i < 4; ++i) tmem_st16(tS + 16 * ((quarter + i) & 3), none);
+      for (int i = 1; i < 4; ++i) tmem_st16(tS + 16 * ((quarter + i) & 3), none);
+    }
   }
   l_run = l_run * corr + (ls.x + ls.y);
   if (!first && __any_sync(0xffffffffu, corr != 1.f)) {  // warp-uniform: tcgen05.ld/st are collective
@@ -1082,11 +1118,11 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
       for (int j = static_cast<int>((slot ^ g) & 1); j < steps; j += 2) {
         const int kt = wk.kt0 + (NT == 2 ? j >> 1 : j), j0 = tile_key<EXT>(wk.it, kt);
         const long long gg = g + j;
-        if (!(ok = wait_bar_warp(&bars[L::SFull + slot], (gg >> 1) & 1, abort_flag, budget))) break;
         const int sc_at = NT == 2 ? vc + kt - wk.kt0 : static_cast<int>(gg);  // HELD: the tile, counted by the CTA
-        if constexpr (HELD) {
+        if constexpr (HELD) {  // the scales are there first
           if (!(ok = wait_bar_warp(&bars[L::ScFull + sc_at % L::SS], (sc_at / L::SS) & 1, abort_flag, budget))) break;
         }
+        if (!(ok = wait_bar_warp(&bars[L::SFull + slot], (gg >> 1) & 1, abort_flag, budget))) break;
         const Scales& scales = reinterpret_cast<const Scales*>(sm + L::sc)[HELD ? sc_at % (HELD ? L::SS : 1) : 0];
         // the row's factor: its way into shared memory ends before its warps say that
         // the piece's first scales are there, and the next but one comes after this
@@ -1099,7 +1135,7 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
           bool all = j0 + kTile <= min(open, wk.it.keys);
           if constexpr (EXT) all = all && (c.window == 0 || j0 >= low_last || j0 + kTile <= c.sinks);
           if constexpr (HELD) {
-            softmax_held(tS, tO, row_sc, scales, !all, [&](int i) {
+            softmax_held<NT>(tS, tO, row_sc, scales, !all, [&](int i) {
               uint32_t w = valid ? key_bits<TREE>(j0 + 32 * i, wk.it, t, anc) : 0u;
               if (EXT && c.window > 0) w &= window_bits<TREE>(j0 + 32 * i, low, c.sinks, wk.it.prefix);
               return w;
