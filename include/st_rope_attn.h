@@ -336,7 +336,7 @@ ST_API st_status st_cache_append(const st_tensor* q, const st_tensor* k, const s
  * as c[d] = x[d] / s rounded to nearest even, with s = max |x[d]| / 448 (E4M3) or
  * / 127 (I8): each value is off by at most half a step of what is held. Rows
  * whose s would be below 2^-100 are held as zeros with s = 0; a row with an
- * infinity or NaN has it in its scale and reads as NaN. */
+ * infinity or NaN has NaN as its scale and reads as NaN. */
 ST_API st_status st_cache_append_held(const st_tensor* q, const st_tensor* k, const st_tensor* v, const st_tensor* q_norm_w,
                                       const st_tensor* k_norm_w, float eps, const st_rope* rope, const st_kv_cache* cache,
                                       const st_kv_scales* scales, const st_tensor* lens, const st_tensor* counts,

@@ -84,34 +84,45 @@ __device__ __forceinline__ float2 append_pair(const AppendParams& p, int b, int 
   return cs;
 }
 
+// Largest magnitude of three; NaN where one is.
+__device__ __forceinline__ float top3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 // A row of a cache of 8 bits, eight of its elements per lane of a half-warp: its
 // scale s = max |x| / top and x / s rounded to nearest even, so that each value
-// is off by half a step of the held type. The magnitudes are compared as
-// integers, where NaN stands above infinity and that above every number: a row
-// with one of them gets it as its scale and reads as NaN.
+// is off by half a step of the held type. A row with an infinity or NaN gets NaN as
+// its scale and reads as NaN. int8: x / s + 1.5 2^23 has the rounded quotient in its
+// low byte, in one step (conversions to integers run at a quarter of that rate: with
+// them, two divisions and comparisons of bits 4608 tokens of two samples, 24 + 24 heads,
+// took 101 us, so 96).
 template <int KV>
 __device__ __forceinline__ uint2 hold_row(const float (&y)[8], float* scale) {
-  uint32_t top = 0;
+  float top = top3(top3(y[0], y[1], y[2]), top3(y[3], y[4], y[5]), top3(y[6], y[7], y[7]));
 #pragma unroll
-  for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(y[e]) & 0x7fffffffu);
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const float s = __uint_as_float(top) / top_of(KV);
+  for (int o = 8; o > 0; o >>= 1) {
+    const float t = __shfl_xor_sync(0xffffffffu, top, o);
+    top = top3(top, t, t);
+  }
+  constexpr float kInvTop = 1.f / top_of(KV);
+  const float s = top * kInvTop;
   const bool none = s < kMinScale;
   const float inv = none ? 0.f : 1.f / s;
-  *scale = none ? 0.f : s;
+  *scale = none ? 0.f : (top < INFINITY ? s : NAN);
+  const float2 inv2 = make_float2(inv, inv);
   uint32_t w[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const float *x = y + 4 * i;
+    const float2 x0 = make_float2(y[4 * i], y[4 * i + 1]), x1 = make_float2(y[4 * i + 2], y[4 * i + 3]);
     if constexpr (KV == kDtE4M3) {
+      const float2 a = __fmul2_rn(x0, inv2), b = __fmul2_rn(x1, inv2);
       asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\tmov.b32 %0, {a, b};\n}"
-          : "=r"(w[i]) : "f"(x[0] * inv), "f"(x[1] * inv), "f"(x[2] * inv), "f"(x[3] * inv));
+          : "=r"(w[i]) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     } else {
-      uint32_t v[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = static_cast<uint32_t>(__float2int_rn(x[e] * inv));
-      w[i] = __byte_perm(__byte_perm(v[0], v[1], 0x0040), __byte_perm(v[2], v[3], 0x0040), 0x5410);
+      const float2 magic = make_float2(12582912.f, 12582912.f), a = __ffma2_rn(x0, inv2, magic), b = __ffma2_rn(x1, inv2, magic);
+      w[i] = __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
+                         __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
     }
   }
   return make_uint2(w[0], w[1]);
@@ -120,8 +131,12 @@ __device__ __forceinline__ uint2 hold_row(const float (&y)[8], float* scale) {
 // SRC: type of q and k; DST: of v, q' and (KV = 0) the cache; KV: kDtE4M3 or
 // kDtI8, a cache of that type. u_q, u_k: units of a token's q rows, and of its k
 // (and v) rows.
+// Over 8 bits the registers are held down to those of the 16-bit forms, 28 warps an
+// SM from fp32 rows and 36 from 16-bit ones, for the loads in flight (24 and 28 warps:
+// 96 us against 91 for the prompts above in int8; 32 and 40, with spills in the
+// stream: 96).
 template <int NI, int SRC, int DST, int KV>
-__global__ void __launch_bounds__(kAppWarps * 32) append_kernel(const __grid_constant__ AppendParams p, int u_q, int u_k) {
+__global__ void __launch_bounds__(kAppWarps * 32, KV == 0 ? 0 : (SRC == kDtF32 ? 7 : 9)) append_kernel(const __grid_constant__ AppendParams p, int u_q, int u_k) {
   __shared__ float4 tab[kAppWarps][kPairs / 2];
   grid_dependency_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
