@@ -94,7 +94,11 @@ struct Lay {  // shared memory, offsets from a 1024-byte aligned base
   // thread waits for every phase of the stages that it uses, and a wait on
   // parity says nothing where phases went by unseen.
   static constexpr int KS = NT == 1 || HELD ? 2 : 3, VS = NT == 1 && !HELD ? 4 : 2;
-  static constexpr int SS = HELD ? 4 : 0;                   // stages of scales (NT = 1: of one slot, as above)
+  // Stages of scales. Nothing says when one is free: those of tile n + 2 (NT = 2: n + 1)
+  // are fetched while tile n is converted, whose place was free after the scores of
+  // n - 2 (K; V: the products of n - 2), which were issued after the products of n - 4
+  // (n - 3), whose weights were there. So 6 (4) do; NT = 1 takes a power of two.
+  static constexpr int SS = HELD ? (NT == 1 ? 8 : 4) : 0;
   // stages of bytes, of K and of V each, and their keys: 48 KB where reading bounds
   static constexpr int RS = HELD ? 3 : 0, kRawRows = NT == 1 ? 64 : 32;
   static constexpr uint32_t kRawBytes = kRawRows * kD;
@@ -107,7 +111,7 @@ struct Lay {  // shared memory, offsets from a 1024-byte aligned base
   static constexpr uint32_t qs = lens + (HELD ? 144 : 0);  // HELD: [2][NT][128] the rows' factors, by the parity of the piece
   static constexpr uint32_t bytes = qs + (HELD ? 2 * NT * 128 * 4 : 0);
   enum { QFull = 0, QEmpty, KFull, KEmpty = KFull + KS, VFull = KEmpty + KS, VEmpty = VFull + VS, SFull = VEmpty + VS,
-         PFull = SFull + 2, OFull = PFull + 2, MlFull, ORead = MlFull + 2, Drain = ORead + 2, ScFull = Drain + 2, ScEmpty = ScFull + SS, Num = ScEmpty + SS };
+         PFull = SFull + 2, OFull = PFull + 2, MlFull, ORead = MlFull + 2, Drain = ORead + 2, ScFull = Drain + 2, Num = ScFull + SS };
 };
 static_assert(Lay<1>::bytes <= 232448 && Lay<2>::bytes <= 232448, "shared memory");
 static_assert(Lay<1, true>::bytes <= 232448 && Lay<2, true>::bytes <= 232448, "shared memory");
@@ -938,10 +942,7 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
     mbar_init(&bars[L::QFull], kQWarps * 32);
     mbar_init(&bars[L::QEmpty], 2);
     if constexpr (HELD)
-      for (int s = 0; s < L::SS; ++s) {
-        mbar_init(&bars[L::ScFull + s], 2 * kQWarps);
-        mbar_init(&bars[L::ScEmpty + s], 4 * NT);  // NT = 1: a slot's own
-      }
+      for (int s = 0; s < L::SS; ++s) mbar_init(&bars[L::ScFull + s], 2 * kQWarps);
     for (int s = 0; s < L::KS; ++s) {
       mbar_init(&bars[L::KFull + s], HELD ? kQWarps * 32 : 1);
       mbar_init(&bars[L::KEmpty + s], NT);  // NT = 1: a tile is one slot's
@@ -1154,10 +1155,6 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
           }
         }
         first = false;
-        if constexpr (HELD) {
-          __syncwarp();
-          if (lane_id == 0) mbar_arrive(&bars[L::ScEmpty + sc_at % L::SS]);
-        }
         if (!HELD && (j0 + kTile > wk.it.keys || (EXT && j0 < wk.it.low && j0 + kTile > c.sinks))) {
           // rows of V behind the last key (or before every window) hold anything:
           // zero weights do not silence infinities and NaN, zeros do (with NT = 2
@@ -1321,7 +1318,7 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
       int i_tile = 0;
       bool i_have = false;
       uint32_t off = kNowhere;  // of the lane's row
-      auto fetch = [&](int i_part, uint8_t* dst) -> bool {
+      auto fetch = [&](int i_part, uint8_t* dst) {
         if (i_part == 0) {
           i_have = there;
           if (there) {
@@ -1336,7 +1333,6 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
             there = l_have;
             if (there) look();
             const int st = i_tile % L::SS;
-            if (i_tile >= L::SS && !wait_bar_warp(&bars[L::ScEmpty + st], ((i_tile / L::SS) - 1) & 1, abort_flag, budget)) return false;
             Scales& s = reinterpret_cast<Scales*>(sm + L::sc)[st];
             cp_async4(is_v ? &s.v[my_row] : &s.k[my_row], sc_base + sc_at, off != kNowhere);
             ++i_tile;
@@ -1350,7 +1346,6 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
           for (int u = 0; u < kU; ++u) cp_async16(dst + u * 2048, base + (o[u] == kNowhere ? 0u : o[u]) * static_cast<uint64_t>(16), o[u] != kNowhere);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-        return true;
       };
       // ---- the conversion. Columns 16 cg .. + 16 are chunks 2 cg and 2 cg + 1; rows
       // r0 + 16 u have the swizzle of r0.
@@ -1358,7 +1353,7 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
       bool ok = true, have = next_piece(wk, all_lanes, false);
       int kt = wk.kt0, n = 0, slot = 0;
 #pragma unroll
-      for (int i = 0; i < L::RS; ++i) fetch(i % kParts, raw + i * L::kRawBytes);  // fewer tiles than SS: no wait
+      for (int i = 0; i < L::RS; ++i) fetch(i % kParts, raw + i * L::kRawBytes);
 #pragma unroll 1
       while (ok && have) {
         if (!is_v && kt == wk.kt0) {
@@ -1383,7 +1378,7 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
             if (is_v) {
               const float v = fabsf(s.v[my_row]);
               const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, v == v ? __float_as_uint(v) : 0u));
-              if (lane_id == 0) s.top[gw] = fminf(fmaxf(log2f(top), -kTopRange), kTopRange);
+              if (lane_id == 0) s.top[gw] = fminf(fmaxf(__log2f(top), -kTopRange), kTopRange);  // any number near it does
             }
             __syncwarp();
             if (lane_id == 0) mbar_arrive(&bars[L::ScFull + st]);
@@ -1403,7 +1398,7 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
             *reinterpret_cast<uint4*>(dst + at0 + (part * kU + u) * 16 * 128) = a;
             *reinterpret_cast<uint4*>(dst + at1 + (part * kU + u) * 16 * 128) = b;
           }
-          if (!(ok = fetch((part + L::RS) % kParts, src))) break;  // into the stage that has just been read, by this thread
+          fetch((part + L::RS) % kParts, src);  // into the stage that has just been read, by this thread
           slot = slot == L::RS - 1 ? 0 : slot + 1;
         }
         if (!ok) break;
