@@ -1297,22 +1297,28 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
       // of the fetch, and has that row's scale.
       const int my_row = 4 * gw + (lane_id & 3) + 16 * (lane_id >> 2);
       Walk<EXT> wl = wk;
-      bool l_have = next_piece(wl, all_lanes, true), l_in = false;
-      int lt = wl.kt0, l_pg = 0, l_row = 0, l_h = 0;
-      auto look = [&]() {  // the next tile
-        const int j = tile_key<EXT>(wl.it, lt) + my_row;
-        l_in = j < wl.it.keys && (!EXT || j >= wl.it.low || j < c.sinks);  // (keys lie within the table)
-        l_h = wl.ph;
-        if (l_in) {
-          const int page = kv.page_shift >= 0 ? j >> kv.page_shift : j / kv.page;
-          l_row = j - page * kv.page;
-          l_pg = ld_now(kv.pages + (EXT && wl.pb < 0 ? pre_b : wl.pb) * kv.p_sb + page);
-        }
-        if (++lt == wl.kt1) {
-          l_have = next_piece(wl, all_lanes, true);
-          lt = wl.kt0;
-        }
+      bool l_have = false, l_in = false;
+      int lt = 0, l_left = 0, l_pg = 0;
+      uint32_t l_off = 0, l_sc = 0;  // the row's place in its page
+      const int32_t* l_pages = nullptr;
+      auto look_on = [&]() {  // the next piece
+        l_have = next_piece(wl, all_lanes, true);
+        lt = wl.kt0;
+        l_left = wl.kt1 - wl.kt0;
+        l_pages = kv.pages + (EXT && wl.pb < 0 ? pre_b : wl.pb) * kv.p_sb;
       };
+      auto look = [&]() {  // the next tile
+        const int j = tile_key<EXT>(wl.it, lt++) + my_row;
+        l_in = j < wl.it.keys && (!EXT || j >= wl.it.low || j < c.sinks);  // (keys lie within the table)
+        if (l_in) {
+          const int page = kv.page_shift >= 0 ? j >> kv.page_shift : j / kv.page, row = j - page * kv.page;
+          l_pg = ld_now(l_pages + page);
+          l_off = row * at.sr + wl.ph * at.sh;
+          l_sc = row + wl.ph * at.sc_sh;
+        }
+        if (--l_left == 0) look_on();
+      };
+      look_on();
       bool there = l_have;  // a tile was looked up
       if (there) look();
       int i_tile = 0;
@@ -1327,8 +1333,8 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
             if (l_in && static_cast<unsigned>(l_pg) >= static_cast<unsigned>(kv.n_pages)) {
               atomicOr(c.status, kStatusIndex);  // reads as zeros
             } else if (l_in) {
-              off = l_pg * at.sp + l_row * at.sr + l_h * at.sh;
-              sc_at = l_pg * at.sc_sp + l_h * at.sc_sh + l_row;
+              off = l_pg * at.sp + l_off;
+              sc_at = l_pg * at.sc_sp + l_sc;
             }
             there = l_have;
             if (there) look();
@@ -1350,22 +1356,26 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
       // ---- the conversion. Columns 16 cg .. + 16 are chunks 2 cg and 2 cg + 1; rows
       // r0 + 16 u have the swizzle of r0.
       const uint32_t at0 = half * kHalfBytes + sw128_off(r0, 2 * (lane_id & 3)), at1 = half * kHalfBytes + sw128_off(r0, 2 * (lane_id & 3) + 1);
-      bool ok = true, have = next_piece(wk, all_lanes, false);
-      int kt = wk.kt0, n = 0, slot = 0;
+      bool ok = true;
+      int left = 0, n = 0, slot = 0;  // left: tiles of the present piece
 #pragma unroll
       for (int i = 0; i < L::RS; ++i) fetch(i % kParts, raw + i * L::kRawBytes);
 #pragma unroll 1
-      while (ok && have) {
-        if (!is_v && kt == wk.kt0) {
-          // a new piece: its rows, once the last one's scores are done
-          const bool q_few = NT == 1 && P.few && wk.pb >= 0;
-          float* qs = reinterpret_cast<float*>(sm + L::qs) + (n_piece & 1) * NT * 128;
-          if (!load_q_held<NT, F16, EXT, kQWarps * 32>(P, wk, sm + L::q, qs, qt, q_few, [&]() -> bool {
-                return n_piece == 0 || wait_bar_warp(&bars[L::QEmpty], (n_piece - 1) & 1, abort_flag, budget);
-              }))
-            break;
-          mbar_arrive(&bars[L::QFull]);
-          ++n_piece;
+      while (ok) {
+        if (left == 0) {
+          if (!next_piece(wk, all_lanes, false)) break;
+          left = wk.kt1 - wk.kt0;
+          if (!is_v) {
+            // its rows, once the last one's scores are done
+            const bool q_few = NT == 1 && P.few && wk.pb >= 0;
+            float* qs = reinterpret_cast<float*>(sm + L::qs) + (n_piece & 1) * NT * 128;
+            if (!load_q_held<NT, F16, EXT, kQWarps * 32>(P, wk, sm + L::q, qs, qt, q_few, [&]() -> bool {
+                  return n_piece == 0 || wait_bar_warp(&bars[L::QEmpty], (n_piece - 1) & 1, abort_flag, budget);
+                }))
+              break;
+            mbar_arrive(&bars[L::QFull]);
+            ++n_piece;
+          }
         }
         const int op = n % L::KS;
         uint8_t* dst = tiles + op * kTileBytes;
@@ -1405,10 +1415,7 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
         fence_proxy_async_smem();
         mbar_arrive(&full[op]);
         ++n;
-        if (++kt == wk.kt1) {
-          have = next_piece(wk, all_lanes, false);
-          kt = wk.kt0;
-        }
+        --left;
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
