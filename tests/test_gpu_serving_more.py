@@ -249,7 +249,8 @@ ATTEND = [
     ("fp16", "e4m3", 2, 40, 8, 2, [0, 200], [40, 13], 8, False, 0, 0),
     ("bf16", "e4m3", 2, 61, 14, 2, [77, 900], [61, 50], 64, True, 0, 0),
     ("fp16", "int8", 1, 150, 4, 4, [33], None, 128, True, 0, 0),
-    ("bf16", "int8", 5, 3, 7, 7, [1, 2, 3, 4, 5], None, 7, True, 0, 0),   # CUDA cores
+    ("bf16", "int8", 5, 3, 7, 7, [1, 2, 3, 4, 5], None, 7, True, 0, 0),
+    ("bf16", "e4m3", 2, 3, 4, 2, [300, 7], None, 1, False, 0, 0),
     ("fp32", "e4m3", 2, 5, 6, 2, [0, 333], [5, 4], 16, False, 0, 0),
     ("fp32", "int8", 2, 9, 4, 1, [100, 65], None, 5, True, 0, 0),
     ("bf16", "bf16", 2, 1, 8, 2, [700, 40], None, 16, False, 100, 0),
@@ -275,6 +276,11 @@ ATTEND = [
     ("bf16", "int8", 60, 32, 16, 4, [(37 * i) % 500 for i in range(60)], None, 64, True, 0, 0),
     ("fp16", "e4m3", 60, 32, 16, 4, [(37 * i) % 400 for i in range(60)], None, 16, False, 0, 0),
     ("fp16", "int8", 50, 70, 8, 4, [(53 * i) % 300 for i in range(50)], None, 32, False, 90, 9),
+    # many tiles of one sequence for each CTA: few rows, one query tile, two
+    ("bf16", "e4m3", 3, 1, 16, 8, [60000, 33333, 50001], None, 16, False, 0, 0),
+    ("fp16", "int8", 2, 12, 16, 4, [70000, 60003], None, 48, False, 0, 0),
+    ("bf16", "int8", 1, 100, 16, 8, [50000], None, 64, False, 0, 0),
+    ("fp16", "e4m3", 1, 70, 16, 8, [60000], None, 64, True, 30000, 200),
 ]
 
 
