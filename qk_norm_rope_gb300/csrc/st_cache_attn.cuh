@@ -206,7 +206,20 @@ __device__ __forceinline__ int tile_key(const Item& it, int kt) {
   return (EXT && kt >= it.lead ? kt + it.gap : kt) * kTile;
 }
 
-// A CTA's walk over its range: pieces of items.
+// What an item costs beyond its key tiles, in tiles: its rows' way in and its results'
+// way out hold the pipeline up. The deal goes by the sum, so that no CTA gets the
+// short items of many sequences while another has one long one. Measured from 0 to 10:
+// 22 trees of 40 nodes, 41 keys of their own each after 7349 shared tokens in bf16
+// 263 us with 0, 141 with 2 to 4, 148 with 7; 64 tokens after up to 8191 keys in e4m3
+// 167, 160 with 4, 163 with 7; 64 tokens, 1000 keys of their own after 16384 shared ones
+// in bf16 96, 86 with 2 and 3, 101 with 7, in e4m3 101, 107 with 2, 121 with 4 (a tile
+// of the prefix has 128 rows and takes longer there than one of a single token's).
+// The plain 16-bit forms, older, are dealt by tiles alone.
+template <int NT, bool CL, int KV, bool EXT>
+constexpr int kItemCost = CL || (KV == 0 && !EXT) ? 0 : (NT == 2 || !EXT ? 4 : (KV == 0 ? 3 : 2));
+
+// A CTA's walk over its range: pieces of items. An item's range is its cost and then
+// its tiles.
 template <bool EXT>
 struct Walk {
   int h, b, m, off;
@@ -235,7 +248,7 @@ struct Walk {
     kt1 = t1;
   }
   template <bool ONE>
-  __device__ __forceinline__ bool next(const TcAttnParams& p, int nt, const Lens* lens = nullptr) {
+  __device__ __forceinline__ bool next(const TcAttnParams& p, int nt, int cost, const Lens* lens = nullptr) {
     if (left <= 0) return false;
     if constexpr (ONE) {
       left = 0;
@@ -248,7 +261,7 @@ struct Walk {
         if (i < 0) i += p.c.B;
       }
       it = i < kLens ? item_from<EXT>(p, nt, m, p0, lens->len[i], lens->cnt[i]) : item_of<EXT>(p, nt, b, m, p0);
-      if (off < it.n) break;
+      if (it.n > 0 && off < it.n + cost) break;
       advance(p);
       if (h >= p.c.kv.Hkv) {  // lengths that changed under the kernel: no tiles are left
         left = 0;
@@ -258,12 +271,13 @@ struct Walk {
     ph = h;
     pb = b;
     pm = m;
-    kt0 = off;
-    kt1 = static_cast<int>(min(static_cast<long long>(it.n), off + left));
-    left -= kt1 - kt0;
-    off = kt1;
-    if (off == it.n) advance(p);
-    return true;
+    const int end = static_cast<int>(min(static_cast<long long>(it.n) + cost, off + left));
+    kt0 = max(off - cost, 0);
+    kt1 = end - cost;
+    left -= end - off;
+    off = end;
+    if (off == it.n + cost) advance(p);
+    return kt1 > kt0;  // else the range ends before the item's first tile
   }
   __device__ __forceinline__ bool whole() const { return kt0 == 0 && kt1 == it.n; }
   // HELD: what the walk goes on from lies in shared memory between pieces, and the
@@ -289,7 +303,7 @@ struct Walk {
 // not hold: every role was held up by its own instructions (64 tokens after up to
 // 8191 keys in e4m3 253 us).
 template <bool EXT>
-__device__ __noinline__ bool next_piece_of(const TcAttnParams& p, int nt, typename Walk<EXT>::Place* at, const Lens* lens) {
+__device__ __noinline__ bool next_piece_of(const TcAttnParams& p, int nt, int cost, typename Walk<EXT>::Place* at, const Lens* lens) {
   Walk<EXT> w;
   w.h = at->h;
   w.b = at->b;
@@ -297,13 +311,13 @@ __device__ __noinline__ bool next_piece_of(const TcAttnParams& p, int nt, typena
   w.off = at->off;
   w.left = at->left;
   w.p0 = at->p0;
-  if (!w.template next<false>(p, nt, lens)) return false;
+  if (!w.template next<false>(p, nt, cost, lens)) return false;
   *at = {w.h, w.b, w.m, w.off, w.left, w.p0, w.ph, w.pb, w.pm, w.kt0, w.kt1, w.it};
   return true;
 }
 
-// The deal: CTA x has the tiles [first(x), first(x + 1)) of the call's, shares
-// that differ by one at most. 32-bit division where the numbers allow it.
+// The deal: CTA x has [first(x), first(x + 1)) of the call's tiles (and items' costs),
+// shares that differ by one at most. 32-bit division where the numbers allow it.
 struct Deal {
   long long total, share;
   int ctas, extra;
@@ -329,7 +343,7 @@ struct Start {  // found by the block, read by every role
   int h, b, m, off;
   long long left;
   int p0, pre_b;           // EXT: tiles of the shared prefix, the sequence whose pages hold it
-  long long first, total;  // joined by items: the range's first tile, the call's tiles
+  long long first, total;  // joined by items: where the range begins, the call's sum
 };
 
 // The shared prefix: whole tiles of what the least of the sequences that have
@@ -367,7 +381,7 @@ __device__ __forceinline__ void find_shared(const TcAttnParams& p, int* scratch,
 // (sequence, group) pairs (the shared prefix's groups first), a block scan places
 // the runs.
 template <bool EXT, int W, bool ITEMS>  // ITEMS: the call may join by items
-__device__ __forceinline__ void find_start(const TcAttnParams& p, int nt, long long* scan, Start* st) {
+__device__ __forceinline__ void find_start(const TcAttnParams& p, int nt, int cost, long long* scan, Start* st) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int p0 = 0;
   if constexpr (EXT) {
@@ -389,7 +403,7 @@ __device__ __forceinline__ void find_start(const TcAttnParams& p, int nt, long l
   long long sum = 0;
   for (int e = lo, b = b0, m = m0; e < hi; ++e) {
     const Item it = item_of<EXT>(p, nt, b, m, p0);
-    sum += it.n;
+    sum += it.n > 0 ? it.n + cost : 0;
     if (m == 0 && b >= 0 && blockIdx.x == 0 && (ld_now(p.c.lens + b) < 0 || static_cast<int64_t>(ld_now(p.c.lens + b)) + it.cnt > it.keys))
       atomicOr(p.c.status, kStatusIndex);
     if (++m == (EXT && b < 0 ? pre : p.n_groups)) {
@@ -427,7 +441,8 @@ __device__ __forceinline__ void find_start(const TcAttnParams& p, int nt, long l
     if (rem >= 0 && rem < sum) {  // one thread
       for (int e = lo, b = b0, m = m0; e < hi; ++e) {
         const Item it = item_of<EXT>(p, nt, b, m, p0);
-        if (rem < it.n) {
+        const int all = it.n > 0 ? it.n + cost : 0;
+        if (rem < all) {
           st->h = h;
           st->b = b;
           st->m = m;
@@ -438,14 +453,14 @@ __device__ __forceinline__ void find_start(const TcAttnParams& p, int nt, long l
           // who has the item's tiles?
           JoinMeta meta{0, 0, h, b, m, it.cnt};
           const long long item = s0 - rem;
-          if (rem > 0 && d.first(blockIdx.x - 1) <= item) {
-            meta.parts = d.holder(item + it.n - 1) - static_cast<int>(blockIdx.x) + 2;
-            meta.slot0 = 2 * (static_cast<int>(blockIdx.x) - 1) + (d.first(blockIdx.x - 1) == item ? 0 : 1);
+          if (rem > cost && d.first(blockIdx.x - 1) <= item + cost) {
+            meta.parts = d.holder(item + all - 1) - static_cast<int>(blockIdx.x) + 2;
+            meta.slot0 = 2 * (static_cast<int>(blockIdx.x) - 1) + (d.first(blockIdx.x - 1) >= item ? 0 : 1);
           }
           p.meta[blockIdx.x] = meta;
           break;
         }
-        rem -= it.n;
+        rem -= all;
         if (++m == (EXT && b < 0 ? pre : p.n_groups)) {
           m = 0;
           ++b;
@@ -918,6 +933,7 @@ template <int NT, bool F16, bool TREE, bool CL, int KV, bool EXT>
 __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const __grid_constant__ TcAttnParams P) {
   constexpr bool HELD = KV != 0, OP16 = F16 || HELD;  // fp16 operands
   using L = Lay<NT, HELD>;
+  constexpr int kCost = kItemCost<NT, CL, KV, EXT>;
   constexpr int kWarpMma = Roles<HELD>::kWarpMma, kWarpK = Roles<HELD>::kWarpK, kWarpV = Roles<HELD>::kWarpV, kTcWarps = Roles<HELD>::kWarps;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw;
@@ -990,7 +1006,7 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
       atomicOr(c.status, kStatusIndex);
   } else {
     // the scan's scratch lies in the Q tile, which is written later
-    find_start<EXT, kTcWarps, EXT || HELD>(P, NT, reinterpret_cast<long long*>(sm + L::q), start);
+    find_start<EXT, kTcWarps, EXT || HELD>(P, NT, kCost, reinterpret_cast<long long*>(sm + L::q), start);
     wk.h = start->h;
     wk.b = start->b;
     wk.m = start->m;
@@ -1032,15 +1048,15 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
       bool more = false;
       if constexpr (decltype(warp_wide)::value) {
         __syncwarp();  // every lane has what it wants of the last piece
-        if (lane_id == 0) more = next_piece_of<EXT>(P, NT, at, lens);
+        if (lane_id == 0) more = next_piece_of<EXT>(P, NT, kCost, at, lens);
         more = __shfl_sync(0xffffffffu, more, 0);
       } else {
-        more = next_piece_of<EXT>(P, NT, at, lens);
+        more = next_piece_of<EXT>(P, NT, kCost, at, lens);
       }
       if (more) w.take(at);
       return more;
     } else {
-      return w.template next<CL>(P, NT);
+      return w.template next<CL>(P, NT, kCost);
     }
   };
   constexpr std::true_type all_lanes;
@@ -1076,7 +1092,7 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
     int vc = 0;         // key tiles before the present piece
     int n_piece = 0;
     bool ok = true, at_start = true;
-    long long tile_at = by_items ? start->first : 0;  // of the call's
+    const long long range_end = by_items ? start->first + start->left : 0;
     while (ok && next_piece(wk, all_lanes, false)) {
       const int steps = (wk.kt1 - wk.kt0) * NT;
       const bool few = call_few && wk.pb >= 0;
@@ -1181,11 +1197,11 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
           if (tid == 0 && wk.kt0 == 0) {
             Deal d;
             d.make(start->total, P.ctas);
+            // where the item ends: as far behind the piece as it has tiles behind it
+            const long long end = range_end - (HELD ? place->left : wk.left) + wk.it.n - wk.kt1;
             P.item_meta[item_index(P, wk.ph, wk.pb, wk.pm)] =
-                wk.whole() ? make_int2(1, -1)
-                           : make_int2(d.holder(tile_at + wk.it.n - 1) - static_cast<int>(blockIdx.x) + 1, static_cast<int>(pslot));
+                wk.whole() ? make_int2(1, -1) : make_int2(d.holder(end - 1) - static_cast<int>(blockIdx.x) + 1, static_cast<int>(pslot));
           }
-          tile_at += wk.kt1 - wk.kt0;
         }
       }
       if (!(ok = wait_bar_warp(&bars[L::OFull], n_piece & 1, abort_flag, budget))) break;
@@ -1419,7 +1435,7 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
-      while (wk.template next<CL>(P, NT)) {
+      while (wk.template next<CL>(P, NT, kCost)) {
         if (n_piece > 0 && !wait_bar_warp(&bars[L::QEmpty], (n_piece - 1) & 1, abort_flag, budget)) break;
         load_q<NT, EXT, kQWarps * 32>(P, wk, sm + L::q, qt);
         mbar_arrive(&bars[L::QFull]);
@@ -1440,7 +1456,7 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
       const int half = lane_id >> (7 - P.box_shift), x = half * 64;  // a lane per box: two halves of 128 / box
       const uint32_t dst = half * kHalfBytes + ((lane_id & ((kTile >> P.box_shift) - 1)) << P.box_shift) * 128;
       int n = 0;
-      bool ok = true, have = wk.template next<CL>(P, NT);
+      bool ok = true, have = wk.template next<CL>(P, NT, kCost);
       int kt = wk.kt0;
       Box box{false, 0, 0};
       if (have) box = find_box<EXT>(P, wk, kt, lane_id, pre_b);
@@ -1454,7 +1470,7 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
           tma_load_4d(ring + st * kTileBytes + dst, map, &full[st], x, r_first ? box.row : wk.ph, r_first ? wk.ph : box.row, box.pg);
         // the next tile's pages are looked up while its stage is in use
         if (++kt == wk.kt1) {
-          have = wk.template next<CL>(P, NT);
+          have = wk.template next<CL>(P, NT, kCost);
           kt = wk.kt0;
         }
         if (have) box = find_box<EXT>(P, wk, kt, lane_id, pre_b);
