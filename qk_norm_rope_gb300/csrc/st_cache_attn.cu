@@ -84,8 +84,21 @@ __global__ void __launch_bounds__(256) join_items_kernel(const __grid_constant__
   if (row >= static_cast<int64_t>(c.B) * c.T * c.H) return;  // with W = 8 these hold for the whole block
   const int64_t tok = row / c.H;  // at most 2^30
   const int hq = static_cast<int>(row - tok * c.H), b = static_cast<int>(tok / c.T), t = static_cast<int>(tok - static_cast<int64_t>(b) * c.T);
-  if (t >= row_count(c.counts, b, c.T)) return;  // the attention kernel wrote it
-  const int h = hq / c.group, g = hq - h * c.group, tpg = P.tpt * nt, p0 = c.shared ? ld_now(P.p0) : 0;
+  const int h = hq / c.group, g = hq - h * c.group, tpg = P.tpt * nt, im = t / tpg, pm = static_cast<int>(tok / tpg);
+  // everything that says where the parts are in one round trip
+  const int cnt = row_count(c.counts, b, c.T), len = ld_now(c.lens + b), p0 = c.shared ? ld_now(P.p0) : 0;
+  const int2 own = P.item_meta[item_index(P, h, b, im)], pre = c.shared ? P.item_meta[item_index(P, h, -1, pm)] : make_int2(0, 0);
+  if (t >= cnt) return;  // the attention kernel wrote it
+  // the prefix's parts come first, then those of the row's own keys (no tiles: what is
+  // said of them is of another call)
+  const int copies = P.few ? 4 : 1, n_pre = p0 > 0 ? pre.x : 0;
+  const int n = n_pre + (item_from<true>(P, nt, im, p0, len, cnt).n > 0 ? own.x * copies : 0);
+  auto place = [&](const int2& meta, int m, int ib, int i, int copy, int r) {
+    const int64_t first = meta.y < 0 ? whole_part(P, h, ib, m) : static_cast<int64_t>(meta.y) * P.split_rows;
+    return (i == 0 ? first : 2 * (static_cast<int64_t>(meta.y >> 1) + i) * P.split_rows) + copy * P.part_rows + r;
+  };
+  // rows in their items: tiles of tpt tokens follow one another without gaps
+  const int own_r = (t - im * tpg) * c.group + g, pre_r = (static_cast<int>(tok) - pm * tpg) * c.group + g;
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   auto merge = [&](const float2 (&x)[4], const float4 (&y)[4]) {
@@ -101,29 +114,19 @@ __global__ void __launch_bounds__(256) join_items_kernel(const __grid_constant__
       o = make_float4(fmaf(f, y[u].x, o.x), fmaf(f, y[u].y, o.y), fmaf(f, y[u].z, o.z), fmaf(f, y[u].w, o.w));
     }
   };
-#pragma unroll 1
-  for (int which = p0 > 0 ? 0 : 1; which < 2; ++which) {
-    const int ib = which == 0 ? -1 : b, at = which == 0 ? static_cast<int>(tok) : t, im = at / tpg;
-    if (item_of<true>(P, nt, ib, im, p0).n == 0) continue;
-    const int in = at - im * tpg, r = in * c.group + g;  // tiles of tpt tokens follow one another without gaps
-    const int copies = P.few && which == 1 ? 4 : 1;
-    const int2 meta = P.item_meta[item_index(P, h, ib, im)];
-    const int64_t first = meta.y < 0 ? whole_part(P, h, ib, im) : static_cast<int64_t>(meta.y) * P.split_rows;
-    const int64_t cta = meta.y >> 1;
-    const int n = meta.x * copies;
-    for (int i0 = 4 * part; i0 < n; i0 += 4 * W) {
-      float2 x[4];
-      float4 y[4];
+  for (int i0 = 4 * part; i0 < n; i0 += 4 * W) {
+    float2 x[4];
+    float4 y[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int v = min(i0 + u, n - 1), i = copies == 4 ? v >> 2 : v, copy = copies == 4 ? v & 3 : 0;
-        const int64_t at_row = (i == 0 ? first : 2 * (cta + i) * P.split_rows) + copy * P.part_rows + r;
-        x[u] = P.part_ml[at_row];
-        y[u] = reinterpret_cast<const float4*>(c.part + at_row * kD)[lane];
-        if (i0 + u >= n) x[u] = make_float2(-INFINITY, 0.f);
-      }
-      merge(x, y);
+    for (int u = 0; u < 4; ++u) {
+      const int v = min(i0 + u, n - 1), w = v - n_pre;
+      const int64_t at = w < 0 ? place(pre, pm, -1, v, 0, pre_r)
+                               : place(own, im, b, copies == 4 ? w >> 2 : w, copies == 4 ? w & 3 : 0, own_r);
+      x[u] = P.part_ml[at];
+      y[u] = reinterpret_cast<const float4*>(c.part + at * kD)[lane];
+      if (i0 + u >= n) x[u] = make_float2(-INFINITY, 0.f);
     }
+    merge(x, y);
   }
   if constexpr (W > 1) {
     so[warp][lane] = o;
