@@ -162,10 +162,10 @@ cudaError_t launch_cache_attn_tc(const TcAttnParams& p, int nt, bool f16, cudaSt
 cudaError_t launch_cache_attn_join(const TcAttnParams& p, int nt, cudaStream_t stream) {
   if (p.item_meta) {
     const int64_t rows = static_cast<int64_t>(p.c.B) * p.c.T * p.c.H;
-    // eight warps a row where the rows' blocks then run at once (one token of 8 K/V
-    // heads after 240000 keys 22 us with one warp and 10 with eight, 512 rows 11.7 and
-    // 9.7, 1152 rows 12.2 and 12.4, 4608 rows 12 and 31)
-    const int warps = rows <= 1024 ? 8 : 1;
+    // eight warps a row where all blocks then run at once and have several parts each
+    // (one token of 8 K/V heads after 240000 keys 25 us with one warp and 10 with eight,
+    // 512 rows 10.6 and 8.7, 1024 rows 9.4 and 11.8, 4608 rows 10 and 25)
+    const int warps = rows <= 768 ? 8 : 1;
     return launch_chained(warps == 8 ? join_items_kernel<8> : join_items_kernel<1>, dim3(static_cast<unsigned>((rows * warps + 7) / 8)), dim3(256),
                           0, stream, p, nt);
   }

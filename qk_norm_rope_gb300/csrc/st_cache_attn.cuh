@@ -587,7 +587,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float sc,
 // alike are in its units. There are no registers for a row of 128 scores: they go back
 // to TMEM, scaled and masked, while the maximum is found, and come again for the
 // weights, which take the place of scores that have been read. (Scaled and masked a
-// second time instead, 2048 tokens after 16384 took 926 us over e4m3, now 751: the
+// second time instead 2048 tokens after 16384 took 926 us over e4m3, so 755: the
 // reads of the scales from shared memory stand in line with the MMAs' operands.)
 template <int N>
 __device__ __forceinline__ void scale_chunk(uint32_t (&x)[N], const float* ks) {
@@ -655,9 +655,10 @@ __device__ __forceinline__ void for_halves(uint32_t tS, F&& f) {
   }
 }
 // bits(i): the keys of chunk i that the row sees, where a mask is needed. With two
-// query tiles a softmax thread's own time is what bounds (a tile of 2048 tokens after
-// 16384 751 us rolled, 685 by halves), with one the kernel's size and its registers
-// (64 tokens after up to 8191 keys 181 and 186 us).
+// query tiles a softmax thread's own time is what bounds (2048 tokens after 16384
+// 755 us rolled, 689 by halves), with one the kernel's size and its registers (64
+// tokens after up to 8191 keys 181 and 186 us, by halves in both passes several times
+// that).
 template <int NT, class Bits>
 __device__ __forceinline__ void softmax_held(uint32_t tS, uint32_t tO, float sc, const Scales& scales, bool mask, Bits&& bits, bool few, int quarter,
                                              bool first, float& m_run, float& l_run) {
@@ -753,13 +754,6 @@ __device__ __forceinline__ void held_f16(uint32_t w, uint32_t& lo, uint32_t& hi)
   }
 }
 
-// 32 bytes of a thread in one store: a thread per row writes whole sectors, in
-// half as many instructions of 32 sectors each as with 16-byte stores.
-__device__ __forceinline__ void st_v8(void* p, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
-               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
 // Columns [32 q4, 32 q4 + 32) of a row: fp32 into a part, or 16 bits into the
 // result (`wide`: its rows start on 32 bytes).
 __device__ __forceinline__ void store_part32(float* row, int q4, const float (&y)[32]) {

@@ -196,12 +196,13 @@ st_status plan_attn(const st_tensor* q, const st_kv_cache* cache, const st_cache
     TcAttnParams& t = P->tc;
     P->nt = tc_tiles(p.T, p.group);
     // A shared prefix's rows are the whole batch's: two tiles of them for each K/V
-    // tile, unless that leaves the sequences' own tiles nearly empty (fewer than 16
-    // rows, or the form for few rows). 8 trees of 24 rows after 32768 shared tokens
-    // 188 us with one tile, 163 with two, 292 and 245 over e4m3; 64 x 4 rows after
-    // 16384 164 and 146; 64 single tokens 90 and 98.
+    // tile, unless that leaves the sequences' own tiles nearly empty (half of one
+    // tile's rows, over 8 bits those of the form for few rows, where a tile's
+    // conversion counts for more). 16384 to 32768 shared tokens, up to 2000 more: 72
+    // rows of a sequence 132 us with one tile and 129 with two, over e4m3 189 and 166;
+    // 36 rows 134 and 147, 195 and 182; 16 rows 86 and 101, 116 and 124.
     const int64_t own_rows = static_cast<int64_t>(p.T) * p.group;
-    if (p.shared && P->nt == 1 && own_rows >= (held(p.kv) ? 33 : 16)) P->nt = tc_tiles(static_cast<int64_t>(p.B) * p.T, p.group);
+    if (p.shared && P->nt == 1 && own_rows >= (held(p.kv) ? 33 : 64)) P->nt = tc_tiles(static_cast<int64_t>(p.B) * p.T, p.group);
     t.box_shift = 3;
     while ((1 << t.box_shift) < kTile && p.kv.page % (2 << t.box_shift) == 0) ++t.box_shift;
     t.tpt = kTile / p.group;
@@ -616,6 +617,11 @@ st_status st_cache_read(const st_kv_cache* cache, const st_kv_scales* scales, co
   p.k_sb = rk.sb; p.k_ss = rk.ss; p.k_sh = rk.sh;
   p.v_sb = rv.sb; p.v_ss = rv.ss; p.v_sh = rv.sh;
   p.dt = k->dtype;
+  const int per32 = 32 / static_cast<int>(elem_bytes(p.dt));
+  auto wide = [&](const void* x, int64_t sb, int64_t ss, int64_t sh) {
+    return (reinterpret_cast<uintptr_t>(x) & 31u) == 0 && sb % per32 == 0 && ss % per32 == 0 && sh % per32 == 0;
+  };
+  p.wide = wide(p.k, p.k_sb, p.k_ss, p.k_sh) && wide(p.v, p.v_sb, p.v_ss, p.v_sh);
   p.status = dev.status;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   return cuda_check(launch_counted(ST_K_CACHE_KEEP, stream, [&] { return launch_cache_read(p, stream); }), "cache read launch");

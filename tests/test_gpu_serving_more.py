@@ -163,7 +163,7 @@ READ = [
 
 
 @pytest.mark.parametrize("kv,out,B,T,Hkv,start,counts,page", READ)
-@pytest.mark.parametrize("strided", [False, True])
+@pytest.mark.parametrize("strided", [0, 1, 2])
 def test_read(cuda_lib, kv, out, B, T, Hkv, start, counts, page, strided):
     kt, ot = DT[kv], DT[out]
     n = [a + T for a in start]
@@ -174,6 +174,9 @@ def test_read(cuda_lib, kv, out, B, T, Hkv, start, counts, page, strided):
     if strided:  # heads before rows, in one buffer, with room between
         big = torch.full((2, B, Hkv, T, 2 * D), 7.0, dtype=ot, device="cuda")
         outs = dict(k=big[0, ..., :D].transpose(1, 2), v=big[1, ..., :D].transpose(1, 2))
+    if strided == 2:  # K's rows begin on 16 bytes and not on 32
+        at = 16 // ot.itemsize
+        outs["k"] = big[0, ..., at:at + D].transpose(1, 2)
     got = cuda_lib.st_cache_read(cache, i32(start).cuda(), T, counts=gpu(cnt), dtype=ot, **outs)
     cuda_lib.st_check_status()
     for x, s, y in zip(c[:2], c[3:], got):
@@ -189,8 +192,10 @@ def test_read(cuda_lib, kv, out, B, T, Hkv, start, counts, page, strided):
                     held = x.view(torch.int8)[pg, row].view(kt).float()
                     want[b, :m] = (held * s[pg, :, row][..., None]).to(ot)  # one fp32 product, one rounding
         assert torch.equal(y.cpu(), want)
-    if strided:
+    if strided == 1:
         assert bool((big[..., D:] == 7).all())
+    elif strided == 2:
+        assert bool((big[0, ..., :at] == 7).all()) and bool((big[0, ..., at + D:] == 7).all()) and bool((big[1, ..., D:] == 7).all())
 
 
 def test_read_out_of_range(cuda_lib):
