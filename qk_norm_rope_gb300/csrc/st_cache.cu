@@ -3,6 +3,7 @@
 // brings rows back.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 #include "st_kernels.h"
 #include "st_serve.h"
 
@@ -96,8 +97,9 @@ __device__ __forceinline__ float top3(float a, float b, float c) {
 // its scale and reads as NaN. int8: x / s + 1.5 2^23 has the rounded quotient in its
 // low byte, in one step (conversions to integers run at a quarter of that rate: with
 // them, two divisions and comparisons of bits 4608 tokens of two samples, 24 + 24 heads,
-// took 101 us, so 96).
-template <int KV>
+// took 101 us, so 96). EXACT (v of fp32 in int8): s and x / s are divided, and v is held
+// bit for bit as elementwise fp32 code holds it.
+template <int KV, bool EXACT>
 __device__ __forceinline__ uint2 hold_row(const float (&y)[8], float* scale) {
   float top = top3(top3(y[0], y[1], y[2]), top3(y[3], y[4], y[5]), top3(y[6], y[7], y[7]));
 #pragma unroll
@@ -106,7 +108,7 @@ __device__ __forceinline__ uint2 hold_row(const float (&y)[8], float* scale) {
     top = top3(top, t, t);
   }
   constexpr float kInvTop = 1.f / top_of(KV);
-  const float s = top * kInvTop;
+  const float s = EXACT ? top / top_of(KV) : top * kInvTop;
   const bool none = s < kMinScale;
   const float inv = none ? 0.f : 1.f / s;
   *scale = none ? 0.f : (top < INFINITY ? s : NAN);
@@ -120,7 +122,16 @@ __device__ __forceinline__ uint2 hold_row(const float (&y)[8], float* scale) {
       asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\tmov.b32 %0, {a, b};\n}"
           : "=r"(w[i]) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     } else {
-      const float2 magic = make_float2(12582912.f, 12582912.f), a = __ffma2_rn(x0, inv2, magic), b = __ffma2_rn(x1, inv2, magic);
+      const float2 magic = make_float2(12582912.f, 12582912.f);
+      float2 a, b;
+      if constexpr (EXACT) {
+        const float d = none ? INFINITY : s;
+        a = __fadd2_rn(make_float2(x0.x / d, x0.y / d), magic);
+        b = __fadd2_rn(make_float2(x1.x / d, x1.y / d), magic);
+      } else {
+        a = __ffma2_rn(x0, inv2, magic);
+        b = __ffma2_rn(x1, inv2, magic);
+      }
       w[i] = __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
                          __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
     }
@@ -179,10 +190,10 @@ __global__ void __launch_bounds__(kAppWarps * 32, KV == 0 ? 0 : (SRC == kDtF32 ?
       sc_sh = kind == 1 ? p.kv.ks_sh : p.kv.vs_sh;
     }
   };
-  auto hold = [&](const float (&y)[8], int h) {  // every lane calls it
+  auto hold = [&](const float (&y)[8], int h, auto exact) {  // every lane calls it
     if constexpr (KV != 0) {
       float s;
-      const uint2 w = hold_row<KV>(y, &s);
+      const uint2 w = hold_row<KV, decltype(exact)::value>(y, &s);
       if (!room || h >= heads) return;
       *reinterpret_cast<uint2*>(static_cast<uint8_t*>(out) + o_off + h * o_sh) = w;
       if (l == 0) sc_out[h * sc_sh] = s;
@@ -200,7 +211,7 @@ __global__ void __launch_bounds__(kAppWarps * 32, KV == 0 ? 0 : (SRC == kDtF32 ?
       for (int i = 0; i < NI; ++i) {
         float y[8];
         x[i].get(y);
-        hold(y, h0 + 2 * i);
+        hold(y, h0 + 2 * i, std::bool_constant<KV == kDtI8 && DST == kDtF32>());
       }
       return;
     }
@@ -245,7 +256,7 @@ __global__ void __launch_bounds__(kAppWarps * 32, KV == 0 ? 0 : (SRC == kDtF32 ?
       y[2 * e + 1] = n0 * cs[e].y + n1 * cs[e].x;
     }
     if (KV != 0 && kind == 1) {
-      hold(y, h0 + 2 * i);
+      hold(y, h0 + 2 * i, std::false_type());
       continue;
     }
     Raw8<DST> r;

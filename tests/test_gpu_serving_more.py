@@ -125,6 +125,22 @@ def test_rows_that_are_not_finite_or_tiny(cuda_lib, kv):
                 R.close("row", got[0, t, h], y, held_tolerance(y[None], s[None], kt)[0] * (1 + 2.0 ** -20))
 
 
+def test_fp32_rows_are_divided_into_int8(cuda_lib):
+    """v of fp32 is held as elementwise fp32 code holds it, bit for bit, scales too."""
+    B, T, Hkv = 2, 300, 3
+    v = rand(1, B, T, Hkv, D) * torch.exp2(rand(2, B, T, Hkv, 1) * 8)
+    c = M.make_cache(B, [T] * B, Hkv, 16, torch.int8, [0] * B, 3, behind=0.0)
+    cache = dev_cache(cuda_lib, c)
+    w, ids = torch.ones(D).cuda(), torch.zeros(1, T, 1, dtype=torch.int32).cuda()
+    k = rand(3, B, T, Hkv, D).cuda()
+    cuda_lib.st_cache_append(k, k, v.cuda(), w, w, 1e-6, ids, (128,), 1e4, cache, i32([0] * B).cuda())
+    s = v.abs().amax(-1) / 127.0
+    want = (v / s[..., None]).round().to(torch.int8)
+    for b in range(B):
+        pg, row = R.slots(c[2], 16, b, torch.arange(T))
+        assert torch.equal(cache.v.cpu()[pg, row], want[b]) and torch.equal(cache.v_scale.cpu()[pg, :, row], s[b])
+
+
 def test_append_beyond_the_pages(cuda_lib):
     x = rand(1, 2, 4, 1, D, dtype=torch.bfloat16).cuda()
     w = torch.ones(D, device="cuda")
