@@ -423,55 +423,65 @@ __global__ void __launch_bounds__(THREADS) keep_kernel(const __grid_constant__ K
 // these are so many: four rows are in flight per lane and the token's page is
 // looked up once. Values of 8 bits leave in stores of 32 bytes (in two of 16, each half
 // of a sector, 4608 tokens of two samples and 24 heads took 38 us from int8 to bf16
-// instead of 35). KV: 8-bit type of the cache, or 0: rows of type OUT are copied.
+// instead of 35). ONE: a unit is of one token, whose place is found once (for each of a
+// lane's rows, instructions were what bounded: those 35 us are 31 so, and 65332 tokens
+// of 8 heads from e4m3 took 75 and take 66). KV: 8-bit type of the cache, or 0: rows of type OUT are copied.
 constexpr int kReadWarps = 8, kReadRows = 16;
-template <int KV, int OUT>
-__global__ void __launch_bounds__(kReadWarps * 32) read_kernel(const __grid_constant__ ReadParams p, int tokens, int groups) {
+template <int KV, int OUT, bool ONE>
+__global__ void __launch_bounds__(kReadWarps * 32, KV != 0 ? 5 : 0) read_kernel(const __grid_constant__ ReadParams p, int tokens, int groups) {
   // a unit: `tokens` tokens (where a token has fewer rows than 16), or a group of 16 rows of one
   constexpr int kEs = OUT == kDtF32 ? 4 : 2, kPieces = KV != 0 ? 1 : kEs;  // 16-byte pieces a lane reads of a row
+  constexpr int kU = kReadRows / 4, kPlaces = ONE ? 1 : kU;
   grid_dependency_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane & 7;
-  const unsigned unit = blockIdx.x * kReadWarps + warp, at = unit / static_cast<unsigned>(groups);
-  const int group = static_cast<int>(unit - at * groups), per = 2 * p.kv.Hkv;  // rows of a token
+  const unsigned unit = blockIdx.x * kReadWarps + warp, at = ONE ? unit / static_cast<unsigned>(groups) : unit;
+  const int group = ONE ? static_cast<int>(unit - at * groups) : 0, per = 2 * p.kv.Hkv;  // rows of a token
   const unsigned all = static_cast<unsigned>(p.B) * p.T, tok0 = at * tokens;  // at most 2^30
   if (tok0 >= all) return;
-  uint4 x[kReadRows / 4][kPieces];
-  float s[kReadRows / 4];
-  int where[kReadRows / 4];      // (head or Hkv + head), -1: no row of this unit
-  unsigned tok[kReadRows / 4];
+  // of a token: where it lies (pg < 0: nowhere, its rows are zeros) and goes
+  int pg[kPlaces], row[kPlaces];
+  int64_t to_k[kPlaces], to_v[kPlaces];
+  uint4 x[kU][kPieces];
+  float s[kU];
+  int where[kU];  // (head or Hkv + head), -1: no row of this unit
 #pragma unroll
-  for (int u = 0; u < kReadRows / 4; ++u) {
-    const int r = 4 * u + (lane >> 3), step = tokens > 1 ? r / per : 0;
-    const int i = tokens > 1 ? r - step * per : group * kReadRows + r;
-    tok[u] = tok0 + step;
-    where[u] = i < per && step < tokens && tok[u] < all ? i : -1;
+  for (int u = 0; u < kU; ++u) {
+    const int r = 4 * u + (lane >> 3), step = ONE ? 0 : r / per, a = ONE ? 0 : u;
+    const int i = ONE ? group * kReadRows + r : r - step * per;
+    const unsigned tok = tok0 + step;
+    where[u] = i < per && step < tokens && tok < all ? i : -1;
     s[u] = 0.f;
 #pragma unroll
     for (int c = 0; c < kPieces; ++c) x[u][c] = make_uint4(0, 0, 0, 0);
-    if (where[u] < 0) continue;
-    const int b = static_cast<int>(tok[u] / static_cast<unsigned>(p.T)), t = static_cast<int>(tok[u] - static_cast<unsigned>(b) * p.T);
-    if (t >= row_count(p.counts, b, p.T)) continue;
-    const int start = ld_now(p.start + b);
-    int pg, row;
-    if (start < 0 || !kv_locate(p.kv, b, static_cast<int64_t>(start) + t, &pg, &row)) {
-      if (l == 0) atomicOr(p.status, kStatusIndex);
-      continue;  // zeros
+    if (u == 0 || (!ONE && where[u] >= 0)) {
+      const int b = static_cast<int>(tok / static_cast<unsigned>(p.T)), t = static_cast<int>(tok - static_cast<unsigned>(b) * p.T);
+      to_k[a] = b * p.k_sb + t * p.k_ss;
+      to_v[a] = b * p.v_sb + t * p.v_ss;
+      pg[a] = -1;
+      if ((ONE || where[u] >= 0) && t < row_count(p.counts, b, p.T)) {
+        const int start = ld_now(p.start + b);
+        if (start < 0 || !kv_locate(p.kv, b, static_cast<int64_t>(start) + t, &pg[a], &row[a])) {
+          if (l == 0) atomicOr(p.status, kStatusIndex);
+          pg[a] = -1;
+        }
+      }
     }
+    if (where[u] < 0 || pg[a] < 0) continue;
     const bool v = i >= p.kv.Hkv;
     const int h = v ? i - p.kv.Hkv : i;
-    const int64_t off = v ? pg * p.kv.v_sp + row * p.kv.v_sr + h * p.kv.v_sh : pg * p.kv.k_sp + row * p.kv.k_sr + h * p.kv.k_sh;
+    const int64_t off = v ? pg[a] * p.kv.v_sp + row[a] * p.kv.v_sr + h * p.kv.v_sh : pg[a] * p.kv.k_sp + row[a] * p.kv.k_sr + h * p.kv.k_sh;
     const uint8_t* src = static_cast<const uint8_t*>(v ? p.kv.v : p.kv.k) + off * (KV != 0 ? 1 : kEs);
 #pragma unroll
     for (int c = 0; c < kPieces; ++c) x[u][c] = ld_v4(src + 16 * (l + 8 * c));
-    if constexpr (KV != 0) s[u] = v ? ld_now(p.kv.vs + pg * p.kv.vs_sp + h * p.kv.vs_sh + row) : ld_now(p.kv.ks + pg * p.kv.ks_sp + h * p.kv.ks_sh + row);
+    if constexpr (KV != 0)
+      s[u] = v ? ld_now(p.kv.vs + pg[a] * p.kv.vs_sp + h * p.kv.vs_sh + row[a]) : ld_now(p.kv.ks + pg[a] * p.kv.ks_sp + h * p.kv.ks_sh + row[a]);
   }
 #pragma unroll
-  for (int u = 0; u < kReadRows / 4; ++u) {
+  for (int u = 0; u < kU; ++u) {
     if (where[u] < 0) continue;
-    const int b = static_cast<int>(tok[u] / static_cast<unsigned>(p.T)), t = static_cast<int>(tok[u] - static_cast<unsigned>(b) * p.T);
+    const int a = ONE ? 0 : u;
     const bool v = where[u] >= p.kv.Hkv;
-    const int h = v ? where[u] - p.kv.Hkv : where[u];
-    const int64_t off = v ? b * p.v_sb + t * p.v_ss + h * p.v_sh : b * p.k_sb + t * p.k_ss + h * p.k_sh;
+    const int64_t off = v ? to_v[a] + (where[u] - p.kv.Hkv) * p.v_sh : to_k[a] + where[u] * p.k_sh;
     uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(v ? p.v : p.k) + off * kEs);
     if constexpr (KV != 0) {
       const uint32_t w[4] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w};
@@ -481,7 +491,11 @@ __global__ void __launch_bounds__(kReadWarps * 32) read_kernel(const __grid_cons
         float z[4];
         held4<KV>(w[e], z);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) y[4 * e + k] = z[k] * s[u];
+        for (int k = 0; k < 4; k += 2) {
+          const float2 q = __fmul2_rn(make_float2(z[k], z[k + 1]), make_float2(s[u], s[u]));
+          y[4 * e + k] = q.x;
+          y[4 * e + k + 1] = q.y;
+        }
       }
       constexpr int kW = OUT == kDtF32 ? 2 : 1;  // runs of 32 bytes
 #pragma unroll
@@ -560,7 +574,7 @@ template <int KV, int OUT>
 cudaError_t launch_read_t(const ReadParams& p, cudaStream_t stream) {
   const int per = 2 * p.kv.Hkv, tokens = per < kReadRows ? kReadRows / per : 1, groups = tokens > 1 ? 1 : (per + kReadRows - 1) / kReadRows;
   const int64_t units = (static_cast<int64_t>(p.B) * p.T + tokens - 1) / tokens * groups;
-  return launch_chained(read_kernel<KV, OUT>, dim3(static_cast<unsigned>((units + kReadWarps - 1) / kReadWarps)), dim3(kReadWarps * 32), 0,
+  return launch_chained(tokens > 1 ? read_kernel<KV, OUT, false> : read_kernel<KV, OUT, true>, dim3(static_cast<unsigned>((units + kReadWarps - 1) / kReadWarps)), dim3(kReadWarps * 32), 0,
                         stream, p, tokens, groups);
 }
 template <int KV>
