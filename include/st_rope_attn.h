@@ -393,12 +393,17 @@ ST_API st_status st_cache_attn(const st_tensor* q_rot, const st_kv_cache* cache,
  *           scales and sums are fp32, the softmax weights times V's scales are
  *           rounded to fp16 (relative to the largest scale of 128 keys; scales of
  *           V are good from 2^-50 to 2^50), with fp32 rows nothing is. The scales
- *           of keys that no row sees are not used.
+ *           of keys that no row sees are not used; those that a row sees must be
+ *           finite, as V's values, for the rows that do not see them. Pages may
+ *           hold any number of rows. (K or V that spans more than 64 GB, and fp32
+ *           rows, take the kernel without tensor cores.)
  *  window:  0: none. Else a row at position p sees, of the keys that it would see
  *           without, those at positions above p - window and those below sinks.
  *           Positions are lens[b] + t for a chain, lens[b] plus the number of its
- *           ancestors for a node of a tree. Keys that no row sees are not read,
- *           nor are pages that hold no other: their table entries may be anything.
+ *           ancestors for a node of a tree. Keys that no row sees may hold
+ *           anything, and pages that hold no other are not looked up: their table
+ *           entries may be anything. A sequence whose window lies beyond the page
+ *           table sees nothing: O = 0, LSE = -inf.
  *  sinks:   first tokens that stay visible (only with a window).
  *  shared:  [1] int32 on the device, or NULL: the first shared[0] tokens of every
  *           sequence that has rows lie in the same pages. What is a multiple of

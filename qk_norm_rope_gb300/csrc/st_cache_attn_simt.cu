@@ -1,6 +1,7 @@
 // Cached attention on the CUDA cores: fp32 caches (every product and sum in
-// fp32), 16-bit and 8-bit caches whose pages the tensor-core kernel's boxes do
-// not fit (page sizes that are no multiple of 8), and fp32 rows over 8-bit caches.
+// fp32), 16-bit caches whose pages the tensor-core kernel's boxes do not fit (page
+// sizes that are no multiple of 8), fp32 rows over 8-bit caches, and 8-bit caches of
+// more than 64 GB.
 //
 // EXT: the forms with a window or an 8-bit cache. A window's keys are two runs,
 // the first tokens and what the rows' windows hold; they are walked as one list
