@@ -45,8 +45,8 @@
 //
 // Roles (512 threads, KV: 576; one CTA per SM):
 //   warps 0-7   softmax, two groups of four warps; thread = query row = TMEM lane
-//   warps 8-11  Q rows of the next item into shared memory; KV: also K's conversion,
-//               and four more warps V's
+//   warps 8-11  Q rows of the next item into shared memory; KV: K's conversion, and
+//               four more warps V's and the Q rows
 //   then        tcgen05.mma issue for slot 0 (one thread; TMEM allocation); TMA of K
 //               boxes, one lane per box, and of V boxes (KV: neither); tcgen05.mma
 //               issue for slot 1
@@ -1189,12 +1189,15 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
           prow0 = pslot * P.split_rows;
           if (wk.whole()) prow0 = whole_part(P, wk.ph, wk.pb, wk.pm);
           if (tid == 0 && wk.kt0 == 0) {
-            Deal d;
-            d.make(start->total, P.ctas);
-            // where the item ends: as far behind the piece as it has tiles behind it
-            const long long end = range_end - (HELD ? place->left : wk.left) + wk.it.n - wk.kt1;
-            P.item_meta[item_index(P, wk.ph, wk.pb, wk.pm)] =
-                wk.whole() ? make_int2(1, -1) : make_int2(d.holder(end - 1) - static_cast<int>(blockIdx.x) + 1, static_cast<int>(pslot));
+            int2 meta = make_int2(1, -1);
+            if (!wk.whole()) {
+              Deal d;
+              d.make(start->total, P.ctas);
+              // where the item ends: as far behind the piece as it has tiles behind it
+              const long long end = range_end - (HELD ? place->left : wk.left) + wk.it.n - wk.kt1;
+              meta = make_int2(d.holder(end - 1) - static_cast<int>(blockIdx.x) + 1, static_cast<int>(pslot));
+            }
+            P.item_meta[item_index(P, wk.ph, wk.pb, wk.pm)] = meta;
           }
         }
       }
@@ -1245,8 +1248,10 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
             const int q4 = 2 * slot + q;
             uint32_t a[32], d[32];
             float y[32];
-            tmem_ld32(tO + 32 * q4, a);
-            tmem_ld32(tOther + 32 * q4, d);
+            tmem_ld32_issue(tO + 32 * q4, a);
+            tmem_ld32_issue(tOther + 32 * q4, d);
+            tmem_ld_wait32(a);
+            tmem_ld_wait32(d);
 #pragma unroll
             for (int e = 0; e < 32; ++e) {  // a slot without tiles holds anything
               const float v0 = mine ? __uint_as_float(a[e]) : 0.f, v1 = theirs ? __uint_as_float(d[e]) : 0.f;
@@ -1375,11 +1380,12 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
         if (left == 0) {
           if (!next_piece(wk, all_lanes, false)) break;
           left = wk.kt1 - wk.kt0;
-          if (!is_v) {
-            // its rows, once the last one's scores are done
+          if (is_v) {
+            // its rows, once the last one's scores are done: V's warps bring them, whose tiles
+            // are wanted after K's (K's warps: 256 tokens of short sequences 160 us, so 156)
             const bool q_few = NT == 1 && P.few && wk.pb >= 0;
             float* qs = reinterpret_cast<float*>(sm + L::qs) + (n_piece & 1) * NT * 128;
-            if (!load_q_held<NT, F16, EXT, kQWarps * 32>(P, wk, sm + L::q, qs, qt, q_few, [&]() -> bool {
+            if (!load_q_held<NT, F16, EXT, kQWarps * 32>(P, wk, sm + L::q, qs, qt & 127, q_few, [&]() -> bool {
                   return n_piece == 0 || wait_bar_warp(&bars[L::QEmpty], (n_piece - 1) & 1, abort_flag, budget);
                 }))
               break;

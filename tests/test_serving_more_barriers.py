@@ -83,7 +83,7 @@ def model(nt, pieces, rnd, ss):
             fetch(fetched)
         fetched = RAW
         for p, tiles in enumerate(pieces):
-            if name == "K":  # its warps bring the rows
+            if name == "V":  # its warps bring the rows
                 if p:
                     yield "QE", p - 1
                 q[0] = None
