@@ -391,8 +391,9 @@ ST_API st_status st_cache_attn(const st_tensor* q_rot, const st_kv_cache* cache,
  *  scales:  the scales of a cache of 8 bits, else NULL. q_rot is then bf16, fp16
  *           or fp32 and o of its type; the held values enter the products exactly,
  *           scales and sums are fp32, the softmax weights times V's scales are
- *           rounded to fp16 (relative to the largest scale of 128 keys; scales of
- *           V are good from 2^-50 to 2^50), with fp32 rows nothing is. The scales
+ *           rounded to fp16 (off by 2^-11 of each, or by 2^-24 of the row's largest
+ *           weight times the largest scale that it sees; scales of V are good from
+ *           2^-50 to 2^50), with fp32 rows nothing is. The scales
  *           of keys that no row sees are not used; those that a row sees must be
  *           finite, as V's values, for the rows that do not see them. Pages may
  *           hold any number of rows. (K or V that spans more than 64 GB, and fp32

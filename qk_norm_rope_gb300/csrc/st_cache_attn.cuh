@@ -118,17 +118,21 @@ static_assert(Lay<1, true>::bytes <= 232448 && Lay<2, true>::bytes <= 232448, "s
 static_assert(Lay<1>::Num * 8 + 128 <= 512 && Lay<2>::Num * 8 + 128 <= 512, "barrier area");
 static_assert(Lay<1, true>::Num * 8 + 128 <= 512 && Lay<2, true>::Num * 8 + 128 <= 512, "barrier area");
 
-// The scales of a key tile; those of keys that no row sees are 0. top: log2 of
-// V's largest, of the keys that each of four warps fetched.
+// The scales of a key tile; those of keys that no row sees are 0. ends: log2 of V's
+// largest, and minus that of its least but 0, of the keys that each of four warps fetched.
 struct Scales {
   float k[kTile], v[kTile];
-  float top[4];
+  __half2 ends[4];
 };
 static_assert(sizeof(Scales) == 1040, "layout");
 // V's scales are good in this range (base 2): between its ends a row's sum, in
 // units of them, may shrink by 2^-100, and a share of it above 2^-26 stays in ex2's
 // range.
 constexpr float kTopRange = 50.f;
+// Where V's scales in a tile differ by more than this (base 2), a row's reference goes
+// by its own largest product of a weight and a scale. Else the largest scale stands for
+// all: a row whose keys have lesser ones has its largest weight at 2^-1 or above.
+constexpr float kTopSpread = 8.f;
 
 __device__ __forceinline__ constexpr uint32_t kofs(int kk) { return (kk >> 2) * kHalfBytes + (kk & 3) * 32; }
 __device__ __forceinline__ constexpr uint32_t mofs(int kk) { return kk * 2048; }
@@ -584,7 +588,12 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float sc,
 // weights of the others are zero). Scores are s ks sc: ks the key's scale, sc the row's
 // factor. The weights are rounded as P vs, vs V's scale, and so that they end at 2^15
 // the reference has log2 of the tile's largest vs added to it; sums and accumulators
-// alike are in its units. There are no registers for a row of 128 scores: they go back
+// alike are in its units. (Only where the tile's vs are of about one size. Else the
+// largest may be that of a key which the row does not see, or hardly, and its weights
+// would end below fp16's range: with 2^32 between them the row read as zeros. There the
+// reference is the largest sum of a score and its key's log2 vs, found in a pass of its
+// own: where every tile takes it, 64 tokens after up to 8191 keys in e4m3 201 us instead
+// of 154, 2048 after 16384 1090 instead of 670.) There are no registers for a row of 128 scores: they go back
 // to TMEM, scaled and masked, while the maximum is found, and come again for the
 // weights, which take the place of scores that have been read. (Scaled and masked a
 // second time instead 2048 tokens after 16384 took 926 us over e4m3, so 755: the
@@ -638,6 +647,28 @@ __device__ __forceinline__ float2 weigh_chunk(uint32_t tP, const uint32_t (&x)[N
   else tmem_st8(tP, pw);
   return ls;
 }
+// The largest sum of a scaled score and log2 of its key's vs over n chunks of scores in
+// TMEM (vs within the range in which these are good; one of 0 counts as its lower end).
+// A function of its own: inlined, the kernel's size cost 13% where no tile comes here
+// (256 tokens of short sequences in e4m3 158 us, 177; so 163).
+__device__ __noinline__ float max_product(uint32_t tS, const float* vs, int n, float sc) {
+  float m = -INFINITY;
+#pragma unroll 1
+  for (int i = 0; i < 2 * n; ++i) {
+    uint32_t x[16];
+    tmem_ld16_issue(tS + 16 * i, x);
+    tmem_ld_wait16(x);
+#pragma unroll
+    for (int t = 0; t < 16; t += 4) {
+      const float4 v4 = *reinterpret_cast<const float4*>(vs + 16 * i + t);
+      const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        m = fmaxf(m, fmaf(__uint_as_float(x[t + e]), sc, fminf(fmaxf(__log2f(fabsf(v[e])), -kTopRange), kTopRange)));
+    }
+  }
+  return m;
+}
 // The eight runs of 16 columns from tS on, each on its way from TMEM while f works on
 // the one before it.
 template <class F>
@@ -682,8 +713,19 @@ __device__ __forceinline__ void softmax_held(uint32_t tS, uint32_t tO, float sc,
     }
   }
   if (!few) tmem_st_wait();
-  const float4 vt = *reinterpret_cast<const float4*>(scales.top);
-  const float mt = fmaf(top, sc, fmaxf(fmaxf(vt.x, vt.y), fmaxf(vt.z, vt.w)) - kLift<true>);
+  const uint4 ew = *reinterpret_cast<const uint4*>(scales.ends);
+  const __half2 e01 = __hmax2(*reinterpret_cast<const __half2*>(&ew.x), *reinterpret_cast<const __half2*>(&ew.y));
+  const __half2 ends = __hmax2(e01, __hmax2(*reinterpret_cast<const __half2*>(&ew.z), *reinterpret_cast<const __half2*>(&ew.w)));
+  const float v_top = __low2float(ends);
+  float mt = fmaf(top, sc, v_top - kLift<true>);
+  if (v_top + __high2float(ends) > kTopSpread) {  // the same for all threads
+    if (few) {
+      tmem_st32(tS + 32 * c0, x);
+      tmem_st_wait();
+    }
+    mt = max_product(tS + 32 * c0, scales.v + 32 * c0, c1 - c0, sc) - kLift<true>;
+    if (few) tmem_ld32(tS + 32 * c0, x);
+  }
   float corr = 1.f;
   if (mt > m_run + kRescale || (m_run == -INFINITY && mt > -INFINITY)) {
     corr = ex2(m_run - mt);  // 0 when m_run is -inf
@@ -1402,9 +1444,12 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
             const int st = n % L::SS;
             Scales& s = reinterpret_cast<Scales*>(sm + L::sc)[st];
             if (is_v) {
-              const float v = fabsf(s.v[my_row]);
+              const float v = fabsf(s.v[my_row]);  // 0: not seen, or a row of zeros
               const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, v == v ? __float_as_uint(v) : 0u));
-              if (lane_id == 0) s.top[gw] = fminf(fmaxf(__log2f(top), -kTopRange), kTopRange);  // any number near it does
+              const float low = __uint_as_float(__reduce_min_sync(0xffffffffu, v > 0.f ? __float_as_uint(v) : 0x7f800000u));
+              // any numbers near them do; no key but zeros: -50 and -50
+              if (lane_id == 0)
+                s.ends[gw] = __floats2half2_rn(fminf(fmaxf(__log2f(top), -kTopRange), kTopRange), fminf(fmaxf(-__log2f(low), -kTopRange), kTopRange));
             }
             __syncwarp();
             if (lane_id == 0) mbar_arrive(&bars[L::ScFull + st]);

@@ -1,0 +1,93 @@
+"""Edges of the calls over 8-bit caches, on the GPU: rows beside keys that they do not see, caches without pages, CTAs
+without work, caches of many heads, arguments that are not there."""
+import math
+
+import pytest
+import torch
+
+import _serving as R
+import _serving_more as M
+from test_gpu_serving_more import D, DT, HELD, attend_inputs, dev_cache, gpu, i32, rand
+
+pytestmark = pytest.mark.gpu
+
+
+def row_by_row(q, c, lens, parents, window, sinks):
+    """The 64-bit results and bounds of each row over the keys that it sees and no others. Of V's rows a row's bound has the
+    largest that it sees: its weights times V's scales are rounded to fp16 where the largest of them is 2^7, or down to 2^-1
+    where V's scales differ by up to 2^8 among 128 keys, and the smallest numbers' half step is 2^-25: 2^-24 of the largest."""
+    B, T, H, _ = q.shape
+    o, lse = torch.zeros(B, T, H, D, dtype=torch.float64), torch.zeros(B, H, T, dtype=torch.float64)
+    bound, lse_bound = torch.zeros_like(o), torch.zeros_like(lse)
+    page = c[0].shape[1]
+    for b, n in enumerate(lens):
+        vis = M.seen(n, T, None if parents is None else parents[b].tolist(), window, sinks)
+        for t in range(T):
+            kept = vis[t].nonzero()[:, 0]
+            pg, row = R.slots(c[2], page, b, kept)
+            k, v = (x.view(torch.int8)[pg, row][None].view(x.dtype) for x in c[:2])
+            ks, vs = (s[pg, :, row].T[None].contiguous() for s in c[3:])
+            m = len(kept)
+            w = M.attention(q[b:b + 1, t:t + 1], k, v, i32([[0]]), [m - 1], None, None, scales=(ks, vs))
+            top = M.values(v, vs).abs().amax((0, 1, 3)).repeat_interleave(H // k.shape[2])
+            o[b, t], bound[b, t] = w[0][0, 0], w[2][0, 0] + (m * 2.0 ** -24 * top)[:, None]
+            lse[b, :, t], lse_bound[b, :, t] = w[1][0, :, 0], w[3][0, :, 0]
+    return o, lse, bound, lse_bound
+
+
+@pytest.mark.parametrize("kv", HELD)
+@pytest.mark.parametrize("B,T,tree,window", [(2, 6, False, 0), (2, 6, True, 0), (1, 40, False, 0), (2, 50, True, 0),
+                                             (2, 6, False, 100), (2, 48, True, 90)])
+@pytest.mark.parametrize("wide", [False, True])
+def test_rows_beside_much_larger_values(cuda_lib, kv, B, T, tree, window, wide):
+    """V rows of 2^40 times a row's own, that it does not see (later rows, other branches, keys before its window), lie in
+    its tiles of 128 keys."""
+    H, Hkv, page, sinks = 8, 2, 16, 2 if window else 0
+    lens = [300, 130][:B]
+    q, c, par, _ = attend_inputs("bf16", kv, B, T, H, Hkv, lens, None, page, tree, 0, 0)
+    scale = c[4].clone()
+    for b, n in enumerate(lens):
+        at = torch.arange(n + T)
+        up = torch.zeros(n + T)
+        up[n + T // 2:] = 1.0            # the later half of the new rows
+        if window:
+            up[sinks:n - window + 3] = 1.0   # keys that leave the window from the third position on
+        pg, row = R.slots(c[2], page, b, at)
+        scale[pg, :, row] *= torch.exp2(40 * up - 20)[:, None]
+    c = (*c[:4], scale)
+    d = c
+    if wide:  # dealt over all CTAs instead of clusters
+        pages = torch.full((B, 6000), 1 << 30, dtype=torch.int32)
+        pages[:, :c[2].shape[1]] = c[2]
+        d = (c[0], c[1], pages, c[3], c[4])
+    o, lse = cuda_lib.st_cache_attn(q.cuda(), dev_cache(cuda_lib, d), i32(lens).cuda(), parents=gpu(par), window=window, sinks=sinks)
+    cuda_lib.st_check_status()
+    want = row_by_row(q, c, lens, par, window, sinks)
+    R.close("o", o, want[0], want[2])
+    R.close("lse", lse, want[1], want[3])
+
+
+@pytest.mark.parametrize("kv", HELD)
+@pytest.mark.parametrize("T", [1, 40])
+def test_a_key_with_all_the_weight_and_a_small_value(cuda_lib, kv, T):
+    """The key that has nearly the whole weight lies beside one of 2^44 times its V row and 2^-115 of its weight."""
+    H, Hkv, page, n = 4, 2, 16, 200
+    q, c, _, _ = attend_inputs("bf16", kv, 1, T, H, Hkv, [n], None, page, False, 0, 0, spread=0.0)
+    q[:] = q[:, :1, :1]
+    pg, row = R.slots(c[2], page, 0, torch.arange(n + T))
+    c[4][pg, :, row] *= 2.0 ** -22
+    x = q[0, 0, 0].float() / q.float().abs().max()
+    held = ((x * M.TOP[DT[kv]]).round()).to(DT[kv]).view(torch.int8)
+    for at, sign in ((70, 1.0), (90, -1.0)):
+        pg, row = R.slots(c[2], page, 0, torch.tensor([at]))
+        c[0].view(torch.int8)[pg, row] = held
+        c[3][pg, :, row] = sign * 6.0 / M.TOP[DT[kv]]
+    c[4][pg, :, row] *= 2.0 ** 44
+    o, lse = cuda_lib.st_cache_attn(q.cuda(), dev_cache(cuda_lib, c), i32([n]).cuda())
+    cuda_lib.st_check_status()
+    pg, row = R.slots(c[2], page, 0, torch.tensor([90]))
+    small = (*c[:4], c[4].clone())
+    small[4][pg, :, row] = 0.0           # its own share is below 2^-40 of the result
+    want = row_by_row(q, small, [n], None, 0, 0)
+    R.close("o", o, want[0], want[2])
+    R.close("lse", lse, want[1], want[3])
