@@ -566,7 +566,7 @@ cudaError_t launch_keep_t(const KeepParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_cache_keep(const KeepParams& p, cudaStream_t stream) {
-  if (p.kv.ks) return p.wide ? launch_keep_t<1024, 2, true>(p, stream) : launch_keep_t<256, 4, true>(p, stream);
+  if (held(p.kv)) return p.wide ? launch_keep_t<1024, 2, true>(p, stream) : launch_keep_t<256, 4, true>(p, stream);
   return p.wide ? launch_keep_t<1024, 2, false>(p, stream) : launch_keep_t<256, 4, false>(p, stream);
 }
 

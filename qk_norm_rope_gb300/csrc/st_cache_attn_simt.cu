@@ -549,7 +549,7 @@ cudaError_t launch_cache_attn_simt_join(const CacheAttnParams& p, cudaStream_t s
   // several warps a row where its parts are many: with one, 125 parts took 27 us
   // more than one (10 us in all with eight)
   const int warps = p.splits > 4 * p.B ? 8 : 1;
-  const bool ext = p.kv.ks || p.window > 0;
+  const bool ext = held(p.kv) || p.window > 0;  // as above: by the type (a cache without pages has no scales)
   const auto kern = ext ? (warps == 8 ? simt_join_kernel<8, true> : simt_join_kernel<1, true>)
                         : (warps == 8 ? simt_join_kernel<8, false> : simt_join_kernel<1, false>);
   return launch_chained(kern, dim3(static_cast<unsigned>((items * kR * warps + 7) / 8)), dim3(256), 0, stream, p, n_rt, items);

@@ -63,6 +63,8 @@ struct PagedKV {
   int64_t ks_sp, ks_sh, vs_sp, vs_sh;
 };
 
+inline bool held(const PagedKV& kv) { return kv.dt == kDtE4M3 || kv.dt == kDtI8; }
+
 // Four held bytes (the lowest first) as numbers.
 template <int DT>
 __device__ __forceinline__ void held4(uint32_t w, float (&y)[4]) {

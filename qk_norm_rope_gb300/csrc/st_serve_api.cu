@@ -110,7 +110,6 @@ st_status check_cache(const st_kv_cache* c, const st_kv_scales* sc, int64_t B, P
   if ((st = check_scales(sc->k, "k_scale", n, H, page, &out->ks, &out->ks_sp, &out->ks_sh)) != ST_OK) return st;
   return check_scales(sc->v, "v_scale", n, H, page, &out->vs, &out->vs_sp, &out->vs_sh);
 }
-bool held(const PagedKV& kv) { return kv.dt == kDtE4M3 || kv.dt == kDtI8; }
 
 // Sizes of a new-rows tensor [B, T, H, D].
 st_status check_new_rows(const st_tensor* q, const char* name, int* B, int* T, int* H) {

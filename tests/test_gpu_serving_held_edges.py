@@ -91,3 +91,36 @@ def test_a_key_with_all_the_weight_and_a_small_value(cuda_lib, kv, T):
     want = row_by_row(q, small, [n], None, 0, 0)
     R.close("o", o, want[0], want[2])
     R.close("lse", lse, want[1], want[3])
+
+
+# ---------------------------------------------------------- caches without pages
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("kv", HELD)
+@pytest.mark.parametrize("T,tree", [(1, False), (5, True)])
+def test_a_cache_without_pages(cuda_lib, dtype, kv, T, tree):
+    """Every page number is out of range: the keys read as zeros, so that O is 0 and LSE the logarithm of their number, and
+    the status says so. A table of more than 64 tokens splits the keys."""
+    B, H, Hkv, page, lens = 2, 4, 2, 16, [200, 70]
+    k = torch.empty(0, page, Hkv, D, dtype=torch.int8, device="cuda").view(DT[kv])
+    s = torch.empty(0, Hkv, page, device="cuda")
+    cache = cuda_lib.KVCache(k, k.clone(), torch.zeros(B, 20, dtype=torch.int32, device="cuda"), s, s.clone())
+    q, par = rand(1, B, T, H, D, dtype=DT[dtype]).cuda(), R.tree(B, T, 2, 3) if tree else None
+    o = torch.full_like(q, 7.0)
+    _, lse = cuda_lib.st_cache_attn(q, cache, i32(lens).cuda(), parents=gpu(par), o=o)
+    with pytest.raises(cuda_lib.StError) as e:
+        cuda_lib.st_check_status()
+    assert e.value.status == cuda_lib.ST_ERR_INVALID_ARG
+    assert bool((o == 0).all())
+    for b, n in enumerate(lens):
+        seen = M.seen(n, T, None if par is None else par[b].tolist(), 0, 0).sum(-1).double().log()
+        # the sum of as many ones, log2 and a product with ln 2, each rounded
+        R.close("lse", lse[b], seen.expand(H, T), (2.0 ** -22 * (1 + seen)).expand(H, T))
+    rows = i32([[0, 2], [1, 3]]).cuda()
+    new = cuda_lib.st_cache_keep(cache, i32([0, 4]).cuda(), rows, i32([2, 2]).cuda())
+    assert new.tolist() == [2, 6]
+    with pytest.raises(cuda_lib.StError):
+        cuda_lib.st_check_status()
+    back = cuda_lib.st_cache_read(cache, i32([0, 4]).cuda(), 3, dtype=DT[dtype])
+    assert bool((back[0] == 0).all()) and bool((back[1] == 0).all())
+    with pytest.raises(cuda_lib.StError):
+        cuda_lib.st_check_status()
