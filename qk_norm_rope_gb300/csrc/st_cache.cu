@@ -300,9 +300,9 @@ struct KeepLay {
   __host__ __device__ size_t bytes() const { return ring() + static_cast<size_t>(2) * tables * table * 8; }
 };
 
-// SC: a cache of 8 bits. Blocks from 2 Hkv on move the scales of one head, K's
-// and then V's: THREADS rows at a time are read, and written once all are read
-// (a later turn's rows lie behind all that this one writes).
+// SC: a cache of 8 bits. The last of a head's blocks (of K or of V) moves its scales:
+// THREADS rows at a time are read, and written once all are read (a later turn's rows
+// lie behind all that this one writes).
 template <int THREADS, int PER, bool SC>
 __global__ void __launch_bounds__(THREADS) keep_kernel(const __grid_constant__ KeepParams p) {
   extern __shared__ __align__(16) uint8_t raw[];
@@ -321,13 +321,12 @@ __global__ void __launch_bounds__(THREADS) keep_kernel(const __grid_constant__ K
     p.lens[b] = start < 0 ? start : start + n;
   }
   if (start < 0) return;
+  const bool is_v = blockIdx.y >= p.kv.Hkv;
+  const int h = is_v ? blockIdx.y - p.kv.Hkv : blockIdx.y;
   if constexpr (SC) {
-    if (blockIdx.y >= 2 * p.kv.Hkv) {
-      if (blockIdx.x > 0) return;
-      const int u = blockIdx.y - 2 * p.kv.Hkv;
-      const bool v = u >= p.kv.Hkv;
-      float* sc = v ? p.kv.vs + (u - p.kv.Hkv) * p.kv.vs_sh : p.kv.ks + u * p.kv.ks_sh;
-      const int64_t sp = v ? p.kv.vs_sp : p.kv.ks_sp;
+    if (blockIdx.x == gridDim.x - 1) {
+      float* sc = is_v ? p.kv.vs + h * p.kv.vs_sh : p.kv.ks + h * p.kv.ks_sh;
+      const int64_t sp = is_v ? p.kv.vs_sp : p.kv.ks_sp;
       const int32_t* list = p.rows + b * p.r_sb;
       for (int i0 = 0; i0 < n; i0 += THREADS) {
         const int i = i0 + tid, r = i < n ? ld_now(list + i) : -1, before = i < n && i > 0 ? ld_now(list + i - 1) : -1;
@@ -344,8 +343,6 @@ __global__ void __launch_bounds__(THREADS) keep_kernel(const __grid_constant__ K
   }
 
   const int eb = p.kv.dt == kDtF32 ? 4 : (SC ? 1 : 2);
-  const bool is_v = blockIdx.y >= p.kv.Hkv;
-  const int h = is_v ? blockIdx.y - p.kv.Hkv : blockIdx.y;
   uint8_t* base = static_cast<uint8_t*>(is_v ? p.kv.v : p.kv.k) + h * (is_v ? p.kv.v_sh : p.kv.k_sh) * eb;
   const int64_t sp = (is_v ? p.kv.v_sp : p.kv.k_sp) * eb, sr = (is_v ? p.kv.v_sr : p.kv.k_sr) * eb;
   const int lanes = p.part_lanes, lane = tid % lanes, row0 = tid / lanes;
@@ -561,7 +558,7 @@ cudaError_t launch_keep_t(const KeepParams& p, cudaStream_t stream) {
   cudaError_t e = opt_in_smem(keep_kernel<THREADS, PER, SC>, kKeepStages * Lay::kChunkBytes + 4 * kKeepTable * 8, configured);
   if (e != cudaSuccess) return e;
   const int row_lanes = kD * (p.kv.dt == kDtF32 ? 4 : (SC ? 1 : 2)) / 16;
-  return launch_chained(keep_kernel<THREADS, PER, SC>, dim3(row_lanes / p.part_lanes, (SC ? 4 : 2) * p.kv.Hkv, p.B), dim3(THREADS),
+  return launch_chained(keep_kernel<THREADS, PER, SC>, dim3(row_lanes / p.part_lanes + (SC ? 1 : 0), 2 * p.kv.Hkv, p.B), dim3(THREADS),
                         Lay(p.N, p.part_lanes).bytes(), stream, p);
 }
 

@@ -124,3 +124,24 @@ def test_a_cache_without_pages(cuda_lib, dtype, kv, T, tree):
     assert bool((back[0] == 0).all()) and bool((back[1] == 0).all())
     with pytest.raises(cuda_lib.StError):
         cuda_lib.st_check_status()
+
+
+# ---------------------------------------------------------------- many heads
+@pytest.mark.parametrize("kv", HELD)
+@pytest.mark.parametrize("Hkv", [16383, 16384, 32767])
+def test_keep_of_many_heads(cuda_lib, kv, Hkv):
+    """As many heads as a cache may have: rows and scales move all the same."""
+    g = torch.Generator(device="cuda").manual_seed(Hkv)
+    page, n = 2, 3
+    k, v = (torch.randint(-127, 128, (n, page, Hkv, D), generator=g, dtype=torch.int8, device="cuda") for _ in range(2))
+    ks, vs = (torch.rand(n, Hkv, page, generator=g, device="cuda") for _ in range(2))
+    cache = cuda_lib.KVCache(k.view(DT[kv]), v.view(DT[kv]), i32([[2, 0, 1]]).cuda(), ks, vs)
+    flat = lambda x, rows_first: (x if rows_first else x.transpose(1, 2))[[2, 0, 1]].reshape(n * page, Hkv, -1).clone()  # noqa: E731
+    want = [flat(k, True), flat(v, True), flat(ks, False), flat(vs, False)]
+    for w in want:
+        w[1:4] = w[[2, 4, 5]].clone()
+    lens = cuda_lib.st_cache_keep(cache, i32([1]).cuda(), i32([[1, 3, 4]]).cuda(), i32([3]).cuda())
+    cuda_lib.st_check_status()
+    assert lens.tolist() == [4]
+    for x, rows_first, w in ((k, True, want[0]), (v, True, want[1]), (ks, False, want[2]), (vs, False, want[3])):
+        assert torch.equal(flat(x, rows_first), w)
