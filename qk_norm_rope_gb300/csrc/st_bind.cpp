@@ -324,8 +324,9 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (!THPDtype_Check(a[8])) throw Refused(ST_ERR_INVALID_ARG, "dtype must be a torch.dtype");
       ty = reinterpret_cast<THPDtype*>(a[8])->scalar_type;
     }
-    const int64_t B = dim_of(*c.tensor(a[2], "cache.pages"), 0, "cache.pages"), H = dim_of(*c.tensor(a[0], "cache.k"), 2, "cache.k");
-    const int64_t D = dim_of(*c.tensor(a[0], "cache.k"), 3, "cache.k");
+    const at::Tensor *kt = c.tensor(a[0], "cache.k"), *pt = c.tensor(a[2], "cache.pages");
+    if (!pt) throw Refused(ST_ERR_INVALID_ARG, "cache.pages is None");
+    const int64_t B = dim_of(*pt, 0, "cache.pages"), H = dim_of(*kt, 2, "cache.k"), D = dim_of(*kt, 3, "cache.k");
     Out k, v;
     k.take(c, a[9], "k", {B, T, H, D}, ty);
     v.take(c, a[10], "v", {B, T, H, D}, ty);

@@ -145,3 +145,35 @@ def test_keep_of_many_heads(cuda_lib, kv, Hkv):
     assert lens.tolist() == [4]
     for x, rows_first, w in ((k, True, want[0]), (v, True, want[1]), (ks, False, want[2]), (vs, False, want[3])):
         assert torch.equal(flat(x, rows_first), w)
+
+
+# ------------------------------------------------------- arguments that are not there
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_what_a_cache_needs(cuda_lib, kv):
+    """Each call refuses a cache without K, V, pages or (of 8 bits) scales, and calls without lengths or numbers of rows."""
+    B, T, H, Hkv, page = 2, 3, 4, 2, 16
+    q, c, _, _ = attend_inputs("bf16", kv, B, T, H, Hkv, [20, 7], None, page, False, 0, 0)
+    x, k, lens = q.cuda(), rand(2, B, T, Hkv, D, dtype=torch.bfloat16).cuda(), i32([20, 7]).cuda()
+    w, ids, rows = torch.ones(D).cuda(), torch.zeros(1, T, 1, dtype=torch.int32).cuda(), i32([[0], [0]]).cuda()
+    one = i32([1, 1]).cuda()
+    calls = {
+        "append": lambda cache, n: cuda_lib.st_cache_append(x, k, k, w, w, 1e-6, ids, (128,), 1e4, cache, n),
+        "attn": lambda cache, n: cuda_lib.st_cache_attn(x, cache, n),
+        "read": lambda cache, n: cuda_lib.st_cache_read(cache, n, T),
+        "keep": lambda cache, n: cuda_lib.st_cache_keep(cache, n, rows, one),
+    }
+    names = ["k", "v", "pages"] + (["k_scale", "v_scale"] if kv == "e4m3" else [])
+    for name, call in calls.items():
+        for gone in names:
+            cache = dev_cache(cuda_lib, c)
+            setattr(cache, gone, None)
+            with pytest.raises(cuda_lib.StError) as e:
+                call(cache, lens)
+            assert e.value.status == cuda_lib.ST_ERR_INVALID_ARG, (name, gone)
+        call(dev_cache(cuda_lib, c), lens)
+        with pytest.raises(cuda_lib.StError) as e:
+            call(dev_cache(cuda_lib, c), None)
+        assert e.value.status == cuda_lib.ST_ERR_INVALID_ARG, name
+    with pytest.raises(TypeError):
+        cuda_lib.st_cache_read(dev_cache(cuda_lib, c), lens, None)
+    cuda_lib.st_check_status()
