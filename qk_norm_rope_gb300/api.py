@@ -87,8 +87,8 @@ class KVCache:
     [B, max_pages] int32; token ``pos`` of sequence ``b`` lies in row
     ``pos % page`` of page ``pages[b, pos // page]``. A cache of 8 bits has
     ``k_scale`` and ``v_scale``, [N_pages, H_kv, page] fp32: a row stands for
-    its scale times what it holds. Holds references only: allocating pages and
-    filling the table is the caller's."""
+    its scale times what it holds (others need not have them). Holds references
+    only: allocating pages and filling the table is the caller's."""
 
     def __init__(self, k, v, pages, k_scale=None, v_scale=None):
         self.k, self.v, self.pages, self.k_scale, self.v_scale = k, v, pages, k_scale, v_scale
@@ -384,17 +384,19 @@ def st_cache_append(q, k, v, q_norm_w, k_norm_w, eps, ids, axes_dim, theta, cach
     m = _bind_mod or _bind()
     if isinstance(ids, RopeTables):
         return m.cache_append(q, k, v, q_norm_w, k_norm_w, eps, None, ids.cos, ids.sin, ids.cos_k, ids.sin_k, (), 0.0,
-                              cache.k, cache.v, cache.pages, cache.k_scale, cache.v_scale, lens, counts, q_rot)
+                              cache.k, cache.v, cache.pages, getattr(cache, "k_scale", None),
+                              getattr(cache, "v_scale", None), lens, counts, q_rot)
     return m.cache_append(q, k, v, q_norm_w, k_norm_w, eps, ids, None, None, None, None, axes_dim, theta, cache.k, cache.v,
-                          cache.pages, cache.k_scale, cache.v_scale, lens, counts, q_rot)
+                          cache.pages, getattr(cache, "k_scale", None), getattr(cache, "v_scale", None), lens, counts, q_rot)
 
 
 def st_cache_attn_workspace_size(q_rot, cache, parents=None, window=0, sinks=0, shared=None) -> int:
     c, opts, sc = st_kv_cache(), st_cache_attn_opts(), st_kv_scales()
-    keep = [_t(x) for x in (cache.k, cache.v, cache.pages, cache.k_scale, cache.v_scale, shared)]
+    keep = [_t(x) for x in (cache.k, cache.v, cache.pages, getattr(cache, "k_scale", None), getattr(cache, "v_scale", None),
+                            shared)]
     c.k, c.v, c.pages, sc.k, sc.v, opts.shared = (_p(x) for x in keep)
     opts.window, opts.sinks = window, sinks
-    if keep[3] or keep[4] or keep[0].dtype in (ST_E4M3, ST_I8):
+    if keep[3] or keep[4] or (keep[0] and keep[0].dtype in (ST_E4M3, ST_I8)):
         opts.scales = ctypes.pointer(sc)
     q, par = _t(q_rot), _t(parents)
     n = lib().st_cache_attn_opt_workspace_size(_p(q), ctypes.byref(c), ctypes.byref(opts), _p(par))
@@ -415,8 +417,9 @@ def st_cache_attn(q_rot, cache, lens, counts=None, parents=None, scale=None, o=N
     window > 0: a row at position p sees keys at positions above p - window and
     below sinks only. shared ([1] int32): that many first tokens lie in the same
     pages for all sequences and are read once for the batch."""
-    return (_bind_mod or _bind()).cache_attn(q_rot, cache.k, cache.v, cache.pages, cache.k_scale, cache.v_scale, lens, counts,
-                                             parents, scale or 0.0, o, lse, workspace, window, sinks, shared)
+    return (_bind_mod or _bind()).cache_attn(q_rot, cache.k, cache.v, cache.pages, getattr(cache, "k_scale", None),
+                                             getattr(cache, "v_scale", None), lens, counts, parents, scale or 0.0, o, lse,
+                                             workspace, window, sinks, shared)
 
 
 def st_tree_verify(target_probs, draft_probs, tokens, parents, u_accept, u_sample, counts=None, path=None,
@@ -430,16 +433,16 @@ def st_tree_verify(target_probs, draft_probs, tokens, parents, u_accept, u_sampl
 def st_cache_keep(cache, start, rows, n_rows, lens=None):
     """Row start[b] + rows[b, i] of each sequence moves to start[b] + i, for
     i < n_rows[b], in place. Returns the new lengths start + n_rows."""
-    return (_bind_mod or _bind()).cache_keep(cache.k, cache.v, cache.pages, cache.k_scale, cache.v_scale, start, rows, n_rows,
-                                             lens)
+    return (_bind_mod or _bind()).cache_keep(cache.k, cache.v, cache.pages, getattr(cache, "k_scale", None),
+                                             getattr(cache, "v_scale", None), start, rows, n_rows, lens)
 
 
 def st_cache_read(cache, start, n_rows, counts=None, dtype=None, k=None, v=None):
     """Rows start[b] .. start[b] + n_rows - 1 of each sequence out of the cache,
     zero behind counts[b]: (k, v), [B, n_rows, H_kv, D] both, in the cache's
     dtype, from a cache of 8 bits in ``dtype`` (bf16 unless given)."""
-    return (_bind_mod or _bind()).cache_read(cache.k, cache.v, cache.pages, cache.k_scale, cache.v_scale, start, n_rows, counts,
-                                             dtype, k, v)
+    return (_bind_mod or _bind()).cache_read(cache.k, cache.v, cache.pages, getattr(cache, "k_scale", None),
+                                             getattr(cache, "v_scale", None), start, n_rows, counts, dtype, k, v)
 
 
 class RopeAttention(torch.autograd.Function):
