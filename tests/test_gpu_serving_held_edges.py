@@ -177,3 +177,27 @@ def test_what_a_cache_needs(cuda_lib, kv):
     with pytest.raises(TypeError):
         cuda_lib.st_cache_read(dev_cache(cuda_lib, c), lens, None)
     cuda_lib.st_check_status()
+
+
+# ------------------------------------------------------------- CTAs without work
+@pytest.mark.parametrize("kv", HELD)
+@pytest.mark.parametrize("kw", [dict(), dict(window=50, sinks=2), dict(shared=True)])
+def test_fewer_tiles_than_ctas(cuda_lib, kv, kw):
+    """Short contexts under a wide table leave CTAs without a range. What an earlier kernel left in their shared memory (words
+    of 0x7fffffff: V's rows in NaN) must not become the number of a sequence."""
+    x = torch.full((64 * 260, 16, 8, 2 * D), -1, dtype=torch.int8, device="cuda").view(torch.bfloat16)
+    x.view(torch.int32).fill_(0x7FFFFFFF)
+    pages = torch.arange(64 * 260, dtype=torch.int32, device="cuda").view(64, 260)
+    q = rand(1, 64, 1, 32, D, dtype=torch.bfloat16).cuda()
+    cuda_lib.st_cache_attn(q, cuda_lib.KVCache(torch.zeros_like(x), x, pages), i32([4100] * 64).cuda())
+    B, lens = 3, [90, 1, 130]
+    q, c, _, _ = attend_inputs("bf16", kv, B, 1, 8, 2, lens, None, 16, False, kw.get("window", 0), kw.get("sinks", 0))
+    wide = torch.full((B, 6000), 1 << 30, dtype=torch.int32)
+    wide[:, :c[2].shape[1]] = c[2]
+    if "shared" in kw:
+        kw = dict(shared=i32([0]).cuda())
+    o, lse = cuda_lib.st_cache_attn(q.cuda(), dev_cache(cuda_lib, (c[0], c[1], wide, c[3], c[4])), i32(lens).cuda(), **kw)
+    cuda_lib.st_check_status()
+    want = M.attention(q, c[0], c[1], c[2], lens, None, None, kw.get("window", 0), kw.get("sinks", 0), (c[3], c[4]))
+    R.close("o", o, want[0], want[2])
+    R.close("lse", lse, want[1], want[3])
