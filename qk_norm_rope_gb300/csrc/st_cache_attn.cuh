@@ -1088,6 +1088,7 @@ __global__ void __launch_bounds__(Roles<KV != 0>::kThreads, 1) tc_kernel(const _
       if constexpr (decltype(warp_wide)::value) {
         __syncwarp();  // every lane has what it wants of the last piece
         if (lane_id == 0) more = next_piece_of<EXT>(P, NT, kCost, at, lens);
+        __syncwarp();  // the place is read by all (a shuffle orders no memory)
         more = __shfl_sync(0xffffffffu, more, 0);
       } else {
         more = next_piece_of<EXT>(P, NT, kCost, at, lens);
