@@ -201,3 +201,52 @@ def test_fewer_tiles_than_ctas(cuda_lib, kv, kw):
     want = M.attention(q, c[0], c[1], c[2], lens, None, None, kw.get("window", 0), kw.get("sinks", 0), (c[3], c[4]))
     R.close("o", o, want[0], want[2])
     R.close("lse", lse, want[1], want[3])
+
+
+# ----------------------------------------------------------- places far apart
+@pytest.mark.parametrize("far", ["k", "v", "k_scale", "v_scale"])
+@pytest.mark.parametrize("dtype,kv", [("bf16", "e4m3"), ("fp16", "int8"), ("fp32", "int8")])
+def test_places_beyond_32_bits(cuda_lib, far, dtype, kv):
+    """Pages (16 GB of rows) or scales (2^32 of them, which takes 16-bit rows to the CUDA cores, too) that lie far apart: append,
+    read, attention of single tokens, a chunk, a tree, with a window, and compaction, each as over the same cache packed."""
+    B, H, Hkv, page, lens = 2, 8, 2, 16, [333, 70]
+    T = 5
+    c = M.make_cache(B, [n + T for n in lens], Hkv, page, DT[kv], lens, 11, behind=0.0)
+    near = dev_cache(cuda_lib, c)
+    wide = dev_cache(cuda_lib, c)
+    x = getattr(near, far)
+    item = x.element_size()
+    step = -(-((1 << 34) // item // (x.shape[0] - 1)) // 16 + 1) * 16
+    room = torch.empty((x.shape[0] - 1) * step + x[0].numel(), dtype=torch.int8 if item == 1 else x.dtype, device="cuda")
+    y = room.as_strided(x.shape, (step, *x.stride()[1:]))
+    if item == 1:
+        y.copy_(x.view(torch.int8))
+        y = y.view(x.dtype)
+    else:
+        y.copy_(x)
+    setattr(wide, far, y)
+    pick = lambda cache: [getattr(cache, n) for n in ("k", "v", "k_scale", "v_scale")]  # noqa: E731
+
+    def same(a, b):
+        for i, j in zip(a, b):
+            i, j = (t.view(torch.int8) if t.element_size() == 1 else t for t in (i, j))
+            assert torch.equal(i, j)
+
+    q, k, v = rand(1, B, T, H, D, dtype=DT[dtype]).cuda(), *(rand(s, B, T, Hkv, D, dtype=DT[dtype]).cuda() for s in (2, 3))
+    w, ids, dl = torch.ones(D).cuda(), torch.zeros(1, T, 1, dtype=torch.int32).cuda(), i32(lens).cuda()
+    qr = [cuda_lib.st_cache_append(q, k, v, w, w, 1e-6, ids, (128,), 1e4, cache, dl) for cache in (near, wide)]
+    same(pick(near), pick(wide))
+    same(qr[:1], qr[1:])
+    same(*(cuda_lib.st_cache_read(cache, dl - 60, 60 + T) for cache in (near, wide)))
+    qr, host = qr[0].cpu(), [t.cpu() for t in pick(near)]
+    par = R.tree(B, T, 3, 3)
+    for rows, parents, window, sinks in ((1, None, 0, 0), (T, None, 0, 0), (T, par, 0, 0), (T, None, 100, 3), (T, par, 30, 0)):
+        o, lse = cuda_lib.st_cache_attn(qr[:, :rows].cuda(), wide, dl, parents=gpu(parents), window=window, sinks=sinks)
+        want = M.attention(qr[:, :rows], host[0], host[1], c[2], lens, None, parents, window, sinks, (host[2], host[3]))
+        R.close("o", o, want[0], want[2])
+        R.close("lse", lse, want[1], want[3])
+    rows = i32([[0, 2, 4], [1, 3, 4]]).cuda()
+    for cache in (near, wide):
+        cuda_lib.st_cache_keep(cache, dl, rows, i32([3, 2]).cuda())
+    same(pick(near), pick(wide))
+    cuda_lib.st_check_status()
