@@ -334,7 +334,10 @@ ST_API st_status st_cache_append(const st_tensor* q, const st_tensor* k, const s
  * bf16, fp16 or fp32, q and k of that type or both fp32, and q_rot is of v's
  * type. A row (a token and K/V head) of the rotated k, in fp32, and of v is held
  * as c[d] = x[d] / s rounded to nearest even, with s = max |x[d]| / 448 (E4M3) or
- * / 127 (I8): each value is off by at most half a step of what is held. Rows
+ * / 127 (I8), within 2^-23 of it. v of fp32 is divided into I8, s too, bit for bit
+ * as fp32 code does it; all else is multiplied by the rounded 1 / s: a value is off
+ * by half a step of what is held and 2^-22.9 of itself at most, as a quotient
+ * that lies that near to a tie may fall to either side. Rows
  * whose s would be below 2^-100 are held as zeros with s = 0; a row with an
  * infinity or NaN has NaN as its scale and reads as NaN. */
 ST_API st_status st_cache_append_held(const st_tensor* q, const st_tensor* k, const st_tensor* v, const st_tensor* q_norm_w,
@@ -347,8 +350,9 @@ ST_API st_status st_cache_append_held(const st_tensor* q, const st_tensor* k, co
  * a cache of 8 bits, in bf16, fp16 or fp32 (s * c[d] in fp32, rounded once).
  *  start:   [B] int32, contiguous; counts: [B] int32 or NULL (all T): the rows
  *           that are wanted; those behind them are zero.
- * Rows whose position is negative or beyond the page table, or whose page number
- * is out of range, are zero, too. */
+ * Rows whose position is beyond the page table, or whose page number is out of
+ * range, are zero, too; with start[b] < 0 all of sequence b's are, as st_cache_append
+ * writes none there. */
 ST_API st_status st_cache_read(const st_kv_cache* cache, const st_kv_scales* scales, const st_tensor* start,
                                const st_tensor* counts, st_tensor* k, st_tensor* v, void* stream);
 
@@ -393,7 +397,7 @@ ST_API st_status st_cache_attn(const st_tensor* q_rot, const st_kv_cache* cache,
  *           scales and sums are fp32, the softmax weights times V's scales are
  *           rounded to fp16 (off by 2^-11 of each, or by 2^-24 of the row's largest
  *           weight times the largest scale that it sees; scales of V are good from
- *           2^-50 to 2^50), with fp32 rows nothing is. The scales
+ *           2^-50 to 2^50, of K up to 2^90), with fp32 rows nothing is. The scales
  *           of keys that no row sees are not used; those that a row sees must be
  *           finite, as V's values, for the rows that do not see them. Pages may
  *           hold any number of rows. (K or V that spans more than 64 GB, and fp32
@@ -404,7 +408,7 @@ ST_API st_status st_cache_attn(const st_tensor* q_rot, const st_kv_cache* cache,
  *           ancestors for a node of a tree. Keys that no row sees may hold
  *           anything, and pages that hold no other are not looked up: their table
  *           entries may be anything. A sequence whose window lies beyond the page
- *           table sees nothing: O = 0, LSE = -inf.
+ *           table sees its first `sinks` tokens alone; without any, O = 0 and LSE = -inf.
  *  sinks:   first tokens that stay visible (only with a window).
  *  shared:  [1] int32 on the device, or NULL: the first shared[0] tokens of every
  *           sequence that has rows lie in the same pages. What is a multiple of

@@ -250,3 +250,17 @@ def test_places_beyond_32_bits(cuda_lib, far, dtype, kv):
         cuda_lib.st_cache_keep(cache, dl, rows, i32([3, 2]).cuda())
     same(pick(near), pick(wide))
     cuda_lib.st_check_status()
+
+
+# ------------------------------------------------------- windows behind the table
+@pytest.mark.parametrize("dtype,kv,page", [("bf16", "bf16", 16), ("fp16", "e4m3", 16), ("bf16", "int8", 5), ("fp32", "fp32", 16), ("fp32", "int8", 8)])
+@pytest.mark.parametrize("B,sinks", [(2, 3), (2, 150), (90, 1), (90, 130)])
+def test_windows_behind_the_table_leave_the_first_tokens(cuda_lib, dtype, kv, page, B, sinks):
+    """Lengths beyond the page table's room: a row sees the first tokens, and nothing else is in its window."""
+    q, c, _, _ = attend_inputs(dtype, kv, B, 1, 4, 2, [200] * B, None, page, False, 0, 0)
+    o, lse = cuda_lib.st_cache_attn(q.cuda(), dev_cache(cuda_lib, c), i32([1 << 30] * B).cuda(), window=30, sinks=sinks)
+    with pytest.raises(cuda_lib.StError):
+        cuda_lib.st_check_status()
+    want = M.attention(q, c[0], c[1], c[2], [sinks - 1] * B, None, None, scales=None if c[3] is None else (c[3], c[4]))
+    R.close("o", o, want[0], want[2])
+    R.close("lse", lse, want[1], want[3])
