@@ -334,10 +334,10 @@ ST_API st_status st_cache_append(const st_tensor* q, const st_tensor* k, const s
  * bf16, fp16 or fp32, q and k of that type or both fp32, and q_rot is of v's
  * type. A row (a token and K/V head) of the rotated k, in fp32, and of v is held
  * as c[d] = x[d] / s rounded to nearest even, with s = max |x[d]| / 448 (E4M3) or
- * / 127 (I8), within 2^-23 of it. v of fp32 is divided into I8, s too, bit for bit
- * as fp32 code does it; all else is multiplied by the rounded 1 / s: a value is off
- * by half a step of what is held and 2^-22.9 of itself at most, as a quotient
- * that lies that near to a tie may fall to either side. Rows
+ * / 127 (I8), within 2^-23 of it. v is divided into I8, s too, bit for bit as fp32
+ * code does it; all else is multiplied by the rounded 1 / s: a value is off by half
+ * a step of what is held and 2^-22.9 of itself at most, as a quotient that lies
+ * that near to a tie may fall to either side. Rows
  * whose s would be below 2^-100 are held as zeros with s = 0; a row with an
  * infinity or NaN has NaN as its scale and reads as NaN. */
 ST_API st_status st_cache_append_held(const st_tensor* q, const st_tensor* k, const st_tensor* v, const st_tensor* q_norm_w,

@@ -97,8 +97,13 @@ __device__ __forceinline__ float top3(float a, float b, float c) {
 // its scale and reads as NaN. int8: x / s + 1.5 2^23 has the rounded quotient in its
 // low byte, in one step (conversions to integers run at a quarter of that rate: with
 // them, two divisions and comparisons of bits 4608 tokens of two samples, 24 + 24 heads,
-// took 101 us, so 96). EXACT (v of fp32 in int8): s and x / s are divided, and v is held
-// bit for bit as elementwise fp32 code holds it.
+// took 101 us, so 96). EXACT (v in int8): s is divided, and x / s is the rounded quotient,
+// so that v is held bit for bit as elementwise fp32 code holds it (16-bit rows have
+// quotients on ties: with products alone 5e-4 of bf16's values fell to the other side).
+// The product q = x (1 / s) comes to the rounded quotient by one step, q + (x - q s) (1 / s),
+// as 1 / s is rounded right (P. Markstein, IBM J. Res. Dev. 34, 1990). In us for the
+// prompts above, q and k of fp32 and of bf16, v of bf16: products 85 and 77, this 87 and 79,
+// divisions 94 and 87.
 template <int KV, bool EXACT>
 __device__ __forceinline__ uint2 hold_row(const float (&y)[8], float* scale) {
   float top = top3(top3(y[0], y[1], y[2]), top3(y[3], y[4], y[5]), top3(y[6], y[7], y[7]));
@@ -125,9 +130,9 @@ __device__ __forceinline__ uint2 hold_row(const float (&y)[8], float* scale) {
       const float2 magic = make_float2(12582912.f, 12582912.f);
       float2 a, b;
       if constexpr (EXACT) {
-        const float d = none ? INFINITY : s;
-        a = __fadd2_rn(make_float2(x0.x / d, x0.y / d), magic);
-        b = __fadd2_rn(make_float2(x1.x / d, x1.y / d), magic);
+        const float2 q0 = __fmul2_rn(x0, inv2), q1 = __fmul2_rn(x1, inv2), ns2 = make_float2(-s, -s);
+        a = __fadd2_rn(__ffma2_rn(__ffma2_rn(q0, ns2, x0), inv2, q0), magic);
+        b = __fadd2_rn(__ffma2_rn(__ffma2_rn(q1, ns2, x1), inv2, q1), magic);
       } else {
         a = __ffma2_rn(x0, inv2, magic);
         b = __ffma2_rn(x1, inv2, magic);
@@ -211,7 +216,7 @@ __global__ void __launch_bounds__(kAppWarps * 32, KV == 0 ? 0 : (SRC == kDtF32 ?
       for (int i = 0; i < NI; ++i) {
         float y[8];
         x[i].get(y);
-        hold(y, h0 + 2 * i, std::bool_constant<KV == kDtI8 && DST == kDtF32>());
+        hold(y, h0 + 2 * i, std::bool_constant<KV == kDtI8>());
       }
       return;
     }

@@ -264,3 +264,29 @@ def test_windows_behind_the_table_leave_the_first_tokens(cuda_lib, dtype, kv, pa
     want = M.attention(q, c[0], c[1], c[2], [sinks - 1] * B, None, None, scales=None if c[3] is None else (c[3], c[4]))
     R.close("o", o, want[0], want[2])
     R.close("lse", lse, want[1], want[3])
+
+
+# ------------------------------------------------------------ quotients near a tie
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("T", [3, 700])
+def test_v_in_int8_is_what_elementwise_code_holds(cuda_lib, dtype, T):
+    """v and its scales bit for bit as max / 127, x / scale and the rounding to nearest even in fp32: 16-bit rows have quotients
+    on and next to ties, which a product with 1 / scale sends to the other side."""
+    B, Hkv, page = 2, 5, 16
+    v = (rand(1, B, T, Hkv, D) * torch.exp2(rand(2, B, T, Hkv, 1) * 2)).to(DT[dtype])
+    v[0, 1] = 0
+    v[1, :, 0] = (torch.randint(-127, 128, (T, D), generator=torch.Generator().manual_seed(4)) + 0.5).to(DT[dtype])
+    v[1, :, 0, 5] = 127 * 4                              # scale 4: every eighth quotient is a tie
+    v[1, :, 1] = v[1, :, 0] * 3
+    v[1, :, 1, 5] = 127 * 1.5                            # some larger than the row's fifth, scales with many bits
+    c = M.make_cache(B, [T] * B, Hkv, page, torch.int8, [0] * B, 3, behind=0.0)
+    cache = dev_cache(cuda_lib, c)
+    w, ids, k = torch.ones(D).cuda(), torch.zeros(1, T, 1, dtype=torch.int32).cuda(), rand(3, B, T, Hkv, D, dtype=DT[dtype]).cuda()
+    cuda_lib.st_cache_append(k, k, v.cuda(), w, w, 1e-6, ids, (128,), 1e4, cache, i32([0] * B).cuda())
+    cuda_lib.st_check_status()
+    s = v.float().abs().amax(-1) / 127.0
+    held = (v.float() / torch.where(s > 0, s, torch.ones_like(s))[..., None]).round().to(torch.int8)
+    for b in range(B):
+        pg, row = R.slots(c[2], page, b, torch.arange(T))
+        assert torch.equal(cache.v_scale.cpu()[pg, :, row], s[b])
+        assert torch.equal(cache.v.cpu()[pg, row], held[b])
