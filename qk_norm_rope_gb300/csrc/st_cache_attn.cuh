@@ -422,9 +422,11 @@ __device__ __forceinline__ void find_start(const TcAttnParams& p, int nt, int co
     if (lane >= o) inc += t;
   }
   if (lane == 31) scan[warp] = inc;
-  if (tid == 0) {  // a CTA behind the last range: no piece, and nothing of an earlier kernel's
-    st->h = st->b = st->m = st->off = 0;
+  if (tid == 0) {
     st->left = 0;
+    // a CTA behind the last range has nothing of an earlier kernel's here (the plain
+    // 16-bit forms look at no more than `left` there)
+    if constexpr (ITEMS) st->h = st->b = st->m = st->off = 0;
   }
   __syncthreads();
   long long before = 0, one = 0;
