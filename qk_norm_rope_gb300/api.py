@@ -416,7 +416,9 @@ def st_cache_attn(q_rot, cache, lens, counts=None, parents=None, scale=None, o=N
 
     window > 0: a row at position p sees keys at positions above p - window and
     below sinks only. shared ([1] int32): that many first tokens lie in the same
-    pages for all sequences and are read once for the batch."""
+    pages for all sequences, and the whole tiles of 128 among them are read once
+    for the batch (not with a window, fp32 rows or 16-bit pages of other than a
+    multiple of 8 rows, where each sequence reads them for itself)."""
     return (_bind_mod or _bind()).cache_attn(q_rot, cache.k, cache.v, cache.pages, getattr(cache, "k_scale", None),
                                              getattr(cache, "v_scale", None), lens, counts, parents, scale or 0.0, o, lse,
                                              workspace, window, sinks, shared)

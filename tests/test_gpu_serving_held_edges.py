@@ -1,5 +1,6 @@
-"""Edges of the calls over 8-bit caches, on the GPU: rows beside keys that they do not see, caches without pages, CTAs
-without work, caches of many heads, arguments that are not there."""
+"""Edges of the calls over 8-bit caches, on the GPU: rows beside keys that they do not see, caches without pages, of many
+heads and spread over more than 2^32 places, arguments that are not there, CTAs without work, windows behind the table,
+quotients near a tie."""
 import math
 
 import pytest
