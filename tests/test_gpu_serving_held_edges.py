@@ -291,3 +291,21 @@ def test_v_in_int8_is_what_elementwise_code_holds(cuda_lib, dtype, T):
         pg, row = R.slots(c[2], page, b, torch.arange(T))
         assert torch.equal(cache.v_scale.cpu()[pg, :, row], s[b])
         assert torch.equal(cache.v.cpu()[pg, row], held[b])
+
+
+def test_v_in_int8_of_every_size(cuda_lib):
+    """fp32 rows from 2^-92 (scales near the least that is held) to 2^120, their elements as much as 2^60 apart."""
+    B, T, Hkv, page = 1, 2000, 3, 16
+    g = torch.Generator().manual_seed(9)
+    v = rand(1, B, T, Hkv, D) * torch.exp2(-60 * torch.rand(B, T, Hkv, D, generator=g) ** 4)
+    v = v * torch.exp2(torch.randint(-92, 119, (B, T, Hkv, 1), generator=g).float())
+    c = M.make_cache(B, [T], Hkv, page, torch.int8, [0], 3, behind=0.0)
+    cache = dev_cache(cuda_lib, c)
+    w, ids, k = torch.ones(D).cuda(), torch.zeros(1, T, 1, dtype=torch.int32).cuda(), rand(3, B, T, Hkv, D).cuda()
+    cuda_lib.st_cache_append(k, k, v.cuda(), w, w, 1e-6, ids, (128,), 1e4, cache, i32([0]).cuda())
+    s = v.abs().amax(-1) / 127.0
+    s = torch.where(s < 2.0 ** -100, torch.zeros_like(s), s)
+    held = torch.where(s[..., None] > 0, v / s[..., None], torch.zeros_like(v)).round().to(torch.int8)
+    pg, row = R.slots(c[2], page, 0, torch.arange(T))
+    assert torch.equal(cache.v_scale.cpu()[pg, :, row], s[0])
+    assert torch.equal(cache.v.cpu()[pg, row], held[0])
