@@ -598,11 +598,12 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, float sc,
 // would end below fp16's range: with 2^32 between them the row read as zeros. There the
 // reference is the largest sum of a score and its key's log2 vs, found in a pass of its
 // own: where every tile takes it, 64 tokens after up to 8191 keys in e4m3 201 us instead
-// of 154, 2048 after 16384 1090 instead of 670.) There are no registers for a row of 128 scores: they go back
-// to TMEM, scaled and masked, while the maximum is found, and come again for the
-// weights, which take the place of scores that have been read. (Scaled and masked a
-// second time instead 2048 tokens after 16384 took 926 us over e4m3, so 755: the
-// reads of the scales from shared memory stand in line with the MMAs' operands.)
+// of 154, 2048 after 16384 1090 instead of 670.) There are no registers for a row of
+// 128 scores: they go back to TMEM, scaled and masked, while the maximum is found, and
+// come again for the weights, which take the place of scores that have been read.
+// (Scaled and masked a second time instead 2048 tokens after 16384 took 926 us over
+// e4m3, so 755: the reads of the scales from shared memory stand in line with the MMAs'
+// operands.)
 template <int N>
 __device__ __forceinline__ void scale_chunk(uint32_t (&x)[N], const float* ks) {
 #pragma unroll
